@@ -333,6 +333,99 @@ moe_status moe_selftest_wait(void* workspace, void* stream);
 /* Round-to-nearest-even conversion of n fp32 values to bf16 (device in/out). */
 moe_status moe_cast_f32_to_bf16(const float* in, void* out, int64_t n, void* stream);
 
+/* ---- Training operators: the layer's steps as calls of their own, on the caller's tensors, with
+ * their gradients. They share nothing with the forward's workspace. All of them are
+ * deterministic, enqueue on `stream` only and take contiguous row-major tensors that start on
+ * 16-byte boundaries. A size outside the stated range returns MOE_ERR_UNSUPPORTED.
+ *
+ * T tokens, k slots a token (1..8), flat slot index f = t*k + j, E experts (1..256). */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
+
+/* Rows of x [T, H] sorted by expert. ids [T, k]: the expert of each slot, or -1 for a slot that
+ * was dropped. Slots are ordered by expert, then by f; dropped ones come last. place(f) is a
+ * slot's row in that order:
+ *   x_perm [T*k, H]   x_perm[place(f)] = x[f / k]; zeros in the rows of dropped slots
+ *   inv [T, k]        place(f), or -1 - place(f) for a dropped slot
+ *   offsets [E + 1]   the first row of each expert; offsets[E] = rows that are not dropped
+ * dtype: any moe_dtype; H 1..65536; T <= 2^24. The workspace (moe_dispatch_workspace_bytes, 0
+ * for sizes outside the range) needs no clearing; its status word, which
+ * moe_read_device_status reads, gets MOE_DEVICE_FLAG_BAD_ID when an id is neither -1 nor in
+ * [0, E) (the slot is then dropped). */
+size_t moe_dispatch_workspace_bytes(int64_t T, int32_t E, int32_t k);
+moe_status moe_dispatch(const void* x, const int32_t* ids, int64_t T, int32_t H, int32_t E,
+                        int32_t k, moe_dtype dtype, void* x_perm, int32_t* inv, int32_t* offsets,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* x_perm alone, by an inv that is there already: for a backward pass that kept x, which is k
+ * times smaller, in place of x_perm. In this and the next three calls a slot whose place lies
+ * outside [0, T*k) counts as dropped and writes no row. */
+moe_status moe_dispatch_rows(const void* x, const int32_t* inv, int64_t T, int32_t H, int32_t k,
+                             moe_dtype dtype, void* x_perm, void* stream);
+
+/* Gradient of moe_dispatch: dx[t] = sum over t's kept slots of dx_perm[inv[t, j]]. */
+moe_status moe_dispatch_backward(const void* dx_perm, const int32_t* inv, int64_t T, int32_t H,
+                                 int32_t k, moe_dtype dtype, void* dx, void* stream);
+
+/* Back to token order: y[t] = sum over t's kept slots of scales[t, j] * rows[inv[t, j]], summed
+ * in fp32 in slot order. scales [T, k] fp32, or NULL for 1. Rows of dropped slots are not read. */
+moe_status moe_combine(const void* rows, const int32_t* inv, const float* scales, int64_t T,
+                       int32_t H, int32_t k, moe_dtype dtype, void* y, void* stream);
+
+/* Gradients of moe_combine: drows[place(f)] = scales[f] * dy[t] (zeros for a dropped slot) and
+ * dscales[f] = <dy[t], rows[inv[f]]> (0 for a dropped slot). */
+moe_status moe_combine_backward(const void* dy, const void* rows, const int32_t* inv,
+                                const float* scales, int64_t T, int32_t H, int32_t k,
+                                moe_dtype dtype, void* drows, float* dscales, void* stream);
+
+/* SwiGLU that keeps its input for the backward pass in 8 bits. gu [R, 2I]: gate, then up, of each
+ * row; h [R, I] = silu(gate) * up. The checkpoint is q [R, 2I], e4m3 values in gu's order, and
+ * q_scales [R, 2 * ceil(I / 32)], a power of two 2^(byte - 127) for each 32 neighbouring channels
+ * of the gate, then of the up half (the last of a half may cover fewer): the least with
+ * |value| <= 448 * scale, so a value v is kept to within |v| / 16 (or 2^-10 of the scale). A
+ * block that holds an infinity or a NaN has scale byte 255 and reads as NaN. dtype: any
+ * moe_dtype; I 1..65536. */
+moe_status moe_swiglu_ckpt(const void* gu, int64_t R, int32_t I, moe_dtype dtype, void* h,
+                           uint8_t* q, uint8_t* q_scales, void* stream);
+
+/* Its gradient at the kept values: dgu [R, 2I] from dh [R, I] and the checkpoint; and, where h is
+ * not NULL, h [R, I] again, from the kept values, for the gradient of the weights behind it. */
+moe_status moe_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const uint8_t* q_scales,
+                                    int64_t R, int32_t I, moe_dtype dtype, void* dgu, void* h,
+                                    void* stream);
+
+/* The experts' products over sorted rows: rows [offsets[e], offsets[e + 1]) are expert e's
+ * (offsets [E + 1] int32 on the device, non-decreasing from 0; kept inside [0, R] by the kernel),
+ * w [E, N, K].
+ *   moe_experts_matmul      y [R, N]:     y[r] = x[r] . w[e]^T     (x [R, K])
+ *   moe_experts_matmul_dx   dx [R, K]:    dx[r] = dy[r] . w[e]     (dy [R, N])
+ *   moe_experts_matmul_dw   dw [E, N, K]: dw[e] = sum over e's rows of dy[r]^T . x[r]
+ * Rows from offsets[E] on are zeros in y and dx; an expert without rows has dw = 0. fp32
+ * accumulation, one rounding. dtype BF16 or F16; dw_dtype the same or F32, and with F32
+ * `accumulate` adds to what dw holds. N and K: multiples of 8 up to 65536; R <= 2^26.
+ * Workspace: for dw moe_experts_workspace_bytes(E) bytes (0 outside 1..256), 128-byte aligned,
+ * not cleared by the caller, its status word cleared by the call. The other two take NULL, or at
+ * least 16 bytes whose status word (cleared by the caller once) receives
+ * MOE_DEVICE_FLAG_TIMEOUT; moe_read_device_status reads it. */
+size_t moe_experts_workspace_bytes(int32_t E);
+moe_status moe_experts_matmul(const void* x, const void* w, const int32_t* offsets, int64_t R,
+                              int32_t E, int32_t N, int32_t K, moe_dtype dtype, void* y,
+                              void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_experts_matmul_dx(const void* dy, const void* w, const int32_t* offsets, int64_t R,
+                                 int32_t E, int32_t N, int32_t K, moe_dtype dtype, void* dx,
+                                 void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
+                                 int32_t E, int32_t N, int32_t K, moe_dtype dtype,
+                                 moe_dtype dw_dtype, int32_t accumulate, void* dw, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route's scales to its logits: dlogits [T, E] (every entry written) from logits
+ * [T, E], the ids [T, k] that moe_route chose and dscales [T, k]. The choice itself has no
+ * gradient (nor has the bias). Takes every method that moe_route runs; of the other parameters
+ * only num_experts, top_k and routed_scaling_factor matter. Slots with an id outside [0, E) take
+ * no part; non-finite logits count as -inf and get 0. */
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dscales,
+                              int64_t T, const moe_route_params* p, float* dlogits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,10 @@ MOE_ERR_DEVICE_BAD_ID = 5
 MOE_ERR_DEVICE_TIMEOUT = 6
 MOE_ERR_NOT_IMPLEMENTED = 7
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+
 MOE_DEVICE_FLAG_BAD_ID = 1
 MOE_DEVICE_FLAG_TIMEOUT = 2
 
@@ -92,6 +96,36 @@ _SIGS = {
     "moe_static_read_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "moe_selftest_wait": (ctypes.c_int, [_P, _P]),
     "moe_cast_f32_to_bf16": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P]),
+    "moe_dispatch_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32,
+                                                       ctypes.c_int32]),
+    "moe_dispatch": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                    ctypes.c_int32, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t,
+                                    _P]),
+    "moe_dispatch_rows": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_int, _P, _P]),
+    "moe_dispatch_backward": (ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int, _P, _P]),
+    "moe_combine": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_int, _P, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int, _P, _P, _P]),
+    "moe_swiglu_ckpt": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, _P, _P, _P,
+                                       _P]),
+    "moe_swiglu_ckpt_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                                ctypes.c_int, _P, _P, _P]),
+    "moe_experts_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "moe_experts_matmul": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P,
+                                          ctypes.c_size_t, _P]),
+    "moe_experts_matmul_dx": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P,
+                                             ctypes.c_size_t, _P]),
+    "moe_experts_matmul_dw": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
+                                             ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.c_size_t,
+                                             _P]),
+    "moe_route_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64,
+                                          ctypes.POINTER(MoeRouteParams), _P, _P]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -404,5 +438,266 @@ def moe_cast_f32_to_bf16(t: torch.Tensor, out: Optional[torch.Tensor] = None, st
     return out
 
 
+# ------------------------------------------------------------------ training operators
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
+           torch.float32: MOE_DTYPE_F32}
+
+
+@dataclass
+class Scratch:
+    """Caller-owned device workspace of a training operator; moe_read_device_status takes it."""
+    buf: torch.Tensor
+
+    @property
+    def ptr(self) -> ctypes.c_void_p:
+        return ctypes.c_void_p(self.buf.data_ptr())
+
+    @property
+    def nbytes(self) -> int:
+        return self.buf.numel()
+
+
+def alloc_dispatch_scratch(T: int, num_experts: int, top_k: int, device="cuda") -> Scratch:
+    """Workspace of moe_dispatch for T tokens."""
+    n = int(_lib.moe_dispatch_workspace_bytes(int(T), int(num_experts), int(top_k)))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_dispatch_workspace_bytes")
+    return Scratch(torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def alloc_experts_scratch(num_experts: int, device="cuda") -> Scratch:
+    """Workspace of the experts' products (all three), its status word cleared."""
+    n = int(_lib.moe_experts_workspace_bytes(int(num_experts)))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_experts_workspace_bytes")
+    return Scratch(torch.zeros(n, dtype=torch.uint8, device=device))
+
+
+def _typed(t: torch.Tensor, name: str, ndim: int) -> int:
+    """The moe_dtype of a contiguous CUDA tensor of `ndim` dimensions."""
+    _cuda(t, name)
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _shaped(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
+    """t, a contiguous CUDA tensor of just this shape and type."""
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _shaped(t, name, shape, dtype)
+
+
+def _slots(inv: torch.Tensor, name: str = "inv"):
+    _cuda(inv, name, torch.int32)
+    if inv.dim() != 2:
+        raise ValueError(f"{name} must be [T, k], got {tuple(inv.shape)}")
+    return inv.shape
+
+
+def moe_dispatch(x, ids, num_experts: int, x_perm=None, inv=None, offsets=None,
+                 scratch: Optional[Scratch] = None, stream=None):
+    """Rows of x [T, H] sorted by expert. ids int32 [T, k], -1 for a dropped slot. Returns
+    (x_perm [T*k, H], inv int32 [T, k], offsets int32 [E + 1]): rows of expert e are
+    x_perm[offsets[e]:offsets[e + 1]], inv the row of each slot (-1 - row of a dropped one, whose
+    row holds zeros)."""
+    dt = _typed(x, "x", 2)
+    T, H = x.shape
+    if _slots(ids, "ids")[0] != T:
+        raise ValueError(f"ids must have {T} rows, got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    dev = x.device
+    x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, dev)
+    inv = _out(inv, "inv", (T, k), torch.int32, dev)
+    offsets = _out(offsets, "offsets", (num_experts + 1,), torch.int32, dev)
+    if scratch is None and T > 0:
+        scratch = alloc_dispatch_scratch(T, num_experts, k, dev)
+    _check(_lib.moe_dispatch(_ptr(x), _ptr(ids), T, H, num_experts, k, dt, _ptr(x_perm), _ptr(inv),
+                             _ptr(offsets), scratch.ptr if scratch else None,
+                             scratch.nbytes if scratch else 0, _stream(stream)), "moe_dispatch")
+    return x_perm, inv, offsets
+
+
+def moe_dispatch_rows(x, inv, x_perm=None, stream=None):
+    """moe_dispatch's x_perm again, by the inv it returned."""
+    dt = _typed(x, "x", 2)
+    T, k = _slots(inv)
+    H = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows, got {tuple(x.shape)}")
+    x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, x.device)
+    _check(_lib.moe_dispatch_rows(_ptr(x), _ptr(inv), T, H, k, dt, _ptr(x_perm), _stream(stream)),
+           "moe_dispatch_rows")
+    return x_perm
+
+
+def moe_dispatch_backward(dx_perm, inv, dx=None, stream=None):
+    """Gradient of moe_dispatch: dx [T, H], each token's kept rows of dx_perm [T*k, H] summed."""
+    dt = _typed(dx_perm, "dx_perm", 2)
+    T, k = _slots(inv)
+    H = dx_perm.shape[1]
+    _shaped(dx_perm, "dx_perm", (T * k, H), dx_perm.dtype)
+    dx = _out(dx, "dx", (T, H), dx_perm.dtype, dx_perm.device)
+    _check(_lib.moe_dispatch_backward(_ptr(dx_perm), _ptr(inv), T, H, k, dt, _ptr(dx),
+                                      _stream(stream)), "moe_dispatch_backward")
+    return dx
+
+
+def moe_combine(rows, inv, scales=None, y=None, stream=None):
+    """Back to token order: y [T, H] = sum of each token's kept rows [T*k, H], weighted by scales
+    fp32 [T, k] (None: 1)."""
+    dt = _typed(rows, "rows", 2)
+    T, k = _slots(inv)
+    H = rows.shape[1]
+    _shaped(rows, "rows", (T * k, H), rows.dtype)
+    if scales is not None:
+        _shaped(scales, "scales", (T, k), torch.float32)
+    y = _out(y, "y", (T, H), rows.dtype, rows.device)
+    _check(_lib.moe_combine(_ptr(rows), _ptr(inv), _ptr(scales), T, H, k, dt, _ptr(y),
+                            _stream(stream)), "moe_combine")
+    return y
+
+
+def moe_combine_backward(dy, rows, inv, scales=None, drows=None, dscales=None, stream=None):
+    """Gradients of moe_combine: (drows [T*k, H], dscales fp32 [T, k])."""
+    dt = _typed(dy, "dy", 2)
+    T, k = _slots(inv)
+    H = dy.shape[1]
+    _shaped(dy, "dy", (T, H), dy.dtype)
+    _shaped(rows, "rows", (T * k, H), dy.dtype)
+    if scales is not None:
+        _shaped(scales, "scales", (T, k), torch.float32)
+    drows = _out(drows, "drows", (T * k, H), dy.dtype, dy.device)
+    dscales = _out(dscales, "dscales", (T, k), torch.float32, dy.device)
+    _check(_lib.moe_combine_backward(_ptr(dy), _ptr(rows), _ptr(inv), _ptr(scales), T, H, k, dt,
+                                     _ptr(drows), _ptr(dscales), _stream(stream)),
+           "moe_combine_backward")
+    return drows, dscales
+
+
+MOE_CKPT_BLOCK = 32
+
+
+def moe_swiglu_ckpt(gu, h=None, ckpt=None, stream=None):
+    """SwiGLU that keeps its input in 8 bits. gu [R, 2I], gate then up. Returns (h [R, I],
+    (q uint8 [R, 2I], q_scales uint8 [R, 2 * ceil(I / 32)])): the e4m3 codes and the exponent
+    bytes (scale 2^(byte - 127)) that moe_swiglu_ckpt_backward reads."""
+    dt = _typed(gu, "gu", 2)
+    R, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError(f"gu must have an even number of columns, got {I2}")
+    I = I2 // 2
+    nb = 2 * (-(-I // MOE_CKPT_BLOCK))
+    h = _out(h, "h", (R, I), gu.dtype, gu.device)
+    q, qs = ckpt if ckpt is not None else (None, None)
+    q = _out(q, "q", (R, I2), torch.uint8, gu.device)
+    qs = _out(qs, "q_scales", (R, nb), torch.uint8, gu.device)
+    _check(_lib.moe_swiglu_ckpt(_ptr(gu), R, I, dt, _ptr(h), _ptr(q), _ptr(qs), _stream(stream)),
+           "moe_swiglu_ckpt")
+    return h, (q, qs)
+
+
+def moe_swiglu_ckpt_backward(dh, ckpt, dgu=None, h=None, want_h: bool = False, stream=None):
+    """Gradient of moe_swiglu_ckpt at the kept values: (dgu [R, 2I], h [R, I] again or None)."""
+    dt = _typed(dh, "dh", 2)
+    R, I = dh.shape
+    q, qs = ckpt
+    _shaped(q, "q", (R, 2 * I), torch.uint8)
+    _shaped(qs, "q_scales", (R, 2 * (-(-I // MOE_CKPT_BLOCK))), torch.uint8)
+    dgu = _out(dgu, "dgu", (R, 2 * I), dh.dtype, dh.device)
+    if want_h or h is not None:
+        h = _out(h, "h", (R, I), dh.dtype, dh.device)
+    _check(_lib.moe_swiglu_ckpt_backward(_ptr(dh), _ptr(q), _ptr(qs), R, I, dt, _ptr(dgu), _ptr(h),
+                                         _stream(stream)), "moe_swiglu_ckpt_backward")
+    return dgu, h
+
+
+def _offsets(offsets, E):
+    return _shaped(offsets, "offsets", (E + 1,), torch.int32)
+
+
+def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None, stream=None):
+    """y [R, N]: each row of x [R, K] times its expert's w[e]^T (w [E, N, K]); rows
+    [offsets[e], offsets[e + 1]) are expert e's, those past the last are zeros in y."""
+    dt = _typed(x, "x", 2)
+    _shaped(w, "w", (w.shape[0], w.shape[1], x.shape[1]) if w.dim() == 3 else (0, 0, 0), x.dtype)
+    E, N, K = w.shape
+    R = x.shape[0]
+    y = _out(y, "y", (R, N), x.dtype, x.device)
+    _check(_lib.moe_experts_matmul(_ptr(x), _ptr(w), _ptr(_offsets(offsets, E)), R, E, N, K, dt,
+                                   _ptr(y), scratch.ptr if scratch else None,
+                                   scratch.nbytes if scratch else 0, _stream(stream)),
+           "moe_experts_matmul")
+    return y
+
+
+def moe_experts_matmul_dx(dy, w, offsets, dx=None, scratch: Optional[Scratch] = None, stream=None):
+    """Gradient of moe_experts_matmul to its rows: dx [R, K] = each row of dy [R, N] times its
+    expert's w[e]."""
+    dt = _typed(dy, "dy", 2)
+    _shaped(w, "w", (w.shape[0], dy.shape[1], w.shape[2]) if w.dim() == 3 else (0, 0, 0), dy.dtype)
+    E, N, K = w.shape
+    R = dy.shape[0]
+    dx = _out(dx, "dx", (R, K), dy.dtype, dy.device)
+    _check(_lib.moe_experts_matmul_dx(_ptr(dy), _ptr(w), _ptr(_offsets(offsets, E)), R, E, N, K, dt,
+                                      _ptr(dx), scratch.ptr if scratch else None,
+                                      scratch.nbytes if scratch else 0, _stream(stream)),
+           "moe_experts_matmul_dx")
+    return dx
+
+
+def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bool = False,
+                          scratch: Optional[Scratch] = None, stream=None):
+    """Gradient of moe_experts_matmul to the weights: dw [E, N, K] = for each expert, dy^T x over
+    its rows. dw is of the inputs' type, or fp32 (dw_dtype, or a dw given); accumulate adds to a
+    given fp32 dw."""
+    dt = _typed(dy, "dy", 2)
+    _cuda(offsets, "offsets", torch.int32)
+    E = offsets.numel() - 1
+    _offsets(offsets, E)
+    R, N = dy.shape
+    _shaped(x, "x", (R, x.shape[-1]), dy.dtype)
+    K = x.shape[1]
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs the dw to add to")
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=dw_dtype or dy.dtype, device=dy.device)
+    out = _typed(dw, "dw", 3)
+    _shaped(dw, "dw", (E, N, K), dw_dtype or dw.dtype)
+    if scratch is None:
+        n = int(_lib.moe_experts_workspace_bytes(E))
+        scratch = Scratch(torch.empty(max(n, 1), dtype=torch.uint8, device=dy.device))
+    _check(_lib.moe_experts_matmul_dw(_ptr(dy), _ptr(x), _ptr(offsets), R, E, N, K, dt, out,
+                                      int(accumulate), _ptr(dw), scratch.ptr, scratch.nbytes,
+                                      _stream(stream)), "moe_experts_matmul_dw")
+    return dw
+
+
+def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor: float = 1.0,
+                       dlogits=None, stream=None):
+    """Gradient of moe_route's scales to its logits: dlogits fp32 [T, E] from logits [T, E], the ids
+    [T, k] it chose and dscales [T, k]."""
+    _cuda(logits, "logits", torch.float32)
+    T, k = _slots(ids, "ids")
+    E = logits.shape[-1]
+    _shaped(logits, "logits", (T, E), torch.float32)
+    _shaped(dscales, "dscales", (T, k), torch.float32)
+    dlogits = _out(dlogits, "dlogits", (T, E), torch.float32, logits.device)
+    p = MoeRouteParams(E, k, method, 1, 1, routed_scaling_factor)
+    _check(_lib.moe_route_backward(_ptr(logits), _ptr(ids), _ptr(dscales), T, ctypes.byref(p),
+                                   _ptr(dlogits), _stream(stream)), "moe_route_backward")
+    return dlogits
+
+
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_", "Moe"))] + [
-    "make_problem", "alloc_workspace", "Workspace", "load_library", "EXPORTED", "LIB_PATH"]
+    "make_problem", "alloc_workspace", "Workspace", "load_library", "EXPORTED", "LIB_PATH",
+    "Scratch", "alloc_dispatch_scratch", "alloc_experts_scratch"]

@@ -1,0 +1,585 @@
+// Rows sorted by expert and back, with the routing weights applied, and the gradients.
+//
+// With f = t*k + j the flat (token, slot) index, the rows of the sorted order are the slots
+// sorted stably by expert, dropped slots (id -1, or out of range) last:
+//   place(f)        the row of slot f;  inv[f] = place(f), or ~place(f) for a dropped slot
+//   dispatch        x_perm[place(f)] = x[f / k], zero for a dropped slot
+//   combine         y[t] = sum_j s[t,j] rows[inv[t,j]] over the kept slots
+//   combine grad    drows[place(f)] = s[f] dy[t] (zero when dropped), ds[f] = <dy[t], rows[inv[f]]>
+//   dispatch grad   dx[t] = sum_j dx_perm[inv[t,j]] over the kept slots
+// Every row of a [T*k, H] result is written exactly once, so nothing needs clearing first. All
+// four are bound by memory: each row is read and written once, token-major, so that the one
+// token row a dispatch reads (or a combine writes) crosses HBM once and not k times. Sums run
+// in fp32 in slot order, by one thread: no atomics, the same result on every run.
+#include <cstdint>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSortThreads = 256;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBins = 257;        // up to 256 experts, then the dropped slots
+constexpr int kMaxSlots = 8;
+
+// The expert bin of an id: [0, E), or E for a dropped slot.
+__device__ __forceinline__ int bin_of(int id, int E) { return id >= 0 && id < E ? id : E; }
+
+struct SortArgs {
+  const int32_t* ids;
+  int64_t T;
+  int64_t P;
+  int E;
+  int k;
+  int nb;               // blocks; block b sorts and copies the tokens [b * chunk, +chunk)
+  int64_t chunk;
+  int32_t* hist;        // [E + 2][nb]: per bin and block; then the blocks' bad-id flags
+  int32_t* totals;      // [E]
+  int32_t* inv;
+  int32_t* offsets;
+  int32_t* status;
+};
+
+// Slots per bin of each block's tokens, and whether an id is neither -1 nor in [0, E).
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
+  __shared__ int32_t h[kMaxBins];
+  __shared__ int s_bad;
+  pdl_trigger();
+  for (int e = threadIdx.x; e <= a.E; e += kSortThreads) h[e] = 0;
+  if (threadIdx.x == 0) s_bad = 0;
+  pdl_wait();
+  __syncthreads();
+  const int64_t f0 = a.chunk * blockIdx.x * a.k;
+  const int64_t f1 = min(a.P, f0 + a.chunk * a.k);
+  for (int64_t f = f0 + threadIdx.x; f < f1; f += kSortThreads) {
+    const int id = a.ids[f];
+    if (id < -1 || id >= a.E) s_bad = 1;
+    atomicAdd(&h[bin_of(id, a.E)], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.E; e += kSortThreads)
+    a.hist[static_cast<int64_t>(e) * a.nb + blockIdx.x] = h[e];
+  if (threadIdx.x == 0) a.hist[static_cast<int64_t>(a.E + 1) * a.nb + blockIdx.x] = s_bad;
+}
+
+// One warp per bin: the exclusive scan of its counts over the blocks, in place, and its total.
+// The last warp turns the blocks' flags into the status word.
+__global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(SortArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int e = blockIdx.x * kSortWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (e > a.E + 1) return;
+  int32_t* row = a.hist + static_cast<int64_t>(e) * a.nb;
+  int run = 0;
+  for (int b0 = 0; b0 < a.nb; b0 += 32) {
+    const int v = b0 + lane < a.nb ? row[b0 + lane] : 0;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (b0 + lane < a.nb && e <= a.E) row[b0 + lane] = run + incl - v;
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (e < a.E && lane == 0) a.totals[e] = run;
+  if (e == a.E + 1 && lane < 4) a.status[lane] = lane == 0 && run ? MOE_DEVICE_FLAG_BAD_ID : 0;
+}
+
+// Block-wide exclusive scan of one value a thread; *total receives the sum.
+__device__ int scan_block(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    if (w < warp) before += s_warp[w];
+    all += s_warp[w];
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+// Copies the rows of `n` tokens from t0 on to their places: dst[i * k + j] is the place of
+// slot j, or ~place of a dropped slot (which gets zeros). A group of 32..256 threads takes a
+// token, each thread up to four vectors at a time.
+template <int kBytes>
+__device__ __forceinline__ void copy_tokens(const char* x, char* x_perm, const int32_t* dst,
+                                            int64_t t0, int n, int k, int nvec) {
+  using Raw = typename RawVec<kBytes>::type;
+  const int g = nvec > 128 ? 256 : nvec > 64 ? 128 : nvec > 32 ? 64 : 32;
+  const int in_group = threadIdx.x & (g - 1);
+  const int64_t row_bytes = static_cast<int64_t>(nvec) * kBytes;
+  Raw zero{};
+  for (int i = threadIdx.x / g; i < n; i += kSortThreads / g) {
+    const Raw* src = reinterpret_cast<const Raw*>(x + (t0 + i) * row_bytes);
+    for (int v = in_group; v < nvec; v += 4 * g) {
+      Raw val[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (v + q * g < nvec) val[q] = __ldg(src + v + q * g);
+      for (int j = 0; j < k; ++j) {
+        const int32_t p = dst[i * k + j];
+        Raw* d = reinterpret_cast<Raw*>(x_perm + static_cast<int64_t>(p < 0 ? ~p : p) * row_bytes);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (v + q * g < nvec) __stcs(d + v + q * g, p < 0 ? zero : val[q]);
+      }
+    }
+  }
+}
+
+// Places of a block's slots and the copy of their rows. kSelfCount: every block counts all
+// ids itself, and nothing ran before it; else the scan kernel left each block its first place
+// in every bin. A sub-chunk of whole tokens (at most one slot a thread) is ranked, published
+// and copied at a time.
+template <int kBytes, bool kSelfCount>
+__global__ void __launch_bounds__(kSortThreads)
+sort_place_kernel(SortArgs a, const char* __restrict__ x, char* __restrict__ x_perm, int nvec) {
+  __shared__ int32_t s_run[kMaxBins];                 // next free place per bin
+  __shared__ int32_t s_tot[kSelfCount ? kMaxBins : 1];
+  __shared__ int32_t s_wcnt[kSortWarps][kMaxBins];    // slots per (warp, bin) of a sub-chunk
+  __shared__ int32_t s_dst[kSortThreads];
+  __shared__ int s_warp[kSortWarps];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t_first = a.chunk * blockIdx.x;
+  const int64_t t_last = min(a.T, t_first + a.chunk);
+  pdl_trigger();
+  for (int i = tid; i < kSortWarps * kMaxBins; i += kSortThreads) (&s_wcnt[0][0])[i] = 0;
+  if (kSelfCount) {
+    for (int e = tid; e <= a.E; e += kSortThreads) s_run[e] = s_tot[e] = 0;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+  }
+  pdl_wait();
+  int total;
+  if (kSelfCount) {
+    for (int64_t f = tid; f < a.P; f += kSortThreads) {
+      const int id = a.ids[f];
+      const int e = bin_of(id, a.E);
+      if (id < -1 || id >= a.E) s_bad = 1;
+      atomicAdd(&s_tot[e], 1);
+      if (f < t_first * a.k) atomicAdd(&s_run[e], 1);   // of an earlier block
+    }
+    __syncthreads();
+    const int off = scan_block(tid < a.E ? s_tot[tid] : 0, s_warp, &total);
+    if (tid < a.E) s_run[tid] += off;
+    if (tid == 0) s_run[a.E] += total;
+    if (blockIdx.x == 0) {
+      if (tid < a.E) a.offsets[tid] = off;
+      if (tid == 0) a.offsets[a.E] = total;
+      if (tid < 4) a.status[tid] = tid == 0 && s_bad ? MOE_DEVICE_FLAG_BAD_ID : 0;
+    }
+  } else {
+    const int off = scan_block(tid < a.E ? a.totals[tid] : 0, s_warp, &total);
+    if (tid < a.E) s_run[tid] = off + a.hist[static_cast<int64_t>(tid) * a.nb + blockIdx.x];
+    if (tid == 0) s_run[a.E] = total + a.hist[static_cast<int64_t>(a.E) * a.nb + blockIdx.x];
+    if (blockIdx.x == 0) {
+      if (tid < a.E) a.offsets[tid] = off;
+      if (tid == 0) a.offsets[a.E] = total;
+    }
+  }
+  const int per = kSortThreads / a.k;   // tokens of a sub-chunk
+  for (int64_t t0 = t_first; t0 < t_last; t0 += per) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(per), t_last - t0));
+    __syncthreads();   // s_run is set; the copy before has read s_dst
+    const bool mine = tid < n * a.k;
+    const int64_t f = t0 * a.k + tid;
+    const int e = mine ? bin_of(a.ids[f], a.E) : -1;
+    const uint32_t peers = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    if (mine && rank == 0) s_wcnt[warp][e] = __popc(peers);
+    __syncthreads();
+    if (mine) {
+      int p = s_run[e] + rank;
+      for (int w = 0; w < warp; ++w) p += s_wcnt[w][e];
+      if (e == a.E) p = ~p;
+      s_dst[tid] = p;
+      a.inv[f] = p;
+    }
+    __syncthreads();
+    for (int b = tid; b <= a.E; b += kSortThreads) {
+      int add = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        add += s_wcnt[w][b];
+        s_wcnt[w][b] = 0;
+      }
+      s_run[b] += add;
+    }
+    copy_tokens<kBytes>(x, x_perm, s_dst, t0, n, a.k, nvec);
+  }
+}
+
+// The same copy by a map that is there already (inv). Places outside [0, T*k) write nothing.
+template <int kBytes>
+__global__ void __launch_bounds__(kSortThreads)
+dispatch_rows_kernel(const char* __restrict__ x, const int32_t* __restrict__ inv, int64_t T, int k,
+                     int nvec, char* __restrict__ x_perm) {
+  using Raw = typename RawVec<kBytes>::type;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t P = T * k;
+  const int g = nvec > 128 ? 256 : nvec > 64 ? 128 : nvec > 32 ? 64 : 32;
+  const int in_group = threadIdx.x & (g - 1);
+  const int64_t row_bytes = static_cast<int64_t>(nvec) * kBytes;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kSortThreads / g);
+  Raw zero{};
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads / g) + threadIdx.x / g; t < T;
+       t += groups) {
+    const Raw* src = reinterpret_cast<const Raw*>(x + t * row_bytes);
+    for (int v = in_group; v < nvec; v += 4 * g) {
+      Raw val[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (v + q * g < nvec) val[q] = __ldg(src + v + q * g);
+      for (int j = 0; j < k; ++j) {
+        const int32_t p = __ldg(inv + t * k + j);
+        const int64_t r = p < 0 ? ~p : p;
+        if (r >= P) continue;
+        Raw* d = reinterpret_cast<Raw*>(x_perm + r * row_bytes);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (v + q * g < nvec) __stcs(d + v + q * g, p < 0 ? zero : val[q]);
+      }
+    }
+  }
+}
+
+// One thread per vector of a token's row: its up to kSlots row loads are issued together and
+// summed in slot order. scales NULL: every weight is 1.
+template <typename T, int kBytes, int kSlots>
+__global__ void __launch_bounds__(kSortThreads)
+combine_kernel(const T* __restrict__ rows, const int32_t* __restrict__ inv,
+               const float* __restrict__ scales, int64_t n_tok, int k, int nvec,
+               T* __restrict__ y) {
+  using V = Vec<T, kBytes>;
+  using Raw = typename V::Raw;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t P = n_tok * k;
+  const int64_t total = n_tok * nvec;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kSortThreads;
+  const Raw* in = reinterpret_cast<const Raw*>(rows);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < total;
+       i += stride) {
+    const int64_t t = total <= UINT32_MAX
+                          ? static_cast<uint32_t>(i) / static_cast<uint32_t>(nvec) : i / nvec;
+    const int v = static_cast<int>(i - t * nvec);
+    int32_t row[kSlots];
+    float s[kSlots];
+    Raw val[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      row[j] = -1;
+      s[j] = 1.0f;
+      if (j < k) {
+        row[j] = __ldg(inv + t * k + j);
+        if (row[j] >= P) row[j] = -1;
+        if (scales) s[j] = __ldg(scales + t * k + j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j)
+      if (row[j] >= 0) val[j] = __ldg(in + static_cast<int64_t>(row[j]) * nvec + v);
+    float acc[V::kN] = {};
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      if (row[j] < 0) continue;
+      float f[V::kN];
+      V::unpack(val[j], f);
+#pragma unroll
+      for (int c = 0; c < V::kN; ++c) acc[c] = fmaf(s[j], f[c], acc[c]);
+    }
+    reinterpret_cast<Raw*>(y)[t * nvec + v] = V::pack(acc);
+  }
+}
+
+// kWarps warps per token: each vector of dy[t] is read once and meets the vectors of the
+// token's kept rows; the k dot products are summed over the lanes (and warps) in fixed order.
+template <typename T, int kBytes, int kSlots, int kWarps>
+__global__ void __launch_bounds__(kSortThreads)
+combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
+                    const int32_t* __restrict__ inv, const float* __restrict__ scales,
+                    int64_t n_tok, int k, int nvec, T* __restrict__ drows,
+                    float* __restrict__ dscales) {
+  using V = Vec<T, kBytes>;
+  using Raw = typename V::Raw;
+  constexpr int kToks = kSortWarps / kWarps;   // tokens a block has at a time
+  __shared__ float s_dot[kWarps > 1 ? kSortWarps : 1][kSlots];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % kWarps;
+  const int64_t P = n_tok * k;
+  const Raw zero{};
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kToks; t0 < n_tok;
+       t0 += static_cast<int64_t>(gridDim.x) * kToks) {
+    const int64_t t = t0 + warp / kWarps;
+    float dot[kSlots] = {};
+    if (t < n_tok) {
+      int32_t row[kSlots];
+      float s[kSlots];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        row[j] = INT32_MIN;   // nothing to write
+        s[j] = 0.0f;
+        if (j < k) {
+          const int32_t p = __ldg(inv + t * k + j);
+          if ((p < 0 ? ~p : p) < P) row[j] = p;
+          s[j] = scales ? __ldg(scales + t * k + j) : 1.0f;
+        }
+      }
+      const Raw* src = reinterpret_cast<const Raw*>(dy) + t * nvec;
+      for (int v = sub * 32 + lane; v < nvec; v += 32 * kWarps) {
+        Raw val[kSlots];
+        const Raw d = __ldg(src + v);
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (row[j] >= 0)
+            val[j] = __ldg(reinterpret_cast<const Raw*>(rows) + static_cast<int64_t>(row[j]) * nvec + v);
+        float df[V::kN];
+        V::unpack(d, df);
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          if (row[j] == INT32_MIN) continue;
+          Raw out = zero;
+          if (row[j] >= 0) {
+            float f[V::kN], o[V::kN];
+            V::unpack(val[j], f);
+#pragma unroll
+            for (int c = 0; c < V::kN; ++c) {
+              dot[j] = fmaf(df[c], f[c], dot[j]);
+              o[c] = s[j] * df[c];
+            }
+            out = V::pack(o);
+          }
+          const int64_t r = row[j] < 0 ? ~row[j] : row[j];
+          __stcs(reinterpret_cast<Raw*>(drows) + r * nvec + v, out);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j)
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
+    if (kWarps == 1) {
+      if (t < n_tok && lane == 0)
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+          if (j < k) dscales[t * k + j] = dot[j];
+    } else {
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) s_dot[warp][j] = dot[j];
+      __syncthreads();
+      if (t < n_tok && sub == 0 && lane < k) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_dot[warp + w][lane];
+        dscales[t * k + lane] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The widest of 16, 8, 4 and 2 bytes that divides a row.
+int copy_bytes(int64_t row_bytes) {
+  return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : 2;
+}
+
+unsigned grid_of(int64_t blocks, int per_sm) {
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * per_sm;
+  return static_cast<unsigned>(blocks < 1 ? 1 : blocks < cap ? blocks : cap);
+}
+
+template <int kBytes>
+cudaError_t launch_place(const SortArgs& a, bool self, const void* x, void* x_perm, int nvec,
+                         cudaStream_t s) {
+  if (self)
+    return launch_pdl(sort_place_kernel<kBytes, true>, dim3(a.nb), dim3(kSortThreads), 0, s, a,
+                      static_cast<const char*>(x), static_cast<char*>(x_perm), nvec);
+  return launch_pdl(sort_place_kernel<kBytes, false>, dim3(a.nb), dim3(kSortThreads), 0, s, a,
+                    static_cast<const char*>(x), static_cast<char*>(x_perm), nvec);
+}
+
+template <typename T, int kBytes, int kSlots>
+cudaError_t combine_t(const void* rows, const int32_t* inv, const float* scales, int64_t n_tok,
+                      int H, int k, void* y, cudaStream_t s) {
+  const int nvec = H / Vec<T, kBytes>::kN;
+  const int64_t blocks = (n_tok * nvec + kSortThreads - 1) / kSortThreads;
+  return launch_pdl(combine_kernel<T, kBytes, kSlots>, dim3(grid_of(blocks, 32)),
+                    dim3(kSortThreads), 0, s, static_cast<const T*>(rows), inv, scales, n_tok, k,
+                    nvec, static_cast<T*>(y));
+}
+
+template <typename T, int kBytes, int kSlots>
+cudaError_t combine_grad_t(const void* dy, const void* rows, const int32_t* inv,
+                           const float* scales, int64_t n_tok, int H, int k, void* drows,
+                           float* dscales, cudaStream_t s) {
+  const int nvec = H / Vec<T, kBytes>::kN;
+  return launch_pdl(combine_grad_kernel<T, kBytes, kSlots, kSortWarps>, dim3(grid_of(n_tok, 32)),
+                    dim3(kSortThreads), 0, s, static_cast<const T*>(dy),
+                    static_cast<const T*>(rows), inv, scales, n_tok, k, nvec,
+                    static_cast<T*>(drows), dscales);
+}
+
+// Calls f<T, bytes, slots>() for the type, the vector width that H allows and k rounded up.
+template <typename F>
+cudaError_t by_form(int dtype, int H, int k, const F& f) {
+  auto slots = [&](auto t, auto bytes) {
+    using T = decltype(t);
+    constexpr int kB = decltype(bytes)::value;
+    if (k == 1) return f.template operator()<T, kB, 1>();
+    if (k == 2) return f.template operator()<T, kB, 2>();
+    if (k <= 4) return f.template operator()<T, kB, 4>();
+    return f.template operator()<T, kB, 8>();
+  };
+  auto width = [&](auto t) {
+    using T = decltype(t);
+    if (static_cast<int64_t>(H) * sizeof(T) % 16 == 0)
+      return slots(t, std::integral_constant<int, 16>());
+    return slots(t, std::integral_constant<int, static_cast<int>(sizeof(T))>());
+  };
+  if (dtype == MOE_DTYPE_BF16) return width(__nv_bfloat16());
+  if (dtype == MOE_DTYPE_F16) return width(__half());
+  return width(float());
+}
+
+struct CombineCall {
+  const void* rows;
+  const int32_t* inv;
+  const float* scales;
+  int64_t T;
+  int H, k;
+  void* y;
+  cudaStream_t s;
+  template <typename E, int kBytes, int kSlots>
+  cudaError_t operator()() const {
+    return combine_t<E, kBytes, kSlots>(rows, inv, scales, T, H, k, y, s);
+  }
+};
+
+struct CombineGradCall {
+  const void* dy;
+  const void* rows;
+  const int32_t* inv;
+  const float* scales;
+  int64_t T;
+  int H, k;
+  void* drows;
+  float* dscales;
+  cudaStream_t s;
+  template <typename E, int kBytes, int kSlots>
+  cudaError_t operator()() const {
+    return combine_grad_t<E, kBytes, kSlots>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
+  }
+};
+
+int elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// Problems of at most this many slots are sorted and copied in one launch.
+constexpr int64_t kSelfCountMax = 4096;
+
+void chunk_plan(int64_t T, int64_t* chunk, int* nb) {
+  const int64_t cap = 152 * 4;
+  *chunk = (T + cap - 1) / cap;
+  *nb = static_cast<int>((T + *chunk - 1) / *chunk);
+}
+
+}  // namespace
+
+size_t dispatch_workspace_bytes(int64_t T, int E) {
+  int64_t chunk = 1;
+  int nb = 1;
+  if (T > 0) chunk_plan(T, &chunk, &nb);
+  return 16 + 4 * (static_cast<size_t>(E) + static_cast<size_t>(E + 2) * nb);
+}
+
+moe_status launch_dispatch(const void* x, const int32_t* ids, int64_t T, int H, int E, int k,
+                           int dtype, void* x_perm, int32_t* inv, int32_t* offsets, char* ws,
+                           cudaStream_t s) {
+  SortArgs a;
+  a.ids = ids;
+  a.T = T;
+  a.P = T * k;
+  a.E = E;
+  a.k = k;
+  chunk_plan(T, &a.chunk, &a.nb);
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.totals = a.status + 4;
+  a.hist = a.totals + E;
+  a.inv = inv;
+  a.offsets = offsets;
+  const bool self = a.P <= kSelfCountMax;
+  cudaError_t err = cudaSuccess;
+  if (!self) {
+    err = launch_pdl(sort_count_kernel, dim3(a.nb), dim3(kSortThreads), 0, s, a);
+    if (err == cudaSuccess)
+      err = launch_pdl(sort_scan_kernel, dim3((E + 2 + kSortWarps - 1) / kSortWarps),
+                       dim3(kSortThreads), 0, s, a);
+  }
+  if (err == cudaSuccess) {
+    const int64_t row = static_cast<int64_t>(H) * elem_bytes(dtype);
+    const int cb = copy_bytes(row);
+    const int nvec = static_cast<int>(row / cb);
+    err = cb == 16  ? launch_place<16>(a, self, x, x_perm, nvec, s)
+          : cb == 8 ? launch_place<8>(a, self, x, x_perm, nvec, s)
+          : cb == 4 ? launch_place<4>(a, self, x, x_perm, nvec, s)
+                    : launch_place<2>(a, self, x, x_perm, nvec, s);
+  }
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "dispatch launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+moe_status launch_dispatch_rows(const void* x, const int32_t* inv, int64_t T, int H, int k,
+                                int dtype, void* x_perm, cudaStream_t s) {
+  const int64_t row = static_cast<int64_t>(H) * elem_bytes(dtype);
+  const int cb = copy_bytes(row);
+  const int nvec = static_cast<int>(row / cb);
+  const dim3 grid(grid_of(T, 16)), block(kSortThreads);
+  const char* in = static_cast<const char*>(x);
+  char* out = static_cast<char*>(x_perm);
+  const cudaError_t err =
+      cb == 16  ? launch_pdl(dispatch_rows_kernel<16>, grid, block, 0, s, in, inv, T, k, nvec, out)
+      : cb == 8 ? launch_pdl(dispatch_rows_kernel<8>, grid, block, 0, s, in, inv, T, k, nvec, out)
+      : cb == 4 ? launch_pdl(dispatch_rows_kernel<4>, grid, block, 0, s, in, inv, T, k, nvec, out)
+                : launch_pdl(dispatch_rows_kernel<2>, grid, block, 0, s, in, inv, T, k, nvec, out);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "dispatch_rows launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+moe_status launch_combine(const void* rows, const int32_t* inv, const float* scales, int64_t T,
+                          int H, int k, int dtype, void* y, cudaStream_t s) {
+  const cudaError_t err = by_form(dtype, H, k, CombineCall{rows, inv, scales, T, H, k, y, s});
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "combine launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+moe_status launch_combine_backward(const void* dy, const void* rows, const int32_t* inv,
+                                   const float* scales, int64_t T, int H, int k, int dtype,
+                                   void* drows, float* dscales, cudaStream_t s) {
+  const cudaError_t err =
+      by_form(dtype, H, k, CombineGradCall{dy, rows, inv, scales, T, H, k, drows, dscales, s});
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "combine_backward launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+}  // namespace moe

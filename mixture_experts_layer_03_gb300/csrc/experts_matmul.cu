@@ -1,0 +1,633 @@
+// The experts' matrix products over ragged groups of rows, with their gradients:
+//   forward   y[r]  = x[r] . w[e]^T           rows r of expert e, w [E, N, K]
+//   dx        dx[r] = dy[r] . w[e]
+//   dw        dw[e] = sum_{r of e} dy[r]^T . x[r]
+// Rows of expert e are [offsets[e], offsets[e+1]), offsets on the device. Rows past offsets[E]
+// are 0 in y and dx; an expert without rows has dw = 0.
+//
+// One persistent kernel over all groups, CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 tiles,
+// fp32 accumulators in TMEM, 64 elements of the contraction a block). The three products differ
+// in which operand runs along the contraction in memory, and the tensor cores take either layout
+// from shared memory, so nothing is transposed:
+//            A (M = 256)                       B (N = 256)                 contraction
+//   forward  x rows, K-major                   w[e] rows, K-major          K
+//   dx       dy rows, K-major                  w[e], N-major               N
+//   dw       dy, M-major (its columns are M)   x, N-major                  the expert's rows
+// A group's last block of rows is ragged. In forward and dx those rows are rows of the result: the
+// tile computes whatever follows the group and the epilogue leaves it out. In dw they are the
+// contraction, where another expert's rows must not enter: every expert gets its own pair of
+// tensor maps whose row count ends at its last row, so that TMA fills what is beyond with zeros
+// (a small kernel writes the maps; 0 * NaN cannot reach a neighbour's gradient).
+//
+// Tiles go to the CTA pairs in order, pair i taking tiles i, i + pairs, ...: neighbouring tiles
+// (eight row blocks by the columns) share operands in L2, and tiles of one expert cost the same,
+// so the pairs stay level without a counter. Every result element is written by one CTA from one
+// accumulator: the same result on every run.
+//
+// Warp roles (192 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first
+// CTA, MMA issuer, warps 2-5 epilogue (TMEM lanes 32 * (warp % 4) .. + 31). Two accumulators let
+// the epilogue of a tile overlap the next one's mainloop.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+#include "tmap.cuh"
+
+namespace moe {
+namespace {
+
+enum : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+constexpr int kXBK = 64;                      // contraction elements a block
+constexpr int kXSlotBytes = 128 * kXBK * 2;   // one operand of one block in one CTA
+constexpr int kXSlots = 6;
+constexpr int kXPerStage = 2;                 // blocks a pipeline stage
+constexpr int kXStages = kXSlots / kXPerStage;
+constexpr int kXAccCols = 256;
+constexpr int kXTmemCols = 512;
+constexpr int kXThreads = 192;
+constexpr int kXGroups = 257;                 // up to 256 experts, then the rows past the last
+constexpr int kXRowBlocks = 8;                // row blocks that are walked together
+constexpr int kXBoxBytes = 2048;              // an epilogue box: 32 rows of 64 bytes
+constexpr int kXSmemBytes = 1024 + 2 * kXSlots * kXSlotBytes + 4 * 2 * kXBoxBytes;
+constexpr uint16_t kXPairMask = 0x3;
+
+struct ExpertsArgs {
+  const int32_t* offsets;   // [E + 1]
+  int32_t E;
+  int32_t R;                // rows of x, dy, y, dx
+  int32_t m_ext;            // dw: rows of a dw[e] (N); else unused
+  int32_t n_ext;            // columns of the result
+  int32_t k_ext;            // forward, dx: the contraction
+  int32_t f16;              // 16-bit type: 0 bf16, 1 f16
+  int32_t add;              // dw, f32: add to what is there
+  void* out;                // forward, dx: the result rows (masked stores)
+  const CUtensorMap* maps;  // dw: [2][E] maps of dy and of x, cut off at each expert's end
+  int32_t* status;          // or NULL
+};
+
+struct Tile {
+  int g;
+  int a0;       // first row of the result tile in this CTA (forward, dx: a row of x; dw: of dw[g])
+  int valid;    // rows of it that exist, 0..128
+  int peer;     // the same in the other CTA
+  int n0;       // first column of the result tile
+  int k0;       // dw: first row of the contraction
+  int nkb;      // contraction blocks; 0: the tile is zeros
+};
+
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+
+template <int kMode>
+__device__ __forceinline__ Tile decode_tile(int idx, const int32_t* s_off, const int32_t* s_start,
+                                            const int32_t* s_rows, int G, const ExpertsArgs& a,
+                                            int rank) {
+  int lo = 0, hi = G;   // s_off[lo] <= idx < s_off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_off[mid] <= idx) lo = mid;
+    else hi = mid;
+  }
+  Tile t;
+  t.g = lo;
+  const int rows = kMode == kDw ? a.m_ext : s_rows[lo];   // rows of the result
+  const int mt = (rows + 255) >> 8, nt = (a.n_ext + 255) >> 8;
+  const int local = idx - s_off[lo];
+  const int mb = local / (kXRowBlocks * nt);
+  const int rest = local - mb * kXRowBlocks * nt;
+  const int here = min(kXRowBlocks, mt - mb * kXRowBlocks);
+  const int n = rest / here;
+  const int m = mb * kXRowBlocks + rest - n * here;
+  const int base = kMode == kDw ? 0 : s_start[lo];
+  t.a0 = base + m * 256 + 128 * rank;
+  t.valid = clamp_int(base + rows - t.a0, 0, 128);
+  t.peer = clamp_int(base + rows - (base + m * 256 + 128 * (rank ^ 1)), 0, 128);
+  t.n0 = n * 256;
+  t.k0 = kMode == kDw ? s_start[lo] : 0;
+  t.nkb = ((kMode == kDw ? s_rows[lo] : lo < a.E ? a.k_ext : 0) + kXBK - 1) / kXBK;
+  return t;
+}
+
+__device__ __forceinline__ void x_timeout(int32_t* status, volatile int* abort) {
+  *abort = 1;
+  if (status) atomicOr(status, MOE_DEVICE_FLAG_TIMEOUT);
+}
+
+// The loads of one tile in this CTA. A: its 128 rows (skipped where none of them exists: what the
+// stage holds then only reaches rows that are not stored); B: its half of the 256 columns. An
+// operand along the contraction is one box of 128 rows; one across it is two boxes of 64 columns.
+template <int kMode>
+__device__ __forceinline__ bool produce_tile(const Tile& t, const CUtensorMap* ma,
+                                             const CUtensorMap* mb, int rank, int& fills,
+                                             uint8_t* sA, uint8_t* sB, uint32_t lead_full,
+                                             uint64_t* full_bar, uint64_t* empty_bar,
+                                             volatile int* abort) {
+  const uint32_t tx = kXSlotBytes * (2u + (t.valid > 0) + (t.peer > 0));
+  const int bn = t.n0 + 128 * rank;
+  for (int kb = 0; kb < t.nkb; kb += kXPerStage) {
+    const int nk = min(t.nkb - kb, kXPerStage);
+    const int stage = fills % kXStages;
+    if (!mbar_wait<true>(&empty_bar[stage], ((fills / kXStages) & 1) ^ 1u, abort)) return false;
+    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], nk * tx);
+    const uint32_t fb = lead_full + 8u * stage;
+    for (int b = 0; b < nk; ++b) {
+      uint8_t* as = sA + (stage * kXPerStage + b) * kXSlotBytes;
+      uint8_t* bs = sB + (stage * kXPerStage + b) * kXSlotBytes;
+      const int kc = t.k0 + (kb + b) * kXBK;
+      if (t.valid > 0) {
+        if (kMode == kDw) {
+          tma_load_2d_pair(as, ma, fb, t.a0, kc);
+          tma_load_2d_pair(as + kXSlotBytes / 2, ma, fb, t.a0 + 64, kc);
+        } else {
+          tma_load_2d_pair(as, ma, fb, kc, t.a0);
+        }
+      }
+      if (kMode == kFwd) {
+        tma_load_3d_pair(bs, mb, fb, kc, bn, t.g);
+      } else if (kMode == kDx) {
+        tma_load_3d_pair(bs, mb, fb, bn, kc, t.g);
+        tma_load_3d_pair(bs + kXSlotBytes / 2, mb, fb, bn + 64, kc, t.g);
+      } else {
+        tma_load_2d_pair(bs, mb, fb, bn, kc);
+        tma_load_2d_pair(bs + kXSlotBytes / 2, mb, fb, bn + 64, kc);
+      }
+    }
+    ++fills;
+  }
+  return true;
+}
+
+template <int kMode>
+__device__ __forceinline__ bool multiply_tile(uint32_t d, uint32_t idesc, int nkb, int& stage,
+                                              uint32_t& phase, uint64_t da0, uint64_t db0,
+                                              uint64_t* full_bar, uint64_t* empty_bar,
+                                              volatile int* abort) {
+  // 16 elements of the contraction further on: 32 bytes inside the rows, or 16 rows of 128 bytes.
+  constexpr uint32_t kStepA = (kMode == kDw ? 2048u : 32u) >> 4;
+  constexpr uint32_t kStepB = (kMode == kFwd ? 32u : 2048u) >> 4;
+  for (int kb = 0; kb < nkb; kb += kXPerStage) {
+    if (!mbar_wait<true>(&full_bar[stage], phase, abort)) return false;
+    tc_fence_after();
+    const uint32_t at = (stage * kXPerStage * kXSlotBytes) >> 4;
+#pragma unroll
+    for (int b = 0; b < kXPerStage; ++b) {
+      if (b > 0 && kb + b >= nkb) break;
+#pragma unroll
+      for (int kk = 0; kk < kXBK / 16; ++kk)
+        umma_bf16_pair(d, da0 + at + b * (kXSlotBytes >> 4) + kk * kStepA,
+                       db0 + at + b * (kXSlotBytes >> 4) + kk * kStepB, idesc, (kb | b | kk) != 0);
+    }
+    umma_commit_pair(&empty_bar[stage], kXPairMask);
+    if (++stage == kXStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One warp's 32 rows of a tile, a box of 64 bytes of columns (32 or 16 of them) at a time. Whole
+// boxes go through shared memory and TMA, which leaves out what lies beyond the tensor (N, and
+// for dw its rows); a warp that holds the last rows of a group in forward or dx stores those
+// from registers.
+template <int kMode, bool kF32>
+__device__ __forceinline__ void store_tile(uint32_t tb, const Tile& t, int q, int lane,
+                                           uint8_t* stage, int& sbuf, const CUtensorMap* map,
+                                           const ExpertsArgs& a) {
+  constexpr int kCols = kF32 ? 16 : 32;
+  const int rows = clamp_int(t.valid - 32 * q, 0, 32);
+  if (rows == 0) return;
+  const bool whole = kMode == kDw || rows == 32;
+  const bool f16 = a.f16 != 0;
+  const int sw = (lane >> 1) & 3;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 256; c0 += kCols) {
+    if (t.n0 + c0 >= a.n_ext) break;
+    float va[16] = {}, vb[16] = {};
+    uint4 v[4];
+    if (kF32) {
+      if (t.nkb > 0) tmem_ld_x16(tb + c0, va);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_uint4(__float_as_uint(va[4 * i]), __float_as_uint(va[4 * i + 1]),
+                          __float_as_uint(va[4 * i + 2]), __float_as_uint(va[4 * i + 3]));
+    } else {
+      if (t.nkb > 0) tmem_ld2_x16(tb + c0, tb + c0 + 16, va, vb);
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        pk[i] = pack_16bit(va[2 * i], va[2 * i + 1], f16);
+        pk[8 + i] = pack_16bit(vb[2 * i], vb[2 * i + 1], f16);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+    }
+    if (!whole) {
+      if (lane < rows) {
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        static_cast<int64_t>(t.a0 + 32 * q + lane) * a.n_ext + t.n0 + c0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // n_ext is a multiple of 8
+          if (t.n0 + c0 + 8 * i < a.n_ext) reinterpret_cast<uint4*>(dst)[i] = v[i];
+      }
+      continue;
+    }
+    uint8_t* buf = stage + sbuf * kXBoxBytes;
+    // The box stored from this buffer two boxes ago must have been read out of it.
+    if (lane == 0) bulk_wait_group_read<1>();
+    __syncwarp();
+    uint4* row = reinterpret_cast<uint4*>(buf + lane * 64);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row[i ^ sw] = v[i];
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (kMode != kDw) tma_store_2d(map, buf, t.n0 + c0, t.a0 + 32 * q);
+      else if (kF32 && a.add) tma_add_3d(map, buf, t.n0 + c0, t.a0 + 32 * q, t.g);
+      else tma_store_3d(map, buf, t.n0 + c0, t.a0 + 32 * q, t.g);
+      bulk_commit_group();
+    }
+    sbuf ^= 1;
+  }
+}
+
+template <int kMode, bool kF32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
+experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_out, ExpertsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_bar[kXStages], empty_bar[kXStages];
+  __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+  __shared__ int32_t s_off[kXGroups + 1], s_start[kXGroups], s_rows[kXGroups];
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool lead = rank == 0;
+  // 1024-byte aligned stages, at the same offsets in both CTAs.
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  uint8_t* sB = sA + kXSlots * kXSlotBytes;
+  uint8_t* sOut = sB + kXSlots * kXSlotBytes;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(&full_bar[s], 1);    // first CTA: its producer's arrival and both CTAs' bytes
+      mbar_init(&empty_bar[s], 1);   // the pair commit, delivered to both CTAs
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull_bar[s], 1);
+      mbar_init(&tempty_bar[s], 8);  // first CTA: the epilogue warps of both CTAs
+    }
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    tma_prefetch_map(&map_out);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem_base, kXTmemCols);   // collective with the other CTA's warp 1
+    tmem_relinquish_pair();
+  }
+  pdl_wait();
+  // The groups and the exclusive scan of their tiles. Offsets are kept inside [0, R] and in
+  // order here, so that none of them can lead a load or a store out of range.
+  const int G = kMode == kDw ? a.E : a.E + 1;
+  if (warp == 2) {
+    const int nt = (a.n_ext + 255) >> 8;
+    constexpr int kPer = kXGroups / 32 + 1;   // 32 * kPer > kXGroups: a lane reaches s_off[G]
+    int tiles[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = lane * kPer + i;
+      tiles[i] = 0;
+      if (g < G) {
+        const int start = clamp_int(a.offsets[g], 0, a.R);
+        const int end = g < a.E ? clamp_int(a.offsets[g + 1], start, a.R) : a.R;
+        s_start[g] = start;
+        s_rows[g] = end - start;
+        const int mt = ((kMode == kDw ? a.m_ext : end - start) + 255) >> 8;
+        tiles[i] = mt * nt;
+      }
+      sum += tiles[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = lane * kPer + i;
+      if (g <= G) s_off[g] = at;
+      at += tiles[i];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any remote arrival or copy
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem_base;
+  volatile int* abort = &s_abort;
+  const int total = s_off[G];
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
+  const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      int fills = 0, last_g = -1;
+      for (int idx = first; idx < total; idx += step) {
+        const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, rank);
+        if (t.nkb == 0) continue;
+        const CUtensorMap* ma = &map_a;
+        const CUtensorMap* mb = &map_b;
+        if (kMode == kDw) {
+          ma = a.maps + t.g;
+          mb = a.maps + a.E + t.g;
+          if (t.g != last_g) {
+            tmap_acquire(ma);
+            tmap_acquire(mb);
+            last_g = t.g;
+          }
+        }
+        if (!produce_tile<kMode>(t, ma, mb, rank, fills, sA, sB, lead_full, full_bar, empty_bar,
+                                 abort)) {
+          x_timeout(a.status, abort);
+          break;
+        }
+      }
+      // The commits of the last stages arrive in this CTA's barriers before it may leave.
+      volatile int never = 0;
+      for (int f = fills > kXStages ? fills - kXStages : 0; f < fills; ++f)
+        mbar_wait<true>(&empty_bar[f % kXStages], (f / kXStages) & 1, &never);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && lead) {
+      // ------------------------------------------------------------ MMA issuer (first CTA)
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t da0 = kMode == kDw ? sdesc_mn_major(smem_u32(sA), kXSlotBytes / 2)
+                                        : sdesc_k_major(smem_u32(sA), 128);
+      const uint64_t db0 = kMode == kFwd ? sdesc_k_major(smem_u32(sB), 128)
+                                         : sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2);
+      const uint32_t idesc = idesc_16bit_f32(256, 256, a.f16 != 0, kMode == kDw, kMode != kFwd);
+      for (int idx = first; idx < total; idx += step) {
+        const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, 0);
+        if (t.nkb == 0) continue;
+        ok = mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort);
+        if (ok) {
+          tc_fence_after();
+          ok = multiply_tile<kMode>(tmem_base + acc * kXAccCols, idesc, t.nkb, stage, phase, da0,
+                                    db0, full_bar, empty_bar, abort);
+        }
+        if (!ok) {
+          x_timeout(a.status, abort);
+          break;
+        }
+        umma_commit_pair(&tfull_bar[acc], kXPairMask);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // Every MMA issued so far ends (bounded wait) before TMEM is released.
+        umma_commit_pair(&drain_bar, 0x1);
+        volatile int never = 0;
+        mbar_wait(&drain_bar, 0, &never);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3;   // TMEM lane quarter of this warp
+    uint8_t* my_out = sOut + q * 2 * kXBoxBytes;
+    int sbuf = 0, acc = 0;
+    uint32_t acc_phase = 0;
+    for (int idx = first; idx < total; idx += step) {
+      const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, rank);
+      const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
+      if (t.nkb == 0) {
+        if (!(kF32 && a.add)) store_tile<kMode, kF32>(tb, t, q, lane, my_out, sbuf, &map_out, a);
+        continue;
+      }
+      const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
+      // Lanes may leave the poll at different times; tcgen05.ld is warp-collective.
+      if (!__all_sync(0xffffffffu, got)) {
+        x_timeout(a.status, abort);
+        break;
+      }
+      tc_fence_after();
+      store_tile<kMode, kF32>(tb, t, q, lane, my_out, sbuf, &map_out, a);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (lead) mbar_arrive(&tempty_bar[acc]);
+        else mbar_arrive_cluster(lead_tempty + 8u * acc);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    // Every TMA store of this warp has written its box before the CTA ends.
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kXTmemCols);   // collective with the other CTA's warp 1
+  }
+  // No CTA leaves while the other may still write into it or arrive on its barriers.
+  cluster_sync();
+}
+
+// The maps of dw: for each expert with rows, dy's and x's map with the row count cut off at the
+// expert's last row. One warp a map. Also clears the status word.
+__global__ void __launch_bounds__(256)
+experts_maps_kernel(const __grid_constant__ CUtensorMap map_dy,
+                    const __grid_constant__ CUtensorMap map_x, const int32_t* __restrict__ offsets,
+                    int E, int R, CUtensorMap* maps, int32_t* status) {
+  __shared__ __align__(128) CUtensorMap s_map[8];
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + warp;   // [0, E): dy's, [E, 2E): x's
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(i < E ? &map_dy : &map_x);
+  reinterpret_cast<uint32_t*>(&s_map[warp])[lane] = src[lane];
+  __syncwarp();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 4) status[threadIdx.x] = 0;
+  if (i >= 2 * E) return;
+  const int g = i < E ? i : i - E;
+  const int start = clamp_int(offsets[g], 0, R);
+  const int end = clamp_int(offsets[g + 1], start, R);
+  if (end == start) return;   // never loaded through
+  if (lane == 0) tmap_set_extent<1>(&s_map[warp], static_cast<uint32_t>(end));
+  __syncwarp();
+  tmap_publish(maps + i, &s_map[warp]);
+}
+
+// A tensor map of a 16-bit or f32 tensor [planes, rows, cols] (cols contiguous; planes 0: a
+// matrix), boxes of box_cols x box_rows, swizzled by `swizzle`.
+bool encode_any(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
+                CUtensorMapDataType type, uint32_t box_cols, uint32_t box_rows,
+                CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const uint64_t eb = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols * eb, rows * cols * eb};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, type, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The shared-memory opt-in of a kernel form and how many of its clusters can be resident, found
+// once a device (published after the attribute is set; a second thread does the same again).
+template <int kMode, bool kF32>
+moe_status prepare_form(int* max_clusters) {
+  static std::atomic<int> clusters_dev[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(MOE_ERR_CUDA, "cudaGetDevice failed");
+  int have = clusters_dev[dev].load(std::memory_order_acquire);
+  if (!have) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(experts_matmul_kernel<kMode, kF32>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmemBytes);
+    if (e != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    const int sms = device_sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+    cfg.blockDim = dim3(kXThreads, 1, 1);
+    cfg.dynamicSmemBytes = kXSmemBytes;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, experts_matmul_kernel<kMode, kF32>, &cfg) != cudaSuccess ||
+        n < 1) {
+      cudaGetLastError();   // clear the failed query; fall back to one cluster per SM pair
+      n = sms / 2;
+    }
+    clusters_dev[dev].store(n, std::memory_order_release);
+    have = n;
+  }
+  *max_clusters = have;
+  return MOE_OK;
+}
+
+template <int kMode, bool kF32>
+moe_status launch_form(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
+                       const ExpertsArgs& a, int64_t tiles, cudaStream_t s) {
+  int clusters = 1;
+  const moe_status st = prepare_form<kMode, kF32>(&clusters);
+  if (st != MOE_OK) return st;
+  if (clusters > tiles) clusters = static_cast<int>(tiles);
+  const cudaError_t err =
+      launch_pdl(experts_matmul_kernel<kMode, kF32>, dim3(2 * static_cast<unsigned>(clusters)),
+                 dim3(kXThreads), kXSmemBytes, s, ma, mb, mo, a);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "experts_matmul launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == MOE_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : dtype == MOE_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+}  // namespace
+
+size_t experts_workspace_bytes(int E) { return 128 + 2 * static_cast<size_t>(E) * sizeof(CUtensorMap); }
+
+moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
+                               int64_t R, int E, int N, int K, int dtype, void* out,
+                               int32_t* status, cudaStream_t s) {
+  const CUtensorMapDataType t = map_type(dtype);
+  const int kc = dx ? N : K, nc = dx ? K : N;   // contraction, columns of the result
+  CUtensorMap ma, mb, mo;
+  // w [E, N, K]: forward reads boxes of 64 K x 128 N rows, dx of 64 K (columns) x 64 N.
+  const bool ok =
+      encode_any(&ma, in, 0, R, kc, t, kXBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mb, w, E, N, K, t, 64, dx ? kXBK : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mo, out, 0, R, nc, t, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  ExpertsArgs a = {};
+  a.offsets = offsets;
+  a.E = E;
+  a.R = static_cast<int32_t>(R);
+  a.n_ext = nc;
+  a.k_ext = kc;
+  a.f16 = dtype == MOE_DTYPE_F16;
+  a.out = out;
+  a.status = status;
+  const int64_t tiles = (R / 256 + E + 1) * ((nc + 255) / 256);
+  return dx ? launch_form<kDx, false>(ma, mb, mo, a, tiles, s)
+            : launch_form<kFwd, false>(ma, mb, mo, a, tiles, s);
+}
+
+moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
+                             int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
+                             char* ws, cudaStream_t s) {
+  const CUtensorMapDataType t = map_type(dtype);
+  const bool f32 = out_dtype == MOE_DTYPE_F32;
+  CUtensorMap ma, mb, mo;
+  const bool ok =
+      encode_any(&ma, dy, 0, R, N, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mb, x, 0, R, K, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mo, dw, E, N, K, map_type(out_dtype), f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  ExpertsArgs a = {};
+  a.offsets = offsets;
+  a.E = E;
+  a.R = static_cast<int32_t>(R);
+  a.m_ext = N;
+  a.n_ext = K;
+  a.f16 = dtype == MOE_DTYPE_F16;
+  a.add = add;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(ws + 128);
+  a.maps = maps;
+  const cudaError_t err =
+      launch_pdl(experts_maps_kernel, dim3((2 * E + 7) / 8), dim3(256), 0, s, ma, mb, offsets, E,
+                 a.R, maps, a.status);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "experts_maps launch: %s", cudaGetErrorString(err));
+  const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
+  return f32 ? launch_form<kDw, true>(ma, mb, mo, a, tiles, s)
+             : launch_form<kDw, false>(ma, mb, mo, a, tiles, s);
+}
+
+}  // namespace moe

@@ -107,4 +107,40 @@ moe_status launch_gate(const void* x, const void* wg, int64_t T, int H, int E, i
 
 moe_status launch_cast_f32_bf16(const float* in, void* out, int64_t n, cudaStream_t s);
 
+// ---- training operators (dispatch.cu, swiglu_ckpt.cu, experts_matmul.cu, route_backward.cu);
+// dtype: a moe_dtype
+
+size_t dispatch_workspace_bytes(int64_t T, int E);
+moe_status launch_dispatch(const void* x, const int32_t* ids, int64_t T, int H, int E, int k,
+                           int dtype, void* x_perm, int32_t* inv, int32_t* offsets, char* ws,
+                           cudaStream_t s);
+moe_status launch_dispatch_rows(const void* x, const int32_t* inv, int64_t T, int H, int k,
+                                int dtype, void* x_perm, cudaStream_t s);
+// scales NULL: weight 1 everywhere
+moe_status launch_combine(const void* rows, const int32_t* inv, const float* scales, int64_t T,
+                          int H, int k, int dtype, void* y, cudaStream_t s);
+moe_status launch_combine_backward(const void* dy, const void* rows, const int32_t* inv,
+                                   const float* scales, int64_t T, int H, int k, int dtype,
+                                   void* drows, float* dscales, cudaStream_t s);
+
+moe_status launch_swiglu_ckpt(const void* gu, int64_t R, int I, int dtype, void* h, uint8_t* q,
+                              uint8_t* qs, cudaStream_t s);
+// h NULL: not wanted
+moe_status launch_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const uint8_t* qs,
+                                       int64_t R, int I, int dtype, void* dgu, void* h,
+                                       cudaStream_t s);
+
+size_t experts_workspace_bytes(int E);
+// dx false: out[r] = in[r] . w[e]^T ([R, K] -> [R, N]); true: out[r] = in[r] . w[e] ([R, N] ->
+// [R, K]). status (or NULL) receives device flags.
+moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
+                               int64_t R, int E, int N, int K, int dtype, void* out,
+                               int32_t* status, cudaStream_t s);
+moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
+                             int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
+                             char* ws, cudaStream_t s);
+
+moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* ds,
+                                 int64_t T, const moe_route_params& p, float* dl, cudaStream_t s);
+
 }  // namespace moe

@@ -159,6 +159,47 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// 3-D tiled store, and the same with an fp32 addition into global memory in place of the
+// write (one addition an element).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t c0,
+                                             int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int32_t c0,
+                                           int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// A tensor map in shared memory (128-byte aligned) gets another extent of dimension `kDim`,
+// by one thread; then the whole warp copies it to global memory (128-byte aligned), releasing it
+// to the tensor-map proxy.
+template <int kDim>
+__device__ __forceinline__ void tmap_set_extent(CUtensorMap* smem_map, uint32_t extent) {
+  asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], %1, %2;" ::"r"(
+                   smem_u32(smem_map)),
+               "n"(kDim), "r"(extent)
+               : "memory");
+}
+__device__ __forceinline__ void tmap_publish(CUtensorMap* global_map, const CUtensorMap* smem_map) {
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned"
+      " [%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(global_map)),
+      "r"(smem_u32(smem_map))
+      : "memory");
+}
+// Before the first TMA through a map that an earlier kernel published.
+__device__ __forceinline__ void tmap_acquire(const CUtensorMap* global_map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(global_map))
+               : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -354,6 +395,29 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same for 16-bit operands of either type (both bf16 or both f16: type field 1 or 0) and
+// either layout: an operand whose rows run along M or N instead of K sets bit 15 (A) or 16 (B).
+__host__ __device__ constexpr uint32_t idesc_16bit_f32(int M, int N, bool f16, bool a_mn,
+                                                       bool b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor for an M- or N-major tile: boxes of 64 elements (128 bytes)
+// along M/N by `box_bytes` / 128 rows of K, written by TMA with the 128-byte swizzle, one after
+// the other. Leading byte offset: from one box to the next (64 further along M/N); stride byte
+// offset: 8 rows of K. 16 elements of K are 2048 bytes further.
+__device__ __forceinline__ uint64_t sdesc_mn_major(uint32_t saddr, uint32_t box_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(box_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
 }
 
 // Shared-memory matrix descriptor for a K-major tile written by TMA with a swizzle as
