@@ -401,7 +401,7 @@ moe_status moe_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const uint
  *   moe_experts_matmul_dw   dw [E, N, K]: dw[e] = sum over e's rows of dy[r]^T . x[r]
  * Rows from offsets[E] on are zeros in y and dx; an expert without rows has dw = 0. fp32
  * accumulation, one rounding. dtype BF16 or F16; dw_dtype the same or F32, and with F32
- * `accumulate` adds to what dw holds. N and K: multiples of 8 up to 65536; R <= 2^26.
+ * `accumulate` adds to what dw holds. N and K: multiples of 8 up to 65536; R <= 2^23.
  * Workspace: for dw moe_experts_workspace_bytes(E) bytes (0 outside 1..256), 128-byte aligned,
  * not cleared by the caller, its status word cleared by the call. The other two take NULL, or at
  * least 16 bytes whose status word (cleared by the caller once) receives

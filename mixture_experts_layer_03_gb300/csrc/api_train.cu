@@ -29,8 +29,8 @@ moe_status check_rows(int64_t T, int32_t H, int32_t k, int dtype) {
 }
 
 moe_status check_experts(int64_t R, int32_t E, int32_t N, int32_t K, int dtype) {
-  if (R < 0 || R > (int64_t{1} << 26))
-    return set_error(MOE_ERR_UNSUPPORTED, "R %lld outside [0, 2^26]", static_cast<long long>(R));
+  if (R < 0 || R > (int64_t{1} << 23))
+    return set_error(MOE_ERR_UNSUPPORTED, "R %lld outside [0, 2^23]", static_cast<long long>(R));
   if (E < 1 || E > 256) return set_error(MOE_ERR_UNSUPPORTED, "E %d outside [1, 256]", E);
   if (N < 8 || N % 8 != 0 || N > 65536 || K < 8 || K % 8 != 0 || K > 65536)
     return set_error(MOE_ERR_UNSUPPORTED, "N %d and K %d must be multiples of 8 in [8, 65536]", N, K);

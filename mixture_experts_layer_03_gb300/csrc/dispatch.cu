@@ -23,7 +23,6 @@ namespace {
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 257;        // up to 256 experts, then the dropped slots
-constexpr int kMaxSlots = 8;
 
 // The expert bin of an id: [0, E), or E for a dropped slot.
 __device__ __forceinline__ int bin_of(int id, int E) { return id >= 0 && id < E ? id : E; }

@@ -24,9 +24,9 @@
 // so the pairs stay level without a counter. Every result element is written by one CTA from one
 // accumulator: the same result on every run.
 //
-// Warp roles (192 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first
-// CTA, MMA issuer, warps 2-5 epilogue (TMEM lanes 32 * (warp % 4) .. + 31). Two accumulators let
-// the epilogue of a tile overlap the next one's mainloop.
+// Warp roles (320 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first
+// CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, 128 columns each). Two
+// accumulators let the epilogue of a tile overlap the next one's mainloop.
 #include <atomic>
 #include <cstdint>
 
@@ -50,11 +50,12 @@ constexpr int kXPerStage = 2;                 // blocks a pipeline stage
 constexpr int kXStages = kXSlots / kXPerStage;
 constexpr int kXAccCols = 256;
 constexpr int kXTmemCols = 512;
-constexpr int kXThreads = 192;
+constexpr int kXEpiWarps = 8;                 // two per TMEM lane quarter, 128 columns each
+constexpr int kXThreads = 64 + 32 * kXEpiWarps;
 constexpr int kXGroups = 257;                 // up to 256 experts, then the rows past the last
 constexpr int kXRowBlocks = 8;                // row blocks that are walked together
-constexpr int kXBoxBytes = 2048;              // an epilogue box: 32 rows of 64 bytes
-constexpr int kXSmemBytes = 1024 + 2 * kXSlots * kXSlotBytes + 4 * 2 * kXBoxBytes;
+constexpr int kXBoxBytes = 4096;              // an epilogue warp's box: 32 rows of 128 bytes
+constexpr int kXSmemBytes = 1024 + 2 * kXSlots * kXSlotBytes + kXEpiWarps * kXBoxBytes;
 constexpr uint16_t kXPairMask = 0x3;
 
 struct ExpertsArgs {
@@ -79,39 +80,55 @@ struct Tile {
   int n0;       // first column of the result tile
   int k0;       // dw: first row of the contraction
   int nkb;      // contraction blocks; 0: the tile is zeros
+  int nks;      // contraction steps of 16 elements, the last one filled up with zeros
 };
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
   return v < lo ? lo : v > hi ? hi : v;
 }
 
+// s_blk[g]: row blocks of 256 of the groups before g; s_start[g]: the first row of g (s_start[G]
+// the last one's end). Not used where every group has the same blocks (dw: s_blk).
 template <int kMode>
-__device__ __forceinline__ Tile decode_tile(int idx, const int32_t* s_off, const int32_t* s_start,
-                                            const int32_t* s_rows, int G, const ExpertsArgs& a,
-                                            int rank) {
-  int lo = 0, hi = G;   // s_off[lo] <= idx < s_off[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_off[mid] <= idx) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, const int32_t* s_start,
+                                            int G, const ExpertsArgs& a, int rank) {
+  const int nt = (a.n_ext + 255) >> 8;
+  const int blk = idx / nt;
+  int g, mt, before;
+  if (kMode == kDw) {
+    mt = (a.m_ext + 255) >> 8;
+    g = blk / mt;
+    before = g * mt;
+  } else {
+    int hi = G;
+    g = 0;   // s_blk[g] <= blk < s_blk[hi]
+    while (hi - g > 1) {
+      const int mid = (g + hi) >> 1;
+      if (s_blk[mid] <= blk) g = mid;
+      else hi = mid;
+    }
+    before = s_blk[g];
+    mt = s_blk[g + 1] - before;
   }
   Tile t;
-  t.g = lo;
-  const int rows = kMode == kDw ? a.m_ext : s_rows[lo];   // rows of the result
-  const int mt = (rows + 255) >> 8, nt = (a.n_ext + 255) >> 8;
-  const int local = idx - s_off[lo];
+  t.g = g;
+  const int start = s_start[g], in_group = s_start[g + 1] - start;
+  const int local = idx - before * nt;
   const int mb = local / (kXRowBlocks * nt);
   const int rest = local - mb * kXRowBlocks * nt;
   const int here = min(kXRowBlocks, mt - mb * kXRowBlocks);
   const int n = rest / here;
   const int m = mb * kXRowBlocks + rest - n * here;
-  const int base = kMode == kDw ? 0 : s_start[lo];
-  t.a0 = base + m * 256 + 128 * rank;
-  t.valid = clamp_int(base + rows - t.a0, 0, 128);
-  t.peer = clamp_int(base + rows - (base + m * 256 + 128 * (rank ^ 1)), 0, 128);
+  const int base = (kMode == kDw ? 0 : start) + m * 256;
+  const int end = kMode == kDw ? a.m_ext : start + in_group;
+  t.a0 = base + 128 * rank;
+  t.valid = clamp_int(end - t.a0, 0, 128);
+  t.peer = clamp_int(end - (base + 128 * (rank ^ 1)), 0, 128);
   t.n0 = n * 256;
-  t.k0 = kMode == kDw ? s_start[lo] : 0;
-  t.nkb = ((kMode == kDw ? s_rows[lo] : lo < a.E ? a.k_ext : 0) + kXBK - 1) / kXBK;
+  t.k0 = kMode == kDw ? start : 0;
+  const int len = kMode == kDw ? in_group : g < a.E ? a.k_ext : 0;
+  t.nkb = (len + kXBK - 1) / kXBK;
+  t.nks = (len + 15) / 16;
   return t;
 }
 
@@ -165,24 +182,25 @@ __device__ __forceinline__ bool produce_tile(const Tile& t, const CUtensorMap* m
 }
 
 template <int kMode>
-__device__ __forceinline__ bool multiply_tile(uint32_t d, uint32_t idesc, int nkb, int& stage,
+__device__ __forceinline__ bool multiply_tile(uint32_t d, uint32_t idesc, int nks, int& stage,
                                               uint32_t& phase, uint64_t da0, uint64_t db0,
                                               uint64_t* full_bar, uint64_t* empty_bar,
                                               volatile int* abort) {
   // 16 elements of the contraction further on: 32 bytes inside the rows, or 16 rows of 128 bytes.
   constexpr uint32_t kStepA = (kMode == kDw ? 2048u : 32u) >> 4;
   constexpr uint32_t kStepB = (kMode == kFwd ? 32u : 2048u) >> 4;
-  for (int kb = 0; kb < nkb; kb += kXPerStage) {
+  constexpr int kPer = kXPerStage * (kXBK / 16);   // instructions a full stage
+  for (int ks = 0; ks < nks; ks += kPer) {
     if (!mbar_wait<true>(&full_bar[stage], phase, abort)) return false;
     tc_fence_after();
     const uint32_t at = (stage * kXPerStage * kXSlotBytes) >> 4;
+    const uint64_t da = da0 + at, db = db0 + at;
 #pragma unroll
-    for (int b = 0; b < kXPerStage; ++b) {
-      if (b > 0 && kb + b >= nkb) break;
-#pragma unroll
-      for (int kk = 0; kk < kXBK / 16; ++kk)
-        umma_bf16_pair(d, da0 + at + b * (kXSlotBytes >> 4) + kk * kStepA,
-                       db0 + at + b * (kXSlotBytes >> 4) + kk * kStepB, idesc, (kb | b | kk) != 0);
+    for (int i = 0; i < kPer; ++i) {
+      if (ks + i >= nks) break;
+      const uint32_t b = (i / (kXBK / 16)) * (kXSlotBytes >> 4);
+      umma_bf16_pair(d, da + b + (i % (kXBK / 16)) * kStepA, db + b + (i % (kXBK / 16)) * kStepB,
+                     idesc, (ks | i) != 0);
     }
     umma_commit_pair(&empty_bar[stage], kXPairMask);
     if (++stage == kXStages) {
@@ -202,69 +220,87 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One warp's 32 rows of a tile, a box of 64 bytes of columns (32 or 16 of them) at a time. Whole
-// boxes go through shared memory and TMA, which leaves out what lies beyond the tensor (N, and
-// for dw its rows); a warp that holds the last rows of a group in forward or dx stores those
-// from registers.
-template <int kMode, bool kF32>
-__device__ __forceinline__ void store_tile(uint32_t tb, const Tile& t, int q, int lane,
-                                           uint8_t* stage, int& sbuf, const CUtensorMap* map,
-                                           const ExpertsArgs& a) {
-  constexpr int kCols = kF32 ? 16 : 32;
+// One warp's part of a tile: 32 rows (TMEM lane quarter q) by 128 columns, 64 of them at a time.
+// They go through shared memory, in boxes of 128 bytes of columns (64 16-bit or 32 f32 values), and
+// out by TMA, which leaves out what lies beyond the tensor (its columns, and for dw its rows); a
+// warp that holds the last rows of a group in forward or dx stores those from registers. `done`
+// runs once the accumulator has been read.
+// Two warps a lane quarter: a box costs a warp about 700 cycles of latency (TMEM load, fence, the
+// store's read of the box), so that four warps held 256 x 256 tiles of dw with short contractions
+// to 3.3 us (256 experts of 128 rows, N = 7168, K = 2048: 2.50 ms against 1.21 ms of traffic).
+template <int kMode, bool kF32, typename Done>
+__device__ __forceinline__ void store_tile(uint32_t tb, const Tile& t, int q, int half, int lane,
+                                           uint8_t* buf, const CUtensorMap* map,
+                                           const ExpertsArgs& a, Done&& done) {
   const int rows = clamp_int(t.valid - 32 * q, 0, 32);
-  if (rows == 0) return;
+  const int col = t.n0 + 128 * half;
+  if (rows == 0 || col >= a.n_ext) {
+    done();
+    return;
+  }
   const bool whole = kMode == kDw || rows == 32;
   const bool f16 = a.f16 != 0;
-  const int sw = (lane >> 1) & 3;
+  const int row = t.a0 + 32 * q;
+  uint4* mine = reinterpret_cast<uint4*>(buf + lane * 128);   // this lane's row of the box
 #pragma unroll 1
-  for (int c0 = 0; c0 < 256; c0 += kCols) {
-    if (t.n0 + c0 >= a.n_ext) break;
-    float va[16] = {}, vb[16] = {};
-    uint4 v[4];
-    if (kF32) {
-      if (t.nkb > 0) tmem_ld_x16(tb + c0, va);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = make_uint4(__float_as_uint(va[4 * i]), __float_as_uint(va[4 * i + 1]),
-                          __float_as_uint(va[4 * i + 2]), __float_as_uint(va[4 * i + 3]));
+  for (int c0 = 0; c0 < 128; c0 += 64) {
+    uint32_t v[64];
+    if (t.nkb > 0) {
+      tmem_ld_x64(tb + 128 * half + c0, v);
     } else {
-      if (t.nkb > 0) tmem_ld2_x16(tb + c0, tb + c0 + 16, va, vb);
-      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = 0;
+    }
+    const bool last = c0 == 64 || col + 64 >= a.n_ext;
+    if (last) done();
+    if (kF32) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (col + c0 + 32 * b >= a.n_ext) break;
+        if (lane == 0) bulk_wait_group_read<0>();   // the box before has been read out
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          mine[i ^ (lane & 7)] = make_uint4(v[32 * b + 4 * i], v[32 * b + 4 * i + 1],
+                                            v[32 * b + 4 * i + 2], v[32 * b + 4 * i + 3]);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (a.add) tma_add_3d(map, buf, col + c0 + 32 * b, row, t.g);
+          else tma_store_3d(map, buf, col + c0 + 32 * b, row, t.g);
+          bulk_commit_group();
+        }
+      }
+    } else {
+      uint4 o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        pk[i] = pack_16bit(va[2 * i], va[2 * i + 1], f16);
-        pk[8 + i] = pack_16bit(vb[2 * i], vb[2 * i + 1], f16);
-      }
+        uint32_t* w = reinterpret_cast<uint32_t*>(&o[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-    }
-    if (!whole) {
-      if (lane < rows) {
+        for (int j = 0; j < 4; ++j)
+          w[j] = pack_16bit(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]), f16);
+      }
+      if (whole) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine[i ^ (lane & 7)] = o[i];
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (kMode == kDw) tma_store_3d(map, buf, col + c0, row, t.g);
+          else tma_store_2d(map, buf, col + c0, row);
+          bulk_commit_group();
+        }
+      } else if (lane < rows) {
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        static_cast<int64_t>(t.a0 + 32 * q + lane) * a.n_ext + t.n0 + c0;
+                        static_cast<int64_t>(row + lane) * a.n_ext + col + c0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)   // n_ext is a multiple of 8
-          if (t.n0 + c0 + 8 * i < a.n_ext) reinterpret_cast<uint4*>(dst)[i] = v[i];
+        for (int i = 0; i < 8; ++i)   // n_ext is a multiple of 8
+          if (col + c0 + 8 * i < a.n_ext) reinterpret_cast<uint4*>(dst)[i] = o[i];
       }
-      continue;
     }
-    uint8_t* buf = stage + sbuf * kXBoxBytes;
-    // The box stored from this buffer two boxes ago must have been read out of it.
-    if (lane == 0) bulk_wait_group_read<1>();
-    __syncwarp();
-    uint4* row = reinterpret_cast<uint4*>(buf + lane * 64);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) row[i ^ sw] = v[i];
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      if (kMode != kDw) tma_store_2d(map, buf, t.n0 + c0, t.a0 + 32 * q);
-      else if (kF32 && a.add) tma_add_3d(map, buf, t.n0 + c0, t.a0 + 32 * q, t.g);
-      else tma_store_3d(map, buf, t.n0 + c0, t.a0 + 32 * q, t.g);
-      bulk_commit_group();
-    }
-    sbuf ^= 1;
+    if (last) break;
   }
 }
 
@@ -278,7 +314,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
-  __shared__ int32_t s_off[kXGroups + 1], s_start[kXGroups], s_rows[kXGroups];
+  __shared__ uint16_t s_blk[kXGroups + 1];
+  __shared__ int32_t s_start[kXGroups + 1];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -298,7 +335,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull_bar[s], 1);
-      mbar_init(&tempty_bar[s], 8);  // first CTA: the epilogue warps of both CTAs
+      mbar_init(&tempty_bar[s], 2 * kXEpiWarps);  // first CTA: the epilogue warps of both
     }
     mbar_init(&drain_bar, 1);
     s_abort = 0;
@@ -314,27 +351,31 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     tmem_relinquish_pair();
   }
   pdl_wait();
-  // The groups and the exclusive scan of their tiles. Offsets are kept inside [0, R] and in
-  // order here, so that none of them can lead a load or a store out of range.
+  // The groups: their first rows, kept inside [0, R] and in order here, so that no offset can
+  // lead a load or a store out of range, and the scan of their row blocks.
   const int G = kMode == kDw ? a.E : a.E + 1;
   if (warp == 2) {
-    const int nt = (a.n_ext + 255) >> 8;
-    constexpr int kPer = kXGroups / 32 + 1;   // 32 * kPer > kXGroups: a lane reaches s_off[G]
-    int tiles[kPer], sum = 0;
+    constexpr int kPer = kXGroups / 32 + 1;   // 32 * kPer > kXGroups: a lane reaches entry G
+    int start[kPer + 1], most = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = lane * kPer + i;
-      tiles[i] = 0;
-      if (g < G) {
-        const int start = clamp_int(a.offsets[g], 0, a.R);
-        const int end = g < a.E ? clamp_int(a.offsets[g + 1], start, a.R) : a.R;
-        s_start[g] = start;
-        s_rows[g] = end - start;
-        const int mt = ((kMode == kDw ? a.m_ext : end - start) + 255) >> 8;
-        tiles[i] = mt * nt;
-      }
-      sum += tiles[i];
+      // Group E of forward and dx: the rows past the last expert's, up to R.
+      start[i] = g <= a.E ? clamp_int(a.offsets[g], 0, a.R) : a.R;
+      if (i > 0) start[i] = max(start[i], start[i - 1]);
     }
+    most = start[kPer - 1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) most = max(most, __shfl_up_sync(0xffffffffu, most, off));
+    most = __shfl_up_sync(0xffffffffu, most, 1);
+    if (lane == 0) most = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) start[i] = max(start[i], most);
+    start[kPer] = __shfl_down_sync(0xffffffffu, start[0], 1);
+    if (lane == 31) start[kPer] = a.R;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += (start[i + 1] - start[i] + 255) >> 8;
     int incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -345,8 +386,11 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = lane * kPer + i;
-      if (g <= G) s_off[g] = at;
-      at += tiles[i];
+      if (g <= G) {
+        s_start[g] = start[i];
+        s_blk[g] = static_cast<uint16_t>(at);
+      }
+      at += (start[i + 1] - start[i] + 255) >> 8;
     }
   }
   tc_fence_before();
@@ -355,7 +399,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort = &s_abort;
-  const int total = s_off[G];
+  const int nt = (a.n_ext + 255) >> 8;
+  const int total = nt * (kMode == kDw ? a.E * ((a.m_ext + 255) >> 8) : s_blk[G]);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
@@ -365,7 +410,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       // ------------------------------------------------------------ TMA producer
       int fills = 0, last_g = -1;
       for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, rank);
+        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, rank);
         if (t.nkb == 0) continue;
         const CUtensorMap* ma = &map_a;
         const CUtensorMap* mb = &map_b;
@@ -401,12 +446,12 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
                                          : sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2);
       const uint32_t idesc = idesc_16bit_f32(256, 256, a.f16 != 0, kMode == kDw, kMode != kFwd);
       for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, 0);
+        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, 0);
         if (t.nkb == 0) continue;
         ok = mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort);
         if (ok) {
           tc_fence_after();
-          ok = multiply_tile<kMode>(tmem_base + acc * kXAccCols, idesc, t.nkb, stage, phase, da0,
+          ok = multiply_tile<kMode>(tmem_base + acc * kXAccCols, idesc, t.nks, stage, phase, da0,
                                     db0, full_bar, empty_bar, abort);
         }
         if (!ok) {
@@ -429,14 +474,16 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;   // TMEM lane quarter of this warp
-    uint8_t* my_out = sOut + q * 2 * kXBoxBytes;
-    int sbuf = 0, acc = 0;
+    const int half = (warp - 2) >> 2;
+    uint8_t* my_box = sOut + (warp - 2) * kXBoxBytes;
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = decode_tile<kMode>(idx, s_off, s_start, s_rows, G, a, rank);
+      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, rank);
       const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
       if (t.nkb == 0) {
-        if (!(kF32 && a.add)) store_tile<kMode, kF32>(tb, t, q, lane, my_out, sbuf, &map_out, a);
+        if (!(kF32 && a.add))
+          store_tile<kMode, kF32>(tb, t, q, half, lane, my_box, &map_out, a, [] {});
         continue;
       }
       const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
@@ -446,13 +493,14 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
         break;
       }
       tc_fence_after();
-      store_tile<kMode, kF32>(tb, t, q, lane, my_out, sbuf, &map_out, a);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (lead) mbar_arrive(&tempty_bar[acc]);
-        else mbar_arrive_cluster(lead_tempty + 8u * acc);
-      }
+      store_tile<kMode, kF32>(tb, t, q, half, lane, my_box, &map_out, a, [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (lead) mbar_arrive(&tempty_bar[acc]);
+          else mbar_arrive_cluster(lead_tempty + 8u * acc);
+        }
+      });
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
@@ -472,8 +520,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   cluster_sync();
 }
 
-// The maps of dw: for each expert with rows, dy's and x's map with the row count cut off at the
-// expert's last row. One warp a map. Also clears the status word.
+// The maps of dw: for each expert, dy's and x's map with the row count cut off at the expert's
+// last row. One warp a map. Also clears the status word.
 __global__ void __launch_bounds__(256)
 experts_maps_kernel(const __grid_constant__ CUtensorMap map_dy,
                     const __grid_constant__ CUtensorMap map_x, const int32_t* __restrict__ offsets,
@@ -489,9 +537,10 @@ experts_maps_kernel(const __grid_constant__ CUtensorMap map_dy,
   if (blockIdx.x == 0 && threadIdx.x < 4) status[threadIdx.x] = 0;
   if (i >= 2 * E) return;
   const int g = i < E ? i : i - E;
-  const int start = clamp_int(offsets[g], 0, R);
-  const int end = clamp_int(offsets[g + 1], start, R);
-  if (end == start) return;   // never loaded through
+  // The expert's end as the product's kernel has it: no less than any offset before it.
+  int end = 0;
+  for (int j = lane; j <= g + 1; j += 32) end = max(end, clamp_int(offsets[j], 0, R));
+  end = max(__reduce_max_sync(0xffffffffu, end), 1);   // (an extent of 0 is none; no rows, no load)
   if (lane == 0) tmap_set_extent<1>(&s_map[warp], static_cast<uint32_t>(end));
   __syncwarp();
   tmap_publish(maps + i, &s_map[warp]);
@@ -582,7 +631,7 @@ moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int
   const bool ok =
       encode_any(&ma, in, 0, R, kc, t, kXBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
       encode_any(&mb, w, E, N, K, t, 64, dx ? kXBK : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_any(&mo, out, 0, R, nc, t, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+      encode_any(&mo, out, 0, R, nc, t, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   ExpertsArgs a = {};
   a.offsets = offsets;
@@ -607,7 +656,7 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
   const bool ok =
       encode_any(&ma, dy, 0, R, N, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
       encode_any(&mb, x, 0, R, K, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_any(&mo, dw, E, N, K, map_type(out_dtype), f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+      encode_any(&mo, dw, E, N, K, map_type(out_dtype), f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   ExpertsArgs a = {};
   a.offsets = offsets;
