@@ -5,27 +5,32 @@
 // Rows of expert e are [offsets[e], offsets[e+1]), offsets on the device. Rows past offsets[E]
 // are 0 in y and dx; an expert without rows has dw = 0.
 //
-// One persistent kernel over all groups, CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 tiles,
-// fp32 accumulators in TMEM, 64 elements of the contraction a block). The three products differ
-// in which operand runs along the contraction in memory, and the tensor cores take either layout
-// from shared memory, so nothing is transposed:
-//            A (M = 256)                       B (N = 256)                 contraction
-//   forward  x rows, K-major                   w[e] rows, K-major          K
-//   dx       dy rows, K-major                  w[e], N-major               N
-//   dw       dy, M-major (its columns are M)   x, N-major                  the expert's rows
-// A group's last block of rows is ragged. In forward and dx those rows are rows of the result: the
-// tile computes whatever follows the group and the epilogue leaves it out. In dw they are the
-// contraction, where another expert's rows must not enter: every expert gets its own pair of
-// tensor maps whose row count ends at its last row, so that TMA fills what is beyond with zeros
-// (a small kernel writes the maps; 0 * NaN cannot reach a neighbour's gradient).
+// One persistent kernel over all groups, CTA pairs (tcgen05.mma.cta_group::2, M = 256, N up to 256,
+// fp32 accumulators in TMEM, 64 elements of the contraction a block). The tensor cores take an
+// operand from shared memory along the contraction (K-major) or across it (M- or N-major), so that
+// nothing is transposed on the way in:
+//            A, M = 256                          B, N <= 256             contraction
+//   forward  channels of w[e] (rows), K-major    x rows, K-major         K
+//   dx       channels of w[e] (columns), M-major dy rows, K-major        N
+//   dw       columns of dy, M-major              columns of x, N-major   the expert's rows
+//
+// Ragged rows. In forward and dx they are N, which the instruction takes in steps of 16: an expert's
+// rows are cut into equal tiles of at most 256, rounded up to 16, and little is multiplied that is
+// not wanted (with the rows as M = 256 the tiles of 512-row experts held a quarter of waste, which
+// the power limit turns into time). The result then lies channels by rows in TMEM and is turned over
+// in the epilogue's boxes. What a tile reads past its rows stays in columns that are not stored.
+// In dw the rows are the contraction, where another expert's must not enter: every expert gets
+// its own pair of tensor maps whose row count ends at its last row, so that TMA fills what is
+// beyond with zeros (a small kernel writes the maps; 0 * NaN cannot reach a neighbour's gradient),
+// and steps of 16 rows with nothing in them are not issued.
 //
 // Tiles go to the CTA pairs in order, pair i taking tiles i, i + pairs, ...: neighbouring tiles
-// (eight row blocks by the columns) share operands in L2, and tiles of one expert cost the same,
+// (eight row tiles by the channels) share operands in L2, and tiles of one expert cost the same,
 // so the pairs stay level without a counter. Every result element is written by one CTA from one
 // accumulator: the same result on every run.
 //
 // Warp roles (320 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first
-// CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, 128 columns each). Two
+// CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, two warps to each). Two
 // accumulators let the epilogue of a tile overlap the next one's mainloop.
 #include <atomic>
 #include <cstdint>
@@ -45,25 +50,23 @@ enum : int { kFwd = 0, kDx = 1, kDw = 2 };
 
 constexpr int kXBK = 64;                      // contraction elements a block
 constexpr int kXSlotBytes = 128 * kXBK * 2;   // one operand of one block in one CTA
-constexpr int kXSlots = 6;
-constexpr int kXPerStage = 2;                 // blocks a pipeline stage
-constexpr int kXStages = kXSlots / kXPerStage;
 constexpr int kXAccCols = 256;
 constexpr int kXTmemCols = 512;
 constexpr int kXEpiWarps = 8;                 // two per TMEM lane quarter, 128 columns each
 constexpr int kXThreads = 64 + 32 * kXEpiWarps;
 constexpr int kXGroups = 257;                 // up to 256 experts, then the rows past the last
 constexpr int kXRowBlocks = 8;                // row blocks that are walked together
-constexpr int kXBoxBytes = 4096;              // an epilogue warp's box: 32 rows of 128 bytes
-constexpr int kXSmemBytes = 1024 + 2 * kXSlots * kXSlotBytes + kXEpiWarps * kXBoxBytes;
+constexpr int kXStages = 6;                   // a block of both operands each
+constexpr int kXBoxBytes = 4096;              // epilogue staging of a warp
+constexpr int kXSmemBytes = 1024 + 2 * kXStages * kXSlotBytes + kXEpiWarps * kXBoxBytes;
 constexpr uint16_t kXPairMask = 0x3;
 
 struct ExpertsArgs {
   const int32_t* offsets;   // [E + 1]
   int32_t E;
   int32_t R;                // rows of x, dy, y, dx
-  int32_t m_ext;            // dw: rows of a dw[e] (N); else unused
-  int32_t n_ext;            // columns of the result
+  int32_t m_ext;            // forward, dx: columns of the result (M); dw: rows of a dw[e] (M)
+  int32_t n_ext;            // dw: columns of a dw[e] (N)
   int32_t k_ext;            // forward, dx: the contraction
   int32_t f16;              // 16-bit type: 0 bf16, 1 f16
   int32_t add;              // dw, f32: add to what is there
@@ -74,10 +77,12 @@ struct ExpertsArgs {
 
 struct Tile {
   int g;
-  int a0;       // first row of the result tile in this CTA (forward, dx: a row of x; dw: of dw[g])
-  int valid;    // rows of it that exist, 0..128
-  int peer;     // the same in the other CTA
-  int n0;       // first column of the result tile
+  int m0;       // this CTA's first index along M: a channel of the result, or a row of dw[g]
+  int m_here;   // how many of its 128 exist
+  int m_peer;   // the same of the other CTA
+  int n0;       // the pair's first index along N: a row, or a column of dw[g]
+  int n_here;   // how many exist, 1..256
+  int n;        // the instruction's N: n_here rounded up to 16
   int k0;       // dw: first row of the contraction
   int nkb;      // contraction blocks; 0: the tile is zeros
   int nks;      // contraction steps of 16 elements, the last one filled up with zeros
@@ -87,18 +92,43 @@ __device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
   return v < lo ? lo : v > hi ? hi : v;
 }
 
-// s_blk[g]: row blocks of 256 of the groups before g; s_start[g]: the first row of g (s_start[G]
-// the last one's end). Not used where every group has the same blocks (dw: s_blk).
+// n / d by a rounded 1 / d: exact for 0 <= n < 2^24 (the quotient is off by one at most, which the
+// remainder shows). The divisions of a tile's index are on the epilogue's path between two tiles.
+struct Div {
+  int d;
+  float inv;
+  __device__ __forceinline__ explicit Div(int d_) : d(d_), inv(1.0f / static_cast<float>(d_)) {}
+  __device__ __forceinline__ int operator()(int n) const {
+    const int q = static_cast<int>(static_cast<float>(n) * inv);
+    const int r = n - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+  }
+};
+
+// Divisors of a tile's index. "Outer" tiles are those of the rows in forward and dx and of M in dw,
+// "inner" ones those of M and of N: kXRowBlocks outer tiles by all inner ones make a set, walked
+// outer tile first.
+struct Walk {
+  Div inner, set, outer;
+  template <int kMode>
+  __device__ __forceinline__ static Walk of(const ExpertsArgs& a) {
+    const int inner = ((kMode == kDw ? a.n_ext : a.m_ext) + 255) >> 8;
+    return Walk{Div(inner), Div(inner * kXRowBlocks), Div(kMode == kDw ? (a.m_ext + 255) >> 8 : 1)};
+  }
+};
+
+// s_blk[g] (forward, dx): row tiles of the groups before g. s_start[g]: the first row of g;
+// s_start[G] the last one's end.
 template <int kMode>
 __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, const int32_t* s_start,
-                                            int G, const ExpertsArgs& a, int rank) {
-  const int nt = (a.n_ext + 255) >> 8;
-  const int blk = idx / nt;
-  int g, mt, before;
+                                            int G, const ExpertsArgs& a, const Walk& w,
+                                            int rank) {
+  const int blk = w.inner(idx);
+  int g, outer, before;
   if (kMode == kDw) {
-    mt = (a.m_ext + 255) >> 8;
-    g = blk / mt;
-    before = g * mt;
+    outer = w.outer.d;
+    g = w.outer(blk);
+    before = g * outer;
   } else {
     int hi = G;
     g = 0;   // s_blk[g] <= blk < s_blk[hi]
@@ -108,25 +138,36 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
       else hi = mid;
     }
     before = s_blk[g];
-    mt = s_blk[g + 1] - before;
+    outer = s_blk[g + 1] - before;
   }
+  const int start = s_start[g], rows = s_start[g + 1] - start;
+  const int local = idx - before * w.inner.d;
+  const int set = w.set(local);
+  const int rest = local - set * w.set.d;
+  const int here = min(kXRowBlocks, outer - set * kXRowBlocks);
+  const int i = here == kXRowBlocks ? rest / kXRowBlocks : Div(here)(rest);   // inner tile
+  const int o = set * kXRowBlocks + rest - i * here;                          // outer tile
   Tile t;
   t.g = g;
-  const int start = s_start[g], in_group = s_start[g + 1] - start;
-  const int local = idx - before * nt;
-  const int mb = local / (kXRowBlocks * nt);
-  const int rest = local - mb * kXRowBlocks * nt;
-  const int here = min(kXRowBlocks, mt - mb * kXRowBlocks);
-  const int n = rest / here;
-  const int m = mb * kXRowBlocks + rest - n * here;
-  const int base = (kMode == kDw ? 0 : start) + m * 256;
-  const int end = kMode == kDw ? a.m_ext : start + in_group;
-  t.a0 = base + 128 * rank;
-  t.valid = clamp_int(end - t.a0, 0, 128);
-  t.peer = clamp_int(end - (base + 128 * (rank ^ 1)), 0, 128);
-  t.n0 = n * 256;
-  t.k0 = kMode == kDw ? start : 0;
-  const int len = kMode == kDw ? in_group : g < a.E ? a.k_ext : 0;
+  int n_end;
+  if (kMode == kDw) {
+    t.m0 = o * 256;
+    t.n0 = i * 256;
+    n_end = min(a.n_ext, t.n0 + 256);
+    t.k0 = start;
+  } else {
+    const int size = (((rows + 15) >> 4) + outer - 1) / outer * 16;   // of the group's equal tiles
+    t.m0 = i * 256;
+    t.n0 = start + o * size;
+    n_end = min(start + rows, t.n0 + size);
+    t.k0 = 0;
+  }
+  t.n_here = n_end - t.n0;
+  t.n = (t.n_here + 15) & ~15;
+  t.m_peer = clamp_int(a.m_ext - (t.m0 + 128 * (rank ^ 1)), 0, 128);
+  t.m0 += 128 * rank;
+  t.m_here = clamp_int(a.m_ext - t.m0, 0, 128);
+  const int len = kMode == kDw ? rows : g < a.E ? a.k_ext : 0;
   t.nkb = (len + kXBK - 1) / kXBK;
   t.nks = (len + 15) / 16;
   return t;
@@ -137,72 +178,90 @@ __device__ __forceinline__ void x_timeout(int32_t* status, volatile int* abort) 
   if (status) atomicOr(status, MOE_DEVICE_FLAG_TIMEOUT);
 }
 
-// The loads of one tile in this CTA. A: its 128 rows (skipped where none of them exists: what the
-// stage holds then only reaches rows that are not stored); B: its half of the 256 columns. An
-// operand along the contraction is one box of 128 rows; one across it is two boxes of 64 columns.
+// Loads are issued by the whole warp, one thread of it taking effect: descriptors, addresses and
+// coordinates are then the same in all lanes and stay in uniform registers, where the TMA unit takes
+// them from. Issued from a branch of one lane, their way there cost 100 cycles and more an
+// instruction, and the producer, not the tensor cores, set the pace (dw at 8192 x 14336 x 4096
+// over 8 experts, four boxes a block: 768 us, so 604; dx there, three boxes: 691 us, so 571).
+//
+// The loads of one tile in this CTA. A: its 128 indices along M (left out where none exists: what
+// the stage holds then only reaches accumulator lanes that are not stored). B: its half of the
+// tile's N, in one box of 128 rows, or of 32 rows each where at most 64 are wanted (mb32); in dw
+// in boxes of 64 columns. An operand across the contraction comes in boxes of 64 (its swizzle's
+// width) by the 64 of the block.
 template <int kMode>
 __device__ __forceinline__ bool produce_tile(const Tile& t, const CUtensorMap* ma,
-                                             const CUtensorMap* mb, int rank, int& fills,
-                                             uint8_t* sA, uint8_t* sB, uint32_t lead_full,
-                                             uint64_t* full_bar, uint64_t* empty_bar,
-                                             volatile int* abort) {
-  const uint32_t tx = kXSlotBytes * (2u + (t.valid > 0) + (t.peer > 0));
-  const int bn = t.n0 + 128 * rank;
-  for (int kb = 0; kb < t.nkb; kb += kXPerStage) {
-    const int nk = min(t.nkb - kb, kXPerStage);
-    const int stage = fills % kXStages;
-    if (!mbar_wait<true>(&empty_bar[stage], ((fills / kXStages) & 1) ^ 1u, abort)) return false;
-    if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], nk * tx);
-    const uint32_t fb = lead_full + 8u * stage;
-    for (int b = 0; b < nk; ++b) {
-      uint8_t* as = sA + (stage * kXPerStage + b) * kXSlotBytes;
-      uint8_t* bs = sB + (stage * kXPerStage + b) * kXSlotBytes;
-      const int kc = t.k0 + (kb + b) * kXBK;
-      if (t.valid > 0) {
-        if (kMode == kDw) {
-          tma_load_2d_pair(as, ma, fb, t.a0, kc);
-          tma_load_2d_pair(as + kXSlotBytes / 2, ma, fb, t.a0 + 64, kc);
+                                             const CUtensorMap* mb, const CUtensorMap* mb32,
+                                             int rank, int& stage, uint32_t& phase, uint8_t* sA,
+                                             uint8_t* sB, uint32_t lead_full, uint64_t* full_bar,
+                                             uint64_t* empty_bar, volatile int* abort) {
+  const int half = t.n >> 1;
+  const bool narrow = kMode != kDw && half <= 64;
+  const int box = kMode == kDw ? 64 : narrow ? 32 : 128;   // of B along N; 128 bytes each
+  const bool two = half > box;
+  const CUtensorMap* mbx = narrow ? mb32 : mb;
+  const uint32_t tx =
+      kXSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) + 2 * (two ? 2 : 1) * box * 128;
+  const int n0 = t.n0 + rank * half;
+  for (int kb = 0; kb < t.nkb; ++kb) {
+    if (!__all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort))) return false;
+    if (elect_one()) {
+      if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
+      const uint32_t fb = lead_full + 8u * stage;
+      uint8_t* as = sA + stage * kXSlotBytes;
+      uint8_t* bs = sB + stage * kXSlotBytes;
+      const int kc = t.k0 + kb * kXBK;
+      if (t.m_here > 0) {
+        if (kMode == kFwd) {
+          tma_load_3d_pair(as, ma, fb, kc, t.m0, t.g);
+        } else if (kMode == kDx) {
+          tma_load_3d_pair(as, ma, fb, t.m0, kc, t.g);
+          tma_load_3d_pair(as + kXSlotBytes / 2, ma, fb, t.m0 + 64, kc, t.g);
         } else {
-          tma_load_2d_pair(as, ma, fb, kc, t.a0);
+          tma_load_2d_pair(as, ma, fb, t.m0, kc);
+          tma_load_2d_pair(as + kXSlotBytes / 2, ma, fb, t.m0 + 64, kc);
         }
       }
-      if (kMode == kFwd) {
-        tma_load_3d_pair(bs, mb, fb, kc, bn, t.g);
-      } else if (kMode == kDx) {
-        tma_load_3d_pair(bs, mb, fb, bn, kc, t.g);
-        tma_load_3d_pair(bs + kXSlotBytes / 2, mb, fb, bn + 64, kc, t.g);
+      if (kMode == kDw) {
+        tma_load_2d_pair(bs, mbx, fb, n0, kc);
+        if (two) tma_load_2d_pair(bs + kXSlotBytes / 2, mbx, fb, n0 + 64, kc);
       } else {
-        tma_load_2d_pair(bs, mb, fb, bn, kc);
-        tma_load_2d_pair(bs + kXSlotBytes / 2, mb, fb, bn + 64, kc);
+        tma_load_2d_pair(bs, mbx, fb, kc, n0);
+        if (two) tma_load_2d_pair(bs + 32 * 128, mbx, fb, kc, n0 + 32);
       }
     }
-    ++fills;
+    __syncwarp();
+    if (++stage == kXStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
   }
   return true;
 }
 
+// The MMAs of one tile, issued the same way (2% faster there than from one lane's branch).
 template <int kMode>
 __device__ __forceinline__ bool multiply_tile(uint32_t d, uint32_t idesc, int nks, int& stage,
                                               uint32_t& phase, uint64_t da0, uint64_t db0,
                                               uint64_t* full_bar, uint64_t* empty_bar,
                                               volatile int* abort) {
   // 16 elements of the contraction further on: 32 bytes inside the rows, or 16 rows of 128 bytes.
-  constexpr uint32_t kStepA = (kMode == kDw ? 2048u : 32u) >> 4;
-  constexpr uint32_t kStepB = (kMode == kFwd ? 32u : 2048u) >> 4;
-  constexpr int kPer = kXPerStage * (kXBK / 16);   // instructions a full stage
+  constexpr uint32_t kStepA = (kMode == kFwd ? 32u : 2048u) >> 4;
+  constexpr uint32_t kStepB = (kMode == kDw ? 2048u : 32u) >> 4;
+  constexpr int kPer = kXBK / 16;   // instructions a block
   for (int ks = 0; ks < nks; ks += kPer) {
-    if (!mbar_wait<true>(&full_bar[stage], phase, abort)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait<true>(&full_bar[stage], phase, abort))) return false;
     tc_fence_after();
-    const uint32_t at = (stage * kXPerStage * kXSlotBytes) >> 4;
-    const uint64_t da = da0 + at, db = db0 + at;
+    const uint64_t da = da0 + ((stage * kXSlotBytes) >> 4), db = db0 + ((stage * kXSlotBytes) >> 4);
+    if (elect_one()) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (ks + i >= nks) break;
-      const uint32_t b = (i / (kXBK / 16)) * (kXSlotBytes >> 4);
-      umma_bf16_pair(d, da + b + (i % (kXBK / 16)) * kStepA, db + b + (i % (kXBK / 16)) * kStepB,
-                     idesc, (ks | i) != 0);
+      for (int i = 0; i < kPer; ++i) {
+        if (ks + i >= nks) break;
+        umma_bf16_pair(d, da + i * kStepA, db + i * kStepB, idesc, (ks | i) != 0);
+      }
+      umma_commit_pair(&empty_bar[stage], kXPairMask);
     }
-    umma_commit_pair(&empty_bar[stage], kXPairMask);
+    __syncwarp();
     if (++stage == kXStages) {
       stage = 0;
       phase ^= 1u;
@@ -220,87 +279,119 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One warp's part of a tile: 32 rows (TMEM lane quarter q) by 128 columns, 64 of them at a time.
-// They go through shared memory, in boxes of 128 bytes of columns (64 16-bit or 32 f32 values), and
-// out by TMA, which leaves out what lies beyond the tensor (its columns, and for dw its rows); a
-// warp that holds the last rows of a group in forward or dx stores those from registers. `done`
-// runs once the accumulator has been read.
+// dw: one warp's part of a tile, 32 rows of dw[g] (TMEM lane quarter q) by 128 columns, in boxes of
+// 128 bytes of columns (64 16-bit or 32 f32 values) through shared memory and out by TMA, which
+// leaves out what lies beyond dw[g]. `done` runs once the accumulator has been read.
 // Two warps a lane quarter: a box costs a warp about 700 cycles of latency (TMEM load, fence, the
-// store's read of the box), so that four warps held 256 x 256 tiles of dw with short contractions
-// to 3.3 us (256 experts of 128 rows, N = 7168, K = 2048: 2.50 ms against 1.21 ms of traffic).
-template <int kMode, bool kF32, typename Done>
-__device__ __forceinline__ void store_tile(uint32_t tb, const Tile& t, int q, int half, int lane,
-                                           uint8_t* buf, const CUtensorMap* map,
-                                           const ExpertsArgs& a, Done&& done) {
-  const int rows = clamp_int(t.valid - 32 * q, 0, 32);
-  const int col = t.n0 + 128 * half;
-  if (rows == 0 || col >= a.n_ext) {
+// store's read of the box), so that four warps held tiles with short contractions to 3.3 us (256
+// experts of 128 rows, N = 7168, K = 2048: 2.50 ms, with eight 1.9 ms; writing the result alone
+// takes 1.87 at the 4.0 TB/s that a write-only stream reaches).
+template <bool kF32, typename Done>
+__device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int half, int lane,
+                                         uint8_t* buf, const CUtensorMap* map,
+                                         const ExpertsArgs& a, Done&& done) {
+  const int cols = min(128, t.n_here - 128 * half);
+  if (32 * q >= t.m_here || cols <= 0) {
     done();
     return;
   }
-  const bool whole = kMode == kDw || rows == 32;
+  constexpr int kCols = kF32 ? 32 : 64;   // of a box
   const bool f16 = a.f16 != 0;
-  const int row = t.a0 + 32 * q;
-  uint4* mine = reinterpret_cast<uint4*>(buf + lane * 128);   // this lane's row of the box
+  const int row = t.m0 + 32 * q, col = t.n0 + 128 * half;
+  uint4* mine = reinterpret_cast<uint4*>(buf + lane * 128);
 #pragma unroll 1
-  for (int c0 = 0; c0 < 128; c0 += 64) {
-    uint32_t v[64];
+  for (int c0 = 0; c0 < cols; c0 += kCols) {
+    uint32_t v[kCols];
     if (t.nkb > 0) {
-      tmem_ld_x64(tb + 128 * half + c0, v);
+      tmem_ld(tb + 128 * half + c0, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = 0;
+      for (int i = 0; i < kCols; ++i) v[i] = 0;
     }
-    const bool last = c0 == 64 || col + 64 >= a.n_ext;
-    if (last) done();
-    if (kF32) {
+    if (c0 + kCols >= cols) done();
+    uint4 o[8];
+    uint32_t* w = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (col + c0 + 32 * b >= a.n_ext) break;
-        if (lane == 0) bulk_wait_group_read<0>();   // the box before has been read out
-        __syncwarp();
+    for (int i = 0; i < 32; ++i) {
+      if constexpr (kF32) w[i] = v[i];
+      else w[i] = pack_16bit(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
+    }
+    if (lane == 0) bulk_wait_group_read<0>();   // the box before has been read out
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          mine[i ^ (lane & 7)] = make_uint4(v[32 * b + 4 * i], v[32 * b + 4 * i + 1],
-                                            v[32 * b + 4 * i + 2], v[32 * b + 4 * i + 3]);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if (a.add) tma_add_3d(map, buf, col + c0 + 32 * b, row, t.g);
-          else tma_store_3d(map, buf, col + c0 + 32 * b, row, t.g);
-          bulk_commit_group();
-        }
-      }
+    for (int i = 0; i < 8; ++i) mine[i ^ (lane & 7)] = o[i];
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (kF32 && a.add) tma_add_3d(map, buf, col + c0, row, t.g);
+      else tma_store_3d(map, buf, col + c0, row, t.g);
+      bulk_commit_group();
+    }
+  }
+}
+
+// Forward and dx: one warp's part of a tile, 32 channels (its TMEM lane quarter, a lane each) by
+// every second block of 32 rows. Two rows of a channel are packed, exchanged with the neighbouring
+// lane's, and leave the even lane with both channels of the first row and the odd lane with
+// those of the second: 4-byte stores, without bank conflicts, into a box of 32 rows of 64 bytes
+// (64-byte swizzle). Whole boxes go out by TMA, which leaves out channels past the last; a group's
+// last rows straight to memory.
+template <typename Done>
+__device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, int half, int lane,
+                                           uint8_t* buf, int& sbuf, const CUtensorMap* map,
+                                           const ExpertsArgs& a, Done&& done) {
+  if (32 * q >= t.m_here || 32 * half >= t.n_here) {
+    done();
+    return;
+  }
+  const bool f16 = a.f16 != 0;
+  const bool odd = lane & 1;
+  const int ch = t.m0 + 32 * q;
+  const int pair = lane >> 1;   // channels ch + 2 * pair and the next
+#pragma unroll 1
+  for (int r0 = 32 * half; r0 < t.n_here; r0 += 64) {
+    uint32_t v[32];
+    if (t.nkb > 0) {
+      tmem_ld(tb + r0, v);
     } else {
-      uint4 o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&o[i]);
+      for (int i = 0; i < 32; ++i) v[i] = 0;
+    }
+    if (r0 + 64 >= t.n_here) done();
+    uint32_t o[16];   // row 2i of the block in even lanes, 2i + 1 in odd ones
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = pack_16bit(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]), f16);
-      }
-      if (whole) {
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i ^ (lane & 7)] = o[i];
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if (kMode == kDw) tma_store_3d(map, buf, col + c0, row, t.g);
-          else tma_store_2d(map, buf, col + c0, row);
-          bulk_commit_group();
-        }
-      } else if (lane < rows) {
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t mine =
+          pack_16bit(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+      o[i] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+    }
+    const int rows = t.n_here - r0;
+    if (rows < 32) {
+      if (32 * q + 2 * pair < t.m_here) {   // m_ext is even
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        static_cast<int64_t>(row + lane) * a.n_ext + col + c0;
+                        static_cast<int64_t>(t.n0 + r0 + odd) * a.m_ext + ch + 2 * pair;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)   // n_ext is a multiple of 8
-          if (col + c0 + 8 * i < a.n_ext) reinterpret_cast<uint4*>(dst)[i] = o[i];
+        for (int i = 0; i < 16; ++i)
+          if (2 * i + odd < rows)
+            *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(2 * i) * a.m_ext) = o[i];
       }
+      continue;
     }
-    if (last) break;
+    uint8_t* box = buf + sbuf * (kXBoxBytes / 2);
+    if (lane == 0) bulk_wait_group_read<1>();   // what was stored from this box before is out
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      *reinterpret_cast<uint32_t*>(box + (2 * i + odd) * 64 + (((pair >> 2) ^ (i & 3)) << 4) +
+                                   (pair & 3) * 4) = o[i];
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, box, ch, t.n0 + r0);
+      bulk_commit_group();
+    }
+    sbuf ^= 1;
   }
 }
 
@@ -308,6 +399,7 @@ template <int kMode, bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXThreads, 1)
 experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ CUtensorMap map_b32,
                       const __grid_constant__ CUtensorMap map_out, ExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[kXStages], empty_bar[kXStages];
@@ -324,8 +416,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   // 1024-byte aligned stages, at the same offsets in both CTAs.
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-  uint8_t* sB = sA + kXSlots * kXSlotBytes;
-  uint8_t* sOut = sB + kXSlots * kXSlotBytes;
+  uint8_t* sB = sA + kXStages * kXSlotBytes;
+  uint8_t* sOut = sB + kXStages * kXSlotBytes;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -344,6 +436,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
+    tma_prefetch_map(&map_b32);
     tma_prefetch_map(&map_out);
   }
   if (warp == 1) {
@@ -399,58 +492,64 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort = &s_abort;
-  const int nt = (a.n_ext + 255) >> 8;
-  const int total = nt * (kMode == kDw ? a.E * ((a.m_ext + 255) >> 8) : s_blk[G]);
+  const Walk walk = Walk::of<kMode>(a);
+  const int total = walk.inner.d * (kMode == kDw ? a.E * walk.outer.d : s_blk[G]);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
-      int fills = 0, last_g = -1;
-      for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, rank);
-        if (t.nkb == 0) continue;
-        const CUtensorMap* ma = &map_a;
-        const CUtensorMap* mb = &map_b;
-        if (kMode == kDw) {
-          ma = a.maps + t.g;
-          mb = a.maps + a.E + t.g;
-          if (t.g != last_g) {
-            tmap_acquire(ma);
-            tmap_acquire(mb);
-            last_g = t.g;
-          }
-        }
-        if (!produce_tile<kMode>(t, ma, mb, rank, fills, sA, sB, lead_full, full_bar, empty_bar,
-                                 abort)) {
-          x_timeout(a.status, abort);
-          break;
+    // ------------------------------------------------------------ TMA producer
+    int stage = 0, last_g = -1;
+    uint32_t phase = 0;
+    for (int idx = first; idx < total; idx += step) {
+      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank);
+      if (t.nkb == 0) continue;
+      const CUtensorMap* ma = &map_a;
+      const CUtensorMap* mb = &map_b;
+      if (kMode == kDw) {
+        ma = a.maps + t.g;
+        mb = a.maps + a.E + t.g;
+        if (t.g != last_g) {
+          tmap_acquire(ma);
+          tmap_acquire(mb);
+          last_g = t.g;
         }
       }
-      // The commits of the last stages arrive in this CTA's barriers before it may leave.
-      volatile int never = 0;
-      for (int f = fills > kXStages ? fills - kXStages : 0; f < fills; ++f)
-        mbar_wait<true>(&empty_bar[f % kXStages], (f / kXStages) & 1, &never);
+      if (!produce_tile<kMode>(t, ma, mb, &map_b32, rank, stage, phase, sA, sB, lead_full, full_bar,
+                               empty_bar, abort)) {
+        x_timeout(a.status, abort);
+        break;
+      }
+    }
+    // Every commit of a stage that was filled arrives in this CTA's barriers before it may leave
+    // (a stage never filled passes at once).
+    volatile int never = 0;
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_wait<true>(&empty_bar[stage], phase ^ 1u, &never);
+      if (++stage == kXStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0 && lead) {
+    if (lead) {
       // ------------------------------------------------------------ MMA issuer (first CTA)
+      // The whole warp walks the tiles; one thread issues.
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint64_t da0 = kMode == kDw ? sdesc_mn_major(smem_u32(sA), kXSlotBytes / 2)
-                                        : sdesc_k_major(smem_u32(sA), 128);
-      const uint64_t db0 = kMode == kFwd ? sdesc_k_major(smem_u32(sB), 128)
-                                         : sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2);
-      const uint32_t idesc = idesc_16bit_f32(256, 256, a.f16 != 0, kMode == kDw, kMode != kFwd);
+      const uint64_t da0 = kMode == kFwd ? sdesc_k_major(smem_u32(sA), 128)
+                                         : sdesc_mn_major(smem_u32(sA), kXSlotBytes / 2);
+      const uint64_t db0 = kMode == kDw ? sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2)
+                                        : sdesc_k_major(smem_u32(sB), 128);
       for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, 0);
+        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, 0);
         if (t.nkb == 0) continue;
-        ok = mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort);
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort));
         if (ok) {
           tc_fence_after();
+          const uint32_t idesc = idesc_16bit_f32(256, t.n, a.f16 != 0, kMode != kFwd, kMode == kDw);
           ok = multiply_tile<kMode>(tmem_base + acc * kXAccCols, idesc, t.nks, stage, phase, da0,
                                     db0, full_bar, empty_bar, abort);
         }
@@ -458,7 +557,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
           x_timeout(a.status, abort);
           break;
         }
-        umma_commit_pair(&tfull_bar[acc], kXPairMask);
+        if (elect_one()) umma_commit_pair(&tfull_bar[acc], kXPairMask);
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
@@ -466,7 +566,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       }
       if (!ok) {
         // Every MMA issued so far ends (bounded wait) before TMEM is released.
-        umma_commit_pair(&drain_bar, 0x1);
+        if (elect_one()) umma_commit_pair(&drain_bar, 0x1);
         volatile int never = 0;
         mbar_wait(&drain_bar, 0, &never);
       }
@@ -476,32 +576,36 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     const int q = warp & 3;   // TMEM lane quarter of this warp
     const int half = (warp - 2) >> 2;
     uint8_t* my_box = sOut + (warp - 2) * kXBoxBytes;
-    int acc = 0;
+    int sbuf = 0, acc = 0;
     uint32_t acc_phase = 0;
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, rank);
+      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank);
       const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      if (t.nkb == 0) {
-        if (!(kF32 && a.add))
-          store_tile<kMode, kF32>(tb, t, q, half, lane, my_box, &map_out, a, [] {});
-        continue;
+      const bool zeros = t.nkb == 0;   // nothing was multiplied, no accumulator taken
+      if (zeros && kF32 && a.add) continue;
+      if (!zeros) {
+        const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
+        // Lanes may leave the poll at different times; tcgen05.ld is warp-collective.
+        if (!__all_sync(0xffffffffu, got)) {
+          x_timeout(a.status, abort);
+          break;
+        }
+        tc_fence_after();
       }
-      const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
-      // Lanes may leave the poll at different times; tcgen05.ld is warp-collective.
-      if (!__all_sync(0xffffffffu, got)) {
-        x_timeout(a.status, abort);
-        break;
-      }
-      tc_fence_after();
-      store_tile<kMode, kF32>(tb, t, q, half, lane, my_box, &map_out, a, [&] {
+      auto done = [&] {
+        if (zeros) return;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (lead) mbar_arrive(&tempty_bar[acc]);
           else mbar_arrive_cluster(lead_tempty + 8u * acc);
         }
-      });
-      if (++acc == 2) {
+      };
+      if constexpr (kMode == kDw)
+        store_dw<kF32>(tb, t, q, half, lane, my_box, &map_out, a, done);
+      else
+        store_rows(tb, t, q, half, lane, my_box, sbuf, &map_out, a, done);
+      if (!zeros && ++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
@@ -597,15 +701,15 @@ moe_status prepare_form(int* max_clusters) {
 }
 
 template <int kMode, bool kF32>
-moe_status launch_form(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
-                       const ExpertsArgs& a, int64_t tiles, cudaStream_t s) {
+moe_status launch_form(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mb32,
+                       const CUtensorMap& mo, const ExpertsArgs& a, int64_t tiles, cudaStream_t s) {
   int clusters = 1;
   const moe_status st = prepare_form<kMode, kF32>(&clusters);
   if (st != MOE_OK) return st;
   if (clusters > tiles) clusters = static_cast<int>(tiles);
   const cudaError_t err =
       launch_pdl(experts_matmul_kernel<kMode, kF32>, dim3(2 * static_cast<unsigned>(clusters)),
-                 dim3(kXThreads), kXSmemBytes, s, ma, mb, mo, a);
+                 dim3(kXThreads), kXSmemBytes, s, ma, mb, mb32, mo, a);
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_matmul launch: %s", cudaGetErrorString(err));
   return MOE_OK;
@@ -626,25 +730,27 @@ moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int
                                int32_t* status, cudaStream_t s) {
   const CUtensorMapDataType t = map_type(dtype);
   const int kc = dx ? N : K, nc = dx ? K : N;   // contraction, columns of the result
-  CUtensorMap ma, mb, mo;
-  // w [E, N, K]: forward reads boxes of 64 K x 128 N rows, dx of 64 K (columns) x 64 N.
+  CUtensorMap ma, mb, mb32, mo;
+  // A, w [E, N, K]: boxes of 64 K x 128 channels (rows of w[e]), or of 64 channels x 64 N. B: boxes
+  // of 64 x 128 and 64 x 32 rows.
   const bool ok =
-      encode_any(&ma, in, 0, R, kc, t, kXBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_any(&mb, w, E, N, K, t, 64, dx ? kXBK : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_any(&mo, out, 0, R, nc, t, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+      encode_any(&ma, w, E, N, K, t, 64, dx ? kXBK : 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mb, in, 0, R, kc, t, kXBK, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mb32, in, 0, R, kc, t, kXBK, 32, CU_TENSOR_MAP_SWIZZLE_128B) &&
+      encode_any(&mo, out, 0, R, nc, t, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   ExpertsArgs a = {};
   a.offsets = offsets;
   a.E = E;
   a.R = static_cast<int32_t>(R);
-  a.n_ext = nc;
+  a.m_ext = nc;
   a.k_ext = kc;
   a.f16 = dtype == MOE_DTYPE_F16;
   a.out = out;
   a.status = status;
   const int64_t tiles = (R / 256 + E + 1) * ((nc + 255) / 256);
-  return dx ? launch_form<kDx, false>(ma, mb, mo, a, tiles, s)
-            : launch_form<kFwd, false>(ma, mb, mo, a, tiles, s);
+  return dx ? launch_form<kDx, false>(ma, mb, mb32, mo, a, tiles, s)
+            : launch_form<kFwd, false>(ma, mb, mb32, mo, a, tiles, s);
 }
 
 moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
@@ -675,8 +781,8 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_maps launch: %s", cudaGetErrorString(err));
   const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
-  return f32 ? launch_form<kDw, true>(ma, mb, mo, a, tiles, s)
-             : launch_form<kDw, false>(ma, mb, mo, a, tiles, s);
+  return f32 ? launch_form<kDw, true>(ma, mb, mb, mo, a, tiles, s)
+             : launch_form<kDw, false>(ma, mb, mb, mo, a, tiles, s);
 }
 
 }  // namespace moe
