@@ -350,7 +350,9 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dt
  * dtype: any moe_dtype; H 1..65536; T <= 2^24. The workspace (moe_dispatch_workspace_bytes, 0
  * for sizes outside the range) needs no clearing; its status word, which
  * moe_read_device_status reads, gets MOE_DEVICE_FLAG_BAD_ID when an id is neither -1 nor in
- * [0, E) (the slot is then dropped). */
+ * [0, E) (the slot is then dropped). Up to MOE_DISPATCH_SMALL_SLOTS slots (T*k) need no workspace:
+ * it may be NULL, and a bad id is then dropped without a flag. */
+#define MOE_DISPATCH_SMALL_SLOTS 12288
 size_t moe_dispatch_workspace_bytes(int64_t T, int32_t E, int32_t k);
 moe_status moe_dispatch(const void* x, const int32_t* ids, int64_t T, int32_t H, int32_t E,
                         int32_t k, moe_dtype dtype, void* x_perm, int32_t* inv, int32_t* offsets,

@@ -166,12 +166,13 @@ def _ptr(t: Optional[torch.Tensor]):
 # The current stream's handle without the Stream object around it (2.8 us of a call's 10 on the
 # host when it was built for each call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -515,12 +516,16 @@ def _slots(inv: torch.Tensor, name: str = "inv"):
     return inv.shape
 
 
+MOE_DISPATCH_SMALL_SLOTS = 12288
+
+
 def moe_dispatch(x, ids, num_experts: int, x_perm=None, inv=None, offsets=None,
                  scratch: Optional[Scratch] = None, stream=None):
     """Rows of x [T, H] sorted by expert. ids int32 [T, k], -1 for a dropped slot. Returns
     (x_perm [T*k, H], inv int32 [T, k], offsets int32 [E + 1]): rows of expert e are
     x_perm[offsets[e]:offsets[e + 1]], inv the row of each slot (-1 - row of a dropped one, whose
-    row holds zeros)."""
+    row holds zeros). Pass a scratch to read back (moe_read_device_status) whether an id was
+    neither -1 nor an expert."""
     dt = _typed(x, "x", 2)
     T, H = x.shape
     if _slots(ids, "ids")[0] != T:
@@ -530,10 +535,10 @@ def moe_dispatch(x, ids, num_experts: int, x_perm=None, inv=None, offsets=None,
     x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, dev)
     inv = _out(inv, "inv", (T, k), torch.int32, dev)
     offsets = _out(offsets, "offsets", (num_experts + 1,), torch.int32, dev)
-    if scratch is None and T > 0:
+    if scratch is None and T * k > MOE_DISPATCH_SMALL_SLOTS:
         scratch = alloc_dispatch_scratch(T, num_experts, k, dev)
-    _check(_lib.moe_dispatch(_ptr(x), _ptr(ids), T, H, num_experts, k, dt, _ptr(x_perm), _ptr(inv),
-                             _ptr(offsets), scratch.ptr if scratch else None,
+    _check(_lib.moe_dispatch(x.data_ptr(), ids.data_ptr(), T, H, num_experts, k, dt, x_perm.data_ptr(), inv.data_ptr(),
+                             offsets.data_ptr(), scratch.ptr if scratch else None,
                              scratch.nbytes if scratch else 0, _stream(stream)), "moe_dispatch")
     return x_perm, inv, offsets
 
@@ -546,7 +551,7 @@ def moe_dispatch_rows(x, inv, x_perm=None, stream=None):
     if x.shape[0] != T:
         raise ValueError(f"x must have {T} rows, got {tuple(x.shape)}")
     x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, x.device)
-    _check(_lib.moe_dispatch_rows(_ptr(x), _ptr(inv), T, H, k, dt, _ptr(x_perm), _stream(stream)),
+    _check(_lib.moe_dispatch_rows(x.data_ptr(), inv.data_ptr(), T, H, k, dt, x_perm.data_ptr(), _stream(stream)),
            "moe_dispatch_rows")
     return x_perm
 
@@ -558,7 +563,7 @@ def moe_dispatch_backward(dx_perm, inv, dx=None, stream=None):
     H = dx_perm.shape[1]
     _shaped(dx_perm, "dx_perm", (T * k, H), dx_perm.dtype)
     dx = _out(dx, "dx", (T, H), dx_perm.dtype, dx_perm.device)
-    _check(_lib.moe_dispatch_backward(_ptr(dx_perm), _ptr(inv), T, H, k, dt, _ptr(dx),
+    _check(_lib.moe_dispatch_backward(dx_perm.data_ptr(), inv.data_ptr(), T, H, k, dt, dx.data_ptr(),
                                       _stream(stream)), "moe_dispatch_backward")
     return dx
 
@@ -573,7 +578,7 @@ def moe_combine(rows, inv, scales=None, y=None, stream=None):
     if scales is not None:
         _shaped(scales, "scales", (T, k), torch.float32)
     y = _out(y, "y", (T, H), rows.dtype, rows.device)
-    _check(_lib.moe_combine(_ptr(rows), _ptr(inv), _ptr(scales), T, H, k, dt, _ptr(y),
+    _check(_lib.moe_combine(rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt, y.data_ptr(),
                             _stream(stream)), "moe_combine")
     return y
 
@@ -589,8 +594,8 @@ def moe_combine_backward(dy, rows, inv, scales=None, drows=None, dscales=None, s
         _shaped(scales, "scales", (T, k), torch.float32)
     drows = _out(drows, "drows", (T * k, H), dy.dtype, dy.device)
     dscales = _out(dscales, "dscales", (T, k), torch.float32, dy.device)
-    _check(_lib.moe_combine_backward(_ptr(dy), _ptr(rows), _ptr(inv), _ptr(scales), T, H, k, dt,
-                                     _ptr(drows), _ptr(dscales), _stream(stream)),
+    _check(_lib.moe_combine_backward(dy.data_ptr(), rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt,
+                                     drows.data_ptr(), dscales.data_ptr(), _stream(stream)),
            "moe_combine_backward")
     return drows, dscales
 
@@ -612,7 +617,7 @@ def moe_swiglu_ckpt(gu, h=None, ckpt=None, stream=None):
     q, qs = ckpt if ckpt is not None else (None, None)
     q = _out(q, "q", (R, I2), torch.uint8, gu.device)
     qs = _out(qs, "q_scales", (R, nb), torch.uint8, gu.device)
-    _check(_lib.moe_swiglu_ckpt(_ptr(gu), R, I, dt, _ptr(h), _ptr(q), _ptr(qs), _stream(stream)),
+    _check(_lib.moe_swiglu_ckpt(gu.data_ptr(), R, I, dt, _ptr(h), q.data_ptr(), qs.data_ptr(), _stream(stream)),
            "moe_swiglu_ckpt")
     return h, (q, qs)
 
@@ -627,7 +632,7 @@ def moe_swiglu_ckpt_backward(dh, ckpt, dgu=None, h=None, want_h: bool = False, s
     dgu = _out(dgu, "dgu", (R, 2 * I), dh.dtype, dh.device)
     if want_h or h is not None:
         h = _out(h, "h", (R, I), dh.dtype, dh.device)
-    _check(_lib.moe_swiglu_ckpt_backward(_ptr(dh), _ptr(q), _ptr(qs), R, I, dt, _ptr(dgu), _ptr(h),
+    _check(_lib.moe_swiglu_ckpt_backward(dh.data_ptr(), q.data_ptr(), qs.data_ptr(), R, I, dt, dgu.data_ptr(), _ptr(h),
                                          _stream(stream)), "moe_swiglu_ckpt_backward")
     return dgu, h
 
@@ -644,8 +649,8 @@ def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None,
     E, N, K = w.shape
     R = x.shape[0]
     y = _out(y, "y", (R, N), x.dtype, x.device)
-    _check(_lib.moe_experts_matmul(_ptr(x), _ptr(w), _ptr(_offsets(offsets, E)), R, E, N, K, dt,
-                                   _ptr(y), scratch.ptr if scratch else None,
+    _check(_lib.moe_experts_matmul(x.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(), R,
+                                   E, N, K, dt, y.data_ptr(), scratch.ptr if scratch else None,
                                    scratch.nbytes if scratch else 0, _stream(stream)),
            "moe_experts_matmul")
     return y
@@ -659,8 +664,9 @@ def moe_experts_matmul_dx(dy, w, offsets, dx=None, scratch: Optional[Scratch] = 
     E, N, K = w.shape
     R = dy.shape[0]
     dx = _out(dx, "dx", (R, K), dy.dtype, dy.device)
-    _check(_lib.moe_experts_matmul_dx(_ptr(dy), _ptr(w), _ptr(_offsets(offsets, E)), R, E, N, K, dt,
-                                      _ptr(dx), scratch.ptr if scratch else None,
+    _check(_lib.moe_experts_matmul_dx(dy.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(),
+                                      R, E, N, K, dt, dx.data_ptr(),
+                                      scratch.ptr if scratch else None,
                                       scratch.nbytes if scratch else 0, _stream(stream)),
            "moe_experts_matmul_dx")
     return dx
@@ -687,8 +693,8 @@ def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bo
     if scratch is None:
         n = _lib.moe_experts_workspace_bytes(E)
         scratch = Scratch(torch.empty(max(n, 1), dtype=torch.uint8, device=dy.device))
-    _check(_lib.moe_experts_matmul_dw(_ptr(dy), _ptr(x), _ptr(offsets), R, E, N, K, dt, out,
-                                      int(accumulate), _ptr(dw), scratch.ptr, scratch.nbytes,
+    _check(_lib.moe_experts_matmul_dw(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), R, E, N, K,
+                                      dt, out, int(accumulate), dw.data_ptr(), scratch.ptr, scratch.nbytes,
                                       _stream(stream)), "moe_experts_matmul_dw")
     return dw
 
@@ -704,8 +710,8 @@ def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor:
     _shaped(dscales, "dscales", (T, k), torch.float32)
     dlogits = _out(dlogits, "dlogits", (T, E), torch.float32, logits.device)
     p = MoeRouteParams(E, k, method, 1, 1, routed_scaling_factor)
-    _check(_lib.moe_route_backward(_ptr(logits), _ptr(ids), _ptr(dscales), T, ctypes.byref(p),
-                                   _ptr(dlogits), _stream(stream)), "moe_route_backward")
+    _check(_lib.moe_route_backward(logits.data_ptr(), ids.data_ptr(), dscales.data_ptr(), T, ctypes.byref(p),
+                                   dlogits.data_ptr(), _stream(stream)), "moe_route_backward")
     return dlogits
 
 

@@ -85,8 +85,9 @@ moe_status moe_dispatch(const void* x, const int32_t* ids, int64_t T, int32_t H,
   }
   if (bad(x) || bad(ids) || bad(x_perm) || bad(inv) || !offsets || !aligned(offsets, 4))
     return set_error(MOE_ERR_INVALID_ARG, "dispatch tensors NULL or not 16-byte aligned");
-  if (bad(workspace)) return set_error(MOE_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
-  const size_t need = dispatch_workspace_bytes(T, E);
+  if (!aligned(workspace, 16) || (!workspace && T * k > MOE_DISPATCH_SMALL_SLOTS))
+    return set_error(MOE_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+  const size_t need = workspace ? dispatch_workspace_bytes(T, E) : 0;
   if (ws_bytes < need)
     return set_error(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
   return launch_dispatch(x, ids, T, H, E, k, dtype, x_perm, inv, offsets,

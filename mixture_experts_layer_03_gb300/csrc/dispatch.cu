@@ -44,7 +44,7 @@ struct SortArgs {
   int32_t* totals;      // [E]
   int32_t* inv;
   int32_t* offsets;
-  int32_t* status;
+  int32_t* status;      // NULL (one launch only): no flag
 };
 
 // Slots per bin of each block's tokens, and whether an id is neither -1 nor in [0, E).
@@ -193,7 +193,7 @@ sort_place_kernel(SortArgs a, const char* __restrict__ x, char* __restrict__ x_p
     if (blockIdx.x == 0) {
       if (tid < a.E) a.offsets[tid] = off;
       if (tid == 0) a.offsets[a.E] = total;
-      if (tid < 4) a.status[tid] = tid == 0 && s_bad ? MOE_DEVICE_FLAG_BAD_ID : 0;
+      if (a.status && tid < 4) a.status[tid] = tid == 0 && s_bad ? MOE_DEVICE_FLAG_BAD_ID : 0;
     }
   } else {
     const int count = tid < a.E ? a.totals[tid] : 0;
@@ -531,7 +531,7 @@ int elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // Problems of at most this many slots are sorted and copied in one launch, every block counting all
 // ids (9222 slots, rows of 1001 f32: 13.5 us, in three launches 14.5; 32768 slots of 4096 bf16:
 // 69 us, in three launches 64).
-constexpr int64_t kSelfCountMax = 12 * 1024;
+constexpr int64_t kSelfCountMax = MOE_DISPATCH_SMALL_SLOTS;
 
 void chunk_plan(int64_t T, int64_t* chunk, int* nb) {
   *chunk = (T + kMaxBlocks - 1) / kMaxBlocks;
@@ -558,8 +558,8 @@ moe_status launch_dispatch(const void* x, const int32_t* ids, int64_t T, int H, 
   a.k = k;
   chunk_plan(T, &a.chunk, &a.nb);
   a.status = reinterpret_cast<int32_t*>(ws);
-  a.totals = a.status + 4;
-  a.hist = a.totals + E;
+  a.totals = ws ? a.status + 4 : nullptr;
+  a.hist = ws ? a.totals + E : nullptr;
   a.inv = inv;
   a.offsets = offsets;
   const bool self = a.P <= kSelfCountMax;

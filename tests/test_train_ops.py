@@ -61,7 +61,7 @@ def make_ids(T, E, k, kind, seed):
 SORTS = [(1, 8, 4, 2, "plain"), (1, 1, 1, 1, "plain"), (2, 64, 3, 8, "dropped"),
          (64, 2048, 128, 8, "plain"), (63, 1001, 60, 6, "dropped"), (513, 72, 256, 8, "dropped"),
          (700, 20, 8, 7, "one"), (300, 36, 5, 3, "none"), (3000, 40, 17, 3, "dropped"),
-         (5000, 8, 256, 8, "plain"), (1500, 520, 2, 5, "one"), (1025, 100, 33, 4, "dropped")]
+         (5000, 8, 256, 8, "plain"), (13000, 12, 40, 1, "dropped"), (1500, 520, 2, 5, "one"), (1025, 100, 33, 4, "dropped")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
@@ -114,7 +114,7 @@ def test_combine_gradient_against_differences(moe):
 
 
 def test_dispatch_flags_bad_ids_and_drops_them(moe):
-    for T in (4, 4000):                     # one launch, three launches
+    for T in (4, 7000):                     # one launch, three launches
         ids = make_ids(T, 8, 2, "plain", 1)
         ids[T // 2, 1] = 8
         ids[1, 0] = -2
