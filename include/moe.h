@@ -396,12 +396,13 @@ moe_status moe_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const uint
                                     void* stream);
 
 /* The experts' products over sorted rows: rows [offsets[e], offsets[e + 1]) are expert e's
- * (offsets [E + 1] int32 on the device, non-decreasing from 0; kept inside [0, R] by the kernel),
- * w [E, N, K].
+ * (offsets [E + 1] int32 on the device, non-decreasing; the kernel keeps them inside [0, R] and in
+ * order), w [E, N, K]. A part of the experts can be run with its part of a longer list of offsets.
  *   moe_experts_matmul      y [R, N]:     y[r] = x[r] . w[e]^T     (x [R, K])
  *   moe_experts_matmul_dx   dx [R, K]:    dx[r] = dy[r] . w[e]     (dy [R, N])
  *   moe_experts_matmul_dw   dw [E, N, K]: dw[e] = sum over e's rows of dy[r]^T . x[r]
- * Rows from offsets[E] on are zeros in y and dx; an expert without rows has dw = 0. fp32
+ * Rows of no expert (before offsets[0], from offsets[E] on) are zeros in y and dx; an expert
+ * without rows has dw = 0. fp32
  * accumulation, one rounding. dtype BF16 or F16; dw_dtype the same or F32, and with F32
  * `accumulate` adds to what dw holds. N and K: multiples of 8 up to 65536; R <= 2^23.
  * Workspace: for dw moe_experts_workspace_bytes(E) bytes (0 outside 1..256), 128-byte aligned,

@@ -643,7 +643,7 @@ def _offsets(offsets, E):
 
 def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None, stream=None):
     """y [R, N]: each row of x [R, K] times its expert's w[e]^T (w [E, N, K]); rows
-    [offsets[e], offsets[e + 1]) are expert e's, those past the last are zeros in y."""
+    [offsets[e], offsets[e + 1]) are expert e's, rows of no expert are zeros in y."""
     dt = _typed(x, "x", 2)
     _shaped(w, "w", (w.shape[0], w.shape[1], x.shape[1]) if w.dim() == 3 else (0, 0, 0), x.dtype)
     E, N, K = w.shape

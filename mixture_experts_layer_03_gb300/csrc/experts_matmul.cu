@@ -2,8 +2,8 @@
 //   forward   y[r]  = x[r] . w[e]^T           rows r of expert e, w [E, N, K]
 //   dx        dx[r] = dy[r] . w[e]
 //   dw        dw[e] = sum_{r of e} dy[r]^T . x[r]
-// Rows of expert e are [offsets[e], offsets[e+1]), offsets on the device. Rows past offsets[E]
-// are 0 in y and dx; an expert without rows has dw = 0.
+// Rows of expert e are [offsets[e], offsets[e+1]), offsets on the device. Rows of no expert, before
+// offsets[0] and from offsets[E] on, are 0 in y and dx; an expert without rows has dw = 0.
 //
 // One persistent kernel over all groups, CTA pairs (tcgen05.mma.cta_group::2, M = 256, N up to 256,
 // fp32 accumulators in TMEM, 64 elements of the contraction a block). The tensor cores take an
@@ -54,7 +54,7 @@ constexpr int kXAccCols = 256;
 constexpr int kXTmemCols = 512;
 constexpr int kXEpiWarps = 8;                 // two per TMEM lane quarter, 128 columns each
 constexpr int kXThreads = 64 + 32 * kXEpiWarps;
-constexpr int kXGroups = 257;                 // up to 256 experts, then the rows past the last
+constexpr int kXGroups = 258;                 // up to 256 experts, and the rows before and after them
 constexpr int kXRowBlocks = 8;                // row blocks that are walked together
 constexpr int kXStages = 6;                   // a block of both operands each
 constexpr int kXBoxBytes = 4096;              // epilogue staging of a warp
@@ -76,7 +76,7 @@ struct ExpertsArgs {
 };
 
 struct Tile {
-  int g;
+  int g;        // the expert
   int m0;       // this CTA's first index along M: a channel of the result, or a row of dw[g]
   int m_here;   // how many of its 128 exist
   int m_peer;   // the same of the other CTA
@@ -118,7 +118,9 @@ struct Walk {
 };
 
 // s_blk[g] (forward, dx): row tiles of the groups before g. s_start[g]: the first row of g;
-// s_start[G] the last one's end.
+// s_start[G] the last one's end. dw's groups are the experts; forward and dx have the rows before
+// the first expert's as group 0, expert e as group e + 1 and the rows past the last one's as
+// group E + 1.
 template <int kMode>
 __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, const int32_t* s_start,
                                             int G, const ExpertsArgs& a, const Walk& w,
@@ -167,7 +169,8 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
   t.m_peer = clamp_int(a.m_ext - (t.m0 + 128 * (rank ^ 1)), 0, 128);
   t.m0 += 128 * rank;
   t.m_here = clamp_int(a.m_ext - t.m0, 0, 128);
-  const int len = kMode == kDw ? rows : g < a.E ? a.k_ext : 0;
+  if (kMode != kDw) t.g = g - 1;
+  const int len = kMode == kDw ? rows : g > 0 && g <= a.E ? a.k_ext : 0;
   t.nkb = (len + kXBK - 1) / kXBK;
   t.nks = (len + 15) / 16;
   return t;
@@ -446,15 +449,15 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   pdl_wait();
   // The groups: their first rows, kept inside [0, R] and in order here, so that no offset can
   // lead a load or a store out of range, and the scan of their row blocks.
-  const int G = kMode == kDw ? a.E : a.E + 1;
+  const int G = kMode == kDw ? a.E : a.E + 2;
+  constexpr int kHead = kMode == kDw ? 0 : 1;
   if (warp == 2) {
     constexpr int kPer = kXGroups / 32 + 1;   // 32 * kPer > kXGroups: a lane reaches entry G
     int start[kPer + 1], most = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = lane * kPer + i;
-      // Group E of forward and dx: the rows past the last expert's, up to R.
-      start[i] = g <= a.E ? clamp_int(a.offsets[g], 0, a.R) : a.R;
+      start[i] = g < kHead ? 0 : g - kHead <= a.E ? clamp_int(a.offsets[g - kHead], 0, a.R) : a.R;
       if (i > 0) start[i] = max(start[i], start[i - 1]);
     }
     most = start[kPer - 1];
@@ -748,7 +751,7 @@ moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int
   a.f16 = dtype == MOE_DTYPE_F16;
   a.out = out;
   a.status = status;
-  const int64_t tiles = (R / 256 + E + 1) * ((nc + 255) / 256);
+  const int64_t tiles = (R / 256 + E + 2) * ((nc + 255) / 256);
   return dx ? launch_form<kDx, false>(ma, mb, mb32, mo, a, tiles, s)
             : launch_form<kFwd, false>(ma, mb, mb32, mo, a, tiles, s);
 }

@@ -276,7 +276,8 @@ def ragged(R, E, kind, seed):
     if kind == "empty":                      # no rows with any expert
         return np.zeros(E + 1, np.int32)
     cut = np.sort(rng.integers(0, R + 1, E + 1)).astype(np.int32)   # empties, a tail of no expert
-    cut[0] = 0
+    if kind != "part":                       # part: rows before the first expert's too
+        cut[0] = 0
     return cut
 
 
@@ -284,7 +285,8 @@ EXPERTS = [(1, 1, 8, 8, "even"), (1, 3, 16, 24, "last"), (5, 4, 72, 8, "cut"), (
            (128, 1, 64, 128, "even"), (129, 1, 136, 264, "even"), (255, 1, 128, 256, "first"),
            (257, 1, 320, 520, "even"), (300, 7, 200, 136, "cut"), (513, 256, 64, 64, "cut"),
            (700, 3, 328, 1032, "cut"), (64, 5, 512, 512, "empty"), (2100, 2, 72, 72, "cut"),
-           (1024, 4, 1024, 512, "even"), (2000, 1, 192, 2056, "even"), (40, 256, 256, 256, "cut")]
+           (1024, 4, 1024, 512, "even"), (2000, 1, 192, 2056, "even"), (40, 256, 256, 256, "cut"),
+           (700, 3, 64, 96, "part"), (900, 255, 64, 40, "part"), (2600, 256, 32, 32, "part")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -294,8 +296,9 @@ def test_experts_products(moe, R, E, K, N, kind, dtype):
     offsets = torch.from_numpy(off).cuda()
     x, dy = randn((R, K), dtype, 1), randn((R, N), dtype, 2)
     w = randn((E, N, K), dtype, 3, K ** -0.5)
-    x[off[E]:] = float("nan")                # rows of no expert reach nothing
-    dy[off[E]:] = float("nan")
+    for t in (x, dy):                        # rows of no expert reach nothing
+        t[off[E]:] = float("nan")
+        t[:off[0]] = float("nan")
     X, Y, W = n64(x), n64(dy), n64(w)
     scratch = moe.alloc_experts_scratch(E)
     got = {"y": moe.moe_experts_matmul(x, w, offsets, scratch=scratch),
