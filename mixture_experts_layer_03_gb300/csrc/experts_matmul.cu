@@ -29,9 +29,9 @@
 // so the pairs stay level without a counter. Every result element is written by one CTA from one
 // accumulator: the same result on every run.
 //
-// Warp roles (320 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first
-// CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, two warps to each). Two
-// accumulators let the epilogue of a tile overlap the next one's mainloop.
+// Warp roles (352 threads per CTA): warps 0 and 10 TMA producers of A and of B, warp 1 TMEM allocator
+// and, in the first CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, two
+// warps to each). Two accumulators let the epilogue of a tile overlap the next one's mainloop.
 #include <atomic>
 #include <cstdint>
 
@@ -53,7 +53,8 @@ constexpr int kXSlotBytes = 128 * kXBK * 2;   // one operand of one block in one
 constexpr int kXAccCols = 256;
 constexpr int kXTmemCols = 512;
 constexpr int kXEpiWarps = 8;                 // two per TMEM lane quarter, 128 columns each
-constexpr int kXThreads = 64 + 32 * kXEpiWarps;
+constexpr int kXWarpB = 2 + kXEpiWarps;       // the producer of B
+constexpr int kXThreads = 32 * (kXWarpB + 1);
 constexpr int kXGroups = 258;                 // up to 256 experts, and the rows before and after them
 constexpr int kXRowBlocks = 8;                // row blocks that are walked together
 constexpr int kXStages = 6;                   // a block of both operands each
@@ -117,28 +118,28 @@ struct Walk {
   }
 };
 
-// s_blk[g] (forward, dx): row tiles of the groups before g. s_start[g]: the first row of g;
+// The tile of an index, by a whole warp whose indices only grow (`from`: the group of its last
+// one, 0 to begin with). s_blk[g] (forward, dx): row tiles of the groups before g. s_start[g]: the first row of g;
 // s_start[G] the last one's end. dw's groups are the experts; forward and dx have the rows before
 // the first expert's as group 0, expert e as group e + 1 and the rows past the last one's as
 // group E + 1.
 template <int kMode>
 __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, const int32_t* s_start,
                                             int G, const ExpertsArgs& a, const Walk& w,
-                                            int rank) {
+                                            int rank, int lane, int& from) {
   const int blk = w.inner(idx);
   int g, outer, before;
   if (kMode == kDw) {
+    (void)lane, (void)from, (void)s_blk, (void)G;
     outer = w.outer.d;
     g = w.outer(blk);
     before = g * outer;
   } else {
-    int hi = G;
-    g = 0;   // s_blk[g] <= blk < s_blk[hi]
-    while (hi - g > 1) {
-      const int mid = (g + hi) >> 1;
-      if (s_blk[mid] <= blk) g = mid;
-      else hi = mid;
-    }
+    // On from the last tile's group, 32 groups a step: s_blk[g] <= blk < s_blk[g + 1].
+    g = from;
+    for (int more = 32; more == 32; g += more)
+      more = __popc(__ballot_sync(0xffffffffu, s_blk[min(g + 1 + lane, G)] <= blk));
+    from = g;
     before = s_blk[g];
     outer = s_blk[g + 1] - before;
   }
@@ -158,7 +159,7 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
     n_end = min(a.n_ext, t.n0 + 256);
     t.k0 = start;
   } else {
-    const int size = (((rows + 15) >> 4) + outer - 1) / outer * 16;   // of the group's equal tiles
+    const int size = Div(outer)(((rows + 15) >> 4) + outer - 1) * 16;   // of the group's equal tiles
     t.m0 = i * 256;
     t.n0 = start + o * size;
     n_end = min(start + rows, t.n0 + size);
@@ -193,26 +194,17 @@ __device__ __forceinline__ void x_timeout(int32_t* status, volatile int* abort) 
 // in boxes of 64 columns. An operand across the contraction comes in boxes of 64 (its swizzle's
 // width) by the 64 of the block.
 template <int kMode>
-__device__ __forceinline__ bool produce_tile(const Tile& t, const CUtensorMap* ma,
-                                             const CUtensorMap* mb, const CUtensorMap* mb32,
-                                             int rank, int& stage, uint32_t& phase, uint8_t* sA,
-                                             uint8_t* sB, uint32_t lead_full, uint64_t* full_bar,
-                                             uint64_t* empty_bar, volatile int* abort) {
-  const int half = t.n >> 1;
-  const bool narrow = kMode != kDw && half <= 64;
-  const int box = kMode == kDw ? 64 : narrow ? 32 : 128;   // of B along N; 128 bytes each
-  const bool two = half > box;
-  const CUtensorMap* mbx = narrow ? mb32 : mb;
-  const uint32_t tx =
-      kXSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) + 2 * (two ? 2 : 1) * box * 128;
-  const int n0 = t.n0 + rank * half;
+__device__ __forceinline__ bool produce_a(const Tile& t, const CUtensorMap* ma, int rank, int& stage,
+                                          uint32_t& phase, uint8_t* sA, uint32_t lead_full,
+                                          uint64_t* full_bar, uint64_t* empty_bar,
+                                          volatile int* abort) {
+  const uint32_t tx = kXSlotBytes * ((t.m_here > 0) + (t.m_peer > 0));
   for (int kb = 0; kb < t.nkb; ++kb) {
     if (!__all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort))) return false;
     if (elect_one()) {
       if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
       const uint32_t fb = lead_full + 8u * stage;
       uint8_t* as = sA + stage * kXSlotBytes;
-      uint8_t* bs = sB + stage * kXSlotBytes;
       const int kc = t.k0 + kb * kXBK;
       if (t.m_here > 0) {
         if (kMode == kFwd) {
@@ -225,6 +217,36 @@ __device__ __forceinline__ bool produce_tile(const Tile& t, const CUtensorMap* m
           tma_load_2d_pair(as + kXSlotBytes / 2, ma, fb, t.m0 + 64, kc);
         }
       }
+    }
+    __syncwarp();
+    if (++stage == kXStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  return true;
+}
+
+template <int kMode>
+__device__ __forceinline__ bool produce_b(const Tile& t, const CUtensorMap* mb,
+                                          const CUtensorMap* mb32, int rank, int& stage,
+                                          uint32_t& phase, uint8_t* sB, uint32_t lead_full,
+                                          uint64_t* full_bar, uint64_t* empty_bar,
+                                          volatile int* abort) {
+  const int half = t.n >> 1;
+  const bool narrow = kMode != kDw && half <= 64;
+  const int box = kMode == kDw ? 64 : narrow ? 32 : 128;   // along N; 128 bytes each
+  const bool two = half > box;
+  const CUtensorMap* mbx = narrow ? mb32 : mb;
+  const uint32_t tx = 2 * (two ? 2 : 1) * box * 128;
+  const int n0 = t.n0 + rank * half;
+  for (int kb = 0; kb < t.nkb; ++kb) {
+    if (!__all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort))) return false;
+    if (elect_one()) {
+      if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], tx);
+      const uint32_t fb = lead_full + 8u * stage;
+      uint8_t* bs = sB + stage * kXSlotBytes;
+      const int kc = t.k0 + kb * kXBK;
       if (kMode == kDw) {
         tma_load_2d_pair(bs, mbx, fb, n0, kc);
         if (two) tma_load_2d_pair(bs + kXSlotBytes / 2, mbx, fb, n0 + 64, kc);
@@ -333,12 +355,11 @@ __device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int 
   }
 }
 
-// Forward and dx: one warp's part of a tile, 32 channels (its TMEM lane quarter, a lane each) by
-// every second block of 32 rows. Two rows of a channel are packed, exchanged with the neighbouring
-// lane's, and leave the even lane with both channels of the first row and the odd lane with
-// those of the second: 4-byte stores, without bank conflicts, into a box of 32 rows of 64 bytes
-// (64-byte swizzle). Whole boxes go out by TMA, which leaves out channels past the last; a group's
-// last rows straight to memory.
+// Forward and dx: one warp's part of a tile, 32 channels (its TMEM lane quarter) by every second
+// block of 32 rows. The accumulator, channels by rows, is read in matrix fragments, two rows of a
+// channel packed together, and transposed by the matrix store into a box of 32 rows of 64 bytes
+// (64-byte swizzle). Whole boxes go out by TMA, which leaves out channels past the last; of the
+// box with a group's last rows, the rows that exist.
 template <typename Done>
 __device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, int half, int lane,
                                            uint8_t* buf, int& sbuf, const CUtensorMap* map,
@@ -348,46 +369,50 @@ __device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, in
     return;
   }
   const bool f16 = a.f16 != 0;
-  const bool odd = lane & 1;
   const int ch = t.m0 + 32 * q;
-  const int pair = lane >> 1;   // channels ch + 2 * pair and the next
 #pragma unroll 1
   for (int r0 = 32 * half; r0 < t.n_here; r0 += 64) {
     uint32_t v[32];
     if (t.nkb > 0) {
-      tmem_ld(tb + r0, v);
+      tmem_ld_fragments(tb + r0, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0;
     }
     if (r0 + 64 >= t.n_here) done();
-    uint32_t o[16];   // row 2i of the block in even lanes, 2i + 1 in odd ones
+    uint32_t p[16];   // [channels 8 b .. + 7][rows 8 i .. + 7]: p[4 i + b]
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t mine =
-          pack_16bit(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-      o[i] = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-    }
-    const int rows = t.n_here - r0;
-    if (rows < 32) {
-      if (32 * q + 2 * pair < t.m_here) {   // m_ext is even
-        uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        static_cast<int64_t>(t.n0 + r0 + odd) * a.m_ext + ch + 2 * pair;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (2 * i + odd < rows)
-            *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(2 * i) * a.m_ext) = o[i];
+      for (int b = 0; b < 4; ++b) {
+        const int r = 16 * (b >> 1) + 4 * i + 2 * (b & 1);
+        p[4 * i + b] = pack_16bit(__uint_as_float(v[r]), __uint_as_float(v[r + 1]), f16);
       }
-      continue;
-    }
     uint8_t* box = buf + sbuf * (kXBoxBytes / 2);
     if (lane == 0) bulk_wait_group_read<1>();   // what was stored from this box before is out
     __syncwarp();
+    // Row 8 i + lane % 8, chunk of 8 channels lane / 8.
+    const uint32_t at = smem_u32(box) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      *reinterpret_cast<uint32_t*>(box + (2 * i + odd) * 64 + (((pair >> 2) ^ (i & 3)) << 4) +
-                                   (pair & 3) * 4) = o[i];
+    for (int i = 0; i < 4; ++i)
+      stmatrix_trans(at + i * 512, p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+    const int rows = t.n_here - r0;
+    if (rows < 32) {
+      __syncwarp();
+      const int c = lane & 3;   // chunk of 8 channels; m_ext is a multiple of 8
+      if (32 * q + 8 * c < t.m_here) {
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        static_cast<int64_t>(t.n0 + r0) * a.m_ext + ch + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 2);
+          if (row < rows)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * a.m_ext) =
+                *reinterpret_cast<const uint4*>(box + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+        }
+      }
+      continue;   // a group's last box; the next tile's waits for the warp at its own barrier
+    }
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {
@@ -425,7 +450,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
-      mbar_init(&full_bar[s], 1);    // first CTA: its producer's arrival and both CTAs' bytes
+      mbar_init(&full_bar[s], 2);    // first CTA: its two producers, and both CTAs' bytes
       mbar_init(&empty_bar[s], 1);   // the pair commit, delivered to both CTAs
     }
     for (int s = 0; s < 2; ++s) {
@@ -501,26 +526,25 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  int group = 0;   // of this warp's last tile
+  if (warp == 0 || warp == kXWarpB) {
+    // ------------------------------------------------------------ TMA producers of A and of B
     int stage = 0, last_g = -1;
     uint32_t phase = 0;
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank);
+      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
       if (t.nkb == 0) continue;
-      const CUtensorMap* ma = &map_a;
-      const CUtensorMap* mb = &map_b;
+      const CUtensorMap* map = warp == 0 ? &map_a : &map_b;
       if (kMode == kDw) {
-        ma = a.maps + t.g;
-        mb = a.maps + a.E + t.g;
-        if (t.g != last_g) {
-          tmap_acquire(ma);
-          tmap_acquire(mb);
-          last_g = t.g;
-        }
+        map = a.maps + (warp == 0 ? 0 : a.E) + t.g;
+        if (t.g != last_g) tmap_acquire(map);
+        last_g = t.g;
       }
-      if (!produce_tile<kMode>(t, ma, mb, &map_b32, rank, stage, phase, sA, sB, lead_full, full_bar,
-                               empty_bar, abort)) {
+      const bool ok = warp == 0 ? produce_a<kMode>(t, map, rank, stage, phase, sA, lead_full,
+                                                   full_bar, empty_bar, abort)
+                                : produce_b<kMode>(t, map, &map_b32, rank, stage, phase, sB,
+                                                   lead_full, full_bar, empty_bar, abort);
+      if (!ok) {
         x_timeout(a.status, abort);
         break;
       }
@@ -547,7 +571,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       const uint64_t db0 = kMode == kDw ? sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2)
                                         : sdesc_k_major(smem_u32(sB), 128);
       for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, 0);
+        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, 0, lane, group);
         if (t.nkb == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort));
         if (ok) {
@@ -582,7 +606,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     int sbuf = 0, acc = 0;
     uint32_t acc_phase = 0;
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank);
+      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
       const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
       const bool zeros = t.nkb == 0;   // nothing was multiplied, no accumulator taken
       if (zeros && kF32 && a.add) continue;

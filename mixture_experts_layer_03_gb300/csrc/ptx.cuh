@@ -525,4 +525,32 @@ __device__ __forceinline__ void tmem_ld(uint32_t ta, uint32_t (&r)[64]) {
       : "memory");
 }
 
+// Two 16x256b.x4 TMEM loads (lanes 0-15 and 16-31 of the warp's quarter, 32 columns each) and the
+// wait. In each 8 x 8 block of (lane, column) a thread holds two neighbouring columns of one
+// lane, the layout of a matrix fragment: r[16 h + 4 i + 2 s + c] is lane 16 h + 8 s + t / 4, column
+// 8 i + 2 (t % 4) + c of thread t.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t ta, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta), "r"(ta + (16u << 16))
+      : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit fragments, transposed, to shared memory: thread t gives the address of
+// row t % 8 of block t / 8 (16 bytes each).
+__device__ __forceinline__ void stmatrix_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 }  // namespace moe
