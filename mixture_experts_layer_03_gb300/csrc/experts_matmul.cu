@@ -30,8 +30,8 @@
 // accumulator: the same result on every run.
 //
 // Warp roles (352 threads per CTA): warps 0 and 10 TMA producers of A and of B, warp 1 TMEM allocator
-// and, in the first CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31, two
-// warps to each). Two accumulators let the epilogue of a tile overlap the next one's mainloop.
+// and, in the first CTA, MMA issuer, warps 2-9 epilogue (TMEM lanes 32 * (warp % 4) .. + 31), four
+// to each of two accumulators, so that the epilogue of a tile overlaps the next one's mainloop.
 #include <atomic>
 #include <cstdint>
 
@@ -52,7 +52,7 @@ constexpr int kXBK = 64;                      // contraction elements a block
 constexpr int kXSlotBytes = 128 * kXBK * 2;   // one operand of one block in one CTA
 constexpr int kXAccCols = 256;
 constexpr int kXTmemCols = 512;
-constexpr int kXEpiWarps = 8;                 // two per TMEM lane quarter, 128 columns each
+constexpr int kXEpiWarps = 8;                 // two sets of four, one set to an accumulator
 constexpr int kXWarpB = 2 + kXEpiWarps;       // the producer of B
 constexpr int kXThreads = 32 * (kXWarpB + 1);
 constexpr int kXGroups = 258;                 // up to 256 experts, and the rows before and after them
@@ -106,6 +106,12 @@ struct Div {
   }
 };
 
+// n / d for 0 <= n < 2^12 and small d, by an approximate reciprocal: (n + 1/2) / d is at least 1 / 2d
+// from a whole number, far more than its error.
+__device__ __forceinline__ int small_div(int n, int d) {
+  return static_cast<int>(__fdividef(static_cast<float>(n) + 0.5f, static_cast<float>(d)));
+}
+
 // Divisors of a tile's index. "Outer" tiles are those of the rows in forward and dx and of M in dw,
 // "inner" ones those of M and of N: kXRowBlocks outer tiles by all inner ones make a set, walked
 // outer tile first.
@@ -148,8 +154,8 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
   const int set = w.set(local);
   const int rest = local - set * w.set.d;
   const int here = min(kXRowBlocks, outer - set * kXRowBlocks);
-  const int i = here == kXRowBlocks ? rest / kXRowBlocks : Div(here)(rest);   // inner tile
-  const int o = set * kXRowBlocks + rest - i * here;                          // outer tile
+  const int i = small_div(rest, here);              // inner tile (rest < 8 * 256)
+  const int o = set * kXRowBlocks + rest - i * here;   // outer tile
   Tile t;
   t.g = g;
   int n_end;
@@ -159,7 +165,10 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
     n_end = min(a.n_ext, t.n0 + 256);
     t.k0 = start;
   } else {
-    const int size = Div(outer)(((rows + 15) >> 4) + outer - 1) * 16;   // of the group's equal tiles
+    // Of the group's equal tiles: u = rows / 16 (rounded up) over `outer` = u / 16 (rounded up),
+    // rounded up, that is 16 - (16 outer - u) / outer, where 16 outer - u < 16.
+    const int spare = 16 * outer - ((rows + 15) >> 4);
+    const int size = 256 - 16 * small_div(spare, outer);
     t.m0 = i * 256;
     t.n0 = start + o * size;
     n_end = min(start + rows, t.n0 + size);
@@ -304,122 +313,147 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// dw: one warp's part of a tile, 32 rows of dw[g] (TMEM lane quarter q) by 128 columns, in boxes of
+// dw: one warp's part of a tile, 32 rows of dw[g] (TMEM lane quarter q) by its columns, in boxes of
 // 128 bytes of columns (64 16-bit or 32 f32 values) through shared memory and out by TMA, which
 // leaves out what lies beyond dw[g]. `done` runs once the accumulator has been read.
-// Two warps a lane quarter: a box costs a warp about 700 cycles of latency (TMEM load, fence, the
-// store's read of the box), so that four warps held tiles with short contractions to 3.3 us (256
-// experts of 128 rows, N = 7168, K = 2048: 2.50 ms, with eight 1.9 ms; writing the result alone
-// takes 1.87 at the 4.0 TB/s that a write-only stream reaches).
+// Eight warps, two to a lane quarter: a box costs a warp about 700 cycles of latency (TMEM load,
+// fence, the store's read of the box), so that four warps held tiles with short contractions to 3.3
+// us (256 experts of 128 rows, N = 7168, K = 2048: 2.50 ms, with eight 1.9 ms; writing the result
+// alone takes 1.87 at the 4.0 TB/s that a write-only stream reaches).
 template <bool kF32, typename Done>
-__device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int half, int lane,
+__device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int lane,
                                          uint8_t* buf, const CUtensorMap* map,
                                          const ExpertsArgs& a, Done&& done) {
-  const int cols = min(128, t.n_here - 128 * half);
-  if (32 * q >= t.m_here || cols <= 0) {
+  const int cols = t.n_here;
+  if (32 * q >= t.m_here) {
     done();
     return;
   }
   constexpr int kCols = kF32 ? 32 : 64;   // of a box
   const bool f16 = a.f16 != 0;
-  const int row = t.m0 + 32 * q, col = t.n0 + 128 * half;
+  const int row = t.m0 + 32 * q, col = t.n0;
   uint4* mine = reinterpret_cast<uint4*>(buf + lane * 128);
 #pragma unroll 1
-  for (int c0 = 0; c0 < cols; c0 += kCols) {
-    uint32_t v[kCols];
+  for (int c0 = 0; c0 < cols; c0 += 64) {
+    uint32_t v[2][32];
     if (t.nkb > 0) {
-      tmem_ld(tb + 128 * half + c0, v);
+      tmem_issue(tb + c0, v[0]);
+      tmem_issue(tb + c0 + 32, v[1]);
+      tmem_wait();
+      tmem_ready(v[0]);
+      tmem_ready(v[1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] = 0;
+      for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0;
     }
-    if (c0 + kCols >= cols) done();
-    uint4 o[8];
-    uint32_t* w = reinterpret_cast<uint32_t*>(o);
+    if (c0 + 64 >= cols) done();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if constexpr (kF32) w[i] = v[i];
-      else w[i] = pack_16bit(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
-    }
-    if (lane == 0) bulk_wait_group_read<0>();   // the box before has been read out
-    __syncwarp();
+    for (int c = 0; c < 64; c += kCols) {
+      if (c0 + c >= cols) break;
+      uint4 o[8];
+      uint32_t* w = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mine[i ^ (lane & 7)] = o[i];
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      if (kF32 && a.add) tma_add_3d(map, buf, col + c0, row, t.g);
-      else tma_store_3d(map, buf, col + c0, row, t.g);
-      bulk_commit_group();
+      for (int i = 0; i < 32; ++i) {
+        if constexpr (kF32)
+          w[i] = v[c / 32][i];
+        else
+          w[i] = pack_16bit(__uint_as_float(v[i / 16][2 * i % 32]),
+                            __uint_as_float(v[i / 16][2 * i % 32 + 1]), f16);
+      }
+      if (lane == 0) bulk_wait_group_read<0>();   // the box before has been read out
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine[i ^ (lane & 7)] = o[i];
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (kF32 && a.add) tma_add_3d(map, buf, col + c0 + c, row, t.g);
+        else tma_store_3d(map, buf, col + c0 + c, row, t.g);
+        bulk_commit_group();
+      }
     }
   }
 }
 
-// Forward and dx: one warp's part of a tile, 32 channels (its TMEM lane quarter) by every second
-// block of 32 rows. The accumulator, channels by rows, is read in matrix fragments, two rows of a
+// Forward and dx: one warp's part of a tile, 32 channels (its TMEM lane quarter) by the tile's rows, 32
+// at a time. The accumulator, channels by rows, is read in matrix fragments, two rows of a
 // channel packed together, and transposed by the matrix store into a box of 32 rows of 64 bytes
 // (64-byte swizzle). Whole boxes go out by TMA, which leaves out channels past the last; of the
 // box with a group's last rows, the rows that exist.
 template <typename Done>
-__device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, int half, int lane,
+__device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, int lane,
                                            uint8_t* buf, int& sbuf, const CUtensorMap* map,
                                            const ExpertsArgs& a, Done&& done) {
-  if (32 * q >= t.m_here || 32 * half >= t.n_here) {
+  if (32 * q >= t.m_here) {
     done();
     return;
   }
   const bool f16 = a.f16 != 0;
   const int ch = t.m0 + 32 * q;
 #pragma unroll 1
-  for (int r0 = 32 * half; r0 < t.n_here; r0 += 64) {
-    uint32_t v[32];
+  for (int r2 = 0; r2 < t.n_here; r2 += 64) {
+    // Two of them at once: a load takes 400 cycles beside the tile's other warps.
+    uint32_t v[2][2][16];   // [block of 32 rows][lanes 0-15, 16-31]
+    const bool both = r2 + 32 < t.n_here;
     if (t.nkb > 0) {
-      tmem_ld_fragments(tb + r0, v);
+      tmem_issue_fragments(tb + r2, v[0][0]);
+      tmem_issue_fragments(tb + r2 + (16u << 16), v[0][1]);
+      if (both) {
+        tmem_issue_fragments(tb + r2 + 32, v[1][0]);
+        tmem_issue_fragments(tb + r2 + 32 + (16u << 16), v[1][1]);
+      }
+      tmem_wait();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ready(v[i >> 1][i & 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0;
+      for (int i = 0; i < 64; ++i) v[i >> 5][(i >> 4) & 1][i & 15] = 0;
     }
-    if (r0 + 64 >= t.n_here) done();
-    uint32_t p[16];   // [channels 8 b .. + 7][rows 8 i .. + 7]: p[4 i + b]
+    if (r2 + 64 >= t.n_here) done();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !both) break;
+      const int r0 = r2 + 32 * k;
+      uint32_t p[16];   // [channels 8 b .. + 7][rows 8 i .. + 7]: p[4 i + b]
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int r = 16 * (b >> 1) + 4 * i + 2 * (b & 1);
-        p[4 * i + b] = pack_16bit(__uint_as_float(v[r]), __uint_as_float(v[r + 1]), f16);
-      }
-    uint8_t* box = buf + sbuf * (kXBoxBytes / 2);
-    if (lane == 0) bulk_wait_group_read<1>();   // what was stored from this box before is out
-    __syncwarp();
-    // Row 8 i + lane % 8, chunk of 8 channels lane / 8.
-    const uint32_t at = smem_u32(box) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      stmatrix_trans(at + i * 512, p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-    const int rows = t.n_here - r0;
-    if (rows < 32) {
+        for (int b = 0; b < 4; ++b)
+          p[4 * i + b] = pack_16bit(__uint_as_float(v[k][b >> 1][4 * i + 2 * (b & 1)]),
+                                    __uint_as_float(v[k][b >> 1][4 * i + 2 * (b & 1) + 1]), f16);
+      uint8_t* box = buf + sbuf * (kXBoxBytes / 2);
+      if (lane == 0) bulk_wait_group_read<1>();   // what was stored from this box before is out
       __syncwarp();
-      const int c = lane & 3;   // chunk of 8 channels; m_ext is a multiple of 8
-      if (32 * q + 8 * c < t.m_here) {
-        uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        static_cast<int64_t>(t.n0 + r0) * a.m_ext + ch + 8 * c;
+      // Row 8 i + lane % 8, chunk of 8 channels lane / 8.
+      const uint32_t at = smem_u32(box) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * i + (lane >> 2);
-          if (row < rows)
-            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * a.m_ext) =
-                *reinterpret_cast<const uint4*>(box + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+      for (int i = 0; i < 4; ++i)
+        stmatrix_trans(at + i * 512, p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+      const int rows = t.n_here - r0;
+      if (rows < 32) {
+        __syncwarp();
+        const int c = lane & 3;   // chunk of 8 channels; m_ext is a multiple of 8
+        if (32 * q + 8 * c < t.m_here) {
+          uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                          static_cast<int64_t>(t.n0 + r0) * a.m_ext + ch + 8 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2);
+            if (row < rows)
+              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * a.m_ext) =
+                  *reinterpret_cast<const uint4*>(box + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+          }
         }
+        break;   // a tile's last box
       }
-      continue;   // a group's last box; the next tile's waits for the warp at its own barrier
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(map, box, ch, t.n0 + r0);
+        bulk_commit_group();
+      }
+      sbuf ^= 1;
     }
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(map, box, ch, t.n0 + r0);
-      bulk_commit_group();
-    }
-    sbuf ^= 1;
   }
 }
 
@@ -455,7 +489,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull_bar[s], 1);
-      mbar_init(&tempty_bar[s], 2 * kXEpiWarps);  // first CTA: the epilogue warps of both
+      mbar_init(&tempty_bar[s], kXEpiWarps);  // first CTA: four epilogue warps of each CTA
     }
     mbar_init(&drain_bar, 1);
     s_abort = 0;
@@ -563,8 +597,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     if (lead) {
       // ------------------------------------------------------------ MMA issuer (first CTA)
       // The whole warp walks the tiles; one thread issues.
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      int stage = 0, acc = 1;
+      uint32_t phase = 0, acc_phase = 0;   // bit `acc`: of that accumulator's barriers
       bool ok = true;
       const uint64_t da0 = kMode == kFwd ? sdesc_k_major(smem_u32(sA), 128)
                                          : sdesc_mn_major(smem_u32(sA), kXSlotBytes / 2);
@@ -572,8 +606,9 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
                                         : sdesc_k_major(smem_u32(sB), 128);
       for (int idx = first; idx < total; idx += step) {
         const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, 0, lane, group);
+        acc ^= 1;
         if (t.nkb == 0) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], acc_phase ^ 1u, abort));
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], ~(acc_phase >> acc) & 1u, abort));
         if (ok) {
           tc_fence_after();
           const uint32_t idesc = idesc_16bit_f32(256, t.n, a.f16 != 0, kMode != kFwd, kMode == kDw);
@@ -586,10 +621,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         if (elect_one()) umma_commit_pair(&tfull_bar[acc], kXPairMask);
         __syncwarp();
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        acc_phase ^= 1u << acc;
       }
       if (!ok) {
         // Every MMA issued so far ends (bounded wait) before TMEM is released.
@@ -600,15 +632,17 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
+    // Tile i of the pair has accumulator i % 2, which one set of four warps reads: a set's latency
+    // from one tile to its next has two tiles' time.
     const int q = warp & 3;   // TMEM lane quarter of this warp
-    const int half = (warp - 2) >> 2;
+    const int acc = (warp - 2) >> 2;
     uint8_t* my_box = sOut + (warp - 2) * kXBoxBytes;
-    int sbuf = 0, acc = 0;
+    const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
+    int sbuf = 0;
     uint32_t acc_phase = 0;
-    for (int idx = first; idx < total; idx += step) {
+    for (int idx = first + acc * step; idx < total; idx += 2 * step) {
       const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
-      const uint32_t tb = tmem_base + acc * kXAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      const bool zeros = t.nkb == 0;   // nothing was multiplied, no accumulator taken
+      const bool zeros = t.nkb == 0;   // nothing was multiplied
       if (zeros && kF32 && a.add) continue;
       if (!zeros) {
         const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
@@ -618,6 +652,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
           break;
         }
         tc_fence_after();
+        acc_phase ^= 1u;
       }
       auto done = [&] {
         if (zeros) return;
@@ -629,13 +664,9 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
         }
       };
       if constexpr (kMode == kDw)
-        store_dw<kF32>(tb, t, q, half, lane, my_box, &map_out, a, done);
+        store_dw<kF32>(tb, t, q, lane, my_box, &map_out, a, done);
       else
-        store_rows(tb, t, q, half, lane, my_box, sbuf, &map_out, a, done);
-      if (!zeros && ++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+        store_rows(tb, t, q, lane, my_box, sbuf, &map_out, a, done);
     }
     // Every TMA store of this warp has written its box before the CTA ends.
     if (lane == 0) bulk_wait_group<0>();
