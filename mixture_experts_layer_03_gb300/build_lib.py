@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", platform.machine())
 LIB_NAME = "libmoe_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "route.cu", "permute.cu", "grouped_gemm.cu", "finalize.cu", "gate.cu",
-           "selftest.cu", "dispatch.cu", "swiglu_ckpt.cu", "experts_matmul.cu",
+           "selftest.cu", "dispatch.cu", "swiglu_ckpt.cu", "experts_matmul.cu", "experts_few.cu",
            "route_backward.cu", "api_train.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -56,6 +56,9 @@ moe_status experts_rows(bool dx, const void* in, const void* w, const int32_t* o
   if (st != MOE_OK || R == 0) return st;
   if (bad(in) || bad(w) || bad(out) || !offsets || !aligned(offsets, 4))
     return set_error(MOE_ERR_INVALID_ARG, "rows, weights or offsets NULL or misaligned");
+  if (experts_few(dx, R, E, K))
+    return launch_experts_few(dx, in, w, offsets, R, E, N, K, dtype, out,
+                              static_cast<cudaStream_t>(stream));
   return launch_experts_rows(dx, in, w, offsets, R, E, N, K, dtype, out, status,
                              static_cast<cudaStream_t>(stream));
 }

@@ -136,6 +136,10 @@ size_t experts_workspace_bytes(int E);
 moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
                                int64_t R, int E, int N, int K, int dtype, void* out,
                                int32_t* status, cudaStream_t s);
+// The same for few rows, where experts_few says so (R <= 16).
+bool experts_few(bool dx, int64_t R, int E, int K);
+moe_status launch_experts_few(bool dx, const void* in, const void* w, const int32_t* offsets,
+                              int64_t R, int E, int N, int K, int dtype, void* out, cudaStream_t s);
 moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
                              char* ws, cudaStream_t s);

@@ -281,7 +281,9 @@ def ragged(R, E, kind, seed):
     return cut
 
 
-EXPERTS = [(1, 1, 8, 8, "even"), (1, 3, 16, 24, "last"), (5, 4, 72, 8, "cut"), (127, 2, 64, 256, "cut"),
+EXPERTS = [(1, 1, 8, 8, "even"), (4, 3, 520, 3080, "cut"), (3, 1, 264, 136, "last"), (4, 200, 72, 9000, "part"), (2, 5, 2056, 72, "part"), (9, 2, 4104, 136, "cut"), (16, 256, 264, 200, "cut"),
+           (13, 1, 72, 5000, "even"), (16, 3, 1032, 2056, "part"), (7, 40, 24, 16, "empty"),
+           (17, 4, 136, 520, "cut"), (1, 3, 16, 24, "last"), (5, 4, 72, 8, "cut"), (127, 2, 64, 256, "cut"),
            (128, 1, 64, 128, "even"), (129, 1, 136, 264, "even"), (255, 1, 128, 256, "first"),
            (257, 1, 320, 520, "even"), (300, 7, 200, 136, "cut"), (513, 256, 64, 64, "cut"),
            (700, 3, 328, 1032, "cut"), (64, 5, 512, 512, "empty"), (2100, 2, 72, 72, "cut"),
