@@ -58,6 +58,7 @@ route_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ 
       if (id >= 0) {
         d = __ldg(ds + t * k + lane);
         l = finite_or_low(__ldg(row + id));
+        if (l == -INFINITY) d = 0.0f;   // its weight is 0 whatever the logit
       }
     }
     float p[kSlots], common = 0.0f;   // Default: this lane's probabilities and sum_j ds_j p_j

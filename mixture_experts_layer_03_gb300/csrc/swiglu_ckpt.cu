@@ -217,7 +217,11 @@ swiglu_ckpt_grad_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
   }
 }
 
-// Any I: one channel a lane, a warp to a block of 32 channels.
+// Any I: neighbouring channels to neighbouring lanes, a warp to kAnyBlocks blocks of 32 channels.
+// (Eight channels a lane here, as above but one element at a time, took 19 us for the backward
+// pass of 2000 rows of 1001 channels, this form 11.)
+constexpr int kAnyBlocks = 4;
+
 template <typename T>
 __global__ void __launch_bounds__(kCkptThreads)
 swiglu_ckpt_any_kernel(const T* __restrict__ gu, int64_t R, int I, T* __restrict__ h,
@@ -226,25 +230,33 @@ swiglu_ckpt_any_kernel(const T* __restrict__ gu, int64_t R, int I, T* __restrict
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w(nb); w.row < R; w.next()) {
-    const int c = w.seg * kCkptBlock + lane;
-    const bool in = c < I;
-    const T* src = gu + w.row * 2 * I + c;
-    const float g = in ? to_f32<T>(src[0]) : 0.0f;
-    const float u = in ? to_f32<T>(src[I]) : 0.0f;
-    const uint32_t mg = __reduce_max_sync(0xffffffffu, __float_as_uint(g) & 0x7fffffffu);
-    const uint32_t mu = __reduce_max_sync(0xffffffffu, __float_as_uint(u) & 0x7fffffffu);
-    const uint32_t sg = scale_byte(__uint_as_float(mg)), su = scale_byte(__uint_as_float(mu));
-    if (in) {
-      h[w.row * I + c] = from_f32<T>(g * sigmoid_fast(g) * u);
-      uint8_t* dst = q + w.row * 2 * I + c;
-      dst[0] = static_cast<uint8_t>(quant2(g * inv_scale(sg), 0.0f));
-      dst[I] = static_cast<uint8_t>(quant2(u * inv_scale(su), 0.0f));
+  for (Walk w((nb + kAnyBlocks - 1) / kAnyBlocks); w.row < R; w.next()) {
+    const int b0 = w.seg * kAnyBlocks;
+    const T* src = gu + w.row * 2 * I;
+    float g[kAnyBlocks], u[kAnyBlocks];
+#pragma unroll
+    for (int i = 0; i < kAnyBlocks; ++i) {
+      const int c = (b0 + i) * kCkptBlock + lane;
+      g[i] = c < I ? to_f32<T>(__ldg(src + c)) : 0.0f;
+      u[i] = c < I ? to_f32<T>(__ldg(src + I + c)) : 0.0f;
     }
-    if (lane == 0) {
-      uint8_t* sd = qs + w.row * 2 * nb + w.seg;
-      sd[0] = static_cast<uint8_t>(sg);
-      sd[nb] = static_cast<uint8_t>(su);
+#pragma unroll
+    for (int i = 0; i < kAnyBlocks; ++i) {
+      const int c = (b0 + i) * kCkptBlock + lane;
+      const uint32_t mg = __reduce_max_sync(0xffffffffu, __float_as_uint(g[i]) & 0x7fffffffu);
+      const uint32_t mu = __reduce_max_sync(0xffffffffu, __float_as_uint(u[i]) & 0x7fffffffu);
+      const uint32_t sg = scale_byte(__uint_as_float(mg)), su = scale_byte(__uint_as_float(mu));
+      if (c < I) {
+        h[w.row * I + c] = from_f32<T>(g[i] * sigmoid_fast(g[i]) * u[i]);
+        uint8_t* dst = q + w.row * 2 * I + c;
+        dst[0] = static_cast<uint8_t>(quant2(g[i] * inv_scale(sg), 0.0f));
+        dst[I] = static_cast<uint8_t>(quant2(u[i] * inv_scale(su), 0.0f));
+      }
+      if (lane == 0 && b0 + i < nb) {
+        uint8_t* sd = qs + w.row * 2 * nb + b0 + i;
+        sd[0] = static_cast<uint8_t>(sg);
+        sd[nb] = static_cast<uint8_t>(su);
+      }
     }
   }
 }
@@ -258,19 +270,30 @@ swiglu_ckpt_grad_any_kernel(const T* __restrict__ dh, const uint8_t* __restrict_
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w(nb); w.row < R; w.next()) {
-    const int c = w.seg * kCkptBlock + lane;
-    if (c >= I) continue;
-    const uint8_t* src = q + w.row * 2 * I + c;
-    const uint8_t* ss = qs + w.row * 2 * nb + w.seg;
-    const float g = dequant2(src[0]).x * scale_of(ss[0]);
-    const float u = dequant2(src[I]).x * scale_of(ss[nb]);
-    float dg, du, y;
-    grad_of(to_f32<T>(dh[w.row * I + c]), g, u, &dg, &du, &y);
-    T* dst = dgu + w.row * 2 * I + c;
-    dst[0] = from_f32<T>(dg);
-    dst[I] = from_f32<T>(du);
-    if (kWantH) h[w.row * I + c] = from_f32<T>(y);
+  for (Walk w((nb + kAnyBlocks - 1) / kAnyBlocks); w.row < R; w.next()) {
+    const int b0 = w.seg * kAnyBlocks;
+    float d[kAnyBlocks], g[kAnyBlocks], u[kAnyBlocks];
+#pragma unroll
+    for (int i = 0; i < kAnyBlocks; ++i) {
+      // Lanes past the row's end read its last channel, and write nothing.
+      const int c = min((b0 + i) * kCkptBlock + lane, I - 1);
+      const uint8_t* src = q + w.row * 2 * I + c;
+      const uint8_t* ss = qs + w.row * 2 * nb + c / kCkptBlock;
+      d[i] = to_f32<T>(__ldg(dh + w.row * I + c));
+      g[i] = dequant2(__ldg(src)).x * scale_of(__ldg(ss));
+      u[i] = dequant2(__ldg(src + I)).x * scale_of(__ldg(ss + nb));
+    }
+#pragma unroll
+    for (int i = 0; i < kAnyBlocks; ++i) {
+      const int c = (b0 + i) * kCkptBlock + lane;
+      if (c >= I) continue;
+      float dg, du, y;
+      grad_of(d[i], g[i], u[i], &dg, &du, &y);
+      T* dst = dgu + w.row * 2 * I + c;
+      dst[0] = from_f32<T>(dg);
+      dst[I] = from_f32<T>(du);
+      if (kWantH) h[w.row * I + c] = from_f32<T>(y);
+    }
   }
 }
 
@@ -291,7 +314,7 @@ cudaError_t forward_t(const void* gu, int64_t R, int I, void* h, uint8_t* q, uin
     return launch_pdl(swiglu_ckpt_kernel<T>, dim3(ckpt_grid(R, (I + 255) / 256)),
                       dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I,
                       static_cast<T*>(h), q, qs);
-  return launch_pdl(swiglu_ckpt_any_kernel<T>, dim3(ckpt_grid(R, (I + 31) / 32)),
+  return launch_pdl(swiglu_ckpt_any_kernel<T>, dim3(ckpt_grid(R, (I + 127) / 128)),
                     dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I,
                     static_cast<T*>(h), q, qs);
 }
@@ -303,7 +326,7 @@ cudaError_t backward_t(const void* dh, const uint8_t* q, const uint8_t* qs, int6
     return launch_pdl(swiglu_ckpt_grad_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 255) / 256)),
                       dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                       static_cast<T*>(dgu), static_cast<T*>(h));
-  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 31) / 32)),
+  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 127) / 128)),
                     dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                     static_cast<T*>(dgu), static_cast<T*>(h));
 }

@@ -417,6 +417,21 @@ def test_route_backward(moe, T, E, k, method):
 
 
 @pytest.mark.parametrize("method", [0, 1, 2, 3, 4, 5, 6, 16])
+def test_route_backward_of_slots_that_take_no_part(moe, method):
+    """What comes in for a dropped slot, or one whose logit is not finite, reaches nothing."""
+    rng = np.random.default_rng(method)
+    logits = torch.from_numpy(rng.standard_normal((3, 16)).astype(np.float32)).cuda()
+    ids = torch.tensor([[1, 5, 9], [2, -1, 4], [0, 16, 3]], dtype=torch.int32).cuda()
+    logits[0, 5] = float("nan")
+    ds = torch.from_numpy(rng.standard_normal((3, 3)).astype(np.float32)).cuda()
+    ds[:, 1] = 0
+    want = moe.moe_route_backward(logits, ids, ds, method, 2.5)
+    ds[:, 1] = float("nan")
+    assert torch.equal(moe.moe_route_backward(logits, ids, ds, method, 2.5), want)
+    assert torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("method", [0, 1, 2, 3, 4, 5, 6, 16])
 def test_route_gradient_against_differences(moe, method):
     rng = np.random.default_rng(method)
     T, E, k, rsf, step = 4, 12, 3, 2.5, 1e-5
