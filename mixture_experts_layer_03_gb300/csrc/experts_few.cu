@@ -6,8 +6,8 @@
 // experts that is a few tiles, each streamed by one pair at what its stages keep in flight. Here
 // the plain FMA units, which a weight's use by at most four rows keeps well inside their rate, let
 // the work be cut as finely as is wanted:
-//   forward  a block of eight warps has 8 channels; the warps share K, 8 elements a lane and 8 loads
-//            of 16 bytes in flight; the sums meet in shuffles and shared memory
+//   forward  up to eight warps share 8 channels, each an interleaved part of K, 8 elements a lane and 8
+//            loads of 16 bytes in flight
 //   dx       a block has 64 channels (a 128-byte line of every row of w[e]); its warps and the eight
 //            blocks of its cluster share N; the blocks' sums meet through the cluster's shared memory
 // Sums are in fp32, in a fixed order: the same result on every run. An expert with more than four
@@ -90,16 +90,16 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
   return v;
 }
 
+// The sums of 8 channels over this warp's part of K: every `share`-th 256 elements from the sub-th on.
+// Lane l < 8 gets channel l's.
 template <typename T, int kRows>
-__device__ __forceinline__ void forward_unit(const T* __restrict__ x, const T* __restrict__ w,
-                                             const Item& it, int c0, int N, int K, float* s_sum,
-                                             T* __restrict__ y) {
+__device__ __forceinline__ void forward_partial(const T* __restrict__ x, const T* __restrict__ wp,
+                                                const Item& it, int K, int sub, int share,
+                                                float (&sum)[kFewRows]) {
   using V = Vec<T, 16>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   float acc[kRows][kFwdChannels] = {};
-  const T* wp = w + (static_cast<int64_t>(it.e) * N + c0) * K;
-  const int chans = min(kFwdChannels, N - c0);   // 8: N is a multiple of 8
-  for (int k = (warp * 32 + lane) * 8; k < K; k += kFewThreads * 8) {
+  for (int k = (sub * 32 + lane) * 8; k < K; k += share * 256) {
     uint4 raw[kFwdChannels];
 #pragma unroll
     for (int c = 0; c < kFwdChannels; ++c) raw[c] = load_weights(wp + static_cast<int64_t>(c) * K + k);
@@ -118,64 +118,74 @@ __device__ __forceinline__ void forward_unit(const T* __restrict__ x, const T* _
         for (int i = 0; i < 8; ++i) acc[r][c] = fmaf(xf[r][i], wf[i], acc[r][c]);
     }
   }
-  // Over the lanes: at each step a lane keeps half of the channels, and in the last two steps all lanes
-  // that hold the same channel add up; lane l then has channel l % 8.
+  // Over the lanes: at each of three steps a lane keeps half of the channels, and in the last two
+  // all lanes that hold the same channel add up.
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     float v[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = acc[r][c];
 #pragma unroll
-    for (int n = 4, bit = 4; n >= 1; n >>= 1, bit >>= 1) {
-      const bool up = lane & bit;
+    for (int n = 4; n >= 1; n >>= 1) {
+      const bool up = lane & n;
 #pragma unroll
       for (int c = 0; c < n; ++c) {
         const float give = up ? v[c] : v[c + n];
         const float keep = up ? v[c + n] : v[c];
-        v[c] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        v[c] = keep + __shfl_xor_sync(0xffffffffu, give, n);
       }
     }
     v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
-    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-    if (lane < 8) s_sum[(warp * kRows + r) * 8 + lane] = v[0];
+    sum[r] = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
   }
-  __syncthreads();
-  const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
-  if (r < it.rows && c < chans) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kFewWarps; ++i) sum += s_sum[(i * kRows + r) * 8 + c];
-    y[static_cast<int64_t>(it.r0 + r) * N + c0 + c] = from_f32<T>(sum);
-  }
-  __syncthreads();   // s_sum is read
 }
 
+// `share` warps (1, 2, 4 or 8) to a unit of 8 channels of an item, 8 / share units to a block.
 template <typename T>
 __global__ void __launch_bounds__(kFewThreads, 2)
 experts_few_forward_kernel(const T* __restrict__ x, const T* __restrict__ w,
                            const int32_t* __restrict__ offsets, int R, int E, int N, int K,
-                           T* __restrict__ y) {
+                           int share, T* __restrict__ y) {
   __shared__ int32_t s_start[257];
   __shared__ Item s_item[kMaxFew];
   __shared__ int s_count;
-  __shared__ float s_sum[kFewWarps * kFewRows * kFwdChannels];
+  __shared__ float s_sum[2][kFewWarps][kFewRows][kFwdChannels];
   pdl_trigger();
   pdl_wait();
   if (threadIdx.x < 32) find_items(offsets, E, R, s_start, s_item, &s_count);
   __syncthreads();
-  const int blocks = N / kFwdChannels;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at_once = kFewWarps / share, mine = warp / share, sub = warp - mine * share;
+  const int blocks = N / kFwdChannels;   // N is a multiple of 8
   const int units = s_count * blocks;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int i = u / blocks, c0 = (u - i * blocks) * kFwdChannels;
+  int turn = 0;
+  for (int u0 = blockIdx.x * at_once; u0 < units; u0 += gridDim.x * at_once) {
+    const int u = u0 + mine;
+    const bool live = u < units;
+    const int i = live ? u / blocks : 0, c0 = live ? (u - i * blocks) * kFwdChannels : 0;
     const Item it = s_item[i];
-    if (it.e < 0) {
-      if (threadIdx.x < kFwdChannels)
-        y[static_cast<int64_t>(it.r0) * N + c0 + threadIdx.x] = from_f32<T>(0.0f);
-      continue;
+    float sum[kFewRows] = {};
+    if (live && it.e >= 0) {
+      const T* wp = w + (static_cast<int64_t>(it.e) * N + c0) * K;
+      if (it.rows == 1) forward_partial<T, 1>(x, wp, it, K, sub, share, sum);
+      else if (it.rows == 2) forward_partial<T, 2>(x, wp, it, K, sub, share, sum);
+      else forward_partial<T, 4>(x, wp, it, K, sub, share, sum);
     }
-    if (it.rows == 1) forward_unit<T, 1>(x, w, it, c0, N, K, s_sum, y);
-    else if (it.rows == 2) forward_unit<T, 2>(x, w, it, c0, N, K, s_sum, y);
-    else forward_unit<T, 4>(x, w, it, c0, N, K, s_sum, y);
+    // Lane l of a unit's first warp then has row l / 8, channel l % 8. Two sets of sums in turn: who
+    // writes one has passed the barrier that its readers reach after reading.
+    if (lane < 8)
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r)
+        if (r < it.rows) s_sum[turn][warp][r][lane] = sum[r];
+    if (share > 1) __syncthreads();
+    else __syncwarp();
+    const int r = lane >> 3, c = lane & 7;
+    if (live && sub == 0 && r < it.rows) {
+      float total = 0.0f;
+      for (int q = 0; q < share; ++q) total += s_sum[turn][warp + q][r][c];
+      y[static_cast<int64_t>(it.r0 + r) * N + c0 + c] = from_f32<T>(total);
+    }
+    turn ^= 1;
   }
 }
 
@@ -325,11 +335,18 @@ cudaError_t launch_few(bool dx, const void* in, const void* w, const int32_t* of
                               static_cast<const T*>(w), offsets, R, E, N, K, split,
                               static_cast<T*>(out));
   }
+  // The most warps to a unit whose shares of K, in steps of 256, leave few lanes without work: K = 2280
+  // over eight warps would take two steps for 1.1 (R = 2, N = 8792: 22.6 us, over two warps 16.5).
   const int64_t units = static_cast<int64_t>(R) * (N / kFwdChannels);
+  auto steps = [&](int share) { return (K + 256 * share - 1) / (256 * share) * share; };
+  int share = kFewWarps;
+  while (share > 1 && 17 * steps(share) > 20 * steps(1)) share /= 2;
+  const int64_t blocks = (units * share + kFewWarps - 1) / kFewWarps;
   const int64_t cap = 2 * sms;
-  return launch_pdl(experts_few_forward_kernel<T>, dim3(static_cast<unsigned>(units < cap ? units : cap)),
-                    dim3(kFewThreads), 0, s, static_cast<const T*>(in), static_cast<const T*>(w),
-                    offsets, R, E, N, K, static_cast<T*>(out));
+  return launch_pdl(experts_few_forward_kernel<T>,
+                    dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kFewThreads), 0, s,
+                    static_cast<const T*>(in), static_cast<const T*>(w), offsets, R, E, N, K, share,
+                    static_cast<T*>(out));
 }
 
 }  // namespace
