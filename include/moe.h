@@ -405,11 +405,15 @@ moe_status moe_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const uint
  * without rows has dw = 0. fp32
  * accumulation, one rounding. dtype BF16 or F16; dw_dtype the same or F32, and with F32
  * `accumulate` adds to what dw holds. N and K: multiples of 8 up to 65536; R <= 2^23.
- * Workspace: for dw moe_experts_workspace_bytes(E) bytes (0 outside 1..256), 128-byte aligned,
- * not cleared by the caller, its status word cleared by the call. The other two take NULL, or at
- * least 16 bytes whose status word (cleared by the caller once) receives
- * MOE_DEVICE_FLAG_TIMEOUT; moe_read_device_status reads it. */
+ * Workspace, 128-byte aligned, not cleared by the caller but for its status word (first 16 bytes):
+ * for dw at least moe_experts_workspace_bytes(E) bytes (0 outside 1..256), status word cleared by
+ * the call. The other two take NULL, or at least 16 bytes whose status word, cleared by the
+ * caller once, receives MOE_DEVICE_FLAG_TIMEOUT (moe_read_device_status reads it). Given
+ * moe_experts_split_bytes(product, ...) bytes, a product (0 forward, 1 dx, 2 dw) with few tiles
+ * and a long contraction works on parts of it side by side; 0: this one does not. That changes
+ * the order of the sums, not from run to run. */
 size_t moe_experts_workspace_bytes(int32_t E);
+size_t moe_experts_split_bytes(int32_t product, int64_t R, int32_t E, int32_t N, int32_t K);
 moe_status moe_experts_matmul(const void* x, const void* w, const int32_t* offsets, int64_t R,
                               int32_t E, int32_t N, int32_t K, moe_dtype dtype, void* y,
                               void* workspace, size_t ws_bytes, void* stream);

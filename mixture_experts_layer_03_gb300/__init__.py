@@ -114,6 +114,8 @@ _SIGS = {
     "moe_swiglu_ckpt_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
                                                 ctypes.c_int, _P, _P, _P]),
     "moe_experts_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "moe_experts_split_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                                  ctypes.c_int32, ctypes.c_int32]),
     "moe_experts_matmul": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int32,
                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int, _P, _P,
                                           ctypes.c_size_t, _P]),
@@ -474,12 +476,24 @@ def alloc_dispatch_scratch(T: int, num_experts: int, top_k: int, device="cuda") 
     return Scratch(torch.empty(n, dtype=torch.uint8, device=device))
 
 
-def alloc_experts_scratch(num_experts: int, device="cuda") -> Scratch:
-    """Workspace of the experts' products (all three), its status word cleared."""
+def alloc_experts_scratch(num_experts: int, rows: int = 0, N: int = 8, K: int = 8,
+                          device="cuda") -> Scratch:
+    """Workspace of the experts' products (all three), its status word cleared. With the sizes
+    given, large enough for each of them to split its contraction."""
     n = _lib.moe_experts_workspace_bytes(num_experts)
     if n == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_experts_workspace_bytes")
-    return Scratch(torch.zeros(n, dtype=torch.uint8, device=device))
+    n = max(n, *(_lib.moe_experts_split_bytes(p, rows, num_experts, N, K) for p in range(3)))
+    scratch = Scratch(torch.empty(n, dtype=torch.uint8, device=device))
+    scratch.buf[:16].zero_()
+    return scratch
+
+
+def _split_scratch(product: int, R: int, E: int, N: int, K: int, device) -> Optional[Scratch]:
+    """A workspace for one call whose contraction is split, else None. (Its status word is not
+    read by anyone.)"""
+    n = _lib.moe_experts_split_bytes(product, R, E, N, K)
+    return Scratch(torch.empty(n, dtype=torch.uint8, device=device)) if n else None
 
 
 # The checks below are on the path of calls that take a few microseconds on the device: one
@@ -649,6 +663,8 @@ def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None,
     E, N, K = w.shape
     R = x.shape[0]
     y = _out(y, "y", (R, N), x.dtype, x.device)
+    if scratch is None:
+        scratch = _split_scratch(0, R, E, N, K, x.device)
     _check(_lib.moe_experts_matmul(x.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(), R,
                                    E, N, K, dt, y.data_ptr(), scratch.ptr if scratch else None,
                                    scratch.nbytes if scratch else 0, _stream(stream)),
@@ -664,6 +680,8 @@ def moe_experts_matmul_dx(dy, w, offsets, dx=None, scratch: Optional[Scratch] = 
     E, N, K = w.shape
     R = dy.shape[0]
     dx = _out(dx, "dx", (R, K), dy.dtype, dy.device)
+    if scratch is None:
+        scratch = _split_scratch(1, R, E, N, K, dy.device)
     _check(_lib.moe_experts_matmul_dx(dy.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(),
                                       R, E, N, K, dt, dx.data_ptr(),
                                       scratch.ptr if scratch else None,
@@ -691,7 +709,7 @@ def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bo
     out = _typed(dw, "dw", 3)
     _shaped(dw, "dw", (E, N, K), dw_dtype or dw.dtype)
     if scratch is None:
-        n = _lib.moe_experts_workspace_bytes(E)
+        n = _lib.moe_experts_split_bytes(2, R, E, N, K) or _lib.moe_experts_workspace_bytes(E)
         scratch = Scratch(torch.empty(max(n, 1), dtype=torch.uint8, device=dy.device))
     _check(_lib.moe_experts_matmul_dw(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), R, E, N, K,
                                       dt, out, int(accumulate), dw.data_ptr(), scratch.ptr, scratch.nbytes,

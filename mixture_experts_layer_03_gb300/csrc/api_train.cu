@@ -37,29 +37,21 @@ moe_status check_experts(int64_t R, int32_t E, int32_t N, int32_t K, int dtype) 
   return check_dtype(dtype, false);
 }
 
-// The status word of a product's workspace (optional there), or an error.
-moe_status experts_status(void* workspace, size_t ws_bytes, int32_t** status) {
-  *status = nullptr;
-  if (!workspace) return MOE_OK;
-  if (!aligned(workspace, 16) || ws_bytes < 16)
-    return set_error(MOE_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold 16 bytes");
-  *status = static_cast<int32_t*>(workspace);
-  return MOE_OK;
-}
-
 moe_status experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets, int64_t R,
                         int32_t E, int32_t N, int32_t K, int dtype, void* out, void* workspace,
                         size_t ws_bytes, void* stream) {
-  moe_status st = check_experts(R, E, N, K, dtype);
-  int32_t* status = nullptr;
-  if (st == MOE_OK) st = experts_status(workspace, ws_bytes, &status);
-  if (st != MOE_OK || R == 0) return st;
+  const moe_status st = check_experts(R, E, N, K, dtype);
+  if (st != MOE_OK) return st;
+  if (workspace && (!aligned(workspace, 128) || ws_bytes < 16))
+    return set_error(MOE_ERR_INVALID_ARG, "workspace must be 128-byte aligned and hold 16 bytes");
+  if (R == 0) return MOE_OK;
   if (bad(in) || bad(w) || bad(out) || !offsets || !aligned(offsets, 4))
     return set_error(MOE_ERR_INVALID_ARG, "rows, weights or offsets NULL or misaligned");
   if (experts_few(dx, R, E, K))
     return launch_experts_few(dx, in, w, offsets, R, E, N, K, dtype, out,
                               static_cast<cudaStream_t>(stream));
-  return launch_experts_rows(dx, in, w, offsets, R, E, N, K, dtype, out, status,
+  return launch_experts_rows(dx, in, w, offsets, R, E, N, K, dtype, out,
+                             static_cast<char*>(workspace), ws_bytes,
                              static_cast<cudaStream_t>(stream));
 }
 
@@ -161,6 +153,13 @@ size_t moe_experts_workspace_bytes(int32_t E) {
   return E < 1 || E > 256 ? 0 : experts_workspace_bytes(E);
 }
 
+size_t moe_experts_split_bytes(int32_t product, int64_t R, int32_t E, int32_t N, int32_t K) {
+  if (product < 0 || product > 2 || check_experts(R, E, N, K, MOE_DTYPE_BF16) != MOE_OK || R == 0)
+    return 0;
+  if (product < 2 && experts_few(product == 1, R, E, K)) return 0;
+  return experts_split_bytes(product, R, E, N, K);
+}
+
 moe_status moe_experts_matmul(const void* x, const void* w, const int32_t* offsets, int64_t R,
                               int32_t E, int32_t N, int32_t K, moe_dtype dtype, void* y,
                               void* workspace, size_t ws_bytes, void* stream) {
@@ -198,7 +197,8 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
     return set_error(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes,
                      experts_workspace_bytes(E));
   return launch_experts_dw(dy, x, offsets, R, E, N, K, dtype, dw_dtype, accumulate != 0, dw,
-                           static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
+                           static_cast<char*>(workspace), ws_bytes,
+                           static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dscales,

@@ -24,6 +24,9 @@
 // beyond with zeros (a small kernel writes the maps; 0 * NaN cannot reach a neighbour's gradient),
 // and steps of 16 rows with nothing in them are not issued.
 //
+// Where the tiles are few and the contraction long (experts_split), it is cut into 2, 4 or 8 parts, tiles
+// of their own whose f32 sums go to the workspace and are added up, in order, by a second kernel.
+//
 // Tiles go to the CTA pairs in order, pair i taking tiles i, i + pairs, ...: neighbouring tiles
 // (eight row tiles by the channels) share operands in L2, and tiles of one expert cost the same,
 // so the pairs stay level without a counter. Every result element is written by one CTA from one
@@ -71,7 +74,9 @@ struct ExpertsArgs {
   int32_t k_ext;            // forward, dx: the contraction
   int32_t f16;              // 16-bit type: 0 bf16, 1 f16
   int32_t add;              // dw, f32: add to what is there
+  int32_t split;            // log2 of the parts that the contraction is cut into
   void* out;                // forward, dx: the result rows (masked stores)
+  float* part;              // forward, dx with f32 results: [parts][R][m_ext] sums of the parts
   const CUtensorMap* maps;  // dw: [2][E] maps of dy and of x, cut off at each expert's end
   int32_t* status;          // or NULL
 };
@@ -84,7 +89,8 @@ struct Tile {
   int n0;       // the pair's first index along N: a row, or a column of dw[g]
   int n_here;   // how many exist, 1..256
   int n;        // the instruction's N: n_here rounded up to 16
-  int k0;       // dw: first row of the contraction
+  int k0;       // first element of the contraction (dw: a row)
+  int part;     // of the contraction's parts
   int nkb;      // contraction blocks; 0: the tile is zeros
   int nks;      // contraction steps of 16 elements, the last one filled up with zeros
 };
@@ -129,10 +135,13 @@ struct Walk {
 // s_start[G] the last one's end. dw's groups are the experts; forward and dx have the rows before
 // the first expert's as group 0, expert e as group e + 1 and the rows past the last one's as
 // group E + 1.
-template <int kMode>
+// f32 results: neighbouring indices are the parts of a tile's contraction, whole blocks each.
+template <int kMode, bool kF32>
 __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, const int32_t* s_start,
                                             int G, const ExpertsArgs& a, const Walk& w,
                                             int rank, int lane, int& from) {
+  const int part = kF32 ? idx & ((1 << a.split) - 1) : 0;
+  if (kF32) idx >>= a.split;
   const int blk = w.inner(idx);
   int g, outer, before;
   if (kMode == kDw) {
@@ -181,8 +190,15 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
   t.m_here = clamp_int(a.m_ext - t.m0, 0, 128);
   if (kMode != kDw) t.g = g - 1;
   const int len = kMode == kDw ? rows : g > 0 && g <= a.E ? a.k_ext : 0;
+  t.part = part;
   t.nkb = (len + kXBK - 1) / kXBK;
   t.nks = (len + 15) / 16;
+  if (kF32) {
+    const int b0 = t.nkb * part >> a.split, b1 = t.nkb * (part + 1) >> a.split;
+    t.k0 += b0 * kXBK;
+    t.nks = min(t.nks, b1 * (kXBK / 16)) - b0 * (kXBK / 16);
+    t.nkb = b1 - b0;
+  }
   return t;
 }
 
@@ -367,8 +383,10 @@ __device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int 
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        if (kF32 && a.add) tma_add_3d(map, buf, col + c0 + c, row, t.g);
-        else tma_store_3d(map, buf, col + c0 + c, row, t.g);
+        // Parts of a split contraction are planes of their own.
+        const int plane = kF32 ? t.part * a.E + t.g : t.g;
+        if (kF32 && a.add) tma_add_3d(map, buf, col + c0 + c, row, plane);
+        else tma_store_3d(map, buf, col + c0 + c, row, plane);
         bulk_commit_group();
       }
     }
@@ -454,6 +472,35 @@ __device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, in
       }
       sbuf ^= 1;
     }
+  }
+}
+
+// The same for one part of a split contraction: f32 sums, a lane to a channel, row by row.
+template <typename Done>
+__device__ __forceinline__ void store_part(uint32_t tb, const Tile& t, int q, int lane,
+                                           const ExpertsArgs& a, Done&& done) {
+  if (32 * q >= t.m_here) {
+    done();
+    return;
+  }
+  const bool mine = 32 * q + lane < t.m_here;
+  float* dst = a.part + (static_cast<int64_t>(t.part) * a.R + t.n0) * a.m_ext + t.m0 + 32 * q + lane;
+#pragma unroll 1
+  for (int r0 = 0; r0 < t.n_here; r0 += 32) {
+    uint32_t v[32];
+    if (t.nkb > 0) {
+      tmem_issue(tb + r0, v);
+      tmem_wait();
+      tmem_ready(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0;
+    }
+    if (r0 + 32 >= t.n_here) done();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (mine && r0 + i < t.n_here)
+        dst[static_cast<int64_t>(r0 + i) * a.m_ext] = __uint_as_float(v[i]);
   }
 }
 
@@ -555,7 +602,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort = &s_abort;
   const Walk walk = Walk::of<kMode>(a);
-  const int total = walk.inner.d * (kMode == kDw ? a.E * walk.outer.d : s_blk[G]);
+  const int total = walk.inner.d * (kMode == kDw ? a.E * walk.outer.d : s_blk[G])
+                    << (kF32 ? a.split : 0);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
@@ -566,7 +614,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     int stage = 0, last_g = -1;
     uint32_t phase = 0;
     for (int idx = first; idx < total; idx += step) {
-      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
+      const Tile t = decode_tile<kMode, kF32>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
       if (t.nkb == 0) continue;
       const CUtensorMap* map = warp == 0 ? &map_a : &map_b;
       if (kMode == kDw) {
@@ -605,7 +653,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       const uint64_t db0 = kMode == kDw ? sdesc_mn_major(smem_u32(sB), kXSlotBytes / 2)
                                         : sdesc_k_major(smem_u32(sB), 128);
       for (int idx = first; idx < total; idx += step) {
-        const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, 0, lane, group);
+        const Tile t = decode_tile<kMode, kF32>(idx, s_blk, s_start, G, a, walk, 0, lane, group);
         acc ^= 1;
         if (t.nkb == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], ~(acc_phase >> acc) & 1u, abort));
@@ -641,9 +689,9 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     int sbuf = 0;
     uint32_t acc_phase = 0;
     for (int idx = first + acc * step; idx < total; idx += 2 * step) {
-      const Tile t = decode_tile<kMode>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
+      const Tile t = decode_tile<kMode, kF32>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
       const bool zeros = t.nkb == 0;   // nothing was multiplied
-      if (zeros && kF32 && a.add) continue;
+      if (zeros && kMode == kDw && kF32 && a.add) continue;
       if (!zeros) {
         const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
         // Lanes may leave the poll at different times; tcgen05.ld is warp-collective.
@@ -665,6 +713,8 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       };
       if constexpr (kMode == kDw)
         store_dw<kF32>(tb, t, q, lane, my_box, &map_out, a, done);
+      else if constexpr (kF32)
+        store_part(tb, t, q, lane, a, done);
       else
         store_rows(tb, t, q, lane, my_box, sbuf, &map_out, a, done);
     }
@@ -779,13 +829,90 @@ CUtensorMapDataType map_type(int dtype) {
                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
+// out[i] (+)= the sum of the parts' i-th values, in order; 8 values a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+sum_parts_kernel(const float* __restrict__ part, int parts, int64_t n, T* __restrict__ out,
+                 bool add) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256 * 8;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8; i < n; i += stride) {
+    float sum[8] = {};
+    for (int p = 0; p < parts; ++p) {
+      const float4* src = reinterpret_cast<const float4*>(part + p * n + i);
+      const float4 a = __ldg(src), b = __ldg(src + 1);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+    constexpr int kN = 16 / static_cast<int>(sizeof(T));
+    uint4* dst = reinterpret_cast<uint4*>(out + i);
+#pragma unroll
+    for (int h = 0; h < 8 / kN; ++h) {
+      float f[kN], old[kN] = {};
+      if (add) Vec<T, 16>::unpack(dst[h], old);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) f[j] = old[j] + sum[h * kN + j];
+      dst[h] = Vec<T, 16>::pack(f);
+    }
+  }
+}
+
+moe_status launch_sum_parts(const float* part, int parts, int64_t n, int dtype, bool add, void* out,
+                            cudaStream_t s) {
+  const int64_t blocks = (n / 8 + 255) / 256, cap = static_cast<int64_t>(device_sm_count()) * 8;
+  const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap)), block(256);
+  const cudaError_t err =
+      dtype == MOE_DTYPE_F32 ? launch_pdl(sum_parts_kernel<float>, grid, block, 0, s, part, parts, n,
+                                          static_cast<float*>(out), add)
+      : dtype == MOE_DTYPE_F16 ? launch_pdl(sum_parts_kernel<__half>, grid, block, 0, s, part, parts,
+                                            n, static_cast<__half*>(out), add)
+                               : launch_pdl(sum_parts_kernel<__nv_bfloat16>, grid, block, 0, s, part,
+                                            parts, n, static_cast<__nv_bfloat16*>(out), add);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "sum_parts launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+size_t to_128(size_t n) { return (n + 127) / 128 * 128; }
+
 }  // namespace
+
+int experts_split(int product, int64_t R, int E, int N, int K) {
+  const int64_t pairs = device_sm_count() / 2;
+  int64_t tiles, blocks;
+  if (product == kDw) {
+    tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
+    blocks = R / E / kXBK;
+  } else {
+    const int cols = product == kDx ? K : N;
+    tiles = (R / 256 + (R < E ? R : E)) * ((cols + 255) / 256);
+    blocks = (product == kDx ? N : K) / kXBK;
+  }
+  // Cut only where that takes more off the blocks' 0.28 us each than the 5 us of adding up: 100 rows of
+  // one expert (N = 136, K = 14336) 58 us, in eight parts 17; dw of 8192 rows (256 x 4096) 42 us, in
+  // four 26; but 2000 rows (256 x 1024, 16 blocks) 11 us, in four 18.
+  int split = 0;
+  while (split < 3 && (tiles << (split + 1)) <= pairs &&
+         blocks >> (split + 1) >= (split == 0 ? 24 : 12))
+    ++split;
+  return split;
+}
 
 size_t experts_workspace_bytes(int E) { return 128 + 2 * static_cast<size_t>(E) * sizeof(CUtensorMap); }
 
+size_t experts_split_bytes(int product, int64_t R, int E, int N, int K) {
+  const int split = experts_split(product, R, E, N, K);
+  if (split == 0) return 0;
+  const int64_t n = product == kDw ? static_cast<int64_t>(E) * N * K
+                                   : R * static_cast<int64_t>(product == kDx ? K : N);
+  return to_128(experts_workspace_bytes(E)) + (sizeof(float) * n << split);
+}
+
 moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
                                int64_t R, int E, int N, int K, int dtype, void* out,
-                               int32_t* status, cudaStream_t s) {
+                               char* ws, size_t ws_bytes, cudaStream_t s) {
   const CUtensorMapDataType t = map_type(dtype);
   const int kc = dx ? N : K, nc = dx ? K : N;   // contraction, columns of the result
   CUtensorMap ma, mb, mb32, mo;
@@ -805,22 +932,37 @@ moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int
   a.k_ext = kc;
   a.f16 = dtype == MOE_DTYPE_F16;
   a.out = out;
-  a.status = status;
+  a.status = reinterpret_cast<int32_t*>(ws);
   const int64_t tiles = (R / 256 + E + 2) * ((nc + 255) / 256);
+  const size_t need = ws ? experts_split_bytes(dx ? kDx : kFwd, R, E, N, K) : 0;
+  if (need > 0 && ws_bytes >= need) {
+    a.split = experts_split(dx ? kDx : kFwd, R, E, N, K);
+    a.part = reinterpret_cast<float*>(ws + to_128(experts_workspace_bytes(E)));
+    const moe_status st = dx ? launch_form<kDx, true>(ma, mb, mb32, mo, a, tiles << a.split, s)
+                             : launch_form<kFwd, true>(ma, mb, mb32, mo, a, tiles << a.split, s);
+    if (st != MOE_OK) return st;
+    return launch_sum_parts(a.part, 1 << a.split, R * nc, dtype, false, out, s);
+  }
   return dx ? launch_form<kDx, false>(ma, mb, mb32, mo, a, tiles, s)
             : launch_form<kFwd, false>(ma, mb, mb32, mo, a, tiles, s);
 }
 
 moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
-                             char* ws, cudaStream_t s) {
+                             char* ws, size_t ws_bytes, cudaStream_t s) {
   const CUtensorMapDataType t = map_type(dtype);
-  const bool f32 = out_dtype == MOE_DTYPE_F32;
+  const size_t need = experts_split_bytes(kDw, R, E, N, K);
+  const int split = need > 0 && ws_bytes >= need ? experts_split(kDw, R, E, N, K) : 0;
+  float* part = reinterpret_cast<float*>(ws + to_128(experts_workspace_bytes(E)));
+  const bool f32 = split > 0 || out_dtype == MOE_DTYPE_F32;   // what the product's kernel writes
   CUtensorMap ma, mb, mo;
   const bool ok =
       encode_any(&ma, dy, 0, R, N, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
       encode_any(&mb, x, 0, R, K, t, 64, kXBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
-      encode_any(&mo, dw, E, N, K, map_type(out_dtype), f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+      (split > 0 ? encode_any(&mo, part, static_cast<uint64_t>(E) << split, N, K,
+                              CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B)
+                 : encode_any(&mo, dw, E, N, K, map_type(out_dtype), f32 ? 32 : 64, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B));
   if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   ExpertsArgs a = {};
   a.offsets = offsets;
@@ -829,7 +971,8 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
   a.m_ext = N;
   a.n_ext = K;
   a.f16 = dtype == MOE_DTYPE_F16;
-  a.add = add;
+  a.add = add && split == 0;
+  a.split = split;
   a.status = reinterpret_cast<int32_t*>(ws);
   CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(ws + 128);
   a.maps = maps;
@@ -839,8 +982,10 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_maps launch: %s", cudaGetErrorString(err));
   const int64_t tiles = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);
-  return f32 ? launch_form<kDw, true>(ma, mb, mb, mo, a, tiles, s)
-             : launch_form<kDw, false>(ma, mb, mb, mo, a, tiles, s);
+  const moe_status st = f32 ? launch_form<kDw, true>(ma, mb, mb, mo, a, tiles << split, s)
+                            : launch_form<kDw, false>(ma, mb, mb, mo, a, tiles, s);
+  if (st != MOE_OK || split == 0) return st;
+  return launch_sum_parts(part, 1 << split, static_cast<int64_t>(E) * N * K, out_dtype, add, dw, s);
 }
 
 }  // namespace moe

@@ -131,18 +131,22 @@ moe_status launch_swiglu_ckpt_backward(const void* dh, const uint8_t* q, const u
                                        cudaStream_t s);
 
 size_t experts_workspace_bytes(int E);
+// log2 of the parts that a product (0 forward, 1 dx, 2 dw) cuts its contraction into, where its
+// workspace holds their sums, and the workspace for that (0: it is not cut).
+int experts_split(int product, int64_t R, int E, int N, int K);
+size_t experts_split_bytes(int product, int64_t R, int E, int N, int K);
 // dx false: out[r] = in[r] . w[e]^T ([R, K] -> [R, N]); true: out[r] = in[r] . w[e] ([R, N] ->
-// [R, K]). status (or NULL) receives device flags.
+// [R, K]). ws (or NULL): its status word receives device flags.
 moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
-                               int64_t R, int E, int N, int K, int dtype, void* out,
-                               int32_t* status, cudaStream_t s);
+                               int64_t R, int E, int N, int K, int dtype, void* out, char* ws,
+                               size_t ws_bytes, cudaStream_t s);
 // The same for few rows, where experts_few says so (R <= 16).
 bool experts_few(bool dx, int64_t R, int E, int K);
 moe_status launch_experts_few(bool dx, const void* in, const void* w, const int32_t* offsets,
                               int64_t R, int E, int N, int K, int dtype, void* out, cudaStream_t s);
 moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
-                             char* ws, cudaStream_t s);
+                             char* ws, size_t ws_bytes, cudaStream_t s);
 
 moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* ds,
                                  int64_t T, const moe_route_params& p, float* dl, cudaStream_t s);

@@ -322,6 +322,55 @@ def test_experts_products(moe, R, E, K, N, kind, dtype):
     assert torch.equal(sum_, start + dw)     # one fp32 addition an element
 
 
+SPLITS = [(100, 1, 6200, 136, "even"), (40, 2, 4104, 264, "cut"), (300, 1, 136, 6504, "part"),
+          (9000, 1, 72, 264, "even"), (6500, 2, 136, 264, "cut"), (1500, 3, 256, 256, "part"),
+          (513, 2, 520, 8200, "last"), (700, 2, 3080, 40, "empty"), (200, 3, 14344, 72, "cut")]
+
+
+def test_which_contractions_are_split(moe):
+    """Each product is in some of the cases of the next test (the sixth: in none, a short one)."""
+    for p in range(3):
+        assert sum(moe._lib.moe_experts_split_bytes(p, R, E, N, K) > 0 for R, E, K, N, _ in SPLITS) >= 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("R,E,K,N,kind", SPLITS)
+def test_split_contractions(moe, R, E, K, N, kind, dtype):
+    """Few tiles and a long contraction: parts of it side by side, where the workspace holds their
+    sums. As close, and the same on every run."""
+    off = ragged(R, E, kind, R + E)
+    offsets = torch.from_numpy(off).cuda()
+    x, dy, w = randn((R, K), dtype, 1), randn((R, N), dtype, 2), randn((E, N, K), dtype, 3, K ** -0.5)
+    for t in (x, dy):
+        t[off[E]:] = float("nan")
+        t[:off[0]] = float("nan")
+    X, Y, W = n64(x), n64(dy), n64(w)
+    scratch = moe.alloc_experts_scratch(E, R, N, K)
+    runs = []
+    for sc in (scratch, None, scratch):
+        if sc is not None:
+            sc.buf[16:].fill_(0xFF)          # NaNs: nothing of it is read before it is written
+        runs.append((moe.moe_experts_matmul(x, w, offsets, scratch=sc),
+                     moe.moe_experts_matmul_dx(dy, w, offsets, scratch=sc),
+                     moe.moe_experts_matmul_dw(dy, x, offsets, scratch=sc)))
+    assert moe.moe_read_device_status(scratch) == (moe.MOE_OK, 0)
+    for again in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], again))
+    rows = max(np.diff(off).max(), 1)
+    for name, got, f, a, b, n in (("y", runs[0][0], ref.experts_matmul, X, W, K),
+                                  ("dx", runs[0][1], ref.experts_matmul_dx, Y, W, N),
+                                  ("dw", runs[0][2], ref.experts_matmul_dw, Y, X, rows)):
+        want, mag = f(a, b, off), f(np.abs(a), np.abs(b), off)
+        close(got, want, U[dtype] * np.abs(want) + (n + 8) * 2.0 ** -23 * mag * (1 + U[dtype]) + TINY[dtype], name)
+    dw = moe.moe_experts_matmul_dw(dy, x, offsets, dw_dtype=torch.float32)
+    want, mag = ref.experts_matmul_dw(Y, X, off), ref.experts_matmul_dw(np.abs(Y), np.abs(X), off)
+    close(dw, want, (rows + 8) * 2.0 ** -23 * mag + 1e-40, "dw f32")
+    start = randn((E, N, K), "f32", 4)
+    sum_ = start.clone()
+    moe.moe_experts_matmul_dw(dy, x, offsets, dw=sum_, accumulate=True)
+    assert torch.equal(sum_, start + dw)
+
+
 def test_a_neighbours_rows_do_not_reach_dw(moe):
     """Infinities and NaNs in the rows right behind (and before) an expert's leave its dw alone."""
     R, E, K, N = 200, 3, 64, 128
