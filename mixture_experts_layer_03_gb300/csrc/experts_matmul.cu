@@ -552,6 +552,11 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
     tmem_alloc_pair(&s_tmem_base, kXTmemCols);   // collective with the other CTA's warp 1
     tmem_relinquish_pair();
   }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any remote arrival or copy
+  tc_fence_after();
+  // Everything above overlaps the kernel before.
   pdl_wait();
   // The groups: their first rows, kept inside [0, R] and in order here, so that no offset can
   // lead a load or a store out of range, and the scan of their row blocks.
@@ -595,10 +600,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
       at += (start[i + 1] - start[i] + 255) >> 8;
     }
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync();   // both CTAs' barriers exist before any remote arrival or copy
-  tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort = &s_abort;
   const Walk walk = Walk::of<kMode>(a);
