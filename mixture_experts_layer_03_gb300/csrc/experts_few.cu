@@ -351,9 +351,9 @@ cudaError_t launch_few(bool dx, const void* in, const void* w, const int32_t* of
 
 }  // namespace
 
-// Measured against the tensor-core kernel. Forward: 8 rows over 128 experts (N = 1536, K = 2048) 12.7
-// us against 14.3, 5 rows of one (N = 136, K = 14336) 8.4 against 57; 32 rows of 8 (14336 x 4096)
-// 234 against 142. dx is behind as soon as that kernel has a tile for most CTA pairs: 1 row
+// Measured against the tensor-core kernel. Forward: 8 rows over 128 experts (N = 1536, K = 2048, 50 MB
+// of weights) 12.1 us against 14.3, 8 rows over 256 (N = 4096, K = 7168) 75.7 against 78.9, 5 rows of
+// one (N = 136, K = 14336) 8.4 against 17; 32 rows of 8 (14336 x 4096) 234 against 142. dx is behind as soon as that kernel has a tile for most CTA pairs: 1 row
 // (N = 14336, K = 4096, 16 tiles) 27 us against 59, 8 rows of 8 experts (N = 7168, K = 2048, 64
 // tiles) 46 against 39; nor does it take an expert's rows twice (12 rows of one: 37 against 21).
 bool experts_few(bool dx, int64_t R, int E, int K) {

@@ -27,6 +27,13 @@
 // Where the tiles are few and the contraction long (experts_split), it is cut into 2, 4 or 8 parts, tiles
 // of their own whose f32 sums go to the workspace and are added up, in order, by a second kernel.
 //
+// Measured (one GB300, calls of one product back to back): forward of 8192 x 14336 x 4096 over 8 experts
+// 541 us, 0.92 of cuBLAS's burst rate (0.92 of its sustained one too, 625 us, where the power limit
+// holds for a second and more); the tensor pipe is active for 92% of the cycles. dx and dw of 32768 x
+// 1536 x 4096 over 64 experts 265 and 273 us, bound by the L2's way to the SMs (32 KB a block of 512
+// tensor cycles) and, dw, by writing beside it. dx and dw over 256 experts (32768 x 2048 x 7168) 1.16 and
+// 1.27 ms, bound by memory.
+//
 // Tiles go to the CTA pairs in order, pair i taking tiles i, i + pairs, ...: neighbouring tiles
 // (eight row tiles by the channels) share operands in L2, and tiles of one expert cost the same,
 // so the pairs stay level without a counter. Every result element is written by one CTA from one
@@ -211,7 +218,8 @@ __device__ __forceinline__ void x_timeout(int32_t* status, volatile int* abort) 
 // coordinates are then the same in all lanes and stay in uniform registers, where the TMA unit takes
 // them from. Issued from a branch of one lane, their way there cost 100 cycles and more an
 // instruction, and the producer, not the tensor cores, set the pace (dw at 8192 x 14336 x 4096
-// over 8 experts, four boxes a block: 768 us, so 604; dx there, three boxes: 691 us, so 571).
+// over 8 experts, four boxes a block: 768 us, so 604; dx there, three boxes: 691 us, so 571). A and
+// B have a warp each: one warp for both took 5% more for dw.
 //
 // The loads of one tile in this CTA. A: its 128 indices along M (left out where none exists: what
 // the stage holds then only reaches accumulator lanes that are not stored). B: its half of the
@@ -332,10 +340,11 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
 // dw: one warp's part of a tile, 32 rows of dw[g] (TMEM lane quarter q) by its columns, in boxes of
 // 128 bytes of columns (64 16-bit or 32 f32 values) through shared memory and out by TMA, which
 // leaves out what lies beyond dw[g]. `done` runs once the accumulator has been read.
-// Eight warps, two to a lane quarter: a box costs a warp about 700 cycles of latency (TMEM load,
-// fence, the store's read of the box), so that four warps held tiles with short contractions to 3.3
-// us (256 experts of 128 rows, N = 7168, K = 2048: 2.50 ms, with eight 1.9 ms; writing the result
-// alone takes 1.87 at the 4.0 TB/s that a write-only stream reaches).
+// A box costs its warp about 700 cycles of latency (TMEM load, fence, the store's read of the box
+// before), and with a short contraction the epilogue is the longer part of a tile. 256 experts of 128
+// rows, N = 7168, K = 2048 (8.1 GB): 2.50 ms with one set of four warps, 1.87 with eight that each had
+// half of a tile's columns, 1.55 with a set to each accumulator, 1.25 once the accumulators went back
+// without a release of these stores; 6.5 TB/s, bound by memory.
 template <bool kF32, typename Done>
 __device__ __forceinline__ void store_dw(uint32_t tb, const Tile& t, int q, int lane,
                                          uint8_t* buf, const CUtensorMap* map,
@@ -410,7 +419,7 @@ __device__ __forceinline__ void store_rows(uint32_t tb, const Tile& t, int q, in
   const int ch = t.m0 + 32 * q;
 #pragma unroll 1
   for (int r2 = 0; r2 < t.n_here; r2 += 64) {
-    // Two of them at once: a load takes 400 cycles beside the tile's other warps.
+    // Two of them at once: a load takes 400 cycles beside the others.
     uint32_t v[2][2][16];   // [block of 32 rows][lanes 0-15, 16-31]
     const bool both = r2 + 32 < t.n_here;
     if (t.nkb > 0) {

@@ -96,6 +96,8 @@ def test_experts_products_refuse(moe):
     assert L.moe_experts_matmul(None, None, None, 0, 2, 64, 64, 0, None, None, 0, None) == 0
     assert L.moe_experts_workspace_bytes(0) == 0 == L.moe_experts_workspace_bytes(257)
     assert L.moe_experts_workspace_bytes(256) == 128 + 2 * 256 * 128
+    for bad in ((3, 100, 1, 64, 64), (0, -1, 1, 64, 64), (1, 100, 0, 64, 64), (2, 100, 1, 12, 64), (0, 0, 1, 64, 64)):
+        assert L.moe_experts_split_bytes(*bad) == 0
     assert L.moe_dispatch_workspace_bytes(10, 0, 2) == 0 == L.moe_dispatch_workspace_bytes(10, 8, 9)
     assert 0 < L.moe_dispatch_workspace_bytes(1 << 24, 256, 8) < 2 << 20
 
