@@ -47,8 +47,8 @@ moe_status experts_rows(bool dx, const void* in, const void* w, const int32_t* o
   if (R == 0) return MOE_OK;
   if (bad(in) || bad(w) || bad(out) || !offsets || !aligned(offsets, 4))
     return set_error(MOE_ERR_INVALID_ARG, "rows, weights or offsets NULL or misaligned");
-  if (experts_few(dx, R, E, K))
-    return launch_experts_few(dx, in, w, offsets, R, E, N, K, dtype, out,
+  if (!dx && experts_few(R, E))
+    return launch_experts_few(in, w, offsets, R, E, N, K, dtype, out,
                               static_cast<cudaStream_t>(stream));
   return launch_experts_rows(dx, in, w, offsets, R, E, N, K, dtype, out,
                              static_cast<char*>(workspace), ws_bytes,
@@ -156,7 +156,7 @@ size_t moe_experts_workspace_bytes(int32_t E) {
 size_t moe_experts_split_bytes(int32_t product, int64_t R, int32_t E, int32_t N, int32_t K) {
   if (product < 0 || product > 2 || check_experts(R, E, N, K, MOE_DTYPE_BF16) != MOE_OK || R == 0)
     return 0;
-  if (product < 2 && experts_few(product == 1, R, E, K)) return 0;
+  if (product == 0 && experts_few(R, E)) return 0;
   return experts_split_bytes(product, R, E, N, K);
 }
 

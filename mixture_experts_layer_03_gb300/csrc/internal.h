@@ -140,10 +140,10 @@ size_t experts_split_bytes(int product, int64_t R, int E, int N, int K);
 moe_status launch_experts_rows(bool dx, const void* in, const void* w, const int32_t* offsets,
                                int64_t R, int E, int N, int K, int dtype, void* out, char* ws,
                                size_t ws_bytes, cudaStream_t s);
-// The same for few rows, where experts_few says so (R <= 16).
-bool experts_few(bool dx, int64_t R, int E, int K);
-moe_status launch_experts_few(bool dx, const void* in, const void* w, const int32_t* offsets,
-                              int64_t R, int E, int N, int K, int dtype, void* out, cudaStream_t s);
+// The forward product for few rows, where experts_few says so (R <= 16).
+bool experts_few(int64_t R, int E);
+moe_status launch_experts_few(const void* x, const void* w, const int32_t* offsets, int64_t R, int E,
+                              int N, int K, int dtype, void* y, cudaStream_t s);
 moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offsets, int64_t R,
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
                              char* ws, size_t ws_bytes, cudaStream_t s);
