@@ -518,8 +518,9 @@ def _shaped(t: torch.Tensor, name: str, shape: tuple, dtype) -> torch.Tensor:
     raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
 
 
-def _out(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, device) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _shaped(t, name, shape, dtype)
+def _like(t: torch.Tensor, out: Optional[torch.Tensor], name: str, shape: tuple) -> torch.Tensor:
+    """`out`, of just this shape and t's type, or a new tensor."""
+    return t.new_empty(shape) if out is None else _shaped(out, name, shape, t.dtype)
 
 
 def _slots(inv: torch.Tensor, name: str = "inv"):
@@ -545,13 +546,13 @@ def moe_dispatch(x, ids, num_experts: int, x_perm=None, inv=None, offsets=None,
     if _slots(ids, "ids")[0] != T:
         raise ValueError(f"ids must have {T} rows, got {tuple(ids.shape)}")
     k = ids.shape[1]
-    dev = x.device
-    x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, dev)
-    inv = _out(inv, "inv", (T, k), torch.int32, dev)
-    offsets = _out(offsets, "offsets", (num_experts + 1,), torch.int32, dev)
+    x_perm = _like(x, x_perm, "x_perm", (T * k, H))
+    inv = _like(ids, inv, "inv", (T, k))
+    offsets = _like(ids, offsets, "offsets", (num_experts + 1,))
     if scratch is None and T * k > MOE_DISPATCH_SMALL_SLOTS:
-        scratch = alloc_dispatch_scratch(T, num_experts, k, dev)
-    _check(_lib.moe_dispatch(x.data_ptr(), ids.data_ptr(), T, H, num_experts, k, dt, x_perm.data_ptr(), inv.data_ptr(),
+        scratch = alloc_dispatch_scratch(T, num_experts, k, x.device)
+    _check(_lib.moe_dispatch(x.data_ptr(), ids.data_ptr(), T, H, num_experts, k, dt,
+                             x_perm.data_ptr(), inv.data_ptr(),
                              offsets.data_ptr(), scratch.ptr if scratch else None,
                              scratch.nbytes if scratch else 0, _stream(stream)), "moe_dispatch")
     return x_perm, inv, offsets
@@ -564,7 +565,7 @@ def moe_dispatch_rows(x, inv, x_perm=None, stream=None):
     H = x.shape[1]
     if x.shape[0] != T:
         raise ValueError(f"x must have {T} rows, got {tuple(x.shape)}")
-    x_perm = _out(x_perm, "x_perm", (T * k, H), x.dtype, x.device)
+    x_perm = _like(x, x_perm, "x_perm", (T * k, H))
     _check(_lib.moe_dispatch_rows(x.data_ptr(), inv.data_ptr(), T, H, k, dt, x_perm.data_ptr(), _stream(stream)),
            "moe_dispatch_rows")
     return x_perm
@@ -576,7 +577,7 @@ def moe_dispatch_backward(dx_perm, inv, dx=None, stream=None):
     T, k = _slots(inv)
     H = dx_perm.shape[1]
     _shaped(dx_perm, "dx_perm", (T * k, H), dx_perm.dtype)
-    dx = _out(dx, "dx", (T, H), dx_perm.dtype, dx_perm.device)
+    dx = _like(dx_perm, dx, "dx", (T, H))
     _check(_lib.moe_dispatch_backward(dx_perm.data_ptr(), inv.data_ptr(), T, H, k, dt, dx.data_ptr(),
                                       _stream(stream)), "moe_dispatch_backward")
     return dx
@@ -591,7 +592,7 @@ def moe_combine(rows, inv, scales=None, y=None, stream=None):
     _shaped(rows, "rows", (T * k, H), rows.dtype)
     if scales is not None:
         _shaped(scales, "scales", (T, k), torch.float32)
-    y = _out(y, "y", (T, H), rows.dtype, rows.device)
+    y = _like(rows, y, "y", (T, H))
     _check(_lib.moe_combine(rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt, y.data_ptr(),
                             _stream(stream)), "moe_combine")
     return y
@@ -606,8 +607,9 @@ def moe_combine_backward(dy, rows, inv, scales=None, drows=None, dscales=None, s
     _shaped(rows, "rows", (T * k, H), dy.dtype)
     if scales is not None:
         _shaped(scales, "scales", (T, k), torch.float32)
-    drows = _out(drows, "drows", (T * k, H), dy.dtype, dy.device)
-    dscales = _out(dscales, "dscales", (T, k), torch.float32, dy.device)
+    drows = _like(rows, drows, "drows", (T * k, H))
+    dscales = (torch.empty((T, k), dtype=torch.float32, device=dy.device) if dscales is None
+               else _shaped(dscales, "dscales", (T, k), torch.float32))
     _check(_lib.moe_combine_backward(dy.data_ptr(), rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt,
                                      drows.data_ptr(), dscales.data_ptr(), _stream(stream)),
            "moe_combine_backward")
@@ -617,36 +619,82 @@ def moe_combine_backward(dy, rows, inv, scales=None, drows=None, dscales=None, s
 MOE_CKPT_BLOCK = 32
 
 
+class Checkpoint:
+    """What moe_swiglu_ckpt keeps of gu [R, 2I]: the e4m3 codes q [R, 2I] and the exponent bytes
+    q_scales [R, 2 * ceil(I / 32)] (scale 2^(byte - 127)), in one buffer `buf` (uint8; to be saved
+    between the passes). Unpacks and indexes as (q, q_scales)."""
+    __slots__ = ("buf", "R", "I")
+
+    def __init__(self, buf: torch.Tensor, R: int, I: int):
+        if buf.dtype is not torch.uint8 or buf.numel() < self.nbytes(R, I):
+            raise ValueError(f"a checkpoint of [{R}, {2 * I}] takes {self.nbytes(R, I)} bytes (uint8)")
+        self.buf, self.R, self.I = buf, R, I
+
+    @staticmethod
+    def scales_at(R: int, I: int) -> int:
+        return (R * 2 * I + 15) // 16 * 16
+
+    @staticmethod
+    def nbytes(R: int, I: int) -> int:
+        return Checkpoint.scales_at(R, I) + R * 2 * (-(-I // MOE_CKPT_BLOCK))
+
+    @property
+    def q(self) -> torch.Tensor:
+        return self.buf[:self.R * 2 * self.I].view(self.R, 2 * self.I)
+
+    @property
+    def q_scales(self) -> torch.Tensor:
+        return self.buf[self.scales_at(self.R, self.I):self.nbytes(self.R, self.I)].view(
+            self.R, 2 * (-(-self.I // MOE_CKPT_BLOCK)))
+
+    def __len__(self):
+        return 2
+
+    def __getitem__(self, i):
+        return (self.q, self.q_scales)[i]
+
+
+def _ckpt_ptrs(ckpt, R: int, I: int):
+    """Addresses of the codes and the scales of a Checkpoint, or of a pair of tensors."""
+    if type(ckpt) is Checkpoint:
+        if ckpt.R != R or ckpt.I != I or not ckpt.buf.is_cuda or not ckpt.buf.is_contiguous():
+            raise ValueError(f"the checkpoint must be of [{R}, {2 * I}], contiguous, on the GPU")
+        at = ckpt.buf.data_ptr()
+        return at, at + Checkpoint.scales_at(R, I)
+    q, qs = ckpt
+    return (_shaped(q, "q", (R, 2 * I), torch.uint8).data_ptr(),
+            _shaped(qs, "q_scales", (R, 2 * (-(-I // MOE_CKPT_BLOCK))), torch.uint8).data_ptr())
+
+
 def moe_swiglu_ckpt(gu, h=None, ckpt=None, stream=None):
-    """SwiGLU that keeps its input in 8 bits. gu [R, 2I], gate then up. Returns (h [R, I],
-    (q uint8 [R, 2I], q_scales uint8 [R, 2 * ceil(I / 32)])): the e4m3 codes and the exponent
-    bytes (scale 2^(byte - 127)) that moe_swiglu_ckpt_backward reads."""
+    """SwiGLU that keeps its input in 8 bits. gu [R, 2I], gate then up. Returns (h [R, I], a
+    Checkpoint, for moe_swiglu_ckpt_backward). ckpt: a Checkpoint, or the pair (q, q_scales), to
+    write to."""
     dt = _typed(gu, "gu", 2)
     R, I2 = gu.shape
     if I2 % 2:
         raise ValueError(f"gu must have an even number of columns, got {I2}")
     I = I2 // 2
-    nb = 2 * (-(-I // MOE_CKPT_BLOCK))
-    h = _out(h, "h", (R, I), gu.dtype, gu.device)
-    q, qs = ckpt if ckpt is not None else (None, None)
-    q = _out(q, "q", (R, I2), torch.uint8, gu.device)
-    qs = _out(qs, "q_scales", (R, nb), torch.uint8, gu.device)
-    _check(_lib.moe_swiglu_ckpt(gu.data_ptr(), R, I, dt, _ptr(h), q.data_ptr(), qs.data_ptr(), _stream(stream)),
+    h = gu.new_empty((R, I)) if h is None else _shaped(h, "h", (R, I), gu.dtype)
+    if ckpt is None:
+        ckpt = Checkpoint(gu.new_empty(Checkpoint.nbytes(R, I), dtype=torch.uint8), R, I)
+    q, qs = _ckpt_ptrs(ckpt, R, I)
+    _check(_lib.moe_swiglu_ckpt(gu.data_ptr(), R, I, dt, h.data_ptr(), q, qs, _stream(stream)),
            "moe_swiglu_ckpt")
-    return h, (q, qs)
+    return h, ckpt
 
 
 def moe_swiglu_ckpt_backward(dh, ckpt, dgu=None, h=None, want_h: bool = False, stream=None):
     """Gradient of moe_swiglu_ckpt at the kept values: (dgu [R, 2I], h [R, I] again or None)."""
     dt = _typed(dh, "dh", 2)
     R, I = dh.shape
-    q, qs = ckpt
-    _shaped(q, "q", (R, 2 * I), torch.uint8)
-    _shaped(qs, "q_scales", (R, 2 * (-(-I // MOE_CKPT_BLOCK))), torch.uint8)
-    dgu = _out(dgu, "dgu", (R, 2 * I), dh.dtype, dh.device)
-    if want_h or h is not None:
-        h = _out(h, "h", (R, I), dh.dtype, dh.device)
-    _check(_lib.moe_swiglu_ckpt_backward(dh.data_ptr(), q.data_ptr(), qs.data_ptr(), R, I, dt, dgu.data_ptr(), _ptr(h),
+    q, qs = _ckpt_ptrs(ckpt, R, I)
+    dgu = dh.new_empty((R, 2 * I)) if dgu is None else _shaped(dgu, "dgu", (R, 2 * I), dh.dtype)
+    if h is not None:
+        _shaped(h, "h", (R, I), dh.dtype)
+    elif want_h:
+        h = torch.empty_like(dh)
+    _check(_lib.moe_swiglu_ckpt_backward(dh.data_ptr(), q, qs, R, I, dt, dgu.data_ptr(), _ptr(h),
                                          _stream(stream)), "moe_swiglu_ckpt_backward")
     return dgu, h
 
@@ -662,7 +710,7 @@ def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None,
     _shaped(w, "w", (w.shape[0], w.shape[1], x.shape[1]) if w.dim() == 3 else (0, 0, 0), x.dtype)
     E, N, K = w.shape
     R = x.shape[0]
-    y = _out(y, "y", (R, N), x.dtype, x.device)
+    y = _like(x, y, "y", (R, N))
     if scratch is None:
         scratch = _split_scratch(0, R, E, N, K, x.device)
     _check(_lib.moe_experts_matmul(x.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(), R,
@@ -679,7 +727,7 @@ def moe_experts_matmul_dx(dy, w, offsets, dx=None, scratch: Optional[Scratch] = 
     _shaped(w, "w", (w.shape[0], dy.shape[1], w.shape[2]) if w.dim() == 3 else (0, 0, 0), dy.dtype)
     E, N, K = w.shape
     R = dy.shape[0]
-    dx = _out(dx, "dx", (R, K), dy.dtype, dy.device)
+    dx = _like(dy, dx, "dx", (R, K))
     if scratch is None:
         scratch = _split_scratch(1, R, E, N, K, dy.device)
     _check(_lib.moe_experts_matmul_dx(dy.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(),
@@ -726,7 +774,7 @@ def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor:
     E = logits.shape[-1]
     _shaped(logits, "logits", (T, E), torch.float32)
     _shaped(dscales, "dscales", (T, k), torch.float32)
-    dlogits = _out(dlogits, "dlogits", (T, E), torch.float32, logits.device)
+    dlogits = _like(logits, dlogits, "dlogits", (T, E))
     p = MoeRouteParams(E, k, method, 1, 1, routed_scaling_factor)
     _check(_lib.moe_route_backward(logits.data_ptr(), ids.data_ptr(), dscales.data_ptr(), T, ctypes.byref(p),
                                    dlogits.data_ptr(), _stream(stream)), "moe_route_backward")
@@ -735,4 +783,4 @@ def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor:
 
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_", "Moe"))] + [
     "make_problem", "alloc_workspace", "Workspace", "load_library", "EXPORTED", "LIB_PATH",
-    "Scratch", "alloc_dispatch_scratch", "alloc_experts_scratch"]
+    "Checkpoint", "Scratch", "alloc_dispatch_scratch", "alloc_experts_scratch"]

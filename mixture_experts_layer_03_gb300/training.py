@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward,
+from . import (Checkpoint, moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward,
                moe_dispatch_rows, moe_experts_matmul, moe_experts_matmul_dw,
                moe_experts_matmul_dx, moe_gate_route, moe_route_backward, moe_swiglu_ckpt,
                moe_swiglu_ckpt_backward)
@@ -32,20 +32,20 @@ class _MoeLayer(torch.autograd.Function):
                                                 rsf, want_logits=True)
         x_perm, inv, offsets = moe_dispatch(x, ids, E)
         gu = moe_experts_matmul(x_perm, w13, offsets)
-        h, (q, q_scales) = moe_swiglu_ckpt(gu)
+        h, ckpt = moe_swiglu_ckpt(gu)
         rows = moe_experts_matmul(h, w2, offsets)
         y = moe_combine(rows, inv, scales)
-        ctx.save_for_backward(x, wg, w13, w2, ids, scales, logits, inv, offsets, q, q_scales, rows)
+        ctx.save_for_backward(x, wg, w13, w2, ids, scales, logits, inv, offsets, ckpt.buf, rows)
         ctx.method, ctx.rsf = method, rsf
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        x, wg, w13, w2, ids, scales, logits, inv, offsets, q, q_scales, rows = ctx.saved_tensors
+        x, wg, w13, w2, ids, scales, logits, inv, offsets, ckpt, rows = ctx.saved_tensors
         need_x, need_wg, need_w13, need_w2 = ctx.needs_input_grad[:4]
         drows, dscales = moe_combine_backward(dy.contiguous(), rows, inv, scales)
         dh = moe_experts_matmul_dx(drows, w2, offsets)
-        dgu, h = moe_swiglu_ckpt_backward(dh, (q, q_scales), want_h=need_w2)
+        dgu, h = moe_swiglu_ckpt_backward(dh, Checkpoint(ckpt, *dh.shape), want_h=need_w2)
         dw2 = moe_experts_matmul_dw(drows, h, offsets) if need_w2 else None
         dw13 = moe_experts_matmul_dw(dgu, moe_dispatch_rows(x, inv), offsets) if need_w13 else None
         dx = dwg = None

@@ -213,6 +213,28 @@ def test_swiglu_checkpoint(moe, R, I, dtype):
     close(dgu, want, U[dtype] * np.abs(want) + 2 * np.concatenate([e, e], 1) * mag * (1 + U[dtype]) + TINY[dtype] + 1e-37, "dgu")
 
 
+def test_checkpoint_object(moe):
+    """One buffer for codes and scales, or the caller's own two tensors: the same bits; the sizes are
+    checked."""
+    R, I = 7, 33
+    gu, dh = randn((R, 2 * I), "bf16", 1), randn((R, I), "bf16", 2)
+    h, ck = moe.moe_swiglu_ckpt(gu)
+    q = torch.zeros((R, 2 * I), dtype=torch.uint8, device="cuda")
+    qs = torch.zeros((R, 4), dtype=torch.uint8, device="cuda")
+    moe.moe_swiglu_ckpt(gu, ckpt=(q, qs))
+    assert torch.equal(ck.q, q) and torch.equal(ck.q_scales, qs)
+    again = moe.Checkpoint(ck.buf.clone(), R, I)
+    moe.moe_swiglu_ckpt(gu, ckpt=again)
+    for c in (ck, again, (q, qs)):
+        assert torch.equal(moe.moe_swiglu_ckpt_backward(dh, c)[0], moe.moe_swiglu_ckpt_backward(dh, ck)[0])
+    with pytest.raises(ValueError):
+        moe.Checkpoint(ck.buf[:-1], R, I)
+    with pytest.raises(ValueError):
+        moe.moe_swiglu_ckpt_backward(dh[:6].contiguous(), ck)
+    with pytest.raises(ValueError):
+        moe.moe_swiglu_ckpt_backward(dh, (q, qs[:, :3].contiguous()))
+
+
 def test_checkpoint_scale_boundaries(moe):
     """Largest magnitudes at, just under and just over 448 times a power of two, the type's own
     largest, and signs."""
