@@ -531,6 +531,42 @@ def test_the_weights_whose_gradient_is_taken_are_the_routers(moe, method):
     np.testing.assert_allclose(scales.cpu().numpy(), want, rtol=1e-6)
 
 
+# ---------------------------------------------------------------------------------- graphs
+
+def test_operators_in_a_captured_graph(moe):
+    """Captured once and replayed on other values in the same tensors: what the calls give outside."""
+    T, H, I, E, k = 70, 128, 96, 6, 3
+    ids = torch.from_numpy(make_ids(T, E, k, "dropped", 1)).cuda()
+    x, w13, w2 = randn((T, H), "bf16", 1), randn((E, 2 * I, H), "bf16", 2, 0.1), randn((E, H, I), "bf16", 3, 0.1)
+    scales, dy, logits = torch.rand((T, k)).cuda(), randn((T, H), "bf16", 4), randn((T, E), "f32", 5)
+
+    def step():
+        xp, inv, off = moe.moe_dispatch(x, ids, E)
+        h, ck = moe.moe_swiglu_ckpt(moe.moe_experts_matmul(xp, w13, off))
+        rows = moe.moe_experts_matmul(h, w2, off)
+        y = moe.moe_combine(rows, inv, scales)
+        drows, ds = moe.moe_combine_backward(dy, rows, inv, scales)
+        dgu, h2 = moe.moe_swiglu_ckpt_backward(moe.moe_experts_matmul_dx(drows, w2, off), ck, want_h=True)
+        return (xp, inv, off, y, ds, moe.moe_experts_matmul_dw(drows, h2, off),
+                moe.moe_experts_matmul_dw(dgu, xp, off),
+                moe.moe_dispatch_backward(moe.moe_experts_matmul_dx(dgu, w13, off), inv),
+                moe.moe_route_backward(logits, ids, ds, 4))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    x.copy_(randn((T, H), "bf16", 11))
+    ids.copy_(torch.from_numpy(make_ids(T, E, k, "dropped", 12)))
+    dy.copy_(randn((T, H), "bf16", 13))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, step()):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------- empty and refused
 
 def test_no_rows(moe):
