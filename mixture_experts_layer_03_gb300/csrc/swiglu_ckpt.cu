@@ -217,83 +217,130 @@ swiglu_ckpt_grad_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
   }
 }
 
-// Any I: neighbouring channels to neighbouring lanes, a warp to kAnyBlocks blocks of 32 channels.
-// (Eight channels a lane here, as above but one element at a time, took 19 us for the backward
-// pass of 2000 rows of 1001 channels, this form 11.)
-constexpr int kAnyBlocks = 4;
+// Any I: neighbouring channels to neighbouring lanes, a warp to a segment of kBlocks blocks of 32
+// channels of g and of u. These kernels are bound by instructions, so lane j looks after the scale of
+// block j alone (those of g, then of u) and full segments go without a check: 1941 rows of 13603
+// channels bf16, forward and backward with h, 48 and 58 us; with each scale in every lane 73 and 79.
+// (Vectors of 16 bytes, shifted into place through shuffles or through shared memory, took 62 to 82
+// and 80 to 103.) Eight blocks, or four where these hold a row: 8000 rows of 70 channels 4.4 and 4.8 us
+// so, with eight 5.3 and 5.4; 1941 of 13603 with four 50 and 62.
 
-template <typename T>
+// v[lane % n], for n values that are the same in every lane.
+template <int n>
+__device__ __forceinline__ uint32_t pick_lane(uint32_t (&v)[n], int lane) {
+#pragma unroll
+  for (int w = n / 2, bit = n / 2; w >= 1; w /= 2, bit /= 2)
+#pragma unroll
+    for (int i = 0; i < w; ++i) v[i] = lane & bit ? v[i + w] : v[i];
+  return v[0];
+}
+
+// A warp's segment: channels from c0 on; kFull: all of them below I.
+template <typename T, int kBlocks, bool kFull>
+__device__ __forceinline__ void ckpt_segment(const T* src, int I, int c0, T* h, uint8_t* q,
+                                             uint8_t* qs) {
+  const int lane = threadIdx.x & 31;
+  const int nb = (I + kCkptBlock - 1) / kCkptBlock, b0 = c0 / kCkptBlock;
+  float g[kBlocks], u[kBlocks];
+  const T* in = src + c0 + lane;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const bool there = kFull || c0 + i * kCkptBlock + lane < I;
+    g[i] = there ? to_f32<T>(__ldg(in + i * kCkptBlock)) : 0.0f;
+    u[i] = there ? to_f32<T>(__ldg(in + I + i * kCkptBlock)) : 0.0f;
+  }
+  uint32_t m[2 * kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    m[i] = __reduce_max_sync(0xffffffffu, __float_as_uint(g[i]) & 0x7fffffffu);
+    m[kBlocks + i] = __reduce_max_sync(0xffffffffu, __float_as_uint(u[i]) & 0x7fffffffu);
+  }
+  const uint32_t mine = scale_byte(__uint_as_float(pick_lane(m, lane)));
+  const float inv = inv_scale(mine);
+  const int block = b0 + lane % kBlocks;
+  if (lane < 2 * kBlocks && (kFull || block < nb))
+    qs[lane < kBlocks ? block : nb + block] = static_cast<uint8_t>(mine);
+  T* out_h = h + c0 + lane;
+  uint8_t* out_q = q + c0 + lane;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const float ig = __shfl_sync(0xffffffffu, inv, i);
+    const float iu = __shfl_sync(0xffffffffu, inv, kBlocks + i);
+    if (!kFull && c0 + i * kCkptBlock + lane >= I) continue;
+    out_h[i * kCkptBlock] = from_f32<T>(g[i] * sigmoid_fast(g[i]) * u[i]);
+    const uint32_t two = quant2(g[i] * ig, u[i] * iu);
+    out_q[i * kCkptBlock] = static_cast<uint8_t>(two);
+    out_q[I + i * kCkptBlock] = static_cast<uint8_t>(two >> 8);
+  }
+}
+
+template <typename T, int kBlocks>
 __global__ void __launch_bounds__(kCkptThreads)
 swiglu_ckpt_any_kernel(const T* __restrict__ gu, int64_t R, int I, T* __restrict__ h,
                        uint8_t* __restrict__ q, uint8_t* __restrict__ qs) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  constexpr int kSegment = kBlocks * kCkptBlock;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((nb + kAnyBlocks - 1) / kAnyBlocks); w.row < R; w.next()) {
-    const int b0 = w.seg * kAnyBlocks;
-    const T* src = gu + w.row * 2 * I;
-    float g[kAnyBlocks], u[kAnyBlocks];
-#pragma unroll
-    for (int i = 0; i < kAnyBlocks; ++i) {
-      const int c = (b0 + i) * kCkptBlock + lane;
-      g[i] = c < I ? to_f32<T>(__ldg(src + c)) : 0.0f;
-      u[i] = c < I ? to_f32<T>(__ldg(src + I + c)) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < kAnyBlocks; ++i) {
-      const int c = (b0 + i) * kCkptBlock + lane;
-      const uint32_t mg = __reduce_max_sync(0xffffffffu, __float_as_uint(g[i]) & 0x7fffffffu);
-      const uint32_t mu = __reduce_max_sync(0xffffffffu, __float_as_uint(u[i]) & 0x7fffffffu);
-      const uint32_t sg = scale_byte(__uint_as_float(mg)), su = scale_byte(__uint_as_float(mu));
-      if (c < I) {
-        h[w.row * I + c] = from_f32<T>(g[i] * sigmoid_fast(g[i]) * u[i]);
-        uint8_t* dst = q + w.row * 2 * I + c;
-        dst[0] = static_cast<uint8_t>(quant2(g[i] * inv_scale(sg), 0.0f));
-        dst[I] = static_cast<uint8_t>(quant2(u[i] * inv_scale(su), 0.0f));
-      }
-      if (lane == 0 && b0 + i < nb) {
-        uint8_t* sd = qs + w.row * 2 * nb + b0 + i;
-        sd[0] = static_cast<uint8_t>(sg);
-        sd[nb] = static_cast<uint8_t>(su);
-      }
-    }
+  for (Walk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
+    const int c0 = w.seg * kSegment;
+    const int64_t at = w.row * I;
+    if (c0 + kSegment <= I)
+      ckpt_segment<T, kBlocks, true>(gu + 2 * at, I, c0, h + at, q + 2 * at, qs + w.row * 2 * nb);
+    else
+      ckpt_segment<T, kBlocks, false>(gu + 2 * at, I, c0, h + at, q + 2 * at, qs + w.row * 2 * nb);
   }
 }
 
-template <typename T, bool kWantH>
+template <typename T, int kBlocks, bool kWantH, bool kFull>
+__device__ __forceinline__ void ckpt_grad_segment(const T* dh, const uint8_t* q, const uint8_t* qs,
+                                                  int I, int c0, T* dgu, T* h) {
+  const int lane = threadIdx.x & 31;
+  const int nb = (I + kCkptBlock - 1) / kCkptBlock, b0 = c0 / kCkptBlock;
+  float d[kBlocks];
+  uint32_t two[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    // Lanes past the row's end read its last channel, and write nothing.
+    const int c = kFull ? c0 + i * kCkptBlock + lane : min(c0 + i * kCkptBlock + lane, I - 1);
+    d[i] = to_f32<T>(__ldg(dh + c));
+    two[i] = __ldg(q + c) | __ldg(q + I + c) << 8;
+  }
+  const int block = kFull ? b0 + lane % kBlocks : min(b0 + lane % kBlocks, nb - 1);
+  const float scale = scale_of(__ldg(qs + (lane & kBlocks ? nb + block : block)));
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const float2 v = dequant2(two[i]);
+    const float g = v.x * __shfl_sync(0xffffffffu, scale, i);
+    const float u = v.y * __shfl_sync(0xffffffffu, scale, kBlocks + i);
+    const int c = c0 + i * kCkptBlock + lane;
+    if (!kFull && c >= I) continue;
+    float dg, du, y;
+    grad_of(d[i], g, u, &dg, &du, &y);
+    dgu[c] = from_f32<T>(dg);
+    dgu[I + c] = from_f32<T>(du);
+    if (kWantH) h[c] = from_f32<T>(y);
+  }
+}
+
+template <typename T, int kBlocks, bool kWantH>
 __global__ void __launch_bounds__(kCkptThreads)
 swiglu_ckpt_grad_any_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
                             const uint8_t* __restrict__ qs, int64_t R, int I, T* __restrict__ dgu,
                             T* __restrict__ h) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  constexpr int kSegment = kBlocks * kCkptBlock;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((nb + kAnyBlocks - 1) / kAnyBlocks); w.row < R; w.next()) {
-    const int b0 = w.seg * kAnyBlocks;
-    float d[kAnyBlocks], g[kAnyBlocks], u[kAnyBlocks];
-#pragma unroll
-    for (int i = 0; i < kAnyBlocks; ++i) {
-      // Lanes past the row's end read its last channel, and write nothing.
-      const int c = min((b0 + i) * kCkptBlock + lane, I - 1);
-      const uint8_t* src = q + w.row * 2 * I + c;
-      const uint8_t* ss = qs + w.row * 2 * nb + c / kCkptBlock;
-      d[i] = to_f32<T>(__ldg(dh + w.row * I + c));
-      g[i] = dequant2(__ldg(src)).x * scale_of(__ldg(ss));
-      u[i] = dequant2(__ldg(src + I)).x * scale_of(__ldg(ss + nb));
-    }
-#pragma unroll
-    for (int i = 0; i < kAnyBlocks; ++i) {
-      const int c = (b0 + i) * kCkptBlock + lane;
-      if (c >= I) continue;
-      float dg, du, y;
-      grad_of(d[i], g[i], u[i], &dg, &du, &y);
-      T* dst = dgu + w.row * 2 * I + c;
-      dst[0] = from_f32<T>(dg);
-      dst[I] = from_f32<T>(du);
-      if (kWantH) h[w.row * I + c] = from_f32<T>(y);
-    }
+  for (Walk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
+    const int c0 = w.seg * kSegment;
+    const int64_t at = w.row * I;
+    if (c0 + kSegment <= I)
+      ckpt_grad_segment<T, kBlocks, kWantH, true>(dh + at, q + 2 * at, qs + w.row * 2 * nb, I, c0,
+                                         dgu + 2 * at, h + at);
+    else
+      ckpt_grad_segment<T, kBlocks, kWantH, false>(dh + at, q + 2 * at, qs + w.row * 2 * nb, I, c0,
+                                          dgu + 2 * at, h + at);
   }
 }
 
@@ -314,9 +361,12 @@ cudaError_t forward_t(const void* gu, int64_t R, int I, void* h, uint8_t* q, uin
     return launch_pdl(swiglu_ckpt_kernel<T>, dim3(ckpt_grid(R, (I + 255) / 256)),
                       dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I,
                       static_cast<T*>(h), q, qs);
-  return launch_pdl(swiglu_ckpt_any_kernel<T>, dim3(ckpt_grid(R, (I + 127) / 128)),
-                    dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I,
-                    static_cast<T*>(h), q, qs);
+  if (I <= 128)
+    return launch_pdl(swiglu_ckpt_any_kernel<T, 4>, dim3(ckpt_grid(R, 1)), dim3(kCkptThreads), 0, s,
+                      static_cast<const T*>(gu), R, I, static_cast<T*>(h), q, qs);
+  return launch_pdl(swiglu_ckpt_any_kernel<T, 8>, dim3(ckpt_grid(R, (I + 255) / 256)),
+                    dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I, static_cast<T*>(h), q,
+                    qs);
 }
 
 template <typename T, bool kWantH>
@@ -326,7 +376,11 @@ cudaError_t backward_t(const void* dh, const uint8_t* q, const uint8_t* qs, int6
     return launch_pdl(swiglu_ckpt_grad_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 255) / 256)),
                       dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                       static_cast<T*>(dgu), static_cast<T*>(h));
-  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 127) / 128)),
+  if (I <= 128)
+    return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 4, kWantH>, dim3(ckpt_grid(R, 1)),
+                      dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
+                      static_cast<T*>(dgu), static_cast<T*>(h));
+  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 8, kWantH>, dim3(ckpt_grid(R, (I + 255) / 256)),
                     dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                     static_cast<T*>(dgu), static_cast<T*>(h));
 }
