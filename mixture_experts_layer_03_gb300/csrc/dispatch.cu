@@ -114,33 +114,78 @@ __global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(SortArgs a) {
   }
 }
 
-// How a block copies token rows: a group of 32..256 threads takes a token, each thread up to four
-// vectors of it at a time.
-__device__ __forceinline__ int group_of(int nvec) {
-  return nvec > 128 ? 256 : nvec > 64 ? 128 : nvec > 32 ? 64 : 32;
+// How a block copies token rows: a group of 32..256 threads takes a token, each thread up to kQ vectors
+// of it at a time, a group apart.
+__device__ __forceinline__ int group_of(int n) {
+  return n > 128 ? 256 : n > 64 ? 128 : n > 32 ? 64 : 32;
 }
 
-// Up to four vectors of a token's row from v on, a group apart.
 template <int kBytes>
-__device__ __forceinline__ void load4(typename RawVec<kBytes>::type (&val)[4], const char* row, int v,
-                                      int g, int nvec) {
-  const auto* src = reinterpret_cast<const typename RawVec<kBytes>::type*>(row);
+struct RowCopy {
+  using Raw = uint4;
+  static_assert(kBytes == 16);
+  static constexpr int kQ = 4;
+  __device__ __forceinline__ static int group(int nvec) { return group_of(nvec); }
+  __device__ __forceinline__ static int first(int in_group) { return in_group; }
+  __device__ __forceinline__ static void load(Raw (&val)[kQ], const char* row, int v, int g, int nvec) {
+    const Raw* src = reinterpret_cast<const Raw*>(row);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (v + q * g < nvec) val[q] = __ldg(src + v + q * g);
-}
+    for (int q = 0; q < kQ; ++q)
+      if (v + q * g < nvec) val[q] = __ldg(src + v + q * g);
+  }
+  // The same vectors to row p of x_perm, or zeros to row ~p (a dropped slot).
+  __device__ __forceinline__ static void store(const Raw (&val)[kQ], char* x_perm, int32_t p, int v,
+                                               int g, int nvec) {
+    Raw* d = reinterpret_cast<Raw*>(x_perm + static_cast<int64_t>(p < 0 ? ~p : p) * nvec * kBytes);
+    const Raw zero{};
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+      if (v + q * g < nvec) __stcs(d + v + q * g, p < 0 ? zero : val[q]);
+  }
+};
 
-// The same vectors to row p of x_perm, or zeros to row ~p (a dropped slot).
+// Narrower vectors, whose copies are bound by instructions: a thread's lie 32 apart, so that one address
+// and constants reach them, and are not checked one by one where all exist. (4096 tokens to six rows
+// each of 7167 bf16 97 us, of 7164 81; in the form above 156 and 85.)
 template <int kBytes>
-__device__ __forceinline__ void store4(const typename RawVec<kBytes>::type (&val)[4], char* x_perm,
-                                       int32_t p, int v, int g, int nvec) {
+struct NarrowCopy {
   using Raw = typename RawVec<kBytes>::type;
-  Raw* d = reinterpret_cast<Raw*>(x_perm + static_cast<int64_t>(p < 0 ? ~p : p) * nvec * kBytes);
-  const Raw zero{};
+  static constexpr int kQ = 8;
+  __device__ __forceinline__ static int group(int nvec) { return group_of((nvec + kQ - 1) / kQ); }
+  __device__ __forceinline__ static int first(int in_group) {
+    return (in_group & ~31) * kQ + (in_group & 31);
+  }
+  __device__ __forceinline__ static void load(Raw (&val)[kQ], const char* row, int v, int, int nvec) {
+    const Raw* src = reinterpret_cast<const Raw*>(row) + v;
+    if (v + (kQ - 1) * 32 < nvec) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (v + q * g < nvec) __stcs(d + v + q * g, p < 0 ? zero : val[q]);
-}
+      for (int q = 0; q < kQ; ++q) val[q] = __ldg(src + q * 32);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        if (v + q * 32 < nvec) val[q] = __ldg(src + q * 32);
+    }
+  }
+  __device__ __forceinline__ static void store(const Raw (&val)[kQ], char* x_perm, int32_t p, int v,
+                                               int, int nvec) {
+    Raw* d = reinterpret_cast<Raw*>(x_perm) + static_cast<int64_t>(p < 0 ? ~p : p) * nvec + v;
+    const Raw zero{};
+    if (p >= 0 && v + (kQ - 1) * 32 < nvec) {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) __stcs(d + q * 32, val[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        if (v + q * 32 < nvec) __stcs(d + q * 32, p < 0 ? zero : val[q]);
+    }
+  }
+};
+template <>
+struct RowCopy<8> : NarrowCopy<8> {};
+template <>
+struct RowCopy<4> : NarrowCopy<4> {};
+template <>
+struct RowCopy<2> : NarrowCopy<2> {};
 
 // Places of a block's slots and the copy of their rows. kSelfCount: every block counts all
 // ids itself, and nothing ran before it; else the scan kernel left each block its first place
@@ -159,7 +204,8 @@ sort_place_kernel(SortArgs a, const char* __restrict__ x, char* __restrict__ x_p
   const int64_t t_first = a.chunk * blockIdx.x;
   const int64_t t_last = min(a.T, t_first + a.chunk);
   const int64_t row_bytes = static_cast<int64_t>(nvec) * kBytes;
-  const int g = group_of(nvec), in_group = tid & (g - 1), my_token = tid / g;
+  using Copy = RowCopy<kBytes>;
+  const int g = Copy::group(nvec), first = Copy::first(tid & (g - 1)), my_token = tid / g;
   pdl_trigger();
   for (int i = tid; i < kSortWarps * kMaxBins; i += kSortThreads) (&s_wcnt[0][0])[i] = 0;
   if (kSelfCount) {
@@ -168,9 +214,9 @@ sort_place_kernel(SortArgs a, const char* __restrict__ x, char* __restrict__ x_p
     __syncthreads();
   }
   pdl_wait();
-  typename RawVec<kBytes>::type val[4];
+  typename Copy::Raw val[Copy::kQ];
   if (t_first + my_token < t_last)
-    load4<kBytes>(val, x + (t_first + my_token) * row_bytes, in_group, g, nvec);
+    Copy::load(val, x + (t_first + my_token) * row_bytes, first, g, nvec);
   int total;
   if (kSelfCount) {
     const int P = static_cast<int>(a.P), f_first = static_cast<int>(t_first) * a.k;
@@ -242,10 +288,10 @@ sort_place_kernel(SortArgs a, const char* __restrict__ x, char* __restrict__ x_p
     }
     for (int i = my_token; i < n; i += kSortThreads / g) {
       const char* row = x + (t0 + i) * row_bytes;
-      for (int v = in_group; v < nvec; v += 4 * g) {
-        if (t0 > t_first || i > my_token || v > in_group) load4<kBytes>(val, row, v, g, nvec);
+      for (int v = first; v < nvec; v += Copy::kQ * g) {
+        if (t0 > t_first || i > my_token || v > first) Copy::load(val, row, v, g, nvec);
         for (int j = 0; j < a.k; ++j)
-          store4<kBytes>(val, x_perm, s_dst[i * a.k + j], v, g, nvec);
+          Copy::store(val, x_perm, s_dst[i * a.k + j], v, g, nvec);
       }
     }
   }
@@ -259,45 +305,42 @@ dispatch_rows_kernel(const char* __restrict__ x, const int32_t* __restrict__ inv
   pdl_trigger();
   pdl_wait();
   const int64_t P = T * k;
-  const int g = group_of(nvec), in_group = threadIdx.x & (g - 1);
+  using Copy = RowCopy<kBytes>;
+  const int g = Copy::group(nvec), first = Copy::first(threadIdx.x & (g - 1));
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (kSortThreads / g);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kSortThreads / g) + threadIdx.x / g; t < T;
        t += groups) {
     const char* row = x + t * nvec * kBytes;
-    for (int v = in_group; v < nvec; v += 4 * g) {
-      typename RawVec<kBytes>::type val[4];
-      load4<kBytes>(val, row, v, g, nvec);
+    for (int v = first; v < nvec; v += Copy::kQ * g) {
+      typename Copy::Raw val[Copy::kQ];
+      Copy::load(val, row, v, g, nvec);
       for (int j = 0; j < k; ++j) {
         const int32_t p = __ldg(inv + t * k + j);
-        if ((p < 0 ? ~p : p) < P) store4<kBytes>(val, x_perm, p, v, g, nvec);
+        if ((p < 0 ? ~p : p) < P) Copy::store(val, x_perm, p, v, g, nvec);
       }
     }
   }
 }
 
-// A thread takes kU vectors of a token's row, a kU-th of the row apart (16 bytes in all where the
-// vectors are single elements, so that the token's places and weights are read for as many bytes
-// either way): their row loads are issued together and summed in slot order. scales NULL: every
-// weight is 1.
-template <typename T, int kBytes, int kSlots, int kU>
+// A thread takes a vector of a token's row: the row loads of its slots are issued together and summed
+// in slot order. scales NULL: every weight is 1.
+template <typename T, int kSlots>
 __global__ void __launch_bounds__(kSortThreads)
 combine_kernel(const T* __restrict__ rows, const int32_t* __restrict__ inv,
                const float* __restrict__ scales, int64_t n_tok, int k, int nvec,
                T* __restrict__ y) {
-  using V = Vec<T, kBytes>;
-  using Raw = typename V::Raw;
+  using V = Vec<T, 16>;
   pdl_trigger();
   pdl_wait();
   const int64_t P = n_tok * k;
-  const int per = (nvec + kU - 1) / kU;   // threads of a token
-  const int64_t total = n_tok * per;
+  const int64_t total = n_tok * nvec;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kSortThreads;
-  const Raw* in = reinterpret_cast<const Raw*>(rows);
+  const uint4* in = reinterpret_cast<const uint4*>(rows);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < total;
        i += stride) {
     const int64_t t = total <= UINT32_MAX
-                          ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
-    const int v = static_cast<int>(i - t * per);
+                          ? static_cast<uint32_t>(i) / static_cast<uint32_t>(nvec) : i / nvec;
+    const int v = static_cast<int>(i - t * nvec);
     int32_t row[kSlots];
     float s[kSlots];
 #pragma unroll
@@ -310,49 +353,111 @@ combine_kernel(const T* __restrict__ rows, const int32_t* __restrict__ inv,
         if (scales) s[j] = __ldg(scales + t * k + j);
       }
     }
-    float acc[kU][V::kN] = {};
-    Raw val[kU][kSlots];
+    float acc[V::kN] = {};
+    uint4 val[kSlots];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int j = 0; j < kSlots; ++j)
+      if (row[j] >= 0) val[j] = __ldg(in + static_cast<int64_t>(row[j]) * nvec + v);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (row[j] >= 0 && v + u * per < nvec)
-          val[u][j] = __ldg(in + static_cast<int64_t>(row[j]) * nvec + v + u * per);
+    for (int j = 0; j < kSlots; ++j) {
+      if (row[j] < 0) continue;
+      float f[V::kN];
+      V::unpack(val[j], f);
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (v + u * per >= nvec) break;
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        if (row[j] < 0) continue;
-        float f[V::kN];
-        V::unpack(val[u][j], f);
-#pragma unroll
-        for (int c = 0; c < V::kN; ++c) acc[u][c] = fmaf(s[j], f[c], acc[u][c]);
-      }
-      reinterpret_cast<Raw*>(y)[t * nvec + v + u * per] = V::pack(acc[u]);
+      for (int c = 0; c < V::kN; ++c) acc[c] = fmaf(s[j], f[c], acc[c]);
     }
+    reinterpret_cast<uint4*>(y)[t * nvec + v] = V::pack(acc);
+  }
+}
+
+// Rows that do not start on 16 bytes: vectors of kBytes. These kernels are bound by instructions, so a
+// warp takes kU times 32 neighbouring vectors, which one address a row reaches, unchecked where all of
+// them exist (kFull), kJ slots at a time. (4096 tokens, k = 6, bf16: H = 7167 94 us, H = 7164 75; a
+// thread for every four vectors, each with its own addresses, took 154 for either. Reading rows in
+// aligned 16-byte vectors and shifting these into place took 125, and 1001 f32 69 instead of 23.)
+template <typename T, int kBytes, int kU, int kJ, bool kFull>
+__device__ __forceinline__ void combine_segment(const T* rows, int32_t place, float scale, int64_t P,
+                                                int k, int nvec, int v, T* y) {
+  using V = Vec<T, kBytes>;
+  using Raw = typename V::Raw;
+  float acc[kU][V::kN] = {};
+  for (int j = 0; j < k; j += kJ) {
+    Raw val[kJ][kU];
+    float s[kJ];
+#pragma unroll
+    for (int h = 0; h < kJ; ++h) {
+      const int32_t p = __shfl_sync(0xffffffffu, place, j + h);   // (-1 in the lanes past k)
+      s[h] = __shfl_sync(0xffffffffu, scale, j + h);
+      const bool kept = p >= 0 && p < P;
+      const Raw* src = reinterpret_cast<const Raw*>(rows) + static_cast<int64_t>(p) * nvec + v;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        val[h][u] = Raw{};
+        if (kept && (kFull || v + u * 32 < nvec)) val[h][u] = __ldg(src + u * 32);
+      }
+      if (!kept) s[h] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < kJ; ++h)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float f[V::kN];
+        V::unpack(val[h][u], f);
+#pragma unroll
+        for (int c = 0; c < V::kN; ++c) acc[u][c] = fmaf(s[h], f[c], acc[u][c]);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+    if (kFull || v + u * 32 < nvec) reinterpret_cast<Raw*>(y)[v + u * 32] = V::pack(acc[u]);
+}
+
+template <typename T, int kBytes, int kU, int kJ>
+__global__ void __launch_bounds__(kSortThreads)
+combine_narrow_kernel(const T* __restrict__ rows, const int32_t* __restrict__ inv,
+                      const float* __restrict__ scales, int64_t n_tok, int k, int nvec,
+                      T* __restrict__ y) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t P = n_tok * k;
+  const int segs = (nvec + 32 * kU - 1) / (32 * kU);
+  const int64_t total = n_tok * segs, stride = static_cast<int64_t>(gridDim.x) * kSortWarps;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortWarps + (threadIdx.x >> 5); i < total;
+       i += stride) {
+    const int64_t t = total <= UINT32_MAX
+                          ? static_cast<uint32_t>(i) / static_cast<uint32_t>(segs) : i / segs;
+    const int v = static_cast<int>(i - t * segs) * 32 * kU;
+    int32_t place = -1;
+    float scale = 1.0f;
+    if (lane < k) {
+      place = __ldg(inv + t * k + lane);
+      if (scales) scale = __ldg(scales + t * k + lane);
+    }
+    T* to = y + t * nvec * Vec<T, kBytes>::kN;
+    if (v + 32 * kU <= nvec)
+      combine_segment<T, kBytes, kU, kJ, true>(rows, place, scale, P, k, nvec, v + lane, to);
+    else
+      combine_segment<T, kBytes, kU, kJ, false>(rows, place, scale, P, k, nvec, v + lane, to);
   }
 }
 
 // kWarps warps per token: each vector of dy[t] is read once and meets the vectors of the
 // token's kept rows; the k dot products are summed over the lanes (and warps) in fixed order.
-template <typename T, int kBytes, int kSlots, int kWarps>
+template <typename T, int kSlots, int kWarps>
 __global__ void __launch_bounds__(kSortThreads)
 combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
                     const int32_t* __restrict__ inv, const float* __restrict__ scales,
                     int64_t n_tok, int k, int nvec, T* __restrict__ drows,
                     float* __restrict__ dscales) {
-  using V = Vec<T, kBytes>;
-  using Raw = typename V::Raw;
+  using V = Vec<T, 16>;
   constexpr int kToks = kSortWarps / kWarps;   // tokens a block has at a time
-  constexpr int kU = kBytes == 16 ? 1 : 4;     // vectors a lane has at a time
   __shared__ float s_dot[kWarps > 1 ? kSortWarps : 1][kSlots];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = warp % kWarps;
   const int64_t P = n_tok * k;
-  const Raw zero{};
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kToks; t0 < n_tok;
        t0 += static_cast<int64_t>(gridDim.x) * kToks) {
     const int64_t t = t0 + warp / kWarps;
@@ -370,43 +475,32 @@ combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
           s[j] = scales ? __ldg(scales + t * k + j) : 1.0f;
         }
       }
-      const Raw* src = reinterpret_cast<const Raw*>(dy) + t * nvec;
-      for (int v0 = sub * 32 + lane; v0 < nvec; v0 += 32 * kWarps * kU) {
-        Raw d[kU], val[kU][kSlots];
+      const uint4* src = reinterpret_cast<const uint4*>(dy) + t * nvec;
+      for (int v = sub * 32 + lane; v < nvec; v += 32 * kWarps) {
+        uint4 val[kSlots];
+        const uint4 d = __ldg(src + v);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = v0 + u * 32 * kWarps;
-          if (v >= nvec) break;
-          d[u] = __ldg(src + v);
+        for (int j = 0; j < kSlots; ++j)
+          if (row[j] >= 0)
+            val[j] = __ldg(reinterpret_cast<const uint4*>(rows) + static_cast<int64_t>(row[j]) * nvec + v);
+        float df[V::kN];
+        V::unpack(d, df);
 #pragma unroll
-          for (int j = 0; j < kSlots; ++j)
-            if (row[j] >= 0)
-              val[u][j] =
-                  __ldg(reinterpret_cast<const Raw*>(rows) + static_cast<int64_t>(row[j]) * nvec + v);
-        }
+        for (int j = 0; j < kSlots; ++j) {
+          if (row[j] == INT32_MIN) continue;
+          uint4 out{};
+          if (row[j] >= 0) {
+            float f[V::kN], o[V::kN];
+            V::unpack(val[j], f);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int v = v0 + u * 32 * kWarps;
-          if (v >= nvec) break;
-          float df[V::kN];
-          V::unpack(d[u], df);
-#pragma unroll
-          for (int j = 0; j < kSlots; ++j) {
-            if (row[j] == INT32_MIN) continue;
-            Raw out = zero;
-            if (row[j] >= 0) {
-              float f[V::kN], o[V::kN];
-              V::unpack(val[u][j], f);
-#pragma unroll
-              for (int c = 0; c < V::kN; ++c) {
-                dot[j] = fmaf(df[c], f[c], dot[j]);
-                o[c] = s[j] * df[c];
-              }
-              out = V::pack(o);
+            for (int c = 0; c < V::kN; ++c) {
+              dot[j] = fmaf(df[c], f[c], dot[j]);
+              o[c] = s[j] * df[c];
             }
-            const int64_t r = row[j] < 0 ? ~row[j] : row[j];
-            __stcs(reinterpret_cast<Raw*>(drows) + r * nvec + v, out);
+            out = V::pack(o);
           }
+          const int64_t r = row[j] < 0 ? ~row[j] : row[j];
+          __stcs(reinterpret_cast<uint4*>(drows) + r * nvec + v, out);
         }
       }
     }
@@ -435,6 +529,93 @@ combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
   }
 }
 
+// The same for rows that do not start on 16 bytes, in vectors of kBytes: kWarps warps to a slot (dy[t]
+// comes from L1 to the second and later ones), a warp kU times 32 neighbouring vectors at a time (4096
+// tokens, k = 6, bf16: H = 7167 175 us, H = 7164 129; the form above with such vectors 212 for either).
+template <typename T, int kBytes, int kU, bool kFull>
+__device__ __forceinline__ float combine_grad_segment(const T* dy, const T* rows, float s, int nvec,
+                                                      int v, T* drows) {
+  using V = Vec<T, kBytes>;
+  using Raw = typename V::Raw;
+  Raw d[kU], val[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    d[u] = val[u] = Raw{};
+    if (kFull || v + u * 32 < nvec) {
+      d[u] = __ldg(reinterpret_cast<const Raw*>(dy) + v + u * 32);
+      val[u] = __ldg(reinterpret_cast<const Raw*>(rows) + v + u * 32);
+    }
+  }
+  float dot = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    float df[V::kN], f[V::kN], o[V::kN];
+    V::unpack(d[u], df);
+    V::unpack(val[u], f);
+#pragma unroll
+    for (int c = 0; c < V::kN; ++c) {
+      dot = fmaf(df[c], f[c], dot);
+      o[c] = s * df[c];
+    }
+    if (kFull || v + u * 32 < nvec) __stcs(reinterpret_cast<Raw*>(drows) + v + u * 32, V::pack(o));
+  }
+  return dot;
+}
+
+template <typename T, int kBytes, int kU, int kWarps>
+__global__ void __launch_bounds__(kSortThreads)
+combine_grad_narrow_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
+                           const int32_t* __restrict__ inv, const float* __restrict__ scales,
+                           int64_t n_tok, int k, int nvec, T* __restrict__ drows,
+                           float* __restrict__ dscales) {
+  using V = Vec<T, kBytes>;
+  using Raw = typename V::Raw;
+  constexpr int kAtOnce = kSortWarps / kWarps;   // slots of a block
+  __shared__ float s_dot[kSortWarps];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
+  const int64_t P = n_tok * k;
+  for (int64_t f0 = static_cast<int64_t>(blockIdx.x) * kAtOnce; f0 < P;
+       f0 += static_cast<int64_t>(gridDim.x) * kAtOnce) {
+    const int64_t f = f0 + warp / kWarps;
+    float dot = 0.0f;
+    if (f < P) {
+      const int32_t p = __ldg(inv + f);
+      const float s = scales ? __ldg(scales + f) : 1.0f;
+      const int64_t t = P <= UINT32_MAX ? static_cast<uint32_t>(f) / static_cast<uint32_t>(k) : f / k;
+      const int64_t r = p < 0 ? ~p : p;
+      const T* from = dy + t * nvec * V::kN;
+      const T* with = rows + r * nvec * V::kN;
+      T* to = drows + r * nvec * V::kN;
+      if (p >= 0 && r < P) {
+        for (int v = sub * 32 * kU; v < nvec; v += kWarps * 32 * kU)
+          dot += v + 32 * kU <= nvec
+                     ? combine_grad_segment<T, kBytes, kU, true>(from, with, s, nvec, v + lane, to)
+                     : combine_grad_segment<T, kBytes, kU, false>(from, with, s, nvec, v + lane, to);
+      } else if (r < P) {
+        for (int v = sub * 32 + lane; v < nvec; v += kWarps * 32)
+          __stcs(reinterpret_cast<Raw*>(to) + v, Raw{});
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (kWarps == 1) {
+      if (f < P && lane == 0) dscales[f] = dot;
+    } else {
+      if (lane == 0) s_dot[warp] = dot;
+      __syncthreads();
+      if (f < P && sub == 0 && lane == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_dot[warp + w];
+        dscales[f] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // The widest of 16, 8, 4 and 2 bytes that divides a row.
 int copy_bytes(int64_t row_bytes) {
   return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : row_bytes % 4 == 0 ? 4 : 2;
@@ -455,56 +636,92 @@ cudaError_t launch_place(const SortArgs& a, bool self, const void* x, void* x_pe
                     static_cast<const char*>(x), static_cast<char*>(x_perm), nvec);
 }
 
-template <typename T, int kBytes, int kSlots>
+template <typename T, int kSlots>
 cudaError_t combine_t(const void* rows, const int32_t* inv, const float* scales, int64_t n_tok,
                       int H, int k, void* y, cudaStream_t s) {
-  const int nvec = H / Vec<T, kBytes>::kN;
-  constexpr int kU = kBytes == 16 ? 1 : 4;
-  const int64_t blocks = (n_tok * ((nvec + kU - 1) / kU) + kSortThreads - 1) / kSortThreads;
-  return launch_pdl(combine_kernel<T, kBytes, kSlots, kU>, dim3(grid_of(blocks, 32)),
-                    dim3(kSortThreads), 0, s, static_cast<const T*>(rows), inv, scales, n_tok, k,
-                    nvec, static_cast<T*>(y));
+  const int nvec = H / Vec<T, 16>::kN;
+  const int64_t blocks = (n_tok * nvec + kSortThreads - 1) / kSortThreads;
+  return launch_pdl(combine_kernel<T, kSlots>, dim3(grid_of(blocks, 32)), dim3(kSortThreads), 0, s,
+                    static_cast<const T*>(rows), inv, scales, n_tok, k, nvec, static_cast<T*>(y));
 }
 
-template <typename T, int kBytes, int kSlots>
+template <typename T, int kSlots>
 cudaError_t combine_grad_t(const void* dy, const void* rows, const int32_t* inv,
                            const float* scales, int64_t n_tok, int H, int k, void* drows,
                            float* dscales, cudaStream_t s) {
-  const int nvec = H / Vec<T, kBytes>::kN;
+  const int nvec = H / Vec<T, 16>::kN;
   // A warp to a token where the tokens alone fill the GPU and a row is short, else a block: 8192 tokens,
   // k = 8, H = 256 bf16 25 us a warp each and 70 a block each, H = 7168 368 and 306; 256 tokens, H =
   // 2048 9.3 and 4.3.
   if (nvec <= 256 && n_tok >= 1024)
-    return launch_pdl(combine_grad_kernel<T, kBytes, kSlots, 1>,
+    return launch_pdl(combine_grad_kernel<T, kSlots, 1>,
                       dim3(grid_of((n_tok + kSortWarps - 1) / kSortWarps, 32)), dim3(kSortThreads),
                       0, s, static_cast<const T*>(dy), static_cast<const T*>(rows), inv, scales,
                       n_tok, k, nvec, static_cast<T*>(drows), dscales);
-  return launch_pdl(combine_grad_kernel<T, kBytes, kSlots, kSortWarps>, dim3(grid_of(n_tok, 32)),
+  return launch_pdl(combine_grad_kernel<T, kSlots, kSortWarps>, dim3(grid_of(n_tok, 32)),
                     dim3(kSortThreads), 0, s, static_cast<const T*>(dy),
                     static_cast<const T*>(rows), inv, scales, n_tok, k, nvec,
                     static_cast<T*>(drows), dscales);
 }
 
-// Calls f<T, bytes, slots>() for the type, the vector width that H allows and k rounded up.
+template <typename T, int kBytes, int kU, int kJ>
+cudaError_t combine_narrow_u(const void* rows, const int32_t* inv, const float* scales,
+                             int64_t n_tok, int nvec, int k, void* y, cudaStream_t s) {
+  const int64_t warps = n_tok * ((nvec + 32 * kU - 1) / (32 * kU));
+  return launch_pdl(combine_narrow_kernel<T, kBytes, kU, kJ>,
+                    dim3(grid_of((warps + kSortWarps - 1) / kSortWarps, 32)), dim3(kSortThreads), 0,
+                    s, static_cast<const T*>(rows), inv, scales, n_tok, k, nvec,
+                    static_cast<T*>(y));
+}
+
+template <typename T, int kBytes>
+cudaError_t combine_narrow_t(const void* rows, const int32_t* inv, const float* scales,
+                             int64_t n_tok, int H, int k, void* y, cudaStream_t s) {
+  const int nvec = H / Vec<T, kBytes>::kN;
+  // 256 vectors a warp, two slots at a time, or, for short rows and where that leaves few warps, 128 and
+  // four: 4096 tokens, k = 6, H = 7167 bf16 94 us the one way and 116 the other; 500 tokens, k = 8, H =
+  // 2050 5.2 and 4.6, 8192 tokens, k = 8, H = 65 f16 10.0 and 7.0.
+  if (nvec <= 128 || n_tok * ((nvec + 255) / 256) <= 4096)
+    return combine_narrow_u<T, kBytes, 4, 4>(rows, inv, scales, n_tok, nvec, k, y, s);
+  return combine_narrow_u<T, kBytes, 8, 2>(rows, inv, scales, n_tok, nvec, k, y, s);
+}
+
+template <typename T, int kBytes>
+cudaError_t combine_grad_narrow_t(const void* dy, const void* rows, const int32_t* inv,
+                                  const float* scales, int64_t n_tok, int H, int k, void* drows,
+                                  float* dscales, cudaStream_t s) {
+  const int nvec = H / Vec<T, kBytes>::kN;
+  const int64_t P = n_tok * k;
+  auto run = [&](auto* kernel, int64_t blocks) {
+    return launch_pdl(kernel, dim3(grid_of(blocks, 32)), dim3(kSortThreads), 0, s,
+                      static_cast<const T*>(dy), static_cast<const T*>(rows), inv, scales, n_tok, k,
+                      nvec, static_cast<T*>(drows), dscales);
+  };
+  // A warp to a slot where the slots alone fill the GPU, or nearly so with short rows, else a block: k =
+  // 8 bf16, 512 tokens of 7167 45 us a warp each and 33 a block each, 4000 tokens of 333 (k = 4) 7.0 and
+  // 18, 256 tokens of 1001 4.2 and 4.6; 4096 tokens of 7167, k = 6, 175 and 183.
+  if (P >= 8192 || (nvec <= 1024 && P >= 2048))
+    return run(combine_grad_narrow_kernel<T, kBytes, 4, 1>, (P + kSortWarps - 1) / kSortWarps);
+  return run(combine_grad_narrow_kernel<T, kBytes, 4, kSortWarps>, P);
+}
+
+// Calls f.wide<T, slots>() with k rounded up where H puts every row on 16 bytes, else f.narrow<T,
+// bytes>(): 4 bytes where rows start on them.
 template <typename F>
 cudaError_t by_form(int dtype, int H, int k, const F& f) {
-  auto slots = [&](auto t, auto bytes) {
+  auto form = [&](auto t) {
     using T = decltype(t);
-    constexpr int kB = decltype(bytes)::value;
-    if (k == 1) return f.template operator()<T, kB, 1>();
-    if (k == 2) return f.template operator()<T, kB, 2>();
-    if (k <= 4) return f.template operator()<T, kB, 4>();
-    return f.template operator()<T, kB, 8>();
+    const int64_t row = static_cast<int64_t>(H) * sizeof(T);
+    if (row % 4 != 0) return f.template narrow<T, static_cast<int>(sizeof(T))>();
+    if (row % 16 != 0) return f.template narrow<T, 4>();
+    if (k == 1) return f.template wide<T, 1>();
+    if (k == 2) return f.template wide<T, 2>();
+    if (k <= 4) return f.template wide<T, 4>();
+    return f.template wide<T, 8>();
   };
-  auto width = [&](auto t) {
-    using T = decltype(t);
-    if (static_cast<int64_t>(H) * sizeof(T) % 16 == 0)
-      return slots(t, std::integral_constant<int, 16>());
-    return slots(t, std::integral_constant<int, static_cast<int>(sizeof(T))>());
-  };
-  if (dtype == MOE_DTYPE_BF16) return width(__nv_bfloat16());
-  if (dtype == MOE_DTYPE_F16) return width(__half());
-  return width(float());
+  if (dtype == MOE_DTYPE_BF16) return form(__nv_bfloat16());
+  if (dtype == MOE_DTYPE_F16) return form(__half());
+  return form(float());
 }
 
 struct CombineCall {
@@ -515,9 +732,13 @@ struct CombineCall {
   int H, k;
   void* y;
   cudaStream_t s;
-  template <typename E, int kBytes, int kSlots>
-  cudaError_t operator()() const {
-    return combine_t<E, kBytes, kSlots>(rows, inv, scales, T, H, k, y, s);
+  template <typename E, int kSlots>
+  cudaError_t wide() const {
+    return combine_t<E, kSlots>(rows, inv, scales, T, H, k, y, s);
+  }
+  template <typename E, int kBytes>
+  cudaError_t narrow() const {
+    return combine_narrow_t<E, kBytes>(rows, inv, scales, T, H, k, y, s);
   }
 };
 
@@ -531,9 +752,13 @@ struct CombineGradCall {
   void* drows;
   float* dscales;
   cudaStream_t s;
-  template <typename E, int kBytes, int kSlots>
-  cudaError_t operator()() const {
-    return combine_grad_t<E, kBytes, kSlots>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
+  template <typename E, int kSlots>
+  cudaError_t wide() const {
+    return combine_grad_t<E, kSlots>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
+  }
+  template <typename E, int kBytes>
+  cudaError_t narrow() const {
+    return combine_grad_narrow_t<E, kBytes>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
   }
 };
 

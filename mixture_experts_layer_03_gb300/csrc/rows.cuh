@@ -1,5 +1,5 @@
 // Row elements of the training operators: bf16, f16 or f32 values moved in vectors of kBytes
-// (16 where every row starts on a 16-byte boundary, else one element) and computed on in fp32.
+// (16 where every row starts on a 16-byte boundary, else 8, 4 or 2) and computed on in fp32.
 #pragma once
 
 #include <cstdint>
