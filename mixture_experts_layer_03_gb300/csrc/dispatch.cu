@@ -14,6 +14,7 @@
 // Measured (bf16): dispatch and combine of 8192 x 4096, k = 4, 61 and 53 us (5.5 and 6.4 TB/s); the
 // gradients of 8192 x 7168, k = 8, 305 and 162 us (6.5 TB/s each, 0.97 of a copy's rate). A decode
 // batch (64 x 2048, k = 8) takes 2.8 and 2.4 us, which is a launch's.
+#include <algorithm>
 #include <cstdint>
 
 #include "internal.h"
@@ -25,9 +26,13 @@ namespace {
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
-// The most blocks that the tokens are cut into, all of them resident, and the scan's threads, one
-// a block. (At 608, four on each of 152 SMs, a dispatch of 8192 x 4096 bf16 to four rows each took
-// 64.3 us, at 1024 61.3.)
+// The most blocks that the tokens are cut into, and the scan's threads, one a block. Four are resident on
+// an SM: a second wave fills in where the first ones' copies end, which pays where the copies are long
+// (8192 x 4096 bf16 to four rows each 61.5 us, with one wave 64.9), while those of up to kOneWaveBytes
+// are cut for one wave (1000 x 101 bf16 to eight rows each 8.0 us, with 1000 blocks 11.4; 8192 x 64 10.8
+// and 12.1).
+constexpr int64_t kOneWaveBytes = 16 << 20;
+constexpr int kBlocksPerSm = 4;
 constexpr int kMaxBlocks = 1024;
 constexpr int kScanThreads = kMaxBlocks;
 constexpr int kMaxBins = 257;        // up to 256 experts, then the dropped slots
@@ -765,12 +770,14 @@ struct CombineGradCall {
 int elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 
 // Problems of at most this many slots are sorted and copied in one launch, every block counting all
-// ids (9222 slots, rows of 1001 f32: 13.5 us, in three launches 14.5; 32768 slots of 4096 bf16:
+// ids (9222 slots, rows of 1001 f32: 12.3 us, in three launches 14.2; 32768 slots of 4096 bf16:
 // 69 us, in three launches 64).
 constexpr int64_t kSelfCountMax = MOE_DISPATCH_SMALL_SLOTS;
 
-void chunk_plan(int64_t T, int64_t* chunk, int* nb) {
-  *chunk = (T + kMaxBlocks - 1) / kMaxBlocks;
+void chunk_plan(int64_t T, int64_t out_bytes, int64_t* chunk, int* nb) {
+  int most = kMaxBlocks;
+  if (out_bytes <= kOneWaveBytes) most = std::min(most, kBlocksPerSm * device_sm_count());
+  *chunk = (T + most - 1) / most;
   *nb = static_cast<int>((T + *chunk - 1) / *chunk);
 }
 
@@ -779,7 +786,7 @@ void chunk_plan(int64_t T, int64_t* chunk, int* nb) {
 size_t dispatch_workspace_bytes(int64_t T, int E) {
   int64_t chunk = 1;
   int nb = 1;
-  if (T > 0) chunk_plan(T, &chunk, &nb);
+  if (T > 0) chunk_plan(T, kOneWaveBytes + 1, &chunk, &nb);   // (the more blocks of the two)
   return 16 + 4 * (static_cast<size_t>(E) + static_cast<size_t>(E + 2) * nb);
 }
 
@@ -792,7 +799,7 @@ moe_status launch_dispatch(const void* x, const int32_t* ids, int64_t T, int H, 
   a.P = T * k;
   a.E = E;
   a.k = k;
-  chunk_plan(T, &a.chunk, &a.nb);
+  chunk_plan(T, a.P * H * elem_bytes(dtype), &a.chunk, &a.nb);
   a.status = reinterpret_cast<int32_t*>(ws);
   a.totals = ws ? a.status + 4 : nullptr;
   a.hist = ws ? a.totals + E : nullptr;
