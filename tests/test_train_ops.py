@@ -96,6 +96,38 @@ def test_dispatch_and_combine(moe, T, H, E, k, kind, dtype):
         close(ds, wds, (H + 8) * 2.0 ** -24 * mag, "dscales")
 
 
+# Rows on 2, 4 and 8 bytes; a segment of a warp full, cut and alone; few and many warps' worth.
+ODD_ROWS = [(4200, 301, 64, 3, "dropped"), (900, 514, 16, 5, "dropped"), (2100, 130, 8, 2, "plain"),
+            (40, 2051, 8, 8, "dropped"), (600, 132, 7, 4, "dropped"), (2, 1, 3, 8, "plain"), (1100, 67, 5, 8, "one")]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,H,E,k,kind", ODD_ROWS)
+def test_rows_of_any_width(moe, T, H, E, k, kind, dtype):
+    test_dispatch_and_combine(moe, T, H, E, k, kind, dtype)
+
+
+@pytest.mark.parametrize("H", [5, 131, 262])
+def test_infinities_in_rows_of_any_width_stay_in_their_token(moe, H):
+    """Neighbouring rows share words, not values."""
+    T, E, k = 50, 6, 3
+    ids = make_ids(T, E, k, "dropped", H)
+    inv, _ = ref.sort_slots(ids, E)
+    inv_gpu = torch.from_numpy(inv.astype(np.int32)).cuda()
+    x, rows, dy = randn((T, H), "bf16", 1), randn((T * k, H), "bf16", 2), randn((T, H), "bf16", 3)
+    clean = [moe.moe_dispatch_rows(x, inv_gpu), moe.moe_combine(rows, inv_gpu), *moe.moe_combine_backward(dy, rows, inv_gpu)]
+    hit = 7
+    mine = inv[hit][inv[hit] >= 0]
+    x[hit], dy[hit], rows[mine] = float("inf"), float("nan"), float("inf")
+    got = [moe.moe_dispatch_rows(x, inv_gpu), moe.moe_combine(rows, inv_gpu), *moe.moe_combine_backward(dy, rows, inv_gpu)]
+    other_rows = torch.ones(T * k, dtype=torch.bool)
+    other_rows[mine] = False
+    other_tokens = torch.arange(T) != hit
+    for a, b, keep in zip(clean, got, (other_rows, other_tokens, other_rows, other_tokens)):
+        assert torch.equal(a.cpu()[keep], b.cpu()[keep])
+    assert len(mine) and not torch.isfinite(got[0].cpu()[mine]).any() and not torch.isfinite(got[1].cpu()[hit]).any()
+
+
 def test_combine_gradient_against_differences(moe):
     T, H, E, k = 5, 24, 4, 3
     ids = make_ids(T, E, k, "dropped", 9)
@@ -269,6 +301,12 @@ def test_checkpoint_of_infinities_and_nans(moe, I):
     bad = np.repeat(hit[:, :nb], 32, 1)[:, :I] | np.repeat(hit[:, nb:], 32, 1)[:, :I]
     assert np.array_equal(np.isnan(n64(h)), bad)
     assert np.isfinite(n64(dgu)[:, :I][~bad]).all() and np.isnan(n64(dgu)[:, :I][bad]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,I", [(3, 127), (2500, 70), (2, 129), (5, 255), (4, 257), (70, 2049), (1, 515), (40, 300)])
+def test_swiglu_checkpoint_of_any_width(moe, R, I, dtype):
+    test_swiglu_checkpoint(moe, R, I, dtype)
 
 
 def test_swiglu_gradient_against_differences(moe):
