@@ -82,7 +82,8 @@ struct ExpertsArgs {
   int32_t f16;              // 16-bit type: 0 bf16, 1 f16
   int32_t add;              // dw, f32: add to what is there
   int32_t split;            // log2 of the parts that the contraction is cut into
-  void* out;                // forward, dx: the result rows (masked stores)
+  void* out;                // forward, dx: the result rows (masked stores); dw: dw (rows of odd
+                            // multiples of 16 bytes)
   float* part;              // forward, dx with f32 results: [parts][R][m_ext] sums of the parts
   const CUtensorMap* maps;  // dw: [2][E] maps of dy and of x, cut off at each expert's end
   int32_t* status;          // or NULL
@@ -335,6 +336,85 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, bool f16) {
   }
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// dw in 16 bits where its rows are an odd number of 16 bytes long, so that every other one starts in the
+// middle of a sector (32 bytes): parts of sectors are what costs L2, and each box below would have two
+// a row. So in those rows a step's 64 columns are those from 8 on, the last 8 being the next step's
+// first, and the tile's first 8 are stored by themselves; steps go out through shared memory by
+// plain stores. 54 experts of 2048 x 4104, 128 rows each: 172 us, by boxes 266 (of 2048 x 4096:
+// 160); 16 rows each 193 and 247.
+template <typename Done>
+__device__ __forceinline__ void store_dw_odd(uint32_t tb, const Tile& t, int q, int lane, uint8_t* buf,
+                                             const ExpertsArgs& a, Done&& done) {
+  const int cols = t.n_here, rows = t.m_here - 32 * q;   // (cols % 8 == 0)
+  if (rows <= 0) {
+    done();
+    return;
+  }
+  const bool f16 = a.f16 != 0;
+  uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                  (static_cast<int64_t>(t.g) * a.m_ext + t.m0 + 32 * q) * a.n_ext + t.n0;
+  const int odd0 = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 4 & 1);   // of the first row
+  const bool odd = ((odd0 ^ lane) & 1) != 0;
+  uint4* mine = reinterpret_cast<uint4*>(buf + lane * 128);
+#pragma unroll 1
+  for (int c0 = 0; c0 < cols; c0 += 64) {
+    uint32_t v[2][32], next[8] = {};
+    tmem_issue(tb + c0, v[0]);
+    tmem_issue(tb + c0 + 32, v[1]);
+    if (c0 + 64 < cols) tmem_issue(tb + c0 + 64, next);
+    tmem_wait();
+    tmem_ready(v[0]);
+    tmem_ready(v[1]);
+    tmem_ready(next);
+    if (c0 + 64 >= cols) done();
+    uint32_t w[36];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      w[i] = pack_16bit(__uint_as_float(v[i / 16][2 * i % 32]),
+                        __uint_as_float(v[i / 16][2 * i % 32 + 1]), f16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[32 + i] = pack_16bit(__uint_as_float(next[2 * i]), __uint_as_float(next[2 * i + 1]), f16);
+    if (c0 == 0 && odd && lane < rows)
+      *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(lane) * a.n_ext) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    __syncwarp();   // the step before has been read out
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 o;
+      o.x = odd ? w[4 * i + 4] : w[4 * i];
+      o.y = odd ? w[4 * i + 5] : w[4 * i + 1];
+      o.z = odd ? w[4 * i + 6] : w[4 * i + 2];
+      o.w = odd ? w[4 * i + 7] : w[4 * i + 3];
+      mine[i ^ (lane & 7)] = o;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const int c = c0 + 8 * ((lane & 7) + ((odd0 ^ r) & 1));
+      if (r < rows && c < cols)
+        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * a.n_ext + c) =
+            *reinterpret_cast<const uint4*>(buf + r * 128 + (((lane ^ r) & 7) << 4));
+    }
+  }
+}
+
+// The zeros of an expert without rows for such a dw, by rows: all of dw[g] is zeros, so that the pieces of
+// rows that start in the middle of a sector are moved on by 8 columns, into the next tile's. 54 experts
+// of 2048 x 4104 bf16, four rows in all: 160 us, by rows alone 199, by boxes 239 (of 2048 x 4096: 144).
+__device__ __forceinline__ void store_dw_zeros(const Tile& t, int q, int lane, const ExpertsArgs& a) {
+  const int rows = min(32, t.m_here - 32 * q);
+  uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                  (static_cast<int64_t>(t.g) * a.m_ext + t.m0 + 32 * q) * a.n_ext;
+  for (int r = 0; r < rows; ++r, dst += a.n_ext) {
+    const int on = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 4 & 1) * 8;   // (n_ext % 8 == 0)
+    const int c = t.n0 + on + 8 * lane;
+    if (8 * lane < t.n_here && c < a.n_ext) *reinterpret_cast<uint4*>(dst + c) = uint4{};
+    if (c == 8 && on) *reinterpret_cast<uint4*>(dst) = uint4{};
+  }
 }
 
 // dw: one warp's part of a tile, 32 rows of dw[g] (TMEM lane quarter q) by its columns, in boxes of
@@ -722,8 +802,12 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
           else mbar_arrive_remote(lead_tempty + 8u * acc);
         }
       };
-      if constexpr (kMode == kDw)
-        store_dw<kF32>(tb, t, q, lane, my_box, &map_out, a, done);
+      if constexpr (kMode == kDw && !kF32) {
+        if (!(a.n_ext & 8)) store_dw<false>(tb, t, q, lane, my_box, &map_out, a, done);
+        else if (zeros) store_dw_zeros(t, q, lane, a);
+        else store_dw_odd(tb, t, q, lane, my_box, a, done);
+      } else if constexpr (kMode == kDw)
+        store_dw<true>(tb, t, q, lane, my_box, &map_out, a, done);
       else if constexpr (kF32)
         store_part(tb, t, q, lane, a, done);
       else
@@ -982,6 +1066,7 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
   a.m_ext = N;
   a.n_ext = K;
   a.f16 = dtype == MOE_DTYPE_F16;
+  a.out = dw;
   a.add = add && split == 0;
   a.split = split;
   a.status = reinterpret_cast<int32_t*>(ws);

@@ -511,6 +511,13 @@ __device__ __forceinline__ void tmem_issue(uint32_t ta, uint32_t (&r)[32]) {
       : "r"(ta)
       : "memory");
 }
+__device__ __forceinline__ void tmem_issue(uint32_t ta, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(ta)
+               : "memory");
+}
 // 16x256b.x4: lanes 0-15 of `ta`, 32 columns. In each 8 x 8 block of (lane, column) a thread holds two
 // neighbouring columns of one lane, the layout of a matrix fragment: r[4 i + 2 s + c] is lane
 // 8 s + t / 4, column 8 i + 2 (t % 4) + c of thread t.

@@ -431,6 +431,23 @@ def test_split_contractions(moe, R, E, K, N, kind, dtype):
     assert torch.equal(sum_, start + dw)
 
 
+@pytest.mark.parametrize("start", [8, 16])
+@pytest.mark.parametrize("K", [8, 24, 72, 248, 264, 328, 776])
+def test_dw_writes_its_own_elements_only(moe, K, start):
+    """Rows of an odd number of 16 bytes, in a dw that starts on 16 or on 32 bytes; experts without
+    rows beside others."""
+    R, E, N = 150, 6, 136
+    off = np.array([0, 0, 70, 71, 71, 140, 140], np.int32)
+    offsets = torch.from_numpy(off).cuda()
+    x, dy = randn((R, K), "bf16", 1), randn((R, N), "bf16", 2)
+    buf = torch.full((E * N * K + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    dw = buf[start:start + E * N * K].view(E, N, K)
+    moe.moe_experts_matmul_dw(dy, x, offsets, dw=dw)
+    assert (buf[:start] == 7).all() and (buf[start + E * N * K:] == 7).all()
+    want, mag = ref.experts_matmul_dw(n64(dy), n64(x), off), ref.experts_matmul_dw(np.abs(n64(dy)), np.abs(n64(x)), off)
+    close(dw, want, U["bf16"] * np.abs(want) + 70 * 2.0 ** -23 * mag * (1 + U["bf16"]) + TINY["bf16"], "dw")
+
+
 def test_a_neighbours_rows_do_not_reach_dw(moe):
     """Infinities and NaNs in the rows right behind (and before) an expert's leave its dw alone."""
     R, E, K, N = 200, 3, 64, 128
@@ -494,6 +511,18 @@ def test_products_over_two_to_the_31_elements(moe):
     dy, x = randn((R, N), "bf16", 3), randn((R, K), "bf16", 4)
     dw = moe.moe_experts_matmul_dw(dy, x, torch.from_numpy(off).cuda())
     for e in (0, 194, 195, 199):
+        a, b = off[e], off[e + 1]
+        want = n64(dy[a:b]).T @ n64(x[a:b])
+        mag = np.abs(n64(dy[a:b])).T @ np.abs(n64(x[a:b]))
+        close(dw[e], want, U["bf16"] * np.abs(want) + (b - a) * 2.0 ** -23 * mag * 1.01, "dw")
+
+
+def test_dw_of_odd_rows_over_two_to_the_31_elements(moe):
+    E, N, K, R = 200, 4096, 2696, 398         # the last expert has no rows
+    off = np.minimum(np.arange(E + 1) * 2, R).astype(np.int32)
+    dy, x = randn((R, N), "bf16", 3), randn((R, K), "bf16", 4)
+    dw = moe.moe_experts_matmul_dw(dy, x, torch.from_numpy(off).cuda())
+    for e in (0, 194, 195, 198, 199):
         a, b = off[e], off[e + 1]
         want = n64(dy[a:b]).T @ n64(x[a:b])
         mag = np.abs(n64(dy[a:b])).T @ np.abs(n64(x[a:b]))
