@@ -12,8 +12,8 @@
 // token row a dispatch reads (or a combine writes) crosses HBM once and not k times. Sums run
 // in fp32 in slot order, by one thread: no atomics, the same result on every run.
 // Measured (bf16): dispatch and combine of 8192 x 4096, k = 4, 61 and 53 us (5.5 and 6.4 TB/s); the
-// gradients of 8192 x 7168, k = 8, 305 and 162 us (6.5 TB/s each, 0.97 of a copy's rate). A decode
-// batch (64 x 2048, k = 8) takes 2.8 and 2.4 us, which is a launch's.
+// gradients of 8192 x 7168, k = 8, 291 and 162 us (6.9 and 6.5 TB/s, as fast as a copy). A decode
+// batch (64 x 2048, k = 8) takes 3.3 and 2.8 us, which is a launch's.
 #include <algorithm>
 #include <cstdint>
 
@@ -447,96 +447,12 @@ combine_narrow_kernel(const T* __restrict__ rows, const int32_t* __restrict__ in
   }
 }
 
-// kWarps warps per token: each vector of dy[t] is read once and meets the vectors of the
-// token's kept rows; the k dot products are summed over the lanes (and warps) in fixed order.
-template <typename T, int kSlots, int kWarps>
-__global__ void __launch_bounds__(kSortThreads)
-combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
-                    const int32_t* __restrict__ inv, const float* __restrict__ scales,
-                    int64_t n_tok, int k, int nvec, T* __restrict__ drows,
-                    float* __restrict__ dscales) {
-  using V = Vec<T, 16>;
-  constexpr int kToks = kSortWarps / kWarps;   // tokens a block has at a time
-  __shared__ float s_dot[kWarps > 1 ? kSortWarps : 1][kSlots];
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = warp % kWarps;
-  const int64_t P = n_tok * k;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kToks; t0 < n_tok;
-       t0 += static_cast<int64_t>(gridDim.x) * kToks) {
-    const int64_t t = t0 + warp / kWarps;
-    float dot[kSlots] = {};
-    if (t < n_tok) {
-      int32_t row[kSlots];
-      float s[kSlots];
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        row[j] = INT32_MIN;   // nothing to write
-        s[j] = 0.0f;
-        if (j < k) {
-          const int32_t p = __ldg(inv + t * k + j);
-          if ((p < 0 ? ~p : p) < P) row[j] = p;
-          s[j] = scales ? __ldg(scales + t * k + j) : 1.0f;
-        }
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(dy) + t * nvec;
-      for (int v = sub * 32 + lane; v < nvec; v += 32 * kWarps) {
-        uint4 val[kSlots];
-        const uint4 d = __ldg(src + v);
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (row[j] >= 0)
-            val[j] = __ldg(reinterpret_cast<const uint4*>(rows) + static_cast<int64_t>(row[j]) * nvec + v);
-        float df[V::kN];
-        V::unpack(d, df);
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          if (row[j] == INT32_MIN) continue;
-          uint4 out{};
-          if (row[j] >= 0) {
-            float f[V::kN], o[V::kN];
-            V::unpack(val[j], f);
-#pragma unroll
-            for (int c = 0; c < V::kN; ++c) {
-              dot[j] = fmaf(df[c], f[c], dot[j]);
-              o[c] = s[j] * df[c];
-            }
-            out = V::pack(o);
-          }
-          const int64_t r = row[j] < 0 ? ~row[j] : row[j];
-          __stcs(reinterpret_cast<uint4*>(drows) + r * nvec + v, out);
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
-    if (kWarps == 1) {
-      if (t < n_tok && lane == 0)
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (j < k) dscales[t * k + j] = dot[j];
-    } else {
-      if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) s_dot[warp][j] = dot[j];
-      __syncthreads();
-      if (t < n_tok && sub == 0 && lane < k) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_dot[warp + w][lane];
-        dscales[t * k + lane] = sum;
-      }
-      __syncthreads();
-    }
-  }
-}
-
-// The same for rows that do not start on 16 bytes, in vectors of kBytes: kWarps warps to a slot (dy[t]
-// comes from L1 to the second and later ones), a warp kU times 32 neighbouring vectors at a time (4096
-// tokens, k = 6, bf16: H = 7167 175 us, H = 7164 129; the form above with such vectors 212 for either).
+// kWarps warps to a slot (dy[t] comes from L1 or L2 to the second and later ones of its token), a warp kU
+// times 32 neighbouring vectors of kBytes at a time, unchecked where all of them exist (kFull). The dot
+// product is summed in a thread, over the lanes and over the warps, in that order. bf16: 8192 tokens of
+// 7168, k = 8, 291 us, of 2048 83, of 256 17; 4096 of 7167, k = 6, 176, of 7164 129. (A token's slots
+// together, dy read once, its dot products side by side: 306, 113, 24, 212 and 212, as fewer loads were
+// in flight and more instructions spent on addresses.)
 template <typename T, int kBytes, int kU, bool kFull>
 __device__ __forceinline__ float combine_grad_segment(const T* dy, const T* rows, float s, int nvec,
                                                       int v, T* drows) {
@@ -569,7 +485,7 @@ __device__ __forceinline__ float combine_grad_segment(const T* dy, const T* rows
 
 template <typename T, int kBytes, int kU, int kWarps>
 __global__ void __launch_bounds__(kSortThreads)
-combine_grad_narrow_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
+combine_grad_kernel(const T* __restrict__ dy, const T* __restrict__ rows,
                            const int32_t* __restrict__ inv, const float* __restrict__ scales,
                            int64_t n_tok, int k, int nvec, T* __restrict__ drows,
                            float* __restrict__ dscales) {
@@ -650,25 +566,6 @@ cudaError_t combine_t(const void* rows, const int32_t* inv, const float* scales,
                     static_cast<const T*>(rows), inv, scales, n_tok, k, nvec, static_cast<T*>(y));
 }
 
-template <typename T, int kSlots>
-cudaError_t combine_grad_t(const void* dy, const void* rows, const int32_t* inv,
-                           const float* scales, int64_t n_tok, int H, int k, void* drows,
-                           float* dscales, cudaStream_t s) {
-  const int nvec = H / Vec<T, 16>::kN;
-  // A warp to a token where the tokens alone fill the GPU and a row is short, else a block: 8192 tokens,
-  // k = 8, H = 256 bf16 25 us a warp each and 70 a block each, H = 7168 368 and 306; 256 tokens, H =
-  // 2048 9.3 and 4.3.
-  if (nvec <= 256 && n_tok >= 1024)
-    return launch_pdl(combine_grad_kernel<T, kSlots, 1>,
-                      dim3(grid_of((n_tok + kSortWarps - 1) / kSortWarps, 32)), dim3(kSortThreads),
-                      0, s, static_cast<const T*>(dy), static_cast<const T*>(rows), inv, scales,
-                      n_tok, k, nvec, static_cast<T*>(drows), dscales);
-  return launch_pdl(combine_grad_kernel<T, kSlots, kSortWarps>, dim3(grid_of(n_tok, 32)),
-                    dim3(kSortThreads), 0, s, static_cast<const T*>(dy),
-                    static_cast<const T*>(rows), inv, scales, n_tok, k, nvec,
-                    static_cast<T*>(drows), dscales);
-}
-
 template <typename T, int kBytes, int kU, int kJ>
 cudaError_t combine_narrow_u(const void* rows, const int32_t* inv, const float* scales,
                              int64_t n_tok, int nvec, int k, void* y, cudaStream_t s) {
@@ -691,42 +588,55 @@ cudaError_t combine_narrow_t(const void* rows, const int32_t* inv, const float* 
   return combine_narrow_u<T, kBytes, 8, 2>(rows, inv, scales, n_tok, nvec, k, y, s);
 }
 
-template <typename T, int kBytes>
-cudaError_t combine_grad_narrow_t(const void* dy, const void* rows, const int32_t* inv,
-                                  const float* scales, int64_t n_tok, int H, int k, void* drows,
-                                  float* dscales, cudaStream_t s) {
-  const int nvec = H / Vec<T, kBytes>::kN;
+template <typename T, int kBytes, int kU>
+cudaError_t combine_grad_u(const void* dy, const void* rows, const int32_t* inv,
+                           const float* scales, int64_t n_tok, int k, int nvec, void* drows,
+                           float* dscales, cudaStream_t s) {
   const int64_t P = n_tok * k;
   auto run = [&](auto* kernel, int64_t blocks) {
     return launch_pdl(kernel, dim3(grid_of(blocks, 32)), dim3(kSortThreads), 0, s,
                       static_cast<const T*>(dy), static_cast<const T*>(rows), inv, scales, n_tok, k,
                       nvec, static_cast<T*>(drows), dscales);
   };
-  // A warp to a slot where the slots alone fill the GPU, or nearly so with short rows, else a block: k =
-  // 8 bf16, 512 tokens of 7167 45 us a warp each and 33 a block each, 4000 tokens of 333 (k = 4) 7.0 and
-  // 18, 256 tokens of 1001 4.2 and 4.6; 4096 tokens of 7167, k = 6, 175 and 183.
-  if (P >= 8192 || (nvec <= 1024 && P >= 2048))
-    return run(combine_grad_narrow_kernel<T, kBytes, 4, 1>, (P + kSortWarps - 1) / kSortWarps);
-  return run(combine_grad_narrow_kernel<T, kBytes, 4, kSortWarps>, P);
+  // A warp to a slot where it holds a row, where the slots alone fill the GPU, or nearly so with rows that
+  // are not long, else a block: k = 8 bf16, 512 tokens of 7167 45 us a warp each and 33 a block each, of
+  // 7168 22 and 24, 256 tokens of 1001 4.2 and 4.6, 8192 of 2048 84 and 138; 4000 of 333 (k = 4) 7 and 18.
+  if constexpr (kU == 4) {
+    if (nvec > 32 * kU && P < (nvec <= 1024 ? 2048 : 8192))
+      return run(combine_grad_kernel<T, kBytes, kU, kSortWarps>, P);
+  }
+  return run(combine_grad_kernel<T, kBytes, kU, 1>, (P + kSortWarps - 1) / kSortWarps);
 }
 
-// Calls f.wide<T, slots>() with k rounded up where H puts every row on 16 bytes, else f.narrow<T,
-// bytes>(): 4 bytes where rows start on them.
+template <typename T, int kBytes>
+cudaError_t combine_grad_t(const void* dy, const void* rows, const int32_t* inv,
+                           const float* scales, int64_t n_tok, int H, int k, void* drows,
+                           float* dscales, cudaStream_t s) {
+  const int nvec = H / Vec<T, kBytes>::kN;
+  // As many vectors as a row has for a warp, up to four: 8192 tokens bf16, H = 256, k = 8 17.0 us with
+  // one, 29.6 with four; H = 512, k = 4 15.1 with two, 15.9 and 19.4; H = 2048, k = 8 83 with four, 88
+  // with one.
+  if (nvec <= 32)
+    return combine_grad_u<T, kBytes, 1>(dy, rows, inv, scales, n_tok, k, nvec, drows, dscales, s);
+  if (nvec <= 64)
+    return combine_grad_u<T, kBytes, 2>(dy, rows, inv, scales, n_tok, k, nvec, drows, dscales, s);
+  return combine_grad_u<T, kBytes, 4>(dy, rows, inv, scales, n_tok, k, nvec, drows, dscales, s);
+}
+
+// Calls f<T, bytes>() for the type and the vectors of its rows: 16 bytes where all rows start on them,
+// 4 where they start on these, else an element.
 template <typename F>
-cudaError_t by_form(int dtype, int H, int k, const F& f) {
-  auto form = [&](auto t) {
+cudaError_t by_width(int dtype, int H, const F& f) {
+  auto width = [&](auto t) {
     using T = decltype(t);
     const int64_t row = static_cast<int64_t>(H) * sizeof(T);
-    if (row % 4 != 0) return f.template narrow<T, static_cast<int>(sizeof(T))>();
-    if (row % 16 != 0) return f.template narrow<T, 4>();
-    if (k == 1) return f.template wide<T, 1>();
-    if (k == 2) return f.template wide<T, 2>();
-    if (k <= 4) return f.template wide<T, 4>();
-    return f.template wide<T, 8>();
+    if (row % 16 == 0) return f.template operator()<T, 16>();
+    if (row % 4 == 0) return f.template operator()<T, 4>();
+    return f.template operator()<T, static_cast<int>(sizeof(T))>();
   };
-  if (dtype == MOE_DTYPE_BF16) return form(__nv_bfloat16());
-  if (dtype == MOE_DTYPE_F16) return form(__half());
-  return form(float());
+  if (dtype == MOE_DTYPE_BF16) return width(__nv_bfloat16());
+  if (dtype == MOE_DTYPE_F16) return width(__half());
+  return width(float());
 }
 
 struct CombineCall {
@@ -737,13 +647,16 @@ struct CombineCall {
   int H, k;
   void* y;
   cudaStream_t s;
-  template <typename E, int kSlots>
-  cudaError_t wide() const {
-    return combine_t<E, kSlots>(rows, inv, scales, T, H, k, y, s);
-  }
   template <typename E, int kBytes>
-  cudaError_t narrow() const {
-    return combine_narrow_t<E, kBytes>(rows, inv, scales, T, H, k, y, s);
+  cudaError_t operator()() const {
+    if constexpr (kBytes < 16) {
+      return combine_narrow_t<E, kBytes>(rows, inv, scales, T, H, k, y, s);
+    } else {
+      return k == 1   ? combine_t<E, 1>(rows, inv, scales, T, H, k, y, s)
+             : k == 2 ? combine_t<E, 2>(rows, inv, scales, T, H, k, y, s)
+             : k <= 4 ? combine_t<E, 4>(rows, inv, scales, T, H, k, y, s)
+                      : combine_t<E, 8>(rows, inv, scales, T, H, k, y, s);
+    }
   }
 };
 
@@ -757,13 +670,9 @@ struct CombineGradCall {
   void* drows;
   float* dscales;
   cudaStream_t s;
-  template <typename E, int kSlots>
-  cudaError_t wide() const {
-    return combine_grad_t<E, kSlots>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
-  }
   template <typename E, int kBytes>
-  cudaError_t narrow() const {
-    return combine_grad_narrow_t<E, kBytes>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
+  cudaError_t operator()() const {
+    return combine_grad_t<E, kBytes>(dy, rows, inv, scales, T, H, k, drows, dscales, s);
   }
 };
 
@@ -846,7 +755,7 @@ moe_status launch_dispatch_rows(const void* x, const int32_t* inv, int64_t T, in
 
 moe_status launch_combine(const void* rows, const int32_t* inv, const float* scales, int64_t T,
                           int H, int k, int dtype, void* y, cudaStream_t s) {
-  const cudaError_t err = by_form(dtype, H, k, CombineCall{rows, inv, scales, T, H, k, y, s});
+  const cudaError_t err = by_width(dtype, H, CombineCall{rows, inv, scales, T, H, k, y, s});
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "combine launch: %s", cudaGetErrorString(err));
   return MOE_OK;
@@ -856,7 +765,7 @@ moe_status launch_combine_backward(const void* dy, const void* rows, const int32
                                    const float* scales, int64_t T, int H, int k, int dtype,
                                    void* drows, float* dscales, cudaStream_t s) {
   const cudaError_t err =
-      by_form(dtype, H, k, CombineGradCall{dy, rows, inv, scales, T, H, k, drows, dscales, s});
+      by_width(dtype, H, CombineGradCall{dy, rows, inv, scales, T, H, k, drows, dscales, s});
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "combine_backward launch: %s", cudaGetErrorString(err));
   return MOE_OK;
