@@ -92,15 +92,16 @@ route_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ 
         const float a = z > 0.0f ? ex / z : 0.0f;
         d = a * (d - sum_warp(d * a));
       } else {
-        // sigma(l) and sigma(l) (1 - sigma(l)) from exp(-|l|): no cancellation at either end
+        // sigma(l) (1 - sigma(l)) from exp(-|l|): no cancellation at either end
         const float ex = live ? expf(-fabsf(l)) : 0.0f;
         const float r = 1.0f / (1.0f + ex);
-        const float a = live ? (l >= 0.0f ? r : ex * r) : 0.0f;
         const float slope = ex * r * r;
         if (kForm == kSigmoidSum) {
+          // Where one weight is nearly the sum, d less its share cancels: sigma and the share are rounded
+          // as few times as can be (far below, where exp(-l) ends, sigma is exp(l)).
+          const float a = !live ? 0.0f : l > -80.0f ? 1.0f / (1.0f + expf(-l)) : ex * r;
           const float sum = sum_warp(a) + eps;
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-          d = c * (d - sum_warp(d * a) * inv) * inv;
+          d = sum > 0.0f ? c * (d - sum_warp(d * a) / sum) / sum : 0.0f;
         }
         d *= slope;
       }
