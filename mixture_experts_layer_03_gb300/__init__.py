@@ -4,6 +4,10 @@ Argument marshalling only: every step runs in the library's CUDA kernels. PyTorc
 provides device memory and streams. The names mirror the C ABI in include/moe.h.
 Importing this module fails loudly when the compiled library is missing; there is
 no fallback implementation.
+
+`stream` (a torch stream, or a handle) is the stream of the launch, the current one by
+default. What a call allocates, results and workspace, is allocated on that stream; the
+order between it and other streams' work on the arguments and results is the caller's.
 """
 from __future__ import annotations
 
@@ -177,6 +181,27 @@ def _stream(stream) -> int:
             return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _new(shape, dtype, device, stream, result: bool = True) -> torch.Tensor:
+    """Memory that a call launched on `stream` writes. The caching allocator hands a block out again
+    in the order of the stream that it was allocated on, so that must be the launch's: one of the
+    caller's current stream could still be in use there by work that the launch does not wait for,
+    and, dropped on return (a workspace), would be given out again while the kernels run. A result
+    is used on the caller's current stream too, and is held until that is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, here = _stream(stream), _stream(None)
+    if handle == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    # (0, which ExternalStream takes for no handle, and 1 are names of the default stream.)
+    where = (torch.cuda.ExternalStream(handle, device) if handle > 1
+             else torch.cuda.default_stream(device))
+    with torch.cuda.stream(where):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None):
@@ -468,12 +493,13 @@ class Scratch:
         return self.buf.numel()
 
 
-def alloc_dispatch_scratch(T: int, num_experts: int, top_k: int, device="cuda") -> Scratch:
-    """Workspace of moe_dispatch for T tokens."""
+def alloc_dispatch_scratch(T: int, num_experts: int, top_k: int, device="cuda",
+                           stream=None) -> Scratch:
+    """Workspace of moe_dispatch for T tokens, for calls on `stream` (None: the current one)."""
     n = _lib.moe_dispatch_workspace_bytes(T, num_experts, top_k)
     if n == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_dispatch_workspace_bytes")
-    return Scratch(torch.empty(n, dtype=torch.uint8, device=device))
+    return Scratch(_new(n, torch.uint8, device, stream, result=False))
 
 
 def alloc_experts_scratch(num_experts: int, rows: int = 0, N: int = 8, K: int = 8,
@@ -489,11 +515,12 @@ def alloc_experts_scratch(num_experts: int, rows: int = 0, N: int = 8, K: int = 
     return scratch
 
 
-def _split_scratch(product: int, R: int, E: int, N: int, K: int, device) -> Optional[Scratch]:
+def _split_scratch(product: int, R: int, E: int, N: int, K: int, device,
+                   stream) -> Optional[Scratch]:
     """A workspace for one call whose contraction is split, else None. (Its status word is not
     read by anyone.)"""
     n = _lib.moe_experts_split_bytes(product, R, E, N, K)
-    return Scratch(torch.empty(n, dtype=torch.uint8, device=device)) if n else None
+    return Scratch(_new(n, torch.uint8, device, stream, result=False)) if n else None
 
 
 # The checks below are on the path of calls that take a few microseconds on the device: one
@@ -518,10 +545,11 @@ def _shaped(t: torch.Tensor, name: str, shape: tuple, dtype) -> torch.Tensor:
     raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
 
 
-def _like(t: torch.Tensor, out: Optional[torch.Tensor], name: str, shape: tuple) -> torch.Tensor:
+def _like(t: torch.Tensor, out: Optional[torch.Tensor], name: str, shape: tuple,
+          stream) -> torch.Tensor:
     """`out`, of just this shape and t's type, or a new tensor. (t.new_empty() goes through torch's
     dispatcher twice: 2 us more between two launches.)"""
-    return torch.empty(shape, dtype=t.dtype, device=t.device) if out is None else _shaped(
+    return _new(shape, t.dtype, t.device, stream) if out is None else _shaped(
         out, name, shape, t.dtype)
 
 
@@ -548,11 +576,11 @@ def moe_dispatch(x, ids, num_experts: int, x_perm=None, inv=None, offsets=None,
     if _slots(ids, "ids")[0] != T:
         raise ValueError(f"ids must have {T} rows, got {tuple(ids.shape)}")
     k = ids.shape[1]
-    x_perm = _like(x, x_perm, "x_perm", (T * k, H))
-    inv = _like(ids, inv, "inv", (T, k))
-    offsets = _like(ids, offsets, "offsets", (num_experts + 1,))
+    x_perm = _like(x, x_perm, "x_perm", (T * k, H), stream)
+    inv = _like(ids, inv, "inv", (T, k), stream)
+    offsets = _like(ids, offsets, "offsets", (num_experts + 1,), stream)
     if scratch is None and T * k > MOE_DISPATCH_SMALL_SLOTS:
-        scratch = alloc_dispatch_scratch(T, num_experts, k, x.device)
+        scratch = alloc_dispatch_scratch(T, num_experts, k, x.device, stream)
     _check(_lib.moe_dispatch(x.data_ptr(), ids.data_ptr(), T, H, num_experts, k, dt,
                              x_perm.data_ptr(), inv.data_ptr(),
                              offsets.data_ptr(), scratch.ptr if scratch else None,
@@ -567,7 +595,7 @@ def moe_dispatch_rows(x, inv, x_perm=None, stream=None):
     H = x.shape[1]
     if x.shape[0] != T:
         raise ValueError(f"x must have {T} rows, got {tuple(x.shape)}")
-    x_perm = _like(x, x_perm, "x_perm", (T * k, H))
+    x_perm = _like(x, x_perm, "x_perm", (T * k, H), stream)
     _check(_lib.moe_dispatch_rows(x.data_ptr(), inv.data_ptr(), T, H, k, dt, x_perm.data_ptr(), _stream(stream)),
            "moe_dispatch_rows")
     return x_perm
@@ -579,7 +607,7 @@ def moe_dispatch_backward(dx_perm, inv, dx=None, stream=None):
     T, k = _slots(inv)
     H = dx_perm.shape[1]
     _shaped(dx_perm, "dx_perm", (T * k, H), dx_perm.dtype)
-    dx = _like(dx_perm, dx, "dx", (T, H))
+    dx = _like(dx_perm, dx, "dx", (T, H), stream)
     _check(_lib.moe_dispatch_backward(dx_perm.data_ptr(), inv.data_ptr(), T, H, k, dt, dx.data_ptr(),
                                       _stream(stream)), "moe_dispatch_backward")
     return dx
@@ -594,7 +622,7 @@ def moe_combine(rows, inv, scales=None, y=None, stream=None):
     _shaped(rows, "rows", (T * k, H), rows.dtype)
     if scales is not None:
         _shaped(scales, "scales", (T, k), torch.float32)
-    y = _like(rows, y, "y", (T, H))
+    y = _like(rows, y, "y", (T, H), stream)
     _check(_lib.moe_combine(rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt, y.data_ptr(),
                             _stream(stream)), "moe_combine")
     return y
@@ -609,8 +637,8 @@ def moe_combine_backward(dy, rows, inv, scales=None, drows=None, dscales=None, s
     _shaped(rows, "rows", (T * k, H), dy.dtype)
     if scales is not None:
         _shaped(scales, "scales", (T, k), torch.float32)
-    drows = _like(rows, drows, "drows", (T * k, H))
-    dscales = (torch.empty((T, k), dtype=torch.float32, device=dy.device) if dscales is None
+    drows = _like(rows, drows, "drows", (T * k, H), stream)
+    dscales = (_new((T, k), torch.float32, dy.device, stream) if dscales is None
                else _shaped(dscales, "dscales", (T, k), torch.float32))
     _check(_lib.moe_combine_backward(dy.data_ptr(), rows.data_ptr(), inv.data_ptr(), _ptr(scales), T, H, k, dt,
                                      drows.data_ptr(), dscales.data_ptr(), _stream(stream)),
@@ -677,10 +705,9 @@ def moe_swiglu_ckpt(gu, h=None, ckpt=None, stream=None):
     if I2 % 2:
         raise ValueError(f"gu must have an even number of columns, got {I2}")
     I = I2 // 2
-    h = _like(gu, h, "h", (R, I))
+    h = _like(gu, h, "h", (R, I), stream)
     if ckpt is None:
-        ckpt = Checkpoint(torch.empty(Checkpoint.nbytes(R, I), dtype=torch.uint8, device=gu.device),
-                          R, I)
+        ckpt = Checkpoint(_new(Checkpoint.nbytes(R, I), torch.uint8, gu.device, stream), R, I)
     q, qs = _ckpt_ptrs(ckpt, R, I)
     _check(_lib.moe_swiglu_ckpt(gu.data_ptr(), R, I, dt, h.data_ptr(), q, qs, _stream(stream)),
            "moe_swiglu_ckpt")
@@ -692,11 +719,11 @@ def moe_swiglu_ckpt_backward(dh, ckpt, dgu=None, h=None, want_h: bool = False, s
     dt = _typed(dh, "dh", 2)
     R, I = dh.shape
     q, qs = _ckpt_ptrs(ckpt, R, I)
-    dgu = _like(dh, dgu, "dgu", (R, 2 * I))
+    dgu = _like(dh, dgu, "dgu", (R, 2 * I), stream)
     if h is not None:
         _shaped(h, "h", (R, I), dh.dtype)
     elif want_h:
-        h = torch.empty_like(dh)
+        h = _new((R, I), dh.dtype, dh.device, stream)
     _check(_lib.moe_swiglu_ckpt_backward(dh.data_ptr(), q, qs, R, I, dt, dgu.data_ptr(), _ptr(h),
                                          _stream(stream)), "moe_swiglu_ckpt_backward")
     return dgu, h
@@ -713,9 +740,9 @@ def moe_experts_matmul(x, w, offsets, y=None, scratch: Optional[Scratch] = None,
     _shaped(w, "w", (w.shape[0], w.shape[1], x.shape[1]) if w.dim() == 3 else (0, 0, 0), x.dtype)
     E, N, K = w.shape
     R = x.shape[0]
-    y = _like(x, y, "y", (R, N))
+    y = _like(x, y, "y", (R, N), stream)
     if scratch is None:
-        scratch = _split_scratch(0, R, E, N, K, x.device)
+        scratch = _split_scratch(0, R, E, N, K, x.device, stream)
     _check(_lib.moe_experts_matmul(x.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(), R,
                                    E, N, K, dt, y.data_ptr(), scratch.ptr if scratch else None,
                                    scratch.nbytes if scratch else 0, _stream(stream)),
@@ -730,9 +757,9 @@ def moe_experts_matmul_dx(dy, w, offsets, dx=None, scratch: Optional[Scratch] = 
     _shaped(w, "w", (w.shape[0], dy.shape[1], w.shape[2]) if w.dim() == 3 else (0, 0, 0), dy.dtype)
     E, N, K = w.shape
     R = dy.shape[0]
-    dx = _like(dy, dx, "dx", (R, K))
+    dx = _like(dy, dx, "dx", (R, K), stream)
     if scratch is None:
-        scratch = _split_scratch(1, R, E, N, K, dy.device)
+        scratch = _split_scratch(1, R, E, N, K, dy.device, stream)
     _check(_lib.moe_experts_matmul_dx(dy.data_ptr(), w.data_ptr(), _offsets(offsets, E).data_ptr(),
                                       R, E, N, K, dt, dx.data_ptr(),
                                       scratch.ptr if scratch else None,
@@ -756,12 +783,12 @@ def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bo
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
     if dw is None:
-        dw = torch.empty((E, N, K), dtype=dw_dtype or dy.dtype, device=dy.device)
+        dw = _new((E, N, K), dw_dtype or dy.dtype, dy.device, stream)
     out = _typed(dw, "dw", 3)
     _shaped(dw, "dw", (E, N, K), dw_dtype or dw.dtype)
     if scratch is None:
         n = _lib.moe_experts_split_bytes(2, R, E, N, K) or _lib.moe_experts_workspace_bytes(E)
-        scratch = Scratch(torch.empty(max(n, 1), dtype=torch.uint8, device=dy.device))
+        scratch = Scratch(_new(max(n, 1), torch.uint8, dy.device, stream, result=False))
     _check(_lib.moe_experts_matmul_dw(dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), R, E, N, K,
                                       dt, out, int(accumulate), dw.data_ptr(), scratch.ptr, scratch.nbytes,
                                       _stream(stream)), "moe_experts_matmul_dw")
@@ -777,7 +804,7 @@ def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor:
     E = logits.shape[-1]
     _shaped(logits, "logits", (T, E), torch.float32)
     _shaped(dscales, "dscales", (T, k), torch.float32)
-    dlogits = _like(logits, dlogits, "dlogits", (T, E))
+    dlogits = _like(logits, dlogits, "dlogits", (T, E), stream)
     p = MoeRouteParams(E, k, method, 1, 1, routed_scaling_factor)
     _check(_lib.moe_route_backward(logits.data_ptr(), ids.data_ptr(), dscales.data_ptr(), T, ctypes.byref(p),
                                    dlogits.data_ptr(), _stream(stream)), "moe_route_backward")
