@@ -253,11 +253,12 @@ class Workspace:
         return self.buf[off:off + nbytes].view(dtype)
 
 
-def alloc_workspace(problem: MoeProblem, device="cuda") -> Workspace:
+def alloc_workspace(problem: MoeProblem, device="cuda", stream=None) -> Workspace:
+    """The forward's workspace, for calls on `stream` (None: the current one)."""
     n = moe_workspace_bytes(problem)
     if n == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_workspace_bytes")
-    buf = torch.empty(n + 1024, dtype=torch.uint8, device=device)
+    buf = _new(n + 1024, torch.uint8, device, stream, result=False)
     base = (-buf.data_ptr()) % 1024
     return Workspace(problem, buf, base, n, moe_workspace_layout(problem))
 
@@ -272,9 +273,9 @@ def moe_route(logits: torch.Tensor, method: int, top_k: int, bias: Optional[torc
     if bias is not None:
         _cuda(bias, "bias", torch.float32)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        ids = _new((T, top_k), torch.int32, logits.device, stream)
     if scales is None:
-        scales = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        scales = _new((T, top_k), torch.float32, logits.device, stream)
     p = MoeRouteParams(E, top_k, method, n_group, topk_group, routed_scaling_factor)
     _check(_lib.moe_route(_ptr(logits), T, _ptr(bias), ctypes.byref(p), _ptr(ids), _ptr(scales),
                           _stream(stream)), "moe_route")
@@ -298,9 +299,9 @@ def moe_forward(x, ids, scales, w13, w2, w13_s=None, w2_s=None, y=None,
     _cuda(w2, "w2", torch.bfloat16)
     p = _problem_for(x, ids, w13, w2, w13_s)
     if workspace is None:
-        workspace = alloc_workspace(p, x.device)
+        workspace = alloc_workspace(p, x.device, stream)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     _check(_lib.moe_forward(ctypes.byref(p), _ptr(x), _ptr(ids), _ptr(scales), _ptr(w13), _ptr(w2),
                             _ptr(w13_s), _ptr(w2_s), _ptr(y), workspace.ptr, workspace.nbytes,
                             _stream(stream)), "moe_forward")
@@ -325,9 +326,9 @@ def moe_forward_partial(x, ids, scales, w13_local, w2_local, e_lo: int, e_hi: in
     shared_I = 0 if w13_s is None else w13_s.shape[0] // 2
     p = make_problem(T, H, I, num_experts, k, shared_I)
     if workspace is None:
-        workspace = alloc_workspace(p, x.device)
+        workspace = alloc_workspace(p, x.device, stream)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     if shared_gate is not None:
         _cuda(shared_gate, "shared_gate", torch.float32)
     _check(_lib.moe_forward_partial(ctypes.byref(p), int(e_lo), int(e_hi), _ptr(x), _ptr(ids),
@@ -349,9 +350,9 @@ def moe_gate(x, wg, num_experts: int, routed_logits=None, shared_logits=None, st
     if n_shared not in (0, 1) or wg.shape[1] != H:
         raise ValueError(f"wg must be [{E} or {E + 1}, {H}], got {tuple(wg.shape)}")
     if routed_logits is None:
-        routed_logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        routed_logits = _new((T, E), torch.float32, x.device, stream)
     if n_shared and shared_logits is None:
-        shared_logits = torch.empty((T,), dtype=torch.float32, device=x.device)
+        shared_logits = _new((T,), torch.float32, x.device, stream)
     _check(_lib.moe_gate(_ptr(x), _ptr(wg), T, H, E, n_shared, _ptr(routed_logits),
                          _ptr(shared_logits) if n_shared else None, _stream(stream)), "moe_gate")
     return routed_logits, (shared_logits if n_shared else None)
@@ -376,13 +377,13 @@ def moe_gate_route(x, wg, method: int, top_k: int, num_experts: int,
     if bias is not None:
         _cuda(bias, "bias", torch.float32)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        ids = _new((T, top_k), torch.int32, x.device, stream)
     if scales is None:
-        scales = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        scales = _new((T, top_k), torch.float32, x.device, stream)
     if want_logits and routed_logits is None:
-        routed_logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+        routed_logits = _new((T, E), torch.float32, x.device, stream)
     if n_shared and shared_logits is None:
-        shared_logits = torch.empty((T,), dtype=torch.float32, device=x.device)
+        shared_logits = _new((T,), torch.float32, x.device, stream)
     p = MoeRouteParams(E, top_k, method, n_group, topk_group, routed_scaling_factor)
     _check(_lib.moe_gate_route(_ptr(x), _ptr(wg), T, H, n_shared, _ptr(bias), ctypes.byref(p),
                                _ptr(ids), _ptr(scales), _ptr(routed_logits),
@@ -411,7 +412,7 @@ def moe_forward_static(x, ids, scales, w13, w2, w13_s=None, w2_s=None, y=None, s
     _cuda(w2, "w2", torch.bfloat16)
     p = _problem_for(x, ids, w13, w2, w13_s)
     if y is None:
-        y = torch.empty_like(x)
+        y = _new(x.shape, x.dtype, x.device, stream)
     _check(_lib.moe_forward_static(ctypes.byref(p), _ptr(x), _ptr(ids), _ptr(scales), _ptr(w13),
                                    _ptr(w2), _ptr(w13_s), _ptr(w2_s), _ptr(y), _stream(stream)),
            "moe_forward_static")
@@ -467,7 +468,7 @@ def moe_selftest_wait(workspace: Workspace, stream=None):
 def moe_cast_f32_to_bf16(t: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None):
     _cuda(t, "input", torch.float32)
     if out is None:
-        out = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+        out = _new(t.shape, torch.bfloat16, t.device, stream)
     _check(_lib.moe_cast_f32_to_bf16(_ptr(t), _ptr(out), t.numel(), _stream(stream)),
            "moe_cast_f32_to_bf16")
     return out

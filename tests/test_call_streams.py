@@ -112,6 +112,24 @@ TRAINING = {
 }
 
 
+def weights():
+    return gpu(2, 128, 64), gpu(2, 64, 64)
+
+
+FORWARD = {
+    "route": lambda m, s: m.moe_route(gpu(4, 8, dtype=torch.float32), 0, 2, stream=s),
+    "gate": lambda m, s: m.moe_gate(gpu(4, 64), gpu(9, 64), 8, stream=s),
+    "gate_route": lambda m, s: m.moe_gate_route(gpu(4, 64), gpu(9, 64), 4, 2, 8, want_logits=True, stream=s),
+    "forward": lambda m, s: m.moe_forward(gpu(4, 64), i32(4, 2), gpu(4, 2, dtype=torch.float32),
+                                          *weights(), stream=s),
+    "forward_partial": lambda m, s: m.moe_forward_partial(
+        gpu(4, 64), i32(4, 2), gpu(4, 2, dtype=torch.float32), *weights(), 0, 2, 4, stream=s),
+    "forward_static": lambda m, s: m.moe_forward_static(gpu(4, 64), i32(4, 2), gpu(4, 2, dtype=torch.float32),
+                                                        *weights(), stream=s),
+    "cast": lambda m, s: m.moe_cast_f32_to_bf16(gpu(4, dtype=torch.float32), stream=s),
+}
+
+
 def tensors(out):
     for t in out if isinstance(out, tuple) else (out,):
         if hasattr(t, "buf"):
@@ -139,6 +157,35 @@ def check(moe, allocations, call):
 @pytest.mark.parametrize("name", TRAINING)
 def test_a_training_calls_allocations_are_the_launchs_streams(moe, allocations, name):
     check(moe, allocations, TRAINING[name])
+
+
+@pytest.mark.parametrize("name", FORWARD)
+def test_a_forward_calls_allocations_are_the_launchs_streams(moe, allocations, name):
+    check(moe, allocations, FORWARD[name])
+
+
+@pytest.mark.gpu
+@pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
+def test_two_streams_forwards_under_way_at_once(moe):
+    T, H, I, E, k = 300, 256, 192, 8, 2
+    g = torch.Generator().manual_seed(2)
+    draw = lambda *shape, std=1.0: (torch.randn(shape, generator=g) * std).bfloat16().cuda()   # noqa: E731
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda()
+    scales = torch.rand((T, k), generator=g).cuda()
+    xs, w13, w2 = [draw(T, H), draw(T, H)], draw(E, 2 * I, H, std=H ** -0.5), draw(E, H, I, std=I ** -0.5)
+    want = [moe.moe_forward(x, ids, scales, w13, w2) for x in xs]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+    got = [moe.moe_forward(x, ids, scales, w13, w2, stream=s) for x, s in zip(xs, side)]
+    scribble = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in (4096, 1 << 16, 1 << 20, 1 << 22)]
+    torch.cuda.synchronize()
+    del scribble
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
