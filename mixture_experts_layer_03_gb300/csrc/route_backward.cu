@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kGradThreads = 256;
 constexpr int kSlots = 8;
+constexpr float kFarBelow = -20.0f;
 
 enum : int { kSoftmaxAll, kSoftmaxChosen, kSigmoidSum, kSigmoidEach };
 
@@ -95,13 +96,25 @@ route_grad_kernel(const float* __restrict__ logits, const int32_t* __restrict__ 
         // sigma(l) (1 - sigma(l)) from exp(-|l|): no cancellation at either end
         const float ex = live ? expf(-fabsf(l)) : 0.0f;
         const float r = 1.0f / (1.0f + ex);
-        const float slope = ex * r * r;
+        float slope = ex * r * r;
         if (kForm == kSigmoidSum) {
-          // Where one weight is nearly the sum, d less its share cancels: sigma and the share are rounded
-          // as few times as can be (far below, where exp(-l) ends, sigma is exp(l)).
-          const float a = !live ? 0.0f : l > -80.0f ? 1.0f / (1.0f + expf(-l)) : ex * r;
-          const float sum = sum_warp(a) + eps;
-          d = sum > 0.0f ? c * (d - sum_warp(d * a) / sum) / sum : 0.0f;
+          if (__any_sync(0xffffffffu, live && l > kFarBelow)) {
+            // Where one weight is nearly the sum, d less its share cancels: sigma and the share are rounded
+            // as few times as can be (far below, where exp(-l) ends, sigma is exp(l)).
+            const float a = !live ? 0.0f : l > -80.0f ? 1.0f / (1.0f + expf(-l)) : ex * r;
+            const float sum = sum_warp(a) + eps;
+            d = sum > 0.0f ? c * (d - sum_warp(d * a) / sum) / sum : 0.0f;
+          } else {
+            // Every chosen logit far below zero: sigma(l) = exp(l) and 1 - sigma(l) = 1 to 2^-28. The
+            // sigmoids and 1 / sum leave the range of 32 bits (from -88 on), the weights do not: they
+            // are taken from exp(l - max), eps by exp(-max) in two factors.
+            const float m = max_warp(l);
+            const float e = live ? expf(l - m) : 0.0f;
+            const float half = expf(-0.5f * m);
+            const float w = e / (sum_warp(e) + (eps > 0.0f ? eps * half * half : 0.0f));
+            d = c * (d - sum_warp(d * w));
+            slope = w;
+          }
         }
         d *= slope;
       }
