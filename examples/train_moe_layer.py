@@ -74,6 +74,8 @@ def main(argv=None):
         losses.append(loss.detach())
     end.record()
     torch.cuda.synchronize()
+    if moe.moe_read_timeouts()[0] != moe.MOE_OK:
+        raise RuntimeError("a kernel's wait ran out: the results are incomplete")
     losses = [float(v) for v in losses]
     for i in range(0, a.steps, max(1, a.steps // 6)):
         print(f"step {i:4d}  loss {losses[i]:.5f}")

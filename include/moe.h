@@ -425,6 +425,17 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
                                  moe_dtype dw_dtype, int32_t accumulate, void* dw, void* workspace,
                                  size_t ws_bytes, void* stream);
 
+/* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products above or of
+ * the gate ran out in any call on the current GPU, with a workspace or without, since the last read.
+ * Such a call's results are incomplete. *flags (may be NULL) receives MOE_DEVICE_FLAG_TIMEOUT or 0.
+ * Returns MOE_ERR_DEVICE_TIMEOUT when one did, else MOE_OK. */
+moe_status moe_read_timeouts(void* stream, int32_t* flags);
+
+/* Self-test of that report, with no fault and no hang: one warp waits as the products do, without a
+ * workspace, on a barrier that nothing arrives on, for the 2 s of every wait here. Enqueued on
+ * `stream`; returns at once. */
+moe_status moe_selftest_experts_wait(void* stream);
+
 /* Gradient of moe_route's scales to its logits: dlogits [T, E] (every entry written) from logits
  * [T, E], the ids [T, k] that moe_route chose and dscales [T, k]. The choice itself has no
  * gradient (nor has the bias). Takes every method that moe_route runs; of the other parameters

@@ -130,6 +130,8 @@ _SIGS = {
                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int,
                                              ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.c_size_t,
                                              _P]),
+    "moe_read_timeouts": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),
+    "moe_selftest_experts_wait": (ctypes.c_int, [_P]),
     "moe_route_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64,
                                           ctypes.POINTER(MoeRouteParams), _P, _P]),
 }
@@ -518,8 +520,8 @@ def alloc_experts_scratch(num_experts: int, rows: int = 0, N: int = 8, K: int = 
 
 def _split_scratch(product: int, R: int, E: int, N: int, K: int, device,
                    stream) -> Optional[Scratch]:
-    """A workspace for one call whose contraction is split, else None. (Its status word is not
-    read by anyone.)"""
+    """A workspace for one call whose contraction is split, else None. (Nobody reads its status word;
+    moe_read_timeouts has what it would say.)"""
     n = _lib.moe_experts_split_bytes(product, R, E, N, K)
     return Scratch(_new(n, torch.uint8, device, stream, result=False)) if n else None
 
@@ -794,6 +796,20 @@ def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bo
                                       dt, out, int(accumulate), dw.data_ptr(), scratch.ptr, scratch.nbytes,
                                       _stream(stream)), "moe_experts_matmul_dw")
     return dw
+
+
+def moe_read_timeouts(stream=None):
+    """Synchronise; read and clear whether a wait of the experts' products or of the gate ran out in any
+    call on the current GPU since the last read (its results are incomplete then), whether or not
+    the call was given a scratch. Returns (status, flags)."""
+    flags = ctypes.c_int32(0)
+    st = _lib.moe_read_timeouts(_stream(stream), ctypes.byref(flags))
+    return st, flags.value
+
+
+def moe_selftest_experts_wait(stream=None):
+    """Enqueue the self-test of moe_read_timeouts: a bounded wait that runs out after about 2 s."""
+    _check(_lib.moe_selftest_experts_wait(_stream(stream)), "moe_selftest_experts_wait")
 
 
 def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor: float = 1.0,

@@ -201,6 +201,30 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
                            static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_read_timeouts(void* stream, int32_t* flags) {
+  void* word[2] = {nullptr, nullptr};
+  moe_status st = experts_timeout_word(&word[0]);
+  if (st == MOE_OK) st = gate_timeout_word(&word[1]);
+  if (st != MOE_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t v[2] = {0, 0};
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    e = cudaMemcpyAsync(&v[i], word[i], sizeof(v[i]), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  // Only what was read is cleared: another stream's call may set a word meanwhile.
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    if (v[i]) e = cudaMemsetAsync(word[i], 0, sizeof(v[i]), s);
+  if (e == cudaSuccess && (v[0] | v[1])) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "timeouts read: %s", cudaGetErrorString(e));
+  if (flags) *flags = v[0] | v[1];
+  return v[0] | v[1] ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+}
+
+moe_status moe_selftest_experts_wait(void* stream) {
+  return launch_experts_wait_selftest(static_cast<cudaStream_t>(stream));
+}
+
 moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dscales,
                               int64_t T, const moe_route_params* p, float* dlogits, void* stream) {
   if (!p) return set_error(MOE_ERR_INVALID_ARG, "route params are NULL");

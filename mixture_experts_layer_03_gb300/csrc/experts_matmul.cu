@@ -210,9 +210,13 @@ __device__ __forceinline__ Tile decode_tile(int idx, const uint16_t* s_blk, cons
   return t;
 }
 
+// Set by every wait that runs out, whoever holds the call's workspace, if there is one.
+__device__ int32_t g_experts_timeouts;
+
 __device__ __forceinline__ void x_timeout(int32_t* status, volatile int* abort) {
   *abort = 1;
   if (status) atomicOr(status, MOE_DEVICE_FLAG_TIMEOUT);
+  atomicOr(&g_experts_timeouts, MOE_DEVICE_FLAG_TIMEOUT);
 }
 
 // Loads are issued by the whole warp, one thread of it taking effect: descriptors, addresses and
@@ -827,6 +831,20 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
   cluster_sync();
 }
 
+// A wait of the kernel above for a barrier that nothing arrives on, in a call without a workspace.
+__global__ void __launch_bounds__(32) experts_wait_selftest_kernel() {
+  __shared__ uint64_t bar;
+  __shared__ int s_abort;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  volatile int* abort = &s_abort;
+  if (!__all_sync(0xffffffffu, mbar_wait(&bar, 0, abort))) x_timeout(nullptr, abort);
+}
+
 // The maps of dw: for each expert, dy's and x's map with the row count cut off at the expert's
 // last row. One warp a map. Also clears the status word.
 __global__ void __launch_bounds__(256)
@@ -973,6 +991,19 @@ moe_status launch_sum_parts(const float* part, int parts, int64_t n, int dtype, 
 size_t to_128(size_t n) { return (n + 127) / 128 * 128; }
 
 }  // namespace
+
+moe_status experts_timeout_word(void** word) {
+  const cudaError_t e = cudaGetSymbolAddress(word, g_experts_timeouts);
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
+
+moe_status launch_experts_wait_selftest(cudaStream_t s) {
+  experts_wait_selftest_kernel<<<1, 32, 0, s>>>();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "self-test launch: %s", cudaGetErrorString(e));
+}
 
 int experts_split(int product, int64_t R, int E, int N, int K) {
   const int64_t pairs = device_sm_count() / 2;

@@ -30,6 +30,9 @@
 namespace moe {
 namespace {
 
+// Set when a wait runs out, whether or not the call has a status word.
+__device__ int32_t g_gate_timeouts;
+
 constexpr int kGateBK = 64;                  // K elements per slot
 constexpr int kGateRowBytes = kGateBK * 2;
 // The ring holds up to 8 slots of one K block each (an X box and a W box); a pipeline
@@ -309,7 +312,10 @@ gate_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         r1 - r0, row0 + r0, g.T, g.k, g.method, g.rsf, ps, g.ids, g.scales);
   }
   cluster_sync();   // no CTA leaves while another reads its shared memory
-  if (tid == 0 && *abort && g.status) atomicOr(g.status, MOE_DEVICE_FLAG_TIMEOUT);
+  if (tid == 0 && *abort) {
+    if (g.status) atomicOr(g.status, MOE_DEVICE_FLAG_TIMEOUT);
+    atomicOr(&g_gate_timeouts, MOE_DEVICE_FLAG_TIMEOUT);
+  }
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
@@ -402,6 +408,12 @@ cudaError_t launch_gate_e(const cudaLaunchConfig_t& cfg, const CUtensorMap& mx,
 }
 
 }  // namespace
+
+moe_status gate_timeout_word(void** word) {
+  const cudaError_t e = cudaGetSymbolAddress(word, g_gate_timeouts);
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
 
 moe_status launch_gate(const void* x, const void* wg, int64_t T, int H, int E, int n_shared,
                        float* logits, float* shared_logits, int32_t* status, cudaStream_t s,

@@ -148,6 +148,11 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
                              char* ws, size_t ws_bytes, cudaStream_t s);
 
+// Device words in which the products' and the gate's kernels note that a wait ran out.
+moe_status experts_timeout_word(void** word);
+moe_status gate_timeout_word(void** word);
+moe_status launch_experts_wait_selftest(cudaStream_t s);
+
 moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* ds,
                                  int64_t T, const moe_route_params& p, float* dl, cudaStream_t s);
 

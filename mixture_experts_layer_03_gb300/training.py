@@ -66,7 +66,10 @@ def moe_layer(x, wg, w13, w2, method: int, top_k: int, bias=None, n_group: int =
               topk_group: int = 1, routed_scaling_factor: float = 1.0):
     """y [T, H] of the MoE layer, differentiable in x [T, H], the gate wg [E, H], w13 [E, 2I, H]
     (gate rows, then up rows) and w2 [E, H, I], all bf16. Routing as moe_gate_route (the
-    selection bias has no gradient); E a multiple of 8, H of 64, I of 8."""
+    selection bias has no gradient); E a multiple of 8, H of 64, I of 8.
+
+    The kernels' waits are bounded. One that runs out leaves results incomplete and raises nothing, as
+    that would take a synchronisation: read moe_read_timeouts() where the loop synchronises anyway."""
     if w13.shape[0] % 8 or wg.shape[0] != w13.shape[0]:
         raise ValueError(f"the gate's gradient takes a multiple of 8 experts, one row of wg each: "
                          f"got {w13.shape[0]} experts, wg {tuple(wg.shape)}")
