@@ -41,6 +41,14 @@ class _MoeLayer(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        with torch.no_grad():
+            grads = _MoeLayer.gradients(ctx, dy)
+        if torch.is_grad_enabled():   # create_graph
+            grads = _refuse_second(grads, [dy, *ctx.saved_tensors[:4]])
+        return (*grads, None, None, None, None, None, None)
+
+    @staticmethod
+    def gradients(ctx, dy):
         x, wg, w13, w2, ids, scales, logits, inv, offsets, ckpt, rows = ctx.saved_tensors
         need_x, need_wg, need_w13, need_w2 = ctx.needs_input_grad[:4]
         drows, dscales = moe_combine_backward(dy.contiguous(), rows, inv, scales)
@@ -59,7 +67,27 @@ class _MoeLayer(torch.autograd.Function):
                 dx += moe_experts_matmul_dx(dlogits, wg[None], all_rows)
             if need_wg:
                 dwg = moe_experts_matmul_dw(dlogits, x, all_rows)[0]
-        return dx, dwg, dw13, dw2, None, None, None, None, None, None
+        return dx, dwg, dw13, dw2
+
+
+class _NoSecond(torch.autograd.Function):
+    """First derivatives, as they are, in a graph whose backward pass is an error."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("moe_layer has no second derivative")
+
+
+def _refuse_second(grads, inputs):
+    """The gradient's kernels have no gradient: a loss that takes in the gradients `grads` (functions of
+    `inputs`) must fail, and not count them as constants."""
+    there = [g for g in grads if g is not None]
+    out = iter(_NoSecond.apply(len(there), *there, *inputs))
+    return [None if g is None else next(out) for g in grads]
 
 
 def moe_layer(x, wg, w13, w2, method: int, top_k: int, bias=None, n_group: int = 1,
