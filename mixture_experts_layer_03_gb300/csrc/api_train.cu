@@ -13,6 +13,12 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 // NULL or not on a 16-byte boundary.
 bool bad(const void* p) { return !p || !aligned(p, 16); }
 
+// The status word of a call that launches nothing, where it has a workspace.
+cudaError_t clear_status(void* ws, size_t ws_bytes, uintptr_t align, void* stream) {
+  if (!ws || !aligned(ws, align) || ws_bytes < 16) return cudaSuccess;
+  return cudaMemsetAsync(ws, 0, 16, static_cast<cudaStream_t>(stream));
+}
+
 moe_status check_dtype(int dtype, bool with_f32) {
   if (dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16 || (with_f32 && dtype == MOE_DTYPE_F32))
     return MOE_OK;
@@ -73,8 +79,9 @@ moe_status moe_dispatch(const void* x, const int32_t* ids, int64_t T, int32_t H,
   if (T == 0) {
     // No slots: every expert's rows are empty.
     if (!offsets || !aligned(offsets, 4)) return set_error(MOE_ERR_INVALID_ARG, "offsets NULL or misaligned");
-    const cudaError_t e = cudaMemsetAsync(offsets, 0, 4 * (static_cast<size_t>(E) + 1),
-                                          static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaMemsetAsync(offsets, 0, 4 * (static_cast<size_t>(E) + 1),
+                                    static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = clear_status(workspace, ws_bytes, 16, stream);
     return e == cudaSuccess ? MOE_OK
                             : set_error(MOE_ERR_CUDA, "offsets clear: %s", cudaGetErrorString(e));
   }
@@ -184,9 +191,10 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
     return set_error(MOE_ERR_UNSUPPORTED, "only an f32 dw is added to");
   if (bad(dw)) return set_error(MOE_ERR_INVALID_ARG, "dw NULL or not 16-byte aligned");
   if (R == 0) {
-    if (accumulate) return MOE_OK;
     const size_t n = static_cast<size_t>(E) * N * K * (dw_dtype == MOE_DTYPE_F32 ? 4 : 2);
-    const cudaError_t e = cudaMemsetAsync(dw, 0, n, static_cast<cudaStream_t>(stream));
+    cudaError_t e = clear_status(workspace, ws_bytes, 128, stream);
+    if (e == cudaSuccess && !accumulate)
+      e = cudaMemsetAsync(dw, 0, n, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : set_error(MOE_ERR_CUDA, "dw clear: %s", cudaGetErrorString(e));
   }
   if (bad(dy) || bad(x) || !offsets || !aligned(offsets, 4))

@@ -47,3 +47,24 @@ def test_a_wait_of_the_products_that_runs_out_is_read_without_a_workspace(moe):
     assert torch.equal(again, y)
     assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(again.sum(), args), grads))
     assert moe.moe_read_timeouts() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
+def test_status_words_of_calls_without_rows(moe):
+    """A dispatch writes its workspace's status word, and dw clears its own, with no rows too: what an
+    older call or the memory's last user left is not read as theirs."""
+    ids = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    scratch = moe.alloc_dispatch_scratch(0, 4, 2)
+    scratch.buf.fill_(0x5A)
+    moe.moe_dispatch(x, ids, 4, scratch=scratch)
+    assert moe.moe_read_device_status(scratch) == (moe.MOE_OK, 0)
+    offsets = torch.zeros(5, dtype=torch.int32, device="cuda")
+    for start in (None, torch.ones((4, 32, 64), device="cuda")):
+        scratch = moe.alloc_experts_scratch(4)
+        scratch.buf.fill_(0x5A)
+        moe.moe_experts_matmul_dw(torch.empty((0, 32), dtype=torch.bfloat16, device="cuda"), x, offsets,
+                                  dw=start, accumulate=start is not None, scratch=scratch)
+        assert moe.moe_read_device_status(scratch) == (moe.MOE_OK, 0)
+    assert (start == 1).all()
