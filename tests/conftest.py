@@ -13,6 +13,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: full-size workloads")
 
 
+# Calls with made-up addresses, not all of them refused on the host: the forward and dx beside a dw of a
+# refused type would read them.
+NOT_ON_A_GPU = {"test_train_abi.py::test_experts_products_refuse"}
+
+
+def pytest_collection_modifyitems(items):
+    mine = [i for i in items if i.nodeid.rsplit("/", 1)[-1] in NOT_ON_A_GPU]
+    if not mine:
+        return
+    import torch
+    if torch.cuda.is_available():
+        for item in mine:
+            item.add_marker(pytest.mark.skip(reason="launches kernels on made-up addresses where there is a GPU"))
+
+
 @pytest.fixture(scope="session")
 def golden_dir():
     return os.path.join(ROOT, "tests", "golden")
