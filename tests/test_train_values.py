@@ -67,3 +67,38 @@ def test_route_backward_where_the_sigmoids_underflow_in_64_bits_squared(moe, met
     want, mag = ref.route_backward(logits, ids, ds.astype(np.float64), 1)
     want, mag = (rsf * want, rsf * mag) if method != 2 else (0 * want, 0 * mag)
     within(got, want, 40 * 2.0 ** -24 * mag + 1e-37, "dlogits")
+
+
+@pytest.mark.parametrize("I", [96, 33, 515])
+def test_swiglu_in_f32_is_as_accurate_as_f32(moe, I):
+    """At gates of up to 100 either way, in units of 2^-24: expf 4 (2 ulp), 1 + exp(-|g|) and its
+    reciprocal 4 in all, sigma or 1 - sigma, their product, 9; two products more. Below the normal
+    range a few of its steps, times the other factors."""
+    R = 40
+    g = torch.Generator().manual_seed(I)
+    gu = torch.randn((R, 2 * I), generator=g)
+    gu[:, :I] *= 10.0 ** torch.empty((R, 1)).uniform_(-2, 1.5, generator=g)
+    gu[0, :I] = torch.linspace(-100, 100, I)
+    gu[1, :I] = torch.linspace(-104, -80, I)
+    gu[2, :I] = torch.linspace(10, 20, I)
+    gu = gu.clamp(-104, 104).cuda()
+    dh = torch.randn((R, I), generator=g).cuda()
+    h, ckpt = moe.moe_swiglu_ckpt(gu)
+    dgu, again = moe.moe_swiglu_ckpt_backward(dh, ckpt, want_h=True)
+    unit = 2.0 ** -24
+
+    def parts(v):
+        gate, up = v[:, :I], v[:, I:]
+        return gate, up, 2.0 ** -146 * (1 + np.abs(gate)) * (1 + np.abs(up))
+
+    for got, v in ((h, n64(gu)), (again, ref.kept(*(t.cpu().numpy() for t in ckpt)))):
+        want = ref.swiglu(v)
+        within(got, want, 12 * unit * np.abs(want) + parts(v)[2], "h")
+    gate, up, tiny = parts(v)
+    d = n64(dh)
+    want = ref.swiglu_backward(d, v)
+    s, o = ref.sigmoid(gate), ref.sigmoid(-gate)
+    # sigma + (g sigma) (1 - sigma): 9, and 13 and two products, the sum, two products more
+    mag = np.concatenate([20 * np.abs(d * up) * (s + np.abs(gate) * s * o), 12 * np.abs(want[:, I:])], 1)
+    tiny = tiny * (1 + np.abs(d))
+    within(dgu, want, unit * mag + np.concatenate([tiny, tiny], 1), "dgu")
