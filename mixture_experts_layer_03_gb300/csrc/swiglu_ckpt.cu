@@ -61,8 +61,8 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
 // 2^-e (to quantise) and 2^e (to read) of a scale byte e + 127. Byte 0 is 2^-127, a subnormal;
 // its inverse 2^127 is normal. Byte 255 reads as NaN.
 __device__ __forceinline__ float inv_scale(uint32_t byte) {
-  // 127 - e = 254 - byte as an exponent field; bytes above 246 do not occur but for 255 (448 *
-  // 2^119 is over the largest float), where the products are not used.
+  // 127 - e = 254 - byte as an exponent field; finite values give bytes up to 247 (448 * 2^120 is over
+  // the largest float), and for 255 the products are not used.
   return __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
 }
 __device__ __forceinline__ float scale_of(uint32_t byte) {
