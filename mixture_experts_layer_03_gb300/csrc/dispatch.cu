@@ -149,9 +149,11 @@ struct RowCopy {
   }
 };
 
-// Narrower vectors, whose copies are bound by instructions: a thread's lie 32 apart, so that one address
+// Narrower vectors, whose copies have instructions to save: a thread's lie 32 apart, so that one address
 // and constants reach them, and are not checked one by one where all exist. (4096 tokens to six rows
-// each of 7167 bf16 97 us, of 7164 81; in the form above 156 and 85.)
+// each of 7167 bf16 97 us, of 7164 81; in the form above 156 and 85. What is left at 7167 is neither
+// instructions, 27% of the issue slots, nor bandwidth, 51% of the DRAM's: waiting, with 16 bytes a thread
+// under way at a time.)
 template <int kBytes>
 struct NarrowCopy {
   using Raw = typename RawVec<kBytes>::type;
@@ -375,7 +377,7 @@ combine_kernel(const T* __restrict__ rows, const int32_t* __restrict__ inv,
   }
 }
 
-// Rows that do not start on 16 bytes: vectors of kBytes. These kernels are bound by instructions, so a
+// Rows that do not start on 16 bytes: vectors of kBytes. These kernels have instructions to save, so a
 // warp takes kU times 32 neighbouring vectors, which one address a row reaches, unchecked where all of
 // them exist (kFull), kJ slots at a time. (4096 tokens, k = 6, bf16: H = 7167 94 us, H = 7164 75; a
 // thread for every four vectors, each with its own addresses, took 154 for either. Reading rows in

@@ -204,10 +204,19 @@ cudaError_t launch_few(const void* x, const void* w, const int32_t* offsets, int
 
 }  // namespace
 
-// Measured against the tensor-core kernel: 8 rows over 128 experts (N = 1536, K = 2048, 50 MB of
-// weights) 12.1 us against 13.5, 2 rows of 2 (N = 10256, K = 2976) 24 against 34, 5 rows of one (N =
-// 136, K = 14336) 8.5 against 12.5; but 12 rows of one (4096 x 4096), whose weights are read three
-// times here, 22 against 13, and 32 rows of 8 (14336 x 4096) 234 against 145.
+// A rule on the rows and experts, which is what the host knows: where the rows are, it does not. Against
+// the tensor-core kernel, us:
+//                                       9 rows         12 rows        16 rows
+//   of 128 experts, 1536 x 2048, spread 14.0 | 13.9    16.6 | 15.9    21.8 | 24.6
+//                           all of one  6.7 | 11.7     6.9 | 11.7     8.9 | 11.7
+//   of 8 experts, 4096 x 4096, spread   35 | 44        39 | 42        47 | 45
+//                           all of one  20.4 | 19.9    22.5 | 19.9    28.5 | 19.9
+//   of 8 experts, 14336 x 4096, spread  110 | 107      126 | 114      152 | 130
+//                           all of one  69 | 25        76 | 25        99 | 25
+// and 2 rows over those 14336 x 4096 40 | 45, of one 22.9 | 24.2, 8 rows 106 | 104 and 52 | 24. Rows of one
+// expert of large weights, which are read once for every four rows, are what it decides wrongly. Few
+// experts: 5 rows of one (N = 136, K = 14336) 8.5 | 12.5, 12 of one (4096 x 4096) 22 | 13; 32 rows of 8
+// (14336 x 4096) 234 | 145.
 bool experts_few(int64_t R, int E) { return R <= 16 && R <= 8 * E; }
 
 moe_status launch_experts_few(const void* x, const void* w, const int32_t* offsets, int64_t R, int E,

@@ -60,7 +60,8 @@ class _MoeLayer(torch.autograd.Function):
         if need_x:
             dx = moe_dispatch_backward(moe_experts_matmul_dx(dgu, w13, offsets), inv)
         if need_x or need_wg:
-            # The gate is the product of one expert that has every token.
+            # The gate is the product of one expert that has every token; its gradient's rows are rounded
+            # to the products' type, as all of theirs are.
             dlogits = moe_route_backward(logits, ids, dscales, ctx.method, ctx.rsf).to(x.dtype)
             all_rows = torch.arange(2, dtype=torch.int32, device=x.device) * x.shape[0]
             if need_x:
@@ -95,6 +96,12 @@ def moe_layer(x, wg, w13, w2, method: int, top_k: int, bias=None, n_group: int =
     """y [T, H] of the MoE layer, differentiable in x [T, H], the gate wg [E, H], w13 [E, 2I, H]
     (gate rows, then up rows) and w2 [E, H, I], all bf16. Routing as moe_gate_route (the
     selection bias has no gradient); E a multiple of 8, H of 64, I of 8.
+
+    What the backward pass rounds beside its products' results: gu is kept in 8 bits (always: gradients of
+    x, w13 and w2 are within 6% in norm on normal data, y is not affected; the operators by themselves can
+    keep it as it is), the gradient of the logits goes to x's type before the gate's two products,
+    and dx is the sum of the experts' and the gate's, each in that type. A second derivative is an
+    error.
 
     The kernels' waits are bounded. One that runs out leaves results incomplete and raises nothing, as
     that would take a synchronisation: read moe_read_timeouts() where the loop synchronises anyway."""
