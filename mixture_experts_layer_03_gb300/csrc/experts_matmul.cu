@@ -30,13 +30,13 @@
 // Measured (one GB300, calls of one product back to back): forward of 8192 x 14336 x 4096 over 8 experts
 // 541 us, 0.92 of cuBLAS's burst rate (0.92 of its sustained one too, 625 us, where the power limit
 // holds for a second and more); the tensor pipe is active for 92% of the cycles. dx and dw of 32768 x
-// 1536 x 4096 over 64 experts 259 and 270 us with 512 rows each, 273 and 276 with uneven ones: the power
+// 1536 x 4096 over 64 experts 259 and 270 us with 512 rows each, 273 and 280 with uneven ones: the power
 // limit (1.56 and 1.69 of 2.07 GHz under ncu), the tensor pipe active for 83% and 76% of the cycles, L2 at
 // 54%. Of dx's rest the last round is the most, 10.1 rounds of tiles done as 11. A tile of dw has 8 blocks
 // of 0.385 us and 0.26 us beside them (from 512 and 1024 rows each: 270 and 520 us in 81 rounds). dx and dw
 // over 256 experts (32768 x 2048 x 7168) 1.16 and 1.27 ms, bound by memory. An f32 dw has twice the bytes
-// to write: over those 64 experts 394 us, added to what is there 673, over 256 2.99 and 5.90 ms, 0.75 to
-// 0.8 of the copy rate.
+// to write: over those 64 experts 372 to 394 us, added to what is there 670, over 256 with 128 rows each
+// 2.99 and 5.90 ms (in 16 bits 1.37 to 1.43), 0.75 to 0.8 of the copy rate.
 //
 // Tiles go to the CTA pairs in order, pair i taking tiles i, i + pairs, ...: neighbouring tiles
 // (eight row tiles by the channels) share operands in L2. No counter hands them out: whole tiles of one
