@@ -425,8 +425,8 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
                                  moe_dtype dw_dtype, int32_t accumulate, void* dw, void* workspace,
                                  size_t ws_bytes, void* stream);
 
-/* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products above or of
- * the gate ran out in any call on the current GPU, with a workspace or without, since the last read.
+/* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products (above, or on
+ * 4-bit operands) or of the gate ran out in any call on the current GPU, with a workspace or without, since the last read.
  * Such a call's results are incomplete. *flags (may be NULL) receives MOE_DEVICE_FLAG_TIMEOUT or 0.
  * Returns MOE_ERR_DEVICE_TIMEOUT when one did, else MOE_OK. */
 moe_status moe_read_timeouts(void* stream, int32_t* flags);
@@ -443,6 +443,46 @@ moe_status moe_selftest_experts_wait(void* stream);
  * no part; non-finite logits count as -inf and get 0. */
 moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* dscales,
                               int64_t T, const moe_route_params* p, float* dlogits, void* stream);
+
+/* ---- Serving with 4-bit operands --------------------------------------------------------
+ *
+ * Microscaled 4-bit floating point. A tensor [planes, rows, K] (a matrix: planes = 1) is held as
+ *   codes   [planes, rows, K / 2] bytes: e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6; 8 is the sign), the lower
+ *           channel in the low half of its byte
+ *   scales  [planes, rows, S] bytes, S = K / block rounded up to a multiple of 16, one for each block of
+ *           neighbouring channels; what fills a row up is written as 0 and not looked at
+ *   MX      blocks of 32, byte b stands for 2^(b - 127), 255 for NaN
+ *   NV      blocks of 16, an e4m3 number (0 or positive), times g: one f32 on the device for each plane,
+ *           or NULL for 1
+ * K: a multiple of 32 up to 65536. Tensors are 16-byte aligned, g 4-byte. */
+typedef enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 } moe_fp4_format;
+
+/* x [planes, rows, K] (any moe_dtype) to 4 bits. MX: the least power of two, 2^-127 or more, with every
+ * |value| <= 6 * scale, so that nothing saturates. NV: the scale is amax / (6 g) rounded to nearest, 448
+ * at most; a block whose scale rounds to 0 reads as zeros. Codes are value / scale (/ g) rounded to
+ * nearest, 6 at most; ties to even everywhere; decided as on exact numbers. A block that holds an
+ * infinity or a NaN gets the scale NaN and reads as NaN. g, positive and finite, is given (for weights,
+ * say, amax / (6 * 448) of each expert, for rows a calibrated one); NULL with MX. planes * rows <= 2^31. */
+moe_status moe_quantize_fp4(const void* x, int64_t planes, int64_t rows, int32_t K, moe_dtype dtype,
+                            moe_fp4_format format, const float* g, uint8_t* codes, uint8_t* scales,
+                            void* stream);
+/* SwiGLU of gu [rows, 2I] (gate, then up) in fp32, its result [rows, I] held in 4 bits as above. */
+moe_status moe_swiglu_fp4(const void* gu, int64_t rows, int32_t I, moe_dtype dtype,
+                          moe_fp4_format format, const float* g, uint8_t* codes, uint8_t* scales,
+                          void* stream);
+/* The values again: out [planes, rows, K] of `dtype` (one past its range as an infinity). */
+moe_status moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* g,
+                              int64_t planes, int64_t rows, int32_t K, moe_fp4_format format,
+                              moe_dtype dtype, void* out, void* stream);
+
+/* moe_experts_matmul with both operands in 4 bits of one format: y [R, N] (dtype BF16 or F16), y[r] =
+ * x[r] . w[e]^T for the rows of expert e, x [R, K], w [E, N, K], x_g one value or NULL, w_g [E] or NULL.
+ * Offsets, rows of no expert and limits as there (N a multiple of 8, K of 32). Products of codes and
+ * scales are exact, their sums fp32, one rounding. */
+moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_g,
+                                  const uint8_t* w_codes, const uint8_t* w_scales, const float* w_g,
+                                  const int32_t* offsets, int64_t R, int32_t E, int32_t N, int32_t K,
+                                  moe_fp4_format format, moe_dtype dtype, void* y, void* stream);
 
 #ifdef __cplusplus
 }

@@ -46,6 +46,9 @@ MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1
 MOE_DTYPE_F32 = 2
 
+MOE_FP4_MX = 0
+MOE_FP4_NV = 1
+
 MOE_DEVICE_FLAG_BAD_ID = 1
 MOE_DEVICE_FLAG_TIMEOUT = 2
 
@@ -134,6 +137,15 @@ _SIGS = {
     "moe_selftest_experts_wait": (ctypes.c_int, [_P]),
     "moe_route_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64,
                                           ctypes.POINTER(MoeRouteParams), _P, _P]),
+    "moe_quantize_fp4": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                        ctypes.c_int, ctypes.c_int, _P, _P, _P, _P]),
+    "moe_swiglu_fp4": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_int,
+                                      _P, _P, _P, _P]),
+    "moe_dequantize_fp4": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                          ctypes.c_int, ctypes.c_int, _P, _P]),
+    "moe_experts_matmul_fp4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
+                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_int, ctypes.c_int, _P, _P]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -828,6 +840,122 @@ def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor:
     return dlogits
 
 
+# ------------------------------------------------------------------ 4-bit operands
+
+_FP4_BLOCK = {MOE_FP4_MX: 32, MOE_FP4_NV: 16}
+
+
+class Fp4:
+    """A tensor [rows, K] or [planes, rows, K] in microscaled 4-bit floating point. codes: uint8
+    [..., K / 2], two e2m1 numbers a byte, the lower channel in the low half. scales: uint8
+    [..., S], one for each block of 32 (MOE_FP4_MX: 2^(byte - 127)) or 16 (MOE_FP4_NV: e4m3) channels,
+    S = K / block rounded up to a multiple of 16; what fills a row up is not looked at. g: f32, the
+    factor of all of a matrix (1 element) or of each plane (MOE_FP4_NV; None: 1)."""
+    __slots__ = ("codes", "scales", "format", "g")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, format: int,
+                 g: Optional[torch.Tensor] = None):
+        if format not in _FP4_BLOCK:
+            raise ValueError(f"format must be MOE_FP4_MX or MOE_FP4_NV, got {format}")
+        if codes.dim() not in (2, 3):
+            raise ValueError(f"codes must be [rows, K / 2] or [planes, rows, K / 2], got {tuple(codes.shape)}")
+        shape = codes.shape
+        _shaped(codes, "codes", shape, torch.uint8)
+        _shaped(scales, "scales", shape[:-1] + (self.scale_columns(2 * shape[-1], format),), torch.uint8)
+        if g is not None:
+            if format != MOE_FP4_NV:
+                raise ValueError("only MOE_FP4_NV has a g")
+            _shaped(g, "g", (shape[0] if len(shape) == 3 else 1,), torch.float32)
+            if g.device != codes.device:
+                raise ValueError("g must be on the codes' device")
+        if scales.device != codes.device:
+            raise ValueError("scales must be on the codes' device")
+        self.codes, self.scales, self.format, self.g = codes, scales, format, g
+
+    @staticmethod
+    def scale_columns(K: int, format: int) -> int:
+        return (K // _FP4_BLOCK[format] + 15) // 16 * 16
+
+    @property
+    def shape(self) -> tuple:
+        return tuple(self.codes.shape[:-1]) + (2 * self.codes.shape[-1],)
+
+
+def _new_fp4(shape, format: int, g, device, stream, out: Optional[Fp4]) -> Fp4:
+    if format not in _FP4_BLOCK:
+        raise ValueError(f"format must be MOE_FP4_MX or MOE_FP4_NV, got {format}")
+    if shape[-1] % 32:
+        raise ValueError(f"4-bit rows must be a multiple of 32 channels, got {shape[-1]}")
+    if out is not None:
+        if out.shape != tuple(shape) or out.format != format or out.codes.device != device:
+            raise ValueError(f"out must be of {tuple(shape)} and the same format, got {out.shape}")
+        return Fp4(out.codes, out.scales, format, g)
+    codes = _new(shape[:-1] + (shape[-1] // 2,), torch.uint8, device, stream)
+    scales = _new(shape[:-1] + (Fp4.scale_columns(shape[-1], format),), torch.uint8, device, stream)
+    return Fp4(codes, scales, format, g)
+
+
+def moe_quantize_fp4(x, format: int, g: Optional[torch.Tensor] = None, out: Optional[Fp4] = None,
+                     stream=None) -> Fp4:
+    """x [rows, K] or [planes, rows, K] in 4 bits (MOE_FP4_MX or MOE_FP4_NV). g (MOE_FP4_NV): f32, one
+    value or one for each plane, by which values are divided first: amax / (6 * 448) uses all of the
+    scales' range; kept in the result. out: an Fp4 whose codes and scales are written."""
+    dt = _typed(x, "x", 3 if x.dim() == 3 else 2)
+    q = _new_fp4(x.shape, format, g, x.device, stream, out)
+    planes = x.shape[0] if x.dim() == 3 else 1
+    _check(_lib.moe_quantize_fp4(x.data_ptr(), planes, x.shape[-2], x.shape[-1], dt, format, _ptr(g),
+                                 q.codes.data_ptr(), q.scales.data_ptr(), _stream(stream)),
+           "moe_quantize_fp4")
+    return q
+
+
+def moe_swiglu_fp4(gu, format: int, g: Optional[torch.Tensor] = None, out: Optional[Fp4] = None,
+                   stream=None) -> Fp4:
+    """SwiGLU of gu [R, 2I] (gate, then up), its result [R, I] in 4 bits, as moe_quantize_fp4's."""
+    dt = _typed(gu, "gu", 2)
+    R, I2 = gu.shape
+    if I2 % 2:
+        raise ValueError(f"gu must have an even number of columns, got {I2}")
+    q = _new_fp4((R, I2 // 2), format, g, gu.device, stream, out)
+    _check(_lib.moe_swiglu_fp4(gu.data_ptr(), R, I2 // 2, dt, format, _ptr(g), q.codes.data_ptr(),
+                               q.scales.data_ptr(), _stream(stream)), "moe_swiglu_fp4")
+    return q
+
+
+def moe_dequantize_fp4(q: Fp4, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that q stands for, in bfloat16, float16 or float32."""
+    if out is None:
+        out = _new(q.shape, dtype, q.codes.device, stream)
+    else:
+        _shaped(out, "out", q.shape, dtype)
+    shape = q.shape
+    dt = _typed(out, "out", len(shape))
+    planes = shape[0] if len(shape) == 3 else 1
+    _check(_lib.moe_dequantize_fp4(q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.g), planes, shape[-2],
+                                   shape[-1], q.format, dt, out.data_ptr(), _stream(stream)),
+           "moe_dequantize_fp4")
+    return out
+
+
+def moe_experts_matmul_fp4(x: Fp4, w: Fp4, offsets, dtype=torch.bfloat16, y=None, stream=None):
+    """moe_experts_matmul with both operands in 4 bits of the same format: y [R, N] of `dtype` (bfloat16
+    or float16) from x [R, K] and w [E, N, K]."""
+    if len(x.shape) != 2 or len(w.shape) != 3 or x.shape[1] != w.shape[2] or x.format != w.format:
+        raise ValueError(f"x must be [R, K] and w [E, N, K] of one format, got {x.shape} and {w.shape}")
+    E, N, K = w.shape
+    R = x.shape[0]
+    if y is None:
+        y = _new((R, N), dtype, x.codes.device, stream)
+    else:
+        _shaped(y, "y", (R, N), dtype)
+    _check(_lib.moe_experts_matmul_fp4(x.codes.data_ptr(), x.scales.data_ptr(), _ptr(x.g),
+                                       w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.g),
+                                       _offsets(offsets, E).data_ptr(), R, E, N, K, x.format,
+                                       _typed(y, "y", 2), y.data_ptr(), _stream(stream)),
+           "moe_experts_matmul_fp4")
+    return y
+
+
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_", "Moe"))] + [
     "make_problem", "alloc_workspace", "Workspace", "load_library", "EXPORTED", "LIB_PATH",
-    "Checkpoint", "Scratch", "alloc_dispatch_scratch", "alloc_experts_scratch"]
+    "Checkpoint", "Scratch", "Fp4", "alloc_dispatch_scratch", "alloc_experts_scratch"]

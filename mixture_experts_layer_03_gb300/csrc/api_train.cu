@@ -210,23 +210,27 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
 }
 
 moe_status moe_read_timeouts(void* stream, int32_t* flags) {
-  void* word[2] = {nullptr, nullptr};
+  constexpr int kWords = 3;
+  void* word[kWords] = {};
   moe_status st = experts_timeout_word(&word[0]);
   if (st == MOE_OK) st = gate_timeout_word(&word[1]);
+  if (st == MOE_OK) st = fp4_timeout_word(&word[2]);
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int32_t v[2] = {0, 0};
+  int32_t v[kWords] = {};
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+  for (int i = 0; i < kWords && e == cudaSuccess; ++i)
     e = cudaMemcpyAsync(&v[i], word[i], sizeof(v[i]), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   // Only what was read is cleared: another stream's call may set a word meanwhile.
-  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+  int32_t any = 0;
+  for (int i = 0; i < kWords; ++i) any |= v[i];
+  for (int i = 0; i < kWords && e == cudaSuccess; ++i)
     if (v[i]) e = cudaMemsetAsync(word[i], 0, sizeof(v[i]), s);
-  if (e == cudaSuccess && (v[0] | v[1])) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && any) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "timeouts read: %s", cudaGetErrorString(e));
-  if (flags) *flags = v[0] | v[1];
-  return v[0] | v[1] ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+  if (flags) *flags = any;
+  return any ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
 
 moe_status moe_selftest_experts_wait(void* stream) {

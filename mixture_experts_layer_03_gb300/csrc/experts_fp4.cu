@@ -1,0 +1,614 @@
+// The experts' forward products over ragged groups of rows with both operands in microscaled 4 bits:
+//   y[r, n] = g_x g_w[e] sum over blocks b of sx[r, b] sw[e, n, b] sum over k of b of x[r, k] w[e, n, k]
+// for the rows r of expert e, x [R, K] and w [E, N, K] as codes with block scales (fp4.cuh).
+//
+// tcgen05.mma of block-scaled e2m1 operands takes the scales from TMEM and multiplies 64 elements of the
+// contraction an instruction, so that codes go from memory to the tensor cores as they are. One
+// persistent kernel over all groups, CTA pairs (M = 256 channels of w, N up to 224 rows of x, the
+// tiles and their order those of the 16-bit products); a block is 256 elements of the contraction, 128
+// bytes a row, by TMA with the 128-byte swizzle.
+//
+// Scales. The instruction wants those of 128 rows by 4 bytes of the contraction as 32 lanes by 4 columns
+// (row 32 i + l in lane l, column i), which tcgen05.cp writes from 512 bytes of shared memory, row l of
+// 16 bytes holding rows l, l + 32, l + 64, l + 96. A row's scales lie along the contraction in memory, so
+// four warps read 16 (mx: 8) bytes a row and block, turn 4 x 4 words over between four lanes by
+// shuffles, and write 16 bytes a lane. Each CTA needs the scales of its 128 channels and of all of the
+// tile's rows (the pair shares the rows' codes, but each tensor core scales its own half of D). Bytes
+// past the row's K / block are zeros, whatever fills the row up; codes past K are TMA's zeros.
+// TMEM: two accumulators of 224 columns, 48 columns of scales (nv: 4 x 4 for A, 4 x 8 for B), written
+// anew for every block: copies and products are issued by one thread and run in that order.
+//
+// Warp roles (448 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first CTA, MMA
+// issuer, warps 2-5 scales, warps 6-13 epilogue, four to each accumulator.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "experts_tiles.cuh"
+#include "fp4.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "tmap.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kQBK = 256;                      // contraction elements a block: 128 bytes
+constexpr int kQMost = 224;                    // rows of a tile
+constexpr int kQStages = 5;
+constexpr int kQSlotBytes = 128 * 128;         // codes of one operand of one block in one CTA
+constexpr int kQAtom = 512;                    // scales of 128 rows by 4 bytes
+constexpr int kQScaleBytes = 4 * kQAtom + 8 * kQAtom;   // of A, then of B (two atoms a word)
+constexpr int kQStageBytes = 2 * kQSlotBytes + kQScaleBytes;
+constexpr int kQScaleWarp = 2, kQScaleWarps = 4;
+constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps, kQEpiWarps = 8;
+constexpr int kQThreads = 32 * (kQEpiWarp + kQEpiWarps);
+constexpr int kQBoxBytes = 4096;               // epilogue staging of a warp
+constexpr int kQSmemBytes = 1024 + kQStages * kQStageBytes + kQEpiWarps * kQBoxBytes;
+constexpr int kQTmemCols = 512;
+constexpr int kQAccCols = kQMost;
+constexpr int kQColsA = 2 * kQAccCols, kQColsB = kQColsA + 16;   // scales' TMEM columns
+static_assert(kQColsB + 32 <= kQTmemCols, "TMEM");
+constexpr uint16_t kQPairMask = 0x3;
+
+struct Fp4Args {
+  ExpertsArgs e;
+  const uint8_t* x_scales;   // [R, pitch]
+  const uint8_t* w_scales;   // [E, N, pitch]
+  const float* x_g;          // or NULL
+  const float* w_g;          // [E] or NULL
+  int pitch;
+  int blocks;                // scale bytes of a row
+};
+
+__device__ int32_t g_fp4_timeouts;
+
+__device__ __forceinline__ void q_timeout(volatile int* abort) {
+  *abort = 1;
+  atomicOr(&g_fp4_timeouts, MOE_DEVICE_FLAG_TIMEOUT);
+}
+
+// D (+)= A B^T of the pair, 64 elements of the contraction of e2m1 with scales in TMEM.
+template <bool kNv>
+__device__ __forceinline__ void umma_fp4_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                              uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}\n" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+        "p;\n\t}\n" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales from both CTAs' shared memory to four columns of their TMEM.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t ta, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(ta), "l"(sdesc) : "memory");
+}
+
+// Rows of 16 bytes, unswizzled, 8 of them 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128u >> 4) << 32 |
+         static_cast<uint64_t>(1) << 46;
+}
+
+// kind::mxf4 and mxf4nvf4: A and B e2m1 (1 at bits 7-9 and 10-11), K-major, N >> 3 at bits 17-22, the
+// scales' type at bit 23 (0 e4m3, 1 powers of two), M >> 4 at bits 24-28; which of a word's two halves
+// holds the scales of a step of two blocks: bits 29-30 (A) and 4-5 (B).
+template <bool kNv>
+__device__ __forceinline__ uint32_t idesc_fp4(int N) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | ((kNv ? 0u : 1u) << 23) |
+         (static_cast<uint32_t>(256 >> 4) << 24);
+}
+
+template <bool kNv>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
+experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_x32,
+                   const __grid_constant__ CUtensorMap map_out, Fp4Args q) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full_bar[kQStages], scale_bar[kQStages], empty_bar[kQStages];
+  __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+  __shared__ uint16_t s_blk[kXGroups + 1];
+  __shared__ int32_t s_start[kXGroups + 1];
+
+  const ExpertsArgs& a = q.e;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool lead = rank == 0;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  uint8_t* sB = sA + kQStages * kQSlotBytes;
+  uint8_t* sS = sB + kQStages * kQSlotBytes;
+  uint8_t* sOut = sS + kQStages * kQScaleBytes;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kQStages; ++s) {
+      mbar_init(&full_bar[s], 1);                    // first CTA: its producer, and both CTAs' bytes
+      mbar_init(&scale_bar[s], 2 * kQScaleWarps);    // first CTA: both CTAs' scale warps
+      mbar_init(&empty_bar[s], 1);                   // the pair commit, delivered to both CTAs
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull_bar[s], 1);
+      mbar_init(&tempty_bar[s], kQEpiWarps);         // first CTA: four epilogue warps of each CTA
+    }
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_w);
+    tma_prefetch_map(&map_x);
+    tma_prefetch_map(&map_x32);
+    tma_prefetch_map(&map_out);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem_base, kQTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any remote arrival or copy
+  tc_fence_after();
+  pdl_wait();
+  const int G = a.E + 2;
+  if (warp == 2) scan_groups<kFwd, kQMost>(a, lane, s_blk, s_start);
+  __syncthreads();
+  const uint32_t tmem_base = s_tmem_base;
+  volatile int* abort = &s_abort;
+  const Walk walk = Walk::of<kFwd>(a);
+  const int total = walk.inner.d * s_blk[G];
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const uint32_t lead_full = mapa_shared(smem_u32(&full_bar[0]), 0);
+  const uint32_t lead_scale = mapa_shared(smem_u32(&scale_bar[0]), 0);
+  const uint32_t lead_tempty = mapa_shared(smem_u32(&tempty_bar[0]), 0);
+  const int nkb = (a.k_ext + kQBK - 1) / kQBK;       // blocks and instructions of a tile
+  const int nks = (a.k_ext + 63) / 64;
+
+  int group = 0;   // of this warp's last tile
+  auto tile = [&](int idx) {
+    return decode_tile<kFwd, false, kQMost>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
+  };
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int idx = first; idx < total && ok; idx += step) {
+      const Tile t = tile(idx);
+      if (t.nkb == 0) continue;
+      const int half = t.n >> 1;
+      const bool narrow = half <= 64;
+      const int box = narrow ? 32 : 128;
+      const bool two = half > box;
+      const CUtensorMap* mx = narrow ? &map_x32 : &map_x;
+      const uint32_t tx = kQSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) + 2 * (two ? 2 : 1) * box * 128;
+      const int n0 = t.n0 + rank * half;
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
+        if (!ok) break;
+        if (elect_one()) {
+          if (lead) mbar_arrive_expect_tx(&full_bar[stage], tx);
+          const uint32_t fb = lead_full + 8u * stage;
+          uint8_t* bs = sB + stage * kQSlotBytes;
+          if (t.m_here > 0)
+            tma_load_3d_pair(sA + stage * kQSlotBytes, &map_w, fb, kb * 128, t.m0, t.g);
+          tma_load_2d_pair(bs, mx, fb, kb * 128, n0);
+          if (two) tma_load_2d_pair(bs + 32 * 128, mx, fb, kb * 128, n0 + 32);
+        }
+        __syncwarp();
+        if (++stage == kQStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) q_timeout(abort);
+    // Every commit of a stage that was filled arrives in this CTA's barriers before it may leave.
+    volatile int never = 0;
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_wait<true>(&empty_bar[stage], phase ^ 1u, &never);
+      if (++stage == kQStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    if (lead) {
+      // ------------------------------------------------------------ MMA issuer (first CTA)
+      int stage = 0, acc = 1;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t da0 = sdesc_k_major(smem_u32(sA), 128), db0 = sdesc_k_major(smem_u32(sB), 128);
+      const uint64_t ds0 = sdesc_scales(smem_u32(sS));
+      const uint32_t sfa = tmem_base + kQColsA, sfb = tmem_base + kQColsB;
+      for (int idx = first; idx < total; idx += step) {
+        const Tile t = tile(idx);
+        acc ^= 1;
+        if (t.nkb == 0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], ~(acc_phase >> acc) & 1u, abort));
+        if (ok) tc_fence_after();
+        const uint32_t idesc = idesc_fp4<kNv>(t.n), d = tmem_base + acc * kQAccCols;
+        const bool wide = t.n > 128;
+        for (int ks = 0; ok && ks < nks; ks += 4) {
+          ok = __all_sync(0xffffffffu, mbar_wait<true>(&full_bar[stage], phase, abort) &&
+                                           mbar_wait<true>(&scale_bar[stage], phase, abort));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = da0 + ((stage * kQSlotBytes) >> 4), db = db0 + ((stage * kQSlotBytes) >> 4);
+          const uint64_t ds = ds0 + ((stage * kQScaleBytes) >> 4);
+          if (elect_one()) {
+            constexpr int kWords = kNv ? 4 : 2;   // of scales in a block
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) {
+              tmem_copy_scales_pair(sfa + 4 * j, ds + ((j * kQAtom) >> 4));
+              tmem_copy_scales_pair(sfb + 8 * j, ds + (((4 + 2 * j) * kQAtom) >> 4));
+              if (wide) tmem_copy_scales_pair(sfb + 8 * j + 4, ds + (((5 + 2 * j) * kQAtom) >> 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (ks + i >= nks) break;
+              const int j = kNv ? i : i / 2;
+              const uint32_t part = kNv ? 0u : static_cast<uint32_t>(i & 1) * 2u;
+              umma_fp4_pair<kNv>(d, da + i * 2, db + i * 2, idesc | part << 29 | part << 4, sfa + 4 * j,
+                                 sfb + 8 * j, (ks | i) != 0);
+            }
+            umma_commit_pair(&empty_bar[stage], kQPairMask);
+          }
+          __syncwarp();
+          if (++stage == kQStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) {
+          q_timeout(abort);
+          break;
+        }
+        if (elect_one()) umma_commit_pair(&tfull_bar[acc], kQPairMask);
+        __syncwarp();
+        acc_phase ^= 1u << acc;
+      }
+      if (!ok) {
+        // Every MMA issued so far ends (bounded wait) before TMEM is released.
+        if (elect_one()) umma_commit_pair(&drain_bar, 0x1);
+        volatile int never = 0;
+        mbar_wait(&drain_bar, 0, &never);
+      }
+    }
+  } else if (warp < kQEpiWarp) {
+    // ------------------------------------------------------------ scales (both CTAs)
+    // This warp's rows of each 128: l = 8 * w .. + 7 in lanes by rows l, l + 32, l + 64, l + 96; what is
+    // read lies kAhead blocks before what is written.
+    constexpr int kAhead = 4;
+    constexpr int kWords = kNv ? 4 : 2;
+    const int l = 8 * (warp - kQScaleWarp) + (lane & 7), i = lane >> 3;
+    const int row = l + 32 * i;
+    int idx = first, kb = 0;       // the block to read next
+    Tile t = {};
+    auto settle = [&] {            // idx at a tile that multiplies something
+      while (idx < total) {
+        t = tile(idx);
+        if (t.nkb > 0) break;
+        idx += step;
+      }
+    };
+    settle();
+    uint4 ring[kAhead][3];
+    auto words = [&](const uint8_t* p, bool there, int at) {   // of a row's scales from byte `at` on
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (there) {
+        if (kNv) {
+          v = __ldg(reinterpret_cast<const uint4*>(p + at));
+        } else {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + at));
+          v.x = u.x;
+          v.y = u.y;
+        }
+        const int left = q.blocks - at;   // bytes that are scales
+        if (left < 4 * kWords) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            const int n = left - 4 * j;
+            if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
+          }
+        }
+      }
+      return v;
+    };
+    auto read = [&](uint4 (&r)[3]) {
+      if (idx >= total) return;
+      const int at = kb * 4 * kWords;
+      r[0] = words(q.w_scales + (static_cast<int64_t>(t.g) * a.m_ext + t.m0 + row) * q.pitch, row < t.m_here, at);
+      const uint8_t* xs = q.x_scales + static_cast<int64_t>(t.n0 + row) * q.pitch;
+      r[1] = words(xs, row < t.n_here, at);
+      if (t.n > 128) r[2] = words(xs + static_cast<int64_t>(128) * q.pitch, row + 128 < t.n_here, at);
+      if (++kb == nkb) {
+        kb = 0;
+        idx += step;
+        settle();
+      }
+    };
+    // 4 x 4 words between lanes i = 0..3 of the same l: lane i gets word i of each.
+    auto turn = [&](uint4 v) {
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // words whose index differs from i in bit 0, then in bit 1, change places
+      {
+        const bool odd = i & 1;
+        const uint32_t s0 = odd ? w[0] : w[1], s1 = odd ? w[2] : w[3];
+        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 8), r1 = __shfl_xor_sync(0xffffffffu, s1, 8);
+        if (odd) {
+          w[0] = r0;
+          w[2] = r1;
+        } else {
+          w[1] = r0;
+          w[3] = r1;
+        }
+      }
+      {
+        const bool high = i & 2;
+        const uint32_t s0 = high ? w[0] : w[2], s1 = high ? w[1] : w[3];
+        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 16), r1 = __shfl_xor_sync(0xffffffffu, s1, 16);
+        if (high) {
+          w[0] = r0;
+          w[1] = r1;
+        } else {
+          w[2] = r0;
+          w[3] = r1;
+        }
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    int left = 0;                  // blocks to write
+    {
+      const int g0 = group;
+      group = 0;
+      for (int id = first; id < total; id += step) left += tile(id).nkb > 0 ? nkb : 0;
+      group = g0;
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) read(ring[b]);
+    bool ok = true;
+    while (left > 0 && ok) {
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        if (left == 0 || !ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
+        if (!ok) break;
+        uint8_t* dst = sS + stage * kQScaleBytes + l * 16;
+        const uint4 va = turn(ring[b][0]), vb = turn(ring[b][1]), vc = turn(ring[b][2]);
+        if (i < kWords) {
+          *reinterpret_cast<uint4*>(dst + i * kQAtom) = va;
+          *reinterpret_cast<uint4*>(dst + (4 + 2 * i) * kQAtom) = vb;
+          *reinterpret_cast<uint4*>(dst + (5 + 2 * i) * kQAtom) = vc;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (lead) mbar_arrive(&scale_bar[stage]);
+          else mbar_arrive_cluster(lead_scale + 8u * stage);
+        }
+        read(ring[b]);
+        --left;
+        if (++stage == kQStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) q_timeout(abort);
+  } else {
+    // -------------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;   // TMEM lane quarter of this warp
+    const int acc = (warp - kQEpiWarp) >> 2;
+    uint8_t* buf = sOut + (warp - kQEpiWarp) * kQBoxBytes;
+    const uint32_t tb = tmem_base + acc * kQAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    int sbuf = 0;
+    uint32_t acc_phase = 0;
+    const bool f16 = a.f16 != 0;
+    const float gx = q.x_g ? __ldg(q.x_g) : 1.0f;
+    for (int idx = first + acc * step; idx < total; idx += 2 * step) {
+      const Tile t = tile(idx);
+      const bool zeros = t.nkb == 0;
+      if (!zeros) {
+        const bool got = mbar_wait<true>(&tfull_bar[acc], acc_phase, abort);
+        if (!__all_sync(0xffffffffu, got)) {
+          q_timeout(abort);
+          break;
+        }
+        tc_fence_after();
+        acc_phase ^= 1u;
+      }
+      auto done = [&] {
+        if (zeros) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (lead) mbar_arrive(&tempty_bar[acc]);
+          else mbar_arrive_remote(lead_tempty + 8u * acc);
+        }
+      };
+      if (32 * quarter >= t.m_here) {
+        done();
+        continue;
+      }
+      const float gain = gx * (q.w_g && !zeros ? __ldg(q.w_g + t.g) : 1.0f);
+      const int ch = t.m0 + 32 * quarter;
+      // 32 channels by 32 rows at a time, as the 16-bit products' epilogue: read in matrix fragments,
+      // turned over by the matrix store into a box of 32 rows of 64 bytes, out by TMA.
+#pragma unroll 1
+      for (int r0 = 0; r0 < t.n_here; r0 += 32) {
+        uint32_t v[2][16];
+        if (!zeros) {
+          tmem_issue_fragments(tb + r0, v[0]);
+          tmem_issue_fragments(tb + r0 + (16u << 16), v[1]);
+          tmem_wait();
+          tmem_ready(v[0]);
+          tmem_ready(v[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = 0;
+        }
+        if (r0 + 32 >= t.n_here) done();
+        uint32_t p[16];   // [channels 8 b .. + 7][rows 8 i .. + 7]: p[4 i + b]
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            p[4 * i + b] = pack_16bit(gain * __uint_as_float(v[b >> 1][4 * i + 2 * (b & 1)]),
+                                      gain * __uint_as_float(v[b >> 1][4 * i + 2 * (b & 1) + 1]), f16);
+        uint8_t* box = buf + sbuf * (kQBoxBytes / 2);
+        if (lane == 0) bulk_wait_group_read<1>();   // what was stored from this box before is out
+        __syncwarp();
+        const uint32_t at = smem_u32(box) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          stmatrix_trans(at + i * 512, p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+        const int rows = t.n_here - r0;
+        if (rows < 32) {
+          __syncwarp();
+          const int c = lane & 3;   // chunk of 8 channels; m_ext is a multiple of 8
+          if (32 * quarter + 8 * c < t.m_here) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                            static_cast<int64_t>(t.n0 + r0) * a.m_ext + ch + 8 * c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2);
+              if (r < rows)
+                *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * a.m_ext) =
+                    *reinterpret_cast<const uint4*>(box + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            }
+          }
+          break;   // a tile's last box
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&map_out, box, ch, t.n0 + r0);
+          bulk_commit_group();
+        }
+        sbuf ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kQTmemCols);
+  }
+  // No CTA leaves while the other may still write into it or arrive on its barriers.
+  cluster_sync();
+}
+
+// Bytes [planes, rows, cols] (planes 0: a matrix), boxes of 128 by box_rows with the 128-byte swizzle.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
+                  uint32_t box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols, rows * cols};
+  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, planes ? 3 : 2, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kNv>
+moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mx32,
+                      const CUtensorMap& mo, const Fp4Args& q, int64_t tiles, cudaStream_t s) {
+  static std::atomic<int> clusters_dev[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(MOE_ERR_CUDA, "cudaGetDevice failed");
+  int have = clusters_dev[dev].load(std::memory_order_acquire);
+  if (!have) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        experts_fp4_kernel<kNv>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmemBytes);
+    if (e != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    const int sms = device_sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+    cfg.blockDim = dim3(kQThreads, 1, 1);
+    cfg.dynamicSmemBytes = kQSmemBytes;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, experts_fp4_kernel<kNv>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();   // clear the failed query; fall back to one cluster per SM pair
+      n = sms / 2;
+    }
+    clusters_dev[dev].store(n, std::memory_order_release);
+    have = n;
+  }
+  const unsigned pairs = static_cast<unsigned>(have < tiles ? have : tiles);
+  const cudaError_t err = launch_pdl(experts_fp4_kernel<kNv>, dim3(2 * pairs), dim3(kQThreads),
+                                     kQSmemBytes, s, mw, mx, mx32, mo, q);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "experts_fp4 launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status fp4_timeout_word(void** word) {
+  const cudaError_t e = cudaGetSymbolAddress(word, g_fp4_timeouts);
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
+
+moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const int32_t* offsets, int64_t R,
+                              int E, int N, int K, int fmt, int dtype, void* y, cudaStream_t s) {
+  CUtensorMap mw, mx, mx32, mo;
+  EncodeTiledFn enc = get_encode_fn();
+  bool ok = enc && encode_codes(&mw, w.codes, E, N, K / 2, 128) &&
+            encode_codes(&mx, x.codes, 0, R, K / 2, 128) && encode_codes(&mx32, x.codes, 0, R, K / 2, 32);
+  if (ok) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(R)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * 2};
+    cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    ok = enc(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  if (!ok) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  Fp4Args q = {};
+  q.e.offsets = offsets;
+  q.e.E = E;
+  q.e.R = static_cast<int32_t>(R);
+  q.e.m_ext = N;
+  q.e.k_ext = K;
+  q.e.f16 = dtype == MOE_DTYPE_F16;
+  q.e.out = y;
+  q.x_scales = x.scales;
+  q.w_scales = w.scales;
+  q.x_g = x.g;
+  q.w_g = w.g;
+  q.pitch = fp4_scale_pitch(K, fmt);
+  q.blocks = K / fp4_block(fmt);
+  const int64_t tiles = (R / kQMost + E + 2) * ((N + 255) / 256);
+  return fmt == kFp4Nv ? launch_fp4<true>(mw, mx, mx32, mo, q, tiles, s)
+                       : launch_fp4<false>(mw, mx, mx32, mo, q, tiles, s);
+}
+
+}  // namespace moe

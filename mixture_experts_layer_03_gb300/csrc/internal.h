@@ -148,8 +148,28 @@ moe_status launch_experts_dw(const void* dy, const void* x, const int32_t* offse
                              int E, int N, int K, int dtype, int out_dtype, bool add, void* dw,
                              char* ws, size_t ws_bytes, cudaStream_t s);
 
+// ---- microscaled 4-bit operands (quant_fp4.cu, experts_fp4.cu); fmt: a moe_fp4_format
+
+// Rows of K channels: codes [rows, K / 2], scales [rows, pitch], g one f32 a plane or NULL (1).
+struct Fp4Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* g;
+};
+
+// x [planes, rows, K], or (swiglu) gu [rows, 2K]
+moe_status launch_quantize_fp4(const void* x, int64_t planes, int64_t rows, int K, int dtype, int fmt,
+                               bool swiglu, const float* g, uint8_t* codes, uint8_t* scales,
+                               cudaStream_t s);
+moe_status launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* g,
+                                 int64_t planes, int64_t rows, int K, int fmt, int dtype, void* out,
+                                 cudaStream_t s);
+moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const int32_t* offsets, int64_t R,
+                              int E, int N, int K, int fmt, int dtype, void* y, cudaStream_t s);
+
 // Device words in which the products' and the gate's kernels note that a wait ran out.
 moe_status experts_timeout_word(void** word);
+moe_status fp4_timeout_word(void** word);
 moe_status gate_timeout_word(void** word);
 moe_status launch_experts_wait_selftest(cudaStream_t s);
 

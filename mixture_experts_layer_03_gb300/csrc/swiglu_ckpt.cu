@@ -22,31 +22,13 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "rows.cuh"
+#include "segments.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kCkptThreads = 128;
 constexpr int kCkptBlock = 32;     // channels that share a scale
-constexpr int kPerLane = 8;        // channels a lane holds in the vector form
 constexpr uint32_t kNanScale = 255;
-
-// sigma(g) and 1 - sigma(g). For 16-bit results by the fast exponential and quotient, whose error of 2 +
-// 1.17 |g| units of 2^-23 (under 2^-16 where sigma is not 0) is small beside the one rounding of the
-// result (2^-9 or 2^-12). For f32 ones from exp(-|g|): a few units at any g, and 1 - sigma without
-// cancellation. f32, forward and backward with h, the one way and the other: 8192 x 14336 245 and 325 us,
-// 243 and 370; 1941 x 13603, bound by instructions, 67 and 94, 60 and 88.
-template <typename T>
-__device__ __forceinline__ float2 sigmoid_of(float g) {
-  if constexpr (sizeof(T) == 4) {
-    const float t = expf(-fabsf(g));
-    const float big = 1.0f / (1.0f + t), small = t * big;
-    return g < 0.0f ? make_float2(small, big) : make_float2(big, small);
-  } else {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-    return make_float2(s, 1.0f - s);
-  }
-}
 
 // The scale byte of a block: the least e >= -127 with amax <= 448 * 2^e = 1.75 * 2^(e + 8).
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
@@ -106,65 +88,16 @@ __device__ __forceinline__ void dequant8(uint2 q, float scale, float (&f)[kPerLa
   }
 }
 
-// 8 elements of T as one or two 16-byte vectors.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[kPerLane]) {
-  constexpr int kN = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-  for (int h = 0; h < kPerLane / kN; ++h) {
-    float part[kN];
-    Vec<T, 16>::unpack(__ldg(reinterpret_cast<const uint4*>(p) + h), part);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) f[h * kN + i] = part[i];
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[kPerLane]) {
-  constexpr int kN = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-  for (int h = 0; h < kPerLane / kN; ++h) {
-    float part[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) part[i] = f[h * kN + i];
-    reinterpret_cast<uint4*>(p)[h] = Vec<T, 16>::pack(part);
-  }
-}
-
-// The work of a warp, one after the other: (row, segment) pairs, a segment 256 channels, four
-// lanes to a block of 32. Stepping (row, segment) by the grid's share keeps divisions out.
-struct Walk {
-  int64_t row;
-  int seg;
-  int64_t row_step;
-  int seg_step, segs;
-  __device__ __forceinline__ Walk(int segs_) : segs(segs_) {
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kCkptThreads + threadIdx.x) >> 5;
-    const int64_t n = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
-    row = w / segs_;
-    seg = static_cast<int>(w - row * segs_);
-    row_step = n / segs_;
-    seg_step = static_cast<int>(n - row_step * segs_);
-  }
-  __device__ __forceinline__ void next() {
-    row += row_step;
-    seg += seg_step;
-    if (seg >= segs) {
-      seg -= segs;
-      ++row;
-    }
-  }
-};
-
 // Rows whose halves start on 16-byte boundaries (I % 8 == 0): 8 channels a lane.
 template <typename T>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kSegmentThreads)
 swiglu_ckpt_kernel(const T* __restrict__ gu, int64_t R, int I, T* __restrict__ h,
                    uint8_t* __restrict__ q, uint8_t* __restrict__ qs) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((I + 255) / 256); w.row < R; w.next()) {
+  for (SegmentWalk w((I + 255) / 256); w.row < R; w.next()) {
     const int c = w.seg * 256 + lane * kPerLane;
     const bool in = c < I;
     float g[kPerLane] = {}, u[kPerLane] = {};
@@ -202,7 +135,7 @@ __device__ __forceinline__ void grad_of(float dh, float g, float u, float* dg, f
 }
 
 template <typename T, bool kWantH>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kSegmentThreads)
 swiglu_ckpt_grad_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
                         const uint8_t* __restrict__ qs, int64_t R, int I, T* __restrict__ dgu,
                         T* __restrict__ h) {
@@ -210,7 +143,7 @@ swiglu_ckpt_grad_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((I + 255) / 256); w.row < R; w.next()) {
+  for (SegmentWalk w((I + 255) / 256); w.row < R; w.next()) {
     const int c = w.seg * 256 + lane * kPerLane;
     if (c >= I) continue;
     const uint8_t* src = q + w.row * 2 * I + c;
@@ -289,14 +222,14 @@ __device__ __forceinline__ void ckpt_segment(const T* src, int I, int c0, T* h, 
 }
 
 template <typename T, int kBlocks>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kSegmentThreads)
 swiglu_ckpt_any_kernel(const T* __restrict__ gu, int64_t R, int I, T* __restrict__ h,
                        uint8_t* __restrict__ q, uint8_t* __restrict__ qs) {
   pdl_trigger();
   pdl_wait();
   constexpr int kSegment = kBlocks * kCkptBlock;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
+  for (SegmentWalk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
     const int c0 = w.seg * kSegment;
     const int64_t at = w.row * I;
     if (c0 + kSegment <= I)
@@ -338,7 +271,7 @@ __device__ __forceinline__ void ckpt_grad_segment(const T* dh, const uint8_t* q,
 }
 
 template <typename T, int kBlocks, bool kWantH>
-__global__ void __launch_bounds__(kCkptThreads)
+__global__ void __launch_bounds__(kSegmentThreads)
 swiglu_ckpt_grad_any_kernel(const T* __restrict__ dh, const uint8_t* __restrict__ q,
                             const uint8_t* __restrict__ qs, int64_t R, int I, T* __restrict__ dgu,
                             T* __restrict__ h) {
@@ -346,7 +279,7 @@ swiglu_ckpt_grad_any_kernel(const T* __restrict__ dh, const uint8_t* __restrict_
   pdl_wait();
   constexpr int kSegment = kBlocks * kCkptBlock;
   const int nb = (I + kCkptBlock - 1) / kCkptBlock;
-  for (Walk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
+  for (SegmentWalk w((I + kSegment - 1) / kSegment); w.row < R; w.next()) {
     const int c0 = w.seg * kSegment;
     const int64_t at = w.row * I;
     if (c0 + kSegment <= I)
@@ -358,28 +291,18 @@ swiglu_ckpt_grad_any_kernel(const T* __restrict__ dh, const uint8_t* __restrict_
   }
 }
 
-// Small blocks, four times as many as are resident: a block's warps then end, and their successors'
-// loads begin, at different times. At 8192 x 14336 bf16, forward and backward with h: 149 and 175
-// us (950 MB at 6.36 TB/s, 1.18 GB at 6.75); blocks of 256 threads 162 and 175; eight of those an
-// SM, all resident, 169 and 197.
-unsigned ckpt_grid(int64_t R, int segs) {
-  const int64_t blocks = (R * segs + kCkptThreads / 32 - 1) / (kCkptThreads / 32);
-  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 64;
-  return static_cast<unsigned>(blocks < cap ? blocks : cap);
-}
-
 template <typename T>
 cudaError_t forward_t(const void* gu, int64_t R, int I, void* h, uint8_t* q, uint8_t* qs,
                       cudaStream_t s) {
   if (I % kPerLane == 0)
-    return launch_pdl(swiglu_ckpt_kernel<T>, dim3(ckpt_grid(R, (I + 255) / 256)),
-                      dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I,
+    return launch_pdl(swiglu_ckpt_kernel<T>, dim3(segment_grid(R, (I + 255) / 256)),
+                      dim3(kSegmentThreads), 0, s, static_cast<const T*>(gu), R, I,
                       static_cast<T*>(h), q, qs);
   if (I <= 128)
-    return launch_pdl(swiglu_ckpt_any_kernel<T, 4>, dim3(ckpt_grid(R, 1)), dim3(kCkptThreads), 0, s,
+    return launch_pdl(swiglu_ckpt_any_kernel<T, 4>, dim3(segment_grid(R, 1)), dim3(kSegmentThreads), 0, s,
                       static_cast<const T*>(gu), R, I, static_cast<T*>(h), q, qs);
-  return launch_pdl(swiglu_ckpt_any_kernel<T, 8>, dim3(ckpt_grid(R, (I + 255) / 256)),
-                    dim3(kCkptThreads), 0, s, static_cast<const T*>(gu), R, I, static_cast<T*>(h), q,
+  return launch_pdl(swiglu_ckpt_any_kernel<T, 8>, dim3(segment_grid(R, (I + 255) / 256)),
+                    dim3(kSegmentThreads), 0, s, static_cast<const T*>(gu), R, I, static_cast<T*>(h), q,
                     qs);
 }
 
@@ -387,15 +310,15 @@ template <typename T, bool kWantH>
 cudaError_t backward_t(const void* dh, const uint8_t* q, const uint8_t* qs, int64_t R, int I,
                        void* dgu, void* h, cudaStream_t s) {
   if (I % kPerLane == 0)
-    return launch_pdl(swiglu_ckpt_grad_kernel<T, kWantH>, dim3(ckpt_grid(R, (I + 255) / 256)),
-                      dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
+    return launch_pdl(swiglu_ckpt_grad_kernel<T, kWantH>, dim3(segment_grid(R, (I + 255) / 256)),
+                      dim3(kSegmentThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                       static_cast<T*>(dgu), static_cast<T*>(h));
   if (I <= 128)
-    return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 4, kWantH>, dim3(ckpt_grid(R, 1)),
-                      dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
+    return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 4, kWantH>, dim3(segment_grid(R, 1)),
+                      dim3(kSegmentThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                       static_cast<T*>(dgu), static_cast<T*>(h));
-  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 8, kWantH>, dim3(ckpt_grid(R, (I + 255) / 256)),
-                    dim3(kCkptThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
+  return launch_pdl(swiglu_ckpt_grad_any_kernel<T, 8, kWantH>, dim3(segment_grid(R, (I + 255) / 256)),
+                    dim3(kSegmentThreads), 0, s, static_cast<const T*>(dh), q, qs, R, I,
                     static_cast<T*>(dgu), static_cast<T*>(h));
 }
 
