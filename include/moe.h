@@ -426,7 +426,7 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
                                  size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products (above, or on
- * 4-bit operands) or of the gate ran out in any call on the current GPU, with a workspace or without, since the last read.
+ * 4-bit operands), of the gate or of moe_layer_few ran out in any call on the current GPU, with a workspace or without, since the last read.
  * Such a call's results are incomplete. *flags (may be NULL) receives MOE_DEVICE_FLAG_TIMEOUT or 0.
  * Returns MOE_ERR_DEVICE_TIMEOUT when one did, else MOE_OK. */
 moe_status moe_read_timeouts(void* stream, int32_t* flags);
@@ -483,6 +483,36 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
                                   const uint8_t* w_codes, const uint8_t* w_scales, const float* w_g,
                                   const int32_t* offsets, int64_t R, int32_t E, int32_t N, int32_t K,
                                   moe_fp4_format format, moe_dtype dtype, void* y, void* stream);
+
+/* The whole layer for a few tokens, in two kernels: moe_gate_route and moe_forward (with the shared
+ * expert's gate, moe_forward_partial's) of T <= MOE_FEW_TOKENS tokens without the launches between them.
+ *   p        T, H, I, E, k and shared_I (0: no shared expert); H, I and shared_I multiples of 32, H up to
+ *            32768, I and shared_I to 65536
+ *   route    as moe_route takes it, num_experts = E, top_k = k
+ *   x [T, H], wg [E (+ 1), H] of `dtype` (BF16 or F16); shared_gate 1: wg's last row is the shared
+ *            expert's gate, whose sigmoid is its weight, 0: weight 1
+ *   w13 [E, 2I, H], w2 [E, H, I], w13_s [2 shared_I, H], w2_s [H, shared_I] (NULL without a shared expert)
+ *            all of `dtype` (weights = MOE_WEIGHTS_16BIT), or all in 4 bits of one moe_fp4_format, g one
+ *            f32 an expert (one for the shared expert's) or NULL
+ * Writes y [T, H], ids int32 [T, k] and scales fp32 [T, k]. Between the products h, times its routing
+ * weight, is rounded once: to bf16, or (f16 and 4-bit weights) to 11 bits beside its token's largest.
+ * x and wg are not rounded, sums are fp32. Experts that no token chose are not read. The results are the
+ * same on every run. Workspace: moe_layer_few_workspace_bytes, 256-byte aligned, nothing of it has to be
+ * set; calls that share one must be ordered. Whether a bounded wait ran out: moe_read_timeouts. */
+#define MOE_FEW_TOKENS 16
+#define MOE_WEIGHTS_16BIT (-1)
+typedef struct {
+  const void* w;          /* elements, or 4-bit codes */
+  const uint8_t* scales;  /* of 4-bit weights, else NULL */
+  const float* g;         /* of NV weights, or NULL */
+} moe_weights;
+/* 0 outside the limits. */
+size_t moe_layer_few_workspace_bytes(const moe_problem* p);
+moe_status moe_layer_few(const moe_problem* p, const moe_route_params* route, const void* x,
+                         const void* wg, int32_t shared_gate, const float* bias, const moe_weights* w13,
+                         const moe_weights* w2, const moe_weights* w13_s, const moe_weights* w2_s,
+                         int32_t weights, moe_dtype dtype, int32_t* ids, float* scales, void* y,
+                         void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

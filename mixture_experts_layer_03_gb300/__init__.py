@@ -48,6 +48,8 @@ MOE_DTYPE_F32 = 2
 
 MOE_FP4_MX = 0
 MOE_FP4_NV = 1
+MOE_WEIGHTS_16BIT = -1
+MOE_FEW_TOKENS = 16
 
 MOE_DEVICE_FLAG_BAD_ID = 1
 MOE_DEVICE_FLAG_TIMEOUT = 2
@@ -62,6 +64,10 @@ class MoeRouteParams(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("method", ctypes.c_int32), ("n_group", ctypes.c_int32),
                 ("topk_group", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float)]
+
+
+class MoeWeights(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("g", ctypes.c_void_p)]
 
 
 class MoeWsLayout(ctypes.Structure):
@@ -146,6 +152,10 @@ _SIGS = {
     "moe_experts_matmul_fp4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
                                               ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                               ctypes.c_int, ctypes.c_int, _P, _P]),
+    "moe_layer_few_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(MoeProblem)]),
+    "moe_layer_few": (ctypes.c_int, [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeRouteParams), _P, _P,
+                                     ctypes.c_int32, _P] + [ctypes.POINTER(MoeWeights)] * 4 +
+                      [ctypes.c_int32, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -956,6 +966,77 @@ def moe_experts_matmul_fp4(x: Fp4, w: Fp4, offsets, dtype=torch.bfloat16, y=None
     return y
 
 
+def alloc_few_scratch(problem: MoeProblem, device="cuda", stream=None) -> Scratch:
+    """Workspace of moe_layer_few, for calls on `stream` (None: the current one)."""
+    n = _lib.moe_layer_few_workspace_bytes(ctypes.byref(problem))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_layer_few_workspace_bytes")
+    return Scratch(_new(n, torch.uint8, device, stream, result=False))
+
+
+def _few_weights(w, name: str, shape: tuple, format: int, dtype) -> MoeWeights:
+    """A weight of moe_layer_few: an Fp4 of `format`, or a tensor of `dtype`, of just this shape."""
+    if format == MOE_WEIGHTS_16BIT:
+        if isinstance(w, Fp4):
+            raise ValueError(f"{name} must be a tensor of {dtype} as the other weights are")
+        return MoeWeights(_shaped(w, name, shape, dtype).data_ptr(), None, None)
+    if not isinstance(w, Fp4) or w.format != format or w.shape != shape:
+        raise ValueError(f"{name} must be {shape} in 4 bits of the same format as w13, got "
+                         f"{tuple(getattr(w, 'shape', ()))}")
+    return MoeWeights(w.codes.data_ptr(), w.scales.data_ptr(), _ptr(w.g))
+
+
+def moe_layer_few(x, wg, w13, w2, method: int, top_k: int, bias: Optional[torch.Tensor] = None,
+                  n_group: int = 1, topk_group: int = 1, routed_scaling_factor: float = 1.0,
+                  w13_s=None, w2_s=None, y=None, ids=None, scales=None,
+                  scratch: Optional[Scratch] = None, stream=None):
+    """The whole layer for up to MOE_FEW_TOKENS tokens, in two kernels: gate, routing, the chosen experts
+    (and the shared one) and the weighted sum. x [T, H] and wg [E, H] in bfloat16 or float16; w13
+    [E, 2I, H] and w2 [E, H, I] (w13_s [2Is, H], w2_s [H, Is]) of the same type, or all Fp4 of one
+    format. A wg with E + 1 rows carries the shared expert's gate in its last row. Routing parameters as
+    moe_route's. Returns (y [T, H], ids int32 [T, k], scales fp32 [T, k]). moe_read_timeouts says whether
+    a wait ran out."""
+    code = _typed(x, "x", 2)
+    if code == MOE_DTYPE_F32:
+        raise ValueError("x must be bfloat16 or float16, got torch.float32")
+    T, H = x.shape
+    format = w13.format if isinstance(w13, Fp4) else MOE_WEIGHTS_16BIT
+    if len(w13.shape) != 3:
+        raise ValueError(f"w13 must be [E, 2I, {H}], got {tuple(w13.shape)}")
+    E, I = w13.shape[0], w13.shape[1] // 2
+    if wg.dim() != 2 or wg.shape[0] - E not in (0, 1):
+        raise ValueError(f"wg must be [{E} or {E + 1}, {H}], got {tuple(wg.shape)}")
+    gate = wg.shape[0] - E
+    _shaped(wg, "wg", (E + gate, H), x.dtype)
+    a = _few_weights(w13, "w13", (E, 2 * I, H), format, x.dtype)
+    b = _few_weights(w2, "w2", (E, H, I), format, x.dtype)
+    a_s = b_s = None
+    shared_I = 0
+    if w13_s is not None or w2_s is not None:
+        if w13_s is None or w2_s is None:
+            raise ValueError("w13_s and w2_s belong together")
+        shared_I = w13_s.shape[0] // 2
+        a_s = ctypes.byref(_few_weights(w13_s, "w13_s", (2 * shared_I, H), format, x.dtype))
+        b_s = ctypes.byref(_few_weights(w2_s, "w2_s", (H, shared_I), format, x.dtype))
+    if bias is not None:
+        _shaped(bias, "bias", (E,), torch.float32)
+    y = _like(x, y, "y", (T, H), stream)
+    ids = (_new((T, top_k), torch.int32, x.device, stream) if ids is None
+           else _shaped(ids, "ids", (T, top_k), torch.int32))
+    scales = (_new((T, top_k), torch.float32, x.device, stream) if scales is None
+              else _shaped(scales, "scales", (T, top_k), torch.float32))
+    p = MoeProblem(T, H, I, E, top_k, shared_I)
+    if scratch is None:
+        n = _lib.moe_layer_few_workspace_bytes(ctypes.byref(p))
+        scratch = Scratch(_new(n, torch.uint8, x.device, stream, result=False))
+    r = MoeRouteParams(E, top_k, method, n_group, topk_group, routed_scaling_factor)
+    _check(_lib.moe_layer_few(ctypes.byref(p), ctypes.byref(r), x.data_ptr(), wg.data_ptr(), gate,
+                              _ptr(bias), ctypes.byref(a), ctypes.byref(b), a_s, b_s, format, code,
+                              ids.data_ptr(), scales.data_ptr(), y.data_ptr(), scratch.ptr,
+                              scratch.nbytes, _stream(stream)), "moe_layer_few")
+    return y, ids, scales
+
+
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_", "Moe"))] + [
     "make_problem", "alloc_workspace", "Workspace", "load_library", "EXPORTED", "LIB_PATH",
-    "Checkpoint", "Scratch", "Fp4", "alloc_dispatch_scratch", "alloc_experts_scratch"]
+    "Checkpoint", "Scratch", "Fp4", "alloc_dispatch_scratch", "alloc_few_scratch", "alloc_experts_scratch"]

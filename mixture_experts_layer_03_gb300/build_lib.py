@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "route.cu", "permute.cu", "grouped_gemm.cu", "finalize.cu", "gate.cu",
            "selftest.cu", "dispatch.cu", "swiglu_ckpt.cu", "experts_matmul.cu", "experts_few.cu",
            "route_backward.cu", "api_train.cu", "quant_fp4.cu", "experts_fp4.cu",
-           "api_serve.cu"]
+           "few.cu", "api_serve.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -31,6 +31,11 @@ int32_t problem_reason(const moe_problem& p) {
   return MOE_REASON_OK;
 }
 
+// Per-device SM counts, filled on first use (any thread may fill one; all write the same).
+std::atomic<int> g_sm_count[64];
+
+}  // namespace
+
 int32_t route_reason(int64_t T, const moe_route_params& r) {
   if (T < 0 || T > (int64_t{1} << 31) / 8) return MOE_REASON_T_RANGE;
   if (r.num_experts < 1 || r.num_experts > 256) return MOE_REASON_E_RANGE;
@@ -70,11 +75,6 @@ int32_t route_reason(int64_t T, const moe_route_params& r) {
       return MOE_REASON_METHOD;
   }
 }
-
-// Per-device SM counts, filled on first use (any thread may fill one; all write the same).
-std::atomic<int> g_sm_count[64];
-
-}  // namespace
 
 moe_status set_error(moe_status s, const char* fmt, ...) {
   va_list ap;

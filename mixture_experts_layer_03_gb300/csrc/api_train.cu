@@ -210,11 +210,12 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
 }
 
 moe_status moe_read_timeouts(void* stream, int32_t* flags) {
-  constexpr int kWords = 3;
+  constexpr int kWords = 4;
   void* word[kWords] = {};
   moe_status st = experts_timeout_word(&word[0]);
   if (st == MOE_OK) st = gate_timeout_word(&word[1]);
   if (st == MOE_OK) st = fp4_timeout_word(&word[2]);
+  if (st == MOE_OK) st = few_timeout_word(&word[3]);
   if (st != MOE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t v[kWords] = {};

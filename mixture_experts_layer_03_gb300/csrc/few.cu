@@ -1,0 +1,1010 @@
+// The whole layer for a few tokens (T <= 16) in two kernels:
+//   few_gate_kernel   logits = x wg^T, fp32
+//   few_layer_kernel  routing, both products of the chosen experts and of the shared one, the weighted
+//                     sum:  y[t] = sum over slots j of s[t, j] w2[e] (silu(g) u),  g, u = w13[e] x[t]
+// For a few tokens the layer reads each chosen expert's weights once and little else: the floor is
+// their bytes at the memory's rate, and what is added to it is latency, between kernels and between the
+// two products. So one block an SM stays for the whole layer, and one warp of it (the weights'
+// producer) keeps its ring full from the moment the experts are known, on into the second products'
+// weights while the first products' results are still awaited.
+//
+// Work. Tickets 0..n-1 are slices of the first products: the chosen experts' I channels one after the
+// other (a channel is its gate and its up row), cut into n equal parts to a channel, n blocks. Tickets
+// n..2n-1 are slices of the H rows of the second products, over all experts. A block takes tickets
+// in order until none is left; a slice of the second products waits for the first ones' results, which
+// are in blocks that run already, so that blocks that are not resident yet are waited for by nobody.
+// Every element of h and of y is summed by one block in one order: the same result on every run.
+//
+// Products by mma.sync m16n8k16: 16 rows of weights by 8 tokens, so that one pass over a weight serves all
+// tokens. (tcgen05's least M = 128 rows do not fit slices of some dozen rows; and mma.sync, 8 cycles an
+// instruction on an SM quarter, is used for a third of the time or less: a block's share of the
+// bandwidth brings 16 x 16 weights of 16 bits every 84 cycles, of 4 bits every 25.) All T tokens are
+// columns for every expert, which keeps lists of tokens out of the loops: in the first products the others'
+// results are dropped, in the second an expert's sums are added to those of its tokens only (a weight
+// that is not finite reaches nobody else); the routing weight is multiplied into h.
+// The eight consumer warps cut a chunk of the contraction between them and add up at the end.
+//
+// Numbers. 16-bit weights: operands of x's type, h rounded to it once (with the routing weight; f16 after
+// a power of two for each token, see below). 4-bit weights: codes to f16 exactly; nv scales
+// multiplied in f16, exactly (6 significant bits, 2^-10 to 2688); mx scales, which f16 does not reach,
+// by an FMA a block of 32 on its fp32 sum. x and h go to f16 times a power of two for each token
+// that brings the largest to [2^14, 2^15): x of 8 or 11 significant bits is exact but for what is less
+// than 2^-29 of the token's largest, h is rounded to 11 bits. Sums, SwiGLU and the sum over experts: fp32.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "route_device.cuh"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kFewTokens = MOE_FEW_TOKENS;
+static_assert(kFewTokens == 16, "two column tiles");
+constexpr int kFewExperts = 128 + 1;             // T * k at most, and the shared one
+constexpr int kMmaWarps = 8;                     // consumers
+constexpr int kXWarps = 4;                       // producers of the tokens' side
+constexpr int kWarpW = kMmaWarps, kWarpX = kMmaWarps + 1;
+constexpr int kFewThreads = 32 * (kMmaWarps + 1 + kXWarps);
+constexpr int kXSlots = kXWarps;                 // each of 512 channels of all tokens
+static_assert(kXSlots % 2 == 0, "two slots to a chunk of 4-bit weights");
+constexpr int kXPitch = 1024 + 64;               // (64 more: rows' 16-byte parts on different banks)
+constexpr int kFewRows = 32;                     // rows of weights a stage
+constexpr int kFewSub = 4;                       // stages that share a chunk of tokens
+// The same in the second products, where the sums over the experts take registers too.
+template <int kNt>
+constexpr int few_sub2() { return kNt == 1 ? kFewSub : kFewSub / 2; }
+constexpr int kFewMaxBlocks = 192;
+constexpr int kFewSmem = 232448 - 9216;          // of a block, without the static part
+
+enum : int { kW16b = 0, kW16h = 1, kW4mx = 2, kW4nv = 3 };   // bf16, f16, mx, nv
+
+template <int kW>
+struct FewW {
+  static constexpr bool k4 = kW >= kW4mx;
+  static constexpr int kChunk = k4 ? 1024 : 512;                 // channels of the contraction a stage
+  static constexpr int kHalves = kChunk / 512;                   // slots of the tokens' side
+  static constexpr int kGroups = kChunk / 32 / kMmaWarps;        // of 32 channels, a warp's part
+  static constexpr int kPitch = k4 ? 512 + 16 : 1024 + 64;       // of a row of the stage
+  static constexpr int kScaleBytes = kW == kW4nv ? 64 : kW == kW4mx ? 32 : 0;   // of a row
+  static constexpr int kScalePitch = k4 ? kScaleBytes + 16 : 0;
+  static constexpr int kStage = kFewRows * (kPitch + kScalePitch);
+};
+
+template <int kNt>
+constexpr int few_x_bytes() { return kXSlots * 8 * kNt * kXPitch; }
+template <int kNt>
+constexpr int few_red_bytes() { return kMmaWarps * 2 * kNt * 512; }   // one of two
+template <int kW, int kNt>
+constexpr int few_stages() {
+  constexpr int n = (kFewSmem - 128 - few_x_bytes<kNt>() - 2 * few_red_bytes<kNt>()) / FewW<kW>::kStage;
+  return n < 8 ? n : 8;
+}
+template <int kW, int kNt>
+constexpr int few_smem_bytes() {
+  return 128 + few_x_bytes<kNt>() + 2 * few_red_bytes<kNt>() + few_stages<kW, kNt>() * FewW<kW>::kStage;
+}
+
+struct FewMatrix {
+  const uint8_t* w;        // 16-bit elements or codes
+  const uint8_t* scales;
+  const float* g;          // nv: of each expert, or NULL
+};
+
+struct FewArgs {
+  const void* x;           // [T, H]
+  FewMatrix w13, w2, w13_s, w2_s;
+  const float* bias;
+  moe_route_params route;
+  int32_t* ids;            // [T, k]
+  float* scales;
+  void* y;                 // [T, H]
+  int T, H, I, E, k, shared_I, shared_gate;
+  int bf16;                // x, y: bf16, else f16
+  // workspace
+  int32_t* ticket;         // next slice; then how many channels of the first products are done
+  uint32_t* tmax;          // [16] the largest |h| of each token, as bits
+  float* amax;             // [16] the largest |x|
+  float* logits;           // [T, E]
+  float* shared_logits;    // [T]
+  float* h;                // [T, k + 1, h_ld]
+  int h_ld;
+};
+
+__device__ int32_t g_few_timeouts;
+
+__device__ __forceinline__ void few_timeout(volatile int* abort) {
+  *abort = 1;
+  atomicOr(&g_few_timeouts, MOE_DEVICE_FLAG_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ gate
+
+constexpr int kGateThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  Vec<T, 16>::unpack(v, f);
+}
+
+// A block computes the logits of kPer rows of wg for up to kT tokens, its warps each an eighth of H; blocks
+// past those find the largest |x| of a token each.
+template <typename T, int kT, int kPer>
+__global__ void __launch_bounds__(kGateThreads)
+few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, int H, int E, int rows,
+                int gate_blocks, float* __restrict__ logits, float* __restrict__ shared_logits,
+                int32_t* ticket, uint32_t* tmax, float* amax) {
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nv = H / 8;
+  if (blockIdx.x == 0) {
+    if (tid < 2) ticket[tid] = 0;
+    if (tid < kFewTokens) tmax[tid] = 0;
+  }
+  if (static_cast<int>(blockIdx.x) >= gate_blocks) {
+    __shared__ uint32_t s_max[kGateThreads / 32];
+    const int t = blockIdx.x - gate_blocks;
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * H);
+    uint32_t m = 0;
+    for (int v = tid; v < nv; v += kGateThreads) {
+      float f[8];
+      unpack8<T>(__ldg(src + v), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int i = 1; i < kGateThreads / 32; ++i) m = max(m, s_max[i]);
+      amax[t] = __uint_as_float(m);
+    }
+    return;
+  }
+  __shared__ float s_sum[kGateThreads / 32][kPer][kT];
+  const int e0 = blockIdx.x * kPer;
+  float acc[kPer][kT] = {};
+#pragma unroll 2
+  for (int v = tid; v < nv; v += kGateThreads) {
+    float w[kPer][8];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const int e = min(e0 + p, rows - 1);
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(wg + static_cast<int64_t>(e) * H) + v), w[p]);
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      float f[8];
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(min(t, n_tok - 1)) * H) + v), f);
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[p][t] = fmaf(w[p][i], f[i], acc[p][t]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPer; ++p)
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      float s = acc[p][t];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      if (lane == 0) s_sum[warp][p][t] = s;
+    }
+  __syncthreads();
+  if (tid < kPer * kT) {
+    const int p = tid / kT, t = tid % kT, e = e0 + p;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGateThreads / 32; ++i) s += s_sum[i][p][t];
+    if (t < n_tok && e < rows) {
+      if (e < E) logits[t * E + e] = s;
+      else shared_logits[t] = s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ layer
+
+// d = a (16 rows of weights, 16 channels) b (16 channels, 8 tokens) + c.
+template <bool kBf16>
+__device__ __forceinline__ void mma_16bit(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                          const float (&c)[4]) {
+  if constexpr (kBf16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
+}
+
+// The untiled copy: 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 2^(14 - e) for a largest value of [2^e, 2^(e + 1)), 1 for none or one that is not finite; bounded so
+// that the inverse is a normal number too.
+__device__ __forceinline__ float to_f16_range(float amax) {
+  const uint32_t b = __float_as_uint(amax) >> 23;
+  if (b == 0 || b >= 255) return 1.0f;
+  const uint32_t e = 268u - b;
+  return __uint_as_float((e > 253u ? 253u : e) << 23);
+}
+__device__ __forceinline__ float inverse_power(float p) {
+  return __uint_as_float((254u << 23) - __float_as_uint(p));
+}
+
+// Everything about the chosen experts that the block's warps share.
+struct FewShared {
+  int32_t ids[kFewTokens * kMaxTopK];
+  float scales[kFewTokens * kMaxTopK];
+  int sel[kFewTokens * kMaxTopK];
+  float sel_l[kFewTokens * kMaxTopK];
+  double e[kFewTokens * kMaxTopK];
+  float ek[kFewTokens * kMaxTopK];
+  double z[kFewTokens];
+  uint32_t mask[8];
+  uint8_t list[kFewExperts];               // the chosen experts, ascending
+  int8_t slot[kFewExperts][kFewTokens];    // of a token at a chosen expert, -1: none; last: the shared one
+  float weight_s[kFewTokens];              // of the shared expert
+  float x_mul[kFewTokens], x_inv[kFewTokens];
+  uint32_t tmax[kFewTokens];
+  int n;                                   // chosen experts
+};
+
+// One token by one warp.
+template <int EPL>
+__device__ __noinline__ void few_select(const float* row, const FewArgs& a, int t, float* s_key,
+                                        uint8_t* s_exact, uint8_t* s_list, FewShared* sh) {
+  const int lane = threadIdx.x & 31;
+  const PairSlots ps{sh->sel, sh->sel_l, sh->e, sh->ek, sh->z};
+  const moe_route_params& r = a.route;
+  int sel[kMaxTopK];
+  double z = 0.0;
+  if (r.method == MOE_ROUTE_GROUPED_TOPK) {
+    grouped_topk_select_token<EPL>(row, a.E, a.k, r.n_group, r.topk_group, lane, s_key, sel);
+  } else if (r.method == MOE_ROUTE_DEEPSEEKV3 || r.method == MOE_ROUTE_MINIMAX2) {
+    const bool grouped = r.method == MOE_ROUTE_DEEPSEEKV3;
+    select_token<EPL, true>(row, a.E, a.bias, r.method, a.k, grouped ? r.n_group : 1,
+                            grouped ? r.topk_group : 1, lane, s_key, s_exact, s_list, sel, &z);
+  } else {
+    select_token<EPL, false>(row, a.E, nullptr, r.method, a.k, 1, 1, lane, s_key, s_exact, s_list, sel, &z);
+    if (lane == 0) sh->z[t] = z;
+  }
+  record_selection(row, sel, a.k, lane, ps, t);
+}
+
+// Routing of all tokens by the whole block, and the tables of the chosen experts.
+__device__ __noinline__ void few_route(const FewArgs& a, FewShared* sh, uint8_t* scratch) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  constexpr int kWarps = kFewThreads / 32;
+  static_assert(kWarps * (1024 + 512) <= few_x_bytes<1>(), "routing scratch");
+  float* s_key = reinterpret_cast<float*>(scratch) + warp * 256;
+  uint8_t* s_exact = scratch + kWarps * 1024 + warp * 512;
+  for (int i = tid; i < kFewExperts * kFewTokens; i += kFewThreads) (&sh->slot[0][0])[i] = -1;
+  if (tid < 8) sh->mask[tid] = 0;
+  if (tid < kFewTokens) sh->tmax[tid] = 0;
+  for (int t = warp; t < a.T; t += kWarps) {
+    const float* row = a.logits + t * a.E;
+    if (a.E <= 128) few_select<4>(row, a, t, s_key, s_exact, s_exact + 256, sh);
+    else few_select<8>(row, a, t, s_key, s_exact, s_exact + 256, sh);
+    __syncwarp();
+  }
+  __syncthreads();
+  const PairSlots ps{sh->sel, sh->sel_l, sh->e, sh->ek, sh->z};
+  const int method = a.route.method;
+  const float rsf = a.route.routed_scaling_factor;
+  if (method == MOE_ROUTE_GROUPED_TOPK)
+    block_pair_weights<2>(a.T, 0, a.T, a.k, method, rsf, ps, sh->ids, sh->scales);
+  else if (method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2)
+    block_pair_weights<1>(a.T, 0, a.T, a.k, method, method == MOE_ROUTE_DEEPSEEKV3 ? rsf : 1.0f, ps,
+                          sh->ids, sh->scales);
+  else
+    block_pair_weights<0>(a.T, 0, a.T, a.k, method, 1.0f, ps, sh->ids, sh->scales);
+  const int pairs = a.T * a.k;
+  if (tid < pairs) {
+    const int e = sh->ids[tid];
+    atomicOr(&sh->mask[e >> 5], 1u << (e & 31));
+    if (blockIdx.x == 0) {
+      a.ids[tid] = e;
+      a.scales[tid] = sh->scales[tid];
+    }
+  }
+  __syncthreads();
+  if (tid < pairs) {
+    // The place of expert e among the chosen ones.
+    const int e = sh->ids[tid];
+    int at = __popc(sh->mask[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int i = 0; i < (e >> 5); ++i) at += __popc(sh->mask[i]);
+    sh->list[at] = static_cast<uint8_t>(e);
+    sh->slot[at][tid / a.k] = static_cast<int8_t>(tid % a.k);
+  }
+  if (tid == kFewThreads - 1) {
+    int n = 0;
+    for (int i = 0; i < 8; ++i) n += __popc(sh->mask[i]);
+    sh->n = n;
+  }
+  __syncthreads();
+  if (tid < a.T && a.shared_I > 0) {
+    sh->slot[sh->n][tid] = static_cast<int8_t>(a.k);
+    sh->weight_s[tid] = a.shared_gate ? 1.0f / (1.0f + expf(-a.shared_logits[tid])) : 1.0f;
+  }
+  __syncthreads();
+}
+
+// A part of a slice, as all roles walk them.
+struct FewPart {
+  int a;       // first products: place among the chosen experts (n: the shared one)
+  int at;      // its first channel, or first row of y
+  int n;       // channels or rows
+};
+
+template <int kW, int kNt>
+__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_constant__ FewArgs a) {
+  using W = FewW<kW>;
+  constexpr bool kBf16 = kW == kW16b;            // the products' operands
+  constexpr int kStages = few_stages<kW, kNt>();
+  static_assert(kStages >= 3, "ring");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ FewShared sh;
+  __shared__ uint64_t w_full[kStages], w_empty[kStages], x_full[kXSlots], x_empty[kXSlots];
+  __shared__ int s_ticket[2 * kFewMaxBlocks + 2];
+  __shared__ int s_abort, s_current;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* sW = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+  uint8_t* sX = sW + kStages * W::kStage;
+  float* sRed = reinterpret_cast<float*>(sX + few_x_bytes<kNt>());
+  volatile int* abort = &s_abort;
+
+  pdl_trigger();
+  for (int i = tid; i < 2 * kFewMaxBlocks + 2; i += kFewThreads) s_ticket[i] = -1;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_empty[s], kMmaWarps);
+    }
+    for (int s = 0; s < kXSlots; ++s) {
+      mbar_init(&x_full[s], 1);
+      mbar_init(&x_empty[s], kMmaWarps / W::kHalves);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  const int n_blocks = gridDim.x;
+  // (under way while the tokens are routed)
+  if (tid == 32 * kWarpW) s_ticket[0] = atomicAdd(a.ticket, 1);
+  if (tid < a.T) {
+    const float p = W::k4 ? to_f16_range(__ldcg(a.amax + tid)) : 1.0f;
+    sh.x_mul[tid] = p;
+    sh.x_inv[tid] = inverse_power(p);
+  }
+  few_route(a, &sh, sX);
+
+  const int n_exp = sh.n, T = a.T, H = a.H;
+  const int n_all = n_exp + (a.shared_I > 0);
+  const int routed = n_exp * a.I, total = routed + a.shared_I;   // channels of the first products
+  // Slice `i` of the first products starts at channel cut1(i), of the second at row cut2(i).
+  auto cut1 = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / n_blocks); };
+  auto cut2 = [&](int i) { return static_cast<int>(static_cast<int64_t>(H) * i / n_blocks); };
+  // The part of the first products that starts at channel q of all, in a slice that ends at `end`.
+  auto part1 = [&](int q, int end) {
+    FewPart p;
+    int left;
+    if (q < routed) {
+      p.a = q / a.I;
+      p.at = q - p.a * a.I;
+      left = a.I - p.at;
+    } else {
+      p.a = n_exp;
+      p.at = q - routed;
+      left = a.shared_I - p.at;
+    }
+    p.n = min(16 * kFewSub, min(end - q, left));
+    return p;
+  };
+  constexpr int kSub2 = few_sub2<kNt>();
+  auto part2 = [&](int r, int end) { return FewPart{0, r, min(kFewRows * kSub2, end - r)}; };
+  auto inner = [&](int at) { return at < n_exp ? a.I : a.shared_I; };   // channels of a chosen expert
+  // Ticket i of this block, when it is there; 2 n_blocks (no work) if it does not come.
+  auto ticket_at = [&](int i, bool& ok) {
+    const volatile int* at = &s_ticket[i];
+    int v = *at;
+    const uint64_t t0 = globaltimer_ns();
+    while (v < 0) {
+      if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
+        ok = false;
+        return 2 * n_blocks;
+      }
+      v = *at;
+    }
+    return v;
+  };
+
+  if (warp == kWarpW) {
+    // ------------------------------------------------------------ weights
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // One stage: this lane's row of 32 (or none), from channel k0 of K on.
+    auto load = [&](const FewMatrix& m, int64_t row, bool there, int K, int k0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&w_empty[stage], phase ^ 1u, abort));
+      if (!ok) return;
+      const int len = min(W::kChunk, K - k0);
+      const uint32_t bytes = W::k4 ? len / 2 : len * 2;
+      uint32_t scale_bytes = 0;
+      const uint8_t* scales = nullptr;
+      if (W::k4) {
+        constexpr int kBlock = kW == kW4nv ? 16 : 32;
+        const int pitch = fp4_scale_pitch(K, kW == kW4nv ? kFp4Nv : kFp4Mx);
+        scale_bytes = min(W::kScaleBytes, pitch - k0 / kBlock);
+        scales = m.scales + row * pitch + k0 / kBlock;
+      }
+      const uint32_t rows = __popc(__ballot_sync(0xffffffffu, there));
+      if (lane == 0) mbar_arrive_expect_tx(&w_full[stage], rows * (bytes + scale_bytes));
+      __syncwarp();
+      if (there) {
+        uint8_t* dst = sW + stage * W::kStage;
+        const uint8_t* src = m.w + (W::k4 ? row * (K / 2) + k0 / 2 : (row * K + k0) * 2);
+        bulk_load(dst + lane * W::kPitch, src, bytes, &w_full[stage]);
+        if (W::k4)
+          bulk_load(dst + kFewRows * W::kPitch + lane * W::kScalePitch, scales, scale_bytes, &w_full[stage]);
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    for (int i = 0; ok; ++i) {
+      int ticket = 0;
+      if (lane == 0) {
+        ticket = i == 0 ? s_ticket[0] : atomicAdd(a.ticket, 1);
+        *const_cast<volatile int*>(&s_ticket[i]) = ticket;
+      }
+      ticket = __shfl_sync(0xffffffffu, ticket, 0);
+      if (ticket >= 2 * n_blocks) break;
+      if (ticket < n_blocks) {
+        for (int q = cut1(ticket), end = cut1(ticket + 1); q < end && ok;) {
+          const FewPart p = part1(q, end);
+          q += p.n;
+          const bool own = p.a < n_exp;
+          const FewMatrix& m = own ? a.w13 : a.w13_s;
+          const int width = inner(p.a);
+          const int64_t base = own ? static_cast<int64_t>(sh.list[p.a]) * 2 * width : 0;
+          const int ch = lane & 15;
+          for (int k0 = 0; k0 < H && ok; k0 += W::kChunk)
+            for (int s = 0; s * 16 < p.n && ok; ++s)
+              load(m, base + (lane < 16 ? 0 : width) + p.at + s * 16 + ch, s * 16 + ch < p.n, H, k0);
+        }
+      } else {
+        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end && ok;) {
+          const FewPart p = part2(r, end);
+          r += p.n;
+          for (int e = 0; e < n_all && ok; ++e) {
+            const bool own = e < n_exp;
+            const FewMatrix& m = own ? a.w2 : a.w2_s;
+            const int K = inner(e);
+            const int64_t base = own ? static_cast<int64_t>(sh.list[e]) * H : 0;
+            for (int k0 = 0; k0 < K && ok; k0 += W::kChunk)
+              for (int s = 0; s * kFewRows < p.n && ok; ++s)
+                load(m, base + p.at + s * kFewRows + lane, s * kFewRows + lane < p.n, K, k0);
+          }
+        }
+      }
+    }
+    if (!ok) {
+      few_timeout(abort);
+      // Copies under way end (bounded waits) before the block does.
+      volatile int never = 0;
+      for (int i = 0; i < min(issued, kStages); ++i) {
+        if (--stage < 0) {
+          stage = kStages - 1;
+          phase ^= 1u;
+        }
+        mbar_wait(&w_full[stage], phase, &never);
+      }
+    }
+  } else if (warp >= kWarpX) {
+    // ------------------------------------------------------------ tokens
+    // Slot after slot of 512 channels goes round the four warps.
+    const int mine = warp - kWarpX;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true, waited = false;
+    float t_mul = 1.0f;                     // lane t: token t's power of two for h
+    auto turn = [&] {                       // is it this warp's slot?
+      const bool is = slot == mine;
+      if (++slot == kXSlots) slot = 0;
+      return is;
+    };
+    // (a chunk's second slot is passed on empty where the contraction ends before it)
+    auto slots_end = [](int K) { return (K + W::kChunk - 1) / W::kChunk * W::kChunk; };
+    auto wait_empty = [&] {
+      ok = __all_sync(0xffffffffu, mbar_wait(&x_empty[mine], phase ^ 1u, abort));
+      phase ^= 1u;
+      return ok;
+    };
+    auto publish = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x_full[mine]);
+    };
+    uint8_t* dst = sX + mine * 8 * kNt * kXPitch;
+    for (int i = 0; ok; ++i) {
+      const int ticket = __shfl_sync(0xffffffffu, ticket_at(i, ok), 0);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || ticket >= 2 * n_blocks) break;
+      if (ticket < n_blocks) {
+        for (int q = cut1(ticket), end = cut1(ticket + 1); q < end && ok;) {
+          q += part1(q, end).n;
+          for (int k0 = 0; k0 < slots_end(H) && ok; k0 += 512) {
+            if (!turn()) continue;
+            if (!wait_empty()) break;
+            const int nv = min(512, H - k0) / 8;
+#pragma unroll 4
+            for (int v = lane; v < T * 64; v += 32) {
+              const int t = v >> 6, c = v & 63;
+              if (c >= nv) continue;
+              uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
+                                                             static_cast<int64_t>(t) * H + k0) + c);
+              if (W::k4) {
+                float f[8];
+                if (a.bf16) unpack8<__nv_bfloat16>(u, f);
+                else unpack8<__half>(u, f);
+                const float mul = sh.x_mul[t];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= mul;
+                u = Vec<__half, 16>::pack(f);
+              }
+              *reinterpret_cast<uint4*>(dst + t * kXPitch + c * 16) = u;
+            }
+            publish();
+          }
+        }
+      } else {
+        if (!waited) {
+          // All of h, and each token's largest.
+          ok = __all_sync(0xffffffffu, wait_count(a.ticket + 1, total, abort));
+          if (!ok) break;
+          waited = true;
+          if (!kBf16 && lane < T) t_mul = to_f16_range(__uint_as_float(__ldcg(a.tmax + lane)));
+        }
+        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end && ok;) {
+          r += part2(r, end).n;
+          for (int e = 0; e < n_all && ok; ++e) {
+            const int K = inner(e);
+            for (int k0 = 0; k0 < slots_end(K) && ok; k0 += 512) {
+              if (!turn()) continue;
+              if (!wait_empty()) break;
+              const int nv = min(512, K - k0) / 8;
+              for (int t = 0; t < T; ++t) {
+                const int j = sh.slot[e][t];
+                const float mul = __shfl_sync(0xffffffffu, t_mul, t);
+                const float4* src = reinterpret_cast<const float4*>(
+                    a.h + (static_cast<int64_t>(t) * (a.k + 1) + max(j, 0)) * a.h_ld + k0);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const int c = lane + 32 * half;
+                  if (c >= nv) continue;
+                  uint4 u = make_uint4(0, 0, 0, 0);
+                  if (j >= 0) {
+                    const float4 lo = __ldcg(src + 2 * c), hi = __ldcg(src + 2 * c + 1);
+                    const float f[8] = {lo.x * mul, lo.y * mul, lo.z * mul, lo.w * mul,
+                                        hi.x * mul, hi.y * mul, hi.z * mul, hi.w * mul};
+                    if constexpr (kBf16) u = Vec<__nv_bfloat16, 16>::pack(f);
+                    else u = Vec<__half, 16>::pack(f);
+                  }
+                  *reinterpret_cast<uint4*>(dst + t * kXPitch + c * 16) = u;
+                }
+              }
+              publish();
+            }
+          }
+        }
+      }
+    }
+    if (!ok) few_timeout(abort);
+  } else {
+    // ------------------------------------------------------------ products
+    // A wait that runs out leaves the loops' course as it is (the warps meet at barriers): what is
+    // computed after it is garbage that the host hears of.
+    int stage = 0, slot = 0, red = 0;
+    uint32_t phase = 0, x_phase = 0;
+    bool ok = true;
+    const int g = lane >> 2, c = lane & 3;         // of the fragments
+    constexpr int kHalfWarps = kMmaWarps / W::kHalves;
+    constexpr bool kHold = kNt == 1;               // the tokens' fragments of a chunk stay in registers
+    const int half = warp / kHalfWarps;            // the slot of a chunk that this warp reads
+    auto clear = [](auto& v) {
+#pragma unroll
+      for (auto& sub : v)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sub[m][n][j] = 0.0f;
+    };
+    // A chunk of the contraction (`len` channels) for `subs` stages of rows.
+    auto chunk = [&](auto& acc, int len, int subs) {
+      constexpr int kSubs = sizeof(acc) / sizeof(acc[0]);
+      const int groups = min(max(len / 32 - warp * W::kGroups, 0), W::kGroups);
+      const int xs = slot + half;   // (kXSlots is a multiple of kHalves: a slot is always the same half's)
+      const uint8_t* x_src = sX + (xs * 8 * kNt + g) * kXPitch + (warp % kHalfWarps) * W::kGroups * 64 + c * 16;
+      uint4 held[W::kGroups];
+      ok = mbar_wait(&x_full[xs], x_phase, abort) && ok;
+      if constexpr (kHold) {
+#pragma unroll
+        for (int i = 0; i < W::kGroups; ++i)
+          if (i < groups) held[i] = *reinterpret_cast<const uint4*>(x_src + i * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_empty[xs]);
+      }
+      slot += W::kHalves;
+      if (slot == kXSlots) {
+        slot = 0;
+        x_phase ^= 1u;
+      }
+#pragma unroll
+      for (int s = 0; s < kSubs; ++s) {
+        if (s >= subs) break;
+        ok = mbar_wait(&w_full[stage], phase, abort) && ok;
+        const uint8_t* w = sW + stage * W::kStage + g * W::kPitch + warp * W::kGroups * (W::k4 ? 16 : 64) +
+                           c * (W::k4 ? 4 : 16);
+        const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
+                            warp * (kW == kW4nv ? 8 : 4);
+        // Rows g, g + 8, g + 16, g + 24. nv: f16 pairs, scales of two groups; mx: bytes of four groups.
+        uint32_t scale[4][2] = {};
+        if constexpr (W::k4) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (kW == kW4nv) {
+              const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
+              // this lane's block of each group
+              const uint32_t four = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
+              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                  : "=r"(scale[r][0]), "=r"(scale[r][1])
+                  : "r"(four));
+            } else {
+              scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W::kGroups; ++i) {
+          if (i >= groups) break;
+          uint4 b[kNt];
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            if constexpr (kHold) b[n] = held[i];
+            else b[n] = *reinterpret_cast<const uint4*>(x_src + n * 8 * kXPitch + i * 64);
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
+              if constexpr (W::k4) {
+                fp4_halves8(*reinterpret_cast<const uint32_t*>(src + i * 16), p[r]);
+                if constexpr (kW == kW4nv) {
+                  const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][i >> 1]);
+                  const __half2 one = i & 1 ? __high2half2(both) : __low2half2(both);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
+                    p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                }
+              } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(src + i * 64);
+                p[r][0] = u.x;
+                p[r][1] = u.y;
+                p[r][2] = u.z;
+                p[r][3] = u.w;
+              }
+            }
+            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+            if constexpr (kW == kW4mx) {
+              float f[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t byte = scale[2 * m + r][0] >> (8 * i) & 0xffu;
+                f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
+              }
+#pragma unroll
+              for (int n = 0; n < kNt; ++n) {
+                const float zero[4] = {};
+                float d[4], d2[4];
+                mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
+                mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
+                acc[s][m][n][0] = fmaf(d2[0], f[0], acc[s][m][n][0]);
+                acc[s][m][n][1] = fmaf(d2[1], f[0], acc[s][m][n][1]);
+                acc[s][m][n][2] = fmaf(d2[2], f[1], acc[s][m][n][2]);
+                acc[s][m][n][3] = fmaf(d2[3], f[1], acc[s][m][n][3]);
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNt; ++n) {
+                mma_16bit<kBf16>(acc[s][m][n], a0, b[n].x, b[n].y, acc[s][m][n]);
+                mma_16bit<kBf16>(acc[s][m][n], a1, b[n].z, b[n].w, acc[s][m][n]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!kHold && lane == 0) mbar_arrive(&x_empty[xs]);   // (after the last stage's __syncwarp)
+    };
+    // The warps' sums of one sub-tile meet in shared memory.
+    auto gather = [&](const float (&v)[2][kNt][4]) {
+      float* mine = sRed + red * (few_red_bytes<kNt>() / 4);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+          *reinterpret_cast<float4*>(mine + ((warp * 2 + m) * kNt + n) * 128 + lane * 4) =
+              make_float4(v[m][n][0], v[m][n][1], v[m][n][2], v[m][n][3]);
+      named_barrier_sync(1, 32 * kMmaWarps);
+      red ^= 1;      // (the other one has been read: all warps have passed this barrier)
+      return mine;
+    };
+    auto sum_at = [&](const float* mine, int m, int n, int at) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kMmaWarps; ++w) v += mine[((w * 2 + m) * kNt + n) * 128 + at];
+      return v;
+    };
+
+    bool waited = false;
+    float y_inv = 1.0f;       // lane t: inverse of token t's power of two
+    for (int i = 0;; ++i) {
+      if (tid == 0) s_current = ticket_at(i, ok);
+      named_barrier_sync(1, 32 * kMmaWarps);
+      const int ticket = s_current;
+      named_barrier_sync(1, 32 * kMmaWarps);      // read by all before it is written again
+      if (ticket >= 2 * n_blocks) break;
+      if (ticket < n_blocks) {
+        const int q0 = cut1(ticket), end = cut1(ticket + 1);
+        for (int q = q0; q < end;) {
+          const FewPart p = part1(q, end);
+          q += p.n;
+          const int subs = (p.n + 15) / 16;
+          float acc[kFewSub][2][kNt][4];
+          clear(acc);
+          for (int k0 = 0; k0 < H; k0 += W::kChunk) chunk(acc, min(W::kChunk, H - k0), subs);
+          const bool own = p.a < n_exp;
+          float g13 = 1.0f, g2 = 1.0f;
+          if (kW == kW4nv) {
+            const int e = own ? sh.list[p.a] : 0;
+            const float* p13 = own ? a.w13.g : a.w13_s.g;
+            const float* p2 = own ? a.w2.g : a.w2_s.g;
+            if (p13) g13 = __ldg(p13 + e);
+            if (p2) g2 = __ldg(p2 + e);
+          }
+#pragma unroll
+          for (int s = 0; s < kFewSub; ++s) {
+            if (s >= subs) break;
+            const float* mine = gather(acc[s]);
+            if (tid < 128 * kNt) {
+              const int n = tid >> 7, at = tid & 127, l = at >> 2, j = at & 3;
+              const int row = s * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
+              const int sl = t < T ? sh.slot[p.a][t] : -1;
+              if (sl >= 0 && row < p.n) {
+                const float f = sh.x_inv[t] * g13;
+                const float gate = sum_at(mine, 0, n, at) * f, up = sum_at(mine, 1, n, at) * f;
+                const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
+                const float ex = expf(-fabsf(gate));
+                const float sig = (gate < 0.0f ? ex : 1.0f) / (1.0f + ex);
+                const float h = gate * sig * up * (wt * g2);
+                a.h[(static_cast<int64_t>(t) * (a.k + 1) + sl) * a.h_ld + p.at + row] = h;
+                if (!kBf16) atomicMax(&sh.tmax[t], __float_as_uint(h) & 0x7fffffffu);
+              }
+            }
+          }
+        }
+        // This slice's h, and the largest so far, before the count.
+        named_barrier_sync(1, 32 * kMmaWarps);
+        if (warp == 0 && end > q0) {
+          if (!kBf16 && lane < T) atomicMax(a.tmax + lane, sh.tmax[lane]);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) red_release_gpu_add(a.ticket + 1, end - q0);
+        }
+      } else {
+        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end;) {
+          const FewPart p = part2(r, end);
+          r += p.n;
+          const int subs = (p.n + kFewRows - 1) / kFewRows;
+          float acc[kSub2][2][kNt][4], all[kSub2][2][kNt][4];
+          clear(all);
+          for (int e = 0; e < n_all; ++e) {
+            const int K = inner(e);
+            clear(acc);
+            for (int k0 = 0; k0 < K; k0 += W::kChunk) chunk(acc, min(W::kChunk, K - k0), subs);
+#pragma unroll
+            for (int n = 0; n < kNt; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (sh.slot[e][n * 8 + 2 * c + j] < 0) continue;
+#pragma unroll
+                for (int s = 0; s < kSub2; ++s)
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) {
+                    all[s][m][n][j] += acc[s][m][n][j];
+                    all[s][m][n][j + 2] += acc[s][m][n][j + 2];
+                  }
+              }
+          }
+          if (!waited) {
+            // (h came through the tokens' warps, which waited for all of it)
+            waited = true;
+            if (!kBf16 && lane < T) y_inv = inverse_power(to_f16_range(__uint_as_float(__ldcg(a.tmax + lane))));
+          }
+#pragma unroll
+          for (int s = 0; s < kSub2; ++s) {
+            if (s >= subs) break;
+            const float* mine = gather(all[s]);
+#pragma unroll
+            for (int i2 = 0; i2 < kNt; ++i2) {
+              const int pos = tid + 256 * i2;
+              const int m = pos / (128 * kNt), n = pos / 128 % kNt, at = pos & 127, l = at >> 2, j = at & 3;
+              const int row = s * kFewRows + m * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
+              const float inv = __shfl_sync(0xffffffffu, y_inv, t);
+              if (t < T && row < p.n) {
+                const float v = sum_at(mine, m, n, at) * inv;
+                const int64_t to = static_cast<int64_t>(t) * H + p.at + row;
+                if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
+                else static_cast<__half*>(a.y)[to] = __float2half_rn(v);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (!ok) few_timeout(abort);
+  }
+  __syncthreads();
+}
+
+template <int kW, int kNt>
+moe_status launch_layer(const FewArgs& a, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(MOE_ERR_CUDA, "cudaGetDevice failed");
+  constexpr int kSmem = few_smem_bytes<kW, kNt>();
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(few_layer_kernel<kW, kNt>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    ready[dev].store(true, std::memory_order_release);
+  }
+  const int sms = device_sm_count();
+  const cudaError_t err =
+      launch_pdl(few_layer_kernel<kW, kNt>, dim3(static_cast<unsigned>(sms < kFewMaxBlocks ? sms : kFewMaxBlocks)),
+                 dim3(kFewThreads), kSmem, s, a);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "few_layer launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}
+
+template <typename T, int kT>
+cudaError_t launch_gate_t(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
+  const int rows = a.E + a.shared_gate;
+  const bool two = rows > device_sm_count();   // one wave of blocks
+  const int blocks = two ? (rows + 1) / 2 : rows;
+  const dim3 grid(static_cast<unsigned>(blocks + (want_amax ? a.T : 0)));
+  const T* x = static_cast<const T*>(a.x);
+  const T* w = static_cast<const T*>(wg);
+  return two ? launch_pdl(few_gate_kernel<T, kT, 2>, grid, dim3(kGateThreads), 0, s, x, w, a.T, a.H, a.E,
+                          rows, blocks, a.logits, a.shared_logits, a.ticket, a.tmax, a.amax)
+             : launch_pdl(few_gate_kernel<T, kT, 1>, grid, dim3(kGateThreads), 0, s, x, w, a.T, a.H, a.E,
+                          rows, blocks, a.logits, a.shared_logits, a.ticket, a.tmax, a.amax);
+}
+
+template <typename T>
+cudaError_t launch_gate_tokens(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
+  if (a.T <= 1) return launch_gate_t<T, 1>(a, wg, want_amax, s);
+  if (a.T <= 4) return launch_gate_t<T, 4>(a, wg, want_amax, s);
+  if (a.T <= 8) return launch_gate_t<T, 8>(a, wg, want_amax, s);
+  return launch_gate_t<T, 16>(a, wg, want_amax, s);
+}
+
+size_t to_256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+moe_status few_timeout_word(void** word) {
+  const cudaError_t e = cudaGetSymbolAddress(word, g_few_timeouts);
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
+
+size_t few_workspace_bytes(const moe_problem& p) {
+  const size_t h_ld = p.I > p.shared_I ? p.I : p.shared_I;
+  return 256 + to_256(4 * static_cast<size_t>(p.T) * p.E) + 256 + 4 * static_cast<size_t>(p.T) * (p.k + 1) * h_ld;
+}
+
+moe_status launch_few(const moe_problem& p, const FewLayer& f, char* ws, cudaStream_t s) {
+  auto matrix = [](const moe_weights* w) {
+    return w ? FewMatrix{static_cast<const uint8_t*>(w->w), w->scales, w->g} : FewMatrix{};
+  };
+  FewArgs a = {};
+  a.x = f.x;
+  a.w13 = matrix(f.w13);
+  a.w2 = matrix(f.w2);
+  a.w13_s = matrix(f.w13_s);
+  a.w2_s = matrix(f.w2_s);
+  a.bias = f.bias;
+  a.route = f.route;
+  a.ids = f.ids;
+  a.scales = f.scales;
+  a.y = f.y;
+  a.T = static_cast<int>(p.T);
+  a.H = p.H;
+  a.I = p.I;
+  a.E = p.E;
+  a.k = p.k;
+  a.shared_I = p.shared_I;
+  a.shared_gate = f.shared_gate;
+  a.bf16 = f.dtype == MOE_DTYPE_BF16;
+  a.ticket = reinterpret_cast<int32_t*>(ws);
+  a.tmax = reinterpret_cast<uint32_t*>(ws + 64);
+  a.amax = reinterpret_cast<float*>(ws + 128);
+  a.logits = reinterpret_cast<float*>(ws + 256);
+  char* after = ws + 256 + to_256(4 * static_cast<size_t>(p.T) * p.E);
+  a.shared_logits = reinterpret_cast<float*>(after);
+  a.h = reinterpret_cast<float*>(after + 256);
+  a.h_ld = p.I > p.shared_I ? p.I : p.shared_I;
+  const bool four = f.weights != MOE_WEIGHTS_16BIT;
+  const cudaError_t err = a.bf16 ? launch_gate_tokens<__nv_bfloat16>(a, f.wg, four, s)
+                                 : launch_gate_tokens<__half>(a, f.wg, four, s);
+  if (err != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "few_gate launch: %s", cudaGetErrorString(err));
+  const bool wide = p.T > 8;
+  switch (f.weights) {
+    case MOE_FP4_MX:
+      return wide ? launch_layer<kW4mx, 2>(a, s) : launch_layer<kW4mx, 1>(a, s);
+    case MOE_FP4_NV:
+      return wide ? launch_layer<kW4nv, 2>(a, s) : launch_layer<kW4nv, 1>(a, s);
+    default:
+      if (a.bf16) return wide ? launch_layer<kW16b, 2>(a, s) : launch_layer<kW16b, 1>(a, s);
+      return wide ? launch_layer<kW16h, 2>(a, s) : launch_layer<kW16h, 1>(a, s);
+  }
+}
+
+}  // namespace moe

@@ -167,6 +167,26 @@ moe_status launch_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, co
 moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const int32_t* offsets, int64_t R,
                               int E, int N, int K, int fmt, int dtype, void* y, cudaStream_t s);
 
+// ---- the layer for a few tokens (few.cu)
+struct FewLayer {
+  const void *x, *wg;
+  const float* bias;
+  const moe_weights *w13, *w2, *w13_s, *w2_s;   // the shared expert's NULL where there is none
+  int weights;                                  // MOE_WEIGHTS_16BIT or a moe_fp4_format
+  int dtype;
+  int shared_gate;
+  moe_route_params route;
+  int32_t* ids;
+  float* scales;
+  void* y;
+};
+size_t few_workspace_bytes(const moe_problem& p);
+moe_status launch_few(const moe_problem& p, const FewLayer& f, char* ws, cudaStream_t s);
+moe_status few_timeout_word(void** word);
+
+// Why moe_route does not take these parameters (MOE_REASON_OK: it does).
+int32_t route_reason(int64_t T, const moe_route_params& p);
+
 // Device words in which the products' and the gate's kernels note that a wait ran out.
 moe_status experts_timeout_word(void** word);
 moe_status fp4_timeout_word(void** word);

@@ -171,3 +171,69 @@ def test_the_error_is_half_a_step():
         top = np.abs(x).reshape(20, -1, b).max(2, keepdims=True)
         # the largest step is 2 of 6, the mx scale up to twice, the nv scale 1/16 more than needed
         assert (err <= top * (1 / 3 if fmt == ref.MX else 1 / 6 * (1 + 1 / 16))).all()
+
+
+# ------------------------------------------------------------------------- the layer for a few tokens
+
+def few(moe, T=4, H=64, I=32, E=8, k=2, shared_I=0, method=1, gate=0, weights=-1, dt=0, bias=None, x=GOOD, wg=GOOD,
+        w=GOOD, s=GOOD, g=None, w2=True, shared=True, ids=GOOD, scales=GOOD, y=GOOD, ws=ctypes.c_void_p(1 << 20), n=1 << 24,
+        r_E=None, r_k=None, n_group=1):
+    p = moe.MoeProblem(T, H, I, E, k, shared_I)
+    r = moe.MoeRouteParams(r_E or E, r_k or k, method, n_group, 1, 1.0)
+    m = moe.MoeWeights(w, s, g)
+    ref_m = ctypes.byref(m)
+    return moe._lib.moe_layer_few(ctypes.byref(p), ctypes.byref(r), x, wg, gate, bias, ref_m, ref_m if w2 else None,
+                                  ref_m if shared else None, ref_m if shared else None, weights, dt, ids, scales, y, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), UNSUPPORTED), (dict(T=17), UNSUPPORTED), (dict(H=48), UNSUPPORTED), (dict(H=0), UNSUPPORTED),
+    (dict(H=32800), UNSUPPORTED), (dict(I=16), UNSUPPORTED), (dict(I=65568), UNSUPPORTED), (dict(shared_I=8), UNSUPPORTED),
+    (dict(shared_I=-32), UNSUPPORTED), (dict(E=0), UNSUPPORTED), (dict(E=257), UNSUPPORTED), (dict(k=0), UNSUPPORTED),
+    (dict(k=9, E=16), UNSUPPORTED), (dict(k=4, E=3), UNSUPPORTED), (dict(weights=2), UNSUPPORTED),
+    (dict(weights=-2), UNSUPPORTED), (dict(dt=2), UNSUPPORTED), (dict(method=7), UNSUPPORTED), (dict(method=17), UNSUPPORTED),
+    (dict(method=2, n_group=3), UNSUPPORTED), (dict(r_E=7), INVALID), (dict(r_k=1), INVALID), (dict(gate=1), INVALID),
+    (dict(gate=2, shared_I=32), INVALID), (dict(method=16, bias=GOOD), INVALID), (dict(x=None), INVALID),
+    (dict(x=ODD), INVALID), (dict(wg=ODD), INVALID), (dict(bias=ODD), INVALID), (dict(ids=None), INVALID),
+    (dict(scales=ODD), INVALID), (dict(y=None), INVALID), (dict(w=None), INVALID), (dict(w=ODD), INVALID),
+    (dict(w2=False), INVALID), (dict(shared=False, shared_I=32), INVALID), (dict(weights=0, s=None), INVALID),
+    (dict(weights=1, s=ODD), INVALID), (dict(weights=0, g=GOOD), INVALID), (dict(g=GOOD), INVALID),
+    (dict(weights=1, g=BYTE), INVALID), (dict(ws=None), INVALID), (dict(ws=ctypes.c_void_p((1 << 20) + 128)), INVALID),
+    (dict(n=100), SMALL)])
+def test_layer_few_refuses(moe, kw, status):
+    assert few(moe, **kw) == status
+    assert moe._lib.moe_last_error()
+
+
+def test_layer_few_without_tokens_and_its_workspace(moe):
+    assert few(moe, T=0, x=None, wg=None, w=None, y=None, ws=None) == 0
+    assert moe._lib.moe_layer_few(None, None, *[None] * 2, 0, *[None] * 5, -1, 0, *[None] * 4, 0, None) == INVALID
+    n = lambda *a: moe._lib.moe_layer_few_workspace_bytes(ctypes.byref(moe.MoeProblem(*a)))   # noqa: E731
+    assert n(17, 64, 32, 8, 2, 0) == 0 == n(4, 48, 32, 8, 2, 0) == n(4, 64, 32, 257, 2, 0)
+    # counters and sizes, logits [T, E], the shared gate's, h [T, k + 1, the wider of both] in f32
+    assert n(16, 7168, 2048, 256, 8, 4096) == 256 + 4 * 16 * 256 + 256 + 4 * 16 * 9 * 4096
+    assert n(0, 64, 32, 8, 2, 0) == 512
+
+
+def test_layer_few_wrapper_refuses(moe, monkeypatch):
+    launched = []
+    monkeypatch.setattr(moe._lib, "moe_layer_few", lambda *a: launched.append(a) or 0)
+    monkeypatch.setattr(moe, "_stream", lambda s: 0)
+    monkeypatch.setattr(moe, "_new", lambda shape, dtype, device, stream, result=True: fake(shape, dtype))
+    b16 = torch.bfloat16
+    x, wg, w13, w2 = fake((3, 64), b16), fake((4, 64), b16), fake((4, 64, 64), b16), fake((4, 64, 32), b16)
+    y, ids, sc = moe.moe_layer_few(x, wg, w13, w2, 1, 2)
+    assert y.shape == (3, 64) and ids.shape == (3, 2) and sc.dtype == torch.float32 and len(launched) == 1
+    q13 = moe.Fp4(fake((4, 64, 32), torch.uint8), fake((4, 64, 16), torch.uint8), moe.MOE_FP4_MX)
+    q2 = moe.Fp4(fake((4, 64, 16), torch.uint8), fake((4, 64, 16), torch.uint8), moe.MOE_FP4_MX)
+    q2nv = moe.Fp4(fake((4, 64, 16), torch.uint8), fake((4, 64, 16), torch.uint8), moe.MOE_FP4_NV)
+    moe.moe_layer_few(x, wg, q13, q2, 1, 2)
+    for a, kw in (((x.float(), wg, w13, w2), {}), ((x, fake((6, 64), b16), w13, w2), {}), ((x, fake((4, 32), b16), w13, w2), {}),
+                  ((x, wg.half(), w13, w2), {}), ((x, wg, w13[0], w2), {}), ((x, wg, w13, fake((4, 64, 33), b16)), {}),
+                  ((x, wg, w13, q2), {}), ((x, wg, q13, w2), {}), ((x, wg, q13, q2nv), {}), ((x, wg, w13.half(), w2.half()), {}),
+                  ((x, wg, w13, w2), dict(w13_s=fake((64, 64), b16))), ((x, wg, w13, w2), dict(bias=fake((3,), torch.float32))),
+                  ((x, wg, w13, w2), dict(y=fake((3, 63), b16))), ((x, wg, w13, w2), dict(ids=fake((3, 2), torch.int64))),
+                  ((x, wg, w13, w2), dict(w13_s=fake((64, 64), b16), w2_s=fake((64, 64), b16)))):
+        with pytest.raises(ValueError):
+            moe.moe_layer_few(*a, 1, 2, **kw)
+    assert len(launched) == 2
