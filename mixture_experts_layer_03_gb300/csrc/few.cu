@@ -4,8 +4,8 @@
 //                     sum:  y[t] = sum over slots j of s[t, j] w2[e] (silu(g) u),  g, u = w13[e] x[t]
 // For a few tokens the layer reads each chosen expert's weights once and little else: the floor is
 // their bytes at the memory's rate, and what is added to it is latency, between kernels and between the
-// two products. So one block an SM stays for the whole layer, and one warp of it (the weights'
-// producer) keeps its ring full from the moment the experts are known, on into the second products'
+// two products. So one block an SM stays for the whole layer, and two warps of it (the weights'
+// producers) keep its ring full from the moment the experts are known, on into the second products'
 // weights while the first products' results are still awaited.
 //
 // Work. Tickets 0..n-1 are slices of the first products: the chosen experts' I channels one after the
@@ -51,8 +51,9 @@ static_assert(kFewTokens == 16, "two column tiles");
 constexpr int kFewExperts = 128 + 1;             // T * k at most, and the shared one
 constexpr int kMmaWarps = 8;                     // consumers
 constexpr int kXWarps = 4;                       // producers of the tokens' side
-constexpr int kWarpW = kMmaWarps, kWarpX = kMmaWarps + 1;
-constexpr int kFewThreads = 32 * (kMmaWarps + 1 + kXWarps);
+constexpr int kWWarps = 2;                       // producers of the weights' side, a stage each in turn
+constexpr int kWarpW = kMmaWarps, kWarpX = kWarpW + kWWarps;
+constexpr int kFewThreads = 32 * (kWarpX + kXWarps);
 constexpr int kXSlots = kXWarps;                 // each of 512 channels of all tokens
 static_assert(kXSlots % 2 == 0, "two slots to a chunk of 4-bit weights");
 constexpr int kXPitch = 1024 + 64;               // (64 more: rows' 16-byte parts on different banks)
@@ -235,14 +236,17 @@ __device__ __forceinline__ void mma_16bit(float (&d)[4], const uint32_t (&a)[4],
           "f"(c[3]));
 }
 
-// The untiled copy: 16-byte aligned, a multiple of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes from global to shared memory, past L1, without a register on the way.
+__device__ __forceinline__ void async_load_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
 }
+// One of the arrivals that `bar` counts, once this thread's copies so far are there.
+__device__ __forceinline__ void async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // 2^(14 - e) for a largest value of [2^e, 2^(e + 1)), 1 for none or one that is not finite; bounded so
 // that the inverse is a normal number too.
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   for (int i = tid; i < 2 * kFewMaxBlocks + 2; i += kFewThreads) s_ticket[i] = -1;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&w_full[s], 1);
+      mbar_init(&w_full[s], 32);   // a producer warp's lanes
       mbar_init(&w_empty[s], kMmaWarps);
     }
     for (int s = 0; s < kXSlots; ++s) {
@@ -445,37 +449,48 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     return v;
   };
 
-  if (warp == kWarpW) {
+  if (warp >= kWarpW && warp < kWarpX) {
     // ------------------------------------------------------------ weights
-    int stage = 0, issued = 0;
+    // Rows as they lie in memory, by 16-byte asynchronous copies of whole warps. (Bulk copies of a row each
+    // are issued one lane after the other: 69 us for 5 tokens, 60 experts of 1504 x 736 in mx, so N us.)
+    const int mine = warp - kWarpW;
+    int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // One stage: this lane's row of 32 (or none), from channel k0 of K on.
-    auto load = [&](const FewMatrix& m, int64_t row, bool there, int K, int k0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&w_empty[stage], phase ^ 1u, abort));
-      if (!ok) return;
-      const int len = min(W::kChunk, K - k0);
-      const uint32_t bytes = W::k4 ? len / 2 : len * 2;
-      uint32_t scale_bytes = 0;
-      const uint8_t* scales = nullptr;
-      if (W::k4) {
-        constexpr int kBlock = kW == kW4nv ? 16 : 32;
-        const int pitch = fp4_scale_pitch(K, kW == kW4nv ? kFp4Nv : kFp4Mx);
-        scale_bytes = min(W::kScaleBytes, pitch - k0 / kBlock);
-        scales = m.scales + row * pitch + k0 / kBlock;
+    constexpr int kBlock = kW == kW4nv ? 16 : 32;
+    // n rows of len channels, from `row` of m and channel k0 of K on, to rows from `at` on of the stage.
+    auto rows = [&](const FewMatrix& m, int64_t row, int n, int at, int K, int k0, int len) {
+      uint8_t* dst = sW + stage * W::kStage + at * W::kPitch + lane * 16;
+      const int bytes = W::k4 ? len / 2 : len * 2;
+      const int64_t pitch = W::k4 ? K / 2 : 2 * static_cast<int64_t>(K);
+      const uint8_t* src = m.w + row * pitch + (W::k4 ? k0 / 2 : 2 * k0) + lane * 16;
+      const bool in = lane * 16 < bytes, in2 = !W::k4 && 512 + lane * 16 < bytes;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        if (in) async_load_16(dst, src);
+        if (in2) async_load_16(dst + 512, src + 512);
+        dst += W::kPitch;
+        src += pitch;
       }
-      const uint32_t rows = __popc(__ballot_sync(0xffffffffu, there));
-      if (lane == 0) mbar_arrive_expect_tx(&w_full[stage], rows * (bytes + scale_bytes));
-      __syncwarp();
-      if (there) {
-        uint8_t* dst = sW + stage * W::kStage;
-        const uint8_t* src = m.w + (W::k4 ? row * (K / 2) + k0 / 2 : (row * K + k0) * 2);
-        bulk_load(dst + lane * W::kPitch, src, bytes, &w_full[stage]);
-        if (W::k4)
-          bulk_load(dst + kFewRows * W::kPitch + lane * W::kScalePitch, scales, scale_bytes, &w_full[stage]);
+      if constexpr (W::k4) {
+        constexpr int kLanes = W::kScaleBytes / 16;   // to a row of scales
+        const int sp = fp4_scale_pitch(K, kW == kW4nv ? kFp4Nv : kFp4Mx);
+        const int part = lane % kLanes, there = (sp - k0 / kBlock) / 16;
+        for (int i = lane / kLanes; i < n; i += 32 / kLanes)
+          if (part < there)
+            async_load_16(sW + stage * W::kStage + kFewRows * W::kPitch + (at + i) * W::kScalePitch + part * 16,
+                          m.scales + (row + i) * sp + k0 / kBlock + part * 16);
       }
-      __syncwarp();
-      ++issued;
+    };
+    // A stage is this warp's or the other one's.
+    auto begin = [&] {
+      const bool is = turn == mine;
+      turn = turn + 1 == kWWarps ? 0 : turn + 1;
+      if (is) ok = __all_sync(0xffffffffu, mbar_wait(&w_empty[stage], phase ^ 1u, abort));
+      return is && ok;
+    };
+    auto end_stage = [&](bool is) {
+      if (is) async_arrive(&w_full[stage]);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
@@ -483,9 +498,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     };
     for (int i = 0; ok; ++i) {
       int ticket = 0;
-      if (lane == 0) {
-        ticket = i == 0 ? s_ticket[0] : atomicAdd(a.ticket, 1);
-        *const_cast<volatile int*>(&s_ticket[i]) = ticket;
+      if (mine == 0) {
+        if (lane == 0) {
+          ticket = i == 0 ? s_ticket[0] : atomicAdd(a.ticket, 1);
+          *const_cast<volatile int*>(&s_ticket[i]) = ticket;
+        }
+      } else {
+        ticket = ticket_at(i, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
       ticket = __shfl_sync(0xffffffffu, ticket, 0);
       if (ticket >= 2 * n_blocks) break;
@@ -496,11 +517,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           const bool own = p.a < n_exp;
           const FewMatrix& m = own ? a.w13 : a.w13_s;
           const int width = inner(p.a);
-          const int64_t base = own ? static_cast<int64_t>(sh.list[p.a]) * 2 * width : 0;
-          const int ch = lane & 15;
-          for (int k0 = 0; k0 < H && ok; k0 += W::kChunk)
-            for (int s = 0; s * 16 < p.n && ok; ++s)
-              load(m, base + (lane < 16 ? 0 : width) + p.at + s * 16 + ch, s * 16 + ch < p.n, H, k0);
+          const int64_t base = (own ? static_cast<int64_t>(sh.list[p.a]) * 2 * width : 0) + p.at;
+          for (int k0 = 0; k0 < H && ok; k0 += W::kChunk) {
+            const int len = min(W::kChunk, H - k0);
+            for (int s = 0; s * 16 < p.n && ok; ++s) {
+              const bool is = begin();
+              if (is) {
+                const int n = min(16, p.n - s * 16);
+                rows(m, base + s * 16, n, 0, H, k0, len);
+                rows(m, base + width + s * 16, n, 16, H, k0, len);
+              }
+              end_stage(is);
+            }
+          }
         }
       } else {
         for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end && ok;) {
@@ -510,26 +539,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             const bool own = e < n_exp;
             const FewMatrix& m = own ? a.w2 : a.w2_s;
             const int K = inner(e);
-            const int64_t base = own ? static_cast<int64_t>(sh.list[e]) * H : 0;
+            const int64_t base = (own ? static_cast<int64_t>(sh.list[e]) * H : 0) + p.at;
             for (int k0 = 0; k0 < K && ok; k0 += W::kChunk)
-              for (int s = 0; s * kFewRows < p.n && ok; ++s)
-                load(m, base + p.at + s * kFewRows + lane, s * kFewRows + lane < p.n, K, k0);
+              for (int s = 0; s * kFewRows < p.n && ok; ++s) {
+                const bool is = begin();
+                if (is) rows(m, base + s * kFewRows, min(kFewRows, p.n - s * kFewRows), 0, K, k0, min(W::kChunk, K - k0));
+                end_stage(is);
+              }
           }
         }
       }
     }
-    if (!ok) {
-      few_timeout(abort);
-      // Copies under way end (bounded waits) before the block does.
-      volatile int never = 0;
-      for (int i = 0; i < min(issued, kStages); ++i) {
-        if (--stage < 0) {
-          stage = kStages - 1;
-          phase ^= 1u;
-        }
-        mbar_wait(&w_full[stage], phase, &never);
-      }
-    }
+    if (!ok) few_timeout(abort);
+    async_wait_all();   // (nothing is under way into the memory of a block that has ended)
   } else if (warp >= kWarpX) {
     // ------------------------------------------------------------ tokens
     // Slot after slot of 512 channels goes round the four warps.
