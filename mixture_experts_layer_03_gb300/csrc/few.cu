@@ -22,7 +22,9 @@
 // columns for every expert, which keeps lists of tokens out of the loops: in the first products the others'
 // results are dropped, in the second an expert's sums are added to those of its tokens only (a weight
 // that is not finite reaches nobody else); the routing weight is multiplied into h.
-// The eight consumer warps cut a chunk of the contraction between them and add up at the end.
+// Four teams of four consumer warps: a team takes every fourth stage, its warps a quarter of the
+// stage's channels each, and they add up at the end of a part. (One team of eight or sixteen warps for
+// every stage: a warp then had 60 instructions of overhead to 30 of work, and the teams of 16 spilled.)
 //
 // Numbers. 16-bit weights: operands of x's type, h rounded to it once (with the routing weight; f16 after
 // a power of two for each token, see below). 4-bit weights: codes to f16 exactly; nv scales
@@ -49,48 +51,47 @@ namespace {
 constexpr int kFewTokens = MOE_FEW_TOKENS;
 static_assert(kFewTokens == 16, "two column tiles");
 constexpr int kFewExperts = 128 + 1;             // T * k at most, and the shared one
-constexpr int kMmaWarps = 8;                     // consumers
+constexpr int kMmaWarps = 16;                    // consumers
 constexpr int kXWarps = 4;                       // producers of the tokens' side
 constexpr int kWWarps = 2;                       // producers of the weights' side, a stage each in turn
 constexpr int kWarpW = kMmaWarps, kWarpX = kWarpW + kWWarps;
 constexpr int kFewThreads = 32 * (kWarpX + kXWarps);
-constexpr int kXSlots = kXWarps;                 // each of 512 channels of all tokens
-static_assert(kXSlots % 2 == 0, "two slots to a chunk of 4-bit weights");
-constexpr int kXPitch = 1024 + 64;               // (64 more: rows' 16-byte parts on different banks)
+constexpr int kTeams = 4, kTeamWarps = kMmaWarps / kTeams;   // of consumers
+constexpr int kXSlots = kXWarps;                 // chunks of the tokens' side
+static_assert(kXSlots == kTeams, "a slot belongs to the same teams throughout a part");
 constexpr int kFewRows = 32;                     // rows of weights a stage
-constexpr int kFewSub = 4;                       // stages that share a chunk of tokens
-// The same in the second products, where the sums over the experts take registers too.
-template <int kNt>
-constexpr int few_sub2() { return kNt == 1 ? kFewSub : kFewSub / 2; }
 constexpr int kFewMaxBlocks = 192;
-constexpr int kFewSmem = 232448 - 9216;          // of a block, without the static part
+constexpr int kFewSmem = 232448 - 10240;         // of a block, without the static part
 
 enum : int { kW16b = 0, kW16h = 1, kW4mx = 2, kW4nv = 3 };   // bf16, f16, mx, nv
 
 template <int kW>
 struct FewW {
   static constexpr bool k4 = kW >= kW4mx;
-  static constexpr int kChunk = k4 ? 1024 : 512;                 // channels of the contraction a stage
-  static constexpr int kHalves = kChunk / 512;                   // slots of the tokens' side
-  static constexpr int kGroups = kChunk / 32 / kMmaWarps;        // of 32 channels, a warp's part
-  static constexpr int kPitch = k4 ? 512 + 16 : 1024 + 64;       // of a row of the stage
-  static constexpr int kScaleBytes = kW == kW4nv ? 64 : kW == kW4mx ? 32 : 0;   // of a row
-  static constexpr int kScalePitch = k4 ? kScaleBytes + 16 : 0;
+  static constexpr int kChunk = k4 ? 512 : 256;                  // channels of the contraction a stage
+  static constexpr int kGroups = kChunk / 32 / kTeamWarps;       // of 32 channels, a warp's part
+  static constexpr int kRowBytes = k4 ? kChunk / 2 : 2 * kChunk;
+  static constexpr int kPitch = k4 ? kRowBytes + 16 : kRowBytes + 64;   // (rows' parts on different banks)
+  static constexpr int kScaleBytes = kW == kW4nv ? kChunk / 16 : kW == kW4mx ? kChunk / 32 : 0;
+  static constexpr int kScalePitch = k4 ? 48 : 0;
   static constexpr int kStage = kFewRows * (kPitch + kScalePitch);
+  static constexpr int kXPitch = 2 * kChunk + 64;
 };
 
+template <int kW, int kNt>
+constexpr int few_x_bytes() { return kXSlots * 8 * kNt * FewW<kW>::kXPitch; }
 template <int kNt>
-constexpr int few_x_bytes() { return kXSlots * 8 * kNt * kXPitch; }
-template <int kNt>
-constexpr int few_red_bytes() { return kMmaWarps * 2 * kNt * 512; }   // one of two
+constexpr int few_red_bytes() { return kMmaWarps * 2 * kNt * 512; }
+// A multiple of the teams: a stage's place in the ring then belongs to one team throughout a part, which
+// waits for each of its uses in turn.
 template <int kW, int kNt>
 constexpr int few_stages() {
-  constexpr int n = (kFewSmem - 128 - few_x_bytes<kNt>() - 2 * few_red_bytes<kNt>()) / FewW<kW>::kStage;
-  return n < 8 ? n : 8;
+  constexpr int n = (kFewSmem - 128 - few_x_bytes<kW, kNt>() - few_red_bytes<kNt>()) / FewW<kW>::kStage;
+  return (n < 16 ? n : 16) / kTeams * kTeams;
 }
 template <int kW, int kNt>
 constexpr int few_smem_bytes() {
-  return 128 + few_x_bytes<kNt>() + 2 * few_red_bytes<kNt>() + few_stages<kW, kNt>() * FewW<kW>::kStage;
+  return 128 + few_x_bytes<kW, kNt>() + few_red_bytes<kNt>() + few_stages<kW, kNt>() * FewW<kW>::kStage;
 }
 
 struct FewMatrix {
@@ -135,8 +136,8 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
   Vec<T, 16>::unpack(v, f);
 }
 
-// A block computes the logits of kPer rows of wg for up to kT tokens, its warps each an eighth of H; blocks
-// past those find the largest |x| of a token each.
+// A block computes the logits of kPer rows of wg for kT tokens (of blockIdx.y), its warps each an eighth of H;
+// blocks past those find the largest |x| of a token each.
 template <typename T, int kT, int kPer>
 __global__ void __launch_bounds__(kGateThreads)
 few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, int H, int E, int rows,
@@ -146,11 +147,12 @@ few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, in
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nv = H / 8;
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (tid < 2) ticket[tid] = 0;
     if (tid < kFewTokens) tmax[tid] = 0;
   }
   if (static_cast<int>(blockIdx.x) >= gate_blocks) {
+    if (blockIdx.y != 0) return;
     __shared__ uint32_t s_max[kGateThreads / 32];
     const int t = blockIdx.x - gate_blocks;
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * H);
@@ -172,7 +174,7 @@ few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, in
     return;
   }
   __shared__ float s_sum[kGateThreads / 32][kPer][kT];
-  const int e0 = blockIdx.x * kPer;
+  const int e0 = blockIdx.x * kPer, t0 = blockIdx.y * kT;
   float acc[kPer][kT] = {};
 #pragma unroll 2
   for (int v = tid; v < nv; v += kGateThreads) {
@@ -185,7 +187,7 @@ few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, in
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       float f[8];
-      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(min(t, n_tok - 1)) * H) + v), f);
+      unpack8<T>(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(min(t0 + t, n_tok - 1)) * H) + v), f);
 #pragma unroll
       for (int p = 0; p < kPer; ++p)
 #pragma unroll
@@ -203,10 +205,10 @@ few_gate_kernel(const T* __restrict__ x, const T* __restrict__ wg, int n_tok, in
     }
   __syncthreads();
   if (tid < kPer * kT) {
-    const int p = tid / kT, t = tid % kT, e = e0 + p;
+    const int p = tid / kT, t = t0 + tid % kT, e = e0 + p;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kGateThreads / 32; ++i) s += s_sum[i][p][t];
+    for (int i = 0; i < kGateThreads / 32; ++i) s += s_sum[i][p][tid % kT];
     if (t < n_tok && e < rows) {
       if (e < E) logits[t * E + e] = s;
       else shared_logits[t] = s;
@@ -221,14 +223,14 @@ template <bool kBf16>
 __device__ __forceinline__ void mma_16bit(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                           const float (&c)[4]) {
   if constexpr (kBf16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
           "f"(c[3]));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -248,6 +250,10 @@ __device__ __forceinline__ void async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+
 // 2^(14 - e) for a largest value of [2^e, 2^(e + 1)), 1 for none or one that is not finite; bounded so
 // that the inverse is a normal number too.
 __device__ __forceinline__ float to_f16_range(float amax) {
@@ -260,6 +266,11 @@ __device__ __forceinline__ float inverse_power(float p) {
   return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
+// A number hi + lo.
+struct Pair {
+  float hi, lo;
+};
+
 // Everything about the chosen experts that the block's warps share.
 struct FewShared {
   int32_t ids[kFewTokens * kMaxTopK];
@@ -267,11 +278,13 @@ struct FewShared {
   int sel[kFewTokens * kMaxTopK];
   float sel_l[kFewTokens * kMaxTopK];
   double e[kFewTokens * kMaxTopK];
+  Pair sel_e[kFewTokens * kMaxTopK];
   float ek[kFewTokens * kMaxTopK];
   double z[kFewTokens];
   uint32_t mask[8];
   uint8_t list[kFewExperts];               // the chosen experts, ascending
   int8_t slot[kFewExperts][kFewTokens];    // of a token at a chosen expert, -1: none; last: the shared one
+  uint16_t tokens[kFewExperts];            // of a chosen expert, a bit each
   float weight_s[kFewTokens];              // of the shared expert
   float x_mul[kFewTokens], x_inv[kFewTokens];
   uint32_t tmax[kFewTokens];
@@ -300,33 +313,124 @@ __device__ __noinline__ void few_select(const float* row, const FewArgs& a, int 
   record_selection(row, sel, a.k, lane, ps, t);
 }
 
+// Sums and quotients of pairs, lo half a unit of hi or less: some 2^-28 of the value, for the routing
+// weights' one rounding at the end. (fp64 runs at 1/64 of fp32's rate here and every block routes for
+// itself: an exponential and a division of 128 slots took 10 us.)
+__device__ __forceinline__ Pair pair_of(float a, float b) {      // a + b, |a| >= |b| or a = 0
+  const float s = a + b;
+  return Pair{s, b - (s - a)};
+}
+__device__ __forceinline__ Pair pair_sum(float a, float b) {     // any a, b (Knuth)
+  const float s = a + b, t = s - a;
+  return Pair{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  const Pair s = pair_sum(a.hi, b.hi);
+  return pair_of(s.hi, s.lo + (a.lo + b.lo));
+}
+__device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.hi, b.hi);
+  const float rest = fmaf(-q, b.hi, a.hi) + (a.lo - q * b.lo);
+  return pair_of(q, __fdividef(rest, b.hi));
+}
+// exp(a), -64 <= a <= 0: a = n ln 2 + r with ln 2 in two parts, the first of 16 bits (Cody and Waite), so
+// that n times it is exact; then 1 + r + r^2 / 2 + ..., |r| <= 0.35, its first terms in pairs.
+__device__ __forceinline__ Pair pair_exp(Pair a) {
+  constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = static_cast<float>(0.693147180559945309417 - 0x1.62e4p-1);
+  const float n = rintf(a.hi * 1.44269504f);
+  const Pair r = pair_sum(fmaf(-n, kLn2Hi, a.hi), fmaf(-n, kLn2Lo, a.lo));
+  const float sq = r.hi * r.hi, sq_lo = fmaf(r.hi, r.hi, -sq);
+  float q = 1.0f / 40320;
+  q = fmaf(q, r.hi, 1.0f / 5040);
+  q = fmaf(q, r.hi, 1.0f / 720);
+  q = fmaf(q, r.hi, 1.0f / 120);
+  q = fmaf(q, r.hi, 1.0f / 24);
+  q = fmaf(q, r.hi, 1.0f / 6);
+  // r.lo (1 + r): the slope of exp at r.hi
+  const float small = fmaf(r.lo, r.hi, r.lo) + fmaf(0.5f, sq_lo, r.hi * sq * q);
+  const Pair one = pair_of(1.0f, r.hi);
+  const Pair two = pair_sum(one.hi, 0.5f * sq);
+  const Pair e = pair_of(two.hi, (one.lo + two.lo) + small);
+  const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);
+  return Pair{e.hi * scale, e.lo * scale};
+}
+
+// The weights of block_pair_weights (route_device.cuh) for the methods whose slots are in order already, in
+// pairs; by one thread a slot. False, in every thread: a logit is so far off that fp32's range may not do.
+__device__ __forceinline__ bool few_weights(const FewArgs& a, FewShared* sh) {
+  const int p = threadIdx.x, pairs = a.T * a.k, method = a.route.method;
+  const bool sigmoid = method != MOE_ROUTE_DEFAULT && method != MOE_ROUTE_RENORMALIZE &&
+                       method != MOE_ROUTE_RENORMALIZE_NAIVE;
+  const int t = p / a.k, j = p - t * a.k;
+  bool fits = method != MOE_ROUTE_GROUPED_TOPK;
+  Pair e = {};
+  if (p < pairs && fits) {
+    const float* l = sh->sel_l + t * kMaxTopK;
+    const float v = l[j];
+    if (sigmoid) {
+      fits = fabsf(v) <= 60.0f;
+      const Pair x = pair_exp(Pair{fits ? -fabsf(v) : 0.0f, 0.0f});
+      e = pair_div(v < 0.0f ? x : Pair{1.0f, 0.0f}, pair_add(Pair{1.0f, 0.0f}, x));
+    } else {
+      const Pair d = pair_sum(v, -l[0]);      // slot 0 has the largest logit
+      fits = d.hi >= -60.0f;
+      e = pair_exp(fits ? d : Pair{});
+    }
+    sh->sel_e[p] = e;
+  }
+  if (!__syncthreads_and(fits)) return false;
+  if (p < pairs) {
+    Pair w = e;
+    if (method == MOE_ROUTE_DEFAULT) {
+      const double z = sh->z[t];
+      const float hi = static_cast<float>(z);
+      w = pair_div(e, Pair{hi, static_cast<float>(z - static_cast<double>(hi))});
+    } else if (method != MOE_ROUTE_LLAMA4) {
+      Pair sum = {};
+      for (int i = 0; i < a.k; ++i) sum = pair_add(sum, sh->sel_e[t * a.k + i]);
+      if (method == MOE_ROUTE_DEEPSEEKV3) sum = pair_add(sum, Pair{1e-20f, 0.0f});
+      w = pair_div(e, sum);
+    }
+    const float rsf = method == MOE_ROUTE_DEEPSEEKV3 ? a.route.routed_scaling_factor : 1.0f;
+    const float product = w.hi * rsf;
+    sh->ids[p] = sh->sel[t * kMaxTopK + j];
+    sh->scales[p] = product + (fmaf(w.hi, rsf, -product) + w.lo * rsf);
+  }
+  __syncthreads();
+  return true;
+}
+
+constexpr int kFewRouteBytes = 36 * 1024;        // scratch
+
 // Routing of all tokens by the whole block, and the tables of the chosen experts.
 __device__ __noinline__ void few_route(const FewArgs& a, FewShared* sh, uint8_t* scratch) {
   const int tid = threadIdx.x, warp = tid >> 5;
   constexpr int kWarps = kFewThreads / 32;
-  static_assert(kWarps * (1024 + 512) <= few_x_bytes<1>(), "routing scratch");
+  static_assert(kWarps >= kFewTokens && kWarps * (1024 + 512) <= kFewRouteBytes,
+                "a warp a token, and its scratch");
   float* s_key = reinterpret_cast<float*>(scratch) + warp * 256;
   uint8_t* s_exact = scratch + kWarps * 1024 + warp * 512;
   for (int i = tid; i < kFewExperts * kFewTokens; i += kFewThreads) (&sh->slot[0][0])[i] = -1;
   if (tid < 8) sh->mask[tid] = 0;
   if (tid < kFewTokens) sh->tmax[tid] = 0;
-  for (int t = warp; t < a.T; t += kWarps) {
-    const float* row = a.logits + t * a.E;
-    if (a.E <= 128) few_select<4>(row, a, t, s_key, s_exact, s_exact + 256, sh);
-    else few_select<8>(row, a, t, s_key, s_exact, s_exact + 256, sh);
-    __syncwarp();
+  if (warp < a.T) {
+    const float* row = a.logits + warp * a.E;
+    if (a.E <= 128) few_select<4>(row, a, warp, s_key, s_exact, s_exact + 256, sh);
+    else few_select<8>(row, a, warp, s_key, s_exact, s_exact + 256, sh);
   }
   __syncthreads();
-  const PairSlots ps{sh->sel, sh->sel_l, sh->e, sh->ek, sh->z};
-  const int method = a.route.method;
-  const float rsf = a.route.routed_scaling_factor;
-  if (method == MOE_ROUTE_GROUPED_TOPK)
-    block_pair_weights<2>(a.T, 0, a.T, a.k, method, rsf, ps, sh->ids, sh->scales);
-  else if (method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2)
-    block_pair_weights<1>(a.T, 0, a.T, a.k, method, method == MOE_ROUTE_DEEPSEEKV3 ? rsf : 1.0f, ps,
-                          sh->ids, sh->scales);
-  else
-    block_pair_weights<0>(a.T, 0, a.T, a.k, method, 1.0f, ps, sh->ids, sh->scales);
+  if (!few_weights(a, sh)) {
+    const PairSlots ps{sh->sel, sh->sel_l, sh->e, sh->ek, sh->z};
+    const int method = a.route.method;
+    const float rsf = a.route.routed_scaling_factor;
+    if (method == MOE_ROUTE_GROUPED_TOPK)
+      block_pair_weights<2>(a.T, 0, a.T, a.k, method, rsf, ps, sh->ids, sh->scales);
+    else if (method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2)
+      block_pair_weights<1>(a.T, 0, a.T, a.k, method, method == MOE_ROUTE_DEEPSEEKV3 ? rsf : 1.0f, ps,
+                            sh->ids, sh->scales);
+    else
+      block_pair_weights<0>(a.T, 0, a.T, a.k, method, 1.0f, ps, sh->ids, sh->scales);
+  }
   const int pairs = a.T * a.k;
   if (tid < pairs) {
     const int e = sh->ids[tid];
@@ -356,13 +460,28 @@ __device__ __noinline__ void few_route(const FewArgs& a, FewShared* sh, uint8_t*
     sh->weight_s[tid] = a.shared_gate ? 1.0f / (1.0f + expf(-a.shared_logits[tid])) : 1.0f;
   }
   __syncthreads();
+  if (tid < kFewExperts) {
+    uint32_t bits = 0;
+    for (int t = 0; t < kFewTokens; ++t) bits |= static_cast<uint32_t>(sh->slot[tid][t] >= 0) << t;
+    sh->tokens[tid] = static_cast<uint16_t>(bits);
+  }
+  __syncthreads();
 }
 
-// A part of a slice, as all roles walk them.
+// A part of a slice, as all roles walk them: its rows in 1, 2 or 4 equal subs, a stage each for every chunk
+// of the contraction. Stage i of a part (chunk i / subs, sub i % subs) is team i % 4's, so that a team
+// has one sub throughout a part: its sums are 8 registers a column tile, and with few rows the teams
+// share out the chunks.
 struct FewPart {
   int a;       // first products: place among the chosen experts (n: the shared one)
   int at;      // its first channel, or first row of y
   int n;       // channels or rows
+  int subs, per;
+  __device__ __forceinline__ FewPart(int a_, int at_, int n_, int most) : a(a_), at(at_), n(n_) {
+    subs = n <= most ? 1 : n <= 2 * most ? 2 : 4;
+    per = (n + subs - 1) / subs;
+  }
+  __device__ __forceinline__ int of(int sub) const { return min(per, n - sub * per); }
 };
 
 template <int kW, int kNt>
@@ -370,7 +489,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   using W = FewW<kW>;
   constexpr bool kBf16 = kW == kW16b;            // the products' operands
   constexpr int kStages = few_stages<kW, kNt>();
-  static_assert(kStages >= 3, "ring");
+  static_assert(kStages >= kTeams && kStages % kTeams == 0, "ring");
+  static_assert(kFewRouteBytes <= kStages * W::kStage, "routing scratch");
   extern __shared__ uint8_t smem_raw[];
   __shared__ FewShared sh;
   __shared__ uint64_t w_full[kStages], w_empty[kStages], x_full[kXSlots], x_empty[kXSlots];
@@ -380,19 +500,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* sW = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   uint8_t* sX = sW + kStages * W::kStage;
-  float* sRed = reinterpret_cast<float*>(sX + few_x_bytes<kNt>());
+  float* sRed = reinterpret_cast<float*>(sX + few_x_bytes<kW, kNt>());
   volatile int* abort = &s_abort;
 
   pdl_trigger();
   for (int i = tid; i < 2 * kFewMaxBlocks + 2; i += kFewThreads) s_ticket[i] = -1;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&w_full[s], 32);   // a producer warp's lanes
-      mbar_init(&w_empty[s], kMmaWarps);
+      mbar_init(&w_full[s], 32);           // a producer warp's lanes
+      mbar_init(&w_empty[s], kTeamWarps);
     }
     for (int s = 0; s < kXSlots; ++s) {
       mbar_init(&x_full[s], 1);
-      mbar_init(&x_empty[s], kMmaWarps / W::kHalves);
+      mbar_init(&x_empty[s], kMmaWarps);   // 4 / subs from each warp that reads it
     }
     s_abort = 0;
     fence_barrier_init();
@@ -407,7 +527,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     sh.x_mul[tid] = p;
     sh.x_inv[tid] = inverse_power(p);
   }
-  few_route(a, &sh, sX);
+  few_route(a, &sh, sW);
 
   const int n_exp = sh.n, T = a.T, H = a.H;
   const int n_all = n_exp + (a.shared_I > 0);
@@ -417,34 +537,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   auto cut2 = [&](int i) { return static_cast<int>(static_cast<int64_t>(H) * i / n_blocks); };
   // The part of the first products that starts at channel q of all, in a slice that ends at `end`.
   auto part1 = [&](int q, int end) {
-    FewPart p;
-    int left;
-    if (q < routed) {
-      p.a = q / a.I;
-      p.at = q - p.a * a.I;
-      left = a.I - p.at;
-    } else {
-      p.a = n_exp;
-      p.at = q - routed;
-      left = a.shared_I - p.at;
-    }
-    p.n = min(16 * kFewSub, min(end - q, left));
-    return p;
+    const bool own = q < routed;
+    const int at = own ? q / a.I : n_exp;
+    const int ch = own ? q - at * a.I : q - routed;
+    return FewPart(at, ch, min(kTeams * 16, min(end - q, (own ? a.I : a.shared_I) - ch)), 16);
   };
-  constexpr int kSub2 = few_sub2<kNt>();
-  auto part2 = [&](int r, int end) { return FewPart{0, r, min(kFewRows * kSub2, end - r)}; };
+  // Of the rows left, equal parts.
+  auto part2 = [&](int r, int end) {
+    const int left = end - r, parts = (left + kTeams * kFewRows - 1) / (kTeams * kFewRows);
+    return FewPart(0, r, (left + parts - 1) / parts, kFewRows);
+  };
   auto inner = [&](int at) { return at < n_exp ? a.I : a.shared_I; };   // channels of a chosen expert
   // Ticket i of this block, when it is there; 2 n_blocks (no work) if it does not come.
   auto ticket_at = [&](int i, bool& ok) {
     const volatile int* at = &s_ticket[i];
     int v = *at;
+    if (v >= 0) return v;
     const uint64_t t0 = globaltimer_ns();
-    while (v < 0) {
+    while ((v = *at) < 0) {
       if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
         ok = false;
         return 2 * n_blocks;
       }
-      v = *at;
+      __nanosleep(64);
     }
     return v;
   };
@@ -452,34 +567,41 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   if (warp >= kWarpW && warp < kWarpX) {
     // ------------------------------------------------------------ weights
     // Rows as they lie in memory, by 16-byte asynchronous copies of whole warps. (Bulk copies of a row each
-    // are issued one lane after the other: 69 us for 5 tokens, 60 experts of 1504 x 736 in mx, so N us.)
+    // are issued one lane after the other, at 30 to 60 cycles: 511 us for 4 tokens through 8 experts of
+    // 4096 x 14336 in bf16, so 336.)
     const int mine = warp - kWarpW;
     int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
-    constexpr int kBlock = kW == kW4nv ? 16 : 32;
     // n rows of len channels, from `row` of m and channel k0 of K on, to rows from `at` on of the stage.
     auto rows = [&](const FewMatrix& m, int64_t row, int n, int at, int K, int k0, int len) {
-      uint8_t* dst = sW + stage * W::kStage + at * W::kPitch + lane * 16;
+      constexpr int kLanes = W::kRowBytes / 16, kStep = 32 / kLanes;   // lanes to a row, rows at once
+      const int part = lane % kLanes, first = lane / kLanes;
       const int bytes = W::k4 ? len / 2 : len * 2;
       const int64_t pitch = W::k4 ? K / 2 : 2 * static_cast<int64_t>(K);
-      const uint8_t* src = m.w + row * pitch + (W::k4 ? k0 / 2 : 2 * k0) + lane * 16;
-      const bool in = lane * 16 < bytes, in2 = !W::k4 && 512 + lane * 16 < bytes;
+      uint8_t* dst = sW + stage * W::kStage + (at + first) * W::kPitch + part * 16;
+      const uint8_t* src = m.w + (row + first) * pitch + (W::k4 ? k0 / 2 : 2 * k0) + part * 16;
+      if (part * 16 < bytes) {
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        if (in) async_load_16(dst, src);
-        if (in2) async_load_16(dst + 512, src + 512);
-        dst += W::kPitch;
-        src += pitch;
+        for (int i = first; i < n; i += kStep) {
+          async_load_16(dst, src);
+          dst += kStep * W::kPitch;
+          src += kStep * pitch;
+        }
       }
       if constexpr (W::k4) {
-        constexpr int kLanes = W::kScaleBytes / 16;   // to a row of scales
+        constexpr int kBlock = kW == kW4nv ? 16 : 32;
+        constexpr int kLanesS = W::kScaleBytes / 16;   // to a row of scales
         const int sp = fp4_scale_pitch(K, kW == kW4nv ? kFp4Nv : kFp4Mx);
-        const int part = lane % kLanes, there = (sp - k0 / kBlock) / 16;
-        for (int i = lane / kLanes; i < n; i += 32 / kLanes)
-          if (part < there)
-            async_load_16(sW + stage * W::kStage + kFewRows * W::kPitch + (at + i) * W::kScalePitch + part * 16,
-                          m.scales + (row + i) * sp + k0 / kBlock + part * 16);
+        const int ps = lane % kLanesS, i = lane / kLanesS;
+        static_assert(32 / kLanesS >= 16, "a row each");
+        uint8_t* to = sW + stage * W::kStage + kFewRows * W::kPitch + (at + i) * W::kScalePitch + ps * 16;
+        const uint8_t* from = m.scales + (row + i) * sp + k0 / kBlock + ps * 16;
+        if (ps * 16 < sp - k0 / kBlock) {
+          if (i < n) async_load_16(to, from);
+          if (32 / kLanesS < kFewRows && i + 32 / kLanesS < n)
+            async_load_16(to + 32 / kLanesS * W::kScalePitch, from + 32 / kLanesS * sp);
+        }
       }
     };
     // A stage is this warp's or the other one's.
@@ -520,12 +642,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           const int64_t base = (own ? static_cast<int64_t>(sh.list[p.a]) * 2 * width : 0) + p.at;
           for (int k0 = 0; k0 < H && ok; k0 += W::kChunk) {
             const int len = min(W::kChunk, H - k0);
-            for (int s = 0; s * 16 < p.n && ok; ++s) {
+            for (int s = 0; s < p.subs && ok; ++s) {
               const bool is = begin();
               if (is) {
-                const int n = min(16, p.n - s * 16);
-                rows(m, base + s * 16, n, 0, H, k0, len);
-                rows(m, base + width + s * 16, n, 16, H, k0, len);
+                rows(m, base + s * p.per, p.of(s), 0, H, k0, len);
+                rows(m, base + width + s * p.per, p.of(s), 16, H, k0, len);
               }
               end_stage(is);
             }
@@ -541,9 +662,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             const int K = inner(e);
             const int64_t base = (own ? static_cast<int64_t>(sh.list[e]) * H : 0) + p.at;
             for (int k0 = 0; k0 < K && ok; k0 += W::kChunk)
-              for (int s = 0; s * kFewRows < p.n && ok; ++s) {
+              for (int s = 0; s < p.subs && ok; ++s) {
                 const bool is = begin();
-                if (is) rows(m, base + s * kFewRows, min(kFewRows, p.n - s * kFewRows), 0, K, k0, min(W::kChunk, K - k0));
+                if (is) rows(m, base + s * p.per, p.of(s), 0, K, k0, min(W::kChunk, K - k0));
                 end_stage(is);
               }
           }
@@ -554,19 +675,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     async_wait_all();   // (nothing is under way into the memory of a block that has ended)
   } else if (warp >= kWarpX) {
     // ------------------------------------------------------------ tokens
-    // Slot after slot of 512 channels goes round the four warps.
+    // Chunk after chunk goes round the four warps and slots. Only the rows of an expert's tokens are
+    // written: what the others' hold reaches columns that nobody looks at.
     const int mine = warp - kWarpX;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true, waited = false;
     float t_mul = 1.0f;                     // lane t: token t's power of two for h
+    constexpr int kVecs = W::kChunk / 8, kPer = kVecs / 32;   // of a row of a slot, a lane's
     auto turn = [&] {                       // is it this warp's slot?
       const bool is = slot == mine;
       if (++slot == kXSlots) slot = 0;
       return is;
     };
-    // (a chunk's second slot is passed on empty where the contraction ends before it)
-    auto slots_end = [](int K) { return (K + W::kChunk - 1) / W::kChunk * W::kChunk; };
     auto wait_empty = [&] {
       ok = __all_sync(0xffffffffu, mbar_wait(&x_empty[mine], phase ^ 1u, abort));
       phase ^= 1u;
@@ -576,34 +697,53 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(&x_full[mine]);
     };
-    uint8_t* dst = sX + mine * 8 * kNt * kXPitch;
+    uint8_t* dst = sX + mine * 8 * kNt * W::kXPitch;
     for (int i = 0; ok; ++i) {
       const int ticket = __shfl_sync(0xffffffffu, ticket_at(i, ok), 0);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || ticket >= 2 * n_blocks) break;
       if (ticket < n_blocks) {
         for (int q = cut1(ticket), end = cut1(ticket + 1); q < end && ok;) {
-          q += part1(q, end).n;
-          for (int k0 = 0; k0 < slots_end(H) && ok; k0 += 512) {
+          const FewPart p = part1(q, end);
+          q += p.n;
+          const uint32_t tokens = sh.tokens[p.a];
+          for (int k0 = 0; k0 < H && ok; k0 += W::kChunk) {
             if (!turn()) continue;
             if (!wait_empty()) break;
-            const int nv = min(512, H - k0) / 8;
-#pragma unroll 4
-            for (int v = lane; v < T * 64; v += 32) {
-              const int t = v >> 6, c = v & 63;
-              if (c >= nv) continue;
-              uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
-                                                             static_cast<int64_t>(t) * H + k0) + c);
-              if (W::k4) {
-                float f[8];
-                if (a.bf16) unpack8<__nv_bfloat16>(u, f);
-                else unpack8<__half>(u, f);
-                const float mul = sh.x_mul[t];
+            const int nv = min(W::kChunk, H - k0) / 8;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + k0);
+            // Four tokens' loads at once.
+            for (uint32_t rest = tokens; rest;) {
+              int t[4];
+              uint4 u[4][kPer];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= mul;
-                u = Vec<__half, 16>::pack(f);
+              for (int i4 = 0; i4 < 4; ++i4) {
+                t[i4] = rest ? __ffs(rest) - 1 : -1;
+                rest &= rest - 1;
+#pragma unroll
+                for (int h = 0; h < kPer; ++h)
+                  if (t[i4] >= 0 && lane + 32 * h < nv)
+                    u[i4][h] = __ldg(src + static_cast<int64_t>(t[i4]) * (H / 8) + lane + 32 * h);
               }
-              *reinterpret_cast<uint4*>(dst + t * kXPitch + c * 16) = u;
+#pragma unroll
+              for (int i4 = 0; i4 < 4; ++i4) {
+                if (t[i4] < 0) break;
+                const float mul = sh.x_mul[t[i4]];
+#pragma unroll
+                for (int h = 0; h < kPer; ++h) {
+                  if (lane + 32 * h >= nv) continue;
+                  uint4 v = u[i4][h];
+                  if (W::k4) {
+                    float f[8];
+                    if (a.bf16) unpack8<__nv_bfloat16>(v, f);
+                    else unpack8<__half>(v, f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] *= mul;
+                    v = Vec<__half, 16>::pack(f);
+                  }
+                  *reinterpret_cast<uint4*>(dst + t[i4] * W::kXPitch + (lane + 32 * h) * 16) = v;
+                }
+              }
             }
             publish();
           }
@@ -620,28 +760,42 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           r += part2(r, end).n;
           for (int e = 0; e < n_all && ok; ++e) {
             const int K = inner(e);
-            for (int k0 = 0; k0 < slots_end(K) && ok; k0 += 512) {
+            for (int k0 = 0; k0 < K && ok; k0 += W::kChunk) {
               if (!turn()) continue;
               if (!wait_empty()) break;
-              const int nv = min(512, K - k0) / 8;
-              for (int t = 0; t < T; ++t) {
-                const int j = sh.slot[e][t];
-                const float mul = __shfl_sync(0xffffffffu, t_mul, t);
-                const float4* src = reinterpret_cast<const float4*>(
-                    a.h + (static_cast<int64_t>(t) * (a.k + 1) + max(j, 0)) * a.h_ld + k0);
+              const int nv = min(W::kChunk, K - k0) / 8;
+              for (uint32_t rest = sh.tokens[e]; rest;) {
+                int t[2];
+                float4 u[2][kPer][2];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const int c = lane + 32 * half;
-                  if (c >= nv) continue;
-                  uint4 u = make_uint4(0, 0, 0, 0);
-                  if (j >= 0) {
-                    const float4 lo = __ldcg(src + 2 * c), hi = __ldcg(src + 2 * c + 1);
+                for (int i2 = 0; i2 < 2; ++i2) {
+                  t[i2] = rest ? __ffs(rest) - 1 : -1;
+                  rest &= rest - 1;
+                  if (t[i2] < 0) continue;
+                  const float4* src = reinterpret_cast<const float4*>(
+                      a.h + (static_cast<int64_t>(t[i2]) * (a.k + 1) + sh.slot[e][t[i2]]) * a.h_ld + k0);
+#pragma unroll
+                  for (int h = 0; h < kPer; ++h)
+                    if (lane + 32 * h < nv) {
+                      u[i2][h][0] = __ldcg(src + 2 * (lane + 32 * h));
+                      u[i2][h][1] = __ldcg(src + 2 * (lane + 32 * h) + 1);
+                    }
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < 2; ++i2) {
+                  if (t[i2] < 0) break;
+                  const float mul = __shfl_sync(0xffffffffu, t_mul, t[i2]);
+#pragma unroll
+                  for (int h = 0; h < kPer; ++h) {
+                    if (lane + 32 * h >= nv) continue;
+                    const float4 lo = u[i2][h][0], hi = u[i2][h][1];
                     const float f[8] = {lo.x * mul, lo.y * mul, lo.z * mul, lo.w * mul,
                                         hi.x * mul, hi.y * mul, hi.z * mul, hi.w * mul};
-                    if constexpr (kBf16) u = Vec<__nv_bfloat16, 16>::pack(f);
-                    else u = Vec<__half, 16>::pack(f);
+                    uint4 v;
+                    if constexpr (kBf16) v = Vec<__nv_bfloat16, 16>::pack(f);
+                    else v = Vec<__half, 16>::pack(f);
+                    *reinterpret_cast<uint4*>(dst + t[i2] * W::kXPitch + (lane + 32 * h) * 16) = v;
                   }
-                  *reinterpret_cast<uint4*>(dst + t * kXPitch + c * 16) = u;
                 }
               }
               publish();
@@ -655,159 +809,149 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     // ------------------------------------------------------------ products
     // A wait that runs out leaves the loops' course as it is (the warps meet at barriers): what is
     // computed after it is garbage that the host hears of.
-    int stage = 0, slot = 0, red = 0;
-    uint32_t phase = 0, x_phase = 0;
     bool ok = true;
     const int g = lane >> 2, c = lane & 3;         // of the fragments
-    constexpr int kHalfWarps = kMmaWarps / W::kHalves;
-    constexpr bool kHold = kNt == 1;               // the tokens' fragments of a chunk stay in registers
-    const int half = warp / kHalfWarps;            // the slot of a chunk that this warp reads
-    auto clear = [](auto& v) {
-#pragma unroll
-      for (auto& sub : v)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sub[m][n][j] = 0.0f;
-    };
-    // A chunk of the contraction (`len` channels) for `subs` stages of rows.
-    auto chunk = [&](auto& acc, int len, int subs) {
-      constexpr int kSubs = sizeof(acc) / sizeof(acc[0]);
-      const int groups = min(max(len / 32 - warp * W::kGroups, 0), W::kGroups);
-      const int xs = slot + half;   // (kXSlots is a multiple of kHalves: a slot is always the same half's)
-      const uint8_t* x_src = sX + (xs * 8 * kNt + g) * kXPitch + (warp % kHalfWarps) * W::kGroups * 64 + c * 16;
-      uint4 held[W::kGroups];
+    const int team = warp / kTeamWarps, member = warp % kTeamWarps;
+    int chunks = 0;                                // of the parts before this one: the tokens' slots so far
+    int first = 0;                                 // place in the ring of the part's first stage
+    uint32_t first_phase = 0;
+
+    // Stage i of the part, by its team: sub-tile products of chunk `xc` (of all so far), `len` channels.
+    // `second`: there are rows past the first 16.
+    auto multiply = [&](float (&acc)[2][kNt][4], int i, int xc, int len, int subs, uint32_t tokens, bool second) {
+      const int place = first + i, lap = place / kStages;
+      const int stage = place - lap * kStages, xs = xc % kXSlots;
+      const uint32_t phase = first_phase ^ (lap & 1), x_phase = xc / kXSlots & 1;
+      const int groups = min(max(len / 32 - member * W::kGroups, 0), W::kGroups);
+      const uint8_t* x = sX + (xs * 8 * kNt + g) * W::kXPitch + member * W::kGroups * 64 + c * 16;
+      const uint8_t* w = sW + stage * W::kStage + g * W::kPitch + member * W::kGroups * (W::k4 ? 16 : 64) +
+                         c * (W::k4 ? 4 : 16);
       ok = mbar_wait(&x_full[xs], x_phase, abort) && ok;
-      if constexpr (kHold) {
-#pragma unroll
-        for (int i = 0; i < W::kGroups; ++i)
-          if (i < groups) held[i] = *reinterpret_cast<const uint4*>(x_src + i * 64);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_empty[xs]);
-      }
-      slot += W::kHalves;
-      if (slot == kXSlots) {
-        slot = 0;
-        x_phase ^= 1u;
-      }
-#pragma unroll
-      for (int s = 0; s < kSubs; ++s) {
-        if (s >= subs) break;
-        ok = mbar_wait(&w_full[stage], phase, abort) && ok;
-        const uint8_t* w = sW + stage * W::kStage + g * W::kPitch + warp * W::kGroups * (W::k4 ? 16 : 64) +
-                           c * (W::k4 ? 4 : 16);
+      ok = mbar_wait(&w_full[stage], phase, abort) && ok;
+      // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
+      uint32_t scale[4][2] = {};
+      if constexpr (W::k4) {
+        static_assert(W::kGroups == 4, "scales");
         const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
-                            warp * (kW == kW4nv ? 8 : 4);
-        // Rows g, g + 8, g + 16, g + 24. nv: f16 pairs, scales of two groups; mx: bytes of four groups.
-        uint32_t scale[4][2] = {};
-        if constexpr (W::k4) {
+                            member * (kW == kW4nv ? 8 : 4);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (kW == kW4nv) {
-              const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
-              // this lane's block of each group
-              const uint32_t four = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
-              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                  : "=r"(scale[r][0]), "=r"(scale[r][1])
-                  : "r"(four));
-            } else {
-              scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
-            }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (kW == kW4nv) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
+            // this lane's block of each group
+            const uint32_t four = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
+            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                : "=r"(scale[r][0]), "=r"(scale[r][1])
+                : "r"(four));
+          } else {
+            scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
           }
         }
+      }
+      auto group = [&](int k) {
+        uint4 b[kNt];
 #pragma unroll
-        for (int i = 0; i < W::kGroups; ++i) {
-          if (i >= groups) break;
-          uint4 b[kNt];
+        for (int n = 0; n < kNt; ++n) b[n] = *reinterpret_cast<const uint4*>(x + n * 8 * W::kXPitch + k * 64);
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            if constexpr (kHold) b[n] = held[i];
-            else b[n] = *reinterpret_cast<const uint4*>(x_src + n * 8 * kXPitch + i * 64);
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1 && !second) break;
+          uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
+            if constexpr (W::k4) {
+              fp4_halves8(*reinterpret_cast<const uint32_t*>(src + k * 16), p[r]);
+              if constexpr (kW == kW4nv) {
+                const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][k >> 1]);
+                const __half2 one = k & 1 ? __high2half2(both) : __low2half2(both);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
+                  p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+              }
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(src + k * 64);
+              p[r][0] = u.x;
+              p[r][1] = u.y;
+              p[r][2] = u.z;
+              p[r][3] = u.w;
+            }
           }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
+          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+          if constexpr (kW == kW4mx) {
+            float f[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
-              if constexpr (W::k4) {
-                fp4_halves8(*reinterpret_cast<const uint32_t*>(src + i * 16), p[r]);
-                if constexpr (kW == kW4nv) {
-                  const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][i >> 1]);
-                  const __half2 one = i & 1 ? __high2half2(both) : __low2half2(both);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
-                    p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
-                  }
-                }
-              } else {
-                const uint4 u = *reinterpret_cast<const uint4*>(src + i * 64);
-                p[r][0] = u.x;
-                p[r][1] = u.y;
-                p[r][2] = u.z;
-                p[r][3] = u.w;
-              }
+              const uint32_t byte = scale[2 * m + r][0] >> (8 * k) & 0xffu;
+              f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
             }
-            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-            if constexpr (kW == kW4mx) {
-              float f[2];
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t byte = scale[2 * m + r][0] >> (8 * i) & 0xffu;
-                f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
-              }
+            for (int n = 0; n < kNt; ++n) {
+              if (kNt > 1 && !(tokens >> (8 * n) & 0xffu)) continue;
+              const float zero[4] = {};
+              float d[4], d2[4];
+              mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
+              mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
 #pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                const float zero[4] = {};
-                float d[4], d2[4];
-                mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
-                mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
-                acc[s][m][n][0] = fmaf(d2[0], f[0], acc[s][m][n][0]);
-                acc[s][m][n][1] = fmaf(d2[1], f[0], acc[s][m][n][1]);
-                acc[s][m][n][2] = fmaf(d2[2], f[1], acc[s][m][n][2]);
-                acc[s][m][n][3] = fmaf(d2[3], f[1], acc[s][m][n][3]);
-              }
-            } else {
+              for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d2[j], f[j >> 1], acc[m][n][j]);
+            }
+          } else {
 #pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                mma_16bit<kBf16>(acc[s][m][n], a0, b[n].x, b[n].y, acc[s][m][n]);
-                mma_16bit<kBf16>(acc[s][m][n], a1, b[n].z, b[n].w, acc[s][m][n]);
-              }
+            for (int n = 0; n < kNt; ++n) {
+              if (kNt > 1 && !(tokens >> (8 * n) & 0xffu)) continue;
+              mma_16bit<kBf16>(acc[m][n], a0, b[n].x, b[n].y, acc[m][n]);
+              mma_16bit<kBf16>(acc[m][n], a1, b[n].z, b[n].w, acc[m][n]);
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&w_empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      };
+      if (groups == W::kGroups) {
+#pragma unroll
+        for (int k = 0; k < W::kGroups; ++k) group(k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < W::kGroups - 1; ++k)
+          if (k < groups) group(k);
       }
-      if (!kHold && lane == 0) mbar_arrive(&x_empty[xs]);   // (after the last stage's __syncwarp)
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&w_empty[stage]);
+        mbar_arrive_many(&x_empty[xs], kTeams / subs);
+      }
     };
-    // The warps' sums of one sub-tile meet in shared memory.
-    auto gather = [&](const float (&v)[2][kNt][4]) {
-      float* mine = sRed + red * (few_red_bytes<kNt>() / 4);
+    // The warps' sums of a part meet in shared memory; then the part's stages are behind everybody.
+    auto gather = [&](const float (&v)[2][kNt][4], int stages, int n_chunks) {
+      named_barrier_sync(1, 32 * kMmaWarps);      // what was there has been read
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
-          *reinterpret_cast<float4*>(mine + ((warp * 2 + m) * kNt + n) * 128 + lane * 4) =
+          *reinterpret_cast<float4*>(sRed + ((warp * 2 + m) * kNt + n) * 128 + lane * 4) =
               make_float4(v[m][n][0], v[m][n][1], v[m][n][2], v[m][n][3]);
       named_barrier_sync(1, 32 * kMmaWarps);
-      red ^= 1;      // (the other one has been read: all warps have passed this barrier)
-      return mine;
+      chunks += n_chunks;
+      const int place = first + stages, lap = place / kStages;
+      first = place - lap * kStages;
+      first_phase ^= lap & 1;
     };
-    auto sum_at = [&](const float* mine, int m, int n, int at) {
+    // Sub `s`, value (m, n, at) over the teams that had it.
+    auto sum_at = [&](int subs, int s, int m, int n, int at) {
       float v = 0.0f;
+      for (int t = s; t < kTeams; t += subs)
 #pragma unroll
-      for (int w = 0; w < kMmaWarps; ++w) v += mine[((w * 2 + m) * kNt + n) * 128 + at];
+        for (int w = 0; w < kTeamWarps; ++w) v += sRed[(((t * kTeamWarps + w) * 2 + m) * kNt + n) * 128 + at];
       return v;
+    };
+    auto clear = [](float (&v)[2][kNt][4]) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[m][n][j] = 0.0f;
     };
 
     bool waited = false;
@@ -823,10 +967,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         for (int q = q0; q < end;) {
           const FewPart p = part1(q, end);
           q += p.n;
-          const int subs = (p.n + 15) / 16;
-          float acc[kFewSub][2][kNt][4];
+          const int n_chunks = (H + W::kChunk - 1) / W::kChunk;
+          const uint32_t tokens = sh.tokens[p.a];
+          float acc[2][kNt][4];
           clear(acc);
-          for (int k0 = 0; k0 < H; k0 += W::kChunk) chunk(acc, min(W::kChunk, H - k0), subs);
+          for (int i2 = team; i2 < n_chunks * p.subs; i2 += kTeams) {
+            const int ck = i2 / p.subs;
+            multiply(acc, i2, chunks + ck, min(W::kChunk, H - ck * W::kChunk), p.subs, tokens, true);
+          }
+          gather(acc, n_chunks * p.subs, n_chunks);
           const bool own = p.a < n_exp;
           float g13 = 1.0f, g2 = 1.0f;
           if (kW == kW4nv) {
@@ -836,25 +985,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             if (p13) g13 = __ldg(p13 + e);
             if (p2) g2 = __ldg(p2 + e);
           }
-#pragma unroll
-          for (int s = 0; s < kFewSub; ++s) {
-            if (s >= subs) break;
-            const float* mine = gather(acc[s]);
-            if (tid < 128 * kNt) {
-              const int n = tid >> 7, at = tid & 127, l = at >> 2, j = at & 3;
-              const int row = s * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
-              const int sl = t < T ? sh.slot[p.a][t] : -1;
-              if (sl >= 0 && row < p.n) {
-                const float f = sh.x_inv[t] * g13;
-                const float gate = sum_at(mine, 0, n, at) * f, up = sum_at(mine, 1, n, at) * f;
-                const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
-                const float ex = expf(-fabsf(gate));
-                const float sig = (gate < 0.0f ? ex : 1.0f) / (1.0f + ex);
-                const float h = gate * sig * up * (wt * g2);
-                a.h[(static_cast<int64_t>(t) * (a.k + 1) + sl) * a.h_ld + p.at + row] = h;
-                if (!kBf16) atomicMax(&sh.tmax[t], __float_as_uint(h) & 0x7fffffffu);
-              }
-            }
+          for (int pos = tid; pos < p.subs * kNt * 128; pos += 32 * kMmaWarps) {
+            const int s = pos / (kNt * 128), n = pos / 128 % kNt, at = pos & 127, l = at >> 2, j = at & 3;
+            const int row = (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
+            const int sl = t < T ? sh.slot[p.a][t] : -1;
+            if (sl < 0 || row >= p.of(s)) continue;
+            const float f = sh.x_inv[t] * g13;
+            const float gate = sum_at(p.subs, s, 0, n, at) * f, up = sum_at(p.subs, s, 1, n, at) * f;
+            const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
+            const float ex = expf(-fabsf(gate));
+            const float sig = (gate < 0.0f ? ex : 1.0f) / (1.0f + ex);
+            const float h = gate * sig * up * (wt * g2);
+            a.h[(static_cast<int64_t>(t) * (a.k + 1) + sl) * a.h_ld + p.at + s * p.per + row] = h;
+            if (!kBf16) atomicMax(&sh.tmax[t], __float_as_uint(h) & 0x7fffffffu);
           }
         }
         // This slice's h, and the largest so far, before the count.
@@ -869,49 +1012,48 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end;) {
           const FewPart p = part2(r, end);
           r += p.n;
-          const int subs = (p.n + kFewRows - 1) / kFewRows;
-          float acc[kSub2][2][kNt][4], all[kSub2][2][kNt][4];
+          const int sub = team % p.subs;
+          const bool second = p.of(sub) > 16;
+          float acc[2][kNt][4], all[2][kNt][4];
           clear(all);
+          int ck = 0;
           for (int e = 0; e < n_all; ++e) {
             const int K = inner(e);
+            const uint32_t tokens = sh.tokens[e];
             clear(acc);
-            for (int k0 = 0; k0 < K; k0 += W::kChunk) chunk(acc, min(W::kChunk, K - k0), subs);
+            for (int k0 = 0; k0 < K; k0 += W::kChunk, ++ck) {
+              // (stage ck * subs + sub is this team's in every 4 / subs-th chunk)
+              if ((ck * p.subs + sub) % kTeams == team)
+                multiply(acc, ck * p.subs + sub, chunks + ck, min(W::kChunk, K - k0), p.subs, tokens, second);
+            }
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                if (sh.slot[e][n * 8 + 2 * c + j] < 0) continue;
+                if (!(tokens >> (n * 8 + 2 * c + j) & 1u)) continue;
 #pragma unroll
-                for (int s = 0; s < kSub2; ++s)
-#pragma unroll
-                  for (int m = 0; m < 2; ++m) {
-                    all[s][m][n][j] += acc[s][m][n][j];
-                    all[s][m][n][j + 2] += acc[s][m][n][j + 2];
-                  }
+                for (int m = 0; m < 2; ++m) {
+                  all[m][n][j] += acc[m][n][j];
+                  all[m][n][j + 2] += acc[m][n][j + 2];
+                }
               }
           }
+          gather(all, ck * p.subs, ck);
           if (!waited) {
             // (h came through the tokens' warps, which waited for all of it)
             waited = true;
             if (!kBf16 && lane < T) y_inv = inverse_power(to_f16_range(__uint_as_float(__ldcg(a.tmax + lane))));
           }
-#pragma unroll
-          for (int s = 0; s < kSub2; ++s) {
-            if (s >= subs) break;
-            const float* mine = gather(all[s]);
-#pragma unroll
-            for (int i2 = 0; i2 < kNt; ++i2) {
-              const int pos = tid + 256 * i2;
-              const int m = pos / (128 * kNt), n = pos / 128 % kNt, at = pos & 127, l = at >> 2, j = at & 3;
-              const int row = s * kFewRows + m * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
-              const float inv = __shfl_sync(0xffffffffu, y_inv, t);
-              if (t < T && row < p.n) {
-                const float v = sum_at(mine, m, n, at) * inv;
-                const int64_t to = static_cast<int64_t>(t) * H + p.at + row;
-                if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
-                else static_cast<__half*>(a.y)[to] = __float2half_rn(v);
-              }
-            }
+          for (int pos = tid; pos < p.subs * 2 * kNt * 128; pos += 32 * kMmaWarps) {
+            const int s = pos / (2 * kNt * 128), m = pos / (kNt * 128) % 2, n = pos / 128 % kNt;
+            const int at = pos & 127, l = at >> 2, j = at & 3;
+            const int row = m * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
+            const float inv = __shfl_sync(0xffffffffu, y_inv, t);   // (a warp's positions come and go together)
+            if (t >= T || row >= p.of(s)) continue;
+            const float v = sum_at(p.subs, s, m, n, at) * inv;
+            const int64_t to = static_cast<int64_t>(t) * H + p.at + s * p.per + row;
+            if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
+            else static_cast<__half*>(a.y)[to] = __float2half_rn(v);
           }
         }
       }
@@ -944,26 +1086,24 @@ moe_status launch_layer(const FewArgs& a, cudaStream_t s) {
   return MOE_OK;
 }
 
-template <typename T, int kT>
+template <typename T, int kT, int kPer>
 cudaError_t launch_gate_t(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
-  const int rows = a.E + a.shared_gate;
-  const bool two = rows > device_sm_count();   // one wave of blocks
-  const int blocks = two ? (rows + 1) / 2 : rows;
-  const dim3 grid(static_cast<unsigned>(blocks + (want_amax ? a.T : 0)));
-  const T* x = static_cast<const T*>(a.x);
-  const T* w = static_cast<const T*>(wg);
-  return two ? launch_pdl(few_gate_kernel<T, kT, 2>, grid, dim3(kGateThreads), 0, s, x, w, a.T, a.H, a.E,
-                          rows, blocks, a.logits, a.shared_logits, a.ticket, a.tmax, a.amax)
-             : launch_pdl(few_gate_kernel<T, kT, 1>, grid, dim3(kGateThreads), 0, s, x, w, a.T, a.H, a.E,
-                          rows, blocks, a.logits, a.shared_logits, a.ticket, a.tmax, a.amax);
+  const int rows = a.E + a.shared_gate, blocks = (rows + kPer - 1) / kPer;
+  return launch_pdl(few_gate_kernel<T, kT, kPer>,
+                    dim3(static_cast<unsigned>(blocks + (want_amax ? a.T : 0)), (a.T + kT - 1) / kT),
+                    dim3(kGateThreads), 0, s, static_cast<const T*>(a.x), static_cast<const T*>(wg), a.T, a.H,
+                    a.E, rows, blocks, a.logits, a.shared_logits, a.ticket, a.tmax, a.amax);
 }
 
+// Blocks for about one wave, each of few rows and tokens: x and wg come from L2 again for every block, and a
+// block that has all 16 tokens waits for them one after the other (16 tokens, 256 x 7168: 14 us with two
+// rows by all tokens, N with four by four).
 template <typename T>
 cudaError_t launch_gate_tokens(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
-  if (a.T <= 1) return launch_gate_t<T, 1>(a, wg, want_amax, s);
-  if (a.T <= 4) return launch_gate_t<T, 4>(a, wg, want_amax, s);
-  if (a.T <= 8) return launch_gate_t<T, 8>(a, wg, want_amax, s);
-  return launch_gate_t<T, 16>(a, wg, want_amax, s);
+  const bool many = a.E + a.shared_gate > device_sm_count();
+  if (a.T == 1) return many ? launch_gate_t<T, 1, 2>(a, wg, want_amax, s) : launch_gate_t<T, 1, 1>(a, wg, want_amax, s);
+  if (a.T <= 4) return many ? launch_gate_t<T, 4, 2>(a, wg, want_amax, s) : launch_gate_t<T, 4, 1>(a, wg, want_amax, s);
+  return launch_gate_t<T, 4, 4>(a, wg, want_amax, s);
 }
 
 size_t to_256(size_t n) { return (n + 255) / 256 * 256; }
