@@ -22,9 +22,10 @@
 // columns for every expert, which keeps lists of tokens out of the loops: in the first products the others'
 // results are dropped, in the second an expert's sums are added to those of its tokens only (a weight
 // that is not finite reaches nobody else); the routing weight is multiplied into h.
-// Four teams of four consumer warps: a team takes every fourth stage, its warps a quarter of the
-// stage's channels each, and they add up at the end of a part. (One team of eight or sixteen warps for
-// every stage: a warp then had 60 instructions of overhead to 30 of work, and the teams of 16 spilled.)
+// Four teams of two consumer warps: a team takes every fourth stage, its warps half of the stage's
+// channels each, and they add up at the end of a part. (One team of eight or sixteen warps for every
+// stage: a warp has more instructions beside its work than for it. More warps, fewer registers: what is
+// spilled does not fit what the ring leaves of L1, and each access is one to L2.)
 //
 // Numbers. 16-bit weights: operands of x's type, h rounded to it once (with the routing weight; f16 after
 // a power of two for each token, see below). 4-bit weights: codes to f16 exactly; nv scales
@@ -34,6 +35,7 @@
 // than 2^-29 of the token's largest, h is rounded to 11 bits. Sums, SwiGLU and the sum over experts: fp32.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,13 +53,13 @@ namespace {
 constexpr int kFewTokens = MOE_FEW_TOKENS;
 static_assert(kFewTokens == 16, "two column tiles");
 constexpr int kFewExperts = 128 + 1;             // T * k at most, and the shared one
-constexpr int kMmaWarps = 16;                    // consumers
-constexpr int kXWarps = 4;                       // producers of the tokens' side
-constexpr int kWWarps = 2;                       // producers of the weights' side, a stage each in turn
+constexpr int kMmaWarps = 8;                     // consumers
+constexpr int kXWarps = 4;                       // producers of the tokens' side, a chunk each in turn
+constexpr int kWWarps = 4;                       // producers of the weights' side, a stage each in turn
 constexpr int kWarpW = kMmaWarps, kWarpX = kWarpW + kWWarps;
 constexpr int kFewThreads = 32 * (kWarpX + kXWarps);
 constexpr int kTeams = 4, kTeamWarps = kMmaWarps / kTeams;   // of consumers
-constexpr int kXSlots = kXWarps;                 // chunks of the tokens' side
+constexpr int kXSlots = 4;                       // chunks of the tokens' side
 static_assert(kXSlots == kTeams, "a slot belongs to the same teams throughout a part");
 constexpr int kFewRows = 32;                     // rows of weights a stage
 constexpr int kFewMaxBlocks = 192;
@@ -254,6 +256,27 @@ __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) 
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
+// mbar_wait (ptx.cuh) that leaves the polling to the hardware for up to 20 us at a time: twenty warps that
+// poll by themselves keep the shared-memory pipe from the few that work.
+__device__ __forceinline__ bool few_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  auto poll = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (poll()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!poll())
+    if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+
 // 2^(14 - e) for a largest value of [2^e, 2^(e + 1)), 1 for none or one that is not finite; bounded so
 // that the inverse is a normal number too.
 __device__ __forceinline__ float to_f16_range(float amax) {
@@ -406,17 +429,17 @@ constexpr int kFewRouteBytes = 36 * 1024;        // scratch
 __device__ __noinline__ void few_route(const FewArgs& a, FewShared* sh, uint8_t* scratch) {
   const int tid = threadIdx.x, warp = tid >> 5;
   constexpr int kWarps = kFewThreads / 32;
-  static_assert(kWarps >= kFewTokens && kWarps * (1024 + 512) <= kFewRouteBytes,
-                "a warp a token, and its scratch");
+  static_assert(kWarps * (1024 + 512) <= kFewRouteBytes, "scratch");
   float* s_key = reinterpret_cast<float*>(scratch) + warp * 256;
   uint8_t* s_exact = scratch + kWarps * 1024 + warp * 512;
   for (int i = tid; i < kFewExperts * kFewTokens; i += kFewThreads) (&sh->slot[0][0])[i] = -1;
   if (tid < 8) sh->mask[tid] = 0;
   if (tid < kFewTokens) sh->tmax[tid] = 0;
-  if (warp < a.T) {
-    const float* row = a.logits + warp * a.E;
-    if (a.E <= 128) few_select<4>(row, a, warp, s_key, s_exact, s_exact + 256, sh);
-    else few_select<8>(row, a, warp, s_key, s_exact, s_exact + 256, sh);
+  for (int t = warp; t < a.T; t += kWarps) {
+    const float* row = a.logits + t * a.E;
+    if (a.E <= 128) few_select<4>(row, a, t, s_key, s_exact, s_exact + 256, sh);
+    else few_select<8>(row, a, t, s_key, s_exact, s_exact + 256, sh);
+    __syncwarp();
   }
   __syncthreads();
   if (!few_weights(a, sh)) {
@@ -608,7 +631,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     auto begin = [&] {
       const bool is = turn == mine;
       turn = turn + 1 == kWWarps ? 0 : turn + 1;
-      if (is) ok = __all_sync(0xffffffffu, mbar_wait(&w_empty[stage], phase ^ 1u, abort));
+      if (is) ok = __all_sync(0xffffffffu, few_wait(&w_empty[stage], phase ^ 1u, abort));
       return is && ok;
     };
     auto end_stage = [&](bool is) {
@@ -675,29 +698,35 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     async_wait_all();   // (nothing is under way into the memory of a block that has ended)
   } else if (warp >= kWarpX) {
     // ------------------------------------------------------------ tokens
-    // Chunk after chunk goes round the four warps and slots. Only the rows of an expert's tokens are
+    // Chunk after chunk goes round the warps, and round the slots. Only the rows of an expert's tokens are
     // written: what the others' hold reaches columns that nobody looks at.
     const int mine = warp - kWarpX;
-    int slot = 0;
+    int next = 0, slot = 0;                 // the warp of the next chunk; its slot and the slot's use
     uint32_t phase = 0;
+    uint8_t* dst = sX;
     bool ok = true, waited = false;
     float t_mul = 1.0f;                     // lane t: token t's power of two for h
     constexpr int kVecs = W::kChunk / 8, kPer = kVecs / 32;   // of a row of a slot, a lane's
-    auto turn = [&] {                       // is it this warp's slot?
-      const bool is = slot == mine;
-      if (++slot == kXSlots) slot = 0;
-      return is;
+    // Is the next chunk this warp's? Then once its slot is free, and `publish` passes it on.
+    auto begin = [&] {
+      const bool is = next == mine;
+      if (is) {
+        ok = __all_sync(0xffffffffu, few_wait(&x_empty[slot], phase ^ 1u, abort));
+        dst = sX + slot * 8 * kNt * W::kXPitch;
+      }
+      return is && ok;
     };
-    auto wait_empty = [&] {
-      ok = __all_sync(0xffffffffu, mbar_wait(&x_empty[mine], phase ^ 1u, abort));
-      phase ^= 1u;
-      return ok;
+    auto publish = [&](bool is) {
+      if (is) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_full[slot]);
+      }
+      next = next + 1 == kXWarps ? 0 : next + 1;
+      if (++slot == kXSlots) {
+        slot = 0;
+        phase ^= 1u;
+      }
     };
-    auto publish = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&x_full[mine]);
-    };
-    uint8_t* dst = sX + mine * 8 * kNt * W::kXPitch;
     for (int i = 0; ok; ++i) {
       const int ticket = __shfl_sync(0xffffffffu, ticket_at(i, ok), 0);
       ok = __all_sync(0xffffffffu, ok);
@@ -708,12 +737,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           q += p.n;
           const uint32_t tokens = sh.tokens[p.a];
           for (int k0 = 0; k0 < H && ok; k0 += W::kChunk) {
-            if (!turn()) continue;
-            if (!wait_empty()) break;
+            const bool is = begin();
             const int nv = min(W::kChunk, H - k0) / 8;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + k0);
             // Four tokens' loads at once.
-            for (uint32_t rest = tokens; rest;) {
+            for (uint32_t rest = is ? tokens : 0u; rest;) {
               int t[4];
               uint4 u[4][kPer];
 #pragma unroll
@@ -745,7 +773,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                 }
               }
             }
-            publish();
+            publish(is);
           }
         }
       } else {
@@ -761,10 +789,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           for (int e = 0; e < n_all && ok; ++e) {
             const int K = inner(e);
             for (int k0 = 0; k0 < K && ok; k0 += W::kChunk) {
-              if (!turn()) continue;
-              if (!wait_empty()) break;
+              const bool is = begin();
               const int nv = min(W::kChunk, K - k0) / 8;
-              for (uint32_t rest = sh.tokens[e]; rest;) {
+              for (uint32_t rest = is ? sh.tokens[e] : 0u; rest;) {
                 int t[2];
                 float4 u[2][kPer][2];
 #pragma unroll
@@ -798,7 +825,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                   }
                 }
               }
-              publish();
+              publish(is);
             }
           }
         }
@@ -817,8 +844,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     uint32_t first_phase = 0;
 
     // Stage i of the part, by its team: sub-tile products of chunk `xc` (of all so far), `len` channels.
-    // `second`: there are rows past the first 16.
-    auto multiply = [&](float (&acc)[2][kNt][4], int i, int xc, int len, int subs, uint32_t tokens, bool second) {
+    // `second`: there are rows past the first 16. All columns are multiplied, whoever's token is in them.
+    // (No branch inside a group: the compiler moves loads and conversions over products only within one.)
+    auto multiply = [&](auto second, float (&acc)[2][kNt][4], int i, int xc, int len, int subs) {
+      constexpr int kM = decltype(second)::value ? 2 : 1;
       const int place = first + i, lap = place / kStages;
       const int stage = place - lap * kStages, xs = xc % kXSlots;
       const uint32_t phase = first_phase ^ (lap & 1), x_phase = xc / kXSlots & 1;
@@ -826,96 +855,99 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       const uint8_t* x = sX + (xs * 8 * kNt + g) * W::kXPitch + member * W::kGroups * 64 + c * 16;
       const uint8_t* w = sW + stage * W::kStage + g * W::kPitch + member * W::kGroups * (W::k4 ? 16 : 64) +
                          c * (W::k4 ? 4 : 16);
-      ok = mbar_wait(&x_full[xs], x_phase, abort) && ok;
-      ok = mbar_wait(&w_full[stage], phase, abort) && ok;
-      // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
-      uint32_t scale[4][2] = {};
-      if constexpr (W::k4) {
-        static_assert(W::kGroups == 4, "scales");
-        const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
-                            member * (kW == kW4nv ? 8 : 4);
+      ok = few_wait(&x_full[xs], x_phase, abort) && ok;
+      ok = few_wait(&w_full[stage], phase, abort) && ok;
+      // Four groups of 32 channels, from k0 on, of which `left` are before the contraction's end.
+      auto four = [&](int k0, int left) {
+        // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
+        uint32_t scale[2 * kM][2] = {};
+        if constexpr (W::k4) {
+          const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
+                              (member * W::kGroups + k0) * (kW == kW4nv ? 2 : 1);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (kW == kW4nv) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
-            // this lane's block of each group
-            const uint32_t four = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
-            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                : "=r"(scale[r][0]), "=r"(scale[r][1])
-                : "r"(four));
-          } else {
-            scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
-          }
-        }
-      }
-      auto group = [&](int k) {
-        uint4 b[kNt];
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) b[n] = *reinterpret_cast<const uint4*>(x + n * 8 * W::kXPitch + k * 64);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m == 1 && !second) break;
-          uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
-            if constexpr (W::k4) {
-              fp4_halves8(*reinterpret_cast<const uint32_t*>(src + k * 16), p[r]);
-              if constexpr (kW == kW4nv) {
-                const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][k >> 1]);
-                const __half2 one = k & 1 ? __high2half2(both) : __low2half2(both);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
-                  p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-              }
+          for (int r = 0; r < 2 * kM; ++r) {
+            if constexpr (kW == kW4nv) {
+              const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
+              // this lane's block of each group
+              const uint32_t of_lane = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
+              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                  : "=r"(scale[r][0]), "=r"(scale[r][1])
+                  : "r"(of_lane));
             } else {
-              const uint4 u = *reinterpret_cast<const uint4*>(src + k * 64);
-              p[r][0] = u.x;
-              p[r][1] = u.y;
-              p[r][2] = u.z;
-              p[r][3] = u.w;
+              scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
             }
           }
-          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-          if constexpr (kW == kW4mx) {
-            float f[2];
+        }
+        auto group = [&](int k) {
+          uint4 b[kNt];
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+            b[n] = *reinterpret_cast<const uint4*>(x + n * 8 * W::kXPitch + (k0 + k) * 64);
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const uint32_t byte = scale[2 * m + r][0] >> (8 * k) & 0xffu;
-              f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
+              const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
+              if constexpr (W::k4) {
+                fp4_halves8(*reinterpret_cast<const uint32_t*>(src + (k0 + k) * 16), p[r]);
+                if constexpr (kW == kW4nv) {
+                  const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][k >> 1]);
+                  const __half2 one = k & 1 ? __high2half2(both) : __low2half2(both);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
+                    p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                }
+              } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(src + (k0 + k) * 64);
+                p[r][0] = u.x;
+                p[r][1] = u.y;
+                p[r][2] = u.z;
+                p[r][3] = u.w;
+              }
             }
+            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+            if constexpr (kW == kW4mx) {
+              float f[2];
 #pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              if (kNt > 1 && !(tokens >> (8 * n) & 0xffu)) continue;
-              const float zero[4] = {};
-              float d[4], d2[4];
-              mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
-              mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t byte = scale[2 * m + r][0] >> (8 * k) & 0xffu;
+                f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
+              }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d2[j], f[j >> 1], acc[m][n][j]);
-            }
-          } else {
+              for (int n = 0; n < kNt; ++n) {
+                const float zero[4] = {};
+                float d[4], d2[4];
+                mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
+                mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
 #pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              if (kNt > 1 && !(tokens >> (8 * n) & 0xffu)) continue;
-              mma_16bit<kBf16>(acc[m][n], a0, b[n].x, b[n].y, acc[m][n]);
-              mma_16bit<kBf16>(acc[m][n], a1, b[n].z, b[n].w, acc[m][n]);
+                for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d2[j], f[j >> 1], acc[m][n][j]);
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNt; ++n) {
+                mma_16bit<kBf16>(acc[m][n], a0, b[n].x, b[n].y, acc[m][n]);
+                mma_16bit<kBf16>(acc[m][n], a1, b[n].z, b[n].w, acc[m][n]);
+              }
             }
           }
+        };
+        if (left >= 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) group(k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (k < left) group(k);
         }
       };
-      if (groups == W::kGroups) {
 #pragma unroll
-        for (int k = 0; k < W::kGroups; ++k) group(k);
-      } else {
-#pragma unroll
-        for (int k = 0; k < W::kGroups - 1; ++k)
-          if (k < groups) group(k);
-      }
+      for (int k0 = 0; k0 < W::kGroups; k0 += 4)
+        if (k0 < groups) four(k0, groups - k0);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&w_empty[stage]);
@@ -968,12 +1000,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           const FewPart p = part1(q, end);
           q += p.n;
           const int n_chunks = (H + W::kChunk - 1) / W::kChunk;
-          const uint32_t tokens = sh.tokens[p.a];
           float acc[2][kNt][4];
           clear(acc);
           for (int i2 = team; i2 < n_chunks * p.subs; i2 += kTeams) {
             const int ck = i2 / p.subs;
-            multiply(acc, i2, chunks + ck, min(W::kChunk, H - ck * W::kChunk), p.subs, tokens, true);
+            multiply(std::true_type{}, acc, i2, chunks + ck, min(W::kChunk, H - ck * W::kChunk), p.subs);
           }
           gather(acc, n_chunks * p.subs, n_chunks);
           const bool own = p.a < n_exp;
@@ -1023,8 +1054,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             clear(acc);
             for (int k0 = 0; k0 < K; k0 += W::kChunk, ++ck) {
               // (stage ck * subs + sub is this team's in every 4 / subs-th chunk)
-              if ((ck * p.subs + sub) % kTeams == team)
-                multiply(acc, ck * p.subs + sub, chunks + ck, min(W::kChunk, K - k0), p.subs, tokens, second);
+              if ((ck * p.subs + sub) % kTeams != team) continue;
+              const int len = min(W::kChunk, K - k0);
+              if (second) multiply(std::true_type{}, acc, ck * p.subs + sub, chunks + ck, len, p.subs);
+              else multiply(std::false_type{}, acc, ck * p.subs + sub, chunks + ck, len, p.subs);
             }
 #pragma unroll
             for (int n = 0; n < kNt; ++n)
