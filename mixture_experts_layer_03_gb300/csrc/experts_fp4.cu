@@ -10,11 +10,13 @@
 //
 // Scales. The instruction wants those of 128 rows by 4 bytes of the contraction as 32 lanes by 4 columns
 // (row 32 i + l in lane l, column i), which tcgen05.cp writes from 512 bytes of shared memory, row l of
-// 16 bytes holding rows l, l + 32, l + 64, l + 96. A row's scales lie along the contraction in memory, so
-// four warps read 16 (mx: 8) bytes a row and block, turn 4 x 4 words over between four lanes by
-// shuffles, and write 16 bytes a lane. Each CTA needs the scales of its 128 channels and of all of the
-// tile's rows (the pair shares the rows' codes, but each tensor core scales its own half of D). Bytes
-// past the row's K / block are zeros, whatever fills the row up; codes past K are TMA's zeros.
+// 16 bytes holding rows l, l + 32, l + 64, l + 96. A row's scales lie along the contraction in memory: they
+// come by TMA as they lie, 16 bytes a row (mx: for two blocks), and four warps turn 4 x 4 words over
+// between four lanes by shuffles and write 16 bytes a lane. (Read from memory by those warps, they came
+// one latency after the other: the fence that shows them to the tensor cores waits for the loads under
+// way. N us for N.) Each CTA needs the scales of its 128 channels and of all of the tile's rows (the pair
+// shares the rows' codes, but each tensor core scales its own half of D). Bytes past the row's K / block
+// are zeros, whatever fills the row up; codes past K are TMA's zeros.
 // TMEM: two accumulators of 224 columns, 48 columns of scales (nv: 4 x 4 for A, 4 x 8 for B), written
 // anew for every block: copies and products are issued by one thread and run in that order.
 //
@@ -37,11 +39,12 @@ namespace {
 
 constexpr int kQBK = 256;                      // contraction elements a block: 128 bytes
 constexpr int kQMost = 224;                    // rows of a tile
-constexpr int kQStages = 5;
+constexpr int kQStages = 4;
 constexpr int kQSlotBytes = 128 * 128;         // codes of one operand of one block in one CTA
 constexpr int kQAtom = 512;                    // scales of 128 rows by 4 bytes
 constexpr int kQScaleBytes = 4 * kQAtom + 8 * kQAtom;   // of A, then of B (two atoms a word)
-constexpr int kQStageBytes = 2 * kQSlotBytes + kQScaleBytes;
+constexpr int kQRawBytes = 3 * 128 * 16;       // scales as they lie: A's 128 rows, B's 2 x 128
+constexpr int kQStageBytes = 2 * kQSlotBytes + kQScaleBytes + kQRawBytes;
 constexpr int kQScaleWarp = 2, kQScaleWarps = 4;
 constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps, kQEpiWarps = 8;
 constexpr int kQThreads = 32 * (kQEpiWarp + kQEpiWarps);
@@ -55,11 +58,8 @@ constexpr uint16_t kQPairMask = 0x3;
 
 struct Fp4Args {
   ExpertsArgs e;
-  const uint8_t* x_scales;   // [R, pitch]
-  const uint8_t* w_scales;   // [E, N, pitch]
   const float* x_g;          // or NULL
   const float* w_g;          // [E] or NULL
-  int pitch;
   int blocks;                // scale bytes of a row
 };
 
@@ -116,9 +116,10 @@ template <bool kNv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
 experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const __grid_constant__ CUtensorMap map_x32,
+                   const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
                    const __grid_constant__ CUtensorMap map_out, Fp4Args q) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full_bar[kQStages], scale_bar[kQStages], empty_bar[kQStages];
+  __shared__ uint64_t full_bar[kQStages], raw_bar[kQStages], scale_bar[kQStages], empty_bar[kQStages];
   __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
@@ -134,12 +135,14 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   uint8_t* sB = sA + kQStages * kQSlotBytes;
   uint8_t* sS = sB + kQStages * kQSlotBytes;
-  uint8_t* sOut = sS + kQStages * kQScaleBytes;
+  uint8_t* sRaw = sS + kQStages * kQScaleBytes;
+  uint8_t* sOut = sRaw + kQStages * kQRawBytes;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&full_bar[s], 1);                    // first CTA: its producer, and both CTAs' bytes
+      mbar_init(&raw_bar[s], 1);                     // this CTA's scales, as they lie
       mbar_init(&scale_bar[s], 2 * kQScaleWarps);    // first CTA: both CTAs' scale warps
       mbar_init(&empty_bar[s], 1);                   // the pair commit, delivered to both CTAs
     }
@@ -155,6 +158,8 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     tma_prefetch_map(&map_w);
     tma_prefetch_map(&map_x);
     tma_prefetch_map(&map_x32);
+    tma_prefetch_map(&map_ws);
+    tma_prefetch_map(&map_xs);
     tma_prefetch_map(&map_out);
   }
   if (warp == 1) {
@@ -206,6 +211,12 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           if (lead) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const uint32_t fb = lead_full + 8u * stage;
           uint8_t* bs = sB + stage * kQSlotBytes;
+          uint8_t* raw_s = sRaw + stage * kQRawBytes;
+          const int at = kNv ? kb * 16 : (kb >> 1) * 16;   // (mx: this block's half of it is kb's lowest bit)
+          mbar_arrive_expect_tx(&raw_bar[stage], (1 + (t.n > 128 ? 2 : 1)) * 128 * 16);
+          tma_load_3d(raw_s, &map_ws, &raw_bar[stage], at, t.m0, t.g);
+          tma_load_2d(raw_s + 128 * 16, &map_xs, &raw_bar[stage], at, t.n0);
+          if (t.n > 128) tma_load_2d(raw_s + 256 * 16, &map_xs, &raw_bar[stage], at, t.n0 + 128);
           if (t.m_here > 0)
             tma_load_3d_pair(sA + stage * kQSlotBytes, &map_w, fb, kb * 128, t.m0, t.g);
           tma_load_2d_pair(bs, mx, fb, kb * 128, n0);
@@ -293,57 +304,30 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     }
   } else if (warp < kQEpiWarp) {
     // ------------------------------------------------------------ scales (both CTAs)
-    // This warp's rows of each 128: l = 8 * w .. + 7 in lanes by rows l, l + 32, l + 64, l + 96; what is
-    // read lies kAhead blocks before what is written.
-    constexpr int kAhead = 4;
+    // This warp's rows of each 128: l = 8 * w .. + 7 in lanes by rows l, l + 32, l + 64, l + 96.
     constexpr int kWords = kNv ? 4 : 2;
     const int l = 8 * (warp - kQScaleWarp) + (lane & 7), i = lane >> 3;
     const int row = l + 32 * i;
-    int idx = first, kb = 0;       // the block to read next
-    Tile t = {};
-    auto settle = [&] {            // idx at a tile that multiplies something
-      while (idx < total) {
-        t = tile(idx);
-        if (t.nkb > 0) break;
-        idx += step;
-      }
-    };
-    settle();
-    uint4 ring[kAhead][3];
-    auto words = [&](const uint8_t* p, bool there, int at) {   // of a row's scales from byte `at` on
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (there) {
-        if (kNv) {
-          v = __ldg(reinterpret_cast<const uint4*>(p + at));
-        } else {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + at));
-          v.x = u.x;
-          v.y = u.y;
+    // A row's scales of block kb, those past the row's end as zeros.
+    auto words = [&](const uint8_t* raw_rows, int kb) {
+      uint4 v = *reinterpret_cast<const uint4*>(raw_rows + row * 16);
+      if (!kNv) {
+        if (kb & 1) {
+          v.x = v.z;
+          v.y = v.w;
         }
-        const int left = q.blocks - at;   // bytes that are scales
-        if (left < 4 * kWords) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        v.z = v.w = 0;
+      }
+      const int left = q.blocks - kb * 4 * kWords;   // bytes that are scales
+      if (left < 4 * kWords) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-          for (int j = 0; j < kWords; ++j) {
-            const int n = left - 4 * j;
-            if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
-          }
+        for (int j = 0; j < kWords; ++j) {
+          const int n = left - 4 * j;
+          if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
         }
       }
       return v;
-    };
-    auto read = [&](uint4 (&r)[3]) {
-      if (idx >= total) return;
-      const int at = kb * 4 * kWords;
-      r[0] = words(q.w_scales + (static_cast<int64_t>(t.g) * a.m_ext + t.m0 + row) * q.pitch, row < t.m_here, at);
-      const uint8_t* xs = q.x_scales + static_cast<int64_t>(t.n0 + row) * q.pitch;
-      r[1] = words(xs, row < t.n_here, at);
-      if (t.n > 128) r[2] = words(xs + static_cast<int64_t>(128) * q.pitch, row + 128 < t.n_here, at);
-      if (++kb == nkb) {
-        kb = 0;
-        idx += step;
-        settle();
-      }
     };
     // 4 x 4 words between lanes i = 0..3 of the same l: lane i gets word i of each.
     auto turn = [&](uint4 v) {
@@ -375,39 +359,35 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       }
       return make_uint4(w[0], w[1], w[2], w[3]);
     };
-    int left = 0;                  // blocks to write
-    {
-      const int g0 = group;
-      group = 0;
-      for (int id = first; id < total; id += step) left += tile(id).nkb > 0 ? nkb : 0;
-      group = g0;
-    }
     int stage = 0;
     uint32_t phase = 0;
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) read(ring[b]);
     bool ok = true;
-    while (left > 0 && ok) {
-#pragma unroll
-      for (int b = 0; b < kAhead; ++b) {
-        if (left == 0 || !ok) break;
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
+    for (int idx = first; idx < total && ok; idx += step) {
+      const Tile t = tile(idx);
+      if (t.nkb == 0) continue;
+      const bool wide = t.n > 128;
+      for (int kb = 0; kb < nkb; ++kb) {
+        // (the stage's own place has been given back before its scales were asked for)
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_bar[stage], phase, abort));
         if (!ok) break;
+        const uint8_t* raw_s = sRaw + stage * kQRawBytes;
         uint8_t* dst = sS + stage * kQScaleBytes + l * 16;
-        const uint4 va = turn(ring[b][0]), vb = turn(ring[b][1]), vc = turn(ring[b][2]);
+        const uint4 va = turn(words(raw_s, kb)), vb = turn(words(raw_s + 128 * 16, kb));
+        uint4 vc = {};
+        if (wide) vc = turn(words(raw_s + 256 * 16, kb));
         if (i < kWords) {
           *reinterpret_cast<uint4*>(dst + i * kQAtom) = va;
           *reinterpret_cast<uint4*>(dst + (4 + 2 * i) * kQAtom) = vb;
-          *reinterpret_cast<uint4*>(dst + (5 + 2 * i) * kQAtom) = vc;
+          if (wide) *reinterpret_cast<uint4*>(dst + (5 + 2 * i) * kQAtom) = vc;
         }
+        // What reads these is this SM's own tensor core, whichever CTA's thread issues the copy: the proxy
+        // fence orders the two here, and the arrival need not release to the other SM (1400 cycles).
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
           if (lead) mbar_arrive(&scale_bar[stage]);
-          else mbar_arrive_cluster(lead_scale + 8u * stage);
+          else mbar_arrive_remote(lead_scale + 8u * stage);
         }
-        read(ring[b]);
-        --left;
         if (++stage == kQStages) {
           stage = 0;
           phase ^= 1u;
@@ -521,23 +501,24 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   cluster_sync();
 }
 
-// Bytes [planes, rows, cols] (planes 0: a matrix), boxes of 128 by box_rows with the 128-byte swizzle.
-bool encode_codes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
-                  uint32_t box_rows) {
+// Bytes [planes, rows, cols] (planes 0: a matrix), boxes of 128 (with the 128-byte swizzle) or 16 by box_rows.
+bool encode_bytes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
+                  uint32_t box_cols, uint32_t box_rows) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {cols, rows, planes};
   cuuint64_t strides[2] = {cols, rows * cols};
-  cuuint32_t box[3] = {128, box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, planes ? 3 : 2, const_cast<void*>(base), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kNv>
 moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mx32,
-                      const CUtensorMap& mo, const Fp4Args& q, int64_t tiles, cudaStream_t s) {
+                      const CUtensorMap& mws, const CUtensorMap& mxs, const CUtensorMap& mo, const Fp4Args& q, int64_t tiles, cudaStream_t s) {
   static std::atomic<int> clusters_dev[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
@@ -563,7 +544,7 @@ moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   }
   const unsigned pairs = static_cast<unsigned>(have < tiles ? have : tiles);
   const cudaError_t err = launch_pdl(experts_fp4_kernel<kNv>, dim3(2 * pairs), dim3(kQThreads),
-                                     kQSmemBytes, s, mw, mx, mx32, mo, q);
+                                     kQSmemBytes, s, mw, mx, mx32, mws, mxs, mo, q);
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_fp4 launch: %s", cudaGetErrorString(err));
   return MOE_OK;
@@ -579,10 +560,13 @@ moe_status fp4_timeout_word(void** word) {
 
 moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const int32_t* offsets, int64_t R,
                               int E, int N, int K, int fmt, int dtype, void* y, cudaStream_t s) {
-  CUtensorMap mw, mx, mx32, mo;
+  CUtensorMap mw, mx, mx32, mws, mxs, mo;
+  const int pitch = fp4_scale_pitch(K, fmt);
   EncodeTiledFn enc = get_encode_fn();
-  bool ok = enc && encode_codes(&mw, w.codes, E, N, K / 2, 128) &&
-            encode_codes(&mx, x.codes, 0, R, K / 2, 128) && encode_codes(&mx32, x.codes, 0, R, K / 2, 32);
+  bool ok = enc && encode_bytes(&mw, w.codes, E, N, K / 2, 128, 128) &&
+            encode_bytes(&mx, x.codes, 0, R, K / 2, 128, 128) &&
+            encode_bytes(&mx32, x.codes, 0, R, K / 2, 128, 32) &&
+            encode_bytes(&mws, w.scales, E, N, pitch, 16, 128) && encode_bytes(&mxs, x.scales, 0, R, pitch, 16, 128);
   if (ok) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(R)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * 2};
@@ -600,15 +584,12 @@ moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const in
   q.e.k_ext = K;
   q.e.f16 = dtype == MOE_DTYPE_F16;
   q.e.out = y;
-  q.x_scales = x.scales;
-  q.w_scales = w.scales;
   q.x_g = x.g;
   q.w_g = w.g;
-  q.pitch = fp4_scale_pitch(K, fmt);
   q.blocks = K / fp4_block(fmt);
   const int64_t tiles = (R / kQMost + E + 2) * ((N + 255) / 256);
-  return fmt == kFp4Nv ? launch_fp4<true>(mw, mx, mx32, mo, q, tiles, s)
-                       : launch_fp4<false>(mw, mx, mx32, mo, q, tiles, s);
+  return fmt == kFp4Nv ? launch_fp4<true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s)
+                       : launch_fp4<false>(mw, mx, mx32, mws, mxs, mo, q, tiles, s);
 }
 
 }  // namespace moe
