@@ -20,8 +20,9 @@
 // TMEM: two accumulators of 224 columns, 48 columns of scales (nv: 4 x 4 for A, 4 x 8 for B), written
 // anew for every block: copies and products are issued by one thread and run in that order.
 //
-// Warp roles (448 threads per CTA): warp 0 TMA producer, warp 1 TMEM allocator and, in the first CTA, MMA
-// issuer, warps 2-5 scales, warps 6-13 epilogue, four to each accumulator.
+// Warp roles (608 threads per CTA): warps 0 and 18 TMA producers of the weights and of the rows, warp 1 TMEM
+// allocator and, in the first CTA, MMA issuer, warps 2-9 scales, in two teams that take a block each in
+// turn (a block takes a team 650 cycles of latency), warps 10-17 epilogue, four to each accumulator.
 #include <atomic>
 #include <cstdint>
 
@@ -45,15 +46,17 @@ constexpr int kQAtom = 512;                    // scales of 128 rows by 4 bytes
 constexpr int kQScaleBytes = 4 * kQAtom + 8 * kQAtom;   // of A, then of B (two atoms a word)
 constexpr int kQRawBytes = 3 * 128 * 16;       // scales as they lie: A's 128 rows, B's 2 x 128
 constexpr int kQStageBytes = 2 * kQSlotBytes + kQScaleBytes + kQRawBytes;
-constexpr int kQScaleWarp = 2, kQScaleWarps = 4;
-constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps, kQEpiWarps = 8;
-constexpr int kQThreads = 32 * (kQEpiWarp + kQEpiWarps);
+constexpr int kQScaleWarp = 2, kQScaleWarps = 4, kQScaleTeams = 2;   // a stage each in turn
+constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps * kQScaleTeams, kQEpiWarps = 8;
+constexpr int kQWarpX = kQEpiWarp + kQEpiWarps;   // the producer of the rows
+constexpr int kQThreads = 32 * (kQWarpX + 1);
 constexpr int kQBoxBytes = 4096;               // epilogue staging of a warp
 constexpr int kQSmemBytes = 1024 + kQStages * kQStageBytes + kQEpiWarps * kQBoxBytes;
 constexpr int kQTmemCols = 512;
 constexpr int kQAccCols = kQMost;
 constexpr int kQColsA = 2 * kQAccCols, kQColsB = kQColsA + 16;   // scales' TMEM columns
 static_assert(kQColsB + 32 <= kQTmemCols, "TMEM");
+static_assert(kQScaleTeams == 2 && kQStages % 2 == 0, "stages of the scale teams");
 constexpr uint16_t kQPairMask = 0x3;
 
 struct Fp4Args {
@@ -141,8 +144,8 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQStages; ++s) {
-      mbar_init(&full_bar[s], 1);                    // first CTA: its producer, and both CTAs' bytes
-      mbar_init(&raw_bar[s], 1);                     // this CTA's scales, as they lie
+      mbar_init(&full_bar[s], 2);                    // first CTA: its two producers, and both CTAs' bytes
+      mbar_init(&raw_bar[s], 2);                     // this CTA's scales, as they lie
       mbar_init(&scale_bar[s], 2 * kQScaleWarps);    // first CTA: both CTAs' scale warps
       mbar_init(&empty_bar[s], 1);                   // the pair commit, delivered to both CTAs
     }
@@ -189,8 +192,10 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   auto tile = [&](int idx) {
     return decode_tile<kFwd, false, kQMost>(idx, s_blk, s_start, G, a, walk, rank, lane, group);
   };
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == 0 || warp == kQWarpX) {
+    // ------------------------------------------------------------ TMA producers of the weights and of the rows
+    // (One warp for both took 410 cycles a block, as much as the products of 208 rows.)
+    const bool weights = warp == 0;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -202,7 +207,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const int box = narrow ? 32 : 128;
       const bool two = half > box;
       const CUtensorMap* mx = narrow ? &map_x32 : &map_x;
-      const uint32_t tx = kQSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) + 2 * (two ? 2 : 1) * box * 128;
+      const uint32_t tx = weights ? kQSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) : 2 * (two ? 2 : 1) * box * 128;
       const int n0 = t.n0 + rank * half;
       for (int kb = 0; kb < nkb; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
@@ -213,14 +218,18 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           uint8_t* bs = sB + stage * kQSlotBytes;
           uint8_t* raw_s = sRaw + stage * kQRawBytes;
           const int at = kNv ? kb * 16 : (kb >> 1) * 16;   // (mx: this block's half of it is kb's lowest bit)
-          mbar_arrive_expect_tx(&raw_bar[stage], (1 + (t.n > 128 ? 2 : 1)) * 128 * 16);
-          tma_load_3d(raw_s, &map_ws, &raw_bar[stage], at, t.m0, t.g);
-          tma_load_2d(raw_s + 128 * 16, &map_xs, &raw_bar[stage], at, t.n0);
-          if (t.n > 128) tma_load_2d(raw_s + 256 * 16, &map_xs, &raw_bar[stage], at, t.n0 + 128);
-          if (t.m_here > 0)
-            tma_load_3d_pair(sA + stage * kQSlotBytes, &map_w, fb, kb * 128, t.m0, t.g);
-          tma_load_2d_pair(bs, mx, fb, kb * 128, n0);
-          if (two) tma_load_2d_pair(bs + 32 * 128, mx, fb, kb * 128, n0 + 32);
+          if (weights) {
+            mbar_arrive_expect_tx(&raw_bar[stage], 128 * 16);
+            tma_load_3d(raw_s, &map_ws, &raw_bar[stage], at, t.m0, t.g);
+            if (t.m_here > 0)
+              tma_load_3d_pair(sA + stage * kQSlotBytes, &map_w, fb, kb * 128, t.m0, t.g);
+          } else {
+            mbar_arrive_expect_tx(&raw_bar[stage], (t.n > 128 ? 2 : 1) * 128 * 16);
+            tma_load_2d(raw_s + 128 * 16, &map_xs, &raw_bar[stage], at, t.n0);
+            if (t.n > 128) tma_load_2d(raw_s + 256 * 16, &map_xs, &raw_bar[stage], at, t.n0 + 128);
+            tma_load_2d_pair(bs, mx, fb, kb * 128, n0);
+            if (two) tma_load_2d_pair(bs + 32 * 128, mx, fb, kb * 128, n0 + 32);
+          }
         }
         __syncwarp();
         if (++stage == kQStages) {
@@ -306,7 +315,8 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     // ------------------------------------------------------------ scales (both CTAs)
     // This warp's rows of each 128: l = 8 * w .. + 7 in lanes by rows l, l + 32, l + 64, l + 96.
     constexpr int kWords = kNv ? 4 : 2;
-    const int l = 8 * (warp - kQScaleWarp) + (lane & 7), i = lane >> 3;
+    const int l = 8 * ((warp - kQScaleWarp) % kQScaleWarps) + (lane & 7), i = lane >> 3;
+    const int team = (warp - kQScaleWarp) / kQScaleWarps;
     const int row = l + 32 * i;
     // A row's scales of block kb, those past the row's end as zeros.
     auto words = [&](const uint8_t* raw_rows, int kb) {
@@ -367,7 +377,15 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       if (t.nkb == 0) continue;
       const bool wide = t.n > 128;
       for (int kb = 0; kb < nkb; ++kb) {
-        // (the stage's own place has been given back before its scales were asked for)
+        // (kQStages is even: a stage is always the same team's. Its place has been given back before its
+        // scales were asked for.)
+        if ((stage & 1) != team) {
+          if (++stage == kQStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          continue;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&raw_bar[stage], phase, abort));
         if (!ok) break;
         const uint8_t* raw_s = sRaw + stage * kQRawBytes;
