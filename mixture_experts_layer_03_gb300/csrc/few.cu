@@ -43,6 +43,7 @@
 #include "fp4.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "pairs.cuh"
 #include "ptx.cuh"
 #include "route_device.cuh"
 #include "rows.cuh"
@@ -289,11 +290,6 @@ __device__ __forceinline__ float inverse_power(float p) {
   return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
-// A number hi + lo.
-struct Pair {
-  float hi, lo;
-};
-
 // Everything about the chosen experts that the block's warps share.
 struct FewShared {
   int32_t ids[kFewTokens * kMaxTopK];
@@ -336,50 +332,9 @@ __device__ __noinline__ void few_select(const float* row, const FewArgs& a, int 
   record_selection(row, sel, a.k, lane, ps, t);
 }
 
-// Sums and quotients of pairs, lo half a unit of hi or less: some 2^-28 of the value, for the routing
-// weights' one rounding at the end. (fp64 runs at 1/64 of fp32's rate here and every block routes for
-// itself: an exponential and a division of 128 slots took 10 us.)
-__device__ __forceinline__ Pair pair_of(float a, float b) {      // a + b, |a| >= |b| or a = 0
-  const float s = a + b;
-  return Pair{s, b - (s - a)};
-}
-__device__ __forceinline__ Pair pair_sum(float a, float b) {     // any a, b (Knuth)
-  const float s = a + b, t = s - a;
-  return Pair{s, (a - (s - t)) + (b - t)};
-}
-__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
-  const Pair s = pair_sum(a.hi, b.hi);
-  return pair_of(s.hi, s.lo + (a.lo + b.lo));
-}
-__device__ __forceinline__ Pair pair_div(Pair a, Pair b) {
-  const float q = __fdiv_rn(a.hi, b.hi);
-  const float rest = fmaf(-q, b.hi, a.hi) + (a.lo - q * b.lo);
-  return pair_of(q, __fdividef(rest, b.hi));
-}
-// exp(a), -64 <= a <= 0: a = n ln 2 + r with ln 2 in two parts, the first of 16 bits (Cody and Waite), so
-// that n times it is exact; then 1 + r + r^2 / 2 + ..., |r| <= 0.35, its first terms in pairs.
-__device__ __forceinline__ Pair pair_exp(Pair a) {
-  constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = static_cast<float>(0.693147180559945309417 - 0x1.62e4p-1);
-  const float n = rintf(a.hi * 1.44269504f);
-  const Pair r = pair_sum(fmaf(-n, kLn2Hi, a.hi), fmaf(-n, kLn2Lo, a.lo));
-  const float sq = r.hi * r.hi, sq_lo = fmaf(r.hi, r.hi, -sq);
-  float q = 1.0f / 40320;
-  q = fmaf(q, r.hi, 1.0f / 5040);
-  q = fmaf(q, r.hi, 1.0f / 720);
-  q = fmaf(q, r.hi, 1.0f / 120);
-  q = fmaf(q, r.hi, 1.0f / 24);
-  q = fmaf(q, r.hi, 1.0f / 6);
-  // r.lo (1 + r): the slope of exp at r.hi
-  const float small = fmaf(r.lo, r.hi, r.lo) + fmaf(0.5f, sq_lo, r.hi * sq * q);
-  const Pair one = pair_of(1.0f, r.hi);
-  const Pair two = pair_sum(one.hi, 0.5f * sq);
-  const Pair e = pair_of(two.hi, (one.lo + two.lo) + small);
-  const float scale = __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23);
-  return Pair{e.hi * scale, e.lo * scale};
-}
-
 // The weights of block_pair_weights (route_device.cuh) for the methods whose slots are in order already, in
-// pairs; by one thread a slot. False, in every thread: a logit is so far off that fp32's range may not do.
+// pairs, for one rounding at the end; by one thread a slot. (In fp64, which runs at 1/64 of fp32's rate,
+// the exponentials and divisions of 128 slots took every block 10 us.) False, in every thread: a logit is so far off that fp32's range may not do.
 __device__ __forceinline__ bool few_weights(const FewArgs& a, FewShared* sh) {
   const int p = threadIdx.x, pairs = a.T * a.k, method = a.route.method;
   const bool sigmoid = method != MOE_ROUTE_DEFAULT && method != MOE_ROUTE_RENORMALIZE &&

@@ -7,10 +7,13 @@
 //   code        e2m1(v / (scale [g])), to nearest even
 // A block that holds an infinity or a NaN gets the scale NaN and codes 0.
 //
-// What is rounded is decided as on exact numbers. In f32 the quotients (mx: exact; nv: a few units)
-// and SwiGLU (kNear covers its error) are off by little, so a decision can differ from the exact one
-// only where a value lies that near to the border between two codes or two scale bytes: there, a few
-// times in a million values, the segment is worked out again in 64 bits.
+// What is rounded is decided as on exact numbers. In f32 the quotients (mx: exact; nv: a few units off) and
+// SwiGLU decide otherwise only where a value lies within its error of the border between two codes or
+// two scale bytes. So codes and bytes are made of the value a little less and a little more; where
+// the two differ, the border itself is compared: for values that are given, with the products of the
+// border, the scale and g in two f32 numbers, which is exact (such cases are common: the quotient of two
+// 8-bit mantissas is often a tie but for g's rounding); for SwiGLU, a few times in a million, the
+// segment is worked out again in pairs of f32 (2^-26), and where that does not do either, in 64 bits.
 //
 // Every value is read and written once; bound by memory: 4.56 bits out for 16 in, or for 32.
 #include <cstdint>
@@ -19,16 +22,19 @@
 
 #include "fp4.cuh"
 #include "launch.cuh"
+#include "pairs.cuh"
 #include "segments.cuh"
 
 namespace moe {
 namespace {
 
-// Relative width around a value in which its f32 form may be: x / unit takes two roundings and the
-// unit one (under 2^-22); SwiGLU's sigma 3 units, its products two more (under 2^-21, then the
-// quotient's).
+// Relative widths around a value in which its f32 form may be. A quotient: the divisor's rounding and the
+// reciprocal's, the product's and that of the factor 1 -+ kNear, 2.5 units of 2^-23. SwiGLU (16-bit and
+// f32 rows alike, by the fast exponential and quotient): 2 + 1.17 |gate| units of the exponential, 2 of
+// the quotient, 1 of the products, then the quotient's. SwiGLU in pairs: under 2^-27.
 constexpr float kNearQuotient = 0x1p-21f;
-constexpr float kNearSwiglu = 0x1p-20f;
+constexpr float kNearSwiglu = 1e-6f, kNearGate = 1.5e-7f;
+constexpr float kNearPairs = 0x1p-26f;
 
 struct Fp4Out {
   uint8_t* codes;       // [R, K / 2]
@@ -62,9 +68,122 @@ __device__ __forceinline__ float nv_scale(uint32_t byte) {
   return __half2float(__half(h));
 }
 
+// Is v above a b, or just there and `tie`? a has few bits, so that a b is hi + lo with hi = a b rounded.
+// Where v is known to kTol of itself only and lies that near, `near` is set.
+template <bool kPairs>
+__device__ __forceinline__ bool above(Pair v, float a, float b, bool tie, bool& near) {
+  const float hi = a * b, lo = fmaf(a, b, -hi);
+  if constexpr (kPairs) {
+    const float d = (v.hi - hi) + (v.lo - lo);
+    near |= fabsf(d) <= kNearPairs * hi;
+    return d > 0.0f;
+  } else {
+    return v.hi > hi || (v.hi == hi && (lo < 0.0f || (lo == 0.0f && tie)));
+  }
+}
+
+// The byte of a block and the codes of a lane's 8 values h (+ l, in pairs) of it. `near`: f32 does not
+// decide.
+template <bool kNv, bool kPairs>
+__device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)[8], float g, uint32_t& byte,
+                                           bool& near) {
+  constexpr int kLanes = kNv ? 2 : 4;   // to a block
+  Pair top{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(h[i]), b = kPairs ? (signbit(h[i]) ? -l[i] : l[i]) : 0.0f;
+    if (!(a < top.hi) && !(a == top.hi && b <= top.lo)) top = Pair{a, b};   // (a NaN stays)
+  }
+#pragma unroll
+  for (int d = 1; d < kLanes; d *= 2) {
+    const float a = __shfl_xor_sync(0xffffffffu, top.hi, d);
+    const float b = kPairs ? __shfl_xor_sync(0xffffffffu, top.lo, d) : 0.0f;
+    // magnitudes order as their bit patterns do, infinities and NaNs on top
+    const uint32_t ua = __float_as_uint(a), ut = __float_as_uint(top.hi);
+    if (ua > ut || (ua == ut && b > top.lo)) top = Pair{a, b};
+  }
+  const float amax = top.hi;
+  float inv, scale;
+  if constexpr (kNv) {
+    const float r = __fdividef(amax, 6.0f * g);
+    byte = nv_byte(r * (1.0f - kNearQuotient));
+    // the border between two neighbouring numbers of e4m3, times 6: 7 bits
+    if (byte != nv_byte(r * (1.0f + kNearQuotient)) && byte < 126)
+      byte += above<kPairs>(top, 3.0f * (nv_scale(byte) + nv_scale(byte + 1)), g, byte & 1, near);
+    scale = nv_scale(byte);
+    inv = byte == 0 ? 0.0f : __fdividef(1.0f, scale * g);
+    // Products of g that f32 does not hold in two parts, and quotients that it does not hold at all.
+    near |= !(6.0f * g > 0x1p-90f && 6.0f * g < 0x1p90f) ||
+            (amax > 0.0f && !(amax > 0x1p-90f && amax < 0x1p90f));
+  } else {
+    byte = mx_byte(amax);
+    if (kPairs) {   // on either side of 6 * 2^e
+      const float border = 6.0f * mx_scale(byte), d = (amax - border) + top.lo;
+      const float under = 0.5f * border, d2 = (amax - under) + top.lo;
+      near |= fabsf(d) <= kNearPairs * border || fabsf(d2) <= kNearPairs * under || amax < 0x1p-90f;
+      if (d > 0.0f) ++byte;
+      else if (byte > 0 && d2 <= 0.0f) --byte;
+    }
+    scale = mx_scale(byte);
+    // 2^-(byte - 127): finite values give bytes up to 253.
+    inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
+  }
+  uint32_t codes;
+  if constexpr (!kNv && !kPairs) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = h[i] * inv;   // exact
+    codes = fp4_codes8(z);
+  } else {
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float z = h[i] * inv;
+      lo[i] = z * (1.0f - kNearQuotient);
+      hi[i] = z * (1.0f + kNearQuotient);
+    }
+    codes = fp4_codes8(lo);
+    uint32_t differ = codes ^ fp4_codes8(hi);
+    // hi's code is the next one up: its border, in quarters, is looked up.
+    while (differ) {
+      const int at = (__ffs(differ) - 1) & ~3;
+      const uint32_t c = codes >> at & 7u;
+      const float border = 0.25f * static_cast<float>(0x00140e0a07050301ull >> (8 * c) & 0xffu);
+      Pair v{};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (at == 4 * i) v = Pair{fabsf(h[i]), kPairs ? (signbit(h[i]) ? -l[i] : l[i]) : 0.0f};
+      codes += static_cast<uint32_t>(above<kPairs>(v, border * scale, kNv ? g : 1.0f, c & 1, near)) << at;
+      differ &= ~(0xfu << at);
+    }
+  }
+  return codes;
+}
+
+// SwiGLU in pairs, and what it decides. `near`: a value that pairs do not hold or decide.
+template <bool kNv>
+__device__ __forceinline__ uint32_t fp4_swiglu_pairs(const float (&v)[8], const float (&u)[8], float g,
+                                                  uint32_t* byte, bool* near) {
+  float h[8], l[8];
+  bool doubt = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(v[i]);
+    const Pair x = pair_exp(Pair{a <= 80.0f ? -a : 0.0f, 0.0f});
+    const Pair s = pair_div(v[i] < 0.0f ? x : Pair{1.0f, 0.0f}, pair_add(Pair{1.0f, 0.0f}, x));
+    const Pair y = pair_mul(pair_mul(s, v[i]), u[i]);
+    h[i] = y.hi;
+    l[i] = y.lo;
+    doubt |= !(a <= 80.0f) || !(fabsf(y.hi) < 0x1p90f) || (y.hi != 0.0f && fabsf(y.hi) < 0x1p-90f);
+  }
+  const uint32_t codes = decide<kNv, true>(h, l, g, *byte, doubt);
+  *near = doubt;
+  return codes;
+}
+
 // The same decisions on 8 values in 64 bits: the block's byte and the codes.
 template <bool kNv>
-__device__ __noinline__ uint32_t fp4_exact(const double (&v)[8], float g, uint32_t* byte_out) {
+__device__ __forceinline__ uint32_t fp4_exact(const double (&v)[8], float g, uint32_t* byte_out) {
   double top = 0.0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = fmax(top, fabs(v[i]));
@@ -106,13 +225,34 @@ __device__ __forceinline__ double swiglu_d(float g, float u) {
   return gd / (1.0 + exp(-gd)) * static_cast<double>(u);
 }
 
+// What f32 does not decide, by a whole warp: its lanes' values are read again (a call that takes them in
+// arrays would keep them in memory in every segment). Codes and the block's byte.
+template <typename T, bool kNv, bool kSwiglu>
+__device__ __noinline__ uint2 fp4_again(const T* src, int K, bool in, bool finite, float g) {
+  float v[kPerLane] = {}, u[kPerLane] = {};
+  if (in) {
+    load8(src, v);
+    if (kSwiglu) load8(src + K, u);
+  }
+  uint2 r;
+  if (kSwiglu) {
+    bool near;
+    r.x = fp4_swiglu_pairs<kNv>(v, u, g, &r.y, &near);
+    if (!__any_sync(0xffffffffu, near && finite)) return r;
+  }
+  double d[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) d[i] = !kSwiglu ? static_cast<double>(v[i]) : in ? swiglu_d(v[i], u[i]) : 0.0;
+  r.x = fp4_exact<kNv>(d, g, &r.y);
+  return r;
+}
+
 template <typename T, bool kNv, bool kSwiglu>
 __global__ void __launch_bounds__(kSegmentThreads)
 quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
   pdl_trigger();
   pdl_wait();
   constexpr int kLanes = kNv ? 2 : 4;           // to a block
-  constexpr float kNear = kSwiglu ? kNearSwiglu : kNearQuotient;
   const int lane = threadIdx.x & 31;
   const int pitch = fp4_scale_pitch(K, kNv ? kFp4Nv : kFp4Mx);
   // Segments of 256 channels, over the whole row of scales.
@@ -120,58 +260,66 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
     const int c = w.seg * 256 + lane * kPerLane;
     const bool in = c < K;                      // (K % 32 == 0: the same in all lanes of a block)
     float v[kPerLane] = {}, u[kPerLane] = {};
+    const T* src = x + w.row * (kSwiglu ? 2 : 1) * K + c;
     if (in) {
-      const T* src = x + w.row * (kSwiglu ? 2 : 1) * K + c;
       load8(src, v);
       if (kSwiglu) load8(src + K, u);
     }
     float g = 1.0f;
     if (kNv && out.g)
       g = __ldg(out.g + (out.rows_per_plane < R ? w.row / out.rows_per_plane : 0));
-    float h[kPerLane], amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      // (f32's form of sigma whatever T is: see kNear.)
-      h[i] = kSwiglu ? v[i] * sigmoid_of<float>(v[i]).x * u[i] : v[i];
-      amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(h[i]) & 0x7fffffffu));
-    }
-    amax = lanes_max<kLanes>(amax);
-    const bool finite = __float_as_uint(amax) < 0x7f800000u;
     uint32_t byte, codes;
-    bool near;
-    float inv;
-    if (kNv) {
-      const float r = __fdiv_rn(amax, 6.0f * g);
-      byte = nv_byte(r);
-      near = nv_byte(r * (1.0f - kNear)) != nv_byte(r * (1.0f + kNear));
-      const float unit = nv_scale(byte) * g;
-      inv = byte == 0 ? 0.0f : __fdiv_rn(1.0f, unit);
-      // Out of f32's normal range, as with a g that is far off: in 64 bits too.
-      near |= byte != 0 && !(unit > 0x1p-100f && unit < 0x1p100f);
-    } else {
-      byte = mx_byte(amax);
-      near = kSwiglu && (mx_byte(amax * (1.0f - kNear)) != mx_byte(amax * (1.0f + kNear)));
-      // 2^-(byte - 127): finite values give bytes up to 253.
-      inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
-    }
-    float z[kPerLane];
+    bool finite;
+    if constexpr (!kSwiglu) {
+      uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) z[i] = h[i] * inv;
-    codes = fp4_codes8(z);
-    if (kNv || kSwiglu) {
-      float lo[kPerLane], hi[kPerLane];
+      for (int i = 0; i < kPerLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+      finite = lanes_max<kLanes>(__uint_as_float(top)) < INFINITY;
+      bool near = false;
+      codes = decide<kNv, false>(v, v, g, byte, near);
+      if (kNv && __any_sync(0xffffffffu, near && finite)) {
+        const uint2 r = fp4_again<T, kNv, false>(src, K, in, finite, g);
+        codes = r.x;
+        byte = r.y;
+      }
+    } else {
+      float h[kPerLane], amax = 0.0f, gates = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
-        lo[i] = z[i] * (1.0f - kNear);
-        hi[i] = z[i] * (1.0f + kNear);
+        h[i] = v[i] * __fdividef(1.0f, 1.0f + __expf(-v[i])) * u[i];
+        gates = fmaxf(gates, fabsf(v[i]));
+        amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(h[i]) & 0x7fffffffu));
       }
-      near |= fp4_codes8(lo) != fp4_codes8(hi);
-      if (__any_sync(0xffffffffu, near && finite)) {
-        double d[kPerLane];
+      amax = lanes_max<kLanes>(amax);
+      gates = lanes_max<kLanes>(gates);
+      finite = amax < INFINITY;
+      // A gate below -80: sigma leaves f32's range.
+      bool near = gates > 80.0f || (kNv && !(6.0f * g > 0x1p-90f && 6.0f * g < 0x1p90f));
+      const float by = fmaf(gates, kNearGate, kNearSwiglu);
+      float inv;
+      if constexpr (kNv) {
+        const float r = __fdividef(amax, 6.0f * g);
+        byte = nv_byte(r * (1.0f - by));
+        near |= byte != nv_byte(r * (1.0f + by)) || (amax > 0.0f && !(amax > 0x1p-90f && amax < 0x1p90f));
+        inv = byte == 0 ? 0.0f : __fdividef(1.0f, nv_scale(byte) * g);
+      } else {
+        byte = mx_byte(amax * (1.0f - by));
+        near |= byte != mx_byte(amax * (1.0f + by));
+        inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
+      }
+      float lo[kPerLane], hi[kPerLane];
+      const float less = inv * (1.0f - by), more = inv * (1.0f + by);
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-          d[i] = kSwiglu ? (in ? swiglu_d(v[i], u[i]) : 0.0) : static_cast<double>(v[i]);
-        codes = fp4_exact<kNv>(d, g, &byte);
+      for (int i = 0; i < kPerLane; ++i) {
+        lo[i] = h[i] * less;
+        hi[i] = h[i] * more;
+      }
+      codes = fp4_codes8(lo);
+      near |= codes != fp4_codes8(hi);
+      if (__any_sync(0xffffffffu, near && finite)) {
+        const uint2 r = fp4_again<T, kNv, true>(src, K, in, finite, g);
+        codes = r.x;
+        byte = r.y;
       }
     }
     if (!finite) {
