@@ -248,7 +248,7 @@ __device__ __noinline__ uint2 fp4_again(const T* src, int K, bool in, bool finit
 }
 
 template <typename T, bool kNv, bool kSwiglu>
-__global__ void __launch_bounds__(kSegmentThreads)
+__global__ void __launch_bounds__(kSegmentThreads, 12)
 quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
   pdl_trigger();
   pdl_wait();
@@ -288,7 +288,7 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
       for (int i = 0; i < kPerLane; ++i) {
         h[i] = v[i] * __fdividef(1.0f, 1.0f + __expf(-v[i])) * u[i];
         gates = fmaxf(gates, fabsf(v[i]));
-        amax = __uint_as_float(max(__float_as_uint(amax), __float_as_uint(h[i]) & 0x7fffffffu));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[i])));   // (a NaN stays)
       }
       amax = lanes_max<kLanes>(amax);
       gates = lanes_max<kLanes>(gates);
@@ -334,6 +334,8 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
   }
 }
 
+// Four times 8 channels a lane, loaded before the first is worked on: 4 bytes of codes a lane are little to
+// have under way. (16 channels side by side a lane leave stores of half sectors: N us for N.)
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(kSegmentThreads)
 dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -343,28 +345,40 @@ dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int pitch = fp4_scale_pitch(K, kNv ? kFp4Nv : kFp4Mx);
-  for (SegmentWalk w((K + 255) / 256); w.row < R; w.next()) {
-    const int c = w.seg * 256 + lane * kPerLane;
-    if (c >= K) continue;
-    uint32_t h[4];
-    fp4_halves8(__ldg(reinterpret_cast<const uint32_t*>(codes + w.row * (K / 2) + c / 2)), h);
-    const uint32_t byte = __ldg(scales + w.row * pitch + c / (kNv ? 16 : 32));
-    float scale;
-    if (kNv) {
-      scale = nv_scale(byte);
-    } else {
-      scale = byte == kMxNan ? __uint_as_float(0x7fffffffu) : mx_scale(byte);
-    }
+  for (SegmentWalk w((K + 1023) / 1024); w.row < R; w.next()) {
+    const int c0 = w.seg * 1024 + lane * kPerLane;
+    const uint8_t* src = codes + w.row * (K / 2) + c0 / 2;
+    const uint8_t* sc = scales + w.row * pitch + c0 / (kNv ? 16 : 32);
+    uint32_t code[4], byte[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (c0 + 256 * p < K) {
+        code[p] = __ldg(reinterpret_cast<const uint32_t*>(src + 128 * p));
+        byte[p] = __ldg(sc + (kNv ? 16 : 8) * p);
+      }
     // code * scale has 6 significant bits: exact; then g's rounding and that to T.
     const float g = kNv && gs ? __ldg(gs + (rows_per_plane < R ? w.row / rows_per_plane : 0)) : 1.0f;
-    float f[kPerLane];
+    T* dst = out + w.row * K + c0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      f[2 * i] = two.x * scale * g;
-      f[2 * i + 1] = two.y * scale * g;
+    for (int p = 0; p < 4; ++p) {
+      if (c0 + 256 * p >= K) break;
+      float scale;
+      if (kNv) {
+        scale = nv_scale(byte[p]);
+      } else {
+        scale = byte[p] == kMxNan ? __uint_as_float(0x7fffffffu) : mx_scale(byte[p]);
+      }
+      uint32_t h[4];
+      fp4_halves8(code[p], h);
+      float f[kPerLane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        f[2 * i] = two.x * scale * g;
+        f[2 * i + 1] = two.y * scale * g;
+      }
+      store8(dst + 256 * p, f);
     }
-    store8(out + w.row * K + c, f);
   }
 }
 
@@ -385,7 +399,7 @@ template <typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, const float* g,
                          int64_t rows_per_plane, int64_t R, int K, int fmt, void* out,
                          cudaStream_t s) {
-  const dim3 grid(segment_grid(R, (K + 255) / 256)), block(kSegmentThreads);
+  const dim3 grid(segment_grid(R, (K + 1023) / 1024)), block(kSegmentThreads);
   return fmt == kFp4Nv ? launch_pdl(dequantize_fp4_kernel<T, true>, grid, block, 0, s, codes, scales, g,
                                     rows_per_plane, R, K, static_cast<T*>(out))
                        : launch_pdl(dequantize_fp4_kernel<T, false>, grid, block, 0, s, codes, scales,
