@@ -12,6 +12,7 @@ order between it and other streams' work on the arguments and results is the cal
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -882,6 +883,13 @@ class Fp4:
             raise ValueError("scales must be on the codes' device")
         self.codes, self.scales, self.format, self.g = codes, scales, format, g
 
+    @classmethod
+    def _of(cls, codes, scales, format, g) -> "Fp4":
+        """Of parts that this module has made or checked."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.format, q.g = codes, scales, format, g
+        return q
+
     @staticmethod
     def scale_columns(K: int, format: int) -> int:
         return (K // _FP4_BLOCK[format] + 15) // 16 * 16
@@ -900,9 +908,15 @@ def _new_fp4(shape, format: int, g, device, stream, out: Optional[Fp4]) -> Fp4:
         if out.shape != tuple(shape) or out.format != format or out.codes.device != device:
             raise ValueError(f"out must be of {tuple(shape)} and the same format, got {out.shape}")
         return Fp4(out.codes, out.scales, format, g)
-    codes = _new(shape[:-1] + (shape[-1] // 2,), torch.uint8, device, stream)
-    scales = _new(shape[:-1] + (Fp4.scale_columns(shape[-1], format),), torch.uint8, device, stream)
-    return Fp4(codes, scales, format, g)
+    if g is not None:
+        if format != MOE_FP4_NV:
+            raise ValueError("only MOE_FP4_NV has a g")
+        _shaped(g, "g", (shape[0] if len(shape) == 3 else 1,), torch.float32)
+        if g.device != device:
+            raise ValueError("g must be on the rows' device")
+    head, K = tuple(shape[:-1]), shape[-1]
+    return Fp4._of(_new(head + (K // 2,), torch.uint8, device, stream),
+                   _new(head + (Fp4.scale_columns(K, format),), torch.uint8, device, stream), format, g)
 
 
 def moe_quantize_fp4(x, format: int, g: Optional[torch.Tensor] = None, out: Optional[Fp4] = None,
@@ -974,6 +988,14 @@ def alloc_few_scratch(problem: MoeProblem, device="cuda", stream=None) -> Scratc
     return Scratch(_new(n, torch.uint8, device, stream, result=False))
 
 
+@functools.lru_cache(maxsize=256)
+def _few_plan(T, H, I, E, k, shared_I, method, n_group, topk_group, rsf):
+    """What the library is told of a layer's sizes and routing, and the workspace's size."""
+    p = MoeProblem(T, H, I, E, k, shared_I)
+    r = MoeRouteParams(E, k, method, n_group, topk_group, rsf)
+    return ctypes.byref(p), ctypes.byref(r), _lib.moe_layer_few_workspace_bytes(ctypes.byref(p))
+
+
 def _few_weights(w, name: str, shape: tuple, format: int, dtype) -> MoeWeights:
     """A weight of moe_layer_few: an Fp4 of `format`, or a tensor of `dtype`, of just this shape."""
     if format == MOE_WEIGHTS_16BIT:
@@ -1025,15 +1047,16 @@ def moe_layer_few(x, wg, w13, w2, method: int, top_k: int, bias: Optional[torch.
            else _shaped(ids, "ids", (T, top_k), torch.int32))
     scales = (_new((T, top_k), torch.float32, x.device, stream) if scales is None
               else _shaped(scales, "scales", (T, top_k), torch.float32))
-    p = MoeProblem(T, H, I, E, top_k, shared_I)
+    p, r, n = _few_plan(T, H, I, E, top_k, shared_I, method, n_group, topk_group, routed_scaling_factor)
     if scratch is None:
-        n = _lib.moe_layer_few_workspace_bytes(ctypes.byref(p))
-        scratch = Scratch(_new(n, torch.uint8, x.device, stream, result=False))
-    r = MoeRouteParams(E, top_k, method, n_group, topk_group, routed_scaling_factor)
-    _check(_lib.moe_layer_few(ctypes.byref(p), ctypes.byref(r), x.data_ptr(), wg.data_ptr(), gate,
-                              _ptr(bias), ctypes.byref(a), ctypes.byref(b), a_s, b_s, format, code,
-                              ids.data_ptr(), scales.data_ptr(), y.data_ptr(), scratch.ptr,
-                              scratch.nbytes, _stream(stream)), "moe_layer_few")
+        buf = _new(n, torch.uint8, x.device, stream, result=False)
+    else:
+        buf, n = scratch.buf, scratch.nbytes
+    st = _lib.moe_layer_few(p, r, x.data_ptr(), wg.data_ptr(), gate, _ptr(bias), ctypes.byref(a),
+                            ctypes.byref(b), a_s, b_s, format, code, ids.data_ptr(), scales.data_ptr(),
+                            y.data_ptr(), buf.data_ptr(), n, _stream(stream))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_layer_few")
     return y, ids, scales
 
 

@@ -8,9 +8,10 @@
 // producers) keep its ring full from the moment the experts are known, on into the second products'
 // weights while the first products' results are still awaited.
 //
-// Work. Tickets 0..n-1 are slices of the first products: the chosen experts' I channels one after the
-// other (a channel is its gate and its up row), cut into n equal parts to a channel, n blocks. Tickets
-// n..2n-1 are slices of the H rows of the second products, over all experts. A block takes tickets
+// Work. The first tickets are slices of the first products: the chosen experts' I channels one after the
+// other (a channel is its gate and its up row), and the shared expert's, each cut into equal parts to
+// a channel, one a block. The others are slices of the H rows of the second products, over all experts,
+// one a block. A block takes tickets
 // in order until none is left; a slice of the second products waits for the first ones' results, which
 // are in blocks that run already, so that blocks that are not resident yet are waited for by nobody.
 // Every element of h and of y is summed by one block in one order: the same result on every run.
@@ -60,10 +61,11 @@ constexpr int kWWarps = 4;                       // producers of the weights' si
 constexpr int kWarpW = kMmaWarps, kWarpX = kWarpW + kWWarps;
 constexpr int kFewThreads = 32 * (kWarpX + kXWarps);
 constexpr int kTeams = 4, kTeamWarps = kMmaWarps / kTeams;   // of consumers
-constexpr int kXSlots = 4;                       // chunks of the tokens' side
+constexpr int kXSlots = kXWarps;                 // chunks of the tokens' side, one a producer
 static_assert(kXSlots == kTeams, "a slot belongs to the same teams throughout a part");
 constexpr int kFewRows = 32;                     // rows of weights a stage
 constexpr int kFewMaxBlocks = 192;
+constexpr int kFewTickets = 2 * kFewMaxBlocks + 2;
 constexpr int kFewSmem = 232448 - 10240;         // of a block, without the static part
 
 enum : int { kW16b = 0, kW16h = 1, kW4mx = 2, kW4nv = 3 };   // bf16, f16, mx, nv
@@ -241,10 +243,11 @@ __device__ __forceinline__ void mma_16bit(float (&d)[4], const uint32_t (&a)[4],
           "f"(c[3]));
 }
 
-// 16 bytes from global to shared memory, past L1, without a register on the way.
-__device__ __forceinline__ void async_load_16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src))
+// 16 bytes to shared memory, the first `bytes` of them from global memory, past L1, without a register on the
+// way, the others zeros.
+__device__ __forceinline__ void async_load_16(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                : "memory");
 }
 // One of the arrivals that `bar` counts, once this thread's copies so far are there.
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   __shared__ FewShared sh;
   __shared__ uint64_t w_full[kStages], w_empty[kStages], x_full[kXSlots], x_empty[kXSlots];
-  __shared__ int s_ticket[2 * kFewMaxBlocks + 2];
+  __shared__ int s_ticket[kFewTickets];
   __shared__ int s_abort, s_current;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   volatile int* abort = &s_abort;
 
   pdl_trigger();
-  for (int i = tid; i < 2 * kFewMaxBlocks + 2; i += kFewThreads) s_ticket[i] = -1;
+  for (int i = tid; i < kFewTickets; i += kFewThreads) s_ticket[i] = -1;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&w_full[s], 32);           // a producer warp's lanes
@@ -510,15 +513,30 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   const int n_exp = sh.n, T = a.T, H = a.H;
   const int n_all = n_exp + (a.shared_I > 0);
   const int routed = n_exp * a.I, total = routed + a.shared_I;   // channels of the first products
-  // Slice `i` of the first products starts at channel cut1(i), of the second at row cut2(i).
-  auto cut1 = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / n_blocks); };
-  auto cut2 = [&](int i) { return static_cast<int>(static_cast<int64_t>(H) * i / n_blocks); };
-  // The part of the first products that starts at channel q of all, in a slice that ends at `end`.
-  auto part1 = [&](int q, int end) {
-    const bool own = q < routed;
-    const int at = own ? q / a.I : n_exp;
-    const int ch = own ? q - at * a.I : q - routed;
-    return FewPart(at, ch, min(kTeams * 16, min(end - q, (own ? a.I : a.shared_I) - ch)), 16);
+  // A slice of each of the two products a block. (Four of the first a block, for experts with more tokens,
+  // which take more time, to even out: 602 us became 665 for 16 tokens over 256 experts of 7168 x 2048.)
+  const int n_first = n_blocks;
+  const int n_tickets = n_first + n_blocks;
+  // Slice `i` of the first products: channels [s0, s0 + ns) of the shared expert, then [r0, r0 + nr) of the
+  // chosen ones', one after the other. Every slice has its share of the shared expert, which has all the
+  // tokens and takes more time for its bytes (16 tokens, all of it in the last slices: they ended 1.7
+  // times as late as the others). The second products' slice starts at row cut2(i).
+  struct Slice {
+    int s0, ns, r0, nr;
+    __device__ __forceinline__ int size() const { return ns + nr; }
+  };
+  auto cut = [](int n, int i, int of) { return static_cast<int>(static_cast<int64_t>(n) * i / of); };
+  auto slice1 = [&](int i) {
+    const int s0 = cut(a.shared_I, i, n_first), r0 = cut(routed, i, n_first);
+    return Slice{s0, cut(a.shared_I, i + 1, n_first) - s0, r0, cut(routed, i + 1, n_first) - r0};
+  };
+  auto cut2 = [&](int i) { return cut(H, i, n_blocks); };
+  constexpr int kMost1 = kTeams * 16;
+  // The part at channel z of a slice.
+  auto part1 = [&](const Slice& sl, int z) {
+    if (z < sl.ns) return FewPart(n_exp, sl.s0 + z, min(kMost1, sl.ns - z), 16);
+    const int q = sl.r0 + z - sl.ns, at = q / a.I, ch = q - at * a.I;
+    return FewPart(at, ch, min(kMost1, min(sl.size() - z, a.I - ch)), 16);
   };
   // Of the rows left, equal parts.
   auto part2 = [&](int r, int end) {
@@ -526,7 +544,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     return FewPart(0, r, (left + parts - 1) / parts, kFewRows);
   };
   auto inner = [&](int at) { return at < n_exp ? a.I : a.shared_I; };   // channels of a chosen expert
-  // Ticket i of this block, when it is there; 2 n_blocks (no work) if it does not come.
+  // Ticket i of this block, when it is there; n_tickets (no work) if it does not come.
   auto ticket_at = [&](int i, bool& ok) {
     const volatile int* at = &s_ticket[i];
     int v = *at;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     while ((v = *at) < 0) {
       if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
         ok = false;
-        return 2 * n_blocks;
+        return n_tickets;
       }
       __nanosleep(64);
     }
@@ -551,21 +569,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // n rows of len channels, from `row` of m and channel k0 of K on, to rows from `at` on of the stage.
+    // n rows of len channels, from `row` of m and channel k0 of K on, to rows from `at` on of the stage;
+    // zeros up to the chunk's end (which the products then need not know).
     auto rows = [&](const FewMatrix& m, int64_t row, int n, int at, int K, int k0, int len) {
       constexpr int kLanes = W::kRowBytes / 16, kStep = 32 / kLanes;   // lanes to a row, rows at once
       const int part = lane % kLanes, first = lane / kLanes;
       const int bytes = W::k4 ? len / 2 : len * 2;
       const int64_t pitch = W::k4 ? K / 2 : 2 * static_cast<int64_t>(K);
+      const bool in = part * 16 < bytes;
       uint8_t* dst = sW + stage * W::kStage + (at + first) * W::kPitch + part * 16;
-      const uint8_t* src = m.w + (row + first) * pitch + (W::k4 ? k0 / 2 : 2 * k0) + part * 16;
-      if (part * 16 < bytes) {
+      const uint8_t* src = m.w + (row + first) * pitch + (W::k4 ? k0 / 2 : 2 * k0) + (in ? part * 16 : 0);
 #pragma unroll 4
-        for (int i = first; i < n; i += kStep) {
-          async_load_16(dst, src);
-          dst += kStep * W::kPitch;
-          src += kStep * pitch;
-        }
+      for (int i = first; i < n; i += kStep) {
+        async_load_16(dst, src, in ? 16u : 0u);
+        dst += kStep * W::kPitch;
+        src += kStep * pitch;
       }
       if constexpr (W::k4) {
         constexpr int kBlock = kW == kW4nv ? 16 : 32;
@@ -574,15 +592,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         const int ps = lane % kLanesS, i = lane / kLanesS;
         static_assert(32 / kLanesS >= 16, "a row each");
         uint8_t* to = sW + stage * W::kStage + kFewRows * W::kPitch + (at + i) * W::kScalePitch + ps * 16;
-        const uint8_t* from = m.scales + (row + i) * sp + k0 / kBlock + ps * 16;
-        if (ps * 16 < sp - k0 / kBlock) {
-          if (i < n) async_load_16(to, from);
-          if (32 / kLanesS < kFewRows && i + 32 / kLanesS < n)
-            async_load_16(to + 32 / kLanesS * W::kScalePitch, from + 32 / kLanesS * sp);
-        }
+        // (of the row's own scales: what fills it up may be anything)
+        const int left = (K - k0) / kBlock - ps * 16;
+        const uint32_t there = left <= 0 ? 0u : left < 16 ? left : 16u;
+        const uint8_t* from = m.scales + (row + i) * sp + k0 / kBlock + (there ? ps * 16 : 0);
+        if (i < n) async_load_16(to, from, there);
+        if (32 / kLanesS < kFewRows && i + 32 / kLanesS < n)
+          async_load_16(to + 32 / kLanesS * W::kScalePitch, from + 32 / kLanesS * sp, there);
       }
     };
-    // A stage is this warp's or the other one's.
+    // A stage is this warp's or another one's.
     auto begin = [&] {
       const bool is = turn == mine;
       turn = turn + 1 == kWWarps ? 0 : turn + 1;
@@ -609,11 +628,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         if (!ok) break;
       }
       ticket = __shfl_sync(0xffffffffu, ticket, 0);
-      if (ticket >= 2 * n_blocks) break;
-      if (ticket < n_blocks) {
-        for (int q = cut1(ticket), end = cut1(ticket + 1); q < end && ok;) {
-          const FewPart p = part1(q, end);
-          q += p.n;
+      if (ticket >= n_tickets) break;
+      if (ticket < n_first) {
+        const Slice slice = slice1(ticket);
+        for (int z = 0; z < slice.size() && ok;) {
+          const FewPart p = part1(slice, z);
+          z += p.n;
           const bool own = p.a < n_exp;
           const FewMatrix& m = own ? a.w13 : a.w13_s;
           const int width = inner(p.a);
@@ -631,7 +651,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           }
         }
       } else {
-        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end && ok;) {
+        for (int r = cut2(ticket - n_first), end = cut2(ticket - n_first + 1); r < end && ok;) {
           const FewPart p = part2(r, end);
           r += p.n;
           for (int e = 0; e < n_all && ok; ++e) {
@@ -653,138 +673,155 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     async_wait_all();   // (nothing is under way into the memory of a block that has ended)
   } else if (warp >= kWarpX) {
     // ------------------------------------------------------------ tokens
-    // Chunk after chunk goes round the warps, and round the slots. Only the rows of an expert's tokens are
-    // written: what the others' hold reaches columns that nobody looks at.
+    // Chunk after chunk goes round the four warps and their slots. Only the rows of an expert's tokens are
+    // written: what the others' hold reaches columns that nobody looks at. Rows are loaded two batches
+    // ahead, the first ones (mostly all) before the slot is waited for.
     const int mine = warp - kWarpX;
-    int next = 0, slot = 0;                 // the warp of the next chunk; its slot and the slot's use
     uint32_t phase = 0;
-    uint8_t* dst = sX;
+    int before = 0;                         // chunks of the tickets so far, mod kXWarps
     bool ok = true, waited = false;
     float t_mul = 1.0f;                     // lane t: token t's power of two for h
-    constexpr int kVecs = W::kChunk / 8, kPer = kVecs / 32;   // of a row of a slot, a lane's
-    // Is the next chunk this warp's? Then once its slot is free, and `publish` passes it on.
-    auto begin = [&] {
-      const bool is = next == mine;
-      if (is) {
-        ok = __all_sync(0xffffffffu, few_wait(&x_empty[slot], phase ^ 1u, abort));
-        dst = sX + slot * 8 * kNt * W::kXPitch;
-      }
-      return is && ok;
-    };
-    auto publish = [&](bool is) {
-      if (is) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_full[slot]);
-      }
-      next = next + 1 == kXWarps ? 0 : next + 1;
-      if (++slot == kXSlots) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    };
+    constexpr int kVecs = W::kChunk / 8, kPer = kVecs / 32;   // of 8 channels: of a row of a slot, a lane's
+    uint8_t* dst = sX + mine * 8 * kNt * W::kXPitch;
     for (int i = 0; ok; ++i) {
       const int ticket = __shfl_sync(0xffffffffu, ticket_at(i, ok), 0);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok || ticket >= 2 * n_blocks) break;
-      if (ticket < n_blocks) {
-        for (int q = cut1(ticket), end = cut1(ticket + 1); q < end && ok;) {
-          const FewPart p = part1(q, end);
-          q += p.n;
-          const uint32_t tokens = sh.tokens[p.a];
-          for (int k0 = 0; k0 < H && ok; k0 += W::kChunk) {
-            const bool is = begin();
-            const int nv = min(W::kChunk, H - k0) / 8;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + k0);
-            // Four tokens' loads at once.
-            for (uint32_t rest = is ? tokens : 0u; rest;) {
-              int t[4];
-              uint4 u[4][kPer];
-#pragma unroll
-              for (int i4 = 0; i4 < 4; ++i4) {
-                t[i4] = rest ? __ffs(rest) - 1 : -1;
-                rest &= rest - 1;
-#pragma unroll
-                for (int h = 0; h < kPer; ++h)
-                  if (t[i4] >= 0 && lane + 32 * h < nv)
-                    u[i4][h] = __ldg(src + static_cast<int64_t>(t[i4]) * (H / 8) + lane + 32 * h);
-              }
-#pragma unroll
-              for (int i4 = 0; i4 < 4; ++i4) {
-                if (t[i4] < 0) break;
-                const float mul = sh.x_mul[t[i4]];
-#pragma unroll
-                for (int h = 0; h < kPer; ++h) {
-                  if (lane + 32 * h >= nv) continue;
-                  uint4 v = u[i4][h];
-                  if (W::k4) {
-                    float f[8];
-                    if (a.bf16) unpack8<__nv_bfloat16>(v, f);
-                    else unpack8<__half>(v, f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= mul;
-                    v = Vec<__half, 16>::pack(f);
-                  }
-                  *reinterpret_cast<uint4*>(dst + t[i4] * W::kXPitch + (lane + 32 * h) * 16) = v;
-                }
-              }
-            }
-            publish(is);
-          }
-        }
-      } else {
-        if (!waited) {
-          // All of h, and each token's largest.
-          ok = __all_sync(0xffffffffu, wait_count(a.ticket + 1, total, abort));
-          if (!ok) break;
-          waited = true;
-          if (!kBf16 && lane < T) t_mul = to_f16_range(__uint_as_float(__ldcg(a.tmax + lane)));
-        }
-        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end && ok;) {
-          r += part2(r, end).n;
-          for (int e = 0; e < n_all && ok; ++e) {
-            const int K = inner(e);
-            for (int k0 = 0; k0 < K && ok; k0 += W::kChunk) {
-              const bool is = begin();
-              const int nv = min(W::kChunk, K - k0) / 8;
-              for (uint32_t rest = is ? sh.tokens[e] : 0u; rest;) {
-                int t[2];
-                float4 u[2][kPer][2];
-#pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2) {
-                  t[i2] = rest ? __ffs(rest) - 1 : -1;
-                  rest &= rest - 1;
-                  if (t[i2] < 0) continue;
-                  const float4* src = reinterpret_cast<const float4*>(
-                      a.h + (static_cast<int64_t>(t[i2]) * (a.k + 1) + sh.slot[e][t[i2]]) * a.h_ld + k0);
-#pragma unroll
-                  for (int h = 0; h < kPer; ++h)
-                    if (lane + 32 * h < nv) {
-                      u[i2][h][0] = __ldcg(src + 2 * (lane + 32 * h));
-                      u[i2][h][1] = __ldcg(src + 2 * (lane + 32 * h) + 1);
-                    }
-                }
-#pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2) {
-                  if (t[i2] < 0) break;
-                  const float mul = __shfl_sync(0xffffffffu, t_mul, t[i2]);
-#pragma unroll
-                  for (int h = 0; h < kPer; ++h) {
-                    if (lane + 32 * h >= nv) continue;
-                    const float4 lo = u[i2][h][0], hi = u[i2][h][1];
-                    const float f[8] = {lo.x * mul, lo.y * mul, lo.z * mul, lo.w * mul,
-                                        hi.x * mul, hi.y * mul, hi.z * mul, hi.w * mul};
-                    uint4 v;
-                    if constexpr (kBf16) v = Vec<__nv_bfloat16, 16>::pack(f);
-                    else v = Vec<__half, 16>::pack(f);
-                    *reinterpret_cast<uint4*>(dst + t[i2] * W::kXPitch + (lane + 32 * h) * 16) = v;
-                  }
-                }
-              }
-              publish(is);
-            }
-          }
-        }
+      if (!ok || ticket >= n_tickets) break;
+      const bool fc1 = ticket < n_first;
+      if (!fc1 && !waited) {
+        // All of h, and each token's largest.
+        ok = __all_sync(0xffffffffu, wait_count(a.ticket + 1, total, abort));
+        if (!ok) break;
+        waited = true;
+        if (!kBf16 && lane < T) t_mul = to_f16_range(__uint_as_float(__ldcg(a.tmax + lane)));
       }
+      // Where in the slice: the next part (from `at` on), the expert, the chunk of its contraction.
+      const Slice slice = slice1(fc1 ? ticket : 0);
+      const int end = fc1 ? slice.size() : cut2(ticket - n_first + 1);
+      int at = fc1 ? 0 : cut2(ticket - n_first);
+      int e = 0, chunk = 0, count = 0;
+      bool there = at < end;
+      auto enter = [&] {                    // the part at `at`
+        if (fc1) {
+          const FewPart p = part1(slice, at);
+          at += p.n;
+          e = p.a;
+        } else {
+          at += part2(at, end).n;
+          e = 0;
+        }
+      };
+      auto width = [&] { return fc1 ? H : inner(e); };
+      auto step = [&](int by) {
+        chunk += by;
+        count += by;
+        for (int n; there && chunk >= (n = (width() + W::kChunk - 1) / W::kChunk);) {
+          chunk -= n;
+          if (!fc1 && ++e < n_all) continue;
+          there = at < end;
+          if (there) enter();
+        }
+        if (!there) count -= chunk;         // (chunks past the slice's end)
+      };
+      if (there) {
+        enter();
+        step((mine - before + kXWarps) % kXWarps);
+      }
+      // A batch: rows of x of 4 tokens as they are, or of h in f32 of 2.
+      struct Batch {
+        uint4 u[4][kPer];
+        uint32_t tokens;
+      };
+      uint32_t rest = 0;                    // tokens to load yet
+      auto load = [&](Batch& b) {
+        const int k0 = chunk * W::kChunk, nv = min(W::kChunk, width() - k0) / 8;
+        b.tokens = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!rest || (!fc1 && j >= 2)) break;
+          const int t = __ffs(rest) - 1;
+          rest &= rest - 1;
+          b.tokens |= 1u << t;
+          if (fc1) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) +
+                                                              static_cast<int64_t>(t) * H + k0);
+#pragma unroll
+            for (int h = 0; h < kPer; ++h)
+              if (lane + 32 * h < nv) b.u[j][h] = __ldg(src + lane + 32 * h);
+          } else {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.h + (static_cast<int64_t>(t) * (a.k + 1) + sh.slot[e][t]) * a.h_ld + k0);
+#pragma unroll
+            for (int h = 0; h < kPer; ++h)
+              if (lane + 32 * h < nv) {
+                b.u[2 * (j & 1)][h] = __ldcg(src + 2 * (lane + 32 * h));
+                b.u[2 * (j & 1) + 1][h] = __ldcg(src + 2 * (lane + 32 * h) + 1);
+              }
+          }
+        }
+      };
+      auto store = [&](const Batch& b) {
+        const int nv = min(W::kChunk, width() - chunk * W::kChunk) / 8;
+        uint32_t left = b.tokens;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!left) break;
+          const int t = __ffs(left) - 1;
+          left &= left - 1;
+          const float h_mul = __shfl_sync(0xffffffffu, t_mul, t);
+          const float mul = fc1 ? sh.x_mul[t] : h_mul;
+#pragma unroll
+          for (int h = 0; h < kPer; ++h) {
+            if (lane + 32 * h >= nv) {      // zeros up to the chunk's end
+              *reinterpret_cast<uint4*>(dst + t * W::kXPitch + (lane + 32 * h) * 16) = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 v = b.u[j][h];
+            if (!fc1 || W::k4) {
+              float f[8];
+              if (!fc1) {
+                const uint4 lo = b.u[2 * (j & 1)][h], hi = b.u[2 * (j & 1) + 1][h];
+                f[0] = __uint_as_float(lo.x);
+                f[1] = __uint_as_float(lo.y);
+                f[2] = __uint_as_float(lo.z);
+                f[3] = __uint_as_float(lo.w);
+                f[4] = __uint_as_float(hi.x);
+                f[5] = __uint_as_float(hi.y);
+                f[6] = __uint_as_float(hi.z);
+                f[7] = __uint_as_float(hi.w);
+              } else if (a.bf16) {
+                unpack8<__nv_bfloat16>(v, f);
+              } else {
+                unpack8<__half>(v, f);
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] *= mul;
+              if constexpr (kBf16) v = Vec<__nv_bfloat16, 16>::pack(f);
+              else v = Vec<__half, 16>::pack(f);
+            }
+            *reinterpret_cast<uint4*>(dst + t * W::kXPitch + (lane + 32 * h) * 16) = v;
+          }
+        }
+      };
+      while (there && ok) {
+        Batch one, two;
+        rest = sh.tokens[e];
+        load(one);
+        load(two);
+        ok = __all_sync(0xffffffffu, few_wait(&x_empty[mine], phase ^ 1u, abort));
+        phase ^= 1u;
+        if (!ok) break;
+        while (one.tokens) {
+          store(one);
+          load(one);
+          store(two);
+          load(two);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_full[mine]);
+        step(kXWarps);
+      }
+      before = (before + count) % kXWarps;
     }
     if (!ok) few_timeout(abort);
   } else {
@@ -798,111 +835,120 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     int first = 0;                                 // place in the ring of the part's first stage
     uint32_t first_phase = 0;
 
-    // Stage i of the part, by its team: sub-tile products of chunk `xc` (of all so far), `len` channels.
-    // `second`: there are rows past the first 16. All columns are multiplied, whoever's token is in them.
-    // (No branch inside a group: the compiler moves loads and conversions over products only within one.)
-    auto multiply = [&](auto second, float (&acc)[2][kNt][4], int i, int xc, int len, int subs) {
-      constexpr int kM = decltype(second)::value ? 2 : 1;
+    // Stage i of the part, by its team: products of chunk `xc` (of all so far) with kTiles
+    // column tiles from `tile` on, of all their columns, whoever's token is in them. kM: are there rows
+    // past the first 16? (No branch inside a group: the compiler moves loads and conversions over
+    // products only within one.)
+    auto multiply = [&](auto m_tiles, auto n_tiles, float (&acc)[2][kNt][4], int tile, int i, int xc, int subs) {
+      constexpr int kM = decltype(m_tiles)::value, kTiles = decltype(n_tiles)::value;
       const int place = first + i, lap = place / kStages;
       const int stage = place - lap * kStages, xs = xc % kXSlots;
       const uint32_t phase = first_phase ^ (lap & 1), x_phase = xc / kXSlots & 1;
-      const int groups = min(max(len / 32 - member * W::kGroups, 0), W::kGroups);
-      const uint8_t* x = sX + (xs * 8 * kNt + g) * W::kXPitch + member * W::kGroups * 64 + c * 16;
+      const uint8_t* x = sX + ((xs * kNt + tile) * 8 + g) * W::kXPitch + member * W::kGroups * 64 + c * 16;
       const uint8_t* w = sW + stage * W::kStage + g * W::kPitch + member * W::kGroups * (W::k4 ? 16 : 64) +
                          c * (W::k4 ? 4 : 16);
+      const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
+                          member * W::kGroups * (kW == kW4nv ? 2 : 1);
       ok = few_wait(&x_full[xs], x_phase, abort) && ok;
       ok = few_wait(&w_full[stage], phase, abort) && ok;
-      // Four groups of 32 channels, from k0 on, of which `left` are before the contraction's end.
-      auto four = [&](int k0, int left) {
-        // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
-        uint32_t scale[2 * kM][2] = {};
-        if constexpr (W::k4) {
-          const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
-                              (member * W::kGroups + k0) * (kW == kW4nv ? 2 : 1);
+      // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
+      uint32_t scale[2 * kM][2] = {}, nan[2 * kM] = {};
+      auto scales = [&](int k0) {
 #pragma unroll
-          for (int r = 0; r < 2 * kM; ++r) {
-            if constexpr (kW == kW4nv) {
-              const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch);
-              // this lane's block of each group
-              const uint32_t of_lane = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
-              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                  : "=r"(scale[r][0]), "=r"(scale[r][1])
-                  : "r"(of_lane));
-            } else {
-              scale[r][0] = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch);
-            }
+        for (int r = 0; r < 2 * kM; ++r) {
+          if constexpr (kW == kW4nv) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 8 * W::kScalePitch + k0 * 2);
+            // this lane's block of each group
+            const uint32_t of_lane = __byte_perm(v.x, v.y, c >> 1 ? 0x7531u : 0x6420u);
+            asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                : "=r"(scale[r][0]), "=r"(scale[r][1])
+                : "r"(of_lane));
+          } else if constexpr (kW == kW4mx) {
+            const uint32_t four = *reinterpret_cast<const uint32_t*>(sc + r * 8 * W::kScalePitch + k0);
+            scale[r][0] = four;
+            // a byte of 255: the highest bit of a byte whose other bits carry into it
+            nan[r] |= ((four & 0x7f7f7f7fu) + 0x01010101u) & four & 0x80808080u;
           }
-        }
-        auto group = [&](int k) {
-          uint4 b[kNt];
-#pragma unroll
-          for (int n = 0; n < kNt; ++n)
-            b[n] = *reinterpret_cast<const uint4*>(x + n * 8 * W::kXPitch + (k0 + k) * 64);
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
-              if constexpr (W::k4) {
-                fp4_halves8(*reinterpret_cast<const uint32_t*>(src + (k0 + k) * 16), p[r]);
-                if constexpr (kW == kW4nv) {
-                  const __half2 both = *reinterpret_cast<const __half2*>(&scale[2 * m + r][k >> 1]);
-                  const __half2 one = k & 1 ? __high2half2(both) : __low2half2(both);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
-                    p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
-                  }
-                }
-              } else {
-                const uint4 u = *reinterpret_cast<const uint4*>(src + (k0 + k) * 64);
-                p[r][0] = u.x;
-                p[r][1] = u.y;
-                p[r][2] = u.z;
-                p[r][3] = u.w;
-              }
-            }
-            const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-            const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-            if constexpr (kW == kW4mx) {
-              float f[2];
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t byte = scale[2 * m + r][0] >> (8 * k) & 0xffu;
-                f[r] = __uint_as_float(byte == 0 ? 0x00400000u : byte == kMxNan ? 0x7fffffffu : byte << 23);
-              }
-#pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                const float zero[4] = {};
-                float d[4], d2[4];
-                mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
-                mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d2[j], f[j >> 1], acc[m][n][j]);
-              }
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                mma_16bit<kBf16>(acc[m][n], a0, b[n].x, b[n].y, acc[m][n]);
-                mma_16bit<kBf16>(acc[m][n], a1, b[n].z, b[n].w, acc[m][n]);
-              }
-            }
-          }
-        };
-        if (left >= 4) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) group(k);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (k < left) group(k);
         }
       };
+      auto group = [&](int k, int of) {   // `of` the four that scales() read
+        uint4 b[kTiles];
 #pragma unroll
-      for (int k0 = 0; k0 < W::kGroups; k0 += 4)
-        if (k0 < groups) four(k0, groups - k0);
+        for (int n = 0; n < kTiles; ++n) b[n] = *reinterpret_cast<const uint4*>(x + n * 8 * W::kXPitch + k * 64);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+          uint32_t p[2][4];   // rows g and g + 8 of the tile: four pairs of neighbouring channels
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* src = w + (m * 16 + r * 8) * W::kPitch;
+            if constexpr (W::k4) {
+              fp4_halves8(*reinterpret_cast<const uint32_t*>(src + k * 16), p[r]);
+              if constexpr (kW == kW4nv) {
+                const uint32_t both = of & 2 ? scale[2 * m + r][1] : scale[2 * m + r][0];
+                const uint32_t twice = __byte_perm(both, 0, of & 1 ? 0x3232u : 0x1010u);
+                const __half2 one = *reinterpret_cast<const __half2*>(&twice);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&p[r][j]), one);
+                  p[r][j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+              }
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(src + k * 64);
+              p[r][0] = u.x;
+              p[r][1] = u.y;
+              p[r][2] = u.z;
+              p[r][3] = u.w;
+            }
+          }
+          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
+          if constexpr (kW == kW4mx) {
+            float f[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              // 2^(byte - 127); 2^-127, which is no normal number, as 0
+              const uint32_t word = scale[2 * m + r][0];
+              f[r] = __uint_as_float((of == 3 ? word >> 1 : word << (23 - 8 * of)) & 0x7f800000u);
+            }
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+              const float zero[4] = {};
+              float d[4], d2[4];
+              // (one after the other in the same sum: a third more time)
+              mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
+              mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, zero);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                acc[m][n][j] = fmaf(d2[j], f[j >> 1], fmaf(d[j], f[j >> 1], acc[m][n][j]));
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) {
+              mma_16bit<kBf16>(acc[m][n], a0, b[n].x, b[n].y, acc[m][n]);
+              mma_16bit<kBf16>(acc[m][n], a1, b[n].z, b[n].w, acc[m][n]);
+            }
+          }
+        }
+      };
+      static_assert(W::kGroups % 4 == 0, "groups by fours");
+      // (Not all unrolled, and few forms of it: the instruction cache holds the producers' code as well.)
+#pragma unroll 1
+      for (int k = 0; k < W::kGroups; k += 4) {
+        if (W::k4) scales(k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) group(k + j, j);
+      }
+      if constexpr (kW == kW4mx) {
+#pragma unroll
+        for (int r = 0; r < 2 * kM; ++r)
+          if (nan[r]) {
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+              acc[r >> 1][n][2 * (r & 1)] = acc[r >> 1][n][2 * (r & 1) + 1] = __uint_as_float(0x7fffffffu);
+          }
+      }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&w_empty[stage]);
@@ -948,20 +994,59 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       named_barrier_sync(1, 32 * kMmaWarps);
       const int ticket = s_current;
       named_barrier_sync(1, 32 * kMmaWarps);      // read by all before it is written again
-      if (ticket >= 2 * n_blocks) break;
-      if (ticket < n_blocks) {
-        const int q0 = cut1(ticket), end = cut1(ticket + 1);
-        for (int q = q0; q < end;) {
-          const FewPart p = part1(q, end);
-          q += p.n;
-          const int n_chunks = (H + W::kChunk - 1) / W::kChunk;
+      if (ticket >= n_tickets) break;
+      const bool fc1 = ticket < n_first;
+      const Slice slice = slice1(fc1 ? ticket : 0);
+      const int from = fc1 ? 0 : cut2(ticket - n_first);
+      const int end = fc1 ? slice.size() : cut2(ticket - n_first + 1);
+      for (int at = from; at < end;) {
+        const FewPart p = fc1 ? part1(slice, at) : part2(at, end);
+        at += p.n;
+        // The team's stages: sub `sub` of every 4 / subs-th chunk, over all experts in the second products.
+        const int sub = team % p.subs;
+        const bool second = fc1 || p.of(sub) > 16;
+        float all[2][kNt][4];
+        clear(all);
+        int ck = 0;
+        for (int e = fc1 ? p.a : 0, last = fc1 ? p.a + 1 : n_all; e < last; ++e) {
+          const int K = fc1 ? H : inner(e);
+          const uint32_t tokens = sh.tokens[e];
+          // The column tiles that hold tokens of the expert.
+          const bool both = kNt == 2 && (tokens & 0xffu) && tokens > 0xffu;
+          const int tile = kNt == 2 && !(tokens & 0xffu) ? 1 : 0;
           float acc[2][kNt][4];
           clear(acc);
-          for (int i2 = team; i2 < n_chunks * p.subs; i2 += kTeams) {
-            const int ck = i2 / p.subs;
-            multiply(std::true_type{}, acc, i2, chunks + ck, min(W::kChunk, H - ck * W::kChunk), p.subs);
+#pragma unroll 1
+          for (int k0 = 0; k0 < K; k0 += W::kChunk, ++ck) {
+            if ((ck * p.subs + sub) % kTeams != team) continue;
+            const int i2 = ck * p.subs + sub, xc = chunks + ck;
+            using One = std::integral_constant<int, 1>;
+            using Two = std::integral_constant<int, 2>;
+            if constexpr (kNt == 2) {
+              if (both) {
+                multiply(Two{}, Two{}, acc, 0, i2, xc, p.subs);
+                continue;
+              }
+            }
+            if (second) multiply(Two{}, One{}, acc, tile, i2, xc, p.subs);
+            else multiply(One{}, One{}, acc, tile, i2, xc, p.subs);
           }
-          gather(acc, n_chunks * p.subs, n_chunks);
+          // Sums of the expert's tokens only (in the first products, all: the rest is dropped below).
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (!(tokens >> (n * 8 + 2 * c + j) & 1u)) continue;
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                const float* v = kNt == 2 && both ? acc[m][n] : acc[m][0];
+                all[m][n][j] += v[j];
+                all[m][n][j + 2] += v[j + 2];
+              }
+            }
+        }
+        gather(all, ck * p.subs, ck);
+        if (fc1) {
           const bool own = p.a < n_exp;
           float g13 = 1.0f, g2 = 1.0f;
           if (kW == kW4nv) {
@@ -972,12 +1057,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             if (p2) g2 = __ldg(p2 + e);
           }
           for (int pos = tid; pos < p.subs * kNt * 128; pos += 32 * kMmaWarps) {
-            const int s = pos / (kNt * 128), n = pos / 128 % kNt, at = pos & 127, l = at >> 2, j = at & 3;
+            const int s = pos / (kNt * 128), n = pos / 128 % kNt, at_ = pos & 127, l = at_ >> 2, j = at_ & 3;
             const int row = (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
             const int sl = t < T ? sh.slot[p.a][t] : -1;
             if (sl < 0 || row >= p.of(s)) continue;
             const float f = sh.x_inv[t] * g13;
-            const float gate = sum_at(p.subs, s, 0, n, at) * f, up = sum_at(p.subs, s, 1, n, at) * f;
+            const float gate = sum_at(p.subs, s, 0, n, at_) * f, up = sum_at(p.subs, s, 1, n, at_) * f;
             const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
             const float ex = expf(-fabsf(gate));
             const float sig = (gate < 0.0f ? ex : 1.0f) / (1.0f + ex);
@@ -985,48 +1070,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             a.h[(static_cast<int64_t>(t) * (a.k + 1) + sl) * a.h_ld + p.at + s * p.per + row] = h;
             if (!kBf16) atomicMax(&sh.tmax[t], __float_as_uint(h) & 0x7fffffffu);
           }
-        }
-        // This slice's h, and the largest so far, before the count.
-        named_barrier_sync(1, 32 * kMmaWarps);
-        if (warp == 0 && end > q0) {
-          if (!kBf16 && lane < T) atomicMax(a.tmax + lane, sh.tmax[lane]);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) red_release_gpu_add(a.ticket + 1, end - q0);
-        }
-      } else {
-        for (int r = cut2(ticket - n_blocks), end = cut2(ticket - n_blocks + 1); r < end;) {
-          const FewPart p = part2(r, end);
-          r += p.n;
-          const int sub = team % p.subs;
-          const bool second = p.of(sub) > 16;
-          float acc[2][kNt][4], all[2][kNt][4];
-          clear(all);
-          int ck = 0;
-          for (int e = 0; e < n_all; ++e) {
-            const int K = inner(e);
-            const uint32_t tokens = sh.tokens[e];
-            clear(acc);
-            for (int k0 = 0; k0 < K; k0 += W::kChunk, ++ck) {
-              // (stage ck * subs + sub is this team's in every 4 / subs-th chunk)
-              if ((ck * p.subs + sub) % kTeams != team) continue;
-              const int len = min(W::kChunk, K - k0);
-              if (second) multiply(std::true_type{}, acc, ck * p.subs + sub, chunks + ck, len, p.subs);
-              else multiply(std::false_type{}, acc, ck * p.subs + sub, chunks + ck, len, p.subs);
-            }
-#pragma unroll
-            for (int n = 0; n < kNt; ++n)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!(tokens >> (n * 8 + 2 * c + j) & 1u)) continue;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  all[m][n][j] += acc[m][n][j];
-                  all[m][n][j + 2] += acc[m][n][j + 2];
-                }
-              }
-          }
-          gather(all, ck * p.subs, ck);
+        } else {
           if (!waited) {
             // (h came through the tokens' warps, which waited for all of it)
             waited = true;
@@ -1034,15 +1078,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
           }
           for (int pos = tid; pos < p.subs * 2 * kNt * 128; pos += 32 * kMmaWarps) {
             const int s = pos / (2 * kNt * 128), m = pos / (kNt * 128) % 2, n = pos / 128 % kNt;
-            const int at = pos & 127, l = at >> 2, j = at & 3;
+            const int at_ = pos & 127, l = at_ >> 2, j = at_ & 3;
             const int row = m * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
             const float inv = __shfl_sync(0xffffffffu, y_inv, t);   // (a warp's positions come and go together)
             if (t >= T || row >= p.of(s)) continue;
-            const float v = sum_at(p.subs, s, m, n, at) * inv;
+            const float v = sum_at(p.subs, s, m, n, at_) * inv;
             const int64_t to = static_cast<int64_t>(t) * H + p.at + s * p.per + row;
             if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
             else static_cast<__half*>(a.y)[to] = __float2half_rn(v);
           }
+        }
+      }
+      if (fc1) {
+        // This slice's h, and the largest so far, before the count (a release covers what the block's other
+        // threads wrote before the barrier).
+        named_barrier_sync(1, 32 * kMmaWarps);
+        if (warp == 0 && end > from) {
+          if (!kBf16 && lane < T) atomicMax(a.tmax + lane, sh.tmax[lane]);
+          __syncwarp();
+          if (lane == 0) red_release_gpu_add(a.ticket + 1, end - from);
         }
       }
     }
