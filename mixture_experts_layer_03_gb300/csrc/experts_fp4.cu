@@ -39,25 +39,37 @@ namespace moe {
 namespace {
 
 constexpr int kQBK = 256;                      // contraction elements a block: 128 bytes
-constexpr int kQMost = 224;                    // rows of a tile
-constexpr int kQStages = 4;
-constexpr int kQSlotBytes = 128 * 128;         // codes of one operand of one block in one CTA
 constexpr int kQAtom = 512;                    // scales of 128 rows by 4 bytes
-constexpr int kQScaleBytes = 4 * kQAtom + 8 * kQAtom;   // of A, then of B (two atoms a word)
-constexpr int kQRawBytes = 3 * 128 * 16;       // scales as they lie: A's 128 rows, B's 2 x 128
-constexpr int kQStageBytes = 2 * kQSlotBytes + kQScaleBytes + kQRawBytes;
+constexpr int kQSlotA = 128 * 128;             // codes of the weights of one block in one CTA
+
+// Wide tiles: up to 224 rows. Narrow ones, for launches of few rows an expert: up to 64, with more blocks
+// of weights under way instead.
+template <bool kWide>
+struct QTile {
+  static constexpr int kMost = kWide ? 224 : 64;                 // rows of a tile
+  static constexpr int kStages = kWide ? 4 : 6;
+  static constexpr int kSlotB = (kWide ? 128 : 32) * 128;        // codes of half of the rows
+  static constexpr int kAtomsB = kWide ? 2 : 1;                  // of 128 rows, a word of scales
+  static constexpr int kScaleBytes = 4 * (1 + kAtomsB) * kQAtom; // of A, then of B
+  static constexpr int kRawBytes = (kWide ? 3 : 2) * 128 * 16;   // scales as they lie: A's 128 rows, B's
+  static constexpr int kStage = kQSlotA + kSlotB + kScaleBytes + kRawBytes;
+};
 constexpr int kQScaleWarp = 2, kQScaleWarps = 4, kQScaleTeams = 2;   // a stage each in turn
 constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps * kQScaleTeams, kQEpiWarps = 8;
 constexpr int kQWarpX = kQEpiWarp + kQEpiWarps;   // the producer of the rows
 constexpr int kQThreads = 32 * (kQWarpX + 1);
 constexpr int kQBoxBytes = 4096;               // epilogue staging of a warp
-constexpr int kQSmemBytes = 1024 + kQStages * kQStageBytes + kQEpiWarps * kQBoxBytes;
+template <bool kWide>
+constexpr int kQSmemBytes = 1024 + QTile<kWide>::kStages * QTile<kWide>::kStage + kQEpiWarps * kQBoxBytes;
+static_assert(kQSmemBytes<true> <= 232448 - 2048 && kQSmemBytes<false> <= 232448 - 2048, "shared memory");
 constexpr int kQTmemCols = 512;
-constexpr int kQAccCols = kQMost;
+constexpr int kQAccCols = QTile<true>::kMost;
 constexpr int kQColsA = 2 * kQAccCols, kQColsB = kQColsA + 16;   // scales' TMEM columns
 static_assert(kQColsB + 32 <= kQTmemCols, "TMEM");
-static_assert(kQScaleTeams == 2 && kQStages % 2 == 0, "stages of the scale teams");
+static_assert(kQScaleTeams == 2 && QTile<true>::kStages % 2 == 0 && QTile<false>::kStages % 2 == 0,
+              "stages of the scale teams");
 constexpr uint16_t kQPairMask = 0x3;
+constexpr int kQNarrowRows = 32;
 
 struct Fp4Args {
   ExpertsArgs e;
@@ -115,12 +127,14 @@ __device__ __forceinline__ uint32_t idesc_fp4(int N) {
          (static_cast<uint32_t>(256 >> 4) << 24);
 }
 
-template <bool kNv>
+template <bool kNv, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
 experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const __grid_constant__ CUtensorMap map_x32,
                    const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
                    const __grid_constant__ CUtensorMap map_out, Fp4Args q) {
+  using Q = QTile<kWide>;
+  constexpr int kQStages = Q::kStages, kQMost = Q::kMost;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[kQStages], raw_bar[kQStages], scale_bar[kQStages], empty_bar[kQStages];
   __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
@@ -136,10 +150,10 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   const bool lead = rank == 0;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-  uint8_t* sB = sA + kQStages * kQSlotBytes;
-  uint8_t* sS = sB + kQStages * kQSlotBytes;
-  uint8_t* sRaw = sS + kQStages * kQScaleBytes;
-  uint8_t* sOut = sRaw + kQStages * kQRawBytes;
+  uint8_t* sB = sA + kQStages * kQSlotA;
+  uint8_t* sS = sB + kQStages * Q::kSlotB;
+  uint8_t* sRaw = sS + kQStages * Q::kScaleBytes;
+  uint8_t* sOut = sRaw + kQStages * Q::kRawBytes;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -203,11 +217,12 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const Tile t = tile(idx);
       if (t.nkb == 0) continue;
       const int half = t.n >> 1;
-      const bool narrow = half <= 64;
+      // (narrow tiles: half is 32 at most)
+      const bool narrow = !kWide || half <= 64;
       const int box = narrow ? 32 : 128;
-      const bool two = half > box;
+      const bool two = kWide && half > box;
       const CUtensorMap* mx = narrow ? &map_x32 : &map_x;
-      const uint32_t tx = weights ? kQSlotBytes * ((t.m_here > 0) + (t.m_peer > 0)) : 2 * (two ? 2 : 1) * box * 128;
+      const uint32_t tx = weights ? kQSlotA * ((t.m_here > 0) + (t.m_peer > 0)) : 2 * (two ? 2 : 1) * box * 128;
       const int n0 = t.n0 + rank * half;
       for (int kb = 0; kb < nkb; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
@@ -215,18 +230,18 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         if (elect_one()) {
           if (lead) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const uint32_t fb = lead_full + 8u * stage;
-          uint8_t* bs = sB + stage * kQSlotBytes;
-          uint8_t* raw_s = sRaw + stage * kQRawBytes;
+          uint8_t* bs = sB + stage * Q::kSlotB;
+          uint8_t* raw_s = sRaw + stage * Q::kRawBytes;
           const int at = kNv ? kb * 16 : (kb >> 1) * 16;   // (mx: this block's half of it is kb's lowest bit)
           if (weights) {
             mbar_arrive_expect_tx(&raw_bar[stage], 128 * 16);
             tma_load_3d(raw_s, &map_ws, &raw_bar[stage], at, t.m0, t.g);
             if (t.m_here > 0)
-              tma_load_3d_pair(sA + stage * kQSlotBytes, &map_w, fb, kb * 128, t.m0, t.g);
+              tma_load_3d_pair(sA + stage * kQSlotA, &map_w, fb, kb * 128, t.m0, t.g);
           } else {
-            mbar_arrive_expect_tx(&raw_bar[stage], (t.n > 128 ? 2 : 1) * 128 * 16);
+            mbar_arrive_expect_tx(&raw_bar[stage], (kWide && t.n > 128 ? 2 : 1) * 128 * 16);
             tma_load_2d(raw_s + 128 * 16, &map_xs, &raw_bar[stage], at, t.n0);
-            if (t.n > 128) tma_load_2d(raw_s + 256 * 16, &map_xs, &raw_bar[stage], at, t.n0 + 128);
+            if (kWide && t.n > 128) tma_load_2d(raw_s + 256 * 16, &map_xs, &raw_bar[stage], at, t.n0 + 128);
             tma_load_2d_pair(bs, mx, fb, kb * 128, n0);
             if (two) tma_load_2d_pair(bs + 32 * 128, mx, fb, kb * 128, n0 + 32);
           }
@@ -264,20 +279,20 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], ~(acc_phase >> acc) & 1u, abort));
         if (ok) tc_fence_after();
         const uint32_t idesc = idesc_fp4<kNv>(t.n), d = tmem_base + acc * kQAccCols;
-        const bool wide = t.n > 128;
+        const bool wide = kWide && t.n > 128;
         for (int ks = 0; ok && ks < nks; ks += 4) {
           ok = __all_sync(0xffffffffu, mbar_wait<true>(&full_bar[stage], phase, abort) &&
                                            mbar_wait<true>(&scale_bar[stage], phase, abort));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t da = da0 + ((stage * kQSlotBytes) >> 4), db = db0 + ((stage * kQSlotBytes) >> 4);
-          const uint64_t ds = ds0 + ((stage * kQScaleBytes) >> 4);
+          const uint64_t da = da0 + ((stage * kQSlotA) >> 4), db = db0 + ((stage * Q::kSlotB) >> 4);
+          const uint64_t ds = ds0 + ((stage * Q::kScaleBytes) >> 4);
           if (elect_one()) {
             constexpr int kWords = kNv ? 4 : 2;   // of scales in a block
 #pragma unroll
             for (int j = 0; j < kWords; ++j) {
               tmem_copy_scales_pair(sfa + 4 * j, ds + ((j * kQAtom) >> 4));
-              tmem_copy_scales_pair(sfb + 8 * j, ds + (((4 + 2 * j) * kQAtom) >> 4));
+              tmem_copy_scales_pair(sfb + 8 * j, ds + (((4 + Q::kAtomsB * j) * kQAtom) >> 4));
               if (wide) tmem_copy_scales_pair(sfb + 8 * j + 4, ds + (((5 + 2 * j) * kQAtom) >> 4));
             }
 #pragma unroll
@@ -375,7 +390,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     for (int idx = first; idx < total && ok; idx += step) {
       const Tile t = tile(idx);
       if (t.nkb == 0) continue;
-      const bool wide = t.n > 128;
+      const bool wide = kWide && t.n > 128;
       for (int kb = 0; kb < nkb; ++kb) {
         // (kQStages is even: a stage is always the same team's. Its place has been given back before its
         // scales were asked for.)
@@ -388,14 +403,14 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         }
         ok = __all_sync(0xffffffffu, mbar_wait(&raw_bar[stage], phase, abort));
         if (!ok) break;
-        const uint8_t* raw_s = sRaw + stage * kQRawBytes;
-        uint8_t* dst = sS + stage * kQScaleBytes + l * 16;
+        const uint8_t* raw_s = sRaw + stage * Q::kRawBytes;
+        uint8_t* dst = sS + stage * Q::kScaleBytes + l * 16;
         const uint4 va = turn(words(raw_s, kb)), vb = turn(words(raw_s + 128 * 16, kb));
         uint4 vc = {};
         if (wide) vc = turn(words(raw_s + 256 * 16, kb));
         if (i < kWords) {
           *reinterpret_cast<uint4*>(dst + i * kQAtom) = va;
-          *reinterpret_cast<uint4*>(dst + (4 + 2 * i) * kQAtom) = vb;
+          *reinterpret_cast<uint4*>(dst + (4 + Q::kAtomsB * i) * kQAtom) = vb;
           if (wide) *reinterpret_cast<uint4*>(dst + (5 + 2 * i) * kQAtom) = vc;
         }
         // What reads these is this SM's own tensor core, whichever CTA's thread issues the copy: the proxy
@@ -534,7 +549,7 @@ bool encode_bytes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kNv>
+template <bool kNv, bool kWide>
 moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mx32,
                       const CUtensorMap& mws, const CUtensorMap& mxs, const CUtensorMap& mo, const Fp4Args& q, int64_t tiles, cudaStream_t s) {
   static std::atomic<int> clusters_dev[64];
@@ -544,16 +559,16 @@ moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   int have = clusters_dev[dev].load(std::memory_order_acquire);
   if (!have) {
     const cudaError_t e = cudaFuncSetAttribute(
-        experts_fp4_kernel<kNv>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmemBytes);
+        experts_fp4_kernel<kNv, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmemBytes<kWide>);
     if (e != cudaSuccess)
       return set_error(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int sms = device_sm_count();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
     cfg.blockDim = dim3(kQThreads, 1, 1);
-    cfg.dynamicSmemBytes = kQSmemBytes;
+    cfg.dynamicSmemBytes = kQSmemBytes<kWide>;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, experts_fp4_kernel<kNv>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, experts_fp4_kernel<kNv, kWide>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();   // clear the failed query; fall back to one cluster per SM pair
       n = sms / 2;
     }
@@ -561,8 +576,8 @@ moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
     have = n;
   }
   const unsigned pairs = static_cast<unsigned>(have < tiles ? have : tiles);
-  const cudaError_t err = launch_pdl(experts_fp4_kernel<kNv>, dim3(2 * pairs), dim3(kQThreads),
-                                     kQSmemBytes, s, mw, mx, mx32, mws, mxs, mo, q);
+  const cudaError_t err = launch_pdl(experts_fp4_kernel<kNv, kWide>, dim3(2 * pairs), dim3(kQThreads),
+                                     kQSmemBytes<kWide>, s, mw, mx, mx32, mws, mxs, mo, q);
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_fp4 launch: %s", cudaGetErrorString(err));
   return MOE_OK;
@@ -605,9 +620,14 @@ moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const in
   q.x_g = x.g;
   q.w_g = w.g;
   q.blocks = K / fp4_block(fmt);
-  const int64_t tiles = (R / kQMost + E + 2) * ((N + 255) / 256);
-  return fmt == kFp4Nv ? launch_fp4<true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s)
-                       : launch_fp4<false>(mw, mx, mx32, mws, mxs, mo, q, tiles, s);
+  // Wide tiles where the experts have more than 32 rows on average. (N)
+  const bool wide = R > static_cast<int64_t>(kQNarrowRows) * E;
+  const int64_t tiles = (R / (wide ? QTile<true>::kMost : QTile<false>::kMost) + E + 2) * ((N + 255) / 256);
+  if (wide)
+    return fmt == kFp4Nv ? launch_fp4<true, true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s)
+                         : launch_fp4<false, true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s);
+  return fmt == kFp4Nv ? launch_fp4<true, false>(mw, mx, mx32, mws, mxs, mo, q, tiles, s)
+                       : launch_fp4<false, false>(mw, mx, mx32, mws, mxs, mo, q, tiles, s);
 }
 
 }  // namespace moe
