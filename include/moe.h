@@ -425,10 +425,11 @@ moe_status moe_experts_matmul_dw(const void* dy, const void* x, const int32_t* o
                                  moe_dtype dw_dtype, int32_t accumulate, void* dw, void* workspace,
                                  size_t ws_bytes, void* stream);
 
-/* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products (above, or on
- * 4-bit operands), of the gate or of moe_layer_few ran out in any call on the current GPU, with a workspace or without, since the last read.
- * Such a call's results are incomplete. *flags (may be NULL) receives MOE_DEVICE_FLAG_TIMEOUT or 0.
- * Returns MOE_ERR_DEVICE_TIMEOUT when one did, else MOE_OK. */
+/* Synchronises `stream`; reads and clears whether a bounded wait of the experts' products (above,
+ * or on 4-bit operands), of the gate or of moe_layer_few ran out in any call on the current GPU,
+ * with a workspace or without, since the last read. Such a call's results are incomplete. *flags
+ * (may be NULL) receives MOE_DEVICE_FLAG_TIMEOUT or 0. Returns MOE_ERR_DEVICE_TIMEOUT when one did,
+ * else MOE_OK. */
 moe_status moe_read_timeouts(void* stream, int32_t* flags);
 
 /* Self-test of that report, with no fault and no hang: one warp waits as the products do, without a
@@ -496,9 +497,11 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
  *            f32 an expert (one for the shared expert's) or NULL
  * Writes y [T, H], ids int32 [T, k] and scales fp32 [T, k]. Between the products h, times its routing
  * weight, is rounded once: to bf16, or (f16 and 4-bit weights) to 11 bits beside its token's largest.
- * x and wg are not rounded, sums are fp32. Experts that no token chose are not read. The results are the
- * same on every run. Workspace: moe_layer_few_workspace_bytes, 256-byte aligned, nothing of it has to be
- * set; calls that share one must be ordered. Whether a bounded wait ran out: moe_read_timeouts. */
+ * x and wg are not rounded (with 4-bit weights, what of x is less than 2^-29 of its token's largest is
+ * rounded to steps of at most 2^-38 of that, and an MX scale of 2^-127 counts as 0), sums are fp32.
+ * Experts that no token chose are not read. The results are the same on every run. Workspace:
+ * moe_layer_few_workspace_bytes, 256-byte aligned, nothing of it has to be set; calls that share one
+ * must be ordered. Whether a bounded wait ran out: moe_read_timeouts. */
 #define MOE_FEW_TOKENS 16
 #define MOE_WEIGHTS_16BIT (-1)
 typedef struct {

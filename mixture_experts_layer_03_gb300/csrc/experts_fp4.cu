@@ -12,13 +12,19 @@
 // (row 32 i + l in lane l, column i), which tcgen05.cp writes from 512 bytes of shared memory, row l of
 // 16 bytes holding rows l, l + 32, l + 64, l + 96. A row's scales lie along the contraction in memory: they
 // come by TMA as they lie, 16 bytes a row (mx: for two blocks), and four warps turn 4 x 4 words over
-// between four lanes by shuffles and write 16 bytes a lane. (Read from memory by those warps, they came
-// one latency after the other: the fence that shows them to the tensor cores waits for the loads under
-// way. N us for N.) Each CTA needs the scales of its 128 channels and of all of the tile's rows (the pair
-// shares the rows' codes, but each tensor core scales its own half of D). Bytes past the row's K / block
-// are zeros, whatever fills the row up; codes past K are TMA's zeros.
+// between four lanes by shuffles and write 16 bytes a lane. (Read from memory by those warps themselves:
+// 8192 x 28672 x 4096 over 8 experts 1575 us, by TMA 1148, both with the arrivals' release to the other
+// SM; without that 507.) Each CTA needs the scales of its 128 channels and of all of the tile's rows (the
+// pair shares the rows' codes, but each tensor core scales its own half of D). Bytes past the row's
+// K / block are zeros, whatever fills the row up; codes past K are TMA's zeros.
 // TMEM: two accumulators of 224 columns, 48 columns of scales (nv: 4 x 4 for A, 4 x 8 for B), written
 // anew for every block: copies and products are issued by one thread and run in that order.
+//
+// Measured (one GB300, back to back): 8192 rows over 8 experts, N = 28672, K = 4096, nv, 425 us, 4.5
+// PFLOP/s, 2.4 times cuBLAS's bf16 rate: 880 cycles a block of 256 x 208 x 256, for 43% of which the tensor
+// pipe is active; what feeds it bounds it (L2 at 48%, the scales' way 650 cycles for each of two teams).
+// 512 rows over 128 experts, N = 1536, K = 2048, nv, 43 us and 4096 rows over 256 experts, N = 7168,
+// K = 2048, mx, 361 to 376 us: 5.2 and 5.6 TB/s, bound by memory.
 //
 // Warp roles (608 threads per CTA): warps 0 and 18 TMA producers of the weights and of the rows, warp 1 TMEM
 // allocator and, in the first CTA, MMA issuer, warps 2-9 scales, in two teams that take a block each in
@@ -69,7 +75,7 @@ static_assert(kQColsB + 32 <= kQTmemCols, "TMEM");
 static_assert(kQScaleTeams == 2 && QTile<true>::kStages % 2 == 0 && QTile<false>::kStages % 2 == 0,
               "stages of the scale teams");
 constexpr uint16_t kQPairMask = 0x3;
-constexpr int kQNarrowRows = 32;
+constexpr int kQNarrowRows = 48;
 
 struct Fp4Args {
   ExpertsArgs e;
@@ -620,7 +626,10 @@ moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const in
   q.x_g = x.g;
   q.w_g = w.g;
   q.blocks = K / fp4_block(fmt);
-  // Wide tiles where the experts have more than 32 rows on average. (N)
+  // Wide tiles where the experts have more than 48 rows on average: N = 7168, K = 2048, mx, 256 experts of
+  // 8, 32, 48, 64, 96 rows: narrow 418, 341, 343, 460, 602 us, wide 442, 373, 372, 376, 390; N = 1536, nv,
+  // 128 experts of 32, 64 rows: narrow 44, 56, wide 48, 50 (experts of more than 64 rows read their weights
+  // again for every narrow tile).
   const bool wide = R > static_cast<int64_t>(kQNarrowRows) * E;
   const int64_t tiles = (R / (wide ? QTile<true>::kMost : QTile<false>::kMost) + E + 2) * ((N + 255) / 256);
   if (wide)

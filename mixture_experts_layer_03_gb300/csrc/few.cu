@@ -1139,7 +1139,7 @@ cudaError_t launch_gate_t(const FewArgs& a, const void* wg, bool want_amax, cuda
 
 // Blocks for about one wave, each of few rows and tokens: x and wg come from L2 again for every block, and a
 // block that has all 16 tokens waits for them one after the other (16 tokens, 256 x 7168: 14 us with two
-// rows by all tokens, N with four by four).
+// rows by all tokens, 7 with four by four).
 template <typename T>
 cudaError_t launch_gate_tokens(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
   const bool many = a.E + a.shared_gate > device_sm_count();

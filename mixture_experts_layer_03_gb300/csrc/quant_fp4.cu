@@ -15,7 +15,11 @@
 // 8-bit mantissas is often a tie but for g's rounding); for SwiGLU, a few times in a million, the
 // segment is worked out again in pairs of f32 (2^-26), and where that does not do either, in 64 bits.
 //
-// Every value is read and written once; bound by memory: 4.56 bits out for 16 in, or for 32.
+// Every value is read and written once, 4.25 or 4.5 bits out for 16 in, or for 32 (SwiGLU). Measured, bf16:
+// SwiGLU of 8192 x 14336 to mx 109 us (532 MB at 4.9 TB/s; bound by instructions, 270 a warp and 256
+// channels, of which the two codes and their comparison are a fifth), back to values 56 us (297 MB at 5.3
+// TB/s); 8192 x 7168 to nv and back 89 us. Without the certified decisions, all in 64 bits where f32 was
+// in doubt: 8192 x 7168 to nv 1.06 ms (ties are common there), SwiGLU of 512 x 768 to nv 15 us, so 3.
 #include <cstdint>
 
 #include <cuda_fp8.h>
@@ -335,7 +339,8 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
 }
 
 // Four times 8 channels a lane, loaded before the first is worked on: 4 bytes of codes a lane are little to
-// have under way. (16 channels side by side a lane leave stores of half sectors: N us for N.)
+// have under way. (8192 x 14336, mx to bf16: 56 us; with one load
+// a lane 64; with 16 channels side by side a lane, whose stores leave half of their sectors to the next, 73.)
 template <typename T, bool kNv>
 __global__ void __launch_bounds__(kSegmentThreads)
 dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
