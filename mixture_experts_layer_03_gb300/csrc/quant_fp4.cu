@@ -39,6 +39,9 @@ namespace {
 constexpr float kNearQuotient = 0x1p-21f;
 constexpr float kNearSwiglu = 1e-6f, kNearGate = 1.5e-7f;
 constexpr float kNearPairs = 0x1p-26f;
+// These hold where no product on the way leaves f32's normal numbers by much: for gates from kLeastGate on
+// (or 0) and results from kLeastValue on, as blocks' largest. (bf16's 8 bits survive sigma of a smaller gate.)
+constexpr float kLeastGate = 0x1p-100f, kLeastValue = 0x1p-90f;
 
 struct Fp4Out {
   uint8_t* codes;       // [R, K / 2]
@@ -178,7 +181,8 @@ __device__ __forceinline__ uint32_t fp4_swiglu_pairs(const float (&v)[8], const 
     const Pair y = pair_mul(pair_mul(s, v[i]), u[i]);
     h[i] = y.hi;
     l[i] = y.lo;
-    doubt |= !(a <= 80.0f) || !(fabsf(y.hi) < 0x1p90f) || (y.hi != 0.0f && fabsf(y.hi) < 0x1p-90f);
+    doubt |= !(a <= 80.0f) || (a > 0.0f && a < kLeastGate) || !(fabsf(y.hi) < 0x1p90f) ||
+             (y.hi != 0.0f && fabsf(y.hi) < kLeastValue);
   }
   const uint32_t codes = decide<kNv, true>(h, l, g, *byte, doubt);
   *near = doubt;
@@ -298,13 +302,18 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
       gates = lanes_max<kLanes>(gates);
       finite = amax < INFINITY;
       // A gate below -80: sigma leaves f32's range.
-      bool near = gates > 80.0f || (kNv && !(6.0f * g > 0x1p-90f && 6.0f * g < 0x1p90f));
+      bool near = gates > 80.0f || (kNv && !(6.0f * g > 0x1p-90f && 6.0f * g < 0x1p90f)) ||
+                  (amax > 0.0f && amax < kLeastValue);
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) near |= v[i] != 0.0f && fabsf(v[i]) < kLeastGate;
+      }
       const float by = fmaf(gates, kNearGate, kNearSwiglu);
       float inv;
       if constexpr (kNv) {
         const float r = __fdividef(amax, 6.0f * g);
         byte = nv_byte(r * (1.0f - by));
-        near |= byte != nv_byte(r * (1.0f + by)) || (amax > 0.0f && !(amax > 0x1p-90f && amax < 0x1p90f));
+        near |= byte != nv_byte(r * (1.0f + by)) || amax >= 0x1p90f;
         inv = byte == 0 ? 0.0f : __fdividef(1.0f, nv_scale(byte) * g);
       } else {
         byte = mx_byte(amax * (1.0f - by));
