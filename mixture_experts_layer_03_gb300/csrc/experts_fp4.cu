@@ -557,7 +557,8 @@ bool encode_bytes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t ro
 
 template <bool kNv, bool kWide>
 moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mx32,
-                      const CUtensorMap& mws, const CUtensorMap& mxs, const CUtensorMap& mo, const Fp4Args& q, int64_t tiles, cudaStream_t s) {
+                      const CUtensorMap& mws, const CUtensorMap& mxs, const CUtensorMap& mo,
+                      const Fp4Args& q, int64_t tiles, cudaStream_t s) {
   static std::atomic<int> clusters_dev[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)

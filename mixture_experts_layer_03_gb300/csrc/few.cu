@@ -4,16 +4,16 @@
 //                     sum:  y[t] = sum over slots j of s[t, j] w2[e] (silu(g) u),  g, u = w13[e] x[t]
 // For a few tokens the layer reads each chosen expert's weights once and little else: the floor is
 // their bytes at the memory's rate, and what is added to it is latency, between kernels and between the
-// two products. So one block an SM stays for the whole layer, and two warps of it (the weights'
+// two products. So one block an SM stays for the whole layer, and four warps of it (the weights'
 // producers) keep its ring full from the moment the experts are known, on into the second products'
 // weights while the first products' results are still awaited.
 //
 // Work. The first tickets are slices of the first products: the chosen experts' I channels one after the
 // other (a channel is its gate and its up row), and the shared expert's, each cut into equal parts to
 // a channel, one a block. The others are slices of the H rows of the second products, over all experts,
-// one a block. A block takes tickets
-// in order until none is left; a slice of the second products waits for the first ones' results, which
-// are in blocks that run already, so that blocks that are not resident yet are waited for by nobody.
+// one a block. A block takes tickets in order until none is left; a slice of the second products waits for
+// the first ones' results, which are in blocks that run already, so that blocks that are not resident yet
+// are waited for by nobody.
 // Every element of h and of y is summed by one block in one order: the same result on every run.
 //
 // Products by mma.sync m16n8k16: 16 rows of weights by 8 tokens, so that one pass over a weight serves all
@@ -337,7 +337,8 @@ __device__ __noinline__ void few_select(const float* row, const FewArgs& a, int 
 
 // The weights of block_pair_weights (route_device.cuh) for the methods whose slots are in order already, in
 // pairs, for one rounding at the end; by one thread a slot. (In fp64, which runs at 1/64 of fp32's rate,
-// the exponentials and divisions of 128 slots took every block 10 us.) False, in every thread: a logit is so far off that fp32's range may not do.
+// the exponentials and divisions of 128 slots took every block 10 us.) False, in every thread: a logit is
+// so far off that fp32's range may not do.
 __device__ __forceinline__ bool few_weights(const FewArgs& a, FewShared* sh) {
   const int p = threadIdx.x, pairs = a.T * a.k, method = a.route.method;
   const bool sigmoid = method != MOE_ROUTE_DEFAULT && method != MOE_ROUTE_RENORMALIZE &&
@@ -826,8 +827,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     if (!ok) few_timeout(abort);
   } else {
     // ------------------------------------------------------------ products
-    // A wait that runs out leaves the loops' course as it is (the warps meet at barriers): what is
-    // computed after it is garbage that the host hears of.
+    // A wait that runs out leaves the loops' course as it is (the warps meet at barriers), without further
+    // waits: what is computed after it is garbage that the host hears of.
     bool ok = true;
     const int g = lane >> 2, c = lane & 3;         // of the fragments
     const int team = warp / kTeamWarps, member = warp % kTeamWarps;
@@ -849,8 +850,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
                          c * (W::k4 ? 4 : 16);
       const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
                           member * W::kGroups * (kW == kW4nv ? 2 : 1);
-      ok = few_wait(&x_full[xs], x_phase, abort) && ok;
-      ok = few_wait(&w_full[stage], phase, abort) && ok;
+      ok = ok && few_wait(&x_full[xs], x_phase, abort) && few_wait(&w_full[stage], phase, abort);
       // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
       uint32_t scale[2 * kM][2] = {}, nan[2 * kM] = {};
       auto scales = [&](int k0) {
@@ -1143,8 +1143,10 @@ cudaError_t launch_gate_t(const FewArgs& a, const void* wg, bool want_amax, cuda
 template <typename T>
 cudaError_t launch_gate_tokens(const FewArgs& a, const void* wg, bool want_amax, cudaStream_t s) {
   const bool many = a.E + a.shared_gate > device_sm_count();
-  if (a.T == 1) return many ? launch_gate_t<T, 1, 2>(a, wg, want_amax, s) : launch_gate_t<T, 1, 1>(a, wg, want_amax, s);
-  if (a.T <= 4) return many ? launch_gate_t<T, 4, 2>(a, wg, want_amax, s) : launch_gate_t<T, 4, 1>(a, wg, want_amax, s);
+  if (a.T == 1)
+    return many ? launch_gate_t<T, 1, 2>(a, wg, want_amax, s) : launch_gate_t<T, 1, 1>(a, wg, want_amax, s);
+  if (a.T <= 4)
+    return many ? launch_gate_t<T, 4, 2>(a, wg, want_amax, s) : launch_gate_t<T, 4, 1>(a, wg, want_amax, s);
   return launch_gate_t<T, 4, 4>(a, wg, want_amax, s);
 }
 

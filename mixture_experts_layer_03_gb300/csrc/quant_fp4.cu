@@ -33,7 +33,7 @@ namespace moe {
 namespace {
 
 // Relative widths around a value in which its f32 form may be. A quotient: the divisor's rounding and the
-// reciprocal's, the product's and that of the factor 1 -+ kNear, 2.5 units of 2^-23. SwiGLU (16-bit and
+// reciprocal's (2), the product's and that of the factor 1 -+ kNear, 3.5 units of 2^-23. SwiGLU (16-bit and
 // f32 rows alike, by the fast exponential and quotient): 2 + 1.17 |gate| units of the exponential, 2 of
 // the quotient, 1 of the products, then the quotient's. SwiGLU in pairs: under 2^-27.
 constexpr float kNearQuotient = 0x1p-21f;
@@ -57,6 +57,13 @@ __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
   for (int d = 1; d < kLanes; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   return __uint_as_float(m);
+}
+
+// 1 / x to 2^-23, 0 past f32's normal numbers.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // The least e >= -127 with amax <= 6 * 2^e = 1.5 * 2^(e + 2), as a byte; finite amax.
@@ -89,27 +96,31 @@ __device__ __forceinline__ bool above(Pair v, float a, float b, bool tie, bool& 
   }
 }
 
-// The byte of a block and the codes of a lane's 8 values h (+ l, in pairs) of it. `near`: f32 does not
-// decide.
+// The byte of a block, its largest |value| and the codes of a lane's 8 values h (+ l, in pairs) of it.
+// `near`: f32 does not decide.
 template <bool kNv, bool kPairs>
 __device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)[8], float g, uint32_t& byte,
-                                           bool& near) {
+                                           float& amax, bool& near) {
   constexpr int kLanes = kNv ? 2 : 4;   // to a block
   Pair top{0.0f, 0.0f};
+  if constexpr (kPairs) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(h[i]), b = kPairs ? (signbit(h[i]) ? -l[i] : l[i]) : 0.0f;
-    if (!(a < top.hi) && !(a == top.hi && b <= top.lo)) top = Pair{a, b};   // (a NaN stays)
-  }
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(h[i]), b = signbit(h[i]) ? -l[i] : l[i];
+      if (!(a < top.hi) && !(a == top.hi && b <= top.lo)) top = Pair{a, b};
+    }
 #pragma unroll
-  for (int d = 1; d < kLanes; d *= 2) {
-    const float a = __shfl_xor_sync(0xffffffffu, top.hi, d);
-    const float b = kPairs ? __shfl_xor_sync(0xffffffffu, top.lo, d) : 0.0f;
-    // magnitudes order as their bit patterns do, infinities and NaNs on top
-    const uint32_t ua = __float_as_uint(a), ut = __float_as_uint(top.hi);
-    if (ua > ut || (ua == ut && b > top.lo)) top = Pair{a, b};
+    for (int d = 1; d < kLanes; d *= 2) {
+      const float a = __shfl_xor_sync(0xffffffffu, top.hi, d), b = __shfl_xor_sync(0xffffffffu, top.lo, d);
+      if (!(a < top.hi) && !(a == top.hi && b <= top.lo)) top = Pair{a, b};
+    }
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+    top.hi = lanes_max<kLanes>(__uint_as_float(m));
   }
-  const float amax = top.hi;
+  amax = top.hi;
   float inv, scale;
   if constexpr (kNv) {
     const float r = __fdividef(amax, 6.0f * g);
@@ -143,11 +154,11 @@ __device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)
     codes = fp4_codes8(z);
   } else {
     float lo[8], hi[8];
+    const float less = inv * (1.0f - kNearQuotient), more = inv * (1.0f + kNearQuotient);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float z = h[i] * inv;
-      lo[i] = z * (1.0f - kNearQuotient);
-      hi[i] = z * (1.0f + kNearQuotient);
+      lo[i] = h[i] * less;
+      hi[i] = h[i] * more;
     }
     codes = fp4_codes8(lo);
     uint32_t differ = codes ^ fp4_codes8(hi);
@@ -184,7 +195,8 @@ __device__ __forceinline__ uint32_t fp4_swiglu_pairs(const float (&v)[8], const 
     doubt |= !(a <= 80.0f) || (a > 0.0f && a < kLeastGate) || !(fabsf(y.hi) < 0x1p90f) ||
              (y.hi != 0.0f && fabsf(y.hi) < kLeastValue);
   }
-  const uint32_t codes = decide<kNv, true>(h, l, g, *byte, doubt);
+  float amax;
+  const uint32_t codes = decide<kNv, true>(h, l, g, *byte, amax, doubt);
   *near = doubt;
   return codes;
 }
@@ -279,12 +291,10 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
     uint32_t byte, codes;
     bool finite;
     if constexpr (!kSwiglu) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-      finite = lanes_max<kLanes>(__uint_as_float(top)) < INFINITY;
       bool near = false;
-      codes = decide<kNv, false>(v, v, g, byte, near);
+      float amax;
+      codes = decide<kNv, false>(v, v, g, byte, amax, near);
+      finite = amax < INFINITY;
       if (kNv && __any_sync(0xffffffffu, near && finite)) {
         const uint2 r = fp4_again<T, kNv, false>(src, K, in, finite, g);
         codes = r.x;
@@ -294,7 +304,7 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
       float h[kPerLane], amax = 0.0f, gates = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
-        h[i] = v[i] * __fdividef(1.0f, 1.0f + __expf(-v[i])) * u[i];
+        h[i] = v[i] * reciprocal(1.0f + __expf(-v[i])) * u[i];
         gates = fmaxf(gates, fabsf(v[i]));
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[i])));   // (a NaN stays)
       }

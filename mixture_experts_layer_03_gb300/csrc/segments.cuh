@@ -54,7 +54,8 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[kPerLane]) {
   }
 }
 
-// The work of a warp, one after the other: (row, segment) pairs, a segment 256 channels. Stepping (row, segment) by the grid's share keeps divisions out.
+// The work of a warp, one after the other: (row, segment) pairs, a segment 256 channels. Stepping (row,
+// segment) by the grid's share keeps divisions out.
 struct SegmentWalk {
   int64_t row;
   int seg;
