@@ -34,8 +34,8 @@ namespace {
 
 // Relative widths around a value in which its f32 form may be. A quotient: the divisor's rounding and the
 // reciprocal's (2), the product's and that of the factor 1 -+ kNear, 3.5 units of 2^-23. SwiGLU (16-bit and
-// f32 rows alike, by the fast exponential and quotient): 2 + 1.17 |gate| units of the exponential, 2 of
-// the quotient, 1 of the products, then the quotient's. SwiGLU in pairs: under 2^-27.
+// f32 rows alike): 2 + 0.75 |gate| units of the exponential (its argument's rounding and log2 e's), 1.5 of
+// the sum and its reciprocal, 1 of the products, then the quotient's. SwiGLU in pairs: under 2^-27.
 constexpr float kNearQuotient = 0x1p-21f;
 constexpr float kNearSwiglu = 1e-6f, kNearGate = 1.5e-7f;
 constexpr float kNearPairs = 0x1p-26f;
@@ -64,6 +64,38 @@ __device__ __forceinline__ float reciprocal(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// 2^x to 2^-22, 0 below f32's normal numbers.
+__device__ __forceinline__ float power_of_2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two products or sums an instruction.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float first(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float second(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 8 values times f.
+__device__ __forceinline__ void times8(const float (&v)[8], float f, float (&out)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t r = times(two(v[i], v[i + 1]), two(f, f));
+    out[i] = first(r);
+    out[i + 1] = second(r);
+  }
 }
 
 // The least e >= -127 with amax <= 6 * 2^e = 1.5 * 2^(e + 2), as a byte; finite amax.
@@ -149,17 +181,12 @@ __device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)
   uint32_t codes;
   if constexpr (!kNv && !kPairs) {
     float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = h[i] * inv;   // exact
+    times8(h, inv, z);   // exact
     codes = fp4_codes8(z);
   } else {
     float lo[8], hi[8];
-    const float less = inv * (1.0f - kNearQuotient), more = inv * (1.0f + kNearQuotient);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo[i] = h[i] * less;
-      hi[i] = h[i] * more;
-    }
+    times8(h, inv * (1.0f - kNearQuotient), lo);
+    times8(h, inv * (1.0f + kNearQuotient), hi);
     codes = fp4_codes8(lo);
     uint32_t differ = codes ^ fp4_codes8(hi);
     // hi's code is the next one up: its border, in quarters, is looked up.
@@ -302,9 +329,17 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
       }
     } else {
       float h[kPerLane], amax = 0.0f, gates = 0.0f;
+      constexpr float kMinusLog2E = -1.44269504f;
+#pragma unroll
+      for (int i = 0; i < kPerLane; i += 2) {
+        const uint64_t gate = two(v[i], v[i + 1]), x = times(gate, two(kMinusLog2E, kMinusLog2E));
+        const uint64_t d = plus(two(power_of_2(first(x)), power_of_2(second(x))), two(1.0f, 1.0f));
+        const uint64_t y = times(times(gate, two(reciprocal(first(d)), reciprocal(second(d)))), two(u[i], u[i + 1]));
+        h[i] = first(y);
+        h[i + 1] = second(y);
+      }
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) {
-        h[i] = v[i] * reciprocal(1.0f + __expf(-v[i])) * u[i];
         gates = fmaxf(gates, fabsf(v[i]));
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[i])));   // (a NaN stays)
       }
@@ -331,12 +366,8 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
         inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
       }
       float lo[kPerLane], hi[kPerLane];
-      const float less = inv * (1.0f - by), more = inv * (1.0f + by);
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        lo[i] = h[i] * less;
-        hi[i] = h[i] * more;
-      }
+      times8(h, inv * (1.0f - by), lo);
+      times8(h, inv * (1.0f + by), hi);
       codes = fp4_codes8(lo);
       near |= codes != fp4_codes8(hi);
       if (__any_sync(0xffffffffu, near && finite)) {
