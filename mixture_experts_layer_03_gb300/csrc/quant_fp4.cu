@@ -15,11 +15,12 @@
 // 8-bit mantissas is often a tie but for g's rounding); for SwiGLU, a few times in a million, the
 // segment is worked out again in pairs of f32 (2^-26), and where that does not do either, in 64 bits.
 //
-// Every value is read and written once, 4.25 or 4.5 bits out for 16 in, or for 32 (SwiGLU). Measured, bf16:
-// SwiGLU of 8192 x 14336 to mx 109 us (532 MB at 4.9 TB/s; bound by instructions, 270 a warp and 256
-// channels, of which the two codes and their comparison are a fifth), back to values 56 us (297 MB at 5.3
-// TB/s); 8192 x 7168 to nv and back 89 us. Without the certified decisions, all in 64 bits where f32 was
-// in doubt: 8192 x 7168 to nv 1.06 ms (ties are common there), SwiGLU of 512 x 768 to nv 15 us, so 3.
+// Every value is read and written once, 4.25 or 4.5 bits out for 16 in, or for 32 (SwiGLU). Bound by
+// instructions, hence lanes of 16 channels, two products an instruction, and a border only looked at where
+// two codes differ. Measured, bf16: SwiGLU of 8192 x 14336 to mx 91 us (532 MB at 5.8 TB/s; lanes of 8 109,
+// and with one product an instruction 120), to nv 106; 8192 x 7168 to mx 26, to nv 37 (lanes of 8: 32 and 51);
+// back, 8192 x 14336, 56. All in 64 bits where f32 is in doubt: 8192 x 7168 to nv 1.06 ms (ties are common
+// there), SwiGLU of 512 x 768 to nv 15 us, so 3.
 #include <cstdint>
 
 #include <cuda_fp8.h>
@@ -39,6 +40,11 @@ namespace {
 constexpr float kNearQuotient = 0x1p-21f;
 constexpr float kNearSwiglu = 1e-6f, kNearGate = 1.5e-7f;
 constexpr float kNearPairs = 0x1p-26f;
+// SwiGLU of fewer values goes by lanes of 8: a segment that has to be worked out again takes a lane of 16
+// twice as long, which shows where a warp has few segments. bf16, K = 2048, mx, 512, 2048, 4096, 8192 rows:
+// lanes of 8 4.3, 8.2, 13.4, 20.6 us, of 16 5.5, 9.1, 13.0, 20.9; 8192 x 14336 109 and 93, nv 136 and 106.
+// (f32, whose values fill the registers, always by 8: 152 us, by 16 163.)
+constexpr int64_t kFewValues = int64_t{1} << 23;
 // These hold where no product on the way leaves f32's normal numbers by much: for gates from kLeastGate on
 // (or 0) and results from kLeastValue on, as blocks' largest. (bf16's 8 bits survive sigma of a smaller gate.)
 constexpr float kLeastGate = 0x1p-100f, kLeastValue = 0x1p-90f;
@@ -88,14 +94,43 @@ __device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 8 values times f.
-__device__ __forceinline__ void times8(const float (&v)[8], float f, float (&out)[8]) {
+// N values times f.
+template <int N>
+__device__ __forceinline__ void times_all(const float (&v)[N], float f, float (&out)[N]) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     const uint64_t r = times(two(v[i], v[i + 1]), two(f, f));
     out[i] = first(r);
     out[i + 1] = second(r);
   }
+}
+
+// N channels as they lie in memory.
+template <int N, typename T>
+__device__ __forceinline__ void load_all(const T* p, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float part[8];
+    load8(p + i, part);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i + j] = part[j];
+  }
+}
+template <int N>
+struct alignas(N / 2) Fp4Codes {
+  uint32_t word[N / 8];
+};
+template <int N>
+__device__ __forceinline__ Fp4Codes<N> codes_of(const float (&f)[N]) {
+  Fp4Codes<N> r;
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float part[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[j] = f[i + j];
+    r.word[i / 8] = fp4_codes8(part);
+  }
+  return r;
 }
 
 // The least e >= -127 with amax <= 6 * 2^e = 1.5 * 2^(e + 2), as a byte; finite amax.
@@ -128,16 +163,16 @@ __device__ __forceinline__ bool above(Pair v, float a, float b, bool tie, bool& 
   }
 }
 
-// The byte of a block, its largest |value| and the codes of a lane's 8 values h (+ l, in pairs) of it.
+// The byte of a block, its largest |value| and the codes of a lane's N values h (+ l, in pairs) of it.
 // `near`: f32 does not decide.
-template <bool kNv, bool kPairs>
-__device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)[8], float g, uint32_t& byte,
-                                           float& amax, bool& near) {
-  constexpr int kLanes = kNv ? 2 : 4;   // to a block
+template <bool kNv, bool kPairs, int N>
+__device__ __forceinline__ Fp4Codes<N> decide(const float (&h)[N], const float (&l)[N], float g, uint32_t& byte,
+                                              float& amax, bool& near) {
+  constexpr int kLanes = (kNv ? 16 : 32) / N;   // to a block
   Pair top{0.0f, 0.0f};
   if constexpr (kPairs) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float a = fabsf(h[i]), b = signbit(h[i]) ? -l[i] : l[i];
       if (!(a < top.hi) && !(a == top.hi && b <= top.lo)) top = Pair{a, b};
     }
@@ -149,7 +184,7 @@ __device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)
   } else {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
     top.hi = lanes_max<kLanes>(__uint_as_float(m));
   }
   amax = top.hi;
@@ -178,41 +213,45 @@ __device__ __forceinline__ uint32_t decide(const float (&h)[8], const float (&l)
     // 2^-(byte - 127): finite values give bytes up to 253.
     inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
   }
-  uint32_t codes;
   if constexpr (!kNv && !kPairs) {
-    float z[8];
-    times8(h, inv, z);   // exact
-    codes = fp4_codes8(z);
+    float z[N];
+    times_all(h, inv, z);   // exact
+    return codes_of(z);
   } else {
-    float lo[8], hi[8];
-    times8(h, inv * (1.0f - kNearQuotient), lo);
-    times8(h, inv * (1.0f + kNearQuotient), hi);
-    codes = fp4_codes8(lo);
-    uint32_t differ = codes ^ fp4_codes8(hi);
-    // hi's code is the next one up: its border, in quarters, is looked up.
-    while (differ) {
-      const int at = (__ffs(differ) - 1) & ~3;
-      const uint32_t c = codes >> at & 7u;
-      const float border = 0.25f * static_cast<float>(0x00140e0a07050301ull >> (8 * c) & 0xffu);
-      Pair v{};
+    float lo[N], hi[N];
+    times_all(h, inv * (1.0f - kNearQuotient), lo);
+    times_all(h, inv * (1.0f + kNearQuotient), hi);
+    Fp4Codes<N> codes = codes_of(lo);
+    const Fp4Codes<N> more = codes_of(hi);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at == 4 * i) v = Pair{fabsf(h[i]), kPairs ? (signbit(h[i]) ? -l[i] : l[i]) : 0.0f};
-      codes += static_cast<uint32_t>(above<kPairs>(v, border * scale, kNv ? g : 1.0f, c & 1, near)) << at;
-      differ &= ~(0xfu << at);
+    for (int w = 0; w < N / 8; ++w) {
+      uint32_t differ = codes.word[w] ^ more.word[w];
+      // hi's code is the next one up: its border, in quarters, is looked up.
+      while (differ) {
+        const int at = (__ffs(differ) - 1) & ~3;
+        const uint32_t c = codes.word[w] >> at & 7u;
+        const float border = 0.25f * static_cast<float>(0x00140e0a07050301ull >> (8 * c) & 0xffu);
+        Pair v{};
+#pragma unroll
+        for (int i = 8 * w; i < 8 * w + 8; ++i)
+          if (at == 4 * (i - 8 * w)) v = Pair{fabsf(h[i]), kPairs ? (signbit(h[i]) ? -l[i] : l[i]) : 0.0f};
+        codes.word[w] +=
+            static_cast<uint32_t>(above<kPairs>(v, border * scale, kNv ? g : 1.0f, c & 1, near)) << at;
+        differ &= ~(0xfu << at);
+      }
     }
+    return codes;
   }
-  return codes;
 }
 
 // SwiGLU in pairs, and what it decides. `near`: a value that pairs do not hold or decide.
-template <bool kNv>
-__device__ __forceinline__ uint32_t fp4_swiglu_pairs(const float (&v)[8], const float (&u)[8], float g,
-                                                  uint32_t* byte, bool* near) {
-  float h[8], l[8];
+template <bool kNv, int N>
+__device__ __forceinline__ Fp4Codes<N> fp4_swiglu_pairs(const float (&v)[N], const float (&u)[N], float g,
+                                                        uint32_t* byte, bool* near) {
+  float h[N], l[N];
   bool doubt = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float a = fabsf(v[i]);
     const Pair x = pair_exp(Pair{a <= 80.0f ? -a : 0.0f, 0.0f});
     const Pair s = pair_div(v[i] < 0.0f ? x : Pair{1.0f, 0.0f}, pair_add(Pair{1.0f, 0.0f}, x));
@@ -223,19 +262,19 @@ __device__ __forceinline__ uint32_t fp4_swiglu_pairs(const float (&v)[8], const 
              (y.hi != 0.0f && fabsf(y.hi) < kLeastValue);
   }
   float amax;
-  const uint32_t codes = decide<kNv, true>(h, l, g, *byte, amax, doubt);
+  const Fp4Codes<N> codes = decide<kNv, true, N>(h, l, g, *byte, amax, doubt);
   *near = doubt;
   return codes;
 }
 
-// The same decisions on 8 values in 64 bits: the block's byte and the codes.
-template <bool kNv>
-__device__ __forceinline__ uint32_t fp4_exact(const double (&v)[8], float g, uint32_t* byte_out) {
+// The same decisions on N values in 64 bits: the block's byte and the codes.
+template <bool kNv, int N>
+__device__ __forceinline__ Fp4Codes<N> fp4_exact(const double (&v)[N], float g, uint32_t* byte_out) {
   double top = 0.0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmax(top, fabs(v[i]));
+  for (int i = 0; i < N; ++i) top = fmax(top, fabs(v[i]));
 #pragma unroll
-  for (int d = 1; d < (kNv ? 2 : 4); d *= 2) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
+  for (int d = 1; d < (kNv ? 16 : 32) / N; d *= 2) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
   double unit;
   if (kNv) {
     // e4m3: multiples of 2^(e - 3) from 2^e to 2^(e + 1), of 2^-9 below 2^-6.
@@ -254,15 +293,15 @@ __device__ __forceinline__ uint32_t fp4_exact(const double (&v)[8], float g, uin
     *byte_out = static_cast<uint32_t>(e + 127);
     unit = ldexp(1.0, e);
   }
-  uint32_t codes = 0;
+  Fp4Codes<N> codes = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     const double a = fabs(v[i]);
     uint32_t c = 0;
     if (unit > 0.0)
       c = (a > 0.25 * unit) + (a >= 0.75 * unit) + (a > 1.25 * unit) + (a >= 1.75 * unit) +
           (a > 2.5 * unit) + (a >= 3.5 * unit) + (a > 5.0 * unit);
-    codes |= (c | (signbit(v[i]) ? 8u : 0u)) << (4 * i);
+    codes.word[i / 8] |= (c | (signbit(v[i]) ? 8u : 0u)) << (4 * (i % 8));
   }
   return codes;
 }
@@ -274,64 +313,76 @@ __device__ __forceinline__ double swiglu_d(float g, float u) {
 
 // What f32 does not decide, by a whole warp: its lanes' values are read again (a call that takes them in
 // arrays would keep them in memory in every segment). Codes and the block's byte.
-template <typename T, bool kNv, bool kSwiglu>
-__device__ __noinline__ uint2 fp4_again(const T* src, int K, bool in, bool finite, float g) {
-  float v[kPerLane] = {}, u[kPerLane] = {};
+template <int N>
+struct Fp4Again {
+  Fp4Codes<N> codes;
+  uint32_t byte;
+};
+template <typename T, bool kNv, bool kSwiglu, int N>
+__device__ __noinline__ Fp4Again<N> fp4_again(const T* src, int K, bool in, bool finite, float g) {
+  float v[N] = {}, u[N] = {};
   if (in) {
-    load8(src, v);
-    if (kSwiglu) load8(src + K, u);
+    load_all(src, v);
+    if (kSwiglu) load_all(src + K, u);
   }
-  uint2 r;
+  Fp4Again<N> r;
   if (kSwiglu) {
     bool near;
-    r.x = fp4_swiglu_pairs<kNv>(v, u, g, &r.y, &near);
+    r.codes = fp4_swiglu_pairs<kNv>(v, u, g, &r.byte, &near);
     if (!__any_sync(0xffffffffu, near && finite)) return r;
   }
-  double d[kPerLane];
+  double d[N];
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) d[i] = !kSwiglu ? static_cast<double>(v[i]) : in ? swiglu_d(v[i], u[i]) : 0.0;
-  r.x = fp4_exact<kNv>(d, g, &r.y);
+  for (int i = 0; i < N; ++i) d[i] = !kSwiglu ? static_cast<double>(v[i]) : in ? swiglu_d(v[i], u[i]) : 0.0;
+  r.codes = fp4_exact<kNv>(d, g, &r.byte);
   return r;
 }
 
-template <typename T, bool kNv, bool kSwiglu>
-__global__ void __launch_bounds__(kSegmentThreads, 12)
+// Segments of 32 lanes of `per` channels that reach a row's scales, with what fills them up.
+__host__ __device__ constexpr int quant_segments(int pitch, bool nv, int per) {
+  return (pitch * (nv ? 16 : 32) + 32 * per - 1) / (32 * per);
+}
+
+// By lanes of N channels. (Of 16: what a lane does once is shared by more, and a block of nv is one lane's.)
+template <typename T, bool kNv, bool kSwiglu, int N>
+__global__ void __launch_bounds__(kSegmentThreads, N == 8 ? 12 : kSwiglu && kNv ? 9 : 10)
 quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kLanes = kNv ? 2 : 4;           // to a block
+  constexpr int kLanes = (kNv ? 16 : 32) / N;   // to a block
   const int lane = threadIdx.x & 31;
   const int pitch = fp4_scale_pitch(K, kNv ? kFp4Nv : kFp4Mx);
-  // Segments of 256 channels, over the whole row of scales.
-  for (SegmentWalk w(kNv ? pitch / 16 : pitch / 8); w.row < R; w.next()) {
-    const int c = w.seg * 256 + lane * kPerLane;
+  // Segments of 32 N channels, over the whole row of scales.
+  for (SegmentWalk w(quant_segments(pitch, kNv, N)); w.row < R; w.next()) {
+    const int c = w.seg * 32 * N + lane * N;
     const bool in = c < K;                      // (K % 32 == 0: the same in all lanes of a block)
-    float v[kPerLane] = {}, u[kPerLane] = {};
+    float v[N] = {}, u[N] = {};
     const T* src = x + w.row * (kSwiglu ? 2 : 1) * K + c;
     if (in) {
-      load8(src, v);
-      if (kSwiglu) load8(src + K, u);
+      load_all(src, v);
+      if (kSwiglu) load_all(src + K, u);
     }
     float g = 1.0f;
     if (kNv && out.g)
       g = __ldg(out.g + (out.rows_per_plane < R ? w.row / out.rows_per_plane : 0));
-    uint32_t byte, codes;
+    uint32_t byte;
+    Fp4Codes<N> codes;
     bool finite;
     if constexpr (!kSwiglu) {
       bool near = false;
       float amax;
-      codes = decide<kNv, false>(v, v, g, byte, amax, near);
+      codes = decide<kNv, false, N>(v, v, g, byte, amax, near);
       finite = amax < INFINITY;
       if (kNv && __any_sync(0xffffffffu, near && finite)) {
-        const uint2 r = fp4_again<T, kNv, false>(src, K, in, finite, g);
-        codes = r.x;
-        byte = r.y;
+        const Fp4Again<N> r = fp4_again<T, kNv, false, N>(src, K, in, finite, g);
+        codes = r.codes;
+        byte = r.byte;
       }
     } else {
-      float h[kPerLane], amax = 0.0f, gates = 0.0f;
+      float h[N], amax = 0.0f, gates = 0.0f;
       constexpr float kMinusLog2E = -1.44269504f;
 #pragma unroll
-      for (int i = 0; i < kPerLane; i += 2) {
+      for (int i = 0; i < N; i += 2) {
         const uint64_t gate = two(v[i], v[i + 1]), x = times(gate, two(kMinusLog2E, kMinusLog2E));
         const uint64_t d = plus(two(power_of_2(first(x)), power_of_2(second(x))), two(1.0f, 1.0f));
         const uint64_t y = times(times(gate, two(reciprocal(first(d)), reciprocal(second(d)))), two(u[i], u[i + 1]));
@@ -339,7 +390,7 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
         h[i + 1] = second(y);
       }
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
+      for (int i = 0; i < N; ++i) {
         gates = fmaxf(gates, fabsf(v[i]));
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[i])));   // (a NaN stays)
       }
@@ -351,7 +402,7 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
                   (amax > 0.0f && amax < kLeastValue);
       if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) near |= v[i] != 0.0f && fabsf(v[i]) < kLeastGate;
+        for (int i = 0; i < N; ++i) near |= v[i] != 0.0f && fabsf(v[i]) < kLeastGate;
       }
       const float by = fmaf(gates, kNearGate, kNearSwiglu);
       float inv;
@@ -365,24 +416,26 @@ quantize_fp4_kernel(const T* __restrict__ x, int64_t R, int K, Fp4Out out) {
         near |= byte != mx_byte(amax * (1.0f + by));
         inv = __uint_as_float((254u - (byte < 254u ? byte : 253u)) << 23);
       }
-      float lo[kPerLane], hi[kPerLane];
-      times8(h, inv * (1.0f - by), lo);
-      times8(h, inv * (1.0f + by), hi);
-      codes = fp4_codes8(lo);
-      near |= codes != fp4_codes8(hi);
+      float lo[N], hi[N];
+      times_all(h, inv * (1.0f - by), lo);
+      times_all(h, inv * (1.0f + by), hi);
+      codes = codes_of(lo);
+      const Fp4Codes<N> up = codes_of(hi);
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) near |= codes.word[i] != up.word[i];
       if (__any_sync(0xffffffffu, near && finite)) {
-        const uint2 r = fp4_again<T, kNv, true>(src, K, in, finite, g);
-        codes = r.x;
-        byte = r.y;
+        const Fp4Again<N> r = fp4_again<T, kNv, true, N>(src, K, in, finite, g);
+        codes = r.codes;
+        byte = r.byte;
       }
     }
     if (!finite) {
       byte = kNv ? kNvNan : kMxNan;
-      codes = 0;
+      codes = {};
     }
-    if (in) *reinterpret_cast<uint32_t*>(out.codes + w.row * (K / 2) + c / 2) = codes;
+    if (in) *reinterpret_cast<Fp4Codes<N>*>(out.codes + w.row * (K / 2) + c / 2) = codes;
     // (What fills a row of scales up is zeros.)
-    const int at = c / (kLanes * kPerLane);
+    const int at = c / (kLanes * N);
     if ((lane & (kLanes - 1)) == 0 && at < pitch)
       out.scales[w.row * pitch + at] = static_cast<uint8_t>(in ? byte : 0u);
   }
@@ -437,17 +490,30 @@ dequantize_fp4_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restri
   }
 }
 
+template <typename T, bool kNv, bool kSwiglu, int N>
+cudaError_t quantize_lanes(const T* x, int64_t R, int K, const Fp4Out& out, cudaStream_t s) {
+  const dim3 grid(segment_grid(R, quant_segments(fp4_scale_pitch(K, kNv ? kFp4Nv : kFp4Mx), kNv, N)));
+  return launch_pdl(quantize_fp4_kernel<T, kNv, kSwiglu, N>, grid, dim3(kSegmentThreads), 0, s, x, R, K, out);
+}
+
+template <typename T, bool kNv, bool kSwiglu>
+cudaError_t quantize_one(const T* x, int64_t R, int K, const Fp4Out& out, cudaStream_t s) {
+  if constexpr (kSwiglu) {
+    if (sizeof(T) == 4 || R * K < kFewValues) return quantize_lanes<T, kNv, true, 8>(x, R, K, out, s);
+  }
+  if constexpr (!kSwiglu || sizeof(T) == 2) return quantize_lanes<T, kNv, kSwiglu, 16>(x, R, K, out, s);
+  else return cudaErrorInvalidValue;
+}
+
 template <typename T>
 cudaError_t quantize_t(const void* x, int64_t R, int K, int fmt, bool swiglu, const Fp4Out& out,
                        cudaStream_t s) {
-  const int pitch = fp4_scale_pitch(K, fmt);
-  const dim3 grid(segment_grid(R, fmt == kFp4Nv ? pitch / 16 : pitch / 8)), block(kSegmentThreads);
   const T* src = static_cast<const T*>(x);
   if (fmt == kFp4Nv)
-    return swiglu ? launch_pdl(quantize_fp4_kernel<T, true, true>, grid, block, 0, s, src, R, K, out)
-                  : launch_pdl(quantize_fp4_kernel<T, true, false>, grid, block, 0, s, src, R, K, out);
-  return swiglu ? launch_pdl(quantize_fp4_kernel<T, false, true>, grid, block, 0, s, src, R, K, out)
-                : launch_pdl(quantize_fp4_kernel<T, false, false>, grid, block, 0, s, src, R, K, out);
+    return swiglu ? quantize_one<T, true, true>(src, R, K, out, s)
+                  : quantize_one<T, true, false>(src, R, K, out, s);
+  return swiglu ? quantize_one<T, false, true>(src, R, K, out, s)
+                : quantize_one<T, false, false>(src, R, K, out, s);
 }
 
 template <typename T>

@@ -36,6 +36,28 @@ def test_swiglu_at_the_ends_of_the_range(moe, dtype, fmt, gate, up, g):
     assert np.array_equal(q.codes.cpu().numpy(), codes)
 
 
+@pytest.mark.parametrize("R,I", [(8460, 992), (586, 14336)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("fmt,g", [(ref.MX, None), (ref.NV, None), (ref.NV, 0.011)])
+def test_swiglu_of_many_values(moe, fmt, g, dtype, R, I):
+    """8.4 million values, of rows of very unequal size, some blocks not finite."""
+    gen = torch.Generator().manual_seed(R)
+    gu = torch.randn((R, 2 * I), generator=gen) * torch.exp(2 * torch.randn((R, 1), generator=gen))
+    gu[5, 7], gu[9, I + 40], gu[R - 1, 2 * I - 1] = float("inf"), float("nan"), float("-inf")
+    gu[3, :64] = -30.0
+    if dtype == torch.bfloat16:
+        gu[11:20] *= 2.0 ** -40
+        gu[20, :I], gu[20, I:] = gu[20, :I] * 2.0 ** -128, gu[20, I:] * 2.0 ** 100
+        gu[21, :96] = -95.0
+    gu = gu.to(dtype)
+    q = moe.moe_swiglu_fp4(gu.cuda(), fmt, None if g is None else torch.full((1,), g, device="cuda"))
+    with np.errstate(invalid="ignore", over="ignore"):
+        h = ref.swiglu(gu.double().numpy())
+        codes, scales = ref.quantize(h, fmt, None if g is None else float(np.float32(g)))
+    assert np.array_equal(q.scales.cpu().numpy(), scales)
+    assert np.array_equal(q.codes.cpu().numpy(), codes)
+
+
 def test_conversions_past_32_bit_offsets(moe):
     """4.3 billion channels: the last rows as they are alone."""
     R, K = 65552, 65536
