@@ -498,7 +498,8 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
  * Writes y [T, H], ids int32 [T, k] and scales fp32 [T, k]. Between the products h, times its routing
  * weight, is rounded once: to bf16, or (f16 and 4-bit weights) to 11 bits beside its token's largest.
  * x and wg are not rounded (with 4-bit weights, what of x is less than 2^-29 of its token's largest is
- * rounded to steps of at most 2^-38 of that, and an MX scale of 2^-127 counts as 0), sums are fp32.
+ * rounded to steps of at most 2^-38 of that, an MX scale of 2^-127 counts as 0, and sums of MX products that
+ * are less than 2^-90 and than 2^-105 of the token's largest lose bits), sums are fp32.
  * Experts that no token chose are not read. The results are the same on every run. Workspace:
  * moe_layer_few_workspace_bytes, 256-byte aligned, nothing of it has to be set; calls that share one
  * must be ordered. Whether a bounded wait ran out: moe_read_timeouts. */

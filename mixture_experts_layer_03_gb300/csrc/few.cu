@@ -33,7 +33,9 @@
 // multiplied in f16, exactly (6 significant bits, 2^-10 to 2688); mx scales, which f16 does not reach,
 // by an FMA a block of 32 on its fp32 sum. x and h go to f16 times a power of two for each token
 // that brings the largest to [2^14, 2^15): x of 8 or 11 significant bits is exact but for what is less
-// than 2^-29 of the token's largest, h is rounded to 11 bits. Sums, SwiGLU and the sum over experts: fp32.
+// than 2^-29 of the token's largest, h is rounded to 11 bits. The power comes off the parts' sums; so that no mx
+// scale takes such a sum out of range that its result is in, scales are multiplied by the least of the
+// tokens' inverse powers (see scale_unit). Sums, SwiGLU and the sum over experts: fp32.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -293,6 +295,16 @@ __device__ __forceinline__ float inverse_power(float p) {
   return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
+// What mx scales are multiplied by, of the tokens' inverse powers of two (a lane each, positive): the least, so
+// that a token's sums are at most what they stand for; within [2^-33, 1]. (From 2^-33 down no sum overflows: x or
+// h below 2^15, codes to 6, scales to 2^127, 2^16 channels. Less would cost small scales.) The unit takes an
+// instruction a row and block, which FMAs of two sums each give back but for 2 to 4% (1 token, 256 experts of
+// 7168 x 2048 93.4 us without it and 95.5, 16 tokens 627 and 655; every block's sums by their token's inverse 718).
+__device__ __forceinline__ float scale_unit(float inv) {
+  const float least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(inv)));
+  return fminf(fmaxf(least, 0x1p-33f), 1.0f);
+}
+
 // Everything about the chosen experts that the block's warps share.
 struct FewShared {
   int32_t ids[kFewTokens * kMaxTopK];
@@ -309,6 +321,7 @@ struct FewShared {
   uint16_t tokens[kFewExperts];            // of a chosen expert, a bit each
   float weight_s[kFewTokens];              // of the shared expert
   float x_mul[kFewTokens], x_inv[kFewTokens];
+  float x_unit, h_unit[kXSlots];           // mx: of x, and of h as each producer of the tokens' side has it
   uint32_t tmax[kFewTokens];
   int n;                                   // chosen experts
 };
@@ -509,6 +522,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     sh.x_mul[tid] = p;
     sh.x_inv[tid] = inverse_power(p);
   }
+  if constexpr (kW == kW4mx) {
+    __syncwarp();
+    if (warp == 0) {
+      const float unit = scale_unit(lane < a.T ? sh.x_inv[lane] : 1.0f);
+      if (lane == 0) sh.x_unit = unit;
+    }
+  }
   few_route(a, &sh, sW);
 
   const int n_exp = sh.n, T = a.T, H = a.H;
@@ -695,6 +715,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
         if (!ok) break;
         waited = true;
         if (!kBf16 && lane < T) t_mul = to_f16_range(__uint_as_float(__ldcg(a.tmax + lane)));
+        if (kW == kW4mx) {
+          const float unit = scale_unit(inverse_power(t_mul));
+          if (lane == 0) sh.h_unit[mine] = unit;
+        }
       }
       // Where in the slice: the next part (from `at` on), the expert, the chunk of its contraction.
       const Slice slice = slice1(fc1 ? ticket : 0);
@@ -840,7 +864,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     // column tiles from `tile` on, of all their columns, whoever's token is in them. kM: are there rows
     // past the first 16? (No branch inside a group: the compiler moves loads and conversions over
     // products only within one.)
-    auto multiply = [&](auto m_tiles, auto n_tiles, float (&acc)[2][kNt][4], int tile, int i, int xc, int subs) {
+    auto multiply = [&](auto m_tiles, auto n_tiles, float (&acc)[2][kNt][4], int tile, int i, int xc, int subs,
+                        bool fc1) {
       constexpr int kM = decltype(m_tiles)::value, kTiles = decltype(n_tiles)::value;
       const int place = first + i, lap = place / kStages;
       const int stage = place - lap * kStages, xs = xc % kXSlots;
@@ -851,6 +876,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
       const uint8_t* sc = sW + stage * W::kStage + kFewRows * W::kPitch + g * W::kScalePitch +
                           member * W::kGroups * (kW == kW4nv ? 2 : 1);
       ok = ok && few_wait(&x_full[xs], x_phase, abort) && few_wait(&w_full[stage], phase, abort);
+      const float unit = kW != kW4mx ? 1.0f : fc1 ? sh.x_unit : sh.h_unit[xs];
       // Rows g, g + 8, g + 16, g + 24: scales of four groups, nv as f16 pairs, mx as bytes.
       uint32_t scale[2 * kM][2] = {}, nan[2 * kM] = {};
       auto scales = [&](int k0) {
@@ -910,8 +936,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             for (int r = 0; r < 2; ++r) {
               // 2^(byte - 127); 2^-127, which is no normal number, as 0
               const uint32_t word = scale[2 * m + r][0];
-              f[r] = __uint_as_float((of == 3 ? word >> 1 : word << (23 - 8 * of)) & 0x7f800000u);
+              f[r] = __uint_as_float((of == 3 ? word >> 1 : word << (23 - 8 * of)) & 0x7f800000u) * unit;
             }
+            const uint64_t by[2] = {two(f[0], f[0]), two(f[1], f[1])};
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) {
               const float zero[4] = {};
@@ -920,8 +947,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
               mma_16bit<kBf16>(d, a0, b[n].x, b[n].y, zero);
               mma_16bit<kBf16>(d2, a1, b[n].z, b[n].w, zero);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                acc[m][n][j] = fmaf(d2[j], f[j >> 1], fmaf(d[j], f[j >> 1], acc[m][n][j]));
+              for (int r = 0; r < 2; ++r) {
+                uint64_t sum = two(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
+                sum = times_plus(two(d[2 * r], d[2 * r + 1]), by[r], sum);
+                sum = times_plus(two(d2[2 * r], d2[2 * r + 1]), by[r], sum);
+                acc[m][n][2 * r] = moe::first(sum);
+                acc[m][n][2 * r + 1] = moe::second(sum);
+              }
             }
           } else {
 #pragma unroll
@@ -988,7 +1020,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
     };
 
     bool waited = false;
-    float y_inv = 1.0f;       // lane t: inverse of token t's power of two
+    float y_inv = 1.0f;       // lane t: inverse of token t's power of two; mx: lane 31 of the scales' unit
     for (int i = 0;; ++i) {
       if (tid == 0) s_current = ticket_at(i, ok);
       named_barrier_sync(1, 32 * kMmaWarps);
@@ -1024,12 +1056,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             using Two = std::integral_constant<int, 2>;
             if constexpr (kNt == 2) {
               if (both) {
-                multiply(Two{}, Two{}, acc, 0, i2, xc, p.subs);
+                multiply(Two{}, Two{}, acc, 0, i2, xc, p.subs, fc1);
                 continue;
               }
             }
-            if (second) multiply(Two{}, One{}, acc, tile, i2, xc, p.subs);
-            else multiply(One{}, One{}, acc, tile, i2, xc, p.subs);
+            if (second) multiply(Two{}, One{}, acc, tile, i2, xc, p.subs, fc1);
+            else multiply(One{}, One{}, acc, tile, i2, xc, p.subs, fc1);
           }
           // Sums of the expert's tokens only (in the first products, all: the rest is dropped below).
 #pragma unroll
@@ -1061,8 +1093,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             const int row = (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
             const int sl = t < T ? sh.slot[p.a][t] : -1;
             if (sl < 0 || row >= p.of(s)) continue;
-            const float f = sh.x_inv[t] * g13;
-            const float gate = sum_at(p.subs, s, 0, n, at_) * f, up = sum_at(p.subs, s, 1, n, at_) * f;
+            float f = sh.x_inv[t] * g13;
+            float gate = sum_at(p.subs, s, 0, n, at_) * f, up = sum_at(p.subs, s, 1, n, at_) * f;
+            if constexpr (kW == kW4mx) {
+              f = 1.0f / sh.x_unit;
+              gate *= f;
+              up *= f;
+            }
             const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
             const float ex = expf(-fabsf(gate));
             const float sig = (gate < 0.0f ? ex : 1.0f) / (1.0f + ex);
@@ -1075,14 +1112,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             // (h came through the tokens' warps, which waited for all of it)
             waited = true;
             if (!kBf16 && lane < T) y_inv = inverse_power(to_f16_range(__uint_as_float(__ldcg(a.tmax + lane))));
+            if constexpr (kW == kW4mx) {
+              const float unit = scale_unit(y_inv);
+              if (lane == 31) y_inv = 1.0f / unit;
+            }
           }
           for (int pos = tid; pos < p.subs * 2 * kNt * 128; pos += 32 * kMmaWarps) {
             const int s = pos / (2 * kNt * 128), m = pos / (kNt * 128) % 2, n = pos / 128 % kNt;
             const int at_ = pos & 127, l = at_ >> 2, j = at_ & 3;
             const int row = m * 16 + (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
             const float inv = __shfl_sync(0xffffffffu, y_inv, t);   // (a warp's positions come and go together)
+            const float unit_inv = kW == kW4mx ? __shfl_sync(0xffffffffu, y_inv, 31) : 1.0f;
             if (t >= T || row >= p.of(s)) continue;
-            const float v = sum_at(p.subs, s, m, n, at_) * inv;
+            float v = sum_at(p.subs, s, m, n, at_) * inv;
+            if constexpr (kW == kW4mx) v *= unit_inv;
             const int64_t to = static_cast<int64_t>(t) * H + p.at + s * p.per + row;
             if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[to] = __float2bfloat16_rn(v);
             else static_cast<__half*>(a.y)[to] = __float2half_rn(v);

@@ -1,11 +1,33 @@
 // Numbers hi + lo of two f32, lo half a unit of hi or less: sums, products, quotients and exponentials to some
-// 2^-28 of the value, where fp64, at 1/64 of fp32's rate, would be waited for.
+// 2^-28 of the value, where fp64, at 1/64 of fp32's rate, would be waited for. And two f32 as one operand.
 #pragma once
 
 #include <cstdint>
 
 namespace moe {
 namespace {
+
+// Two products or sums an instruction.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float first(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float second(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t times_plus(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 struct Pair {
   float hi, lo;

@@ -1,0 +1,77 @@
+"""GPU: the serving operators with scales and factors far from 1, where the results themselves are in range.
+Multiplying by powers of two rounds nothing, so that such results are the same bits, moved."""
+import pytest
+import torch
+
+from tests.test_layer_few import Layer
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_layer_03_gb300 as m
+    return m
+
+
+def moved(q, by):
+    """mx weights times 2^by."""
+    s = q.scales.int() + by
+    blocks = q.shape[-1] // 32
+    assert 0 < s[..., :blocks].min() and s[..., :blocks].max() < 255
+    return type(q)(q.codes, s.clamp(0, 255).byte(), q.format)
+
+
+def up_rows_moved(q, by):
+    """The same of the up rows alone (the second half of each plane's)."""
+    half = q.shape[-2] // 2
+    out = moved(q, 0)
+    out.scales[..., half:, :] = moved(q, by).scales[..., half:, :]
+    return out
+
+
+# h is moved by the first power, y by the product of both: first products whose scales are large (2^114 and such),
+# then second products' that are (2^124).
+@pytest.mark.parametrize("up,back", [(118, -118), (60, -60), (-60, 60), (-106, 128)])
+@pytest.mark.parametrize("T,dtype", [(5, "bf16"), (11, "bf16"), (16, "f16")])
+def test_mx_scales_at_the_ends_of_their_range(moe, T, dtype, up, back):
+    if dtype == "f16":
+        back = -up                         # (f16 does not hold y otherwise)
+    layer = Layer(moe, T, 544, 352, 12, 3, 4, "mx", dtype, shared=96, seed=T)
+    layer.x = (2 * layer.x.float() / layer.x.float().abs().amax(1, keepdim=True)).to(layer.x.dtype)
+    y, ids, sc = layer()
+    layer.check((y, ids, sc))
+    layer.w13, layer.w2 = up_rows_moved(layer.w13, up), moved(layer.w2, back)
+    layer.kw["w13_s"], layer.kw["w2_s"] = up_rows_moved(layer.kw["w13_s"], up), moved(layer.kw["w2_s"], back)
+    again = layer()
+    assert moe.moe_read_timeouts() == (moe.MOE_OK, 0)
+    assert torch.isfinite(again[0]).all() and torch.equal(again[0].double(), y.double() * 2.0 ** (up + back))
+    assert torch.equal(again[1], ids) and torch.equal(again[2], sc)
+
+
+@pytest.mark.parametrize("T", [3, 12])
+def test_small_tokens_and_large_mx_scales(moe, T):
+    """x times 2^-120, weights of the first products times 2^120. The gate is zeros, so that it sees neither."""
+    layer = Layer(moe, T, 256, 128, 4, 4, 3, "mx", "bf16")
+    layer.wg.zero_()
+    layer.x = torch.where(layer.x < 0, -1.0, 1.0).bfloat16() * (1 + layer.x.abs().clamp(max=0.75).mul(64).round() / 64).bfloat16()
+    want = layer()
+    layer.check(want)
+    layer.x, layer.w13 = (layer.x.double() * 2.0 ** -120).bfloat16(), moved(layer.w13, 120)
+    got = layer()
+    assert torch.isfinite(want[0]).all() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [4, 13])
+def test_a_small_token_changes_no_other(moe, T):
+    layer = Layer(moe, T, 288, 160, 8, 2, 4, "mx", "bf16", shared=64)
+    want = layer()
+    x = layer.x.clone()
+    x[1] = (x[1].double() * 2.0 ** -100).bfloat16()
+    x[2] = 0
+    got = layer(x=x)
+    rest = [t for t in range(T) if t not in (1, 2)]
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, want))
+    assert not got[0][2].any()
+    layer.check(got, x=x)
