@@ -4,31 +4,33 @@
 //
 // tcgen05.mma of block-scaled e2m1 operands takes the scales from TMEM and multiplies 64 elements of the
 // contraction an instruction, so that codes go from memory to the tensor cores as they are. One
-// persistent kernel over all groups, CTA pairs (M = 256 channels of w, N up to 224 rows of x, the
+// persistent kernel over all groups, CTA pairs (M = 256 channels of w, N up to 208 or 224 rows of x, the
 // tiles and their order those of the 16-bit products); a block is 256 elements of the contraction, 128
 // bytes a row, by TMA with the 128-byte swizzle.
 //
 // Scales. The instruction wants those of 128 rows by 4 bytes of the contraction as 32 lanes by 4 columns
-// (row 32 i + l in lane l, column i), which tcgen05.cp writes from 512 bytes of shared memory, row l of
-// 16 bytes holding rows l, l + 32, l + 64, l + 96. A row's scales lie along the contraction in memory: they
-// come by TMA as they lie, 16 bytes a row (mx: for two blocks), and four warps turn 4 x 4 words over
-// between four lanes by shuffles and write 16 bytes a lane. (Read from memory by those warps themselves:
-// 8192 x 28672 x 4096 over 8 experts 1575 us, by TMA 1148, both with the arrivals' release to the other
-// SM; without that 507.) Each CTA needs the scales of its 128 channels and of all of the tile's rows (the
-// pair shares the rows' codes, but each tensor core scales its own half of D). Bytes past the row's
-// K / block are zeros, whatever fills the row up; codes past K are TMA's zeros.
-// TMEM: two accumulators of 224 columns, 48 columns of scales (nv: 4 x 4 for A, 4 x 8 for B), written
-// anew for every block: copies and products are issued by one thread and run in that order.
+// (row 32 i + l in lane l, column i), the same in each quarter of TMEM's lanes. A row's scales lie along the
+// contraction in memory: they come by TMA as they lie, 16 bytes a row (mx: for two blocks), and four warps, one
+// a quarter, read rows l, l + 32, ... and store them to TMEM. Each CTA needs the scales of its 128 channels and of
+// all of the tile's rows (the pair shares the rows' codes, but each tensor core scales its own half of D). Bytes
+// past the row's K / block are zeros, whatever fills the row up; codes past K are TMA's zeros.
+// (Scales written to shared memory for tcgen05.cp, which the first CTA's thread issues for both, would take a
+// release by the second's writers to the other SM, 1700 cycles a block: 8192 x 28672 x 4096 over 8 experts
+// 815 us, and 425 without it, which PTX does not order. TMEM is handed over by tcgen05.fence instead: 442.)
+// TMEM: two accumulators (nv: of 208 columns, mx: 224) and two sets of scales, each written when the products
+// of the block two before are done (that a copy into columns that a product before it still reads would wait for
+// that is not promised either).
 //
-// Measured (one GB300, back to back): 8192 rows over 8 experts, N = 28672, K = 4096, nv, 425 us, 4.5
-// PFLOP/s, 2.4 times cuBLAS's bf16 rate: 880 cycles a block of 256 x 208 x 256, for 43% of which the tensor
-// pipe is active; what feeds it bounds it (L2 at 48%, the scales' way 650 cycles for each of two teams).
-// 512 rows over 128 experts, N = 1536, K = 2048, nv, 43 us and 4096 rows over 256 experts, N = 7168,
-// K = 2048, mx, 361 to 376 us: 5.2 and 5.6 TB/s, bound by memory.
+// Measured (one GB300, back to back): 8192 rows over 8 experts, N = 28672, K = 4096, nv, 442 us, 4.35
+// PFLOP/s, 2.3 times cuBLAS's bf16 rate: 910 cycles a block of 256 x 208 x 256, of which the products take 380;
+// what feeds the tensor pipe bounds it (with a quarter of the products 469 us, so 487 then).
+// 512 rows over 128 experts, N = 1536, K = 2048, nv, 44 us and 4096 rows over 256 experts, N = 7168,
+// K = 2048, mx, 364 us: 5.1 and 5.7 TB/s, bound by memory. A fifth and a seventh block under way, for which
+// scales in shared memory left no room, are 3% of the first (452 us with four) and 2% of the last (370 with six).
 //
 // Warp roles (608 threads per CTA): warps 0 and 18 TMA producers of the weights and of the rows, warp 1 TMEM
 // allocator and, in the first CTA, MMA issuer, warps 2-9 scales, in two teams that take a block each in
-// turn (a block takes a team 650 cycles of latency), warps 10-17 epilogue, four to each accumulator.
+// turn, warps 10-17 epilogue, four to each accumulator.
 #include <atomic>
 #include <cstdint>
 
@@ -45,35 +47,33 @@ namespace moe {
 namespace {
 
 constexpr int kQBK = 256;                      // contraction elements a block: 128 bytes
-constexpr int kQAtom = 512;                    // scales of 128 rows by 4 bytes
 constexpr int kQSlotA = 128 * 128;             // codes of the weights of one block in one CTA
 
-// Wide tiles: up to 224 rows. Narrow ones, for launches of few rows an expert: up to 64, with more blocks
-// of weights under way instead.
-template <bool kWide>
+// Wide tiles: as many rows as TMEM has room for. Narrow ones, for launches of few rows an expert: up to 64, with
+// more blocks of weights under way instead.
+template <bool kNv, bool kWide>
 struct QTile {
-  static constexpr int kMost = kWide ? 224 : 64;                 // rows of a tile
-  static constexpr int kStages = kWide ? 4 : 6;
+  static constexpr int kMost = !kWide ? 64 : kNv ? 208 : 224;    // rows of a tile
+  static constexpr int kStages = kWide ? 5 : 7;
   static constexpr int kSlotB = (kWide ? 128 : 32) * 128;        // codes of half of the rows
-  static constexpr int kAtomsB = kWide ? 2 : 1;                  // of 128 rows, a word of scales
-  static constexpr int kScaleBytes = 4 * (1 + kAtomsB) * kQAtom; // of A, then of B
   static constexpr int kRawBytes = (kWide ? 3 : 2) * 128 * 16;   // scales as they lie: A's 128 rows, B's
-  static constexpr int kStage = kQSlotA + kSlotB + kScaleBytes + kRawBytes;
+  static constexpr int kStage = kQSlotA + kSlotB + kRawBytes;
+  static constexpr int kWords = kNv ? 4 : 2;                     // of scales, of a row in a block
+  static constexpr int kPitchB = kWide ? 8 : 4;                  // columns a word of up to 256 or 128 rows
+  static constexpr int kColsA = 4 * kWords, kColsB = kPitchB * kWords;
+  static constexpr int kScales = 2 * kMost, kSet = kColsA + kColsB;   // first TMEM column, of a set
+  static_assert(kScales + 2 * kSet <= 512, "TMEM");
 };
 constexpr int kQScaleWarp = 2, kQScaleWarps = 4, kQScaleTeams = 2;   // a stage each in turn
 constexpr int kQEpiWarp = kQScaleWarp + kQScaleWarps * kQScaleTeams, kQEpiWarps = 8;
 constexpr int kQWarpX = kQEpiWarp + kQEpiWarps;   // the producer of the rows
 constexpr int kQThreads = 32 * (kQWarpX + 1);
 constexpr int kQBoxBytes = 4096;               // epilogue staging of a warp
-template <bool kWide>
-constexpr int kQSmemBytes = 1024 + QTile<kWide>::kStages * QTile<kWide>::kStage + kQEpiWarps * kQBoxBytes;
-static_assert(kQSmemBytes<true> <= 232448 - 2048 && kQSmemBytes<false> <= 232448 - 2048, "shared memory");
+template <bool kNv, bool kWide>
+constexpr int kQSmemBytes = 1024 + QTile<kNv, kWide>::kStages * QTile<kNv, kWide>::kStage + kQEpiWarps * kQBoxBytes;
+static_assert(kQSmemBytes<false, true> <= 232448 - 2048 && kQSmemBytes<false, false> <= 232448 - 2048, "shared memory");
 constexpr int kQTmemCols = 512;
-constexpr int kQAccCols = QTile<true>::kMost;
-constexpr int kQColsA = 2 * kQAccCols, kQColsB = kQColsA + 16;   // scales' TMEM columns
-static_assert(kQColsB + 32 <= kQTmemCols, "TMEM");
-static_assert(kQScaleTeams == 2 && QTile<true>::kStages % 2 == 0 && QTile<false>::kStages % 2 == 0,
-              "stages of the scale teams");
+static_assert(kQScaleTeams == 2 && kQScaleWarps == 4, "a team a set of scales, a warp a quarter of TMEM");
 constexpr uint16_t kQPairMask = 0x3;
 constexpr int kQNarrowRows = 48;
 
@@ -113,17 +113,6 @@ __device__ __forceinline__ void umma_fp4_pair(uint32_t d, uint64_t da, uint64_t 
         : "memory");
 }
 
-// 512 bytes of scales from both CTAs' shared memory to four columns of their TMEM.
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t ta, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(ta), "l"(sdesc) : "memory");
-}
-
-// Rows of 16 bytes, unswizzled, 8 of them 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128u >> 4) << 32 |
-         static_cast<uint64_t>(1) << 46;
-}
-
 // kind::mxf4 and mxf4nvf4: A and B e2m1 (1 at bits 7-9 and 10-11), K-major, N >> 3 at bits 17-22, the
 // scales' type at bit 23 (0 e4m3, 1 powers of two), M >> 4 at bits 24-28; which of a word's two halves
 // holds the scales of a step of two blocks: bits 29-30 (A) and 4-5 (B).
@@ -139,10 +128,11 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                    const __grid_constant__ CUtensorMap map_x32,
                    const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
                    const __grid_constant__ CUtensorMap map_out, Fp4Args q) {
-  using Q = QTile<kWide>;
+  using Q = QTile<kNv, kWide>;
   constexpr int kQStages = Q::kStages, kQMost = Q::kMost;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full_bar[kQStages], raw_bar[kQStages], scale_bar[kQStages], empty_bar[kQStages];
+  __shared__ uint64_t full_bar[kQStages], raw_bar[kQStages], read_bar[kQStages], scale_bar[kQStages];
+  __shared__ uint64_t empty_bar[kQStages];
   __shared__ uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
@@ -157,8 +147,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   uint8_t* sB = sA + kQStages * kQSlotA;
-  uint8_t* sS = sB + kQStages * Q::kSlotB;
-  uint8_t* sRaw = sS + kQStages * Q::kScaleBytes;
+  uint8_t* sRaw = sB + kQStages * Q::kSlotB;
   uint8_t* sOut = sRaw + kQStages * Q::kRawBytes;
 
   pdl_trigger();
@@ -166,6 +155,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&full_bar[s], 2);                    // first CTA: its two producers, and both CTAs' bytes
       mbar_init(&raw_bar[s], 2);                     // this CTA's scales, as they lie
+      mbar_init(&read_bar[s], kQScaleWarps);         // they have been read
       mbar_init(&scale_bar[s], 2 * kQScaleWarps);    // first CTA: both CTAs' scale warps
       mbar_init(&empty_bar[s], 1);                   // the pair commit, delivered to both CTAs
     }
@@ -231,7 +221,8 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
       const uint32_t tx = weights ? kQSlotA * ((t.m_here > 0) + (t.m_peer > 0)) : 2 * (two ? 2 : 1) * box * 128;
       const int n0 = t.n0 + rank * half;
       for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort));
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[stage], phase ^ 1u, abort) &&
+                                         mbar_wait(&read_bar[stage], phase ^ 1u, abort));
         if (!ok) break;
         if (elect_one()) {
           if (lead) mbar_arrive_expect_tx(&full_bar[stage], tx);
@@ -272,42 +263,33 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   } else if (warp == 1) {
     if (lead) {
       // ------------------------------------------------------------ MMA issuer (first CTA)
-      int stage = 0, acc = 1;
+      int stage = 0, acc = 1, set = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       const uint64_t da0 = sdesc_k_major(smem_u32(sA), 128), db0 = sdesc_k_major(smem_u32(sB), 128);
-      const uint64_t ds0 = sdesc_scales(smem_u32(sS));
-      const uint32_t sfa = tmem_base + kQColsA, sfb = tmem_base + kQColsB;
       for (int idx = first; idx < total; idx += step) {
         const Tile t = tile(idx);
         acc ^= 1;
         if (t.nkb == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty_bar[acc], ~(acc_phase >> acc) & 1u, abort));
         if (ok) tc_fence_after();
-        const uint32_t idesc = idesc_fp4<kNv>(t.n), d = tmem_base + acc * kQAccCols;
-        const bool wide = kWide && t.n > 128;
+        const uint32_t idesc = idesc_fp4<kNv>(t.n), d = tmem_base + acc * kQMost;
         for (int ks = 0; ok && ks < nks; ks += 4) {
           ok = __all_sync(0xffffffffu, mbar_wait<true>(&full_bar[stage], phase, abort) &&
                                            mbar_wait<true>(&scale_bar[stage], phase, abort));
           if (!ok) break;
           tc_fence_after();
           const uint64_t da = da0 + ((stage * kQSlotA) >> 4), db = db0 + ((stage * Q::kSlotB) >> 4);
-          const uint64_t ds = ds0 + ((stage * Q::kScaleBytes) >> 4);
+          const uint32_t sfa = tmem_base + Q::kScales + set * Q::kSet, sfb = sfa + Q::kColsA;
+          set ^= 1;
           if (elect_one()) {
-            constexpr int kWords = kNv ? 4 : 2;   // of scales in a block
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-              tmem_copy_scales_pair(sfa + 4 * j, ds + ((j * kQAtom) >> 4));
-              tmem_copy_scales_pair(sfb + 8 * j, ds + (((4 + Q::kAtomsB * j) * kQAtom) >> 4));
-              if (wide) tmem_copy_scales_pair(sfb + 8 * j + 4, ds + (((5 + 2 * j) * kQAtom) >> 4));
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (ks + i >= nks) break;
               const int j = kNv ? i : i / 2;
               const uint32_t part = kNv ? 0u : static_cast<uint32_t>(i & 1) * 2u;
               umma_fp4_pair<kNv>(d, da + i * 2, db + i * 2, idesc | part << 29 | part << 4, sfa + 4 * j,
-                                 sfb + 8 * j, (ks | i) != 0);
+                                 sfb + Q::kPitchB * j, (ks | i) != 0);
             }
             umma_commit_pair(&empty_bar[stage], kQPairMask);
           }
@@ -334,99 +316,73 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     }
   } else if (warp < kQEpiWarp) {
     // ------------------------------------------------------------ scales (both CTAs)
-    // This warp's rows of each 128: l = 8 * w .. + 7 in lanes by rows l, l + 32, l + 64, l + 96.
-    constexpr int kWords = kNv ? 4 : 2;
-    const int l = 8 * ((warp - kQScaleWarp) % kQScaleWarps) + (lane & 7), i = lane >> 3;
+    // Block by block in turn, a team's always with the same set of columns.
+    constexpr int kWords = Q::kWords;
     const int team = (warp - kQScaleWarp) / kQScaleWarps;
-    const int row = l + 32 * i;
-    // A row's scales of block kb, those past the row's end as zeros.
-    auto words = [&](const uint8_t* raw_rows, int kb) {
-      uint4 v = *reinterpret_cast<const uint4*>(raw_rows + row * 16);
-      if (!kNv) {
-        if (kb & 1) {
-          v.x = v.z;
-          v.y = v.w;
-        }
-        v.z = v.w = 0;
-      }
+    const uint32_t ts = tmem_base + Q::kScales + team * Q::kSet + (static_cast<uint32_t>(warp & 3) << 21);
+    // Word j of rows lane, lane + 32, ... to registers j * pitch + i, what is past the rows' ends as zeros.
+    auto words = [&](const uint8_t* rows, int n, int pitch, int kb, uint32_t* out) {
       const int left = q.blocks - kb * 4 * kWords;   // bytes that are scales
-      if (left < 4 * kWords) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-          const int n = left - 4 * j;
-          if (n < 4) w[j] = n <= 0 ? 0u : w[j] & ((1u << (8 * n)) - 1u);
-        }
-      }
-      return v;
-    };
-    // 4 x 4 words between lanes i = 0..3 of the same l: lane i gets word i of each.
-    auto turn = [&](uint4 v) {
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      // words whose index differs from i in bit 0, then in bit 1, change places
-      {
-        const bool odd = i & 1;
-        const uint32_t s0 = odd ? w[0] : w[1], s1 = odd ? w[2] : w[3];
-        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 8), r1 = __shfl_xor_sync(0xffffffffu, s1, 8);
-        if (odd) {
-          w[0] = r0;
-          w[2] = r1;
+      for (int i = 0; i < n; ++i) {
+        const uint8_t* src = rows + (32 * i + lane) * 16;
+        uint32_t w[kWords];
+        if constexpr (kNv) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src);
+          w[0] = v.x;
+          w[1] = v.y;
+          w[2] = v.z;
+          w[3] = v.w;
         } else {
-          w[1] = r0;
-          w[3] = r1;
+          const uint2 v = *reinterpret_cast<const uint2*>(src + (kb & 1) * 8);
+          w[0] = v.x;
+          w[1] = v.y;
         }
-      }
-      {
-        const bool high = i & 2;
-        const uint32_t s0 = high ? w[0] : w[2], s1 = high ? w[1] : w[3];
-        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 16), r1 = __shfl_xor_sync(0xffffffffu, s1, 16);
-        if (high) {
-          w[0] = r0;
-          w[1] = r1;
-        } else {
-          w[2] = r0;
-          w[3] = r1;
+        if (left < 4 * kWords) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            const int m = left - 4 * j;
+            if (m < 4) w[j] = m <= 0 ? 0u : w[j] & ((1u << (8 * m)) - 1u);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) out[j * pitch + i] = w[j];
       }
-      return make_uint4(w[0], w[1], w[2], w[3]);
     };
-    int stage = 0;
-    uint32_t phase = 0;
+    int stage = 0, set = 0, before = -1;             // before: the team's stage before this one
+    uint32_t phase = 0, before_phase = 0;
     bool ok = true;
     for (int idx = first; idx < total && ok; idx += step) {
       const Tile t = tile(idx);
       if (t.nkb == 0) continue;
       const bool wide = kWide && t.n > 128;
       for (int kb = 0; kb < nkb; ++kb) {
-        // (kQStages is even: a stage is always the same team's. Its place has been given back before its
-        // scales were asked for.)
-        if ((stage & 1) != team) {
-          if (++stage == kQStages) {
-            stage = 0;
-            phase ^= 1u;
+        if (set == team) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&raw_bar[stage], phase, abort));
+          if (!ok) break;
+          const uint8_t* raw_s = sRaw + stage * Q::kRawBytes;
+          uint32_t sa[Q::kColsA], sb[Q::kColsB] = {};
+          words(raw_s + 128 * 16, 4, Q::kPitchB, kb, sb);
+          if (wide) words(raw_s + 256 * 16, 4, Q::kPitchB, kb, sb + 4);
+          // The products that had this set of columns before are done.
+          if (before >= 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait<true>(&empty_bar[before], before_phase, abort));
+            if (!ok) break;
           }
-          continue;
+          tc_fence_after();
+          tmem_store(ts + Q::kColsA, sb);
+          words(raw_s, 4, 4, kb, sa);                // (now: both at once would not fit the registers)
+          tmem_store(ts, sa);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&read_bar[stage]);
+          tmem_store_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(lead_scale + 8u * stage);
+          before = stage;
+          before_phase = phase;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&raw_bar[stage], phase, abort));
-        if (!ok) break;
-        const uint8_t* raw_s = sRaw + stage * Q::kRawBytes;
-        uint8_t* dst = sS + stage * Q::kScaleBytes + l * 16;
-        const uint4 va = turn(words(raw_s, kb)), vb = turn(words(raw_s + 128 * 16, kb));
-        uint4 vc = {};
-        if (wide) vc = turn(words(raw_s + 256 * 16, kb));
-        if (i < kWords) {
-          *reinterpret_cast<uint4*>(dst + i * kQAtom) = va;
-          *reinterpret_cast<uint4*>(dst + (4 + Q::kAtomsB * i) * kQAtom) = vb;
-          if (wide) *reinterpret_cast<uint4*>(dst + (5 + 2 * i) * kQAtom) = vc;
-        }
-        // What reads these is this SM's own tensor core, whichever CTA's thread issues the copy: the proxy
-        // fence orders the two here, and the arrival need not release to the other SM (1400 cycles).
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if (lead) mbar_arrive(&scale_bar[stage]);
-          else mbar_arrive_remote(lead_scale + 8u * stage);
-        }
+        set ^= 1;
         if (++stage == kQStages) {
           stage = 0;
           phase ^= 1u;
@@ -439,7 +395,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const int quarter = warp & 3;   // TMEM lane quarter of this warp
     const int acc = (warp - kQEpiWarp) >> 2;
     uint8_t* buf = sOut + (warp - kQEpiWarp) * kQBoxBytes;
-    const uint32_t tb = tmem_base + acc * kQAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tb = tmem_base + acc * kQMost + (static_cast<uint32_t>(quarter * 32) << 16);
     int sbuf = 0;
     uint32_t acc_phase = 0;
     const bool f16 = a.f16 != 0;
@@ -566,14 +522,14 @@ moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   int have = clusters_dev[dev].load(std::memory_order_acquire);
   if (!have) {
     const cudaError_t e = cudaFuncSetAttribute(
-        experts_fp4_kernel<kNv, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmemBytes<kWide>);
+        experts_fp4_kernel<kNv, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmemBytes<kNv, kWide>);
     if (e != cudaSuccess)
       return set_error(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     const int sms = device_sm_count();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
     cfg.blockDim = dim3(kQThreads, 1, 1);
-    cfg.dynamicSmemBytes = kQSmemBytes<kWide>;
+    cfg.dynamicSmemBytes = kQSmemBytes<kNv, kWide>;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, experts_fp4_kernel<kNv, kWide>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();   // clear the failed query; fall back to one cluster per SM pair
@@ -584,7 +540,7 @@ moe_status launch_fp4(const CUtensorMap& mw, const CUtensorMap& mx, const CUtens
   }
   const unsigned pairs = static_cast<unsigned>(have < tiles ? have : tiles);
   const cudaError_t err = launch_pdl(experts_fp4_kernel<kNv, kWide>, dim3(2 * pairs), dim3(kQThreads),
-                                     kQSmemBytes<kWide>, s, mw, mx, mx32, mws, mxs, mo, q);
+                                     kQSmemBytes<kNv, kWide>, s, mw, mx, mx32, mws, mxs, mo, q);
   if (err != cudaSuccess)
     return set_error(MOE_ERR_CUDA, "experts_fp4 launch: %s", cudaGetErrorString(err));
   return MOE_OK;
@@ -632,7 +588,8 @@ moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const in
   // 128 experts of 32, 64 rows: narrow 44, 56, wide 48, 50 (experts of more than 64 rows read their weights
   // again for every narrow tile).
   const bool wide = R > static_cast<int64_t>(kQNarrowRows) * E;
-  const int64_t tiles = (R / (wide ? QTile<true>::kMost : QTile<false>::kMost) + E + 2) * ((N + 255) / 256);
+  const int most = !wide ? QTile<true, false>::kMost : fmt == kFp4Nv ? QTile<true, true>::kMost : QTile<false, true>::kMost;
+  const int64_t tiles = (R / most + E + 2) * ((N + 255) / 256);
   if (wide)
     return fmt == kFp4Nv ? launch_fp4<true, true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s)
                          : launch_fp4<false, true>(mw, mx, mx32, mws, mxs, mo, q, tiles, s);

@@ -1,8 +1,10 @@
 """GPU: the serving operators with scales and factors far from 1, where the results themselves are in range.
 Multiplying by powers of two rounds nothing, so that such results are the same bits, moved."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import serve_oracle as ref
 from tests.test_layer_few import Layer
 
 pytestmark = [pytest.mark.gpu,
@@ -75,3 +77,57 @@ def test_a_small_token_changes_no_other(moe, T):
     assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, want))
     assert not got[0][2].any()
     layer.check(got, x=x)
+
+
+def uneven_scales(moe, shape, fmt, seed):
+    """(Fp4, its values in float64): random codes, neighbouring blocks' scales apart by up to 2^16 (mx) or 2^12."""
+    rng = np.random.default_rng(seed)
+    K = shape[-1]
+    codes = rng.integers(0, 256, shape[:-1] + (K // 2,)).astype(np.uint8)
+    scales = np.full(shape[:-1] + (moe.Fp4.scale_columns(K, fmt),), 255, np.uint8)
+    blocks = K // ref.BLOCK[fmt]
+    if fmt == ref.MX:
+        scales[..., :blocks] = rng.integers(119, 136, shape[:-1] + (blocks,))
+    else:
+        scales[..., :blocks] = rng.integers(8, 104, shape[:-1] + (blocks,))
+    q = moe.Fp4(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), fmt)
+    flat = lambda a: a.reshape(-1, a.shape[-1])   # noqa: E731
+    return q, ref.dequantize(flat(codes), flat(scales), fmt).reshape(shape)
+
+
+# Wide and narrow tiles; rows on both sides of 64, 128, 208, 224 and a multiple of each; many blocks of contraction,
+# one, and ones that end inside a block.
+@pytest.mark.parametrize("rows,E,K,N", [(63, 1, 2048, 256), (65, 2, 1312, 520), (127, 1, 4096, 264), (129, 3, 1568, 256),
+                                        (207, 1, 2080, 512), (208, 2, 256, 256), (209, 1, 3104, 264), (223, 1, 2048, 248),
+                                        (225, 2, 2336, 256), (416, 1, 1024, 1032), (448, 3, 544, 512), (40, 60, 2048, 512)])
+@pytest.mark.parametrize("fmt", [ref.MX, ref.NV])
+def test_each_block_has_its_own_scales(moe, fmt, rows, E, K, N):
+    x, X = uneven_scales(moe, (rows * E, K), fmt, rows)
+    w, W = uneven_scales(moe, (E, N, K), fmt, rows + 1)
+    off = np.arange(E + 1, dtype=np.int32) * rows
+    o = torch.from_numpy(off).cuda()
+    y = moe.moe_experts_matmul_fp4(x, w, o)
+    want, mag = ref.experts_matmul(X, W, off), ref.experts_matmul(np.abs(X), np.abs(W), off)
+    # one rounding to bf16, sums of K terms in the tensor cores
+    assert (np.abs(y.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + K * 2.0 ** -23 * mag * 1.01).all()
+    for _ in range(20):
+        assert torch.equal(y, moe.moe_experts_matmul_fp4(x, w, o))
+    assert moe.moe_read_timeouts() == (moe.MOE_OK, 0)
+
+
+def test_products_on_two_streams_at_once(moe):
+    parts = []
+    for fmt, rows, E in ((ref.NV, 300, 4), (ref.MX, 12, 64)):
+        x, w = uneven_scales(moe, (rows * E, 2048), fmt, rows)[0], uneven_scales(moe, (E, 1536, 2048), fmt, E)[0]
+        off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * rows
+        parts.append((x, w, off, moe.moe_experts_matmul_fp4(x, w, off)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in parts]
+    got = [[], []]
+    for _ in range(30):
+        for i, (x, w, off, _) in enumerate(parts):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(moe.moe_experts_matmul_fp4(x, w, off))
+    torch.cuda.synchronize()
+    assert moe.moe_read_timeouts() == (moe.MOE_OK, 0)
+    assert all(torch.equal(g, parts[i][3]) for i in range(2) for g in got[i])
