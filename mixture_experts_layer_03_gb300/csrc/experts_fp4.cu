@@ -91,6 +91,16 @@ __device__ __forceinline__ void q_timeout(volatile int* abort) {
   atomicOr(&g_fp4_timeouts, MOE_DEVICE_FLAG_TIMEOUT);
 }
 
+// Two factors whose product is a b, where f32 does not hold that: each with half of the exponent. (A sum is 0 or
+// between 2^-20 and 2^39, so that from 2^250 or 2^-250 on the result is past f32's range either way.)
+__device__ __noinline__ void split_gain(float a, float b, float& gain, float& rest) {
+  int ea, eb;
+  const float m = frexpf(a, &ea) * frexpf(b, &eb);
+  const int e = max(-250, min(250, ea + eb)), half = e / 2;
+  gain = ldexpf(m, half);
+  rest = ldexpf(1.0f, e - half);
+}
+
 // D (+)= A B^T of the pair, 64 elements of the contraction of e2m1 with scales in TMEM.
 template <bool kNv>
 __device__ __forceinline__ void umma_fp4_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
@@ -425,7 +435,9 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         done();
         continue;
       }
-      const float gain = gx * (q.w_g && !zeros ? __ldg(q.w_g + t.g) : 1.0f);
+      const float gw = q.w_g && !zeros ? __ldg(q.w_g + t.g) : 1.0f;
+      float gain = gx * gw, rest = 1.0f;
+      if (!(gain >= 0x1p-126f && gain < INFINITY)) split_gain(gx, gw, gain, rest);
       const int ch = t.m0 + 32 * quarter;
       // 32 channels by 32 rows at a time, as the 16-bit products' epilogue: read in matrix fragments,
       // turned over by the matrix store into a box of 32 rows of 64 bytes, out by TMA.
@@ -443,6 +455,11 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
           for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = 0;
         }
         if (r0 + 32 >= t.n_here) done();
+        if (rest != 1.0f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j >> 4][j & 15] = __float_as_uint(rest * __uint_as_float(v[j >> 4][j & 15]));
+        }
         uint32_t p[16];   // [channels 8 b .. + 7][rows 8 i .. + 7]: p[4 i + b]
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -131,3 +131,34 @@ def test_products_on_two_streams_at_once(moe):
     torch.cuda.synchronize()
     assert moe.moe_read_timeouts() == (moe.MOE_OK, 0)
     assert all(torch.equal(g, parts[i][3]) for i in range(2) for g in got[i])
+
+
+@pytest.mark.parametrize("gx,gw", [(1.3 * 2.0 ** 100, 1.1 * 2.0 ** 100), (2.0 ** 127, 2.0 ** 127), (1.3 * 2.0 ** -70, 1.7 * 2.0 ** -70),
+                                   (2.0 ** -149, 1.5), (2.0 ** -149, None), (1.9 * 2.0 ** -126, 2.0 ** -20), (1.5 * 2.0 ** 120, 1.3 * 2.0 ** -120),
+                                   (2.0 ** 127, 2.0 ** -149), (2.0 ** -100, 2.0 ** -100)])
+@pytest.mark.parametrize("rows", [5, 300])
+def test_factors_whose_product_f32_does_not_hold(moe, rows, gx, gw):
+    """Rows and channels of zeros give zeros; the others what the factors make of them."""
+    K, N = 4096, 264
+    rng = np.random.default_rng(rows)
+    parts = []
+    for shape in ((rows, K), (2, N, K)):
+        codes = np.full(shape[:-1] + (K // 2,), 0x77, np.uint8)           # 6 and 6
+        codes ^= (rng.integers(0, 16, codes.shape) == 0).astype(np.uint8) * 0x84     # some -6 and 1
+        codes[..., ::7, :] = 0
+        parts.append((codes, rng.integers(100, 127, shape[:-1] + (K // 16,)).astype(np.uint8)))
+    (cx, sx), (cw, sw) = parts
+    t = lambda a: torch.from_numpy(a).cuda()   # noqa: E731
+    g = lambda v, n: None if v is None else torch.full((n,), v, device="cuda")   # noqa: E731
+    x, w = moe.Fp4(t(cx), t(sx), ref.NV, g(gx, 1)), moe.Fp4(t(cw), t(sw), ref.NV, g(gw, 2))
+    off = np.array([0, rows // 2, rows - 1], np.int32)
+    y = moe.moe_experts_matmul_fp4(x, w, t(off)).double().cpu().numpy()
+    X, W = ref.dequantize(cx, sx, ref.NV), ref.dequantize(cw.reshape(2 * N, -1), sw.reshape(2 * N, -1), ref.NV).reshape(2, N, K)
+    by = float(np.float32(gx)) * (1.0 if gw is None else float(np.float32(gw)))
+    want, mag = by * ref.experts_matmul(X, W, off), by * ref.experts_matmul(np.abs(X), np.abs(W), off)
+    assert np.array_equal(y == 0, np.abs(want) <= 2.0 ** -134) and not np.isnan(y).any()
+    big = np.abs(want) > 2.0 ** 128
+    assert np.isinf(y[big]).all() and (np.sign(y[big]) == np.sign(want[big])).all() and np.isfinite(y[~big]).all()
+    # bf16's rounding and its subnormal step, sums of K terms, the factors' two roundings
+    bound = 2.0 ** -8 * np.abs(want) + (K * 2.0 ** -23 + 2.0 ** -22) * mag * 1.01 + 2.0 ** -134
+    assert (np.abs(y - want) <= bound)[~big].all()
