@@ -1093,12 +1093,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
             const int row = (l >> 2) + 8 * (j >> 1), t = n * 8 + (l & 3) * 2 + (j & 1);
             const int sl = t < T ? sh.slot[p.a][t] : -1;
             if (sl < 0 || row >= p.of(s)) continue;
-            float f = sh.x_inv[t] * g13;
+            // (one after the other: their product may be past f32's range where the sums are 0)
+            const float f = sh.x_inv[t], f2 = kW == kW4mx ? 1.0f / sh.x_unit : g13;
             float gate = sum_at(p.subs, s, 0, n, at_) * f, up = sum_at(p.subs, s, 1, n, at_) * f;
-            if constexpr (kW == kW4mx) {
-              f = 1.0f / sh.x_unit;
-              gate *= f;
-              up *= f;
+            if constexpr (W::k4) {
+              gate *= f2;
+              up *= f2;
             }
             const float wt = own ? sh.scales[t * a.k + sl] : sh.weight_s[t];
             const float ex = expf(-fabsf(gate));

@@ -162,3 +162,15 @@ def test_factors_whose_product_f32_does_not_hold(moe, rows, gx, gw):
     # bf16's rounding and its subnormal step, sums of K terms, the factors' two roundings
     bound = 2.0 ** -8 * np.abs(want) + (K * 2.0 ** -23 + 2.0 ** -22) * mag * 1.01 + 2.0 ** -134
     assert (np.abs(y - want) <= bound)[~big].all()
+
+
+@pytest.mark.parametrize("T", [2, 10])
+def test_weights_of_zeros_and_large_tokens(moe, T):
+    """First products that are zeros, whatever x and the experts' factor are."""
+    layer = Layer(moe, T, 128, 64, 4, 2, 4, "nv", "bf16")
+    layer.wg.zero_()
+    layer.x.fill_(2.0 ** 125)
+    layer.w13.codes.zero_()
+    layer.w13.g.fill_(2.0 ** 60)
+    y = layer()[0]
+    assert not y.any()
