@@ -919,18 +919,27 @@ def _new_fp4(shape, format: int, g, device, stream, out: Optional[Fp4]) -> Fp4:
                    _new(head + (Fp4.scale_columns(K, format),), torch.uint8, device, stream), format, g)
 
 
+def _written_fp4(q: Fp4, out: Optional[Fp4]) -> Fp4:
+    """What a conversion returns: `out`, where one was given, with the g that its new values stand for."""
+    if out is None:
+        return q
+    out.g = q.g
+    return out
+
+
 def moe_quantize_fp4(x, format: int, g: Optional[torch.Tensor] = None, out: Optional[Fp4] = None,
                      stream=None) -> Fp4:
     """x [rows, K] or [planes, rows, K] in 4 bits (MOE_FP4_MX or MOE_FP4_NV). g (MOE_FP4_NV): f32, one
     value or one for each plane, by which values are divided first: amax / (6 * 448) uses all of the
-    scales' range; kept in the result. out: an Fp4 whose codes and scales are written."""
+    scales' range; kept in the result. out: an Fp4 whose codes and scales are written and whose g becomes
+    this one; returned."""
     dt = _typed(x, "x", 3 if x.dim() == 3 else 2)
     q = _new_fp4(x.shape, format, g, x.device, stream, out)
     planes = x.shape[0] if x.dim() == 3 else 1
     _check(_lib.moe_quantize_fp4(x.data_ptr(), planes, x.shape[-2], x.shape[-1], dt, format, _ptr(g),
                                  q.codes.data_ptr(), q.scales.data_ptr(), _stream(stream)),
            "moe_quantize_fp4")
-    return q
+    return _written_fp4(q, out)
 
 
 def moe_swiglu_fp4(gu, format: int, g: Optional[torch.Tensor] = None, out: Optional[Fp4] = None,
@@ -943,7 +952,7 @@ def moe_swiglu_fp4(gu, format: int, g: Optional[torch.Tensor] = None, out: Optio
     q = _new_fp4((R, I2 // 2), format, g, gu.device, stream, out)
     _check(_lib.moe_swiglu_fp4(gu.data_ptr(), R, I2 // 2, dt, format, _ptr(g), q.codes.data_ptr(),
                                q.scales.data_ptr(), _stream(stream)), "moe_swiglu_fp4")
-    return q
+    return _written_fp4(q, out)
 
 
 def moe_dequantize_fp4(q: Fp4, dtype=torch.bfloat16, out=None, stream=None):
