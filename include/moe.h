@@ -518,6 +518,11 @@ moe_status moe_layer_few(const moe_problem* p, const moe_route_params* route, co
                          int32_t weights, moe_dtype dtype, int32_t* ids, float* scales, void* y,
                          void* workspace, size_t ws_bytes, void* stream);
 
+/* moe_selftest_experts_wait of the products on 4-bit operands and of moe_layer_few: a wait as each has
+ * them runs out after about 2 s and is reported by moe_read_timeouts, with no fault and no hang. */
+moe_status moe_selftest_fp4_wait(void* stream);
+moe_status moe_selftest_few_wait(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -142,6 +142,8 @@ _SIGS = {
                                              _P]),
     "moe_read_timeouts": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "moe_selftest_experts_wait": (ctypes.c_int, [_P]),
+    "moe_selftest_fp4_wait": (ctypes.c_int, [_P]),
+    "moe_selftest_few_wait": (ctypes.c_int, [_P]),
     "moe_route_backward": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64,
                                           ctypes.POINTER(MoeRouteParams), _P, _P]),
     "moe_quantize_fp4": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
@@ -822,9 +824,10 @@ def moe_experts_matmul_dw(dy, x, offsets, dw=None, dw_dtype=None, accumulate: bo
 
 
 def moe_read_timeouts(stream=None):
-    """Synchronise; read and clear whether a wait of the experts' products or of the gate ran out in any
-    call on the current GPU since the last read (its results are incomplete then), whether or not
-    the call was given a scratch. Returns (status, flags)."""
+    """Synchronise; read and clear whether a wait of the experts' products (on 16-bit or 4-bit operands),
+    of the gate or of moe_layer_few ran out in any call on the current GPU since the last read (its
+    results are incomplete then), whether or not the call was given a scratch. Returns (status,
+    flags)."""
     flags = ctypes.c_int32(0)
     st = _lib.moe_read_timeouts(_stream(stream), ctypes.byref(flags))
     return st, flags.value
@@ -833,6 +836,16 @@ def moe_read_timeouts(stream=None):
 def moe_selftest_experts_wait(stream=None):
     """Enqueue the self-test of moe_read_timeouts: a bounded wait that runs out after about 2 s."""
     _check(_lib.moe_selftest_experts_wait(_stream(stream)), "moe_selftest_experts_wait")
+
+
+def moe_selftest_fp4_wait(stream=None):
+    """The same of the products on 4-bit operands."""
+    _check(_lib.moe_selftest_fp4_wait(_stream(stream)), "moe_selftest_fp4_wait")
+
+
+def moe_selftest_few_wait(stream=None):
+    """The same of moe_layer_few."""
+    _check(_lib.moe_selftest_few_wait(_stream(stream)), "moe_selftest_few_wait")
 
 
 def moe_route_backward(logits, ids, dscales, method: int, routed_scaling_factor: float = 1.0,

@@ -108,6 +108,14 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
                             offsets, R, E, N, K, format, dtype, y, static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_selftest_fp4_wait(void* stream) {
+  return launch_fp4_wait_selftest(static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_selftest_few_wait(void* stream) {
+  return launch_few_wait_selftest(static_cast<cudaStream_t>(stream));
+}
+
 size_t moe_layer_few_workspace_bytes(const moe_problem* p) {
   return p && few_fits(*p) ? few_workspace_bytes(*p) : 0;
 }

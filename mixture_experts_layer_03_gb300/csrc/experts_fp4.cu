@@ -513,6 +513,20 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
   cluster_sync();
 }
 
+// A wait of the kernel above for a barrier that nothing arrives on.
+__global__ void __launch_bounds__(32) fp4_wait_selftest_kernel() {
+  __shared__ uint64_t bar;
+  __shared__ int s_abort;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  volatile int* abort = &s_abort;
+  if (!__all_sync(0xffffffffu, mbar_wait<true>(&bar, 0, abort))) q_timeout(abort);
+}
+
 // Bytes [planes, rows, cols] (planes 0: a matrix), boxes of 128 (with the 128-byte swizzle) or 16 by box_rows.
 bool encode_bytes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
                   uint32_t box_cols, uint32_t box_rows) {
@@ -569,6 +583,13 @@ moe_status fp4_timeout_word(void** word) {
   const cudaError_t e = cudaGetSymbolAddress(word, g_fp4_timeouts);
   return e == cudaSuccess ? MOE_OK
                           : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
+
+moe_status launch_fp4_wait_selftest(cudaStream_t s) {
+  fp4_wait_selftest_kernel<<<1, 32, 0, s>>>();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "self-test launch: %s", cudaGetErrorString(e));
 }
 
 moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const int32_t* offsets, int64_t R,

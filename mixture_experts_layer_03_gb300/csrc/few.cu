@@ -1148,6 +1148,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const __grid_
   __syncthreads();
 }
 
+// The waits of the kernel above, for a barrier that nothing arrives on and for a count that does not come: the
+// first to run out ends the other.
+__global__ void __launch_bounds__(64) few_wait_selftest_kernel() {
+  __shared__ uint64_t bar;
+  __shared__ int s_abort;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  volatile int* abort = &s_abort;
+  if (threadIdx.x < 32) {
+    if (!__all_sync(0xffffffffu, few_wait(&bar, 0, abort))) few_timeout(abort);
+  } else {
+    // Half a limit later, so that the abort flag ends it before its own limit does.
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kWaitLimitNs / 2) __nanosleep(1000000);
+    if (!__all_sync(0xffffffffu, wait_count(&g_few_timeouts, INT32_MAX, abort))) few_timeout(abort);
+  }
+}
+
 template <int kW, int kNt>
 moe_status launch_layer(const FewArgs& a, cudaStream_t s) {
   static std::atomic<bool> ready[64];
@@ -1201,6 +1223,13 @@ moe_status few_timeout_word(void** word) {
   const cudaError_t e = cudaGetSymbolAddress(word, g_few_timeouts);
   return e == cudaSuccess ? MOE_OK
                           : set_error(MOE_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+}
+
+moe_status launch_few_wait_selftest(cudaStream_t s) {
+  few_wait_selftest_kernel<<<1, 64, 0, s>>>();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MOE_OK
+                          : set_error(MOE_ERR_CUDA, "self-test launch: %s", cudaGetErrorString(e));
 }
 
 size_t few_workspace_bytes(const moe_problem& p) {

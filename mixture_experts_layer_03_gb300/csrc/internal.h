@@ -192,6 +192,8 @@ moe_status experts_timeout_word(void** word);
 moe_status fp4_timeout_word(void** word);
 moe_status gate_timeout_word(void** word);
 moe_status launch_experts_wait_selftest(cudaStream_t s);
+moe_status launch_fp4_wait_selftest(cudaStream_t s);
+moe_status launch_few_wait_selftest(cudaStream_t s);
 
 moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* ds,
                                  int64_t T, const moe_route_params& p, float* dl, cudaStream_t s);
