@@ -174,3 +174,65 @@ def test_weights_of_zeros_and_large_tokens(moe, T):
     layer.w13.g.fill_(2.0 ** 60)
     y = layer()[0]
     assert not y.any()
+
+
+def same_where(got, want, bad):
+    """NaN at `bad`, elsewhere the same bits."""
+    return torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], want[~bad])
+
+
+# A block of the second products has some 27 rows of 4096: rows in both halves of a stage. 8 blocks of 32 channels
+# of I, 128 of H: each byte of a word of four scales.
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("T", [5, 12])
+def test_a_scale_of_nan_reaches_its_expert_and_row_only(moe, T, fmt):
+    layer = Layer(moe, T, 4096, 256, 4, 1, 3, fmt, "bf16", seed=1)
+    want, ids, sc = layer()
+    assert torch.isfinite(want).all()
+    e = int(ids[0, 0])
+    hit = (ids[:, 0] == e)[:, None]
+    column = torch.arange(4096, device="cuda")[None]
+    nan = 255 if fmt == "mx" else 127
+    for at in range(8):
+        for rows, of in ((layer.w13.scales[e, 3 + 31 * at], hit.expand(T, 4096)),            # a gate's
+                         (layer.w13.scales[e, 256 + 17 * at], hit.expand(T, 4096)),          # an up's
+                         (layer.w2.scales[e, 27 * at + 2], hit & (column == 27 * at + 2)),
+                         (layer.w2.scales[e, 4095 - 27 * at], hit & (column == 4095 - 27 * at))):
+            kept = int(rows[at])
+            rows[at] = nan
+            got = layer()
+            assert same_where(got[0], want, of) and torch.equal(got[1], ids) and torch.equal(got[2], sc)
+            rows[at] = kept
+    assert torch.equal(layer()[0], want)
+
+
+@pytest.mark.parametrize("T", [5, 12])
+def test_the_largest_mx_scale_is_no_nan(moe, T):
+    """2^127 on blocks of zeros."""
+    layer = Layer(moe, T, 512, 256, 4, 2, 3, "mx", "bf16", seed=2)
+    for q in (layer.w13, layer.w2):
+        q.codes.view(*q.codes.shape[:-1], -1, 16)[..., 1::3, :] = 0
+    want = layer()
+    assert torch.isfinite(want[0]).all()
+    for q in (layer.w13, layer.w2):
+        q.scales[..., 1:q.shape[-1] // 32:3] = 254
+    assert all(torch.equal(a, b) for a, b in zip(layer(), want))
+
+
+def test_an_mx_nan_in_the_products_stays_in_its_row_and_its_channel(moe):
+    x, w = uneven_scales(moe, (70, 512), ref.MX, 1)[0], uneven_scales(moe, (2, 264, 512), ref.MX, 2)[0]
+    off = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
+    want = moe.moe_experts_matmul_fp4(x, w, off)
+    assert torch.isfinite(want).all()
+    for at in range(16):
+        kept = int(x.scales[33, at]), int(w.scales[0, 100 + at, at])
+        x.scales[33, at] = w.scales[0, 100 + at, at] = 255
+        bad = torch.zeros((70, 264), dtype=torch.bool, device="cuda")
+        bad[33] = True
+        bad[:30, 100 + at] = True
+        assert same_where(moe.moe_experts_matmul_fp4(x, w, off), want, bad)
+        x.scales[33, at], w.scales[0, 100 + at, at] = kept
+    x.scales[33, 3] = 254                  # 2^127: whatever it makes, in that row alone
+    got = moe.moe_experts_matmul_fp4(x, w, off)
+    rest = torch.arange(70, device="cuda") != 33
+    assert torch.equal(got[rest], want[rest])
