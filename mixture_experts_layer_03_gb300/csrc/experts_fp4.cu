@@ -75,7 +75,7 @@ static_assert(kQSmemBytes<false, true> <= 232448 - 2048 && kQSmemBytes<false, fa
 constexpr int kQTmemCols = 512;
 static_assert(kQScaleTeams == 2 && kQScaleWarps == 4, "a team a set of scales, a warp a quarter of TMEM");
 constexpr uint16_t kQPairMask = 0x3;
-constexpr int kQNarrowRows = 48;
+constexpr int kQNarrowRows = 16;
 
 struct Fp4Args {
   ExpertsArgs e;
@@ -621,10 +621,12 @@ moe_status launch_experts_fp4(const Fp4Operand& x, const Fp4Operand& w, const in
   q.x_g = x.g;
   q.w_g = w.g;
   q.blocks = K / fp4_block(fmt);
-  // Wide tiles where the experts have more than 48 rows on average: N = 7168, K = 2048, mx, 256 experts of
-  // 8, 32, 48, 64, 96 rows: narrow 418, 341, 343, 460, 602 us, wide 442, 373, 372, 376, 390; N = 1536, nv,
-  // 128 experts of 32, 64 rows: narrow 44, 56, wide 48, 50 (experts of more than 64 rows read their weights
-  // again for every narrow tile).
+  // Wide tiles where the experts have more than 16 rows on average (an expert of more than 64 rows reads its
+  // weights again for every narrow tile). N = 7168, K = 2048, mx, 256 experts of 8, 16, 32, 48 rows on average,
+  // all alike: narrow 411, 370, 343, 342 us, wide 435, 387, 356, 355; spread log-normally, sigma 1: narrow 398, 389,
+  // 397, 437, wide 415, 401, 377, 378; as 1 / rank, an expert having a row of each token at most, eight a token:
+  // narrow 464, 443, 441, 482, wide 474, 436, 416, 421. N = 1536, nv, 128 experts of 4, 16, 32: all alike narrow
+  // 45, 42, 43, wide 47, 44, 45; log-normally 38, 42, 46 and 40, 43, 46.
   const bool wide = R > static_cast<int64_t>(kQNarrowRows) * E;
   const int most = !wide ? QTile<true, false>::kMost : fmt == kFp4Nv ? QTile<true, true>::kMost : QTile<false, true>::kMost;
   const int64_t tiles = (R / most + E + 2) * ((N + 255) / 256);

@@ -236,3 +236,17 @@ def test_an_mx_nan_in_the_products_stays_in_its_row_and_its_channel(moe):
     got = moe.moe_experts_matmul_fp4(x, w, off)
     rest = torch.arange(70, device="cuda") != 33
     assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("hot", [65, 128, 209, 700])
+@pytest.mark.parametrize("fmt", [ref.MX, ref.NV])
+def test_most_rows_in_one_of_many_experts(moe, fmt, hot):
+    E, K, N = 64, 800, 328
+    rows = np.zeros(E, int)
+    rows[E // 2], rows[3], rows[E - 1] = hot, 5, 17
+    off = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    x, X = uneven_scales(moe, (int(off[-1]), K), fmt, hot)
+    w, W = uneven_scales(moe, (E, N, K), fmt, hot + 1)
+    y = moe.moe_experts_matmul_fp4(x, w, torch.from_numpy(off).cuda())
+    want, mag = ref.experts_matmul(X, W, off), ref.experts_matmul(np.abs(X), np.abs(W), off)
+    assert (np.abs(y.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + K * 2.0 ** -23 * mag * 1.01).all()
