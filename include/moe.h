@@ -489,7 +489,7 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
  * expert's gate, moe_forward_partial's) of T <= MOE_FEW_TOKENS tokens without the launches between them.
  *   p        T, H, I, E, k and shared_I (0: no shared expert); H, I and shared_I multiples of 32, H up to
  *            32768, I and shared_I to 65536
- *   route    as moe_route takes it, num_experts = E, top_k = k
+ *   route    as moe_route takes it (DeepSeekV3 also with more than 32 experts a group), num_experts = E, top_k = k
  *   x [T, H], wg [E (+ 1), H] of `dtype` (BF16 or F16); shared_gate 1: wg's last row is the shared
  *            expert's gate, whose sigmoid is its weight, 0: weight 1
  *   w13 [E, 2I, H], w2 [E, H, I], w13_s [2 shared_I, H], w2_s [H, shared_I] (NULL without a shared expert)

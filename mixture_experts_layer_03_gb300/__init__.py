@@ -1038,7 +1038,7 @@ def moe_layer_few(x, wg, w13, w2, method: int, top_k: int, bias: Optional[torch.
     (and the shared one) and the weighted sum. x [T, H] and wg [E, H] in bfloat16 or float16; w13
     [E, 2I, H] and w2 [E, H, I] (w13_s [2Is, H], w2_s [H, Is]) of the same type, or all Fp4 of one
     format. A wg with E + 1 rows carries the shared expert's gate in its last row. Routing parameters as
-    moe_route's. Returns (y [T, H], ids int32 [T, k], scales fp32 [T, k]). moe_read_timeouts says whether
+    moe_route's (and groups of any two or more experts). Returns (y [T, H], ids int32 [T, k], scales fp32 [T, k]). moe_read_timeouts says whether
     a wait ran out."""
     code = _typed(x, "x", 2)
     if code == MOE_DTYPE_F32:

@@ -36,7 +36,7 @@ std::atomic<int> g_sm_count[64];
 
 }  // namespace
 
-int32_t route_reason(int64_t T, const moe_route_params& r) {
+int32_t route_reason(int64_t T, const moe_route_params& r, int most_in_group) {
   if (T < 0 || T > (int64_t{1} << 31) / 8) return MOE_REASON_T_RANGE;
   if (r.num_experts < 1 || r.num_experts > 256) return MOE_REASON_E_RANGE;
   if (r.top_k < 1 || r.top_k > 8 || r.top_k > r.num_experts) return MOE_REASON_TOPK_RANGE;
@@ -53,7 +53,7 @@ int32_t route_reason(int64_t T, const moe_route_params& r) {
       // top_k <= 8, E <= 256, experts per group <= 32, experts per group * topk_group <= 256.
       if (r.n_group < 1 || r.n_group > 32 || r.num_experts % r.n_group != 0) return MOE_REASON_GROUPS;
       const int epg = r.num_experts / r.n_group;
-      if (epg < 2 || epg > 32) return MOE_REASON_GROUPS;
+      if (epg < 2 || epg > most_in_group) return MOE_REASON_GROUPS;
       if (r.topk_group < 1 || r.topk_group > r.n_group) return MOE_REASON_GROUPS;
       if (epg * r.topk_group > 256 || r.top_k > epg * r.topk_group) return MOE_REASON_GROUPS;
       return MOE_REASON_OK;

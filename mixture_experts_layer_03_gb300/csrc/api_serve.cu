@@ -137,7 +137,7 @@ moe_status moe_layer_few(const moe_problem* p, const moe_route_params* route, co
   if (route->num_experts != p->E || route->top_k != p->k)
     return set_error(MOE_ERR_INVALID_ARG, "route params of %d experts, %d slots for a layer of %d, %d",
                      route->num_experts, route->top_k, p->E, p->k);
-  const int32_t reason = route_reason(p->T, *route);
+  const int32_t reason = route_reason(p->T, *route, 256);
   if (reason == MOE_REASON_DEGENERATE)
     return set_error(MOE_ERR_UNSUPPORTED, "grouped top-k with softmax scoring: every group's score "
                      "is 1, so the group choice would rest on tie-breaking alone");

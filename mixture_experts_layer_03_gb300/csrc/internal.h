@@ -184,8 +184,9 @@ size_t few_workspace_bytes(const moe_problem& p);
 moe_status launch_few(const moe_problem& p, const FewLayer& f, char* ws, cudaStream_t s);
 moe_status few_timeout_word(void** word);
 
-// Why moe_route does not take these parameters (MOE_REASON_OK: it does).
-int32_t route_reason(int64_t T, const moe_route_params& p);
+// Why moe_route does not take these parameters (MOE_REASON_OK: it does). The limit on DeepSeekV3's experts a
+// group is that call's; the selection itself takes any number from 2 on.
+int32_t route_reason(int64_t T, const moe_route_params& p, int most_in_group = 32);
 
 // Device words in which the products' and the gate's kernels note that a wait ran out.
 moe_status experts_timeout_word(void** word);
