@@ -240,7 +240,8 @@ __device__ __forceinline__ Fp4Codes<N> fp4_swiglu_pairs(const float (&v)[N], con
     const Pair x = pair_exp(Pair{a <= 80.0f ? -a : 0.0f, 0.0f});
     const Pair s = pair_div(v[i] < 0.0f ? x : Pair{1.0f, 0.0f}, pair_add(Pair{1.0f, 0.0f}, x));
     const Pair y = pair_mul(pair_mul(s, v[i]), u[i]);
-    h[i] = y.hi;
+    // (pairs' sums lose the sign of a zero)
+    h[i] = y.hi != 0.0f ? y.hi : __uint_as_float((__float_as_uint(v[i]) ^ __float_as_uint(u[i])) & 0x80000000u);
     l[i] = y.lo;
     doubt |= !(a <= 80.0f) || (a > 0.0f && a < kLeastGate) || !(fabsf(y.hi) < 0x1p90f) ||
              (y.hi != 0.0f && fabsf(y.hi) < kLeastValue);

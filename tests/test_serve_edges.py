@@ -110,3 +110,20 @@ def test_layer_past_32_bit_offsets(moe):
     assert torch.equal(chosen[ids2[0].long()], ids[0].long())
     # (the gate's sums are the same for any number of rows)
     assert torch.equal(scales, scales2) and torch.isfinite(y).all() and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("fmt,g", [(ref.MX, None), (ref.NV, None), (ref.NV, 0.011)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_swiglu_of_zeros_beside_values_that_are_worked_out_again(moe, dtype, fmt, g):
+    """Small gates of few bits: their SwiGLU is next to a tie. Zeros of both signs in gates and up values keep the
+    sign of the product, in every segment."""
+    gen = torch.Generator().manual_seed(3)
+    R, I = 60, 800
+    gate = torch.randint(-12, 13, (R, I), generator=gen) * 2.0 ** -24
+    up = torch.randint(-9, 10, (R, I), generator=gen) * 0.25
+    gate = torch.where(torch.rand((R, I), generator=gen) < 0.1, -0.0, gate.double())
+    up = torch.where(torch.rand((R, I), generator=gen) < 0.1, -0.0, up.double())
+    gu = torch.cat([gate, up], 1).to(dtype)
+    q = moe.moe_swiglu_fp4(gu.cuda(), fmt, None if g is None else torch.full((1,), g, device="cuda"))
+    codes, scales = ref.quantize(ref.swiglu(gu.double().numpy()), fmt, None if g is None else float(np.float32(g)))
+    assert np.array_equal(q.scales.cpu().numpy(), scales) and np.array_equal(q.codes.cpu().numpy(), codes)
