@@ -487,6 +487,8 @@ moe_status moe_experts_matmul_fp4(const uint8_t* x_codes, const uint8_t* x_scale
 
 /* The whole layer for a few tokens, in two kernels: moe_gate_route and moe_forward (with the shared
  * expert's gate, moe_forward_partial's) of T <= MOE_FEW_TOKENS tokens without the launches between them.
+ * With 16-bit weights it takes less time than those two for a token or two, about as much for four; for more
+ * it is the slower one unless there are many experts and H is 4096 or more.
  *   p        T, H, I, E, k and shared_I (0: no shared expert); H, I and shared_I multiples of 32, H up to
  *            32768, I and shared_I to 65536
  *   route    as moe_route takes it (DeepSeekV3 also with more than 32 experts a group), num_experts = E, top_k = k

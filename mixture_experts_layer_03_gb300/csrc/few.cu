@@ -17,9 +17,11 @@
 // Every element of h and of y is summed by one block in one order: the same result on every run.
 //
 // Products by mma.sync m16n8k16: 16 rows of weights by 8 tokens, so that one pass over a weight serves all
-// tokens. (tcgen05's least M = 128 rows do not fit slices of some dozen rows; and mma.sync, 8 cycles an
-// instruction on an SM quarter, is used for a third of the time or less: a block's share of the
-// bandwidth brings 16 x 16 weights of 16 bits every 84 cycles, of 4 bits every 25.) All T tokens are
+// tokens. (tcgen05's least M, 64 rows of 16-bit operands in one CTA and 128 of 4-bit ones, does not fit slices of
+// some dozen rows. mma.sync takes 8 cycles an instruction on an SM quarter; a block's share of the bandwidth
+// brings 16 x 16 weights of 16 bits every 84 cycles, of 4 bits every 25: it is used for a third of the time or
+// less with one column tile, for a fifth with two of 16 bits and for two thirds with two of 4 bits, which is what
+// nv weights and 16 tokens would need at full bandwidth and, bound by the conversions, do not reach.) All T tokens are
 // columns for every expert, which keeps lists of tokens out of the loops: in the first products the others'
 // results are dropped, in the second an expert's sums are added to those of its tokens only (a weight
 // that is not finite reaches nobody else); the routing weight is multiplied into h.
@@ -262,8 +264,8 @@ __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) 
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
-// mbar_wait (ptx.cuh) that leaves the polling to the hardware for up to 20 us at a time: twenty warps that
-// poll by themselves keep the shared-memory pipe from the few that work.
+// mbar_wait (ptx.cuh) that leaves the polling to the hardware for up to 20 us at a time: of a block's 16 warps
+// those that wait would, polling by themselves, keep the shared-memory pipe from the few that work.
 __device__ __forceinline__ bool few_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   auto poll = [&] {
     uint32_t ok;

@@ -19,7 +19,8 @@
 // instructions, hence lanes of 16 channels, two products an instruction, and a border only looked at where
 // two codes differ. Measured, bf16: SwiGLU of 8192 x 14336 to mx 91 us (532 MB at 5.8 TB/s; lanes of 8 109,
 // and with one product an instruction 120), to nv 106; 8192 x 7168 to mx 26, to nv 37 (lanes of 8: 32 and 51);
-// back, 8192 x 14336, 56. All in 64 bits where f32 is in doubt: 8192 x 7168 to nv 1.06 ms (ties are common
+// back, 8192 x 14336, 56. (At the registers of that many blocks an SM to nv spills 60 bytes a thread, SwiGLU by 16
+// 68 and 128.) All in 64 bits where f32 is in doubt: 8192 x 7168 to nv 1.06 ms (ties are common
 // there), SwiGLU of 512 x 768 to nv 15 us, so 3.
 #include <cstdint>
 

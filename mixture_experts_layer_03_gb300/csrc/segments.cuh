@@ -1,5 +1,6 @@
-// Rows walked a warp to a segment of 256 channels, 8 of them a lane, as the operators between the
-// experts' products do (SwiGLU with its checkpoint, the conversions to and from 4 bits).
+// Rows walked a warp to a segment, as the operators between the experts' products do: SwiGLU with its checkpoint
+// (segments of 256 channels, 8 a lane; of rows that do not start on 16 bytes 4 or 8 blocks of 32) and the
+// conversions to 4 bits (256 or 512, 8 or 16 a lane) and back (1024, four times 8 a lane).
 #pragma once
 
 #include <cstdint>
@@ -11,7 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int kSegmentThreads = 128;
-constexpr int kPerLane = 8;        // channels a lane holds in the vector form
+constexpr int kPerLane = 8;        // channels of a vector load or store of a lane
 
 // sigma(g) and 1 - sigma(g). For 16-bit results by the fast exponential and quotient, whose error of 2 +
 // 1.17 |g| units of 2^-23 (under 2^-16 where sigma is not 0) is small beside the one rounding of the
@@ -54,7 +55,7 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[kPerLane]) {
   }
 }
 
-// The work of a warp, one after the other: (row, segment) pairs, a segment 256 channels. Stepping (row,
+// The work of a warp, one after the other: (row, segment) pairs. Stepping (row,
 // segment) by the grid's share keeps divisions out.
 struct SegmentWalk {
   int64_t row;
