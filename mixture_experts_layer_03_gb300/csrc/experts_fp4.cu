@@ -428,7 +428,7 @@ experts_fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         __syncwarp();
         if (lane == 0) {
           if (lead) mbar_arrive(&tempty_bar[acc]);
-          else mbar_arrive_remote(lead_tempty + 8u * acc);
+          else mbar_arrive_relaxed(lead_tempty + 8u * acc);
         }
       };
       if (32 * quarter >= t.m_here) {

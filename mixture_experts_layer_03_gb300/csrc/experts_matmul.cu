@@ -617,7 +617,7 @@ experts_matmul_kernel(const __grid_constant__ CUtensorMap map_a,
         __syncwarp();
         if (lane == 0) {
           if (lead) mbar_arrive(&tempty_bar[acc]);
-          else mbar_arrive_remote(lead_tempty + 8u * acc);
+          else mbar_arrive_relaxed(lead_tempty + 8u * acc);
         }
       };
       if constexpr (kMode == kDw && !kF32) {

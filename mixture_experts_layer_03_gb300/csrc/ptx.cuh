@@ -140,12 +140,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same without ordering this thread's own writes for the other CTA (release at CTA scope): for a
-// barrier that only hands TMEM back, behind a tc_fence_before().
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // The same without ordering any memory: for what tcgen05.fence orders (TMEM written or read, then
 // tc_fence_before(); on the other side tc_fence_after()).
 __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
